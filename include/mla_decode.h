@@ -74,7 +74,8 @@ typedef enum {
   MLA_ERR_CUDA = 4,                 /* a CUDA runtime call or a kernel launch failed */
   MLA_ERR_DEVICE_INDEX = 5,         /* a kernel found kv_indptr inconsistent with the plan */
   MLA_ERR_DEVICE_TIMEOUT = 6,       /* a kernel gave up waiting for its own copies */
-  MLA_ERR_NO_DEVICE = 7             /* no CUDA device is visible */
+  MLA_ERR_NO_DEVICE = 7,            /* no CUDA device is visible */
+  MLA_ERR_OUT_OF_PAGES = 8          /* a cache has too few free pages for a call (mla_cache.h) */
 } mla_status;
 
 /*

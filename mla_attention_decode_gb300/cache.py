@@ -1,0 +1,413 @@
+"""ctypes binding of include/mla_cache.h: the operators around the latent cache.
+
+``MLACachePool`` is a paged cache with its pages' counts and a workspace; its
+methods write rows (norms, rotation and storage format in one pass), read them
+back as bf16, and manage the pages of a batch's sequences.  ``MLARope`` and
+``MLANorm`` are the rotation and the norms of a layer.  As in
+``mla_attention_decode_gb300.binding`` this marshals arguments only: every step
+runs in the library's CUDA kernels, nothing synchronises, and what only the
+device can see is reported by ``MLACachePool.poll_error``.
+
+A page table is a tuple ``(page_indptr, kv_indices, last_page_len)`` of int32
+CUDA tensors, the arrays that ``PagedMLADecoder`` takes.
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+import threading
+
+import torch
+
+from . import binding
+from .binding import MLA_ERR_INVALID_ARG, MLA_KV_BF16, MLA_KV_FP8_E4M3, MLA_KV_MXFP4, MLA_OK, MLAError
+
+MLA_ERR_OUT_OF_PAGES = 8
+PAIRS, MAX_AXES = 32, 8
+ROW_WIDTH = {MLA_KV_BF16: 576, MLA_KV_FP8_E4M3: 576, MLA_KV_MXFP4: 288}
+_PARTS = ("kv_lat", "kv_pe", "q_lat", "q_pe")
+_PART_COLUMNS = (512, 64, 512, 64)
+
+
+class mla_cache(ctypes.Structure):
+    _fields_ = [("kv", ctypes.c_void_p), ("kv_scale", ctypes.c_void_p), ("kv_layer_bytes", ctypes.c_int64),
+                ("scale_layer_bytes", ctypes.c_int64), ("kv_dtype", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("num_layers", ctypes.c_int32), ("scale_stride", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class mla_rope(ctypes.Structure):
+    _fields_ = [("turn", ctypes.c_uint64 * PAIRS), ("axis", ctypes.c_uint8 * PAIRS), ("num_axes", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class mla_norm(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p * 4), ("apply", ctypes.c_int32), ("weight_fp32", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class mla_append_args(ctypes.Structure):
+    _fields_ = [("kv_lat", ctypes.c_void_p), ("kv_pe", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("q_lat", ctypes.c_void_p), ("q_pe", ctypes.c_void_p),
+                ("q_out", ctypes.c_void_p), ("kv_lat_stride", ctypes.c_int64), ("kv_pe_stride", ctypes.c_int64),
+                ("position_stride", ctypes.c_int64), ("q_lat_token_stride", ctypes.c_int64),
+                ("q_lat_head_stride", ctypes.c_int64), ("q_pe_token_stride", ctypes.c_int64),
+                ("q_pe_head_stride", ctypes.c_int64), ("num_tokens", ctypes.c_int32), ("layer", ctypes.c_int32)]
+
+
+class mla_page_table(ctypes.Structure):
+    _fields_ = [("page_indptr", ctypes.c_void_p), ("kv_indices", ctypes.c_void_p),
+                ("last_page_len", ctypes.c_void_p), ("batch", ctypes.c_int32), ("num_indices", ctypes.c_int32)]
+
+
+# The two structs of a call, packed into a bytes object of the call's own.
+_APPEND = struct.Struct("@7P7q2i")
+_TABLE = struct.Struct("@3P2i")
+
+_lock = threading.Lock()
+_lib: ctypes.CDLL | None = None
+
+
+def load_library() -> ctypes.CDLL:
+    """The library with the entry points of mla_cache.h bound; raises if it is missing."""
+    global _lib
+    if _lib is not None:
+        return _lib
+    lib = binding.load_library()
+    with _lock:
+        if _lib is None:
+            P, i32, i64, sz, B = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_char_p
+            for name, args in (("mla_rope_plan", [P, P, i32, i32, ctypes.c_double, P]),
+                               ("mla_cache_append", [P, P, P, B, P, P]),
+                               ("mla_cache_gather", [P, i32, P, i32, P, i64, P, P]),
+                               ("mla_cache_slots", [P, B, P, i32, P, P, i64, P, P]),
+                               ("mla_cache_copy_pages", [P, P, P, i32, P, P]),
+                               ("mla_cache_fork", [P, P, B, P, B, P, sz, P]),
+                               ("mla_cache_resize", [P, P, B, P, B, P, sz, P]),
+                               ("mla_cache_free", [P, P, P, i32, P, P]),
+                               ("mla_cache_compact", [P, P, P, P, P, i32, P, P, sz, P])):
+                getattr(lib, name).argtypes = args
+                getattr(lib, name).restype = ctypes.c_int
+            lib.mla_cache_workspace_bytes.argtypes = [P, i32]
+            lib.mla_cache_workspace_bytes.restype = sz
+            _lib = lib
+    return _lib
+
+
+class MLARope:
+    """The rotation of the 64 position columns (32 pairs).
+
+    ``inv_freq``: 32 angles per position step (default ``theta ** (-i / 32)``);
+    ``axis_of_pair``: which of a token's positions turns each pair (default: all
+    the first), or ``sections``: that many pairs for each axis in turn;
+    ``interleaved``: pair i is columns (2i, 2i + 1), else (i, i + 32); ``scale``:
+    a factor on the rotated columns."""
+
+    def __init__(self, inv_freq=None, axis_of_pair=None, sections=None, interleaved: bool = True, scale: float = 1.0,
+                 theta: float = 10000.0):
+        freq = [float(theta) ** (-i / PAIRS) for i in range(PAIRS)] if inv_freq is None else [float(f) for f in inv_freq]
+        if sections is not None:
+            if axis_of_pair is not None:
+                raise ValueError("give axis_of_pair or sections, not both")
+            axis_of_pair = [a for a, n in enumerate(sections) for _ in range(int(n))]
+        axes = [0] * PAIRS if axis_of_pair is None else [int(a) for a in axis_of_pair]
+        if len(freq) != PAIRS or len(axes) != PAIRS:
+            raise ValueError(f"a rotation has {PAIRS} pairs: got {len(freq)} frequencies and {len(axes)} axes")
+        self.num_axes = max(axes) + 1
+        self.rope = mla_rope()
+        rc = load_library().mla_rope_plan((ctypes.c_double * PAIRS)(*freq), (ctypes.c_int32 * PAIRS)(*axes),
+                                          self.num_axes, int(bool(interleaved)), float(scale),
+                                          ctypes.addressof(self.rope))
+        if rc != MLA_OK:
+            raise MLAError(rc, "mla_rope_plan")
+        self.address = ctypes.addressof(self.rope)
+
+
+class MLANorm:
+    """Root-mean-square norms of a key row's and of each query head's parts.
+
+    ``kv_lat``, ``kv_pe``, ``q_lat``, ``q_pe``: the weights of the part (a CUDA
+    tensor of 512 or 64, bf16 or fp32, one type for all), True for weights of 1,
+    or None where the part is not normed."""
+
+    def __init__(self, eps: float = 1e-6, kv_lat=None, kv_pe=None, q_lat=None, q_pe=None):
+        self.norm = mla_norm(eps=float(eps))
+        self.weights = []  # kept alive
+        self.device = None
+        dtypes = set()
+        for i, w in enumerate((kv_lat, kv_pe, q_lat, q_pe)):
+            if w is None or w is False:
+                continue
+            self.norm.apply |= 1 << i
+            if w is True:
+                continue
+            if w.numel() != _PART_COLUMNS[i] or not w.is_contiguous() or not w.is_cuda:
+                raise ValueError(f"{_PARTS[i]}: the weights are a contiguous CUDA tensor of {_PART_COLUMNS[i]}")
+            if w.dtype not in (torch.bfloat16, torch.float32):
+                raise ValueError(f"{_PARTS[i]}: the weights are bf16 or fp32, not {w.dtype}")
+            if self.device is not None and w.device != self.device:
+                raise ValueError("the weights are on different devices")
+            dtypes.add(w.dtype)
+            self.device = w.device
+            self.weights.append(w)
+            self.norm.weight[i] = w.data_ptr()
+        if len(dtypes) > 1:
+            raise ValueError("the weights are all bf16 or all fp32")
+        self.norm.weight_fp32 = int(torch.float32 in dtypes)
+        self.address = ctypes.addressof(self.norm)
+
+
+class MLACachePool:
+    """A paged latent cache: its rows, the counts of its pages and a workspace.
+
+    ``kv``: [rows, width] or [layers, rows, width] (rows = pages * page_size):
+    bf16 [.., 576], e4m3 bytes [.., 576] or packed e2m1 [.., 288]; ``kv_scale``:
+    fp32 [1] (or one per layer) for fp8, e8m0 bytes [(layers,) rows, >= 18] for
+    MXFP4.  ``refs``: int32, how many sequences hold each page (default: all
+    free).  A contiguous cache is one with pages of one row.
+
+    Calls that share a pool are ordered on the GPU (one stream, or events).
+    Methods enqueue on ``stream`` (default: torch's current one) of the pool's
+    device; ``poll_error`` synchronises."""
+
+    def __init__(self, kv, kv_dtype, page_size: int, kv_scale=None, refs=None, max_batch: int = 4096):
+        self.kv_dtype = binding._dtype_code(kv_dtype)
+        if self.kv_dtype not in ROW_WIDTH:
+            raise MLAError(binding.MLA_ERR_UNSUPPORTED, "MLACachePool")
+        if kv.dim() not in (2, 3):
+            raise ValueError("kv is [rows, width] or [layers, rows, width]")
+        if not kv.is_cuda:
+            raise ValueError("kv is a CUDA tensor")
+        layered = kv.dim() == 3
+        width, want = ROW_WIDTH[self.kv_dtype], (torch.bfloat16,)
+        if self.kv_dtype != MLA_KV_BF16:
+            want = (torch.uint8, torch.float8_e4m3fn) if self.kv_dtype == MLA_KV_FP8_E4M3 else (torch.uint8,)
+        if kv.dtype not in want or kv.shape[-1] != width or kv.stride(-1) != 1 or kv.stride(-2) != width:
+            raise ValueError(f"kv is {want[0]} [.., {width}] with consecutive rows: got {kv.dtype} {tuple(kv.shape)}")
+        page_size, rows = int(page_size), kv.shape[-2]
+        if page_size < 1 or rows % page_size:
+            raise ValueError(f"{rows} rows are not whole pages of {page_size}")
+        c = self.cache = mla_cache(kv=kv.data_ptr(), kv_dtype=self.kv_dtype, page_size=page_size,
+                                   num_pages=rows // page_size, num_layers=kv.shape[0] if layered else 1)
+        if layered and kv.shape[0] > 1:
+            c.kv_layer_bytes = kv.stride(0) * kv.element_size()
+        if self.kv_dtype == MLA_KV_BF16:
+            if kv_scale is not None:
+                raise ValueError("a bf16 cache has no scales")
+        else:
+            if kv_scale is None or kv_scale.device != kv.device:
+                raise ValueError("kv_scale is on the cache's device")
+            if self.kv_dtype == MLA_KV_FP8_E4M3:
+                if kv_scale.dtype != torch.float32 or kv_scale.numel() not in (1, c.num_layers) or not kv_scale.is_contiguous():
+                    raise ValueError("kv_scale is fp32, one or one per layer")
+                c.scale_layer_bytes = 4 if kv_scale.numel() > 1 else 0
+            else:
+                if (kv_scale.dtype != torch.uint8 or kv_scale.shape[:-1] != kv.shape[:-1] or kv_scale.shape[-1] < 18
+                        or kv_scale.stride(-1) != 1):
+                    raise ValueError("kv_scale is uint8 [.., rows, >= 18]")
+                c.scale_stride = kv_scale.stride(-2)
+                if layered and kv.shape[0] > 1:
+                    c.scale_layer_bytes = kv_scale.stride(0)
+            c.kv_scale = kv_scale.data_ptr()
+        self.kv, self.kv_scale, self.device = kv, kv_scale, kv.device
+        self.page_size, self.num_pages, self.num_layers = page_size, c.num_pages, c.num_layers
+        if refs is None:
+            refs = torch.zeros(self.num_pages, dtype=torch.int32, device=self.device)
+        self._check(refs, "refs", self.num_pages)
+        self.refs = refs
+        self._lib = load_library()
+        self._at = ctypes.addressof(c)
+        nbytes = int(self._lib.mla_cache_workspace_bytes(self._at, int(max_batch)))
+        if nbytes == 0:
+            raise MLAError(MLA_ERR_INVALID_ARG, "mla_cache_workspace_bytes")
+        self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        self._ws, self._ws_bytes = self.workspace.data_ptr(), nbytes
+
+    @classmethod
+    def allocate(cls, kv_dtype, num_pages: int, page_size: int, num_layers: int = 1, device="cuda", kv_scale=1.0,
+                 max_batch: int = 4096):
+        """A pool over new, zeroed storage; ``kv_scale``: fp8 only, the scale of every layer."""
+        code, rows = binding._dtype_code(kv_dtype), int(num_pages) * int(page_size)
+        kv = torch.zeros(num_layers, rows, ROW_WIDTH[code], device=device,
+                         dtype=torch.bfloat16 if code == MLA_KV_BF16 else torch.uint8)
+        scale = None
+        if code == MLA_KV_FP8_E4M3:
+            scale = torch.full((1,), float(kv_scale), dtype=torch.float32, device=device)
+        elif code == MLA_KV_MXFP4:
+            scale = torch.full((num_layers, rows, 18), 127, dtype=torch.uint8, device=device)
+        return cls(kv, code, page_size, kv_scale=scale, max_batch=max_batch)
+
+    # -------------------------------------------------------------- arguments
+    def _check(self, t, what, size=None, dtype=torch.int32):
+        """An int32 (or ``dtype``) vector on the pool's device."""
+        if t.dtype != dtype or t.device != self.device or t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1):
+            raise ValueError(f"{what} is a contiguous {dtype} vector on {self.device}")
+        if size is not None and t.numel() != size:
+            raise ValueError(f"{what} has {size} entries, not {t.numel()}")
+
+    def _table(self, table, what):
+        indptr, indices, last = table
+        batch = indptr.numel() - 1
+        self._check(indptr, what + ".page_indptr")
+        self._check(indices, what + ".kv_indices")
+        self._check(last, what + ".last_page_len", batch)
+        return _TABLE.pack(indptr.data_ptr(), indices.data_ptr(), last.data_ptr(), batch, indices.numel())
+
+    def _call(self, name, stream, *args):
+        """The entry point on ``stream`` (a handle, a torch stream or None), with the pool's device current."""
+        fn = getattr(self._lib, name)
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if torch.cuda.current_device() == self.device.index:
+            rc = fn(self._at, *args, handle)
+        else:
+            with torch.cuda.device(self.device):
+                rc = fn(self._at, *args, handle)
+        if rc != MLA_OK:
+            raise MLAError(rc, name)
+
+    def _empty(self, shape, dtype, stream):
+        """New memory that belongs to the stream the call runs on."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def table(self, batch: int, num_indices: int):
+        """Buffers of a page table of ``batch`` empty sequences, with room for ``num_indices`` entries."""
+        return (torch.zeros(batch + 1, dtype=torch.int32, device=self.device),
+                torch.zeros(num_indices, dtype=torch.int32, device=self.device),
+                torch.zeros(batch, dtype=torch.int32, device=self.device))
+
+    # -------------------------------------------------------------- rows
+    def append(self, kv_lat, kv_pe, slots, rope: MLARope | None = None, positions=None, norm: MLANorm | None = None,
+               q_pe=None, q_lat=None, q_out=None, layer: int = 0, stream=None):
+        """Norms, rotates and stores T tokens' key rows; norms and rotates their queries into ``q_out``.
+
+        ``kv_lat`` [T, 512], ``kv_pe`` [T, 64] (None, None: queries only), ``slots`` [T] (-1: not stored),
+        ``positions`` [T] or [T, axes], ``q_pe`` [T, 16, 64], ``q_lat`` [T, 16, 512] (None: the latent columns of
+        ``q_out`` stay), ``q_out`` [T, 16, 576] contiguous; bf16, the last dimension consecutive."""
+        first = kv_lat if kv_lat is not None else q_pe
+        if first is None:
+            raise ValueError("append needs keys (kv_lat, kv_pe) or queries (q_pe, q_out)")
+        t = first.shape[0]
+        p, s = [0] * 7, [0] * 7
+        if kv_lat is not None:
+            if kv_pe is None or slots is None:
+                raise ValueError("keys come as kv_lat, kv_pe and slots")
+            self._part(kv_lat, "kv_lat", (t, 512))
+            self._part(kv_pe, "kv_pe", (t, 64))
+            self._check(slots, "slots", t)
+            p[0], p[1], p[2] = kv_lat.data_ptr(), kv_pe.data_ptr(), slots.data_ptr()
+            s[0], s[1] = kv_lat.stride(0), kv_pe.stride(0)
+        elif kv_pe is not None:
+            raise ValueError("keys come as kv_lat, kv_pe and slots")
+        if rope is not None:
+            if positions is None or positions.dtype != torch.int32 or positions.device != self.device:
+                raise ValueError(f"positions is int32 on {self.device}")
+            if positions.shape[0] != t or positions.dim() not in (1, 2) or (
+                    rope.num_axes > (positions.shape[1] if positions.dim() == 2 else 1)):
+                raise ValueError(f"positions is [{t}, {rope.num_axes}]: got {tuple(positions.shape)}")
+            if positions.dim() == 2 and positions.shape[1] > 1 and positions.stride(1) != 1:
+                raise ValueError("a token's positions are consecutive")
+            p[3], s[2] = positions.data_ptr(), positions.stride(0)
+        if q_pe is not None:
+            if q_out is None:
+                raise ValueError("queries come as q_pe and q_out")
+            self._part(q_pe, "q_pe", (t, 16, 64))
+            self._part(q_out, "q_out", (t, 16, 576))
+            if not q_out.is_contiguous():
+                raise ValueError("q_out is contiguous")
+            p[5], p[6], s[5], s[6] = q_pe.data_ptr(), q_out.data_ptr(), q_pe.stride(0), q_pe.stride(1)
+            if q_lat is not None:
+                self._part(q_lat, "q_lat", (t, 16, 512))
+                p[4], s[3], s[4] = q_lat.data_ptr(), q_lat.stride(0), q_lat.stride(1)
+        elif q_lat is not None or q_out is not None:
+            raise ValueError("queries come as q_pe and q_out")
+        if norm is not None and norm.device is not None and norm.device != self.device:
+            raise ValueError(f"the norm's weights are not on {self.device}")
+        self._call("mla_cache_append", stream, rope.address if rope is not None else None,
+                   norm.address if norm is not None else None, _APPEND.pack(*p, *s, t, int(layer)), self._ws)
+
+    def _part(self, x, what, shape):
+        if x.dtype != torch.bfloat16 or x.device != self.device or x.shape != shape or x.stride(-1) != 1:
+            raise ValueError(f"{what} is bf16 {list(shape)} on {self.device}, its last dimension consecutive: "
+                             f"got {x.dtype} {list(x.shape)}")
+
+    def gather(self, slots, out=None, layer: int = 0, stream=None):
+        """Rows ``slots`` of a layer as bf16 [T, 576] (``out``'s rows with slot -1 stay as they were; without
+        ``out`` they are unset)."""
+        self._check(slots, "slots")
+        n = slots.numel()
+        if out is None:
+            out = self._empty((n, 576), torch.bfloat16, stream)
+        self._part(out, "out", (n, 576))
+        self._call("mla_cache_gather", stream, int(layer), slots.data_ptr(), n, out.data_ptr(),
+                   out.stride(0) if n > 1 else 576, self._ws)
+        return out
+
+    def slots(self, table, qo_indptr, num_tokens: int, slots=None, rows=None, stream=None):
+        """The cache row of each sequence's last ``qo_indptr[b + 1] - qo_indptr[b]`` tokens, as ``slots`` [num_tokens]
+        (-1 past the batch); with ``rows`` (int32, any stride) the tokens' places in their sequences too."""
+        n = int(num_tokens)
+        if slots is None:
+            slots = self._empty((n,), torch.int32, stream)
+        self._check(slots, "slots", n)
+        self._check(qo_indptr, "qo_indptr", table[0].numel())
+        if rows is not None and (rows.dtype != torch.int32 or rows.device != self.device or rows.shape != (n,)):
+            raise ValueError(f"rows is int32 [{n}] on {self.device}")
+        self._call("mla_cache_slots", stream, self._table(table, "table"), qo_indptr.data_ptr(), n, slots.data_ptr(),
+                   rows.data_ptr() if rows is not None else None, rows.stride(0) if rows is not None else 0, self._ws)
+        return slots, rows
+
+    # -------------------------------------------------------------- pages
+    def copy_pages(self, src, dst, stream=None):
+        """Page ``dst[i]`` becomes a copy of page ``src[i]``, in every layer."""
+        self._check(src, "src")
+        self._check(dst, "dst", src.numel())
+        self._call("mla_cache_copy_pages", stream, src.data_ptr(), dst.data_ptr(), src.numel(), self._ws)
+
+    def fork(self, table, parents, out, stream=None):
+        """Writes to ``out`` a batch whose sequence n is a fork of ``table``'s sequence ``parents[n]``."""
+        self._check(parents, "parents", out[0].numel() - 1)
+        self._call("mla_cache_fork", stream, self.refs.data_ptr(), self._table(table, "table"), parents.data_ptr(),
+                   self._table(out, "out"), self._ws, self._ws_bytes)
+        return out
+
+    def resize(self, table, lengths, out, stream=None):
+        """Writes to ``out`` the table whose sequence b has ``lengths[b]`` rows; ``table`` is void from then on."""
+        self._check(lengths, "lengths", out[0].numel() - 1)
+        self._call("mla_cache_resize", stream, self.refs.data_ptr(), self._table(table, "table"), lengths.data_ptr(),
+                   self._table(out, "out"), self._ws, self._ws_bytes)
+        return out
+
+    def free(self, pages, stream=None):
+        """Ends one hold on each of ``pages`` (-1 entries are skipped)."""
+        self._check(pages, "pages")
+        self._call("mla_cache_free", stream, self.refs.data_ptr(), pages.data_ptr(), pages.numel(), self._ws)
+
+    def compact(self, kv_indices, out=None, stream=None):
+        """Moves the pages in use to the front.  ``out``: (kv_indices, refs, live [1]) to write; without it the
+        pool's counts are rewritten in place and the other two are new.  Returns the three."""
+        self._check(kv_indices, "kv_indices")
+        if out is None:
+            out = (self._empty(kv_indices.shape, torch.int32, stream), self.refs,
+                   self._empty((1,), torch.int32, stream))
+        indices, refs, live = out
+        self._check(indices, "out indices", kv_indices.numel())
+        self._check(refs, "out refs", self.num_pages)
+        self._check(live, "out live", 1)
+        self._call("mla_cache_compact", stream, self.refs.data_ptr(), refs.data_ptr(), kv_indices.data_ptr(),
+                   indices.data_ptr(), kv_indices.numel(), live.data_ptr(), self._ws, self._ws_bytes)
+        return out
+
+    def poll_error(self, stream=None) -> int:
+        """The error that a call on this pool met on the device (0: none), cleared; synchronises the stream."""
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        with torch.cuda.device(self.device):
+            return int(self._lib.mla_decode_poll_error(self._ws, handle))

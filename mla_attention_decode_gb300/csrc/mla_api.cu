@@ -836,11 +836,12 @@ const char* mla_status_string(int status) {
     case MLA_ERR_DEVICE_INDEX: return "kernel found kv_indptr inconsistent with the plan";
     case MLA_ERR_DEVICE_TIMEOUT: return "kernel timed out waiting for its own copies";
     case MLA_ERR_NO_DEVICE: return "no CUDA device visible";
+    case MLA_ERR_OUT_OF_PAGES: return "the cache has too few free pages";
     default: return "unknown status";
   }
 }
 
-const char* mla_decode_version(void) { return "0.2.0"; }
+const char* mla_decode_version(void) { return "0.3.0"; }
 
 int mla_decode_set_trace(uint64_t* buffer) {
 #if defined(MLA_TRACE) && MLA_TRACE

@@ -1,0 +1,401 @@
+// mla_cache_rows.cu -- rows of the latent cache written, read back and found
+// (include/mla_cache.h): mla_cache_append, mla_cache_gather, mla_cache_slots.
+#include <cuda_runtime.h>
+
+#include "mla_cache_internal.h"
+#include "mla_ptx.cuh"
+
+namespace mla {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+
+__device__ __forceinline__ void set_error(int32_t* error, int32_t code) {
+  if (error) *error = code;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+__device__ __forceinline__ void unpack_bf16x8(uint4 r, float (&x)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack_bf16x8(const float (&x)[8]) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                    pack_bf16x2(x[6], x[7]));
+}
+
+// Eight floats -> eight e2m1 codes (nearest, ties to even, saturating at 6),
+// element 2i in the low nibble of byte i.
+__device__ __forceinline__ uint32_t pack_e2m1x8(const float (&x)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return r;
+}
+
+// Four packed bytes (eight e2m1 codes) -> eight floats, exactly.
+__device__ __forceinline__ void unpack_e2m1x8(uint32_t r, float (&x)[8]) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(r));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+// The e8m0 byte of a block with largest magnitude amax: e + 127 for the smallest
+// 2^e with amax <= 6 * 2^e = 1.5 * 2^(e + 2), read off amax's own exponent and
+// fraction (no logarithm, so exact at every border), and the factor 2^-e.
+// All-zero block: 127 (2^0).  Infinity or NaN in the block: 255 (NaN), factor 0.
+__device__ __forceinline__ uint32_t e8m0_of(float amax, float& inv) {
+  const uint32_t bits = __float_as_uint(amax);
+  if (bits == 0) {
+    inv = 1.f;
+    return 127;
+  }
+  if (bits >= 0x7f800000u) {
+    inv = 0.f;
+    return 255;
+  }
+  int e = (int)(bits >> 23) - 127 - 2 + ((bits & 0x7fffffu) > 0x400000u);
+  e = max(e, -127);  // amax < 2^-125 (subnormal amax too): 6 * 2^-127 holds it
+  inv = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-126 .. 2^127
+  return (uint32_t)(e + 127);
+}
+
+// |x| as an ordering key in which NaN is largest (a plain fmaxf drops it).
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// Weights of 8 latent columns from column c, as floats.
+__device__ __forceinline__ void load_weight8(const void* w, bool fp32, int c, float (&y)[8]) {
+  if (fp32) {
+    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(w) + c);
+    const float4 a = __ldg(f), b = __ldg(f + 1);
+    y[0] = a.x, y[1] = a.y, y[2] = a.z, y[3] = a.w, y[4] = b.x, y[5] = b.y, y[6] = b.z, y[7] = b.w;
+  } else {
+    unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + c)), y);
+  }
+}
+__device__ __forceinline__ float load_weight(const void* w, bool fp32, int c) {
+  return fp32 ? __ldg(static_cast<const float*>(w) + c)
+              : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(w) + c) << 16);
+}
+
+// ---------------------------------------------------------------- append
+// The 512 latent columns of a row or head, 16 a lane: columns 8 * lane + j and
+// 256 + 8 * lane + j, so that each load is a warp-wide run of 512 bytes.
+struct Lat {
+  float x[2][8];
+};
+__device__ __forceinline__ void load_lat(const uint16_t* src, int lane, Lat& v) {
+  const uint4* s = reinterpret_cast<const uint4*>(src);
+  const uint4 a = s[lane], b = s[32 + lane];
+  unpack_bf16x8(a, v.x[0]);
+  unpack_bf16x8(b, v.x[1]);
+}
+__device__ __forceinline__ void norm_lat(Lat& v, const mla_norm& n, int part, int lane) {
+  if (!(n.apply >> part & 1)) return;
+  float ss = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(v.x[h][j], v.x[h][j], ss);
+  const float r = rsqrtf(warp_sum(ss) * (1.f / kLat) + n.eps);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    if (n.weight[part]) load_weight8(n.weight[part], n.weight_fp32, 256 * h + 8 * lane, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v.x[h][j] = v.x[h][j] * r * w[j];
+  }
+}
+
+// The cosine and sine of this lane's pair (lane i: pair i) for token t.  The
+// turn count pos * inv_freq / 2 pi matters modulo 1 only: with inv_freq / 2 pi
+// in units of 2^-64 turns the 64-bit product wraps to exactly that, at any
+// position, and its top 32 bits leave an angle error below 2 pi * 2^-33.
+__device__ __forceinline__ float2 cos_sin(const AppendParams& p, int t, int lane) {
+  float c = 1.f, s = 0.f;
+  if (p.rope.num_axes > 0) {
+    const int64_t pos = p.a.positions[(int64_t)t * p.a.position_stride + p.rope.axis[lane]];
+    const uint64_t turns = (uint64_t)pos * p.rope.turn[lane] + 0x80000000ull;
+    sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);
+    c *= p.rope.scale;
+    s *= p.rope.scale;
+  }
+  return make_float2(c, s);
+}
+
+// The 64 position columns normed and rotated; on return lane i holds columns
+// (2i, 2i + 1), whatever the pairing.
+__device__ __forceinline__ float2 turned_pe(const uint16_t* src, const AppendParams& p, int part, float2 cs,
+                                            int lane) {
+  const bool inter = p.rope.interleaved;
+  const int c0 = inter ? 2 * lane : lane, c1 = inter ? 2 * lane + 1 : lane + 32;
+  float a, b;
+  if (inter) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(src + c0);
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xffff0000u);
+  } else {
+    a = __uint_as_float((uint32_t)src[c0] << 16);
+    b = __uint_as_float((uint32_t)src[c1] << 16);
+  }
+  if (p.norm.apply >> part & 1) {
+    const float r = rsqrtf(warp_sum(fmaf(a, a, b * b)) * (1.f / kPe) + p.norm.eps);
+    const void* w = p.norm.weight[part];
+    a = a * r * (w ? load_weight(w, p.norm.weight_fp32, c0) : 1.f);
+    b = b * r * (w ? load_weight(w, p.norm.weight_fp32, c1) : 1.f);
+  }
+  // without a rotation nothing is multiplied: an infinity would make its partner NaN
+  const bool turn = p.rope.num_axes > 0;
+  const float y0 = turn ? fmaf(a, cs.x, -b * cs.y) : a, y1 = turn ? fmaf(a, cs.y, b * cs.x) : b;
+  if (inter) return make_float2(y0, y1);
+  // columns 2i, 2i + 1 are the first elements of pairs 2i, 2i + 1 (i < 16) or
+  // the second elements of pairs 2i - 32, 2i - 31
+  const int from = 2 * lane & 31;
+  const float u0 = __shfl_sync(kFull, y0, from), u1 = __shfl_sync(kFull, y0, from + 1);
+  const float v0 = __shfl_sync(kFull, y1, from), v1 = __shfl_sync(kFull, y1, from + 1);
+  return lane < 16 ? make_float2(u0, u1) : make_float2(v0, v1);
+}
+
+// One key row into row `slot` of the cache, in its format.
+template <int kDtype>
+__device__ __forceinline__ void store_row(const AppendParams& p, int32_t slot, const Lat& lat, float2 pe, int lane) {
+  if (kDtype == MLA_KV_BF16) {
+    uint8_t* dst = p.cache.kv + (int64_t)slot * (2 * kRow);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) reinterpret_cast<uint4*>(dst)[32 * h + lane] = pack_bf16x8(lat.x[h]);
+    reinterpret_cast<uint32_t*>(dst + 2 * kLat)[lane] = pack_bf16x2(pe.x, pe.y);
+  } else if (kDtype == MLA_KV_FP8_E4M3) {
+    // the quotient is the rounded one (not a product with the reciprocal): the
+    // stored code is e4m3(y / scale) at every border
+    const float sc = *static_cast<const float*>(p.cache.scale);
+    uint8_t* dst = p.cache.kv + (int64_t)slot * kRow;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = f32x2_to_e4m3x2(__fdiv_rn(lat.x[h][2 * j], sc), __fdiv_rn(lat.x[h][2 * j + 1], sc));
+      reinterpret_cast<uint2*>(dst)[32 * h + lane] = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+    }
+    reinterpret_cast<uint16_t*>(dst + kLat)[lane] =
+        (uint16_t)f32x2_to_e4m3x2(__fdiv_rn(pe.x, sc), __fdiv_rn(pe.y, sc));
+  } else {
+    uint8_t* dst = p.cache.kv + (int64_t)slot * (kRow / 2);
+    uint8_t* sdst = static_cast<uint8_t*>(p.cache.scale) + (int64_t)slot * p.cache.scale_stride;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // a block of 32 columns: four lanes
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, abs_bits(lat.x[h][j]));
+      m = max(m, __shfl_xor_sync(kFull, m, 1));
+      m = max(m, __shfl_xor_sync(kFull, m, 2));
+      float inv, y[8];
+      const uint32_t byte = e8m0_of(__uint_as_float(m), inv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = byte == 255 ? 0.f : lat.x[h][j] * inv;
+      reinterpret_cast<uint32_t*>(dst)[32 * h + lane] = pack_e2m1x8(y);
+      if ((lane & 3) == 0) sdst[8 * h + (lane >> 2)] = (uint8_t)byte;
+    }
+    // the position columns: two blocks of sixteen lanes
+    uint32_t m = max(abs_bits(pe.x), abs_bits(pe.y));
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+    float inv;
+    const uint32_t byte = e8m0_of(__uint_as_float(m), inv);
+    const float z0 = byte == 255 ? 0.f : pe.x * inv, z1 = byte == 255 ? 0.f : pe.y * inv;
+    const float y[8] = {z0, z1, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    dst[kLat / 2 + lane] = (uint8_t)pack_e2m1x8(y);
+    if ((lane & 15) == 0) sdst[16 + (lane >> 4)] = (uint8_t)byte;
+  }
+}
+
+// One warp per key row or query head of a token (17 parts; 16 or 1 where the
+// call has no keys or no queries).
+template <int kDtype>
+__global__ void __launch_bounds__(256) mla_append_kernel(const __grid_constant__ AppendParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int keys = p.a.kv_lat ? 1 : 0, parts = keys + (p.a.q_pe ? kQueryHeads : 0);
+  const int64_t task = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (task >= (int64_t)p.a.num_tokens * parts) return;
+  const int t = (int)(task / parts), part = (int)(task % parts);
+  const float2 cs = cos_sin(p, t, lane);
+  if (part < keys) {
+    const int32_t slot = p.a.slots[t];
+    if (slot < 0 || slot >= p.cache.rows) {
+      if (slot != -1 && lane == 0) set_error(p.error, MLA_ERR_DEVICE_INDEX);
+      return;
+    }
+    Lat v;
+    load_lat(static_cast<const uint16_t*>(p.a.kv_lat) + (int64_t)t * p.a.kv_lat_stride, lane, v);
+    norm_lat(v, p.norm, MLA_PART_KV_LAT, lane);
+    const float2 pe = turned_pe(static_cast<const uint16_t*>(p.a.kv_pe) + (int64_t)t * p.a.kv_pe_stride, p,
+                                MLA_PART_KV_PE, cs, lane);
+    store_row<kDtype>(p, slot, v, pe, lane);
+    return;
+  }
+  const int h = part - keys;
+  uint16_t* out = static_cast<uint16_t*>(p.a.q_out) + ((int64_t)t * kQueryHeads + h) * kRow;
+  const float2 pe = turned_pe(static_cast<const uint16_t*>(p.a.q_pe) + (int64_t)t * p.a.q_pe_token_stride +
+                                  (int64_t)h * p.a.q_pe_head_stride,
+                              p, MLA_PART_Q_PE, cs, lane);
+  __syncwarp();  // in place: every lane has read its columns before any is written
+  reinterpret_cast<uint32_t*>(out + kLat)[lane] = pack_bf16x2(pe.x, pe.y);
+  if (p.a.q_lat) {
+    Lat v;
+    load_lat(static_cast<const uint16_t*>(p.a.q_lat) + (int64_t)t * p.a.q_lat_token_stride +
+                 (int64_t)h * p.a.q_lat_head_stride,
+             lane, v);
+    norm_lat(v, p.norm, MLA_PART_Q_LAT, lane);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) reinterpret_cast<uint4*>(out)[32 * i + lane] = pack_bf16x8(v.x[i]);
+  }
+}
+
+// ---------------------------------------------------------------- gather
+// One thread per 8 columns of a row (16 bytes out; 16, 8 or 4 bytes in).
+constexpr int kPer = kRow / 8;  // 72 threads a row
+
+template <int kDtype>
+__global__ void __launch_bounds__(256) mla_gather_kernel(const __grid_constant__ GatherParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t t = i / kPer;
+  const int c = (int)(i - t * kPer);
+  if (t >= p.num_rows) return;
+  const int32_t slot = p.slots[t];
+  if (slot < 0 || slot >= p.cache.rows) {
+    if (slot != -1 && c == 0) set_error(p.error, MLA_ERR_DEVICE_INDEX);
+    return;
+  }
+  uint4* out = reinterpret_cast<uint4*>(p.out + t * p.out_stride) + c;
+  if (kDtype == MLA_KV_BF16) {
+    *out = reinterpret_cast<const uint4*>(p.cache.kv + (int64_t)slot * (2 * kRow))[c];
+  } else if (kDtype == MLA_KV_FP8_E4M3) {
+    const float sc = *static_cast<const float*>(p.cache.scale);
+    const uint2 r = reinterpret_cast<const uint2*>(p.cache.kv + (int64_t)slot * kRow)[c];
+    const uint32_t w[4] = {r.x & 0xffffu, r.x >> 16, r.y & 0xffffu, r.y >> 16};
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = __half22float2(e4m3x2_to_h2(w[j]));
+      x[2 * j] = f.x * sc;
+      x[2 * j + 1] = f.y * sc;
+    }
+    *out = pack_bf16x8(x);
+  } else {
+    const uint32_t byte =
+        static_cast<const uint8_t*>(p.cache.scale)[(int64_t)slot * p.cache.scale_stride + (c >> 2)];
+    const uint32_t r = reinterpret_cast<const uint32_t*>(p.cache.kv + (int64_t)slot * (kRow / 2))[c];
+    // 2^(byte - 127): 2^-127 is subnormal, 255 is NaN
+    const float sc = __uint_as_float(byte == 0 ? 0x00400000u : (byte == 255 ? 0x7fc00000u : byte << 23));
+    float x[8];
+    unpack_e2m1x8(r, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] *= sc;
+    *out = pack_bf16x8(x);
+  }
+}
+
+// ---------------------------------------------------------------- slots
+// One thread per token: the sequence by bisection of qo_indptr, then the page
+// of its row.  Whatever the tables hold, nothing outside them is read.
+__global__ void __launch_bounds__(128) mla_slots_kernel(const __grid_constant__ SlotsParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int t = blockIdx.x * 128 + threadIdx.x;
+  if (t >= p.num_tokens) return;
+  const int P = 1 << p.page_shift;
+  int32_t slot = -1;
+  int64_t row = 0;
+  if (p.table.batch > 0 && t < p.qo_indptr[p.table.batch]) {
+    int lo = 0, hi = p.table.batch;  // qo_indptr[lo] <= t < qo_indptr[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.qo_indptr[mid] <= t) lo = mid;
+      else hi = mid;
+    }
+    const int64_t first = p.qo_indptr[lo], end = p.qo_indptr[lo + 1];
+    const int64_t a = p.table.page_indptr[lo], b = p.table.page_indptr[lo + 1];
+    bool ok = first <= t && t < end && 0 <= a && a <= b && b <= p.table.num_indices;
+    int64_t len = 0;
+    if (ok && b > a) {
+      const int32_t last = p.table.last_page_len[lo];
+      ok = last >= 1 && last <= P;
+      len = (b - a - 1) * P + last;
+    }
+    if (ok) {
+      row = len - (end - first) + (t - first);
+      ok = row >= 0;
+    }
+    if (ok) {
+      const int32_t page = p.table.kv_indices[a + (row >> p.page_shift)];
+      ok = page >= 0 && page < p.num_pages;
+      if (ok) slot = (page << p.page_shift) + (int32_t)(row & (P - 1));
+    }
+    if (!ok) set_error(p.error, MLA_ERR_DEVICE_INDEX);
+  }
+  p.slots[t] = slot;
+  if (p.rows) p.rows[(int64_t)t * p.row_stride] = (int32_t)row;
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendParams& p, int kv_dtype, cudaStream_t s) {
+  const int64_t parts = (p.a.kv_lat ? 1 : 0) + (p.a.q_pe ? kQueryHeads : 0);
+  const int64_t tasks = parts * p.a.num_tokens;
+  if (tasks == 0) return cudaSuccess;
+  const unsigned grid = (unsigned)((tasks + 7) / 8);
+  switch (kv_dtype) {
+    case MLA_KV_BF16: return launch_chained(mla_append_kernel<MLA_KV_BF16>, grid, 256, s, p);
+    case MLA_KV_FP8_E4M3: return launch_chained(mla_append_kernel<MLA_KV_FP8_E4M3>, grid, 256, s, p);
+    default: return launch_chained(mla_append_kernel<MLA_KV_MXFP4>, grid, 256, s, p);
+  }
+}
+
+cudaError_t launch_gather(const GatherParams& p, int kv_dtype, cudaStream_t s) {
+  if (p.num_rows == 0) return cudaSuccess;
+  const unsigned grid = (unsigned)(((int64_t)p.num_rows * kPer + 255) / 256);
+  switch (kv_dtype) {
+    case MLA_KV_BF16: return launch_chained(mla_gather_kernel<MLA_KV_BF16>, grid, 256, s, p);
+    case MLA_KV_FP8_E4M3: return launch_chained(mla_gather_kernel<MLA_KV_FP8_E4M3>, grid, 256, s, p);
+    default: return launch_chained(mla_gather_kernel<MLA_KV_MXFP4>, grid, 256, s, p);
+  }
+}
+
+cudaError_t launch_slots(const SlotsParams& p, cudaStream_t s) {
+  if (p.num_tokens == 0) return cudaSuccess;
+  return launch_chained(mla_slots_kernel, (unsigned)((p.num_tokens + 127) / 128), 128, s, p);
+}
+
+}  // namespace mla
