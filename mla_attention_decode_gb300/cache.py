@@ -4,9 +4,10 @@
 methods write rows (norms, rotation and storage format in one pass), read them
 back as bf16, and manage the pages of a batch's sequences.  ``MLARope`` and
 ``MLANorm`` are the rotation and the norms of a layer.  As in
-``mla_attention_decode_gb300.binding`` this marshals arguments only: every step
-runs in the library's CUDA kernels, nothing synchronises, and what only the
-device can see is reported by ``MLACachePool.poll_error``.
+``mla_attention_decode_gb300.binding`` this marshals arguments only (compiled, in
+``_mla_cache.so``, for the calls of a decode step): every step runs in the
+library's CUDA kernels, nothing synchronises, and what only the device can see
+is reported by ``MLACachePool.poll_error``.
 
 A page table is a tuple ``(page_indptr, kv_indices, last_page_len)`` of int32
 CUDA tensors, the arrays that ``PagedMLADecoder`` takes.
@@ -14,7 +15,9 @@ CUDA tensors, the arrays that ``PagedMLADecoder`` takes.
 from __future__ import annotations
 
 import ctypes
-import struct
+import importlib.machinery
+import importlib.util
+import os
 import threading
 
 import torch
@@ -60,17 +63,17 @@ class mla_page_table(ctypes.Structure):
                 ("last_page_len", ctypes.c_void_p), ("batch", ctypes.c_int32), ("num_indices", ctypes.c_int32)]
 
 
-# The two structs of a call, packed into a bytes object of the call's own.
-_APPEND = struct.Struct("@7P7q2i")
-_TABLE = struct.Struct("@3P2i")
-
+EXT_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_mla_cache.so")
+_ENTRY_POINTS = ("append", "gather", "slots", "copy_pages", "fork", "resize", "free", "compact")
 _lock = threading.Lock()
 _lib: ctypes.CDLL | None = None
+_ext = None
 
 
 def load_library() -> ctypes.CDLL:
-    """The library with the entry points of mla_cache.h bound; raises if it is missing."""
-    global _lib
+    """The library with the entry points of mla_cache.h bound, and the extension that marshals
+    their arguments; raises if either is missing."""
+    global _lib, _ext
     if _lib is not None:
         return _lib
     lib = binding.load_library()
@@ -90,7 +93,16 @@ def load_library() -> ctypes.CDLL:
                 getattr(lib, name).restype = ctypes.c_int
             lib.mla_cache_workspace_bytes.argtypes = [P, i32]
             lib.mla_cache_workspace_bytes.restype = sz
-            _lib = lib
+            if not os.path.exists(EXT_PATH):
+                raise RuntimeError(f"{EXT_PATH} is missing: build it with `python -m mla_attention_decode_gb300.build`")
+            loader = importlib.machinery.ExtensionFileLoader("_mla_cache", EXT_PATH)
+            ext = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_mla_cache", EXT_PATH, loader=loader))
+            loader.exec_module(ext)
+            if ext.torch_version != torch.__version__.split("+")[0]:
+                raise RuntimeError(f"{EXT_PATH} was built for torch {ext.torch_version}, this is {torch.__version__}: "
+                                   "build it again")
+            ext.bind(*(ctypes.cast(getattr(lib, "mla_cache_" + n), ctypes.c_void_p).value for n in _ENTRY_POINTS))
+            _ext, _lib = ext, lib
     return _lib
 
 
@@ -154,6 +166,7 @@ class MLANorm:
         if len(dtypes) > 1:
             raise ValueError("the weights are all bf16 or all fp32")
         self.norm.weight_fp32 = int(torch.float32 in dtypes)
+        self.device_index = -1 if self.device is None else self.device.index
         self.address = ctypes.addressof(self.norm)
 
 
@@ -213,15 +226,15 @@ class MLACachePool:
         self.page_size, self.num_pages, self.num_layers = page_size, c.num_pages, c.num_layers
         if refs is None:
             refs = torch.zeros(self.num_pages, dtype=torch.int32, device=self.device)
-        self._check(refs, "refs", self.num_pages)
+        if refs.dtype != torch.int32 or refs.device != self.device or refs.shape != (self.num_pages,):
+            raise ValueError(f"refs is int32 [{self.num_pages}] on {self.device}")
         self.refs = refs
-        self._lib = load_library()
-        self._at = ctypes.addressof(c)
-        nbytes = int(self._lib.mla_cache_workspace_bytes(self._at, int(max_batch)))
+        lib = load_library()
+        nbytes = int(lib.mla_cache_workspace_bytes(ctypes.addressof(c), int(max_batch)))
         if nbytes == 0:
             raise MLAError(MLA_ERR_INVALID_ARG, "mla_cache_workspace_bytes")
         self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
-        self._ws, self._ws_bytes = self.workspace.data_ptr(), nbytes
+        self._core = _ext.core(ctypes.addressof(c), self.workspace.data_ptr(), nbytes, self.device.index)
 
     @classmethod
     def allocate(cls, kv_dtype, num_pages: int, page_size: int, num_layers: int = 1, device="cuda", kv_scale=1.0,
@@ -237,45 +250,6 @@ class MLACachePool:
             scale = torch.full((num_layers, rows, 18), 127, dtype=torch.uint8, device=device)
         return cls(kv, code, page_size, kv_scale=scale, max_batch=max_batch)
 
-    # -------------------------------------------------------------- arguments
-    def _check(self, t, what, size=None, dtype=torch.int32):
-        """An int32 (or ``dtype``) vector on the pool's device."""
-        if t.dtype != dtype or t.device != self.device or t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1):
-            raise ValueError(f"{what} is a contiguous {dtype} vector on {self.device}")
-        if size is not None and t.numel() != size:
-            raise ValueError(f"{what} has {size} entries, not {t.numel()}")
-
-    def _table(self, table, what):
-        indptr, indices, last = table
-        batch = indptr.numel() - 1
-        self._check(indptr, what + ".page_indptr")
-        self._check(indices, what + ".kv_indices")
-        self._check(last, what + ".last_page_len", batch)
-        return _TABLE.pack(indptr.data_ptr(), indices.data_ptr(), last.data_ptr(), batch, indices.numel())
-
-    def _call(self, name, stream, *args):
-        """The entry point on ``stream`` (a handle, a torch stream or None), with the pool's device current."""
-        fn = getattr(self._lib, name)
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        if torch.cuda.current_device() == self.device.index:
-            rc = fn(self._at, *args, handle)
-        else:
-            with torch.cuda.device(self.device):
-                rc = fn(self._at, *args, handle)
-        if rc != MLA_OK:
-            raise MLAError(rc, name)
-
-    def _empty(self, shape, dtype, stream):
-        """New memory that belongs to the stream the call runs on."""
-        if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
-
     def table(self, batch: int, num_indices: int):
         """Buffers of a page table of ``batch`` empty sequences, with room for ``num_indices`` entries."""
         return (torch.zeros(batch + 1, dtype=torch.int32, device=self.device),
@@ -287,127 +261,68 @@ class MLACachePool:
                q_pe=None, q_lat=None, q_out=None, layer: int = 0, stream=None):
         """Norms, rotates and stores T tokens' key rows; norms and rotates their queries into ``q_out``.
 
-        ``kv_lat`` [T, 512], ``kv_pe`` [T, 64] (None, None: queries only), ``slots`` [T] (-1: not stored),
-        ``positions`` [T] or [T, axes], ``q_pe`` [T, 16, 64], ``q_lat`` [T, 16, 512] (None: the latent columns of
-        ``q_out`` stay), ``q_out`` [T, 16, 576] contiguous; bf16, the last dimension consecutive."""
-        first = kv_lat if kv_lat is not None else q_pe
-        if first is None:
-            raise ValueError("append needs keys (kv_lat, kv_pe) or queries (q_pe, q_out)")
-        t = first.shape[0]
-        p, s = [0] * 7, [0] * 7
-        if kv_lat is not None:
-            if kv_pe is None or slots is None:
-                raise ValueError("keys come as kv_lat, kv_pe and slots")
-            self._part(kv_lat, "kv_lat", (t, 512))
-            self._part(kv_pe, "kv_pe", (t, 64))
-            self._check(slots, "slots", t)
-            p[0], p[1], p[2] = kv_lat.data_ptr(), kv_pe.data_ptr(), slots.data_ptr()
-            s[0], s[1] = kv_lat.stride(0), kv_pe.stride(0)
-        elif kv_pe is not None:
-            raise ValueError("keys come as kv_lat, kv_pe and slots")
-        if rope is not None:
-            if positions is None or positions.dtype != torch.int32 or positions.device != self.device:
-                raise ValueError(f"positions is int32 on {self.device}")
-            if positions.shape[0] != t or positions.dim() not in (1, 2) or (
-                    rope.num_axes > (positions.shape[1] if positions.dim() == 2 else 1)):
-                raise ValueError(f"positions is [{t}, {rope.num_axes}]: got {tuple(positions.shape)}")
-            if positions.dim() == 2 and positions.shape[1] > 1 and positions.stride(1) != 1:
-                raise ValueError("a token's positions are consecutive")
-            p[3], s[2] = positions.data_ptr(), positions.stride(0)
-        if q_pe is not None:
-            if q_out is None:
-                raise ValueError("queries come as q_pe and q_out")
-            self._part(q_pe, "q_pe", (t, 16, 64))
-            self._part(q_out, "q_out", (t, 16, 576))
-            if not q_out.is_contiguous():
-                raise ValueError("q_out is contiguous")
-            p[5], p[6], s[5], s[6] = q_pe.data_ptr(), q_out.data_ptr(), q_pe.stride(0), q_pe.stride(1)
-            if q_lat is not None:
-                self._part(q_lat, "q_lat", (t, 16, 512))
-                p[4], s[3], s[4] = q_lat.data_ptr(), q_lat.stride(0), q_lat.stride(1)
-        elif q_lat is not None or q_out is not None:
-            raise ValueError("queries come as q_pe and q_out")
-        if norm is not None and norm.device is not None and norm.device != self.device:
-            raise ValueError(f"the norm's weights are not on {self.device}")
-        self._call("mla_cache_append", stream, rope.address if rope is not None else None,
-                   norm.address if norm is not None else None, _APPEND.pack(*p, *s, t, int(layer)), self._ws)
-
-    def _part(self, x, what, shape):
-        if x.dtype != torch.bfloat16 or x.device != self.device or x.shape != shape or x.stride(-1) != 1:
-            raise ValueError(f"{what} is bf16 {list(shape)} on {self.device}, its last dimension consecutive: "
-                             f"got {x.dtype} {list(x.shape)}")
+        ``kv_lat`` [T, 512], ``kv_pe`` [T, 64] (with ``slots`` None, None, None: queries only), ``slots`` [T] (-1: not
+        stored), ``positions`` [T] or [T, axes], ``q_pe`` [T, 16, 64], ``q_lat`` [T, 16, 512] (None: the latent columns
+        of ``q_out`` stay), ``q_out`` [T, 16, 576] contiguous; bf16, the last dimension consecutive."""
+        rc = _ext.append(self._core, kv_lat, kv_pe, slots, rope, positions, norm, q_pe, q_lat, q_out, layer, stream)
+        if rc:
+            raise MLAError(rc, "mla_cache_append")
 
     def gather(self, slots, out=None, layer: int = 0, stream=None):
         """Rows ``slots`` of a layer as bf16 [T, 576] (``out``'s rows with slot -1 stay as they were; without
         ``out`` they are unset)."""
-        self._check(slots, "slots")
-        n = slots.numel()
-        if out is None:
-            out = self._empty((n, 576), torch.bfloat16, stream)
-        self._part(out, "out", (n, 576))
-        self._call("mla_cache_gather", stream, int(layer), slots.data_ptr(), n, out.data_ptr(),
-                   out.stride(0) if n > 1 else 576, self._ws)
+        rc, out = _ext.gather(self._core, slots, out, layer, stream)
+        if rc:
+            raise MLAError(rc, "mla_cache_gather")
         return out
 
     def slots(self, table, qo_indptr, num_tokens: int, slots=None, rows=None, stream=None):
         """The cache row of each sequence's last ``qo_indptr[b + 1] - qo_indptr[b]`` tokens, as ``slots`` [num_tokens]
         (-1 past the batch); with ``rows`` (int32, any stride) the tokens' places in their sequences too."""
-        n = int(num_tokens)
-        if slots is None:
-            slots = self._empty((n,), torch.int32, stream)
-        self._check(slots, "slots", n)
-        self._check(qo_indptr, "qo_indptr", table[0].numel())
-        if rows is not None and (rows.dtype != torch.int32 or rows.device != self.device or rows.shape != (n,)):
-            raise ValueError(f"rows is int32 [{n}] on {self.device}")
-        self._call("mla_cache_slots", stream, self._table(table, "table"), qo_indptr.data_ptr(), n, slots.data_ptr(),
-                   rows.data_ptr() if rows is not None else None, rows.stride(0) if rows is not None else 0, self._ws)
+        rc, slots = _ext.slots(self._core, table, qo_indptr, num_tokens, slots, rows, stream)
+        if rc:
+            raise MLAError(rc, "mla_cache_slots")
         return slots, rows
 
     # -------------------------------------------------------------- pages
     def copy_pages(self, src, dst, stream=None):
         """Page ``dst[i]`` becomes a copy of page ``src[i]``, in every layer."""
-        self._check(src, "src")
-        self._check(dst, "dst", src.numel())
-        self._call("mla_cache_copy_pages", stream, src.data_ptr(), dst.data_ptr(), src.numel(), self._ws)
+        rc = _ext.copy_pages(self._core, src, dst, stream)
+        if rc:
+            raise MLAError(rc, "mla_cache_copy_pages")
 
     def fork(self, table, parents, out, stream=None):
         """Writes to ``out`` a batch whose sequence n is a fork of ``table``'s sequence ``parents[n]``."""
-        self._check(parents, "parents", out[0].numel() - 1)
-        self._call("mla_cache_fork", stream, self.refs.data_ptr(), self._table(table, "table"), parents.data_ptr(),
-                   self._table(out, "out"), self._ws, self._ws_bytes)
+        rc = _ext.fork(self._core, self.refs, table, parents, out, stream)
+        if rc:
+            raise MLAError(rc, "mla_cache_fork")
         return out
 
     def resize(self, table, lengths, out, stream=None):
         """Writes to ``out`` the table whose sequence b has ``lengths[b]`` rows; ``table`` is void from then on."""
-        self._check(lengths, "lengths", out[0].numel() - 1)
-        self._call("mla_cache_resize", stream, self.refs.data_ptr(), self._table(table, "table"), lengths.data_ptr(),
-                   self._table(out, "out"), self._ws, self._ws_bytes)
+        rc = _ext.resize(self._core, self.refs, table, lengths, out, stream)
+        if rc:
+            raise MLAError(rc, "mla_cache_resize")
         return out
 
     def free(self, pages, stream=None):
         """Ends one hold on each of ``pages`` (-1 entries are skipped)."""
-        self._check(pages, "pages")
-        self._call("mla_cache_free", stream, self.refs.data_ptr(), pages.data_ptr(), pages.numel(), self._ws)
+        rc = _ext.free(self._core, self.refs, pages, stream)
+        if rc:
+            raise MLAError(rc, "mla_cache_free")
 
     def compact(self, kv_indices, out=None, stream=None):
         """Moves the pages in use to the front.  ``out``: (kv_indices, refs, live [1]) to write; without it the
         pool's counts are rewritten in place and the other two are new.  Returns the three."""
-        self._check(kv_indices, "kv_indices")
-        if out is None:
-            out = (self._empty(kv_indices.shape, torch.int32, stream), self.refs,
-                   self._empty((1,), torch.int32, stream))
-        indices, refs, live = out
-        self._check(indices, "out indices", kv_indices.numel())
-        self._check(refs, "out refs", self.num_pages)
-        self._check(live, "out live", 1)
-        self._call("mla_cache_compact", stream, self.refs.data_ptr(), refs.data_ptr(), kv_indices.data_ptr(),
-                   indices.data_ptr(), kv_indices.numel(), live.data_ptr(), self._ws, self._ws_bytes)
-        return out
+        indices, refs, live = (None, None, None) if out is None else out
+        rc, indices, refs, live = _ext.compact(self._core, self.refs, kv_indices, indices, refs, live, stream)
+        if rc:
+            raise MLAError(rc, "mla_cache_compact")
+        return indices, refs, live
 
     def poll_error(self, stream=None) -> int:
         """The error that a call on this pool met on the device (0: none), cleared; synchronises the stream."""
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if stream is not None and not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
         with torch.cuda.device(self.device):
-            return int(self._lib.mla_decode_poll_error(self._ws, handle))
+            return binding.mla_decode_poll_error(self.workspace, stream)
