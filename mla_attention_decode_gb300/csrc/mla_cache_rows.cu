@@ -9,6 +9,9 @@ namespace mla {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
+#ifndef MLA_APPEND_MANY
+#define MLA_APPEND_MANY 608
+#endif
 
 __device__ __forceinline__ void set_error(int32_t* error, int32_t code) {
   if (error) *error = code;
@@ -91,9 +94,18 @@ __device__ __forceinline__ uint32_t e8m0_of(float amax, float& inv) {
 // |x| as an ordering key in which NaN is largest (a plain fmaxf drops it).
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-// Weights of 8 latent columns from column c, as floats.
-__device__ __forceinline__ void load_weight8(const void* w, bool fp32, int c, float (&y)[8]) {
-  if (fp32) {
+// ---------------------------------------------------------------- append
+// A warp holds a row or head as 16 latent columns a lane (8 lane + j and 256 +
+// 8 lane + j: each load is a warp-wide run of 512 bytes) and the position columns
+// 2 lane and 2 lane + 1.
+struct Weights {  // of one lane's columns; 1 where the part has none
+  float lat[2][8], pe[2];
+};
+__device__ __forceinline__ void load_weights8(const void* w, bool fp32, int c, float (&y)[8]) {
+  if (!w) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = 1.f;
+  } else if (fp32) {
     const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(w) + c);
     const float4 a = __ldg(f), b = __ldg(f + 1);
     y[0] = a.x, y[1] = a.y, y[2] = a.z, y[3] = a.w, y[4] = b.x, y[5] = b.y, y[6] = b.z, y[7] = b.w;
@@ -101,96 +113,107 @@ __device__ __forceinline__ void load_weight8(const void* w, bool fp32, int c, fl
     unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + c)), y);
   }
 }
-__device__ __forceinline__ float load_weight(const void* w, bool fp32, int c) {
-  return fp32 ? __ldg(static_cast<const float*>(w) + c)
-              : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(w) + c) << 16);
+__device__ __forceinline__ void load_weights_lat(const mla_norm& n, int part, int lane, Weights& w) {
+  if (!(n.apply >> part & 1)) return;
+  load_weights8(n.weight[part], n.weight_fp32, 8 * lane, w.lat[0]);
+  load_weights8(n.weight[part], n.weight_fp32, 256 + 8 * lane, w.lat[1]);
+}
+__device__ __forceinline__ void load_weights_pe(const mla_norm& n, int part, int lane, Weights& w) {
+  if (!(n.apply >> part & 1)) return;
+  const void* p = n.weight[part];
+  w.pe[0] = w.pe[1] = 1.f;
+  if (p && n.weight_fp32) {
+    const float2 f = __ldg(static_cast<const float2*>(p) + lane);
+    w.pe[0] = f.x, w.pe[1] = f.y;
+  } else if (p) {
+    const uint32_t u = __ldg(static_cast<const uint32_t*>(p) + lane);
+    w.pe[0] = __uint_as_float(u << 16), w.pe[1] = __uint_as_float(u & 0xffff0000u);
+  }
 }
 
-// ---------------------------------------------------------------- append
-// The 512 latent columns of a row or head, 16 a lane: columns 8 * lane + j and
-// 256 + 8 * lane + j, so that each load is a warp-wide run of 512 bytes.
-struct Lat {
-  float x[2][8];
-};
-__device__ __forceinline__ void load_lat(const uint16_t* src, int lane, Lat& v) {
-  const uint4* s = reinterpret_cast<const uint4*>(src);
-  const uint4 a = s[lane], b = s[32 + lane];
-  unpack_bf16x8(a, v.x[0]);
-  unpack_bf16x8(b, v.x[1]);
-}
-__device__ __forceinline__ void norm_lat(Lat& v, const mla_norm& n, int part, int lane) {
+// y = x / sqrt(mean(x^2) + eps) * w over the 512 latent columns.
+__device__ __forceinline__ void norm_lat(const mla_norm& n, int part, const Weights& w, float (&x)[2][8]) {
   if (!(n.apply >> part & 1)) return;
   float ss = 0.f;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(v.x[h][j], v.x[h][j], ss);
+    for (int j = 0; j < 8; ++j) ss = fmaf(x[h][j], x[h][j], ss);
   const float r = rsqrtf(warp_sum(ss) * (1.f / kLat) + n.eps);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-    if (n.weight[part]) load_weight8(n.weight[part], n.weight_fp32, 256 * h + 8 * lane, w);
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v.x[h][j] = v.x[h][j] * r * w[j];
-  }
+    for (int j = 0; j < 8; ++j) x[h][j] = x[h][j] * r * w.lat[h][j];
 }
 
-// The cosine and sine of this lane's pair (lane i: pair i) for token t.  The
-// turn count pos * inv_freq / 2 pi matters modulo 1 only: with inv_freq / 2 pi
+// The rotation as this lane applies it: column 2 lane + k becomes
+// x_k c[k] + partner_k s[k], the sign folded into s.
+struct Turn {
+  float c[2], s[2];
+};
+// The turn count pos * inv_freq / 2 pi matters modulo 1 only: with inv_freq / 2 pi
 // in units of 2^-64 turns the 64-bit product wraps to exactly that, at any
 // position, and its top 32 bits leave an angle error below 2 pi * 2^-33.
-__device__ __forceinline__ float2 cos_sin(const AppendParams& p, int t, int lane) {
-  float c = 1.f, s = 0.f;
-  if (p.rope.num_axes > 0) {
-    const int64_t pos = p.a.positions[(int64_t)t * p.a.position_stride + p.rope.axis[lane]];
-    const uint64_t turns = (uint64_t)pos * p.rope.turn[lane] + 0x80000000ull;
-    sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);
-    c *= p.rope.scale;
-    s *= p.rope.scale;
+// Lane i finds pair i's angle; paired halves (i, i + 32) then fetch the two pairs
+// that their columns belong to.
+__device__ __forceinline__ Turn turn_of(const AppendParams& p, int t, int lane) {
+  Turn r;
+  if (p.rope.num_axes == 0) return r;  // no rotation: not used
+  // through the parameter's address, not the constant bank: each lane reads an
+  // entry of its own, which the constant cache would serve one lane at a time
+  uint64_t step;
+  uint32_t axis;
+  asm("ld.u64 %0, [%1];" : "=l"(step) : "l"(&p.rope.turn[lane]));
+  asm("ld.u8 %0, [%1];" : "=r"(axis) : "l"(&p.rope.axis[lane]));
+  const int64_t pos = p.a.positions[(int64_t)t * p.a.position_stride + axis];
+  const uint64_t turns = (uint64_t)pos * step + 0x80000000ull;
+  float c, s;
+  sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);
+  c *= p.rope.scale;
+  s *= p.rope.scale;
+  if (p.rope.interleaved) {
+    r.c[0] = r.c[1] = c;
+    r.s[0] = -s;
+    r.s[1] = s;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int pair = (2 * lane + k) & 31;
+      r.c[k] = __shfl_sync(kFull, c, pair);
+      const float sk = __shfl_sync(kFull, s, pair);
+      r.s[k] = lane < 16 ? -sk : sk;
+    }
   }
-  return make_float2(c, s);
+  return r;
 }
 
-// The 64 position columns normed and rotated; on return lane i holds columns
-// (2i, 2i + 1), whatever the pairing.
-__device__ __forceinline__ float2 turned_pe(const uint16_t* src, const AppendParams& p, int part, float2 cs,
-                                            int lane) {
-  const bool inter = p.rope.interleaved;
-  const int c0 = inter ? 2 * lane : lane, c1 = inter ? 2 * lane + 1 : lane + 32;
-  float a, b;
-  if (inter) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(src + c0);
-    a = __uint_as_float(w << 16);
-    b = __uint_as_float(w & 0xffff0000u);
-  } else {
-    a = __uint_as_float((uint32_t)src[c0] << 16);
-    b = __uint_as_float((uint32_t)src[c1] << 16);
-  }
+// The lane's two position columns (`u`: their bf16 pair) normed and rotated.
+__device__ __forceinline__ float2 turned_pe(const AppendParams& p, int part, const Weights& w, const Turn& r,
+                                            uint32_t u, int lane) {
+  float x0 = __uint_as_float(u << 16), x1 = __uint_as_float(u & 0xffff0000u);
   if (p.norm.apply >> part & 1) {
-    const float r = rsqrtf(warp_sum(fmaf(a, a, b * b)) * (1.f / kPe) + p.norm.eps);
-    const void* w = p.norm.weight[part];
-    a = a * r * (w ? load_weight(w, p.norm.weight_fp32, c0) : 1.f);
-    b = b * r * (w ? load_weight(w, p.norm.weight_fp32, c1) : 1.f);
+    const float q = rsqrtf(warp_sum(fmaf(x0, x0, x1 * x1)) * (1.f / kPe) + p.norm.eps);
+    x0 = x0 * q * w.pe[0];
+    x1 = x1 * q * w.pe[1];
   }
   // without a rotation nothing is multiplied: an infinity would make its partner NaN
-  const bool turn = p.rope.num_axes > 0;
-  const float y0 = turn ? fmaf(a, cs.x, -b * cs.y) : a, y1 = turn ? fmaf(a, cs.y, b * cs.x) : b;
-  if (inter) return make_float2(y0, y1);
-  // columns 2i, 2i + 1 are the first elements of pairs 2i, 2i + 1 (i < 16) or
-  // the second elements of pairs 2i - 32, 2i - 31
-  const int from = 2 * lane & 31;
-  const float u0 = __shfl_sync(kFull, y0, from), u1 = __shfl_sync(kFull, y0, from + 1);
-  const float v0 = __shfl_sync(kFull, y1, from), v1 = __shfl_sync(kFull, y1, from + 1);
-  return lane < 16 ? make_float2(u0, u1) : make_float2(v0, v1);
+  if (p.rope.num_axes == 0) return make_float2(x0, x1);
+  float y0 = x1, y1 = x0;  // the partners of columns 2 lane, 2 lane + 1
+  if (!p.rope.interleaved) {
+    y0 = __shfl_xor_sync(kFull, x0, 16);
+    y1 = __shfl_xor_sync(kFull, x1, 16);
+  }
+  return make_float2(fmaf(x0, r.c[0], y0 * r.s[0]), fmaf(x1, r.c[1], y1 * r.s[1]));
 }
 
 // One key row into row `slot` of the cache, in its format.
 template <int kDtype>
-__device__ __forceinline__ void store_row(const AppendParams& p, int32_t slot, const Lat& lat, float2 pe, int lane) {
+__device__ __forceinline__ void store_row(const AppendParams& p, int32_t slot, const float (&lat)[2][8], float2 pe,
+                                          int lane) {
   if (kDtype == MLA_KV_BF16) {
     uint8_t* dst = p.cache.kv + (int64_t)slot * (2 * kRow);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) reinterpret_cast<uint4*>(dst)[32 * h + lane] = pack_bf16x8(lat.x[h]);
+    for (int h = 0; h < 2; ++h) reinterpret_cast<uint4*>(dst)[32 * h + lane] = pack_bf16x8(lat[h]);
     reinterpret_cast<uint32_t*>(dst + 2 * kLat)[lane] = pack_bf16x2(pe.x, pe.y);
   } else if (kDtype == MLA_KV_FP8_E4M3) {
     // the quotient is the rounded one (not a product with the reciprocal): the
@@ -202,7 +225,7 @@ __device__ __forceinline__ void store_row(const AppendParams& p, int32_t slot, c
       uint32_t w[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        w[j] = f32x2_to_e4m3x2(__fdiv_rn(lat.x[h][2 * j], sc), __fdiv_rn(lat.x[h][2 * j + 1], sc));
+        w[j] = f32x2_to_e4m3x2(__fdiv_rn(lat[h][2 * j], sc), __fdiv_rn(lat[h][2 * j + 1], sc));
       reinterpret_cast<uint2*>(dst)[32 * h + lane] = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
     }
     reinterpret_cast<uint16_t*>(dst + kLat)[lane] =
@@ -214,13 +237,13 @@ __device__ __forceinline__ void store_row(const AppendParams& p, int32_t slot, c
     for (int h = 0; h < 2; ++h) {  // a block of 32 columns: four lanes
       uint32_t m = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, abs_bits(lat.x[h][j]));
+      for (int j = 0; j < 8; ++j) m = max(m, abs_bits(lat[h][j]));
       m = max(m, __shfl_xor_sync(kFull, m, 1));
       m = max(m, __shfl_xor_sync(kFull, m, 2));
       float inv, y[8];
       const uint32_t byte = e8m0_of(__uint_as_float(m), inv);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = byte == 255 ? 0.f : lat.x[h][j] * inv;
+      for (int j = 0; j < 8; ++j) y[j] = byte == 255 ? 0.f : lat[h][j] * inv;
       reinterpret_cast<uint32_t*>(dst)[32 * h + lane] = pack_e2m1x8(y);
       if ((lane & 3) == 0) sdst[8 * h + (lane >> 2)] = (uint8_t)byte;
     }
@@ -237,47 +260,75 @@ __device__ __forceinline__ void store_row(const AppendParams& p, int32_t slot, c
   }
 }
 
-// One warp per key row or query head of a token (17 parts; 16 or 1 where the
-// call has no keys or no queries).
-template <int kDtype>
+// One warp per key row (the first key_ctas CTAs), or per kHeads query heads of a
+// token, all of whose columns are in flight before the first is used.
+// kQ: 0 no queries, 1 their position columns, 2 their latent columns too.
+template <int kDtype, int kQ, int kHeads>
 __global__ void __launch_bounds__(256) mla_append_kernel(const __grid_constant__ AppendParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int keys = p.a.kv_lat ? 1 : 0, parts = keys + (p.a.q_pe ? kQueryHeads : 0);
-  const int64_t task = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (task >= (int64_t)p.a.num_tokens * parts) return;
-  const int t = (int)(task / parts), part = (int)(task % parts);
-  const float2 cs = cos_sin(p, t, lane);
-  if (part < keys) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Weights w;
+  if ((int)blockIdx.x < p.key_ctas) {
+    const int t = (int)blockIdx.x * 8 + warp;
+    if (t >= p.a.num_tokens) return;
     const int32_t slot = p.a.slots[t];
     if (slot < 0 || slot >= p.cache.rows) {
       if (slot != -1 && lane == 0) set_error(p.error, MLA_ERR_DEVICE_INDEX);
       return;
     }
-    Lat v;
-    load_lat(static_cast<const uint16_t*>(p.a.kv_lat) + (int64_t)t * p.a.kv_lat_stride, lane, v);
-    norm_lat(v, p.norm, MLA_PART_KV_LAT, lane);
-    const float2 pe = turned_pe(static_cast<const uint16_t*>(p.a.kv_pe) + (int64_t)t * p.a.kv_pe_stride, p,
-                                MLA_PART_KV_PE, cs, lane);
-    store_row<kDtype>(p, slot, v, pe, lane);
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.a.kv_lat) +
+                                                      (int64_t)t * p.a.kv_lat_stride);
+    const uint4 a = src[lane], b = src[32 + lane];
+    const uint32_t u = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.a.kv_pe) +
+                                                         (int64_t)t * p.a.kv_pe_stride)[lane];
+    load_weights_lat(p.norm, MLA_PART_KV_LAT, lane, w);
+    load_weights_pe(p.norm, MLA_PART_KV_PE, lane, w);
+    const Turn r = turn_of(p, t, lane);
+    float x[2][8];
+    unpack_bf16x8(a, x[0]);
+    unpack_bf16x8(b, x[1]);
+    norm_lat(p.norm, MLA_PART_KV_LAT, w, x);
+    store_row<kDtype>(p, slot, x, turned_pe(p, MLA_PART_KV_PE, w, r, u, lane), lane);
     return;
   }
-  const int h = part - keys;
-  uint16_t* out = static_cast<uint16_t*>(p.a.q_out) + ((int64_t)t * kQueryHeads + h) * kRow;
-  const float2 pe = turned_pe(static_cast<const uint16_t*>(p.a.q_pe) + (int64_t)t * p.a.q_pe_token_stride +
-                                  (int64_t)h * p.a.q_pe_head_stride,
-                              p, MLA_PART_Q_PE, cs, lane);
-  __syncwarp();  // in place: every lane has read its columns before any is written
-  reinterpret_cast<uint32_t*>(out + kLat)[lane] = pack_bf16x2(pe.x, pe.y);
-  if (p.a.q_lat) {
-    Lat v;
-    load_lat(static_cast<const uint16_t*>(p.a.q_lat) + (int64_t)t * p.a.q_lat_token_stride +
-                 (int64_t)h * p.a.q_lat_head_stride,
-             lane, v);
-    norm_lat(v, p.norm, MLA_PART_Q_LAT, lane);
+  if (kQ == 0) return;
+  constexpr int kGroups = kQueryHeads / kHeads;
+  const int64_t task = (int64_t)((int)blockIdx.x - p.key_ctas) * 8 + warp;
+  const int t = (int)(task / kGroups), h0 = (int)(task % kGroups) * kHeads;
+  if (t >= p.a.num_tokens) return;
+  const uint16_t* pe = static_cast<const uint16_t*>(p.a.q_pe) + (int64_t)t * p.a.q_pe_token_stride +
+                       (int64_t)h0 * p.a.q_pe_head_stride;
+  uint8_t* out = static_cast<uint8_t*>(p.a.q_out) + ((int64_t)t * kQueryHeads + h0) * (2 * kRow);
+  uint32_t u[kHeads];
+  uint4 v[kQ == 2 ? kHeads : 1][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) reinterpret_cast<uint4*>(out)[32 * i + lane] = pack_bf16x8(v.x[i]);
+  for (int h = 0; h < kHeads; ++h) u[h] = reinterpret_cast<const uint32_t*>(pe + h * p.a.q_pe_head_stride)[lane];
+  if (kQ == 2) {
+    const uint16_t* lat = static_cast<const uint16_t*>(p.a.q_lat) + (int64_t)t * p.a.q_lat_token_stride +
+                          (int64_t)h0 * p.a.q_lat_head_stride;
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        v[h][i] = reinterpret_cast<const uint4*>(lat + h * p.a.q_lat_head_stride)[32 * i + lane];
+    load_weights_lat(p.norm, MLA_PART_Q_LAT, lane, w);
+  }
+  load_weights_pe(p.norm, MLA_PART_Q_PE, lane, w);
+  const Turn r = turn_of(p, t, lane);
+#pragma unroll
+  for (int h = 0; h < kHeads; ++h) {
+    const float2 y = turned_pe(p, MLA_PART_Q_PE, w, r, u[h], lane);
+    uint8_t* row = out + h * (2 * kRow);
+    reinterpret_cast<uint32_t*>(row + 2 * kLat)[lane] = pack_bf16x2(y.x, y.y);
+    if (kQ == 2) {
+      float x[2][8];
+      unpack_bf16x8(v[h][0], x[0]);
+      unpack_bf16x8(v[h][1], x[1]);
+      norm_lat(p.norm, MLA_PART_Q_LAT, w, x);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) reinterpret_cast<uint4*>(row)[32 * i + lane] = pack_bf16x8(x[i]);
+    }
   }
 }
 
@@ -371,15 +422,25 @@ __global__ void __launch_bounds__(128) mla_slots_kernel(const __grid_constant__ 
 
 }  // namespace
 
-cudaError_t launch_append(const AppendParams& p, int kv_dtype, cudaStream_t s) {
-  const int64_t parts = (p.a.kv_lat ? 1 : 0) + (p.a.q_pe ? kQueryHeads : 0);
-  const int64_t tasks = parts * p.a.num_tokens;
-  if (tasks == 0) return cudaSuccess;
-  const unsigned grid = (unsigned)((tasks + 7) / 8);
+namespace {
+template <int kDtype>
+cudaError_t launch_append_to(AppendParams& p, cudaStream_t s) {
+  const int64_t T = p.a.num_tokens;
+  p.key_ctas = p.a.kv_lat ? (int32_t)((T + 7) / 8) : 0;
+  const auto grid = [&](int heads) { return (unsigned)(p.key_ctas + (T * (kQueryHeads / heads) + 7) / 8); };
+  if (!p.a.q_pe) return launch_chained(mla_append_kernel<kDtype, 0, 16>, (unsigned)p.key_ctas, 256, s, p);
+  if (p.a.q_lat) return launch_chained(mla_append_kernel<kDtype, 2, 4>, grid(4), 256, s, p);
+  if (T >= MLA_APPEND_MANY) return launch_chained(mla_append_kernel<kDtype, 1, 16>, grid(16), 256, s, p);
+  return launch_chained(mla_append_kernel<kDtype, 1, 4>, grid(4), 256, s, p);
+}
+}  // namespace
+
+cudaError_t launch_append(AppendParams p, int kv_dtype, cudaStream_t s) {
+  if (p.a.num_tokens == 0 || (!p.a.kv_lat && !p.a.q_pe)) return cudaSuccess;
   switch (kv_dtype) {
-    case MLA_KV_BF16: return launch_chained(mla_append_kernel<MLA_KV_BF16>, grid, 256, s, p);
-    case MLA_KV_FP8_E4M3: return launch_chained(mla_append_kernel<MLA_KV_FP8_E4M3>, grid, 256, s, p);
-    default: return launch_chained(mla_append_kernel<MLA_KV_MXFP4>, grid, 256, s, p);
+    case MLA_KV_BF16: return launch_append_to<MLA_KV_BF16>(p, s);
+    case MLA_KV_FP8_E4M3: return launch_append_to<MLA_KV_FP8_E4M3>(p, s);
+    default: return launch_append_to<MLA_KV_MXFP4>(p, s);
   }
 }
 
