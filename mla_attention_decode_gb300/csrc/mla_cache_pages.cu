@@ -1,21 +1,33 @@
 // mla_cache_pages.cu -- pages of the latent cache copied, forked, resized, freed
 // and compacted (include/mla_cache.h).
 //
-// A call that hands out or moves pages is two kernels: one CTA decides (prefix
-// sums over the sequences and over the pages' counts), then a grid carries it
-// out (table entries, counts, rows).  Ranks come from prefix sums, never from
-// the order in which threads arrive, so results are the same from run to run;
-// the only atomics add to counts.
+// A call that hands out or moves pages has two parts: a cluster of CTAs decides
+// (prefix sums over the sequences and over the pages' counts), then a grid, or
+// the same cluster where there is little to do, carries it out (table entries,
+// counts, rows).  Ranks come from prefix sums, never from the order in which
+// threads arrive, so results are the same from run to run; the only atomics add
+// to counts.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include "mla_cache_internal.h"
 #include "mla_ptx.cuh"
 
+namespace cg = cooperative_groups;
+
 namespace mla {
 namespace {
 
+#ifndef MLA_MOVE_CTAS
+#define MLA_MOVE_CTAS 2
+#endif
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kPlan = 1024;             // threads of a deciding CTA
+constexpr int kPlan = 512;              // threads of a deciding CTA
+constexpr int kCluster = 8;             // deciding CTAs
+#ifndef MLA_CLUSTER_FORK_BYTES
+#define MLA_CLUSTER_FORK_BYTES (2 << 20)
+#endif
+constexpr int64_t kClusterEntries = 32768, kClusterForkBytes = MLA_CLUSTER_FORK_BYTES, kClusterResizeBytes = 16 << 20;
 constexpr unsigned kMaxGrid = 152 * 8;  // CTAs of 256 threads that carry out
 
 __device__ __forceinline__ void set_error(int32_t* error, int32_t code) {
@@ -76,7 +88,7 @@ __device__ __forceinline__ void move_segment(const PageBytes& c, int src, int ds
   }
 }
 
-__global__ void __launch_bounds__(256) mla_copy_pages_kernel(const __grid_constant__ CopyParams p) {
+__global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_copy_pages_kernel(const __grid_constant__ CopyParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -95,32 +107,48 @@ __global__ void __launch_bounds__(256) mla_copy_pages_kernel(const __grid_consta
 }
 
 // ---------------------------------------------------------------- prefix sums
-__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {  // inclusive
+// Exclusive prefix sums of kN values over the CTA's kPlan threads, and the
+// totals.  Every thread of the CTA calls.
+template <int kN, class T>
+struct Scan {
+  static constexpr int kWarps = kPlan / 32;
+  T part[kN][kWarps], total[kN];
+  __device__ __forceinline__ void run(T (&v)[kN], T (&sum)[kN]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    T in[kN];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(kFull, v, o);
-    if (lane >= o) v += u;
+    for (int k = 0; k < kN; ++k) in[k] = v[k];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        const T u = __shfl_up_sync(kFull, in[k], o);
+        if (lane >= o) in[k] += u;
+      }
+    if (lane == 31)
+#pragma unroll
+      for (int k = 0; k < kN; ++k) part[k][warp] = in[k];
+    __syncthreads();
+    if (warp < kN) {  // warp k scans value k's warp totals
+      const T x = lane < kWarps ? part[warp][lane] : T(0);
+      T s = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const T u = __shfl_up_sync(kFull, s, o);
+        if (lane >= o) s += u;
+      }
+      if (lane < kWarps) part[warp][lane] = s - x;
+      if (lane == 31) total[warp] = s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      v[k] = in[k] - v[k] + part[k][warp];
+      sum[k] = total[k];
+    }
+    __syncthreads();  // the arrays may be written again
   }
-  return v;
-}
-// Exclusive prefix sum of v over the CTA's kPlan threads, and the total.
-// `part` is 33 words of shared memory; every thread of the CTA calls.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int64_t& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t in = warp_scan(v, lane);
-  if (lane == 31) part[warp] = in;
-  __syncthreads();
-  if (warp == 0) {
-    const int64_t x = part[lane], s = warp_scan(x, lane);
-    part[lane] = s - x;
-    if (lane == 31) part[32] = s;
-  }
-  __syncthreads();
-  const int64_t ex = in - v + part[warp];
-  total = part[32];
-  __syncthreads();  // `part` may be written again
-  return ex;
-}
+};
 
 // The sequence that owns entry e of a table: indptr[n] <= e < indptr[n + 1].
 __device__ __forceinline__ int owner(const int32_t* indptr, int batch, int e) {
@@ -137,13 +165,15 @@ __device__ __forceinline__ int owner(const int32_t* indptr, int batch, int e) {
 // Sequence n of `to` keeps the first `first` pages of its parent and gets fresh
 // pages from there on; the first of them takes a part-filled page's rows where
 // that page has to be copied.
-__global__ void __launch_bounds__(kPlan) mla_table_plan_kernel(const __grid_constant__ TableParams p) {
-  __shared__ int64_t part[33];
-  __shared__ int32_t s_bad, s_release;
-  pdl_wait_primary();
-  pdl_launch_dependents();
+
+// What the first CTA of the cluster decides.
+struct TableTotals {
+  int64_t pages, fresh, copies;
+  int32_t bad, release;
+};
+__device__ __forceinline__ void plan_sequences(const TableParams& p, Scan<3, int64_t>& scan, TableTotals& s) {
   const int tid = threadIdx.x, N = p.to.batch, P = p.c.page_size, shift = p.c.page_shift;
-  if (tid == 0) s_bad = s_release = 0;
+  if (tid == 0) s.bad = s.release = 0;
   __syncthreads();
   int64_t pages = 0, fresh = 0, copies = 0;
   for (int base = 0; base < N; base += kPlan) {
@@ -151,25 +181,20 @@ __global__ void __launch_bounds__(kPlan) mla_table_plan_kernel(const __grid_cons
     int64_t cnt = 0;
     int32_t first = 0, src = -1, rows = 0;
     if (n < N) {
-      const int par = p.forks ? p.by[n] : n;
+      const int by = p.by[n], par = p.forks ? by : n;
       bool ok = par >= 0 && par < p.from.batch;
       int64_t a = 0, b = 0, len = 0, want = 0;
       if (ok) {
         a = p.from.page_indptr[par];
         b = p.from.page_indptr[par + 1];
-        ok = 0 <= a && a <= b && b <= p.from.num_indices;
-      }
-      if (ok && b > a) {
         const int32_t last = p.from.last_page_len[par];
-        ok = last >= 1 && last <= P;
-        len = (b - a - 1) * P + last;
-      }
-      if (ok) {
-        want = p.forks ? len : p.by[n];
-        ok = want >= 0;
+        ok = 0 <= a && a <= b && b <= p.from.num_indices && (a == b || (last >= 1 && last <= P));
+        if (a < b) len = (b - a - 1) * P + last;
+        want = p.forks ? len : by;
+        ok = ok && want >= 0;
       }
       if (!ok) {
-        s_bad = 1;
+        s.bad = 1;
       } else {
         cnt = (want + P - 1) >> shift;
         const int64_t keep = min(cnt, b - a), r0 = min(len, want);
@@ -182,62 +207,54 @@ __global__ void __launch_bounds__(kPlan) mla_table_plan_kernel(const __grid_cons
             first -= 1;
           }
         }
-        if (!p.forks && b - a > first) s_release = 1;
+        if (!p.forks && b - a > first) s.release = 1;
         p.to.last_page_len[n] = cnt ? (int32_t)(want - (cnt - 1) * P) : 0;
         p.ws.first[n] = first;
       }
     }
-    int64_t total;
-    const int64_t at = block_scan(cnt, part, total);
-    if (n < N) p.to.page_indptr[n + 1] = (int32_t)(pages + at + cnt);
-    pages += total;
-    const int64_t fr = fresh + block_scan(cnt - first, part, total);
-    if (n < N) p.ws.fresh[n] = (int32_t)fr;
-    fresh += total;
-    const int64_t c = copies + block_scan(src >= 0, part, total);
+    int64_t v[3] = {cnt, cnt - first, src >= 0}, sum[3];
+    scan.run(v, sum);
+    const int64_t fr = fresh + v[1], c = copies + v[2];
+    if (n < N) {
+      p.to.page_indptr[n + 1] = (int32_t)(pages + v[0] + cnt);
+      p.ws.fresh[n] = (int32_t)fr;
+    }
     if (src >= 0) {
       p.ws.copy_src[c] = src;
       p.ws.copy_rank[c] = (int32_t)fr;
       p.ws.copy_rows[c] = rows;
     }
-    copies += total;
-  }
-  int32_t err = s_bad || pages > p.to.num_indices ? MLA_ERR_DEVICE_INDEX : (fresh > p.c.num_pages ? MLA_ERR_OUT_OF_PAGES : 0);
-  // the free pages of lowest number, as many as are needed
-  int64_t found = 0;
-  for (int base = 0; err == 0 && found < fresh && base < p.c.num_pages; base += kPlan) {
-    const int pg = base + tid;
-    const bool is_free = pg < p.c.num_pages && p.refs[pg] == 0;
-    int64_t total;
-    const int64_t k = found + block_scan(is_free, part, total);
-    if (is_free && k < fresh) p.ws.list[k] = pg;
-    found += total;
-  }
-  if (err == 0 && found < fresh) err = MLA_ERR_OUT_OF_PAGES;
-  __syncthreads();
-  if (err == 0) {
-    for (int64_t k = tid; k < fresh; k += kPlan) p.refs[p.ws.list[k]] = 1;
-    if (tid == 0) p.to.page_indptr[0] = 0;
-  } else {
-    for (int n = tid; n <= N; n += kPlan) {
-      p.to.page_indptr[n] = 0;
-      if (n < N) p.to.last_page_len[n] = 0;
-    }
+    pages += sum[0];
+    fresh += sum[1];
+    copies += sum[2];
   }
   if (tid == 0) {
-    p.ws.head[kHeadOk] = err == 0;
-    p.ws.head[kHeadCopies] = (int32_t)copies;
-    p.ws.head[kHeadReleases] = s_release;
-    if (err) set_error(p.ws.err, err);
+    p.to.page_indptr[0] = 0;
+    s.pages = pages;
+    s.fresh = fresh;
+    s.copies = copies;
   }
 }
 
-__global__ void __launch_bounds__(256) mla_table_apply_kernel(const __grid_constant__ TableParams p) {
-  pdl_wait_primary();
-  pdl_launch_dependents();
-  if (!p.ws.head[kHeadOk]) return;
+// Which of the 8 pages from pg on are free, as bits (refs is 16-byte aligned
+// and pg a multiple of 8).
+__device__ __forceinline__ uint32_t free_bits(const int32_t* refs, int64_t pg, int64_t end) {
+  if (pg + 8 <= end) {
+    const int4 a = *reinterpret_cast<const int4*>(refs + pg), b = *reinterpret_cast<const int4*>(refs + pg + 4);
+    return (uint32_t)(a.x == 0) | (uint32_t)(a.y == 0) << 1 | (uint32_t)(a.z == 0) << 2 | (uint32_t)(a.w == 0) << 3 |
+           (uint32_t)(b.x == 0) << 4 | (uint32_t)(b.y == 0) << 5 | (uint32_t)(b.z == 0) << 6 |
+           (uint32_t)(b.w == 0) << 7;
+  }
+  uint32_t m = 0;
+  for (int i = 0; i < 8; ++i)
+    if (pg + i < end && refs[pg + i] == 0) m |= 1u << i;
+  return m;
+}
+
+// Carries a decided call out: table entries and the counts of shared pages,
+// what a resized sequence no longer holds, rows of part-filled pages.
+__device__ __forceinline__ void apply_table(const TableParams& p, int64_t at, int64_t step) {
   const int lane = threadIdx.x & 31, N = p.to.batch;
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
   const int total = p.to.page_indptr[N];
   for (int64_t e = at; e < total; e += step) {
     const int n = owner(p.to.page_indptr, N, (int)e);
@@ -256,7 +273,7 @@ __global__ void __launch_bounds__(256) mla_table_apply_kernel(const __grid_const
     }
     p.to.kv_indices[e] = page;
   }
-  if (p.ws.head[kHeadReleases]) {  // resize: what a sequence no longer holds
+  if (p.ws.head[kHeadReleases]) {
     const int B = p.from.batch, end = p.from.page_indptr[B];
     for (int64_t e = p.from.page_indptr[0] + at; e < end; e += step) {
       const int n = owner(p.from.page_indptr, B, (int)e);
@@ -277,6 +294,87 @@ __global__ void __launch_bounds__(256) mla_table_apply_kernel(const __grid_const
     const int rest = (int)(task - i * per), l = rest / segs, seg = rest - l * segs;
     move_segment(p.c, p.ws.copy_src[i], p.ws.list[p.ws.copy_rank[i]], p.ws.copy_rows[i], l, seg, ks, lane);
   }
+}
+
+// The cluster's first CTA goes over the sequences while the others count the
+// free pages of a slice each; then those list the free pages of lowest number,
+// as many as are needed.  kApply: and the cluster carries it out.
+template <bool kApply>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlan, 1)
+    mla_table_plan_kernel(const __grid_constant__ TableParams p) {
+  __shared__ Scan<3, int64_t> scan;
+  __shared__ Scan<1, int32_t> scan1;
+  __shared__ TableTotals s_tot;
+  __shared__ int32_t s_free;
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, rank = (int)cluster.block_rank();
+  const int64_t pages = p.c.num_pages;
+  // slices of the CTAs 1 .. kCluster - 1, multiples of 8 pages
+  const int64_t slice = (pages + (kCluster - 1) * 8 - 1) / ((kCluster - 1) * 8) * 8;
+  const int64_t begin = min(pages, (rank - 1) * slice), end = min(pages, rank * slice);
+  uint32_t bits = 0;  // of this thread's 8 pages of the slice's first pass
+  if (rank == 0) {
+    plan_sequences(p, scan, s_tot);
+  } else {
+    int32_t v[1] = {0}, sum[1];
+    for (int64_t pg = begin + 8 * tid; pg < end; pg += 8 * kPlan) {
+      const uint32_t m = free_bits(p.refs, pg, end);
+      if (pg < begin + 8 * kPlan) bits = m;
+      v[0] += __popc(m);
+    }
+    scan1.run(v, sum);
+    if (tid == 0) s_free = sum[0];
+  }
+  cluster.sync();
+  const TableTotals tot = *cluster.map_shared_rank(&s_tot, 0);
+  int64_t before = 0, all = 0;
+  for (int r = 1; r < kCluster; ++r) {
+    const int32_t n = *cluster.map_shared_rank(&s_free, r);
+    if (r < rank) before += n;
+    all += n;
+  }
+  const int32_t err = tot.bad || tot.pages > p.to.num_indices ? MLA_ERR_DEVICE_INDEX
+                                                              : (tot.fresh > all ? MLA_ERR_OUT_OF_PAGES : 0);
+  if (rank == 0) {
+    if (err) {
+      for (int n = tid; n <= p.to.batch; n += kPlan) {
+        p.to.page_indptr[n] = 0;
+        if (n < p.to.batch) p.to.last_page_len[n] = 0;
+      }
+      if (tid == 0) set_error(p.ws.err, err);
+    }
+    if (tid == 0) {
+      p.ws.head[kHeadOk] = err == 0;
+      p.ws.head[kHeadCopies] = (int32_t)tot.copies;
+      p.ws.head[kHeadReleases] = tot.release;
+    }
+  } else if (err == 0) {
+    for (int64_t base = begin; base < end && before < tot.fresh; base += 8 * kPlan) {
+      const int64_t pg = base + 8 * tid;
+      uint32_t m = base == begin ? bits : (pg < end ? free_bits(p.refs, pg, end) : 0u);
+      int32_t v[1] = {__popc(m)}, sum[1];
+      scan1.run(v, sum);
+      for (int64_t k = before + v[0]; m != 0 && k < tot.fresh; ++k) {
+        const int32_t free_page = (int32_t)pg + __ffs(m) - 1;
+        m &= m - 1;
+        p.ws.list[k] = free_page;
+        p.refs[free_page] = 1;
+      }
+      before += sum[0];
+    }
+  }
+  // also keeps every CTA's shared memory alive until the others have read it
+  cluster.sync();
+  if (kApply && err == 0) apply_table(p, (int64_t)rank * kPlan + tid, (int64_t)kCluster * kPlan);
+}
+
+__global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_table_apply_kernel(const __grid_constant__ TableParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  if (!p.ws.head[kHeadOk]) return;
+  apply_table(p, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
 // ---------------------------------------------------------------- free
@@ -303,51 +401,72 @@ __global__ void __launch_bounds__(256) mla_free_kernel(const __grid_constant__ F
 
 // ---------------------------------------------------------------- compact
 // One bit a page (in use), the pages in use before each word of 32, then the
-// two lists: free pages below L, pages in use from L on.
-__global__ void __launch_bounds__(kPlan) mla_compact_plan_kernel(const __grid_constant__ CompactParams p) {
-  __shared__ int64_t part[33];
+// two lists: free pages below L, pages in use from L on.  Each CTA of the
+// cluster has a slice of the words.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlan, 1)
+    mla_compact_plan_kernel(const __grid_constant__ CompactParams p) {
+  __shared__ Scan<1, int32_t> scan;
+  __shared__ int32_t s_live;
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int pages = p.c.num_pages, words = (pages + 31) / 32;
-  for (int w = warp; w < words; w += kPlan / 32) {
-    const int pg = 32 * w + lane;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)cluster.block_rank();
+  const int pages = p.c.num_pages, words = (int)(((int64_t)pages + 31) / 32);
+  const int slice = (words + kCluster - 1) / kCluster;
+  const int begin = min(words, rank * slice), end = min(words, begin + slice);
+  for (int w = begin + warp; w < end; w += kPlan / 32) {
+    const int64_t pg = 32ll * w + lane;
     const uint32_t m = __ballot_sync(kFull, pg < pages && p.refs_in[pg] > 0);
     if (lane == 0) p.ws.mask[w] = m;
   }
   __syncthreads();
-  int64_t live = 0;
-  for (int base = 0; base < words; base += kPlan) {
+  int32_t live = 0;  // of the slice
+  for (int base = begin; base < end; base += kPlan) {
     const int w = base + tid;
-    const int64_t n = w < words ? __popc(p.ws.mask[w]) : 0;
-    int64_t total;
-    const int64_t before = live + block_scan(n, part, total);
-    if (w < words) p.ws.pre[w] = (int32_t)before;
-    live += total;
+    int32_t v[1] = {w < end ? __popc(p.ws.mask[w]) : 0}, sum[1];
+    scan.run(v, sum);
+    if (w < end) p.ws.pre[w] = live + v[0];  // within the slice, so far
+    live += sum[0];
   }
-  __syncthreads();
-  const int L = (int)live;
-  // pages in use below L (L == pages: all of them)
-  const int kept = L == pages ? L : p.ws.pre[L >> 5] + __popc(p.ws.mask[L >> 5] & ((1u << (L & 31)) - 1));
-  for (int w = warp; w < words; w += kPlan / 32) {
-    const int pg = 32 * w + lane;
+  if (tid == 0) s_live = live;
+  cluster.sync();
+  int32_t before = 0, L = 0;
+  for (int r = 0; r < kCluster; ++r) {
+    const int32_t n = *cluster.map_shared_rank(&s_live, r);
+    if (r < rank) before += n;
+    L += n;
+  }
+  // pages in use below L: the slices before L's word, the words of its slice
+  // before it, the bits of the word (L == pages: all of them)
+  int32_t kept = L;
+  if (L < pages) {
+    const int w = L >> 5;
+    kept = p.ws.pre[w] + __popc(p.ws.mask[w] & ((1u << (L & 31)) - 1));
+    for (int r = 0; r < w / slice; ++r) kept += *cluster.map_shared_rank(&s_live, r);
+  }
+  cluster.sync();  // every CTA has read pre[] as it was
+  for (int w = begin + warp; w < end; w += kPlan / 32) {
+    const int64_t pg = 32ll * w + lane;
     const uint32_t m = p.ws.mask[w];
     const bool used = m >> lane & 1;
-    const int before = p.ws.pre[w] + __popc(m & ((1u << lane) - 1));
-    if (pg < L && !used) p.ws.list[pg - before] = pg;
+    const int pre = before + p.ws.pre[w];
+    __syncwarp();
+    if (lane == 0) p.ws.pre[w] = pre;
+    const int rank_of = pre + __popc(m & ((1u << lane) - 1));
+    if (pg < L && !used) p.ws.list[pg - rank_of] = (int32_t)pg;
     if (pg >= L && used) {
-      p.ws.from[before - kept] = pg;
-      p.ws.refs[before - kept] = p.refs_in[pg];
+      p.ws.from[rank_of - kept] = (int32_t)pg;
+      p.ws.refs[rank_of - kept] = p.refs_in[pg];
     }
   }
-  if (tid == 0) {
+  if (rank == 0 && tid == 0) {
     p.ws.head[kHeadLive] = L;
     p.ws.head[kHeadMoves] = L - kept;
     if (p.live) *p.live = L;
   }
 }
 
-__global__ void __launch_bounds__(256) mla_compact_apply_kernel(const __grid_constant__ CompactParams p) {
+__global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_compact_apply_kernel(const __grid_constant__ CompactParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, pages = p.c.num_pages;
@@ -407,13 +526,18 @@ cudaError_t launch_copy_pages(const CopyParams& p, cudaStream_t s) {
   return launch_chained(mla_copy_pages_kernel, grid_for(copy_threads(p.c, p.n)), 256, s, p);
 }
 
+// The cluster carries a call out by itself where that is little: up to
+// kClusterEntries table entries, and at most so many bytes of part-filled pages
+// (a fork copies one per sequence; a resize seldom copies any).
 cudaError_t launch_table(const TableParams& p, cudaStream_t s) {
-  const cudaError_t e = launch_chained(mla_table_plan_kernel, 1, kPlan, s, p);
+  int64_t threads = copy_threads(p.c, p.to.batch), entries = p.to.num_indices;
+  const int64_t most = threads * 128;  // bytes: 8 units of 16 a thread
+  if (!p.forks && entries < p.from.num_indices) entries = p.from.num_indices;
+  if (entries <= kClusterEntries && most <= (p.forks ? kClusterForkBytes : kClusterResizeBytes))
+    return launch_chained(mla_table_plan_kernel<true>, kCluster, kPlan, s, p);
+  const cudaError_t e = launch_chained(mla_table_plan_kernel<false>, kCluster, kPlan, s, p);
   if (e != cudaSuccess) return e;
-  int64_t threads = copy_threads(p.c, p.to.batch);
-  if (threads < p.to.num_indices) threads = p.to.num_indices;
-  if (!p.forks && threads < p.from.num_indices) threads = p.from.num_indices;
-  return launch_chained(mla_table_apply_kernel, grid_for(threads), 256, s, p);
+  return launch_chained(mla_table_apply_kernel, grid_for(threads < entries ? entries : threads), 256, s, p);
 }
 
 cudaError_t launch_free(int32_t* refs, int32_t num_pages, const int32_t* pages, int32_t n, int32_t* error,
@@ -424,7 +548,7 @@ cudaError_t launch_free(int32_t* refs, int32_t num_pages, const int32_t* pages, 
 }
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t s) {
-  const cudaError_t e = launch_chained(mla_compact_plan_kernel, 1, kPlan, s, p);
+  const cudaError_t e = launch_chained(mla_compact_plan_kernel, kCluster, kPlan, s, p);
   if (e != cudaSuccess) return e;
   int64_t threads = copy_threads(p.c, p.c.num_pages / 2);
   if (threads < p.num_indices) threads = p.num_indices;

@@ -333,48 +333,74 @@ __global__ void __launch_bounds__(256) mla_append_kernel(const __grid_constant__
 }
 
 // ---------------------------------------------------------------- gather
-// One thread per 8 columns of a row (16 bytes out; 16, 8 or 4 bytes in).
-constexpr int kPer = kRow / 8;  // 72 threads a row
+// A thread takes 8 columns of a row (16 bytes out; 16, 8 or 4 bytes in), the
+// same columns of kGatherDeep rows: their slots are loaded together, then their
+// bytes, then everything is stored.
+constexpr int kPer = kRow / 8;                      // 72 threads a row
+constexpr int kGatherRows = 4;                      // rows of a CTA's pass
+constexpr int kGatherThreads = kPer * kGatherRows;  // 9 warps
+#ifndef MLA_GATHER_DEEP
+#define MLA_GATHER_DEEP 4
+#endif
+constexpr int kGatherDeep = MLA_GATHER_DEEP;
 
 template <int kDtype>
-__global__ void __launch_bounds__(256) mla_gather_kernel(const __grid_constant__ GatherParams p) {
+__global__ void __launch_bounds__(kGatherThreads) mla_gather_kernel(const __grid_constant__ GatherParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t t = i / kPer;
-  const int c = (int)(i - t * kPer);
-  if (t >= p.num_rows) return;
-  const int32_t slot = p.slots[t];
-  if (slot < 0 || slot >= p.cache.rows) {
-    if (slot != -1 && c == 0) set_error(p.error, MLA_ERR_DEVICE_INDEX);
-    return;
-  }
-  uint4* out = reinterpret_cast<uint4*>(p.out + t * p.out_stride) + c;
-  if (kDtype == MLA_KV_BF16) {
-    *out = reinterpret_cast<const uint4*>(p.cache.kv + (int64_t)slot * (2 * kRow))[c];
-  } else if (kDtype == MLA_KV_FP8_E4M3) {
-    const float sc = *static_cast<const float*>(p.cache.scale);
-    const uint2 r = reinterpret_cast<const uint2*>(p.cache.kv + (int64_t)slot * kRow)[c];
-    const uint32_t w[4] = {r.x & 0xffffu, r.x >> 16, r.y & 0xffffu, r.y >> 16};
-    float x[8];
+  const int c = threadIdx.x % kPer;
+  const int64_t t0 = (int64_t)blockIdx.x * (kGatherRows * kGatherDeep) + threadIdx.x / kPer;
+  int32_t slot[kGatherDeep];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = __half22float2(e4m3x2_to_h2(w[j]));
-      x[2 * j] = f.x * sc;
-      x[2 * j + 1] = f.y * sc;
+  for (int i = 0; i < kGatherDeep; ++i) {
+    const int64_t t = t0 + i * kGatherRows;
+    slot[i] = t < p.num_rows ? p.slots[t] : -1;
+    if (slot[i] >= p.cache.rows || slot[i] < -1) {
+      if (c == 0) set_error(p.error, MLA_ERR_DEVICE_INDEX);
+      slot[i] = -1;
     }
-    *out = pack_bf16x8(x);
-  } else {
-    const uint32_t byte =
-        static_cast<const uint8_t*>(p.cache.scale)[(int64_t)slot * p.cache.scale_stride + (c >> 2)];
-    const uint32_t r = reinterpret_cast<const uint32_t*>(p.cache.kv + (int64_t)slot * (kRow / 2))[c];
-    // 2^(byte - 127): 2^-127 is subnormal, 255 is NaN
-    const float sc = __uint_as_float(byte == 0 ? 0x00400000u : (byte == 255 ? 0x7fc00000u : byte << 23));
-    float x[8];
-    unpack_e2m1x8(r, x);
+  }
+  uint4 raw[kGatherDeep];  // the row's 16, 8 or 4 bytes, and the block's scale byte
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] *= sc;
-    *out = pack_bf16x8(x);
+  for (int i = 0; i < kGatherDeep; ++i) {
+    if (slot[i] < 0) continue;
+    const int64_t s = slot[i];
+    if (kDtype == MLA_KV_BF16) {
+      raw[i] = reinterpret_cast<const uint4*>(p.cache.kv + s * (2 * kRow))[c];
+    } else if (kDtype == MLA_KV_FP8_E4M3) {
+      const uint2 r = reinterpret_cast<const uint2*>(p.cache.kv + s * kRow)[c];
+      raw[i].x = r.x;
+      raw[i].y = r.y;
+    } else {
+      raw[i].x = reinterpret_cast<const uint32_t*>(p.cache.kv + s * (kRow / 2))[c];
+      raw[i].y = static_cast<const uint8_t*>(p.cache.scale)[s * p.cache.scale_stride + (c >> 2)];
+    }
+  }
+  const float tensor_scale = kDtype == MLA_KV_FP8_E4M3 ? *static_cast<const float*>(p.cache.scale) : 1.f;
+#pragma unroll
+  for (int i = 0; i < kGatherDeep; ++i) {
+    if (slot[i] < 0) continue;
+    if (kDtype == MLA_KV_FP8_E4M3) {
+      const uint32_t w[4] = {raw[i].x & 0xffffu, raw[i].x >> 16, raw[i].y & 0xffffu, raw[i].y >> 16};
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = __half22float2(e4m3x2_to_h2(w[j]));
+        x[2 * j] = f.x * tensor_scale;
+        x[2 * j + 1] = f.y * tensor_scale;
+      }
+      raw[i] = pack_bf16x8(x);
+    } else if (kDtype == MLA_KV_MXFP4) {
+      const uint32_t byte = raw[i].y;
+      // 2^(byte - 127): 2^-127 is subnormal, 255 is NaN
+      const float sc = __uint_as_float(byte == 0 ? 0x00400000u : (byte == 255 ? 0x7fc00000u : byte << 23));
+      float x[8];
+      unpack_e2m1x8(raw[i].x, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= sc;
+      raw[i] = pack_bf16x8(x);
+    }
+    reinterpret_cast<uint4*>(p.out + (t0 + i * kGatherRows) * p.out_stride)[c] = raw[i];
   }
 }
 
@@ -446,11 +472,12 @@ cudaError_t launch_append(AppendParams p, int kv_dtype, cudaStream_t s) {
 
 cudaError_t launch_gather(const GatherParams& p, int kv_dtype, cudaStream_t s) {
   if (p.num_rows == 0) return cudaSuccess;
-  const unsigned grid = (unsigned)(((int64_t)p.num_rows * kPer + 255) / 256);
+  constexpr int kRows = kGatherRows * kGatherDeep;
+  const unsigned grid = (unsigned)(((int64_t)p.num_rows + kRows - 1) / kRows);
   switch (kv_dtype) {
-    case MLA_KV_BF16: return launch_chained(mla_gather_kernel<MLA_KV_BF16>, grid, 256, s, p);
-    case MLA_KV_FP8_E4M3: return launch_chained(mla_gather_kernel<MLA_KV_FP8_E4M3>, grid, 256, s, p);
-    default: return launch_chained(mla_gather_kernel<MLA_KV_MXFP4>, grid, 256, s, p);
+    case MLA_KV_BF16: return launch_chained(mla_gather_kernel<MLA_KV_BF16>, grid, kGatherThreads, s, p);
+    case MLA_KV_FP8_E4M3: return launch_chained(mla_gather_kernel<MLA_KV_FP8_E4M3>, grid, kGatherThreads, s, p);
+    default: return launch_chained(mla_gather_kernel<MLA_KV_MXFP4>, grid, kGatherThreads, s, p);
   }
 }
 
