@@ -148,17 +148,22 @@ cudaError_t launch_compact(const CompactParams& p, cudaStream_t s);
 
 // Launches `kernel` so that it may begin before the stream's previous kernel has
 // ended; each of these kernels waits (griddepcontrol.wait) before it reads memory.
+// cluster > 0: in clusters of that many CTAs.
 template <class Kernel, class Params>
-inline cudaError_t launch_chained(Kernel kernel, unsigned grid, unsigned block, cudaStream_t stream, const Params& p) {
+inline cudaError_t launch_chained(Kernel kernel, unsigned grid, unsigned block, cudaStream_t stream, const Params& p,
+                                  unsigned cluster = 0) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 

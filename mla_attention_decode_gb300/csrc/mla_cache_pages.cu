@@ -161,6 +161,23 @@ __device__ __forceinline__ int owner(const int32_t* indptr, int batch, int e) {
   return lo;
 }
 
+// One count per CTA of the cluster: the sum of those of rank below `upto`, and
+// of all (the loads go out together).
+struct ClusterCounts {
+  int32_t n[kCluster];
+  __device__ __forceinline__ ClusterCounts(const cg::cluster_group& cluster, int32_t* mine) {
+    const int ctas = (int)cluster.num_blocks();
+#pragma unroll
+    for (int r = 0; r < kCluster; ++r) n[r] = r < ctas ? *cluster.map_shared_rank(mine, r) : 0;
+  }
+  __device__ __forceinline__ int32_t below(int upto) const {
+    int32_t s = 0;
+#pragma unroll
+    for (int r = 0; r < kCluster; ++r) s += r < upto ? n[r] : 0;
+    return s;
+  }
+};
+
 // ---------------------------------------------------------------- fork, resize
 // Sequence n of `to` keeps the first `first` pages of its parent and gets fresh
 // pages from there on; the first of them takes a part-filled page's rows where
@@ -296,12 +313,11 @@ __device__ __forceinline__ void apply_table(const TableParams& p, int64_t at, in
   }
 }
 
-// The cluster's first CTA goes over the sequences while the others count the
-// free pages of a slice each; then those list the free pages of lowest number,
-// as many as are needed.  kApply: and the cluster carries it out.
+// The first CTA goes over the sequences while the others count the free pages of
+// a slice each; then those list the free pages of lowest number, as many as are
+// needed.  kApply: and the same CTAs carry the call out.
 template <bool kApply>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlan, 1)
-    mla_table_plan_kernel(const __grid_constant__ TableParams p) {
+__global__ void __launch_bounds__(kPlan, 1) mla_table_plan_kernel(const __grid_constant__ TableParams p) {
   __shared__ Scan<3, int64_t> scan;
   __shared__ Scan<1, int32_t> scan1;
   __shared__ TableTotals s_tot;
@@ -309,32 +325,28 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlan, 1)
   pdl_wait_primary();
   pdl_launch_dependents();
   const cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, rank = (int)cluster.block_rank();
+  const int tid = threadIdx.x, rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
   const int64_t pages = p.c.num_pages;
-  // slices of the CTAs 1 .. kCluster - 1, multiples of 8 pages
-  const int64_t slice = (pages + (kCluster - 1) * 8 - 1) / ((kCluster - 1) * 8) * 8;
-  const int64_t begin = min(pages, (rank - 1) * slice), end = min(pages, rank * slice);
+  // slices of 8-page multiples; with several CTAs the first, which has the
+  // sequences to go over, has none
+  const int sliced = ctas > 1 ? ctas - 1 : 1, mine = ctas > 1 ? rank - 1 : 0;
+  const int64_t slice = (pages + sliced * 8 - 1) / (sliced * 8) * 8;
+  const int64_t begin = mine < 0 ? 0 : min(pages, mine * slice), end = mine < 0 ? 0 : min(pages, begin + slice);
   uint32_t bits = 0;  // of this thread's 8 pages of the slice's first pass
-  if (rank == 0) {
-    plan_sequences(p, scan, s_tot);
-  } else {
-    int32_t v[1] = {0}, sum[1];
-    for (int64_t pg = begin + 8 * tid; pg < end; pg += 8 * kPlan) {
-      const uint32_t m = free_bits(p.refs, pg, end);
-      if (pg < begin + 8 * kPlan) bits = m;
-      v[0] += __popc(m);
-    }
-    scan1.run(v, sum);
-    if (tid == 0) s_free = sum[0];
+  int32_t count[1] = {0}, sum[1];
+  for (int64_t pg = begin + 8 * tid; pg < end; pg += 8 * kPlan) {
+    const uint32_t m = free_bits(p.refs, pg, end);
+    if (pg < begin + 8 * kPlan) bits = m;
+    count[0] += __popc(m);
   }
+  scan1.run(count, sum);
+  if (tid == 0) s_free = sum[0];
+  if (rank == 0) plan_sequences(p, scan, s_tot);
   cluster.sync();
   const TableTotals tot = *cluster.map_shared_rank(&s_tot, 0);
-  int64_t before = 0, all = 0;
-  for (int r = 1; r < kCluster; ++r) {
-    const int32_t n = *cluster.map_shared_rank(&s_free, r);
-    if (r < rank) before += n;
-    all += n;
-  }
+  const ClusterCounts free_pages(cluster, &s_free);
+  int64_t before = free_pages.below(rank);
+  const int64_t all = free_pages.below(kCluster);
   const int32_t err = tot.bad || tot.pages > p.to.num_indices ? MLA_ERR_DEVICE_INDEX
                                                               : (tot.fresh > all ? MLA_ERR_OUT_OF_PAGES : 0);
   if (rank == 0) {
@@ -350,11 +362,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlan, 1)
       p.ws.head[kHeadCopies] = (int32_t)tot.copies;
       p.ws.head[kHeadReleases] = tot.release;
     }
-  } else if (err == 0) {
+  }
+  if (err == 0) {
     for (int64_t base = begin; base < end && before < tot.fresh; base += 8 * kPlan) {
       const int64_t pg = base + 8 * tid;
       uint32_t m = base == begin ? bits : (pg < end ? free_bits(p.refs, pg, end) : 0u);
-      int32_t v[1] = {__popc(m)}, sum[1];
+      int32_t v[1] = {__popc(m)};
       scan1.run(v, sum);
       for (int64_t k = before + v[0]; m != 0 && k < tot.fresh; ++k) {
         const int32_t free_page = (int32_t)pg + __ffs(m) - 1;
@@ -367,7 +380,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlan, 1)
   }
   // also keeps every CTA's shared memory alive until the others have read it
   cluster.sync();
-  if (kApply && err == 0) apply_table(p, (int64_t)rank * kPlan + tid, (int64_t)kCluster * kPlan);
+  if (kApply && err == 0) apply_table(p, (int64_t)rank * kPlan + tid, (int64_t)ctas * kPlan);
 }
 
 __global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_table_apply_kernel(const __grid_constant__ TableParams p) {
@@ -400,63 +413,74 @@ __global__ void __launch_bounds__(256) mla_free_kernel(const __grid_constant__ F
 }
 
 // ---------------------------------------------------------------- compact
+// Which of the 8 pages from pg on are in use, as bits.
+__device__ __forceinline__ uint32_t used_bits(const int32_t* refs, int64_t pg, int64_t end) {
+  if (pg + 8 <= end) {
+    const int4 a = *reinterpret_cast<const int4*>(refs + pg), b = *reinterpret_cast<const int4*>(refs + pg + 4);
+    return (uint32_t)(a.x > 0) | (uint32_t)(a.y > 0) << 1 | (uint32_t)(a.z > 0) << 2 | (uint32_t)(a.w > 0) << 3 |
+           (uint32_t)(b.x > 0) << 4 | (uint32_t)(b.y > 0) << 5 | (uint32_t)(b.z > 0) << 6 | (uint32_t)(b.w > 0) << 7;
+  }
+  uint32_t m = 0;
+  for (int i = 0; i < 8; ++i)
+    if (pg + i < end && refs[pg + i] > 0) m |= 1u << i;
+  return m;
+}
+
 // One bit a page (in use), the pages in use before each word of 32, then the
-// two lists: free pages below L, pages in use from L on.  Each CTA of the
-// cluster has a slice of the words.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlan, 1)
-    mla_compact_plan_kernel(const __grid_constant__ CompactParams p) {
+// two lists: free pages below L, pages in use from L on.  A thread takes 8
+// pages, so that a slice of 4096 pages is one pass with every load in flight;
+// each CTA has a slice.
+__global__ void __launch_bounds__(kPlan, 1) mla_compact_plan_kernel(const __grid_constant__ CompactParams p) {
   __shared__ Scan<1, int32_t> scan;
   __shared__ int32_t s_live;
   pdl_wait_primary();
   pdl_launch_dependents();
   const cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)cluster.block_rank();
-  const int pages = p.c.num_pages, words = (int)(((int64_t)pages + 31) / 32);
-  const int slice = (words + kCluster - 1) / kCluster;
-  const int begin = min(words, rank * slice), end = min(words, begin + slice);
-  for (int w = begin + warp; w < end; w += kPlan / 32) {
-    const int64_t pg = 32ll * w + lane;
-    const uint32_t m = __ballot_sync(kFull, pg < pages && p.refs_in[pg] > 0);
-    if (lane == 0) p.ws.mask[w] = m;
-  }
-  __syncthreads();
+  const int tid = threadIdx.x, rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+  const int64_t pages = p.c.num_pages, words = (pages + 31) / 32;
+  const int64_t slice = (words + ctas - 1) / ctas * 32;  // pages
+  const int64_t begin = min(words * 32, rank * slice), end = min(words * 32, begin + slice);
+  uint8_t* mask = reinterpret_cast<uint8_t*>(p.ws.mask);  // byte pg / 8: pages pg .. pg + 7
   int32_t live = 0;  // of the slice
-  for (int base = begin; base < end; base += kPlan) {
-    const int w = base + tid;
-    int32_t v[1] = {w < end ? __popc(p.ws.mask[w]) : 0}, sum[1];
+  for (int64_t base = begin; base < end; base += 8 * kPlan) {
+    const int64_t pg = base + 8 * tid;
+    const uint32_t m = pg < end ? used_bits(p.refs_in, pg, pages) : 0u;
+    int32_t v[1] = {__popc(m)}, sum[1];
     scan.run(v, sum);
-    if (w < end) p.ws.pre[w] = live + v[0];  // within the slice, so far
+    if (pg < end) {
+      mask[pg >> 3] = (uint8_t)m;
+      if ((pg & 31) == 0) p.ws.pre[pg >> 5] = live + v[0];  // within the slice, so far
+    }
     live += sum[0];
   }
   if (tid == 0) s_live = live;
   cluster.sync();
-  int32_t before = 0, L = 0;
-  for (int r = 0; r < kCluster; ++r) {
-    const int32_t n = *cluster.map_shared_rank(&s_live, r);
-    if (r < rank) before += n;
-    L += n;
-  }
-  // pages in use below L: the slices before L's word, the words of its slice
-  // before it, the bits of the word (L == pages: all of them)
+  const ClusterCounts in_use(cluster, &s_live);
+  const int32_t before = in_use.below(rank), L = in_use.below(kCluster);
+  // pages in use below L: the slices before L's, the words of its slice before
+  // its word, the bits of the word (L == pages: all of them)
   int32_t kept = L;
-  if (L < pages) {
-    const int w = L >> 5;
-    kept = p.ws.pre[w] + __popc(p.ws.mask[w] & ((1u << (L & 31)) - 1));
-    for (int r = 0; r < w / slice; ++r) kept += *cluster.map_shared_rank(&s_live, r);
-  }
+  if (L < pages)
+    kept = in_use.below((int)(L / slice)) + p.ws.pre[L >> 5] +
+           __popc(p.ws.mask[L >> 5] & ((1u << (L & 31)) - 1));
   cluster.sync();  // every CTA has read pre[] as it was
-  for (int w = begin + warp; w < end; w += kPlan / 32) {
-    const int64_t pg = 32ll * w + lane;
-    const uint32_t m = p.ws.mask[w];
-    const bool used = m >> lane & 1;
-    const int pre = before + p.ws.pre[w];
-    __syncwarp();
-    if (lane == 0) p.ws.pre[w] = pre;
-    const int rank_of = pre + __popc(m & ((1u << lane) - 1));
-    if (pg < L && !used) p.ws.list[pg - rank_of] = (int32_t)pg;
-    if (pg >= L && used) {
-      p.ws.from[rank_of - kept] = (int32_t)pg;
-      p.ws.refs[rank_of - kept] = p.refs_in[pg];
+  for (int64_t w = begin / 32 + tid; w < end / 32; w += kPlan) p.ws.pre[w] += before;
+  __syncthreads();
+  for (int64_t pg = begin + 8 * tid; pg < end; pg += 8 * kPlan) {
+    const int w = (int)(pg >> 5);
+    const uint32_t word = p.ws.mask[w], m = word >> (pg & 31) & 255u;
+    int32_t at = p.ws.pre[w] + __popc(word & ((1u << (pg & 31)) - 1));
+    for (int i = 0; i < 8; ++i) {
+      const int32_t page = (int32_t)pg + i;
+      if (m >> i & 1) {
+        if (page >= L) {
+          p.ws.from[at - kept] = page;
+          p.ws.refs[at - kept] = p.refs_in[page];
+        }
+        ++at;
+      } else if (page < L) {
+        p.ws.list[page - at] = page;
+      }
     }
   }
   if (rank == 0 && tid == 0) {
@@ -510,6 +534,14 @@ __global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_compact_apply_kernel(c
   }
 }
 
+// The deciding kernel: one CTA where a single pass of its threads covers the
+// pages, else a cluster.
+template <class Kernel, class Params>
+cudaError_t plan_launch(Kernel kernel, int32_t pages, cudaStream_t s, const Params& p) {
+  const unsigned ctas = pages <= 8 * kPlan ? 1 : kCluster;
+  return launch_chained(kernel, ctas, kPlan, s, p, ctas > 1 ? ctas : 0);
+}
+
 // CTAs for `threads` threads of work, at most kMaxGrid (the kernels loop).
 unsigned grid_for(int64_t threads) {
   const int64_t g = (threads + 255) / 256;
@@ -534,8 +566,8 @@ cudaError_t launch_table(const TableParams& p, cudaStream_t s) {
   const int64_t most = threads * 128;  // bytes: 8 units of 16 a thread
   if (!p.forks && entries < p.from.num_indices) entries = p.from.num_indices;
   if (entries <= kClusterEntries && most <= (p.forks ? kClusterForkBytes : kClusterResizeBytes))
-    return launch_chained(mla_table_plan_kernel<true>, kCluster, kPlan, s, p);
-  const cudaError_t e = launch_chained(mla_table_plan_kernel<false>, kCluster, kPlan, s, p);
+    return launch_chained(mla_table_plan_kernel<true>, kCluster, kPlan, s, p, kCluster);
+  const cudaError_t e = plan_launch(mla_table_plan_kernel<false>, p.c.num_pages, s, p);
   if (e != cudaSuccess) return e;
   return launch_chained(mla_table_apply_kernel, grid_for(threads < entries ? entries : threads), 256, s, p);
 }
@@ -548,7 +580,7 @@ cudaError_t launch_free(int32_t* refs, int32_t num_pages, const int32_t* pages, 
 }
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t s) {
-  const cudaError_t e = launch_chained(mla_compact_plan_kernel, kCluster, kPlan, s, p);
+  const cudaError_t e = plan_launch(mla_compact_plan_kernel, p.c.num_pages, s, p);
   if (e != cudaSuccess) return e;
   int64_t threads = copy_threads(p.c, p.c.num_pages / 2);
   if (threads < p.num_indices) threads = p.num_indices;

@@ -9,6 +9,12 @@ namespace mla {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
+#ifndef MLA_HEADS_FULL
+#define MLA_HEADS_FULL 2
+#endif
+#ifndef MLA_APPEND_MIN
+#define MLA_APPEND_MIN 1
+#endif
 #ifndef MLA_APPEND_MANY
 #define MLA_APPEND_MANY 608
 #endif
@@ -264,7 +270,7 @@ __device__ __forceinline__ void store_row(const AppendParams& p, int32_t slot, c
 // token, all of whose columns are in flight before the first is used.
 // kQ: 0 no queries, 1 their position columns, 2 their latent columns too.
 template <int kDtype, int kQ, int kHeads>
-__global__ void __launch_bounds__(256) mla_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(256, MLA_APPEND_MIN) mla_append_kernel(const __grid_constant__ AppendParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -366,13 +372,13 @@ __global__ void __launch_bounds__(kGatherThreads) mla_gather_kernel(const __grid
     if (slot[i] < 0) continue;
     const int64_t s = slot[i];
     if (kDtype == MLA_KV_BF16) {
-      raw[i] = reinterpret_cast<const uint4*>(p.cache.kv + s * (2 * kRow))[c];
+      raw[i] = __ldcs(reinterpret_cast<const uint4*>(p.cache.kv + s * (2 * kRow)) + c);
     } else if (kDtype == MLA_KV_FP8_E4M3) {
-      const uint2 r = reinterpret_cast<const uint2*>(p.cache.kv + s * kRow)[c];
+      const uint2 r = __ldcs(reinterpret_cast<const uint2*>(p.cache.kv + s * kRow) + c);
       raw[i].x = r.x;
       raw[i].y = r.y;
     } else {
-      raw[i].x = reinterpret_cast<const uint32_t*>(p.cache.kv + s * (kRow / 2))[c];
+      raw[i].x = __ldcs(reinterpret_cast<const uint32_t*>(p.cache.kv + s * (kRow / 2)) + c);
       raw[i].y = static_cast<const uint8_t*>(p.cache.scale)[s * p.cache.scale_stride + (c >> 2)];
     }
   }
@@ -400,7 +406,7 @@ __global__ void __launch_bounds__(kGatherThreads) mla_gather_kernel(const __grid
       for (int j = 0; j < 8; ++j) x[j] *= sc;
       raw[i] = pack_bf16x8(x);
     }
-    reinterpret_cast<uint4*>(p.out + (t0 + i * kGatherRows) * p.out_stride)[c] = raw[i];
+    __stcs(reinterpret_cast<uint4*>(p.out + (t0 + i * kGatherRows) * p.out_stride) + c, raw[i]);
   }
 }
 
@@ -455,7 +461,7 @@ cudaError_t launch_append_to(AppendParams& p, cudaStream_t s) {
   p.key_ctas = p.a.kv_lat ? (int32_t)((T + 7) / 8) : 0;
   const auto grid = [&](int heads) { return (unsigned)(p.key_ctas + (T * (kQueryHeads / heads) + 7) / 8); };
   if (!p.a.q_pe) return launch_chained(mla_append_kernel<kDtype, 0, 16>, (unsigned)p.key_ctas, 256, s, p);
-  if (p.a.q_lat) return launch_chained(mla_append_kernel<kDtype, 2, 4>, grid(4), 256, s, p);
+  if (p.a.q_lat) return launch_chained(mla_append_kernel<kDtype, 2, MLA_HEADS_FULL>, grid(MLA_HEADS_FULL), 256, s, p);
   if (T >= MLA_APPEND_MANY) return launch_chained(mla_append_kernel<kDtype, 1, 16>, grid(16), 256, s, p);
   return launch_chained(mla_append_kernel<kDtype, 1, 4>, grid(4), 256, s, p);
 }
