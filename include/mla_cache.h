@@ -197,8 +197,8 @@ MLA_API int mla_cache_copy_pages(const mla_cache* cache, const int32_t* src, con
  * is not counted.
  *
  * The workspace is mla_cache_workspace_bytes(cache, batch of `to`) bytes,
- * 256-byte aligned, its first word (the error word) 0 before its first use;
- * calls that share it must be ordered on the GPU.
+ * 256-byte aligned, zeroed before its first use; calls that share it must be
+ * ordered on the GPU.
  *
  * mla_cache_fork -- sequence n of `to` is a copy of sequence parents[n] of
  * `from` (repeats allowed): it holds the parent's full pages too (their counts

@@ -87,7 +87,7 @@ struct PageWs {
   int32_t* pre;          // [ceil(num_pages / 32)] pages in use before each mask word
   size_t total;
 };
-enum { kHeadOk = 0, kHeadCopies = 1, kHeadReleases = 2, kHeadLive = 3, kHeadMoves = 4 };
+enum { kHeadOk = 0, kHeadCopies = 1, kHeadReleases = 2, kHeadLive = 3, kHeadMoves = 4, kHeadTicket = 5 };
 
 inline PageWs page_ws(void* base, int32_t num_pages, int32_t batch) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };

@@ -28,6 +28,7 @@ constexpr int kCluster = 8;             // deciding CTAs
 #define MLA_CLUSTER_FORK_BYTES (2 << 20)
 #endif
 constexpr int64_t kClusterEntries = 32768, kClusterForkBytes = MLA_CLUSTER_FORK_BYTES, kClusterResizeBytes = 16 << 20;
+constexpr unsigned kLocalGrid = 152 * MLA_MOVE_CTAS;  // all resident at once
 constexpr unsigned kMaxGrid = 152 * 8;  // CTAs of 256 threads that carry out
 
 __device__ __forceinline__ void set_error(int32_t* error, int32_t code) {
@@ -107,11 +108,11 @@ __global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_copy_pages_kernel(cons
 }
 
 // ---------------------------------------------------------------- prefix sums
-// Exclusive prefix sums of kN values over the CTA's kPlan threads, and the
+// Exclusive prefix sums of kN values over the CTA's kThreads threads, and the
 // totals.  Every thread of the CTA calls.
-template <int kN, class T>
+template <int kN, class T, int kThreads = kPlan>
 struct Scan {
-  static constexpr int kWarps = kPlan / 32;
+  static constexpr int kWarps = kThreads / 32;
   T part[kN][kWarps], total[kN];
   __device__ __forceinline__ void run(T (&v)[kN], T (&sum)[kN]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -150,6 +151,17 @@ struct Scan {
   }
 };
 
+// One hold on a page ends.  A page given back more often than it is held keeps
+// the count 0.
+__device__ __forceinline__ void release_page(int32_t* refs, int num_pages, int32_t page, int32_t* error) {
+  if (page < 0 || page >= num_pages) {
+    set_error(error, MLA_ERR_DEVICE_INDEX);
+  } else if (atomicSub(refs + page, 1) <= 0) {
+    atomicAdd(refs + page, 1);
+    set_error(error, MLA_ERR_DEVICE_INDEX);
+  }
+}
+
 // The sequence that owns entry e of a table: indptr[n] <= e < indptr[n + 1].
 __device__ __forceinline__ int owner(const int32_t* indptr, int batch, int e) {
   int lo = 0, hi = batch;
@@ -183,63 +195,84 @@ struct ClusterCounts {
 // pages from there on; the first of them takes a part-filled page's rows where
 // that page has to be copied.
 
+// What a call does with sequence n.
+struct SeqPlan {
+  int64_t a, b;       // its parent's entries in `from`
+  int64_t cnt;        // its pages
+  int64_t want;       // its rows
+  int32_t first;      // the first fresh one
+  int32_t src, rows;  // the part-filled page whose rows that one takes (-1: none)
+  bool ok, release;   // the parent's pages from `first` on are given back
+};
+__device__ __forceinline__ SeqPlan plan_sequence(const TableParams& p, int n) {
+  const int P = p.c.page_size;
+  SeqPlan s;
+  s.a = s.b = s.cnt = s.want = 0;
+  s.first = s.rows = 0;
+  s.src = -1;
+  s.release = false;
+  const int by = p.by[n], par = p.forks ? by : n;
+  s.ok = par >= 0 && par < p.from.batch;
+  if (!s.ok) return s;
+  s.a = p.from.page_indptr[par];
+  s.b = p.from.page_indptr[par + 1];
+  const int32_t last = p.from.last_page_len[par];
+  const int64_t len = s.a < s.b ? (s.b - s.a - 1) * P + last : 0;
+  s.want = p.forks ? len : by;
+  s.ok = 0 <= s.a && s.a <= s.b && s.b <= p.from.num_indices && (s.a == s.b || (last >= 1 && last <= P)) && s.want >= 0;
+  if (!s.ok) return s;
+  s.cnt = (s.want + P - 1) >> p.c.page_shift;
+  const int64_t keep = min(s.cnt, s.b - s.a), r0 = min(len, s.want);
+  s.first = (int32_t)keep;
+  if ((r0 & (P - 1)) != 0 && (p.forks || s.want != len)) {
+    const int32_t page = p.from.kv_indices[s.a + keep - 1];
+    if (page >= 0 && page < p.c.num_pages && (p.forks || p.refs[page] > 1)) {
+      s.src = page;
+      s.rows = (int32_t)(r0 & (P - 1));
+      s.first -= 1;
+    }
+  }
+  s.release = !p.forks && s.b - s.a > s.first;
+  return s;
+}
+// The rows in the last of cnt pages that hold `want` rows.
+__device__ __forceinline__ int32_t last_rows(int64_t want, int64_t cnt, int P) {
+  return cnt ? (int32_t)(want - (cnt - 1) * P) : 0;
+}
+
 // What the first CTA of the cluster decides.
 struct TableTotals {
   int64_t pages, fresh, copies;
   int32_t bad, release;
 };
 __device__ __forceinline__ void plan_sequences(const TableParams& p, Scan<3, int64_t>& scan, TableTotals& s) {
-  const int tid = threadIdx.x, N = p.to.batch, P = p.c.page_size, shift = p.c.page_shift;
+  const int tid = threadIdx.x, N = p.to.batch;
   if (tid == 0) s.bad = s.release = 0;
   __syncthreads();
   int64_t pages = 0, fresh = 0, copies = 0;
   for (int base = 0; base < N; base += kPlan) {
     const int n = base + tid;
-    int64_t cnt = 0;
-    int32_t first = 0, src = -1, rows = 0;
+    SeqPlan q;
+    q.cnt = q.first = 0;
+    q.src = -1;
     if (n < N) {
-      const int by = p.by[n], par = p.forks ? by : n;
-      bool ok = par >= 0 && par < p.from.batch;
-      int64_t a = 0, b = 0, len = 0, want = 0;
-      if (ok) {
-        a = p.from.page_indptr[par];
-        b = p.from.page_indptr[par + 1];
-        const int32_t last = p.from.last_page_len[par];
-        ok = 0 <= a && a <= b && b <= p.from.num_indices && (a == b || (last >= 1 && last <= P));
-        if (a < b) len = (b - a - 1) * P + last;
-        want = p.forks ? len : by;
-        ok = ok && want >= 0;
-      }
-      if (!ok) {
-        s.bad = 1;
-      } else {
-        cnt = (want + P - 1) >> shift;
-        const int64_t keep = min(cnt, b - a), r0 = min(len, want);
-        first = (int32_t)keep;
-        if ((r0 & (P - 1)) != 0 && (p.forks || want != len)) {
-          const int32_t page = p.from.kv_indices[a + keep - 1];
-          if (page >= 0 && page < p.c.num_pages && (p.forks || p.refs[page] > 1)) {
-            src = page;
-            rows = (int32_t)(r0 & (P - 1));
-            first -= 1;
-          }
-        }
-        if (!p.forks && b - a > first) s.release = 1;
-        p.to.last_page_len[n] = cnt ? (int32_t)(want - (cnt - 1) * P) : 0;
-        p.ws.first[n] = first;
-      }
+      q = plan_sequence(p, n);
+      if (!q.ok) s.bad = 1;
+      if (q.release) s.release = 1;
+      p.to.last_page_len[n] = last_rows(q.want, q.cnt, p.c.page_size);
+      p.ws.first[n] = q.first;
     }
-    int64_t v[3] = {cnt, cnt - first, src >= 0}, sum[3];
+    int64_t v[3] = {q.cnt, q.cnt - q.first, q.src >= 0}, sum[3];
     scan.run(v, sum);
     const int64_t fr = fresh + v[1], c = copies + v[2];
     if (n < N) {
-      p.to.page_indptr[n + 1] = (int32_t)(pages + v[0] + cnt);
+      p.to.page_indptr[n + 1] = (int32_t)(pages + v[0] + q.cnt);
       p.ws.fresh[n] = (int32_t)fr;
     }
-    if (src >= 0) {
-      p.ws.copy_src[c] = src;
+    if (q.src >= 0) {
+      p.ws.copy_src[c] = q.src;
       p.ws.copy_rank[c] = (int32_t)fr;
-      p.ws.copy_rows[c] = rows;
+      p.ws.copy_rows[c] = q.rows;
     }
     pages += sum[0];
     fresh += sum[1];
@@ -295,13 +328,7 @@ __device__ __forceinline__ void apply_table(const TableParams& p, int64_t at, in
     for (int64_t e = p.from.page_indptr[0] + at; e < end; e += step) {
       const int n = owner(p.from.page_indptr, B, (int)e);
       if ((int)e - p.from.page_indptr[n] < p.ws.first[n]) continue;
-      const int32_t page = p.from.kv_indices[e];
-      if (page < 0 || page >= p.c.num_pages) {
-        set_error(p.ws.err, MLA_ERR_DEVICE_INDEX);
-      } else if (atomicSub(p.refs + page, 1) <= 0) {
-        atomicAdd(p.refs + page, 1);
-        set_error(p.ws.err, MLA_ERR_DEVICE_INDEX);
-      }
+      release_page(p.refs, p.c.num_pages, p.from.kv_indices[e], p.ws.err);
     }
   }
   const int ks = kv_segs(p.c), segs = ks + scale_segs(p.c);
@@ -315,8 +342,7 @@ __device__ __forceinline__ void apply_table(const TableParams& p, int64_t at, in
 
 // The first CTA goes over the sequences while the others count the free pages of
 // a slice each; then those list the free pages of lowest number, as many as are
-// needed.  kApply: and the same CTAs carry the call out.
-template <bool kApply>
+// needed.
 __global__ void __launch_bounds__(kPlan, 1) mla_table_plan_kernel(const __grid_constant__ TableParams p) {
   __shared__ Scan<3, int64_t> scan;
   __shared__ Scan<1, int32_t> scan1;
@@ -380,7 +406,6 @@ __global__ void __launch_bounds__(kPlan, 1) mla_table_plan_kernel(const __grid_c
   }
   // also keeps every CTA's shared memory alive until the others have read it
   cluster.sync();
-  if (kApply && err == 0) apply_table(p, (int64_t)rank * kPlan + tid, (int64_t)ctas * kPlan);
 }
 
 __global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_table_apply_kernel(const __grid_constant__ TableParams p) {
@@ -388,6 +413,135 @@ __global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_table_apply_kernel(con
   pdl_launch_dependents();
   if (!p.ws.head[kHeadOk]) return;
   apply_table(p, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
+}
+
+// Small calls (up to kPlan sequences, kLocalPages pages): each CTA of the cluster
+// decides the whole call for itself, in shared memory, and carries out its
+// share; nothing is handed from CTA to CTA and nothing else is launched.  Only
+// the counts may not change before every CTA has read them: the cluster's barrier.
+constexpr int kLocalPages = 16384;  // 32 a thread
+struct TableLocal {
+  Scan<4, int32_t> scan;
+  int32_t to_at[kPlan + 1], from_at[kPlan + 1], first[kPlan], fresh[kPlan];
+  int32_t copy_rows[kPlan];
+  uint16_t copy_src[kPlan], copy_rank[kPlan];
+  int32_t flags;
+  union {
+    uint8_t bytes[kLocalPages / 8];  // a bit a page: free
+    uint32_t words[kLocalPages / 32];
+  } mask;
+  uint16_t list[kLocalPages];
+};
+static_assert(sizeof(TableLocal) <= 48 * 1024, "static shared memory");
+
+// Four counts from page pg on, `other` past the end.
+__device__ __forceinline__ int4 four_counts(const int32_t* refs, int pg, int pages, int other) {
+  if (pg + 4 <= pages) return *reinterpret_cast<const int4*>(refs + pg);
+  int4 v = make_int4(other, other, other, other);
+  if (pg < pages) v.x = refs[pg];
+  if (pg + 1 < pages) v.y = refs[pg + 1];
+  if (pg + 2 < pages) v.z = refs[pg + 2];
+  return v;
+}
+// Two lanes' four bits each to a byte of the mask.
+__device__ __forceinline__ void put_nibble(uint8_t* bytes, int quad, uint32_t nib) {
+  const uint32_t next = __shfl_down_sync(kFull, nib, 1);
+  if ((quad & 1) == 0) bytes[quad / 2] = (uint8_t)(nib | next << 4);
+}
+
+__global__ void __launch_bounds__(kPlan, 1) mla_table_local_kernel(const __grid_constant__ TableParams p) {
+  __shared__ TableLocal s;
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, rank = (int)cluster.block_rank(), N = p.to.batch;
+  const int pages = p.c.num_pages;
+  constexpr int kPasses = kLocalPages / (4 * kPlan);
+  if (tid == 0) s.flags = 0;
+  int4 c4[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) c4[i] = four_counts(p.refs, (i * kPlan + tid) * 4, pages, 1);
+  SeqPlan q;
+  q.cnt = q.first = 0;
+  q.src = -1;
+  q.ok = true;
+  q.release = false;
+  if (tid < N) q = plan_sequence(p, tid);
+  // more pages than `to` has room for: the sums below fit 32 bits without it
+  if (q.cnt > p.to.num_indices) q.ok = false;
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i)
+    put_nibble(s.mask.bytes, i * kPlan + tid,
+               (uint32_t)(c4[i].x == 0) | (uint32_t)(c4[i].y == 0) << 1 | (uint32_t)(c4[i].z == 0) << 2 |
+                   (uint32_t)(c4[i].w == 0) << 3);
+  __syncthreads();
+  if (!q.ok) atomicOr(&s.flags, 1);
+  if (q.release) atomicOr(&s.flags, 2);
+  uint32_t m = s.mask.words[tid];
+  int32_t v[4] = {q.ok ? (int32_t)q.cnt : 0, q.ok ? (int32_t)(q.cnt - q.first) : 0, q.ok && q.src >= 0, __popc(m)};
+  int32_t sum[4];
+  s.scan.run(v, sum);
+  const int32_t total = sum[0], fresh = sum[1], copies = sum[2];
+  const bool bad = (s.flags & 1) != 0 || total > p.to.num_indices;
+  const int32_t err = bad ? MLA_ERR_DEVICE_INDEX : (fresh > sum[3] ? MLA_ERR_OUT_OF_PAGES : 0);
+  if (tid < N) {
+    s.to_at[tid] = v[0];
+    s.from_at[tid] = (int32_t)q.a;
+    s.first[tid] = q.first;
+    s.fresh[tid] = v[1];
+    if (tid == N - 1) {
+      s.to_at[N] = total;
+      s.from_at[N] = (int32_t)q.b;
+    }
+    if (q.src >= 0) {
+      s.copy_src[v[2]] = (uint16_t)q.src;
+      s.copy_rank[v[2]] = (uint16_t)v[1];
+      s.copy_rows[v[2]] = q.rows;
+    }
+    if (rank == 0) {
+      p.to.page_indptr[tid] = err ? 0 : v[0];
+      p.to.last_page_len[tid] = err ? 0 : last_rows(q.want, q.cnt, p.c.page_size);
+    }
+  }
+  if (rank == 0 && tid == 0) {
+    p.to.page_indptr[N] = err ? 0 : total;
+    if (err) set_error(p.ws.err, err);
+  }
+  for (int32_t k = v[3]; m != 0 && k < fresh; ++k) {
+    s.list[k] = (uint16_t)(32 * tid + __ffs(m) - 1);
+    m &= m - 1;
+  }
+  cluster.sync();  // this CTA's shared memory is written, every CTA has read the counts
+  if (err) return;
+  const int at = rank * kPlan + tid, step = (int)cluster.num_blocks() * kPlan;
+  for (int e = at; e < total; e += step) {
+    const int n = owner(s.to_at, N, e), j = e - s.to_at[n], first = s.first[n];
+    int32_t page;
+    if (j >= first) {
+      page = s.list[s.fresh[n] + j - first];
+    } else {
+      page = p.from.kv_indices[s.from_at[n] + j];
+      if (page < 0 || page >= pages) {
+        page = -1;
+        set_error(p.ws.err, MLA_ERR_DEVICE_INDEX);
+      } else if (p.forks) {
+        atomicAdd(p.refs + page, 1);
+      }
+    }
+    p.to.kv_indices[e] = page;
+  }
+  for (int k = at; k < fresh; k += step) p.refs[s.list[k]] = 1;
+  if (s.flags & 2)
+    for (int e = s.from_at[0] + at; e < s.from_at[N]; e += step) {
+      const int n = owner(s.from_at, N, e);
+      if (e - s.from_at[n] >= s.first[n]) release_page(p.refs, pages, p.from.kv_indices[e], p.ws.err);
+    }
+  const int ks = kv_segs(p.c), segs = ks + scale_segs(p.c);
+  const int64_t per = (int64_t)segs * p.c.num_layers, tasks = per * copies;
+  for (int64_t task = at >> 5; task < tasks; task += step >> 5) {
+    const int i = (int)(task / per), rest = (int)(task - i * per), l = rest / segs, seg = rest - l * segs;
+    move_segment(p.c, s.copy_src[i], s.list[s.copy_rank[i]], s.copy_rows[i], l, seg, ks, lane);
+  }
 }
 
 // ---------------------------------------------------------------- free
@@ -403,13 +557,7 @@ __global__ void __launch_bounds__(256) mla_free_kernel(const __grid_constant__ F
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= p.n) return;
   const int32_t page = p.pages[i];
-  if (page == -1) return;
-  if (page < 0 || page >= p.num_pages) {
-    set_error(p.error, MLA_ERR_DEVICE_INDEX);
-  } else if (atomicSub(p.refs + page, 1) <= 0) {
-    atomicAdd(p.refs + page, 1);  // given back more often than held: the count stays 0
-    set_error(p.error, MLA_ERR_DEVICE_INDEX);
-  }
+  if (page != -1) release_page(p.refs, p.num_pages, page, p.error);
 }
 
 // ---------------------------------------------------------------- compact
@@ -534,6 +682,95 @@ __global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_compact_apply_kernel(c
   }
 }
 
+// Up to kLocalPages pages: each CTA decides for itself, in shared memory, and
+// moves its share, in one launch.  Counts that are rewritten in place are left
+// to the CTA that has read them last, found by a ticket that it sets back to 0.
+constexpr int kLocalThreads = 256;
+struct CompactLocal {
+  Scan<1, int32_t, kLocalThreads> scan;
+  int32_t kept, last;
+  int32_t pre[kLocalPages / 32];
+  union {
+    uint8_t bytes[kLocalPages / 8];  // a bit a page: in use
+    uint32_t words[kLocalPages / 32];
+  } mask;
+  uint16_t list[kLocalPages / 2], from[kLocalPages / 2];
+};
+__global__ void __launch_bounds__(kLocalThreads, MLA_MOVE_CTAS)
+    mla_compact_local_kernel(const __grid_constant__ CompactParams p) {
+  __shared__ CompactLocal s;
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, pages = p.c.num_pages, words = (pages + 31) / 32;
+#pragma unroll 4
+  for (int base = 0; base < pages; base += 4 * kLocalThreads) {
+    const int4 v = four_counts(p.refs_in, base + 4 * tid, pages, 0);
+    put_nibble(s.mask.bytes, base / 4 + tid,
+               (uint32_t)(v.x > 0) | (uint32_t)(v.y > 0) << 1 | (uint32_t)(v.z > 0) << 2 | (uint32_t)(v.w > 0) << 3);
+  }
+  __syncthreads();
+  if (tid == 0) s.last = p.refs_in == p.refs_out ? atomicAdd(p.ws.head + kHeadTicket, 1) : 0;  // (all has been read)
+  // two words a thread
+  const uint32_t m0 = 2 * tid < words ? s.mask.words[2 * tid] : 0u;
+  const uint32_t m1 = 2 * tid + 1 < words ? s.mask.words[2 * tid + 1] : 0u;
+  int32_t v[1] = {__popc(m0) + __popc(m1)}, sum[1];
+  s.scan.run(v, sum);
+  const int L = sum[0];
+  s.pre[2 * tid] = v[0];
+  s.pre[2 * tid + 1] = v[0] + __popc(m0);
+  __syncthreads();
+  auto rank = [&](int pg, bool& used) {  // pages in use before page pg, and whether pg is
+    const uint32_t m = s.mask.words[pg >> 5];
+    used = m >> (pg & 31) & 1;
+    return s.pre[pg >> 5] + __popc(m & ((1u << (pg & 31)) - 1));
+  };
+  bool unused;
+  const int kept = L < pages ? rank(L, unused) : L, moves = L - kept;
+  for (int pg = tid; pg < pages; pg += kLocalThreads) {
+    bool used;
+    const int before = rank(pg, used);
+    if (pg < L && !used) s.list[pg - before] = (uint16_t)pg;
+    if (pg >= L && used) s.from[before - kept] = (uint16_t)pg;
+  }
+  __syncthreads();
+  const int at = blockIdx.x * kLocalThreads + tid, step = gridDim.x * kLocalThreads;
+  if (at == 0 && p.live) *p.live = L;
+  for (int64_t i = at; i < p.num_indices; i += step) {
+    int32_t pg = p.idx_in[i];
+    if (pg != -1) {
+      bool used = false;
+      const int before = pg >= 0 && pg < pages ? rank(pg, used) : 0;
+      if (!used) {
+        pg = -1;
+        set_error(p.ws.err, MLA_ERR_DEVICE_INDEX);
+      } else if (pg >= L) {
+        pg = s.list[before - kept];
+      }
+    }
+    p.idx_out[i] = pg;
+  }
+  if (p.refs_in != p.refs_out) {
+    for (int pg = at; pg < pages; pg += step) {
+      bool used;
+      const int before = rank(pg, used);
+      p.refs_out[pg] = pg >= L ? 0 : p.refs_in[used ? pg : s.from[pg - before]];
+    }
+  } else if (s.last == (int)gridDim.x - 1) {
+    // every CTA has read the counts: the holes' first, which come from pages
+    // at or above L, then the zeros of those
+    for (int i = tid; i < moves; i += kLocalThreads) p.refs_out[s.list[i]] = p.refs_in[s.from[i]];
+    __syncthreads();
+    for (int pg = L + tid; pg < pages; pg += kLocalThreads) p.refs_out[pg] = 0;
+    if (tid == 0) p.ws.head[kHeadTicket] = 0;
+  }
+  const int ks = kv_segs(p.c), segs = ks + scale_segs(p.c);
+  const int64_t per = (int64_t)segs * p.c.num_layers, tasks = per * moves;
+  for (int64_t task = at >> 5; task < tasks; task += step >> 5) {
+    const int i = (int)(task / per), rest = (int)(task - i * per), l = rest / segs, seg = rest - l * segs;
+    move_segment(p.c, s.from[i], s.list[i], p.c.page_size, l, seg, ks, lane);
+  }
+}
+
 // The deciding kernel: one CTA where a single pass of its threads covers the
 // pages, else a cluster.
 template <class Kernel, class Params>
@@ -565,9 +802,10 @@ cudaError_t launch_table(const TableParams& p, cudaStream_t s) {
   int64_t threads = copy_threads(p.c, p.to.batch), entries = p.to.num_indices;
   const int64_t most = threads * 128;  // bytes: 8 units of 16 a thread
   if (!p.forks && entries < p.from.num_indices) entries = p.from.num_indices;
-  if (entries <= kClusterEntries && most <= (p.forks ? kClusterForkBytes : kClusterResizeBytes))
-    return launch_chained(mla_table_plan_kernel<true>, kCluster, kPlan, s, p, kCluster);
-  const cudaError_t e = plan_launch(mla_table_plan_kernel<false>, p.c.num_pages, s, p);
+  if (p.to.batch <= kPlan && p.c.num_pages <= kLocalPages && entries <= kClusterEntries &&
+      most <= (p.forks ? kClusterForkBytes : kClusterResizeBytes))
+    return launch_chained(mla_table_local_kernel, kCluster, kPlan, s, p, kCluster);
+  const cudaError_t e = plan_launch(mla_table_plan_kernel, p.c.num_pages, s, p);
   if (e != cudaSuccess) return e;
   return launch_chained(mla_table_apply_kernel, grid_for(threads < entries ? entries : threads), 256, s, p);
 }
@@ -580,6 +818,12 @@ cudaError_t launch_free(int32_t* refs, int32_t num_pages, const int32_t* pages, 
 }
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t s) {
+  if (p.c.num_pages <= kLocalPages) {
+    int64_t threads = copy_threads(p.c, p.c.num_pages / 2);
+    if (threads < p.num_indices) threads = p.num_indices;
+    const unsigned grid = grid_for(threads);
+    return launch_chained(mla_compact_local_kernel, grid < kLocalGrid ? grid : kLocalGrid, kLocalThreads, s, p);
+  }
   const cudaError_t e = plan_launch(mla_compact_plan_kernel, p.c.num_pages, s, p);
   if (e != cudaSuccess) return e;
   int64_t threads = copy_threads(p.c, p.c.num_pages / 2);
