@@ -29,7 +29,6 @@ struct AppendParams {
   mla_norm norm;
   mla_append_args a;
   int32_t* error;
-  int32_t key_ctas;      // CTAs that store key rows (set by the launcher)
 };
 
 struct GatherParams {
@@ -137,7 +136,7 @@ struct CompactParams {
   PageWs ws;
 };
 
-cudaError_t launch_append(AppendParams p, int kv_dtype, cudaStream_t s);
+cudaError_t launch_append(const AppendParams& p, int kv_dtype, cudaStream_t s);
 cudaError_t launch_gather(const GatherParams& p, int kv_dtype, cudaStream_t s);
 cudaError_t launch_slots(const SlotsParams& p, cudaStream_t s);
 cudaError_t launch_copy_pages(const CopyParams& p, cudaStream_t s);

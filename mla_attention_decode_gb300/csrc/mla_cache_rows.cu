@@ -12,8 +12,8 @@ constexpr unsigned kFull = 0xffffffffu;
 #ifndef MLA_HEADS_FULL
 #define MLA_HEADS_FULL 2
 #endif
-#ifndef MLA_APPEND_MIN
-#define MLA_APPEND_MIN 1
+#ifndef MLA_APPEND_WARPS
+#define MLA_APPEND_WARPS 4
 #endif
 #ifndef MLA_APPEND_MANY
 #define MLA_APPEND_MANY 608
@@ -266,17 +266,23 @@ __device__ __forceinline__ void store_row(const AppendParams& p, int32_t slot, c
   }
 }
 
-// One warp per key row (the first key_ctas CTAs), or per kHeads query heads of a
-// token, all of whose columns are in flight before the first is used.
+// One warp per key row, or per kHeads query heads of a token, all of whose
+// columns are in flight before the first is used.
 // kQ: 0 no queries, 1 their position columns, 2 their latent columns too.
+constexpr int kAppendWarps = MLA_APPEND_WARPS;
 template <int kDtype, int kQ, int kHeads>
-__global__ void __launch_bounds__(256, MLA_APPEND_MIN) mla_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const __grid_constant__ AppendParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // CTAs come in groups of kAppendWarps tokens: one for the keys (if any), kGroups
+  // for the queries, so that both kinds of traffic are in flight together
+  constexpr int kGroups = kQ ? kQueryHeads / kHeads : 0;
+  const int keys = p.a.kv_lat ? 1 : 0, group = (int)blockIdx.x / (keys + kGroups);
+  const int role = (int)blockIdx.x - group * (keys + kGroups) - keys;  // -1: keys
   Weights w;
-  if ((int)blockIdx.x < p.key_ctas) {
-    const int t = (int)blockIdx.x * 8 + warp;
+  if (role < 0) {
+    const int t = group * kAppendWarps + warp;
     if (t >= p.a.num_tokens) return;
     const int32_t slot = p.a.slots[t];
     if (slot < 0 || slot >= p.cache.rows) {
@@ -299,9 +305,8 @@ __global__ void __launch_bounds__(256, MLA_APPEND_MIN) mla_append_kernel(const _
     return;
   }
   if (kQ == 0) return;
-  constexpr int kGroups = kQueryHeads / kHeads;
-  const int64_t task = (int64_t)((int)blockIdx.x - p.key_ctas) * 8 + warp;
-  const int t = (int)(task / kGroups), h0 = (int)(task % kGroups) * kHeads;
+  const int task = role * kAppendWarps + warp;  // of the group's kGroups * kAppendWarps
+  const int t = group * kAppendWarps + task / (kQ ? kGroups : 1), h0 = task % (kQ ? kGroups : 1) * kHeads;
   if (t >= p.a.num_tokens) return;
   const uint16_t* pe = static_cast<const uint16_t*>(p.a.q_pe) + (int64_t)t * p.a.q_pe_token_stride +
                        (int64_t)h0 * p.a.q_pe_head_stride;
@@ -343,7 +348,10 @@ __global__ void __launch_bounds__(256, MLA_APPEND_MIN) mla_append_kernel(const _
 // same columns of kGatherDeep rows: their slots are loaded together, then their
 // bytes, then everything is stored.
 constexpr int kPer = kRow / 8;                      // 72 threads a row
-constexpr int kGatherRows = 4;                      // rows of a CTA's pass
+#ifndef MLA_GATHER_ROWS
+#define MLA_GATHER_ROWS 2
+#endif
+constexpr int kGatherRows = MLA_GATHER_ROWS;        // rows of a CTA's pass
 constexpr int kGatherThreads = kPer * kGatherRows;  // 9 warps
 #ifndef MLA_GATHER_DEEP
 #define MLA_GATHER_DEEP 4
@@ -411,29 +419,40 @@ __global__ void __launch_bounds__(kGatherThreads) mla_gather_kernel(const __grid
 }
 
 // ---------------------------------------------------------------- slots
-// One thread per token: the sequence by bisection of qo_indptr, then the page
-// of its row.  Whatever the tables hold, nothing outside them is read.
-__global__ void __launch_bounds__(128) mla_slots_kernel(const __grid_constant__ SlotsParams p) {
+// One thread per token: the sequence by bisection of qo_indptr (staged in shared
+// memory up to kSlotsBatch sequences: each step of a bisection in global memory
+// is a round trip), then the page of its row.  Whatever the tables hold,
+// nothing outside them is read.
+constexpr int kSlotsBatch = 2048, kSlotsThreads = 128;
+
+__global__ void __launch_bounds__(kSlotsThreads) mla_slots_kernel(const __grid_constant__ SlotsParams p) {
+  __shared__ int32_t s_qo[kSlotsBatch + 1];
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int t = blockIdx.x * 128 + threadIdx.x;
+  const int t = blockIdx.x * kSlotsThreads + threadIdx.x, batch = p.table.batch;
+  const int32_t* qo = p.qo_indptr;
+  if (batch <= kSlotsBatch) {
+    for (int i = threadIdx.x; i <= batch; i += kSlotsThreads) s_qo[i] = qo[i];
+    __syncthreads();
+    qo = s_qo;
+  }
   if (t >= p.num_tokens) return;
   const int P = 1 << p.page_shift;
   int32_t slot = -1;
   int64_t row = 0;
-  if (p.table.batch > 0 && t < p.qo_indptr[p.table.batch]) {
-    int lo = 0, hi = p.table.batch;  // qo_indptr[lo] <= t < qo_indptr[hi]
+  if (batch > 0 && t < qo[batch]) {
+    int lo = 0, hi = batch;  // qo[lo] <= t < qo[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (p.qo_indptr[mid] <= t) lo = mid;
+      if (qo[mid] <= t) lo = mid;
       else hi = mid;
     }
-    const int64_t first = p.qo_indptr[lo], end = p.qo_indptr[lo + 1];
+    const int64_t first = qo[lo], end = qo[lo + 1];
     const int64_t a = p.table.page_indptr[lo], b = p.table.page_indptr[lo + 1];
+    const int32_t last = p.table.last_page_len[lo];
     bool ok = first <= t && t < end && 0 <= a && a <= b && b <= p.table.num_indices;
     int64_t len = 0;
     if (ok && b > a) {
-      const int32_t last = p.table.last_page_len[lo];
       ok = last >= 1 && last <= P;
       len = (b - a - 1) * P + last;
     }
@@ -455,19 +474,22 @@ __global__ void __launch_bounds__(128) mla_slots_kernel(const __grid_constant__ 
 }  // namespace
 
 namespace {
+template <int kDtype, int kQ, int kHeads>
+cudaError_t launch_append_as(const AppendParams& p, cudaStream_t s) {
+  const int64_t groups = ((int64_t)p.a.num_tokens + kAppendWarps - 1) / kAppendWarps;
+  const int ctas = (p.a.kv_lat ? 1 : 0) + (kQ ? kQueryHeads / kHeads : 0);
+  return launch_chained(mla_append_kernel<kDtype, kQ, kHeads>, (unsigned)(groups * ctas), 32 * kAppendWarps, s, p);
+}
 template <int kDtype>
-cudaError_t launch_append_to(AppendParams& p, cudaStream_t s) {
-  const int64_t T = p.a.num_tokens;
-  p.key_ctas = p.a.kv_lat ? (int32_t)((T + 7) / 8) : 0;
-  const auto grid = [&](int heads) { return (unsigned)(p.key_ctas + (T * (kQueryHeads / heads) + 7) / 8); };
-  if (!p.a.q_pe) return launch_chained(mla_append_kernel<kDtype, 0, 16>, (unsigned)p.key_ctas, 256, s, p);
-  if (p.a.q_lat) return launch_chained(mla_append_kernel<kDtype, 2, MLA_HEADS_FULL>, grid(MLA_HEADS_FULL), 256, s, p);
-  if (T >= MLA_APPEND_MANY) return launch_chained(mla_append_kernel<kDtype, 1, 16>, grid(16), 256, s, p);
-  return launch_chained(mla_append_kernel<kDtype, 1, 4>, grid(4), 256, s, p);
+cudaError_t launch_append_to(const AppendParams& p, cudaStream_t s) {
+  if (!p.a.q_pe) return launch_append_as<kDtype, 0, 16>(p, s);
+  if (p.a.q_lat) return launch_append_as<kDtype, 2, MLA_HEADS_FULL>(p, s);
+  if (p.a.num_tokens >= MLA_APPEND_MANY) return launch_append_as<kDtype, 1, 16>(p, s);
+  return launch_append_as<kDtype, 1, 4>(p, s);
 }
 }  // namespace
 
-cudaError_t launch_append(AppendParams p, int kv_dtype, cudaStream_t s) {
+cudaError_t launch_append(const AppendParams& p, int kv_dtype, cudaStream_t s) {
   if (p.a.num_tokens == 0 || (!p.a.kv_lat && !p.a.q_pe)) return cudaSuccess;
   switch (kv_dtype) {
     case MLA_KV_BF16: return launch_append_to<MLA_KV_BF16>(p, s);
@@ -489,7 +511,7 @@ cudaError_t launch_gather(const GatherParams& p, int kv_dtype, cudaStream_t s) {
 
 cudaError_t launch_slots(const SlotsParams& p, cudaStream_t s) {
   if (p.num_tokens == 0) return cudaSuccess;
-  return launch_chained(mla_slots_kernel, (unsigned)((p.num_tokens + 127) / 128), 128, s, p);
+  return launch_chained(mla_slots_kernel, (unsigned)((p.num_tokens + kSlotsThreads - 1) / kSlotsThreads), kSlotsThreads, s, p);
 }
 
 }  // namespace mla
