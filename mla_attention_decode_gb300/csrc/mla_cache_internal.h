@@ -82,15 +82,17 @@ struct PageWs {
   int32_t* list;         // [num_pages] fresh pages by rank / pages to move into
   int32_t* from;         // [num_pages] pages to move from
   int32_t* refs;         // [num_pages] their counts
-  uint32_t* mask;        // [ceil(num_pages / 32)] pages in use
-  int32_t* pre;          // [ceil(num_pages / 32)] pages in use before each mask word
+  uint32_t* mask;        // [ceil(num_pages / 32)] a bit a page: in use
+  int32_t* pre;          // [ceil(num_pages / 32)] pages in use before each mask word, in its block
+  int32_t* block_used;   // [ceil(num_pages / 4096)] pages in use of each block,
+  int32_t* block_pre;    //   and before it
   size_t total;
 };
 enum { kHeadOk = 0, kHeadCopies = 1, kHeadReleases = 2, kHeadLive = 3, kHeadMoves = 4, kHeadTicket = 5 };
 
 inline PageWs page_ws(void* base, int32_t num_pages, int32_t batch) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t pages = up(4 * (size_t)num_pages), words = up(4 * ((size_t)num_pages + 31) / 32);
+  const size_t pages = up(4 * (size_t)num_pages), words = up(4 * (((size_t)num_pages + 31) / 32));
   const size_t seqs = up(4 * (size_t)batch);
   uint8_t* p = static_cast<uint8_t*>(base);
   PageWs w;
@@ -112,6 +114,9 @@ inline PageWs page_ws(void* base, int32_t num_pages, int32_t batch) {
   w.refs = reinterpret_cast<int32_t*>(take(pages));
   w.mask = reinterpret_cast<uint32_t*>(take(words));
   w.pre = reinterpret_cast<int32_t*>(take(words));
+  const size_t blocks = up(4 * (((size_t)num_pages + 4095) / 4096));
+  w.block_used = reinterpret_cast<int32_t*>(take(blocks));
+  w.block_pre = reinterpret_cast<int32_t*>(take(blocks));
   w.total = at;
   return w;
 }

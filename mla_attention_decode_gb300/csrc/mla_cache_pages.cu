@@ -173,22 +173,78 @@ __device__ __forceinline__ int owner(const int32_t* indptr, int batch, int e) {
   return lo;
 }
 
-// One count per CTA of the cluster: the sum of those of rank below `upto`, and
-// of all (the loads go out together).
-struct ClusterCounts {
-  int32_t n[kCluster];
-  __device__ __forceinline__ ClusterCounts(const cg::cluster_group& cluster, int32_t* mine) {
-    const int ctas = (int)cluster.num_blocks();
-#pragma unroll
-    for (int r = 0; r < kCluster; ++r) n[r] = r < ctas ? *cluster.map_shared_rank(mine, r) : 0;
+// ---------------------------------------------------------------- pages in use
+// Four counts from page pg on, `other` past the end.
+__device__ __forceinline__ int4 four_counts(const int32_t* refs, int pg, int pages, int other) {
+  if (pg + 4 <= pages) return *reinterpret_cast<const int4*>(refs + pg);
+  int4 v = make_int4(other, other, other, other);
+  if (pg < pages) v.x = refs[pg];
+  if (pg + 1 < pages) v.y = refs[pg + 1];
+  if (pg + 2 < pages) v.z = refs[pg + 2];
+  return v;
+}
+// Two lanes' four bits each to a byte of the mask.
+__device__ __forceinline__ void put_nibble(uint8_t* bytes, int quad, uint32_t nib) {
+  const uint32_t next = __shfl_down_sync(kFull, nib, 1);
+  if ((quad & 1) == 0) bytes[quad / 2] = (uint8_t)(nib | next << 4);
+}
+
+// One bit a page (its count is above 0) in mask[], in blocks of kBlock pages, 8 a
+// thread: the bits before word w in its block are in pre[w], the block's in
+// block_used[b].  The rank of a free page follows too: free pages before page x
+// = x - pages in use before x.
+constexpr int kBlock = 8 * kPlan;  // pages
+struct Blocks {
+  Scan<1, int32_t> scan;
+  int32_t before[kPlan];  // pages in use before each of kPlan blocks,
+  int32_t used[kPlan];    //   and in it
+};
+__device__ __forceinline__ void mask_block(const PageWs& ws, const int32_t* refs, int pages, int b, Blocks& s) {
+  const int tid = threadIdx.x, base = b * kBlock, here = min(kBlock, pages - base);
+  const int4 x = four_counts(refs + base, 8 * tid, here, 0), y = four_counts(refs + base, 8 * tid + 4, here, 0);
+  const uint32_t m = (uint32_t)(x.x > 0) | (uint32_t)(x.y > 0) << 1 | (uint32_t)(x.z > 0) << 2 |
+                     (uint32_t)(x.w > 0) << 3 | (uint32_t)(y.x > 0) << 4 | (uint32_t)(y.y > 0) << 5 |
+                     (uint32_t)(y.z > 0) << 6 | (uint32_t)(y.w > 0) << 7;
+  int32_t v[1] = {__popc(m)}, sum[1];
+  s.scan.run(v, sum);
+  const int i = b * kPlan + tid;
+  if ((8 * tid & ~31) < here) {  // whole words, so that their last bits are 0
+    reinterpret_cast<uint8_t*>(ws.mask)[i] = (uint8_t)m;
+    if ((tid & 3) == 0) ws.pre[i >> 2] = v[0];
   }
-  __device__ __forceinline__ int32_t below(int upto) const {
-    int32_t s = 0;
-#pragma unroll
-    for (int r = 0; r < kCluster; ++r) s += r < upto ? n[r] : 0;
-    return s;
+  if (tid == 0) ws.block_used[b] = sum[0];
+}
+// This thread's 8 pages of block b: the first, their bits, the pages in use before it.
+struct Eight {
+  int64_t page;
+  uint32_t used;
+  int32_t before;
+  __device__ __forceinline__ Eight(const PageWs& ws, int b, int32_t before_block, int64_t pages) {
+    const int i = b * kPlan + threadIdx.x, shift = (i & 3) * 8;
+    page = 8ll * i;
+    used = 0;
+    before = 0;
+    if (page >= pages) return;
+    const uint32_t word = ws.mask[i >> 2];
+    used = word >> shift & 255u;
+    before = before_block + ws.pre[i >> 2] + __popc(word & ((1u << shift) - 1));
   }
 };
+__host__ __device__ inline int blocks_of(int32_t pages) { return (int)(((int64_t)pages + kBlock - 1) / kBlock); }
+
+// A CTA per block, for caches of more blocks than the deciding cluster has CTAs
+// (1,049,444 pages: the cluster alone read their counts in 25 us).
+struct MaskParams {
+  PageWs ws;
+  const int32_t* refs;
+  int32_t pages;
+};
+__global__ void __launch_bounds__(kPlan) mla_mask_kernel(const __grid_constant__ MaskParams p) {
+  __shared__ Blocks s;
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  mask_block(p.ws, p.refs, p.pages, blockIdx.x, s);
+}
 
 // ---------------------------------------------------------------- fork, resize
 // Sequence n of `to` keeps the first `first` pages of its parent and gets fresh
@@ -286,21 +342,6 @@ __device__ __forceinline__ void plan_sequences(const TableParams& p, Scan<3, int
   }
 }
 
-// Which of the 8 pages from pg on are free, as bits (refs is 16-byte aligned
-// and pg a multiple of 8).
-__device__ __forceinline__ uint32_t free_bits(const int32_t* refs, int64_t pg, int64_t end) {
-  if (pg + 8 <= end) {
-    const int4 a = *reinterpret_cast<const int4*>(refs + pg), b = *reinterpret_cast<const int4*>(refs + pg + 4);
-    return (uint32_t)(a.x == 0) | (uint32_t)(a.y == 0) << 1 | (uint32_t)(a.z == 0) << 2 | (uint32_t)(a.w == 0) << 3 |
-           (uint32_t)(b.x == 0) << 4 | (uint32_t)(b.y == 0) << 5 | (uint32_t)(b.z == 0) << 6 |
-           (uint32_t)(b.w == 0) << 7;
-  }
-  uint32_t m = 0;
-  for (int i = 0; i < 8; ++i)
-    if (pg + i < end && refs[pg + i] == 0) m |= 1u << i;
-  return m;
-}
-
 // Carries a decided call out: table entries and the counts of shared pages,
 // what a resized sequence no longer holds, rows of part-filled pages.
 __device__ __forceinline__ void apply_table(const TableParams& p, int64_t at, int64_t step) {
@@ -340,41 +381,57 @@ __device__ __forceinline__ void apply_table(const TableParams& p, int64_t at, in
   }
 }
 
-// The first CTA goes over the sequences while the others count the free pages of
-// a slice each; then those list the free pages of lowest number, as many as are
-// needed.
+// The first CTA goes over the sequences, all of them over the pages (where
+// mla_mask_kernel has not), and then list the free pages of lowest number, as
+// many as are needed.
 __global__ void __launch_bounds__(kPlan, 1) mla_table_plan_kernel(const __grid_constant__ TableParams p) {
   __shared__ Scan<3, int64_t> scan;
-  __shared__ Scan<1, int32_t> scan1;
+  __shared__ Blocks s;
   __shared__ TableTotals s_tot;
-  __shared__ int32_t s_free;
   pdl_wait_primary();
   pdl_launch_dependents();
   const cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
-  const int64_t pages = p.c.num_pages;
-  // slices of 8-page multiples; with several CTAs the first, which has the
-  // sequences to go over, has none
-  const int sliced = ctas > 1 ? ctas - 1 : 1, mine = ctas > 1 ? rank - 1 : 0;
-  const int64_t slice = (pages + sliced * 8 - 1) / (sliced * 8) * 8;
-  const int64_t begin = mine < 0 ? 0 : min(pages, mine * slice), end = mine < 0 ? 0 : min(pages, begin + slice);
-  uint32_t bits = 0;  // of this thread's 8 pages of the slice's first pass
-  int32_t count[1] = {0}, sum[1];
-  for (int64_t pg = begin + 8 * tid; pg < end; pg += 8 * kPlan) {
-    const uint32_t m = free_bits(p.refs, pg, end);
-    if (pg < begin + 8 * kPlan) bits = m;
-    count[0] += __popc(m);
-  }
-  scan1.run(count, sum);
-  if (tid == 0) s_free = sum[0];
+  const int pages = p.c.num_pages, blocks = blocks_of(pages);
+  if (blocks <= kCluster)
+    for (int b = ctas - 1 - rank; b < blocks; b += ctas) mask_block(p.ws, p.refs, pages, b, s);
   if (rank == 0) plan_sequences(p, scan, s_tot);
   cluster.sync();
   const TableTotals tot = *cluster.map_shared_rank(&s_tot, 0);
-  const ClusterCounts free_pages(cluster, &s_free);
-  int64_t before = free_pages.below(rank);
-  const int64_t all = free_pages.below(kCluster);
-  const int32_t err = tot.bad || tot.pages > p.to.num_indices ? MLA_ERR_DEVICE_INDEX
-                                                              : (tot.fresh > all ? MLA_ERR_OUT_OF_PAGES : 0);
+  int32_t used = 0;  // before the blocks of this pass
+  int32_t err = tot.bad || tot.pages > p.to.num_indices ? MLA_ERR_DEVICE_INDEX : 0;
+  // every page in use, by all threads of each CTA
+  int32_t all[1] = {0}, sum[1];
+  for (int b = tid; b < blocks; b += kPlan) all[0] += p.ws.block_used[b];
+  s.scan.run(all, sum);
+  if (err == 0 && tot.fresh > pages - sum[0]) err = MLA_ERR_OUT_OF_PAGES;
+  if (err == 0) {
+    for (int base = 0; base < blocks; base += kPlan) {
+      int32_t v[1] = {base + tid < blocks ? p.ws.block_used[base + tid] : 0};
+      s.used[tid] = v[0];
+      s.scan.run(v, sum);
+      s.before[tid] = used + v[0];
+      __syncthreads();
+      const int last = min(blocks - base, kPlan);
+      for (int i = rank; i < last; i += ctas) {
+        const int b = base + i;
+        if ((int64_t)b * kBlock - s.before[i] >= tot.fresh) break;  // so are the blocks after it
+        if (s.used[i] == kBlock) continue;                          // no free page
+        const Eight e(p.ws, b, s.before[i], pages);
+        if (e.page >= pages) continue;
+        uint32_t m = ~e.used & 255u;
+        if (pages - e.page < 8) m &= (1u << (pages - e.page)) - 1;
+        for (int64_t k = e.page - e.before; m != 0 && k < tot.fresh; ++k) {
+          const int32_t free_page = (int32_t)e.page + __ffs(m) - 1;
+          m &= m - 1;
+          p.ws.list[k] = free_page;
+          p.refs[free_page] = 1;
+        }
+      }
+      used += sum[0];
+      __syncthreads();
+    }
+  }
   if (rank == 0) {
     if (err) {
       for (int n = tid; n <= p.to.batch; n += kPlan) {
@@ -389,23 +446,7 @@ __global__ void __launch_bounds__(kPlan, 1) mla_table_plan_kernel(const __grid_c
       p.ws.head[kHeadReleases] = tot.release;
     }
   }
-  if (err == 0) {
-    for (int64_t base = begin; base < end && before < tot.fresh; base += 8 * kPlan) {
-      const int64_t pg = base + 8 * tid;
-      uint32_t m = base == begin ? bits : (pg < end ? free_bits(p.refs, pg, end) : 0u);
-      int32_t v[1] = {__popc(m)};
-      scan1.run(v, sum);
-      for (int64_t k = before + v[0]; m != 0 && k < tot.fresh; ++k) {
-        const int32_t free_page = (int32_t)pg + __ffs(m) - 1;
-        m &= m - 1;
-        p.ws.list[k] = free_page;
-        p.refs[free_page] = 1;
-      }
-      before += sum[0];
-    }
-  }
-  // also keeps every CTA's shared memory alive until the others have read it
-  cluster.sync();
+  cluster.sync();  // the first CTA's shared memory stays until the others have read it
 }
 
 __global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_table_apply_kernel(const __grid_constant__ TableParams p) {
@@ -434,21 +475,6 @@ struct TableLocal {
 };
 static_assert(sizeof(TableLocal) <= 48 * 1024, "static shared memory");
 
-// Four counts from page pg on, `other` past the end.
-__device__ __forceinline__ int4 four_counts(const int32_t* refs, int pg, int pages, int other) {
-  if (pg + 4 <= pages) return *reinterpret_cast<const int4*>(refs + pg);
-  int4 v = make_int4(other, other, other, other);
-  if (pg < pages) v.x = refs[pg];
-  if (pg + 1 < pages) v.y = refs[pg + 1];
-  if (pg + 2 < pages) v.z = refs[pg + 2];
-  return v;
-}
-// Two lanes' four bits each to a byte of the mask.
-__device__ __forceinline__ void put_nibble(uint8_t* bytes, int quad, uint32_t nib) {
-  const uint32_t next = __shfl_down_sync(kFull, nib, 1);
-  if ((quad & 1) == 0) bytes[quad / 2] = (uint8_t)(nib | next << 4);
-}
-
 __global__ void __launch_bounds__(kPlan, 1) mla_table_local_kernel(const __grid_constant__ TableParams p) {
   __shared__ TableLocal s;
   pdl_wait_primary();
@@ -472,8 +498,8 @@ __global__ void __launch_bounds__(kPlan, 1) mla_table_local_kernel(const __grid_
 #pragma unroll
   for (int i = 0; i < kPasses; ++i)
     put_nibble(s.mask.bytes, i * kPlan + tid,
-               (uint32_t)(c4[i].x == 0) | (uint32_t)(c4[i].y == 0) << 1 | (uint32_t)(c4[i].z == 0) << 2 |
-                   (uint32_t)(c4[i].w == 0) << 3);
+               (uint32_t)(c4[i].x <= 0) | (uint32_t)(c4[i].y <= 0) << 1 | (uint32_t)(c4[i].z <= 0) << 2 |
+                   (uint32_t)(c4[i].w <= 0) << 3);
   __syncthreads();
   if (!q.ok) atomicOr(&s.flags, 1);
   if (q.release) atomicOr(&s.flags, 2);
@@ -561,75 +587,60 @@ __global__ void __launch_bounds__(256) mla_free_kernel(const __grid_constant__ F
 }
 
 // ---------------------------------------------------------------- compact
-// Which of the 8 pages from pg on are in use, as bits.
-__device__ __forceinline__ uint32_t used_bits(const int32_t* refs, int64_t pg, int64_t end) {
-  if (pg + 8 <= end) {
-    const int4 a = *reinterpret_cast<const int4*>(refs + pg), b = *reinterpret_cast<const int4*>(refs + pg + 4);
-    return (uint32_t)(a.x > 0) | (uint32_t)(a.y > 0) << 1 | (uint32_t)(a.z > 0) << 2 | (uint32_t)(a.w > 0) << 3 |
-           (uint32_t)(b.x > 0) << 4 | (uint32_t)(b.y > 0) << 5 | (uint32_t)(b.z > 0) << 6 | (uint32_t)(b.w > 0) << 7;
-  }
-  uint32_t m = 0;
-  for (int i = 0; i < 8; ++i)
-    if (pg + i < end && refs[pg + i] > 0) m |= 1u << i;
-  return m;
-}
-
-// One bit a page (in use), the pages in use before each word of 32, then the
-// two lists: free pages below L, pages in use from L on.  A thread takes 8
-// pages, so that a slice of 4096 pages is one pass with every load in flight;
-// each CTA has a slice.
+// The pages in use before each block, then the two lists: free pages below L,
+// pages in use from L on.  Every CTA sums the blocks for itself, so where
+// mla_mask_kernel has gone over the pages any number of CTAs can share the lists.
 __global__ void __launch_bounds__(kPlan, 1) mla_compact_plan_kernel(const __grid_constant__ CompactParams p) {
-  __shared__ Scan<1, int32_t> scan;
-  __shared__ int32_t s_live;
+  __shared__ Blocks s;
   pdl_wait_primary();
   pdl_launch_dependents();
   const cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
-  const int64_t pages = p.c.num_pages, words = (pages + 31) / 32;
-  const int64_t slice = (words + ctas - 1) / ctas * 32;  // pages
-  const int64_t begin = min(words * 32, rank * slice), end = min(words * 32, begin + slice);
-  uint8_t* mask = reinterpret_cast<uint8_t*>(p.ws.mask);  // byte pg / 8: pages pg .. pg + 7
-  int32_t live = 0;  // of the slice
-  for (int64_t base = begin; base < end; base += 8 * kPlan) {
-    const int64_t pg = base + 8 * tid;
-    const uint32_t m = pg < end ? used_bits(p.refs_in, pg, pages) : 0u;
-    int32_t v[1] = {__popc(m)}, sum[1];
-    scan.run(v, sum);
-    if (pg < end) {
-      mask[pg >> 3] = (uint8_t)m;
-      if ((pg & 31) == 0) p.ws.pre[pg >> 5] = live + v[0];  // within the slice, so far
-    }
-    live += sum[0];
+  const int tid = threadIdx.x, rank = (int)blockIdx.x, ctas = (int)gridDim.x;
+  const int pages = p.c.num_pages, blocks = blocks_of(pages);
+  if (blocks <= kCluster) {  // the grid is one cluster
+    for (int b = rank; b < blocks; b += ctas) mask_block(p.ws, p.refs_in, pages, b, s);
+    cluster.sync();
   }
-  if (tid == 0) s_live = live;
-  cluster.sync();
-  const ClusterCounts in_use(cluster, &s_live);
-  const int32_t before = in_use.below(rank), L = in_use.below(kCluster);
-  // pages in use below L: the slices before L's, the words of its slice before
-  // its word, the bits of the word (L == pages: all of them)
-  int32_t kept = L;
-  if (L < pages)
-    kept = in_use.below((int)(L / slice)) + p.ws.pre[L >> 5] +
-           __popc(p.ws.mask[L >> 5] & ((1u << (L & 31)) - 1));
-  cluster.sync();  // every CTA has read pre[] as it was
-  for (int64_t w = begin / 32 + tid; w < end / 32; w += kPlan) p.ws.pre[w] += before;
-  __syncthreads();
-  for (int64_t pg = begin + 8 * tid; pg < end; pg += 8 * kPlan) {
-    const int w = (int)(pg >> 5);
-    const uint32_t word = p.ws.mask[w], m = word >> (pg & 31) & 255u;
-    int32_t at = p.ws.pre[w] + __popc(word & ((1u << (pg & 31)) - 1));
-    for (int i = 0; i < 8; ++i) {
-      const int32_t page = (int32_t)pg + i;
-      if (m >> i & 1) {
-        if (page >= L) {
-          p.ws.from[at - kept] = page;
-          p.ws.refs[at - kept] = p.refs_in[page];
-        }
-        ++at;
-      } else if (page < L) {
-        p.ws.list[page - at] = page;
+  int32_t v[1] = {0}, sum[1];
+  for (int b = tid; b < blocks; b += kPlan) v[0] += p.ws.block_used[b];
+  s.scan.run(v, sum);
+  const int L = sum[0];
+  int kept = L;  // pages in use below L (L == pages: all of them)
+  if (L < pages) {
+    v[0] = 0;
+    for (int b = tid; b < L / kBlock; b += kPlan) v[0] += p.ws.block_used[b];
+    s.scan.run(v, sum);
+    kept = sum[0] + p.ws.pre[L >> 5] + __popc(p.ws.mask[L >> 5] & ((1u << (L & 31)) - 1));
+  }
+  int32_t used = 0;
+  for (int base = 0; base < blocks; base += kPlan) {
+    v[0] = base + tid < blocks ? p.ws.block_used[base + tid] : 0;
+    s.used[tid] = v[0];
+    s.scan.run(v, sum);
+    s.before[tid] = used + v[0];
+    if (rank == 0 && base + tid < blocks) p.ws.block_pre[base + tid] = used + v[0];
+    __syncthreads();
+    const int last = min(blocks - base, kPlan);
+    for (int i = rank; i < last; i += ctas) {
+      // nothing to list: full and below L, or empty and from L on
+      const int64_t first = (int64_t)(base + i) * kBlock;
+      if (s.used[i] == (first + kBlock <= L ? kBlock : (first >= L ? 0 : -1))) continue;
+      const Eight e(p.ws, base + i, s.before[i], pages);
+      // below L the free pages, from L on those in use
+      const uint32_t below = e.page + 8 <= L ? 255u : (e.page >= L ? 0u : (1u << (L - e.page)) - 1);
+      for (uint32_t f = ~e.used & below; f != 0; f &= f - 1) {
+        const int j = __ffs(f) - 1;
+        p.ws.list[(int32_t)e.page + j - (e.before + __popc(e.used & ((1u << j) - 1)))] = (int32_t)e.page + j;
+      }
+      int at = e.before + __popc(e.used & below) - kept;
+      for (uint32_t f = e.used & ~below; f != 0; f &= f - 1, ++at) {
+        const int32_t page = (int32_t)e.page + __ffs(f) - 1;
+        p.ws.from[at] = page;
+        p.ws.refs[at] = p.refs_in[page];
       }
     }
+    used += sum[0];
+    __syncthreads();
   }
   if (rank == 0 && tid == 0) {
     p.ws.head[kHeadLive] = L;
@@ -648,7 +659,7 @@ __global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_compact_apply_kernel(c
   auto rank = [&](int pg, bool& used) {
     const uint32_t m = p.ws.mask[pg >> 5];
     used = m >> (pg & 31) & 1;
-    return p.ws.pre[pg >> 5] + __popc(m & ((1u << (pg & 31)) - 1));
+    return p.ws.block_pre[pg / kBlock] + p.ws.pre[pg >> 5] + __popc(m & ((1u << (pg & 31)) - 1));
   };
   for (int64_t pg = at; pg < pages; pg += step) {
     int32_t n = 0;
@@ -771,11 +782,20 @@ __global__ void __launch_bounds__(kLocalThreads, MLA_MOVE_CTAS)
   }
 }
 
-// The deciding kernel: one CTA where a single pass of its threads covers the
-// pages, else a cluster.
+// The deciding kernel: a cluster of as many CTAs as there are blocks of pages,
+// up to kCluster.  Beyond that a kernel of its own goes over the pages first;
+// `free_ctas`: the deciding CTAs then need no cluster, and are up to 152.
 template <class Kernel, class Params>
-cudaError_t plan_launch(Kernel kernel, int32_t pages, cudaStream_t s, const Params& p) {
-  const unsigned ctas = pages <= 8 * kPlan ? 1 : kCluster;
+cudaError_t plan_launch(Kernel kernel, const int32_t* refs, bool free_ctas, cudaStream_t s, const Params& p) {
+  const int blocks = blocks_of(p.c.num_pages);
+  if (blocks > kCluster) {
+    const MaskParams m{p.ws, refs, p.c.num_pages};
+    const cudaError_t e = launch_chained(mla_mask_kernel, (unsigned)blocks, kPlan, s, m);
+    if (e != cudaSuccess) return e;
+    if (free_ctas) return launch_chained(kernel, (unsigned)(blocks < 152 ? blocks : 152), kPlan, s, p);
+  }
+  unsigned ctas = 1;
+  while ((int)ctas < blocks && ctas < kCluster) ctas *= 2;
   return launch_chained(kernel, ctas, kPlan, s, p, ctas > 1 ? ctas : 0);
 }
 
@@ -805,7 +825,7 @@ cudaError_t launch_table(const TableParams& p, cudaStream_t s) {
   if (p.to.batch <= kPlan && p.c.num_pages <= kLocalPages && entries <= kClusterEntries &&
       most <= (p.forks ? kClusterForkBytes : kClusterResizeBytes))
     return launch_chained(mla_table_local_kernel, kCluster, kPlan, s, p, kCluster);
-  const cudaError_t e = plan_launch(mla_table_plan_kernel, p.c.num_pages, s, p);
+  const cudaError_t e = plan_launch(mla_table_plan_kernel, p.refs, false, s, p);
   if (e != cudaSuccess) return e;
   return launch_chained(mla_table_apply_kernel, grid_for(threads < entries ? entries : threads), 256, s, p);
 }
@@ -824,7 +844,7 @@ cudaError_t launch_compact(const CompactParams& p, cudaStream_t s) {
     const unsigned grid = grid_for(threads);
     return launch_chained(mla_compact_local_kernel, grid < kLocalGrid ? grid : kLocalGrid, kLocalThreads, s, p);
   }
-  const cudaError_t e = plan_launch(mla_compact_plan_kernel, p.c.num_pages, s, p);
+  const cudaError_t e = plan_launch(mla_compact_plan_kernel, p.refs_in, true, s, p);
   if (e != cudaSuccess) return e;
   int64_t threads = copy_threads(p.c, p.c.num_pages / 2);
   if (threads < p.num_indices) threads = p.num_indices;
