@@ -117,6 +117,7 @@ int table_call(const mla_cache* cache, int32_t* page_refs, const mla_page_table*
   p.to = *to;
   p.by = by;
   p.forks = forks;
+  p.entries_apart = 0;
   return done(mla::launch_table(p, static_cast<cudaStream_t>(stream)));
 }
 
@@ -294,6 +295,7 @@ int mla_cache_compact(const mla_cache* cache, const int32_t* page_refs, int32_t*
   p.idx_out = kv_indices_out;
   p.num_indices = num_indices;
   p.live = live;
+  p.entries_apart = 0;
   return done(mla::launch_compact(p, static_cast<cudaStream_t>(stream)));
 }
 

@@ -127,6 +127,7 @@ struct TableParams {     // fork and resize
   mla_page_table from, to;
   const int32_t* by;     // fork: the parent of each sequence; resize: its new length
   int32_t forks;
+  int32_t entries_apart;   // the table entries are another kernel's
   PageWs ws;
 };
 
@@ -138,6 +139,7 @@ struct CompactParams {
   int32_t* idx_out;
   int32_t num_indices;
   int32_t* live;
+  int32_t entries_apart;   // counts and table are another kernel's
   PageWs ws;
 };
 

@@ -28,6 +28,10 @@ constexpr int kCluster = 8;             // deciding CTAs
 #define MLA_CLUSTER_FORK_BYTES (2 << 20)
 #endif
 constexpr int64_t kClusterEntries = 32768, kClusterForkBytes = MLA_CLUSTER_FORK_BYTES, kClusterResizeBytes = 16 << 20;
+#ifndef MLA_APART
+#define MLA_APART 131072
+#endif
+constexpr int64_t kApartEntries = MLA_APART;
 constexpr unsigned kLocalGrid = 152 * MLA_MOVE_CTAS;  // all resident at once
 constexpr unsigned kMaxGrid = 152 * 8;  // CTAs of 256 threads that carry out
 
@@ -38,7 +42,11 @@ __device__ __forceinline__ void set_error(int32_t* error, int32_t code) {
 // ---------------------------------------------------------------- moving rows
 // A page's bytes are cut into segments of 256 units, one warp each: 8 units a
 // lane, all 8 loads in flight before the first store.
-constexpr int kSegUnits = 256;
+#ifndef MLA_DEEP
+#define MLA_DEEP 8
+#endif
+constexpr int kDeep = MLA_DEEP;
+constexpr int kSegUnits = 32 * kDeep;
 
 __host__ __device__ inline int kv_segs(const PageBytes& c) {
   return (int)(((int64_t)c.page_size * c.row_bytes / 16 + kSegUnits - 1) / kSegUnits);
@@ -51,12 +59,12 @@ template <class T>
 __device__ __forceinline__ void move_units(uint8_t* dst, const uint8_t* src, int units, int lane) {
   const T* s = reinterpret_cast<const T*>(src);
   T* d = reinterpret_cast<T*>(dst);
-  T v[8];
+  T v[kDeep];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < kDeep; ++i)
     if (32 * i + lane < units) v[i] = s[32 * i + lane];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < kDeep; ++i)
     if (32 * i + lane < units) d[32 * i + lane] = v[i];
 }
 
@@ -342,10 +350,10 @@ __device__ __forceinline__ void plan_sequences(const TableParams& p, Scan<3, int
   }
 }
 
-// Carries a decided call out: table entries and the counts of shared pages,
-// what a resized sequence no longer holds, rows of part-filled pages.
-__device__ __forceinline__ void apply_table(const TableParams& p, int64_t at, int64_t step) {
-  const int lane = threadIdx.x & 31, N = p.to.batch;
+// Carries a decided call out: table entries and the counts of shared pages, and
+// what a resized sequence no longer holds ...
+__device__ __forceinline__ void apply_entries(const TableParams& p, int64_t at, int64_t step) {
+  const int N = p.to.batch;
   const int total = p.to.page_indptr[N];
   for (int64_t e = at; e < total; e += step) {
     const int n = owner(p.to.page_indptr, N, (int)e);
@@ -372,6 +380,10 @@ __device__ __forceinline__ void apply_table(const TableParams& p, int64_t at, in
       release_page(p.refs, p.c.num_pages, p.from.kv_indices[e], p.ws.err);
     }
   }
+}
+// ... and the rows of part-filled pages.
+__device__ __forceinline__ void apply_copies(const TableParams& p, int64_t at, int64_t step) {
+  const int lane = threadIdx.x & 31;
   const int ks = kv_segs(p.c), segs = ks + scale_segs(p.c);
   const int64_t per = (int64_t)segs * p.c.num_layers, tasks = per * p.ws.head[kHeadCopies];
   for (int64_t task = at >> 5; task < tasks; task += step >> 5) {
@@ -453,7 +465,16 @@ __global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_table_apply_kernel(con
   pdl_wait_primary();
   pdl_launch_dependents();
   if (!p.ws.head[kHeadOk]) return;
-  apply_table(p, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+  if (!p.entries_apart) apply_entries(p, at, step);
+  apply_copies(p, at, step);
+}
+// Long tables apart from the rows: moving rows takes 128 registers a thread, a
+// quarter of the threads that a chain of dependent reads per entry wants.
+__global__ void __launch_bounds__(256) mla_table_entries_kernel(const __grid_constant__ TableParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  if (p.ws.head[kHeadOk]) apply_entries(p, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
 // Small calls (up to kPlan sequences, kLocalPages pages): each CTA of the cluster
@@ -649,12 +670,10 @@ __global__ void __launch_bounds__(kPlan, 1) mla_compact_plan_kernel(const __grid
   }
 }
 
-__global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_compact_apply_kernel(const __grid_constant__ CompactParams p) {
-  pdl_wait_primary();
-  pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, pages = p.c.num_pages;
-  const int L = p.ws.head[kHeadLive], moves = p.ws.head[kHeadMoves], kept = L - moves;
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+// The counts and the table by the pages' new numbers ...
+__device__ __forceinline__ void compact_entries(const CompactParams& p, int64_t at, int64_t step) {
+  const int pages = p.c.num_pages;
+  const int L = p.ws.head[kHeadLive], kept = L - p.ws.head[kHeadMoves];
   // pages in use before page pg, and whether pg is
   auto rank = [&](int pg, bool& used) {
     const uint32_t m = p.ws.mask[pg >> 5];
@@ -684,8 +703,22 @@ __global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_compact_apply_kernel(c
     }
     p.idx_out[i] = pg;
   }
+}
+// ... and their rows; the former by a kernel of its own where that is much (see
+// mla_table_entries_kernel).
+__global__ void __launch_bounds__(256) mla_compact_entries_kernel(const __grid_constant__ CompactParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  compact_entries(p, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
+}
+__global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_compact_apply_kernel(const __grid_constant__ CompactParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+  if (!p.entries_apart) compact_entries(p, at, step);
+  const int lane = threadIdx.x & 31;
   const int ks = kv_segs(p.c), segs = ks + scale_segs(p.c);
-  const int64_t per = (int64_t)segs * p.c.num_layers, tasks = per * moves;
+  const int64_t per = (int64_t)segs * p.c.num_layers, tasks = per * p.ws.head[kHeadMoves];
   for (int64_t task = at >> 5; task < tasks; task += step >> 5) {
     const int64_t i = task / per;
     const int rest = (int)(task - i * per), l = rest / segs, seg = rest - l * segs;
@@ -825,9 +858,17 @@ cudaError_t launch_table(const TableParams& p, cudaStream_t s) {
   if (p.to.batch <= kPlan && p.c.num_pages <= kLocalPages && entries <= kClusterEntries &&
       most <= (p.forks ? kClusterForkBytes : kClusterResizeBytes))
     return launch_chained(mla_table_local_kernel, kCluster, kPlan, s, p, kCluster);
-  const cudaError_t e = plan_launch(mla_table_plan_kernel, p.refs, false, s, p);
+  cudaError_t e = plan_launch(mla_table_plan_kernel, p.refs, false, s, p);
   if (e != cudaSuccess) return e;
-  return launch_chained(mla_table_apply_kernel, grid_for(threads < entries ? entries : threads), 256, s, p);
+  if (p.c.page_size == 1) threads = 0;  // no page is part-filled
+  TableParams q = p;
+  q.entries_apart = entries > kApartEntries || threads == 0;
+  if (q.entries_apart) {
+    e = launch_chained(mla_table_entries_kernel, grid_for(entries), 256, s, q);
+    if (e != cudaSuccess || threads == 0) return e;
+    entries = 0;
+  }
+  return launch_chained(mla_table_apply_kernel, grid_for(threads < entries ? entries : threads), 256, s, q);
 }
 
 cudaError_t launch_free(int32_t* refs, int32_t num_pages, const int32_t* pages, int32_t n, int32_t* error,
@@ -844,12 +885,18 @@ cudaError_t launch_compact(const CompactParams& p, cudaStream_t s) {
     const unsigned grid = grid_for(threads);
     return launch_chained(mla_compact_local_kernel, grid < kLocalGrid ? grid : kLocalGrid, kLocalThreads, s, p);
   }
-  const cudaError_t e = plan_launch(mla_compact_plan_kernel, p.refs_in, true, s, p);
+  cudaError_t e = plan_launch(mla_compact_plan_kernel, p.refs_in, true, s, p);
   if (e != cudaSuccess) return e;
-  int64_t threads = copy_threads(p.c, p.c.num_pages / 2);
-  if (threads < p.num_indices) threads = p.num_indices;
-  if (threads < p.c.num_pages) threads = p.c.num_pages;
-  return launch_chained(mla_compact_apply_kernel, grid_for(threads), 256, s, p);
+  int64_t threads = copy_threads(p.c, p.c.num_pages / 2), entries = p.num_indices;
+  if (entries < p.c.num_pages) entries = p.c.num_pages;
+  CompactParams q = p;
+  q.entries_apart = entries > kApartEntries;
+  if (q.entries_apart) {
+    e = launch_chained(mla_compact_entries_kernel, grid_for(entries), 256, s, q);
+    if (e != cudaSuccess) return e;
+    entries = 0;
+  }
+  return launch_chained(mla_compact_apply_kernel, grid_for(threads < entries ? entries : threads), 256, s, q);
 }
 
 }  // namespace mla

@@ -52,6 +52,15 @@ def bytes_of(pool):
     return torch.cat([kv, sc], -1)
 
 
+def bytes_row(pool, page, r):
+    """One row's bytes (and scale bytes) in every layer."""
+    at = page * pool.page_size + r
+    parts = [pool.kv.view(torch.uint8)[:, at].cpu()]
+    if pool.kv_dtype == binding.MLA_KV_MXFP4:
+        parts.append(pool.kv_scale[:, at].cpu())
+    return torch.cat(parts, -1)
+
+
 @pytest.mark.parametrize("kv_dtype", DTYPES)
 @pytest.mark.parametrize("page", [1, 2, 8, 64, 256])
 @pytest.mark.parametrize("layers,stride", [(1, 18), (3, 32)])
@@ -114,21 +123,28 @@ def check_state(pool, model, table, seqs, before, tags_to_bytes):
                     assert torch.equal(now[:, pg, r], tags_to_bytes[tag]), (pg, r)
 
 
-@pytest.mark.parametrize("kv_dtype,page,layers", [("bf16", 4, 2), ("fp8", 1, 1), ("mxfp4", 8, 3), ("fp8", 16, 1)])
+@pytest.mark.parametrize("kv_dtype,page,layers,pages", [
+    ("bf16", 4, 2, 90), ("fp8", 1, 1, 90), ("mxfp4", 8, 3, 90), ("fp8", 16, 1, 90),
+    # past what one CTA, the deciding cluster, and a kernel of its own for the counts go over
+    ("fp8", 4, 1, 16385), ("mxfp4", 2, 2, 32800), ("mxfp4", 2, 1, 70001)])
 @pytest.mark.parametrize("seed", [1, 2, 3])
-def test_random_life_of_a_pool(kv_dtype, page, layers, seed):
+def test_random_life_of_a_pool(kv_dtype, page, layers, pages, seed):
     """Grow, write, fork, truncate, free and compact in random order: tables,
-    counts and every live row follow the model; pages never handed out twice."""
+    counts and every live row follow the model; pages never handed out twice.
+    In a large cache others hold all but 90 pages, at random places."""
     rng = np.random.RandomState(seed)
-    pages = 90
     pool, model = new_pool(kv_dtype, pages, page, layers), PoolModel(pages, page)
+    others = rng.permutation(pages)[90:]
+    for g in others:
+        model.refs[g] = 1
+    pool.refs[torch.from_numpy(others).to(DEV)] = 1
     seqs, table = [([], 0)] * 3, table_of([([], 0)] * 3, page, 1, DEV)
     tags, tags_to_bytes = 0, {}
 
     def run(call, want, batch):
         """`want`: the model's sequences, or None where it found too few pages."""
         nonlocal seqs, table
-        cap = 2 * pages * 6
+        cap = 1000
         out = pool.table(batch, cap)
         out[1].fill_(-7)
         call(out)
@@ -340,6 +356,49 @@ def test_long_tables_of_many_sequences():
     t2 = pool.resize(t0, i32([n // 2 for n in lens]), pool.table(3000, sum(lens)))
     assert [s[0] for s in seqs_of(t2, 1)] == [list(range(at[i], at[i] + n // 2)) for i, n in enumerate(lens)]
     assert pool.poll_error() == 0
+
+
+def test_long_tables_with_part_filled_pages():
+    """Tables of over 131072 entries whose sequences end inside a page: forks copy
+    it, and so does a cut into a shared page."""
+    rng = np.random.RandomState(1)
+    page, n = 2, 600
+    lens = rng.randint(300, 700, n).tolist()
+    cnt = [-(-x // page) for x in lens]
+    pool = new_pool("mxfp4", 3 * sum(cnt) + 10, page)
+    t0 = pool.resize(pool.table(n, 0), i32(lens), pool.table(n, sum(cnt)))
+    at = np.cumsum([0] + cnt)
+    pages = [list(range(at[i], at[i + 1])) for i in range(n)]
+    assert [s[0] for s in seqs_of(t0, page)] == pages
+    before = bytes_of(pool)
+    t1 = pool.fork(t0, i32(list(range(n))), pool.table(n, sum(cnt)))
+    fresh, want = sum(cnt), []
+    for i in range(n):
+        row = list(pages[i])
+        if lens[i] % 2:
+            row[-1], fresh = fresh, fresh + 1
+        want.append(row)
+    assert [s[0] for s in seqs_of(t1, page)] == want
+    now = bytes_of(pool)
+    odd = [i for i in range(n) if lens[i] % 2]
+    assert torch.equal(now[:, [want[i][-1] for i in odd], 0], before[:, [pages[i][-1] for i in odd], 0])
+    assert torch.equal(now[:, [want[i][-1] for i in odd], 1], before[:, [want[i][-1] for i in odd], 1])
+    # cut to an odd length inside shared pages, and others grown
+    new = [x // 2 | 1 if i % 2 else x + 5 for i, x in enumerate(lens)]
+    t2 = pool.resize(t1, i32(new), pool.table(n, sum(-(-x // page) for x in new)))
+    assert pool.poll_error() == 0
+    for i, (row, length) in enumerate(seqs_of(t2, page)):
+        assert length == new[i] and len(row) == -(-new[i] // page)
+        if i % 2:  # its last page is a copy of the shared one's first row
+            j = len(row) - 1
+            assert row[:j] == want[i][:j] and row[j] >= fresh
+            assert torch.equal(bytes_row(pool, row[j], 0), before[:, pages[i][j], 0])
+        else:
+            assert row[:cnt[i]] == want[i]
+    counts = torch.zeros(pool.num_pages, dtype=torch.int32)
+    for t in (t0, t2):
+        counts.index_add_(0, t[1][:int(t[0][-1])].long().cpu(), torch.ones(int(t[0][-1]), dtype=torch.int32))
+    assert torch.equal(pool.refs.cpu(), counts)
 
 
 @pytest.mark.parametrize("kv_dtype", DTYPES)
