@@ -40,79 +40,178 @@ __device__ __forceinline__ void set_error(int32_t* error, int32_t code) {
 }
 
 // ---------------------------------------------------------------- moving rows
-// A page's bytes are cut into segments of 256 units, one warp each: 8 units a
-// lane, all 8 loads in flight before the first store.
-#ifndef MLA_DEEP
-#define MLA_DEEP 8
-#endif
-constexpr int kDeep = MLA_DEEP;
+// A warp moves up to kSegUnits units of 16 bytes at a time, kDeep a lane, all
+// its loads in flight before the first store.  8 a lane on 128 registers (2 CTAs
+// of 256 an SM) came to 97% of the copy rate over 4001 MXFP4 pages in 6 layers
+// (143 us); 4 a lane with twice the CTAs took 152 us, and 8 a lane forced into 64
+// registers 182 us.
+constexpr int kDeep = 8;
 constexpr int kSegUnits = 32 * kDeep;
 
+__device__ __forceinline__ uint4 load_unit(const uint8_t* p, int unit) {
+  uint4 v;
+  switch (unit) {
+    case 16: v = *reinterpret_cast<const uint4*>(p); break;
+    case 8: v.x = reinterpret_cast<const uint32_t*>(p)[0], v.y = reinterpret_cast<const uint32_t*>(p)[1]; break;
+    case 4: v.x = *reinterpret_cast<const uint32_t*>(p); break;
+    case 2: v.x = *reinterpret_cast<const uint16_t*>(p); break;
+    default: v.x = *p; break;
+  }
+  return v;
+}
+__device__ __forceinline__ void store_unit(uint8_t* p, uint4 v, int unit) {
+  switch (unit) {
+    case 16: *reinterpret_cast<uint4*>(p) = v; break;
+    case 8: reinterpret_cast<uint32_t*>(p)[0] = v.x, reinterpret_cast<uint32_t*>(p)[1] = v.y; break;
+    case 4: *reinterpret_cast<uint32_t*>(p) = v.x; break;
+    case 2: *reinterpret_cast<uint16_t*>(p) = (uint16_t)v.x; break;
+    default: *p = (uint8_t)v.x; break;
+  }
+}
+
+// The first `rows` rows of page src to page dst in layer l, segment `seg`: those
+// of the rows first (`ks` of them for a whole page), then those of the scale rows.
 __host__ __device__ inline int kv_segs(const PageBytes& c) {
   return (int)(((int64_t)c.page_size * c.row_bytes / 16 + kSegUnits - 1) / kSegUnits);
 }
 __host__ __device__ inline int scale_segs(const PageBytes& c) {
   return c.scale ? (int)(((int64_t)c.page_size * c.scale_stride / c.scale_unit + kSegUnits - 1) / kSegUnits) : 0;
 }
-
-template <class T>
-__device__ __forceinline__ void move_units(uint8_t* dst, const uint8_t* src, int units, int lane) {
-  const T* s = reinterpret_cast<const T*>(src);
-  T* d = reinterpret_cast<T*>(dst);
-  T v[kDeep];
-#pragma unroll
-  for (int i = 0; i < kDeep; ++i)
-    if (32 * i + lane < units) v[i] = s[32 * i + lane];
-#pragma unroll
-  for (int i = 0; i < kDeep; ++i)
-    if (32 * i + lane < units) d[32 * i + lane] = v[i];
-}
-
-// Segment `seg` (of kv_segs + scale_segs) of the first `rows` rows of page src
-// to page dst, in layer l.
 __device__ __forceinline__ void move_segment(const PageBytes& c, int src, int dst, int rows, int l, int seg, int ks,
                                              int lane) {
-  if (seg < ks) {
-    const int64_t page = (int64_t)c.page_size * c.row_bytes;
-    const int64_t at = (int64_t)seg * (kSegUnits * 16), bytes = (int64_t)rows * c.row_bytes - at;
-    if (bytes <= 0) return;
-    uint8_t* base = c.kv + l * c.kv_layer + at;
-    move_units<uint4>(base + dst * page, base + src * page, (int)(min(bytes, (int64_t)(kSegUnits * 16)) >> 4), lane);
-    return;
-  }
-  const int u = c.scale_unit;
-  const int64_t page = (int64_t)c.page_size * c.scale_stride;
-  const int64_t at = (int64_t)(seg - ks) * kSegUnits * u, bytes = (int64_t)rows * c.scale_stride - at;
+  const bool kv = seg < ks;
+  const int unit = kv ? 16 : c.scale_unit;
+  const int64_t row = kv ? c.row_bytes : c.scale_stride, page = c.page_size * row;
+  const int64_t at = (int64_t)(kv ? seg : seg - ks) * kSegUnits * unit, bytes = rows * row - at;
   if (bytes <= 0) return;
-  const int units = (int)(min(bytes, (int64_t)kSegUnits * u) / u);
-  uint8_t* base = c.scale + l * c.scale_layer + at;
+  const int units = (int)(min(bytes, (int64_t)kSegUnits * unit) / unit);
+  uint8_t* base = (kv ? c.kv + l * c.kv_layer : c.scale + l * c.scale_layer) + at + (int64_t)lane * unit;
   uint8_t* d = base + dst * page;
   const uint8_t* s = base + src * page;
-  switch (u) {
-    case 16: move_units<uint4>(d, s, units, lane); break;
-    case 8: move_units<uint2>(d, s, units, lane); break;
-    case 4: move_units<uint32_t>(d, s, units, lane); break;
-    case 2: move_units<uint16_t>(d, s, units, lane); break;
-    default: move_units<uint8_t>(d, s, units, lane); break;
+  uint4 v[kDeep];
+  if (unit == 16) {
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i)
+      if (32 * i + lane < units) v[i] = reinterpret_cast<const uint4*>(s)[32 * i];
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i)
+      if (32 * i + lane < units) reinterpret_cast<uint4*>(d)[32 * i] = v[i];
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kDeep; ++i)
+    if (32 * i + lane < units) v[i] = load_unit(s + 32 * i * unit, unit);
+#pragma unroll
+  for (int i = 0; i < kDeep; ++i)
+    if (32 * i + lane < units) store_unit(d + 32 * i * unit, v[i], unit);
+}
+
+// Whole pages: page pair(i) -> (src, dst), i < n, in every layer (src < 0: none).
+// A page and its scale rows are one run of 16-byte units where the latter divide
+// into them; a page of up to kSegUnits units is moved by 4 to 32 lanes, so that
+// a warp has several small pages in flight (a page of one MXFP4 row is 18 units
+// and nine of 2 bytes).  `at`: the thread's index of `step`, both over warps.
+template <class Pair>
+__device__ __forceinline__ void move_pages(const PageBytes& c, int64_t n, int64_t at, int64_t step, Pair pair) {
+  const int lane = threadIdx.x & 31, unit = c.scale_unit;
+  const int64_t kv_page = (int64_t)c.page_size * c.row_bytes;
+  const int64_t scale_page = c.scale ? (int64_t)c.page_size * c.scale_stride : 0;
+  const int64_t kvu = kv_page / 16, su = unit == 16 ? 0 : scale_page / unit;
+  const int64_t units = kvu + (unit == 16 ? scale_page / 16 : 0);
+  const int64_t warp = at >> 5, warps = step >> 5;
+  // the task's quotient by d: in 32 bits where the call's tasks fit
+  const auto split = [](int64_t task, int64_t d, bool narrow, int64_t& rest) {
+    const int64_t q = narrow ? (int64_t)((uint32_t)task / (uint32_t)d) : task / d;
+    rest = task - q * d;
+    return q;
+  };
+  if (units <= kSegUnits) {
+    int g = 4;  // lanes a page
+    while (g * kDeep < units) g *= 2;
+    const int sub = lane / g, gl = lane - sub * g;
+    const int64_t tasks = n * c.num_layers;
+    const bool narrow = tasks <= UINT32_MAX;
+    for (int64_t task = warp * (32 / g) + sub; task < tasks; task += warps * (32 / g)) {
+      int64_t l;
+      const int64_t i = split(task, c.num_layers, narrow, l);
+      const int2 p = pair(i, l == 0 && gl == 0);
+      if (p.x < 0) continue;
+      uint8_t* kv = c.kv + l * c.kv_layer;
+      uint8_t* sc = c.scale + l * c.scale_layer;
+      uint4 v[kDeep], w[3];
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k) {
+        const int64_t u = k * g + gl;
+        if (u < units)
+          v[k] = *reinterpret_cast<const uint4*>(u < kvu ? kv + p.x * kv_page + 16 * u
+                                                         : sc + p.x * scale_page + 16 * (u - kvu));
+      }
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (k * g + gl < su) w[k] = load_unit(sc + p.x * scale_page + (k * g + gl) * unit, unit);
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k) {
+        const int64_t u = k * g + gl;
+        if (u < units)
+          *reinterpret_cast<uint4*>(u < kvu ? kv + p.y * kv_page + 16 * u
+                                            : sc + p.y * scale_page + 16 * (u - kvu)) = v[k];
+      }
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (k * g + gl < su) store_unit(sc + p.y * scale_page + (k * g + gl) * unit, w[k], unit);
+      for (int64_t u = 3 * g + gl; u < su; u += g)  // (scale rows of odd strides)
+        store_unit(sc + p.y * scale_page + u * unit, load_unit(sc + p.x * scale_page + u * unit, unit), unit);
+    }
+    return;
+  }
+  const int64_t us = (units + kSegUnits - 1) / kSegUnits, segs = us + (su + kSegUnits - 1) / kSegUnits;
+  const int64_t per = segs * c.num_layers, tasks = per * n;
+  const bool narrow = tasks <= UINT32_MAX;
+  for (int64_t task = warp; task < tasks; task += warps) {
+    int64_t rest, seg;
+    const int64_t i = split(task, per, narrow, rest), l = split(rest, segs, narrow, seg);
+    const int2 p = pair(i, rest == 0 && lane == 0);
+    if (p.x < 0) continue;
+    uint8_t* kv = c.kv + l * c.kv_layer;
+    uint8_t* sc = c.scale + l * c.scale_layer;
+    uint4 v[kDeep];
+    if (seg < us) {
+      const int64_t u0 = seg * kSegUnits + lane;
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k) {
+        const int64_t u = u0 + 32 * k;
+        if (u < units)
+          v[k] = *reinterpret_cast<const uint4*>(u < kvu ? kv + p.x * kv_page + 16 * u
+                                                         : sc + p.x * scale_page + 16 * (u - kvu));
+      }
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k) {
+        const int64_t u = u0 + 32 * k;
+        if (u < units)
+          *reinterpret_cast<uint4*>(u < kvu ? kv + p.y * kv_page + 16 * u
+                                            : sc + p.y * scale_page + 16 * (u - kvu)) = v[k];
+      }
+    } else {
+      const int64_t u0 = (seg - us) * kSegUnits + lane;
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k)
+        if (u0 + 32 * k < su) v[k] = load_unit(sc + p.x * scale_page + (u0 + 32 * k) * unit, unit);
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k)
+        if (u0 + 32 * k < su) store_unit(sc + p.y * scale_page + (u0 + 32 * k) * unit, v[k], unit);
+    }
   }
 }
 
 __global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_copy_pages_kernel(const __grid_constant__ CopyParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int ks = kv_segs(p.c), segs = ks + scale_segs(p.c);
-  const int64_t per = (int64_t)segs * p.c.num_layers, tasks = per * p.n;
-  for (int64_t task = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); task < tasks; task += (int64_t)gridDim.x * 8) {
-    const int64_t i = task / per;
-    const int rest = (int)(task - i * per), l = rest / segs, seg = rest - l * segs;
+  move_pages(p.c, p.n, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256, [&](int64_t i, bool tell) {
     const int src = p.src[i], dst = p.dst[i];
-    if (src < 0 || src >= p.c.num_pages || dst < 0 || dst >= p.c.num_pages) {
-      if (rest == 0 && lane == 0) set_error(p.error, MLA_ERR_DEVICE_INDEX);
-      continue;
-    }
-    if (src != dst) move_segment(p.c, src, dst, p.c.page_size, l, seg, ks, lane);
-  }
+    const bool ok = src >= 0 && src < p.c.num_pages && dst >= 0 && dst < p.c.num_pages;
+    if (!ok && tell) set_error(p.error, MLA_ERR_DEVICE_INDEX);
+    return ok && src != dst ? make_int2(src, dst) : make_int2(-1, -1);
+  });
 }
 
 // ---------------------------------------------------------------- prefix sums
@@ -716,14 +815,8 @@ __global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_compact_apply_kernel(c
   pdl_launch_dependents();
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
   if (!p.entries_apart) compact_entries(p, at, step);
-  const int lane = threadIdx.x & 31;
-  const int ks = kv_segs(p.c), segs = ks + scale_segs(p.c);
-  const int64_t per = (int64_t)segs * p.c.num_layers, tasks = per * p.ws.head[kHeadMoves];
-  for (int64_t task = at >> 5; task < tasks; task += step >> 5) {
-    const int64_t i = task / per;
-    const int rest = (int)(task - i * per), l = rest / segs, seg = rest - l * segs;
-    move_segment(p.c, p.ws.from[i], p.ws.list[i], p.c.page_size, l, seg, ks, lane);
-  }
+  move_pages(p.c, p.ws.head[kHeadMoves], at, step,
+             [&](int64_t i, bool) { return make_int2(p.ws.from[i], p.ws.list[i]); });
 }
 
 // Up to kLocalPages pages: each CTA decides for itself, in shared memory, and
@@ -745,7 +838,7 @@ __global__ void __launch_bounds__(kLocalThreads, MLA_MOVE_CTAS)
   __shared__ CompactLocal s;
   pdl_wait_primary();
   pdl_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, pages = p.c.num_pages, words = (pages + 31) / 32;
+  const int tid = threadIdx.x, pages = p.c.num_pages, words = (pages + 31) / 32;
 #pragma unroll 4
   for (int base = 0; base < pages; base += 4 * kLocalThreads) {
     const int4 v = four_counts(p.refs_in, base + 4 * tid, pages, 0);
@@ -807,12 +900,7 @@ __global__ void __launch_bounds__(kLocalThreads, MLA_MOVE_CTAS)
     for (int pg = L + tid; pg < pages; pg += kLocalThreads) p.refs_out[pg] = 0;
     if (tid == 0) p.ws.head[kHeadTicket] = 0;
   }
-  const int ks = kv_segs(p.c), segs = ks + scale_segs(p.c);
-  const int64_t per = (int64_t)segs * p.c.num_layers, tasks = per * moves;
-  for (int64_t task = at >> 5; task < tasks; task += step >> 5) {
-    const int i = (int)(task / per), rest = (int)(task - i * per), l = rest / segs, seg = rest - l * segs;
-    move_segment(p.c, s.from[i], s.list[i], p.c.page_size, l, seg, ks, lane);
-  }
+  move_pages(p.c, moves, at, step, [&](int64_t i, bool) { return make_int2(s.from[i], s.list[i]); });
 }
 
 // The deciding kernel: a cluster of as many CTAs as there are blocks of pages,
