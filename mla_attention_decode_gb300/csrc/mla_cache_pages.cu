@@ -18,22 +18,29 @@ namespace cg = cooperative_groups;
 namespace mla {
 namespace {
 
-#ifndef MLA_MOVE_CTAS
-#define MLA_MOVE_CTAS 2
-#endif
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kPlan = 512;              // threads of a deciding CTA
-constexpr int kCluster = 8;             // deciding CTAs
-#ifndef MLA_CLUSTER_FORK_BYTES
-#define MLA_CLUSTER_FORK_BYTES (2 << 20)
-#endif
-constexpr int64_t kClusterEntries = 32768, kClusterForkBytes = MLA_CLUSTER_FORK_BYTES, kClusterResizeBytes = 16 << 20;
-#ifndef MLA_APART
-#define MLA_APART 131072
-#endif
-constexpr int64_t kApartEntries = MLA_APART;
-constexpr unsigned kLocalGrid = 152 * MLA_MOVE_CTAS;  // all resident at once
-constexpr unsigned kMaxGrid = 152 * 8;  // CTAs of 256 threads that carry out
+constexpr int kPlan = 512;               // threads of a deciding CTA
+constexpr int kCluster = 8;              // deciding CTAs
+constexpr int kMoveCtas = 2;             // CTAs an SM that move rows (128 registers a thread)
+constexpr unsigned kLocalGrid = 152 * kMoveCtas;  // all of those resident at once
+constexpr unsigned kMaxGrid = 152 * 8;   // CTAs of 256 threads that carry out a call (the kernels loop)
+
+// Which kernels a call takes; both sides of each border measured in graphs of the
+// call on a GB300.
+// The cluster that decides a small fork or resize also carries it out, up to this
+// many table entries (8192 entries: 6.0 us against 8.3 in two launches) ...
+constexpr int64_t kClusterEntries = 32768;
+// ... and bytes of pages that may have to be copied: a fork of n bf16 sequences
+// of 64-row pages, with its free, takes 8.5 us against 9.9 at n = 16 (1.2 MB),
+// 10.3 against 9.6 at n = 32 and 32 against 12 at n = 256.  A resize copies a page
+// only where a fork's sequence is cut inside a shared one, so it may risk more.
+constexpr int64_t kClusterForkBytes = 2 << 20, kClusterResizeBytes = 16 << 20;
+// Table entries by a kernel of their own: 65,536 entries 11.1 us against 10.4 in
+// one with the rows, 262,144 entries 11.5 against 15.2.
+constexpr int64_t kApartEntries = 131072;
+// The same for a compaction's pages or entries: 200,000 pages 21.2 us against
+// 20.6, 400,000 pages 32.2 against 33.5.
+constexpr int64_t kApartPages = 262144;
 
 __device__ __forceinline__ void set_error(int32_t* error, int32_t code) {
   if (error) *error = code;
@@ -203,7 +210,7 @@ __device__ __forceinline__ void move_pages(const PageBytes& c, int64_t n, int64_
   }
 }
 
-__global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_copy_pages_kernel(const __grid_constant__ CopyParams p) {
+__global__ void __launch_bounds__(256, kMoveCtas) mla_copy_pages_kernel(const __grid_constant__ CopyParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
   move_pages(p.c, p.n, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256, [&](int64_t i, bool tell) {
@@ -560,7 +567,7 @@ __global__ void __launch_bounds__(kPlan, 1) mla_table_plan_kernel(const __grid_c
   cluster.sync();  // the first CTA's shared memory stays until the others have read it
 }
 
-__global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_table_apply_kernel(const __grid_constant__ TableParams p) {
+__global__ void __launch_bounds__(256, kMoveCtas) mla_table_apply_kernel(const __grid_constant__ TableParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
   if (!p.ws.head[kHeadOk]) return;
@@ -810,7 +817,7 @@ __global__ void __launch_bounds__(256) mla_compact_entries_kernel(const __grid_c
   pdl_launch_dependents();
   compact_entries(p, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
-__global__ void __launch_bounds__(256, MLA_MOVE_CTAS) mla_compact_apply_kernel(const __grid_constant__ CompactParams p) {
+__global__ void __launch_bounds__(256, kMoveCtas) mla_compact_apply_kernel(const __grid_constant__ CompactParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
@@ -833,7 +840,7 @@ struct CompactLocal {
   } mask;
   uint16_t list[kLocalPages / 2], from[kLocalPages / 2];
 };
-__global__ void __launch_bounds__(kLocalThreads, MLA_MOVE_CTAS)
+__global__ void __launch_bounds__(kLocalThreads, kMoveCtas)
     mla_compact_local_kernel(const __grid_constant__ CompactParams p) {
   __shared__ CompactLocal s;
   pdl_wait_primary();
@@ -978,7 +985,7 @@ cudaError_t launch_compact(const CompactParams& p, cudaStream_t s) {
   int64_t threads = copy_threads(p.c, p.c.num_pages / 2), entries = p.num_indices;
   if (entries < p.c.num_pages) entries = p.c.num_pages;
   CompactParams q = p;
-  q.entries_apart = entries > kApartEntries;
+  q.entries_apart = entries > kApartPages;
   if (q.entries_apart) {
     e = launch_chained(mla_compact_entries_kernel, grid_for(entries), 256, s, q);
     if (e != cudaSuccess) return e;

@@ -9,15 +9,6 @@ namespace mla {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-#ifndef MLA_HEADS_FULL
-#define MLA_HEADS_FULL 2
-#endif
-#ifndef MLA_APPEND_WARPS
-#define MLA_APPEND_WARPS 4
-#endif
-#ifndef MLA_APPEND_MANY
-#define MLA_APPEND_MANY 608
-#endif
 
 __device__ __forceinline__ void set_error(int32_t* error, int32_t code) {
   if (error) *error = code;
@@ -101,6 +92,10 @@ __device__ __forceinline__ uint32_t e8m0_of(float amax, float& inv) {
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 // ---------------------------------------------------------------- append
+// Bound by bytes at many tokens (a key row's 1152 in and 1152, 576 or 306 out, a
+// query head's 128 or 1152 each way), by a chain of three reads (slot or
+// position, row, store) at few: 2.2 us a call at 4 tokens into bf16, of which an
+// empty launch is 1.2, and 0.7 more into e4m3 for its divisions.
 // A warp holds a row or head as 16 latent columns a lane (8 lane + j and 256 +
 // 8 lane + j: each load is a warp-wide run of 512 bytes) and the position columns
 // 2 lane and 2 lane + 1.
@@ -113,10 +108,10 @@ __device__ __forceinline__ void load_weights8(const void* w, bool fp32, int c, f
     for (int j = 0; j < 8; ++j) y[j] = 1.f;
   } else if (fp32) {
     const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(w) + c);
-    const float4 a = __ldg(f), b = __ldg(f + 1);
+    const float4 a = f[0], b = f[1];
     y[0] = a.x, y[1] = a.y, y[2] = a.z, y[3] = a.w, y[4] = b.x, y[5] = b.y, y[6] = b.z, y[7] = b.w;
   } else {
-    unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + c)), y);
+    unpack_bf16x8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + c), y);
   }
 }
 __device__ __forceinline__ void load_weights_lat(const mla_norm& n, int part, int lane, Weights& w) {
@@ -129,10 +124,10 @@ __device__ __forceinline__ void load_weights_pe(const mla_norm& n, int part, int
   const void* p = n.weight[part];
   w.pe[0] = w.pe[1] = 1.f;
   if (p && n.weight_fp32) {
-    const float2 f = __ldg(static_cast<const float2*>(p) + lane);
+    const float2 f = static_cast<const float2*>(p)[lane];
     w.pe[0] = f.x, w.pe[1] = f.y;
   } else if (p) {
-    const uint32_t u = __ldg(static_cast<const uint32_t*>(p) + lane);
+    const uint32_t u = static_cast<const uint32_t*>(p)[lane];
     w.pe[0] = __uint_as_float(u << 16), w.pe[1] = __uint_as_float(u & 0xffff0000u);
   }
 }
@@ -267,9 +262,16 @@ __device__ __forceinline__ void store_row(const AppendParams& p, int32_t slot, c
 }
 
 // One warp per key row, or per kHeads query heads of a token, all of whose
-// columns are in flight before the first is used.
-// kQ: 0 no queries, 1 their position columns, 2 their latent columns too.
-constexpr int kAppendWarps = MLA_APPEND_WARPS;
+// columns are in flight before the first is used, in CTAs of kAppendWarps warps.
+// kQ: 0 no queries, 1 their position columns (kHeads 16: the angles once per
+// token; 4 heads a warp were no faster at any count, 2.8 against 2.7 us at 64
+// tokens and 7.8 against 5.5 at 4096), 2 their latent columns too (kHeads 2).
+// 8190 tokens into bf16 with every norm and whole queries (321 MB): 90.5 us with
+// a warp per head and the rotation table read from the constant bank, 54.5 with
+// 4 heads a warp and CTAs of 8 warps, 52.1 with 2 heads, 50.5 with CTAs of 4 warps
+// (2: 50.6, 1: 75.8), 50.0 with the keys' CTAs among the queries': 95% of the copy
+// rate.
+constexpr int kAppendWarps = 4;
 template <int kDtype, int kQ, int kHeads>
 __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const __grid_constant__ AppendParams p) {
   pdl_wait_primary();
@@ -344,19 +346,17 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const __g
 }
 
 // ---------------------------------------------------------------- gather
-// A thread takes 8 columns of a row (16 bytes out; 16, 8 or 4 bytes in), the
-// same columns of kGatherDeep rows: their slots are loaded together, then their
-// bytes, then everything is stored.
+// Bound by bytes: a row's own (1152, 576 or 306), its slot, 1152 out.  A thread
+// takes 8 columns of a row (16 bytes out; 16, 8 or 4 bytes in), the same columns
+// of kGatherDeep rows: their slots are loaded together, then their bytes, then
+// everything is stored.  247,792 MXFP4 rows (362 MB): 94 us with one row a
+// thread, 70 with two, 61.7 with four, 66.9 with eight; 58.3 with four when the
+// rows pass the caches as streamed data; 57.4 in CTAs of 2 x 72 threads instead of
+// 4 x 72 (1 x 72: 65.9, 8 x 72: 64.8).  That is 93% of the copy rate.
 constexpr int kPer = kRow / 8;                      // 72 threads a row
-#ifndef MLA_GATHER_ROWS
-#define MLA_GATHER_ROWS 2
-#endif
-constexpr int kGatherRows = MLA_GATHER_ROWS;        // rows of a CTA's pass
-constexpr int kGatherThreads = kPer * kGatherRows;  // 9 warps
-#ifndef MLA_GATHER_DEEP
-#define MLA_GATHER_DEEP 4
-#endif
-constexpr int kGatherDeep = MLA_GATHER_DEEP;
+constexpr int kGatherRows = 2;                      // rows of a CTA's pass
+constexpr int kGatherThreads = kPer * kGatherRows;
+constexpr int kGatherDeep = 4;
 
 template <int kDtype>
 __global__ void __launch_bounds__(kGatherThreads) mla_gather_kernel(const __grid_constant__ GatherParams p) {
@@ -483,9 +483,8 @@ cudaError_t launch_append_as(const AppendParams& p, cudaStream_t s) {
 template <int kDtype>
 cudaError_t launch_append_to(const AppendParams& p, cudaStream_t s) {
   if (!p.a.q_pe) return launch_append_as<kDtype, 0, 16>(p, s);
-  if (p.a.q_lat) return launch_append_as<kDtype, 2, MLA_HEADS_FULL>(p, s);
-  if (p.a.num_tokens >= MLA_APPEND_MANY) return launch_append_as<kDtype, 1, 16>(p, s);
-  return launch_append_as<kDtype, 1, 4>(p, s);
+  if (p.a.q_lat) return launch_append_as<kDtype, 2, 2>(p, s);
+  return launch_append_as<kDtype, 1, 16>(p, s);
 }
 }  // namespace
 
