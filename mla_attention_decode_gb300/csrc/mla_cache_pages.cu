@@ -76,41 +76,71 @@ __device__ __forceinline__ void store_unit(uint8_t* p, uint4 v, int unit) {
   }
 }
 
-// The first `rows` rows of page src to page dst in layer l, segment `seg`: those
-// of the rows first (`ks` of them for a whole page), then those of the scale rows.
+// A page's rows, then its scale rows, in segments of kSegUnits units.
 __host__ __device__ inline int kv_segs(const PageBytes& c) {
   return (int)(((int64_t)c.page_size * c.row_bytes / 16 + kSegUnits - 1) / kSegUnits);
 }
 __host__ __device__ inline int scale_segs(const PageBytes& c) {
   return c.scale ? (int)(((int64_t)c.page_size * c.scale_stride / c.scale_unit + kSegUnits - 1) / kSegUnits) : 0;
 }
-__device__ __forceinline__ void move_segment(const PageBytes& c, int src, int dst, int rows, int l, int seg, int ks,
-                                             int lane) {
-  const bool kv = seg < ks;
-  const int unit = kv ? 16 : c.scale_unit;
-  const int64_t row = kv ? c.row_bytes : c.scale_stride, page = c.page_size * row;
-  const int64_t at = (int64_t)(kv ? seg : seg - ks) * kSegUnits * unit, bytes = rows * row - at;
-  if (bytes <= 0) return;
-  const int units = (int)(min(bytes, (int64_t)kSegUnits * unit) / unit);
-  uint8_t* base = (kv ? c.kv + l * c.kv_layer : c.scale + l * c.scale_layer) + at + (int64_t)lane * unit;
-  uint8_t* d = base + dst * page;
-  const uint8_t* s = base + src * page;
-  uint4 v[kDeep];
-  if (unit == 16) {
+// task / d and its remainder, in 32 bits where the call's tasks fit.
+__device__ __forceinline__ int64_t split(int64_t task, int64_t d, bool narrow, int64_t& rest) {
+  const int64_t q = narrow ? (int64_t)((uint32_t)task / (uint32_t)d) : task / d;
+  rest = task - q * d;
+  return q;
+}
+
+// The first rows of part-filled pages: part(i) -> (source, destination, rows),
+// i < n, in every layer.  Forks of one sequence follow one another and copy the
+// same page: a warp takes up to kShare copies in a row, as far as there are
+// warps' worth of them, and reads a source once.  A fork of 64 sequences into 512
+// that copies 102 MB in 12 layers, with its free: 45.0 us with one copy a warp,
+// 38.5 with 2, 35.8 with 4 and 35.6 with 8; 33.1 with 4 and 3 CTAs an SM instead of
+// 2 (4 CTAs: 35.1).
+constexpr int kShare = 4;
+constexpr int kPartCtas = 3;  // CTAs an SM of the kernel that does this
+template <class Part>
+__device__ __forceinline__ void move_parts(const PageBytes& c, int n, int64_t at, int64_t step, Part part) {
+  const int lane = threadIdx.x & 31, ks = kv_segs(c), segs = ks + scale_segs(c);
+  const int64_t per = (int64_t)segs * c.num_layers, warps = step >> 5;
+  const int share = (int)max((int64_t)1, min((int64_t)kShare, per * n / warps));
+  const int64_t tasks = per * ((n + share - 1) / share);
+  const bool narrow = tasks <= UINT32_MAX;
+  for (int64_t task = at >> 5; task < tasks; task += warps) {
+    int64_t rest, seg;
+    const int i0 = (int)split(task, per, narrow, rest) * share, many = min(share, n - i0);
+    const int64_t l = split(rest, segs, true, seg);
+    const int3 mine = part(i0 + min(lane, many - 1));  // all the copies' pages in one round
+    const bool kv = seg < ks;
+    const int unit = kv ? 16 : c.scale_unit;
+    const int64_t row = kv ? c.row_bytes : c.scale_stride, page = c.page_size * row;
+    const int64_t off = (kv ? seg : seg - ks) * kSegUnits * unit;
+    uint8_t* base = (kv ? c.kv + l * c.kv_layer : c.scale + l * c.scale_layer) + off + (int64_t)lane * unit;
+    uint4 v[kDeep];
+    int src = -1, rows = -1, units = 0;
+    for (int i = 0; i < many; ++i) {
+      const int from = __shfl_sync(kFull, mine.x, i), to = __shfl_sync(kFull, mine.y, i);
+      const int used = __shfl_sync(kFull, mine.z, i);
+      if (from != src || used != rows) {
+        const int64_t bytes = used * row - off;
+        units = bytes <= 0 ? 0 : (int)(min(bytes, (int64_t)kSegUnits * unit) / unit);
+        const uint8_t* s = base + from * page;
 #pragma unroll
-    for (int i = 0; i < kDeep; ++i)
-      if (32 * i + lane < units) v[i] = reinterpret_cast<const uint4*>(s)[32 * i];
+        for (int k = 0; k < kDeep; ++k)
+          if (32 * k + lane < units)
+            v[k] = unit == 16 ? reinterpret_cast<const uint4*>(s)[32 * k] : load_unit(s + 32 * k * unit, unit);
+        src = from;
+        rows = used;
+      }
+      uint8_t* d = base + to * page;
 #pragma unroll
-    for (int i = 0; i < kDeep; ++i)
-      if (32 * i + lane < units) reinterpret_cast<uint4*>(d)[32 * i] = v[i];
-    return;
+      for (int k = 0; k < kDeep; ++k)
+        if (32 * k + lane < units) {
+          if (unit == 16) reinterpret_cast<uint4*>(d)[32 * k] = v[k];
+          else store_unit(d + 32 * k * unit, v[k], unit);
+        }
+    }
   }
-#pragma unroll
-  for (int i = 0; i < kDeep; ++i)
-    if (32 * i + lane < units) v[i] = load_unit(s + 32 * i * unit, unit);
-#pragma unroll
-  for (int i = 0; i < kDeep; ++i)
-    if (32 * i + lane < units) store_unit(d + 32 * i * unit, v[i], unit);
 }
 
 // Whole pages: page pair(i) -> (src, dst), i < n, in every layer (src < 0: none).
@@ -126,12 +156,6 @@ __device__ __forceinline__ void move_pages(const PageBytes& c, int64_t n, int64_
   const int64_t kvu = kv_page / 16, su = unit == 16 ? 0 : scale_page / unit;
   const int64_t units = kvu + (unit == 16 ? scale_page / 16 : 0);
   const int64_t warp = at >> 5, warps = step >> 5;
-  // the task's quotient by d: in 32 bits where the call's tasks fit
-  const auto split = [](int64_t task, int64_t d, bool narrow, int64_t& rest) {
-    const int64_t q = narrow ? (int64_t)((uint32_t)task / (uint32_t)d) : task / d;
-    rest = task - q * d;
-    return q;
-  };
   if (units <= kSegUnits) {
     int g = 4;  // lanes a page
     while (g * kDeep < units) g *= 2;
@@ -489,14 +513,9 @@ __device__ __forceinline__ void apply_entries(const TableParams& p, int64_t at, 
 }
 // ... and the rows of part-filled pages.
 __device__ __forceinline__ void apply_copies(const TableParams& p, int64_t at, int64_t step) {
-  const int lane = threadIdx.x & 31;
-  const int ks = kv_segs(p.c), segs = ks + scale_segs(p.c);
-  const int64_t per = (int64_t)segs * p.c.num_layers, tasks = per * p.ws.head[kHeadCopies];
-  for (int64_t task = at >> 5; task < tasks; task += step >> 5) {
-    const int64_t i = task / per;
-    const int rest = (int)(task - i * per), l = rest / segs, seg = rest - l * segs;
-    move_segment(p.c, p.ws.copy_src[i], p.ws.list[p.ws.copy_rank[i]], p.ws.copy_rows[i], l, seg, ks, lane);
-  }
+  move_parts(p.c, p.ws.head[kHeadCopies], at, step, [&](int i) {
+    return make_int3(p.ws.copy_src[i], p.ws.list[p.ws.copy_rank[i]], p.ws.copy_rows[i]);
+  });
 }
 
 // The first CTA goes over the sequences, all of them over the pages (where
@@ -567,13 +586,18 @@ __global__ void __launch_bounds__(kPlan, 1) mla_table_plan_kernel(const __grid_c
   cluster.sync();  // the first CTA's shared memory stays until the others have read it
 }
 
-__global__ void __launch_bounds__(256, kMoveCtas) mla_table_apply_kernel(const __grid_constant__ TableParams p) {
+__global__ void __launch_bounds__(256, kPartCtas) mla_table_apply_kernel(const __grid_constant__ TableParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
   if (!p.ws.head[kHeadOk]) return;
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
-  if (!p.entries_apart) apply_entries(p, at, step);
-  apply_copies(p, at, step);
+  // every fourth CTA (the grid is a multiple of 4) has entries, a chain of
+  // dependent reads each, while the others keep the rows moving
+  const int64_t quarter = blockIdx.x >> 2, entry_ctas = p.entries_apart ? 0 : gridDim.x >> 2;
+  if (entry_ctas > 0 && (blockIdx.x & 3) == 0)
+    apply_entries(p, quarter * 256 + threadIdx.x, entry_ctas * 256);
+  else
+    apply_copies(p, (blockIdx.x - (entry_ctas > 0 ? quarter + 1 : 0)) * 256 + threadIdx.x,
+                 (gridDim.x - entry_ctas) * 256);
 }
 // Long tables apart from the rows: moving rows takes 128 registers a thread, a
 // quarter of the threads that a chain of dependent reads per entry wants.
@@ -607,7 +631,7 @@ __global__ void __launch_bounds__(kPlan, 1) mla_table_local_kernel(const __grid_
   pdl_wait_primary();
   pdl_launch_dependents();
   const cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, lane = tid & 31, rank = (int)cluster.block_rank(), N = p.to.batch;
+  const int tid = threadIdx.x, rank = (int)cluster.block_rank(), N = p.to.batch;
   const int pages = p.c.num_pages;
   constexpr int kPasses = kLocalPages / (4 * kPlan);
   if (tid == 0) s.flags = 0;
@@ -689,12 +713,8 @@ __global__ void __launch_bounds__(kPlan, 1) mla_table_local_kernel(const __grid_
       const int n = owner(s.from_at, N, e);
       if (e - s.from_at[n] >= s.first[n]) release_page(p.refs, pages, p.from.kv_indices[e], p.ws.err);
     }
-  const int ks = kv_segs(p.c), segs = ks + scale_segs(p.c);
-  const int64_t per = (int64_t)segs * p.c.num_layers, tasks = per * copies;
-  for (int64_t task = at >> 5; task < tasks; task += step >> 5) {
-    const int i = (int)(task / per), rest = (int)(task - i * per), l = rest / segs, seg = rest - l * segs;
-    move_segment(p.c, s.copy_src[i], s.list[s.copy_rank[i]], s.copy_rows[i], l, seg, ks, lane);
-  }
+  move_parts(p.c, copies, at, step,
+             [&](int i) { return make_int3(s.copy_src[i], s.list[s.copy_rank[i]], s.copy_rows[i]); });
 }
 
 // ---------------------------------------------------------------- free
@@ -961,9 +981,11 @@ cudaError_t launch_table(const TableParams& p, cudaStream_t s) {
   if (q.entries_apart) {
     e = launch_chained(mla_table_entries_kernel, grid_for(entries), 256, s, q);
     if (e != cudaSuccess || threads == 0) return e;
-    entries = 0;
+    return launch_chained(mla_table_apply_kernel, grid_for(threads), 256, s, q);
   }
-  return launch_chained(mla_table_apply_kernel, grid_for(threads < entries ? entries : threads), 256, s, q);
+  const unsigned by_rows = (grid_for(threads) + 2) / 3, by_entries = grid_for(entries);
+  const unsigned quarter = by_rows > by_entries ? by_rows : by_entries;
+  return launch_chained(mla_table_apply_kernel, 4 * (quarter < kMaxGrid / 4 ? quarter : kMaxGrid / 4), 256, s, q);
 }
 
 cudaError_t launch_free(int32_t* refs, int32_t num_pages, const int32_t* pages, int32_t n, int32_t* error,

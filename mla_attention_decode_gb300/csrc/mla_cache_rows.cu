@@ -158,8 +158,8 @@ struct Turn {
 // Lane i finds pair i's angle; paired halves (i, i + 32) then fetch the two pairs
 // that their columns belong to.
 __device__ __forceinline__ Turn turn_of(const AppendParams& p, int t, int lane) {
-  Turn r;
-  if (p.rope.num_axes == 0) return r;  // no rotation: not used
+  Turn r = {{1.f, 1.f}, {0.f, 0.f}};
+  if (p.rope.num_axes == 0) return r;
   // through the parameter's address, not the constant bank: each lane reads an
   // entry of its own, which the constant cache would serve one lane at a time
   uint64_t step;
