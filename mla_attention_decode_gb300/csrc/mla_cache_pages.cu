@@ -125,20 +125,28 @@ __device__ __forceinline__ void move_parts(const PageBytes& c, int n, int64_t at
         const int64_t bytes = used * row - off;
         units = bytes <= 0 ? 0 : (int)(min(bytes, (int64_t)kSegUnits * unit) / unit);
         const uint8_t* s = base + from * page;
+        if (unit == 16) {
 #pragma unroll
-        for (int k = 0; k < kDeep; ++k)
-          if (32 * k + lane < units)
-            v[k] = unit == 16 ? reinterpret_cast<const uint4*>(s)[32 * k] : load_unit(s + 32 * k * unit, unit);
+          for (int k = 0; k < kDeep; ++k)
+            if (32 * k + lane < units) v[k] = reinterpret_cast<const uint4*>(s)[32 * k];
+        } else {
+#pragma unroll
+          for (int k = 0; k < kDeep; ++k)
+            if (32 * k + lane < units) v[k] = load_unit(s + 32 * k * unit, unit);
+        }
         src = from;
         rows = used;
       }
       uint8_t* d = base + to * page;
+      if (unit == 16) {
 #pragma unroll
-      for (int k = 0; k < kDeep; ++k)
-        if (32 * k + lane < units) {
-          if (unit == 16) reinterpret_cast<uint4*>(d)[32 * k] = v[k];
-          else store_unit(d + 32 * k * unit, v[k], unit);
-        }
+        for (int k = 0; k < kDeep; ++k)
+          if (32 * k + lane < units) reinterpret_cast<uint4*>(d)[32 * k] = v[k];
+      } else {
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k)
+          if (32 * k + lane < units) store_unit(d + 32 * k * unit, v[k], unit);
+      }
     }
   }
 }
