@@ -82,7 +82,8 @@ enum { MLA_PART_KV_LAT = 0, MLA_PART_KV_PE = 1, MLA_PART_Q_LAT = 2, MLA_PART_Q_P
 
 /*
  * Root-mean-square norms, y = x / sqrt(mean(x^2) + eps) * weight, of the parts
- * in `apply`; queries are normed head by head.
+ * in `apply`; queries are normed head by head.  The squares are summed in fp32
+ * (columns above about 1e18 overflow the sum).
  */
 typedef struct {
   const void* weight[4]; /* device, per part: bf16 or fp32 [512] / [64], 16-byte aligned; NULL: 1 */
@@ -117,7 +118,7 @@ typedef struct {
  *
  * Everything is computed in fp32 (angles exactly, modulo one turn, at any int32
  * position) and rounded once: queries and bf16 rows to bf16; fp8 rows to
- * e4m3(y / kv_scale), saturating at 448 (NaN stays NaN); mxfp4 rows to e2m1
+ * e4m3(y / kv_scale) (the quotient rounded to fp32 first), saturating at 448 (NaN stays NaN); mxfp4 rows to e2m1
  * under the smallest power of two 2^e with max|y| <= 6 * 2^e per block of 32
  * (scale byte e + 127; 127 for a block of zeros; a block with an infinity or a
  * NaN gets scale byte 255 = NaN and codes 0).
@@ -134,7 +135,7 @@ MLA_API int mla_cache_append(const mla_cache* cache, const mla_rope* rope, const
 
 /*
  * mla_cache_gather -- rows of one layer as bf16: out[t, :] = bf16(the value of
- * row slots[t]).  out: device bf16 [num_rows, 576], rows out_stride elements
+ * row slots[t]; fp8: the code times kv_scale in fp32).  out: device bf16 [num_rows, 576], rows out_stride elements
  * apart (a multiple of 8, >= 576), 16-byte aligned.  Rows of out with slot -1
  * are left as they were; so are those with a slot outside the cache, which
  * set MLA_ERR_DEVICE_INDEX.  Slots may repeat.

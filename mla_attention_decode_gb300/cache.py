@@ -181,7 +181,8 @@ class MLACachePool:
 
     Calls that share a pool are ordered on the GPU (one stream, or events).
     Methods enqueue on ``stream`` (default: torch's current one) of the pool's
-    device; ``poll_error`` synchronises."""
+    device; ``poll_error`` synchronises.  As with any kernel, memory that a call
+    on another stream uses is the caller's to keep (``Tensor.record_stream``)."""
 
     def __init__(self, kv, kv_dtype, page_size: int, kv_scale=None, refs=None, max_batch: int = 4096):
         self.kv_dtype = binding._dtype_code(kv_dtype)
@@ -306,14 +307,15 @@ class MLACachePool:
         return out
 
     def free(self, pages, stream=None):
-        """Ends one hold on each of ``pages`` (-1 entries are skipped)."""
+        """Ends one hold on each of ``pages``, e.g. the entries of a table that are in use (-1 is skipped)."""
         rc = _ext.free(self._core, self.refs, pages, stream)
         if rc:
             raise MLAError(rc, "mla_cache_free")
 
     def compact(self, kv_indices, out=None, stream=None):
-        """Moves the pages in use to the front.  ``out``: (kv_indices, refs, live [1]) to write; without it the
-        pool's counts are rewritten in place and the other two are new.  Returns the three."""
+        """Moves the pages in use to the front and renumbers ``kv_indices`` (the entries of a table that are in use).
+        ``out``: (kv_indices, refs, live [1]) to write; without it the pool's counts are rewritten in place and the
+        other two are new.  Returns the three."""
         indices, refs, live = (None, None, None) if out is None else out
         rc, indices, refs, live = _ext.compact(self._core, self.refs, kv_indices, indices, refs, live, stream)
         if rc:

@@ -464,10 +464,10 @@ def test_a_run_with_the_decode(orc, kv_dtype, page):  # noqa: F811
     pool.append(new.to(DEV)[:, :512], new.to(DEV)[:, 512:], slots)
     seqs = [torch.cat([s, x]) for s, x in zip(seqs, new.split(extra))]
     out, lse, q = check(forks, seqs, "continued forks")
-    idx, refs, live = pool.compact(forks[1])
-    held = int(forks[0][-1])
-    assert pool.poll_error() in (0, binding.MLA_ERR_DEVICE_INDEX)  # entries past the table name free pages
-    assert int(idx[:held].max()) < int(live) and int((refs > 0).sum()) == int(live)
+    held = sum(-(-n // page) for n in lens)
+    idx, refs, live = pool.compact(forks[1][:held])
+    assert pool.poll_error() == 0 and int(forks[0][-1]) == held
+    assert int(idx.max()) < int(live) and int((refs > 0).sum()) == int(live)
     out2, lse2 = decode((forks[0], idx, forks[2]), lens, q)
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
     # and every sequence reads back as it was stored
@@ -478,8 +478,8 @@ def test_a_run_with_the_decode(orc, kv_dtype, page):  # noqa: F811
 
 
 def test_a_captured_decode_step():
-    """Table growth, slots, append and decode captured once and replayed: each
-    replay appends another row (the table is grown by the replay itself)."""
+    """Table growth, slots and append captured once and replayed: each replay
+    appends another row (the table is grown by the replay itself)."""
     page, lens = 16, [15, 40]
     pool = cache.MLACachePool.allocate("bf16", 40, page, device=DEV)
     table = pool.resize(pool.table(2, 0), i32(lens), pool.table(2, 12))

@@ -415,6 +415,44 @@ def test_rows_past_32_bit_offsets():
     assert pool.poll_error() == 0
 
 
+def test_layers_with_scales_and_strides_of_their_own():
+    """An e4m3 cache whose layers have a scale each and lie apart in a wider tensor."""
+    g = gen(12)
+    big = torch.zeros(3, 50, 576, dtype=torch.float8_e4m3fn, device=DEV)
+    scale = torch.tensor([0.5, 0.01, 2.0], device=DEV)
+    pool = cache.MLACachePool(big[:, :48], "fp8", 16, kv_scale=scale)
+    x = torch.randn(20, 576, generator=g).to(torch.bfloat16)
+    slots = torch.randperm(48, generator=g)[:20].to(torch.int32)
+    for layer in (2, 0, 1):
+        pool.append(x.to(DEV)[:, :512], x.to(DEV)[:, 512:], slots.to(DEV), layer=layer)
+    assert pool.poll_error() == 0
+    raw = big.view(torch.uint8).cpu()
+    for layer in range(3):
+        want = (x.float() / scale[layer].cpu()).clamp(-448, 448).to(torch.float8_e4m3fn)
+        assert torch.equal(raw[layer, slots.long()], want.view(torch.uint8))
+        got = pool.gather(slots.to(DEV), layer=layer).cpu()
+        assert torch.equal(got, (want.float() * scale[layer].cpu()).to(torch.bfloat16))
+    assert torch.all(raw[:, 48:] == 0), "rows of no layer"
+
+
+@pytest.mark.parametrize("how", ["stream", "handle"])
+def test_memory_made_on_the_calls_stream(how):
+    """Without out= the result belongs to the stream that the call names, as a torch stream or a handle."""
+    pool = new_pool("bf16", 64, 16)
+    table = (torch.tensor([0, 1], dtype=torch.int32, device=DEV), torch.tensor([2], dtype=torch.int32, device=DEV),
+             torch.tensor([9], dtype=torch.int32, device=DEV))
+    qo = torch.tensor([0, 9], dtype=torch.int32, device=DEV)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    named = s if how == "stream" else s.cuda_stream
+    slots, _ = pool.slots(table, qo, 9, stream=named)
+    rows = pool.gather(slots, stream=named)
+    indices, refs, live = pool.compact(table[1], stream=named)
+    s.synchronize()
+    assert slots.tolist() == list(range(32, 41)) and torch.equal(rows, pool.kv[0, 32:41])
+    assert int(live) == 0 and pool.poll_error(named) == binding.MLA_ERR_DEVICE_INDEX  # page 2 is free
+
+
 def test_another_stream_and_a_graph():
     """The calls on a stream of their own, then captured and replayed with new inputs."""
     g = gen(4)
@@ -467,6 +505,18 @@ def test_python_refusals():
                              (torch.zeros(4, 288, dtype=torch.uint8, device=DEV), "mxfp4", 1, torch.zeros(4, 17, dtype=torch.uint8, device=DEV))):
         with pytest.raises(ValueError):
             cache.MLACachePool(kv, dt, page, kv_scale=sc)
+    for call in (lambda: pool.gather([0, 1]), lambda: pool.gather(slots, out=x.float()),
+                 lambda: pool.gather(slots, out=x[:3]), lambda: pool.slots((slots, slots), slots, 1),
+                 lambda: pool.slots((slots[:1], slots, slots[:1]), slots[:1], 1), lambda: pool.free(slots.view(2, 2)),
+                 lambda: pool.slots((slots[:2], slots, slots[:1]), slots[:2], -1),
+                 lambda: pool.copy_pages(slots, slots[:2]), lambda: pool.free(slots[::2]),
+                 lambda: pool.fork(pool.table(1, 4), slots, pool.table(2, 4)),
+                 lambda: pool.resize(pool.table(1, 4), None, pool.table(1, 4)),
+                 lambda: pool.compact(slots, out=(slots, pool.refs[:2], slots[:1]))):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(binding.MLAError):  # rows that overlap
+        pool.gather(slots, out=x[:1].expand(4, 576))
     with pytest.raises(ValueError):
         cache.MLANorm(kv_lat=torch.ones(64, device=DEV))
     with pytest.raises(ValueError):
