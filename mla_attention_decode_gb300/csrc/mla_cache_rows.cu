@@ -1,5 +1,7 @@
 // mla_cache_rows.cu -- rows of the latent cache written, read back and found
 // (include/mla_cache.h): mla_cache_append, mla_cache_gather, mla_cache_slots.
+#include <type_traits>
+
 #include <cuda_runtime.h>
 
 #include "mla_cache_internal.h"
@@ -18,6 +20,33 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   return v;
+}
+
+// Two fp32 operations an instruction, each rounded as the single one is.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+      "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+// The larger of two values, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
 }
 
 __device__ __forceinline__ void unpack_bf16x8(uint4 r, float (&x)[8]) {
@@ -47,6 +76,14 @@ __device__ __forceinline__ uint32_t pack_e2m1x8(const float (&x)[8]) {
       : "=r"(r)
       : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return r;
+}
+
+__device__ __forceinline__ uint8_t pack_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tmov.b32 %0, {a, a, a, a};\n\t}"
+      : "=r"(r)
+      : "f"(lo), "f"(hi));
+  return (uint8_t)r;
 }
 
 // Four packed bytes (eight e2m1 codes) -> eight floats, exactly.
@@ -88,14 +125,14 @@ __device__ __forceinline__ uint32_t e8m0_of(float amax, float& inv) {
   return (uint32_t)(e + 127);
 }
 
-// |x| as an ordering key in which NaN is largest (a plain fmaxf drops it).
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
 // ---------------------------------------------------------------- append
 // Bound by bytes at many tokens (a key row's 1152 in and 1152, 576 or 306 out, a
 // query head's 128 or 1152 each way), by a chain of three reads (slot or
-// position, row, store) at few: 2.2 us a call at 4 tokens into bf16, of which an
-// empty launch is 1.2, and 0.7 more into e4m3 for its divisions.
+// position, row, store) at few: 2.1 us a call at 4 tokens into bf16, 2.4 into e4m3
+// or MXFP4, of which an empty launch is 1.2.  7147 tokens with their queries'
+// position columns (40 to 46 MB): 9.4, 9.0 and 8.8 us; the arithmetic is paired
+// (two fp32 operations an instruction) since instructions were 60% of the issue
+// slots there: 10.0, 10.4 and 9.8 us before.
 // A warp holds a row or head as 16 latent columns a lane (8 lane + j and 256 +
 // 8 lane + j: each load is a warp-wide run of 512 bytes) and the position columns
 // 2 lane and 2 lane + 1.
@@ -135,16 +172,23 @@ __device__ __forceinline__ void load_weights_pe(const mla_norm& n, int part, int
 // y = x / sqrt(mean(x^2) + eps) * w over the 512 latent columns.
 __device__ __forceinline__ void norm_lat(const mla_norm& n, int part, const Weights& w, float (&x)[2][8]) {
   if (!(n.apply >> part & 1)) return;
-  float ss = 0.f;
+  float2 ss = both(0.f);
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(x[h][j], x[h][j], ss);
-  const float r = rsqrtf(warp_sum(ss) * (1.f / kLat) + n.eps);
+    for (int j = 0; j < 8; j += 2) {
+      const float2 v = make_float2(x[h][j], x[h][j + 1]);
+      ss = fma2(v, v, ss);
+    }
+  const float r = rsqrtf(warp_sum(ss.x + ss.y) * (1.f / kLat) + n.eps);
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[h][j] = x[h][j] * r * w.lat[h][j];
+    for (int j = 0; j < 8; j += 2) {
+      const float2 v = mul2(mul2(make_float2(x[h][j], x[h][j + 1]), both(r)), make_float2(w.lat[h][j], w.lat[h][j + 1]));
+      x[h][j] = v.x;
+      x[h][j + 1] = v.y;
+    }
 }
 
 // The rotation as this lane applies it: column 2 lane + k becomes
@@ -188,23 +232,40 @@ __device__ __forceinline__ Turn turn_of(const AppendParams& p, int t, int lane) 
   return r;
 }
 
+// How the position columns turn: not at all (nothing is multiplied: an infinity
+// would make its partner NaN), by pairs (2i, 2i + 1), by pairs (i, i + 32).
+enum { kStill = 0, kPairs2 = 1, kHalves = 2 };
+__device__ __forceinline__ int turn_kind(const AppendParams& p) {
+  return p.rope.num_axes == 0 ? kStill : (p.rope.interleaved ? kPairs2 : kHalves);
+}
 // The lane's two position columns (`u`: their bf16 pair) normed and rotated.
-__device__ __forceinline__ float2 turned_pe(const AppendParams& p, int part, const Weights& w, const Turn& r,
-                                            uint32_t u, int lane) {
-  float x0 = __uint_as_float(u << 16), x1 = __uint_as_float(u & 0xffff0000u);
-  if (p.norm.apply >> part & 1) {
-    const float q = rsqrtf(warp_sum(fmaf(x0, x0, x1 * x1)) * (1.f / kPe) + p.norm.eps);
-    x0 = x0 * q * w.pe[0];
-    x1 = x1 * q * w.pe[1];
+template <int kNorm, int kTurn>
+__device__ __forceinline__ float2 turned_pe(float eps, const Weights& w, const Turn& r, uint32_t u) {
+  float2 x = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  if (kNorm) {
+    const float q = rsqrtf(warp_sum(fmaf(x.x, x.x, x.y * x.y)) * (1.f / kPe) + eps);
+    x = mul2(mul2(x, both(q)), make_float2(w.pe[0], w.pe[1]));
   }
-  // without a rotation nothing is multiplied: an infinity would make its partner NaN
-  if (p.rope.num_axes == 0) return make_float2(x0, x1);
-  float y0 = x1, y1 = x0;  // the partners of columns 2 lane, 2 lane + 1
-  if (!p.rope.interleaved) {
-    y0 = __shfl_xor_sync(kFull, x0, 16);
-    y1 = __shfl_xor_sync(kFull, x1, 16);
+  if (kTurn == kStill) return x;
+  float2 y = make_float2(x.y, x.x);  // the partners of columns 2 lane, 2 lane + 1
+  if (kTurn == kHalves) y = make_float2(__shfl_xor_sync(kFull, x.x, 16), __shfl_xor_sync(kFull, x.y, 16));
+  return fma2(x, make_float2(r.c[0], r.c[1]), mul2(y, make_float2(r.s[0], r.s[1])));
+}
+// f with the call's norm and turn as constants, so that a loop over heads has no
+// branch in it.
+template <int k>
+using Const = std::integral_constant<int, k>;
+template <class F>
+__device__ __forceinline__ void by_kind(bool norm, int turn, F f) {
+  if (norm) {
+    if (turn == kPairs2) f(Const<1>(), Const<kPairs2>());
+    else if (turn == kHalves) f(Const<1>(), Const<kHalves>());
+    else f(Const<1>(), Const<kStill>());
+  } else {
+    if (turn == kPairs2) f(Const<0>(), Const<kPairs2>());
+    else if (turn == kHalves) f(Const<0>(), Const<kHalves>());
+    else f(Const<0>(), Const<kStill>());
   }
-  return make_float2(fmaf(x0, r.c[0], y0 * r.s[0]), fmaf(x1, r.c[1], y1 * r.s[1]));
 }
 
 // One key row into row `slot` of the cache, in its format.
@@ -217,46 +278,68 @@ __device__ __forceinline__ void store_row(const AppendParams& p, int32_t slot, c
     for (int h = 0; h < 2; ++h) reinterpret_cast<uint4*>(dst)[32 * h + lane] = pack_bf16x8(lat[h]);
     reinterpret_cast<uint32_t*>(dst + 2 * kLat)[lane] = pack_bf16x2(pe.x, pe.y);
   } else if (kDtype == MLA_KV_FP8_E4M3) {
-    // the quotient is the rounded one (not a product with the reciprocal): the
-    // stored code is e4m3(y / scale) at every border
-    const float sc = *static_cast<const float*>(p.cache.scale);
+    // e4m3 of the rounded quotient y / scale (not of a product with the reciprocal,
+    // which lands on the other side of some borders).  Markstein's correction
+    // (P. W. Markstein, IBM J. Res. Dev. 34, 1990): with r the rounded reciprocal of
+    // b and q = a r, the residual a - q b is exact in one fma, and q plus residual
+    // times r is a / b correctly rounded, while nothing over- or underflows: a scale
+    // within 2^+-60 and quotients below 1024 (past 448 all saturate); what is
+    // smaller than 2^-10 becomes 0 either way.  Else the division itself.  (Dividing
+    // each of a lane's 18 columns took 200 of 493 instructions a row.)
+    const float sc = *static_cast<const float*>(p.cache.scale), r = __frcp_rn(sc);
+    float2 q[9], top = both(0.f);
+#pragma unroll
+    for (int i = 0; i < 9; ++i) {
+      const float2 y = i < 8 ? make_float2(lat[i >> 2][2 * (i & 3)], lat[i >> 2][2 * (i & 3) + 1]) : pe;
+      const float2 q0 = mul2(y, both(r));
+      top = make_float2(max_nan(top.x, fabsf(q0.x)), max_nan(top.y, fabsf(q0.y)));
+      q[i] = fma2(fma2(q0, both(-sc), y), both(r), q0);
+    }
+    const bool plain = max_nan(top.x, top.y) < 1024.f && sc > 0x1p-60f && sc < 0x1p60f;
+    if (!plain) {
+#pragma unroll
+      for (int i = 0; i < 9; ++i) {
+        const float2 y = i < 8 ? make_float2(lat[i >> 2][2 * (i & 3)], lat[i >> 2][2 * (i & 3) + 1]) : pe;
+        q[i] = make_float2(__fdiv_rn(y.x, sc), __fdiv_rn(y.y, sc));
+      }
+    }
     uint8_t* dst = p.cache.kv + (int64_t)slot * kRow;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t w[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = f32x2_to_e4m3x2(__fdiv_rn(lat[h][2 * j], sc), __fdiv_rn(lat[h][2 * j + 1], sc));
+      for (int j = 0; j < 4; ++j) w[j] = f32x2_to_e4m3x2(q[4 * h + j].x, q[4 * h + j].y);
       reinterpret_cast<uint2*>(dst)[32 * h + lane] = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
     }
-    reinterpret_cast<uint16_t*>(dst + kLat)[lane] =
-        (uint16_t)f32x2_to_e4m3x2(__fdiv_rn(pe.x, sc), __fdiv_rn(pe.y, sc));
+    reinterpret_cast<uint16_t*>(dst + kLat)[lane] = (uint16_t)f32x2_to_e4m3x2(q[8].x, q[8].y);
   } else {
     uint8_t* dst = p.cache.kv + (int64_t)slot * (kRow / 2);
     uint8_t* sdst = static_cast<uint8_t*>(p.cache.scale) + (int64_t)slot * p.cache.scale_stride;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {  // a block of 32 columns: four lanes
-      uint32_t m = 0;
+      float m = fabsf(lat[h][0]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, abs_bits(lat[h][j]));
-      m = max(m, __shfl_xor_sync(kFull, m, 1));
-      m = max(m, __shfl_xor_sync(kFull, m, 2));
+      for (int j = 1; j < 8; ++j) m = max_nan(m, fabsf(lat[h][j]));
+      m = max_nan(m, __shfl_xor_sync(kFull, m, 1));
+      m = max_nan(m, __shfl_xor_sync(kFull, m, 2));
       float inv, y[8];
-      const uint32_t byte = e8m0_of(__uint_as_float(m), inv);
+      const uint32_t byte = e8m0_of(m, inv);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = byte == 255 ? 0.f : lat[h][j] * inv;
-      reinterpret_cast<uint32_t*>(dst)[32 * h + lane] = pack_e2m1x8(y);
+      for (int j = 0; j < 8; j += 2) {
+        const float2 v = mul2(make_float2(lat[h][j], lat[h][j + 1]), both(inv));
+        y[j] = v.x;
+        y[j + 1] = v.y;
+      }
+      reinterpret_cast<uint32_t*>(dst)[32 * h + lane] = byte == 255 ? 0u : pack_e2m1x8(y);
       if ((lane & 3) == 0) sdst[8 * h + (lane >> 2)] = (uint8_t)byte;
     }
     // the position columns: two blocks of sixteen lanes
-    uint32_t m = max(abs_bits(pe.x), abs_bits(pe.y));
+    float m = max_nan(fabsf(pe.x), fabsf(pe.y));
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+    for (int o = 1; o < 16; o <<= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, o));
     float inv;
-    const uint32_t byte = e8m0_of(__uint_as_float(m), inv);
-    const float z0 = byte == 255 ? 0.f : pe.x * inv, z1 = byte == 255 ? 0.f : pe.y * inv;
-    const float y[8] = {z0, z1, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    dst[kLat / 2 + lane] = (uint8_t)pack_e2m1x8(y);
+    const uint32_t byte = e8m0_of(m, inv);
+    dst[kLat / 2 + lane] = byte == 255 ? 0 : pack_e2m1x2(pe.x * inv, pe.y * inv);
     if ((lane & 15) == 0) sdst[16 + (lane >> 4)] = (uint8_t)byte;
   }
 }
@@ -269,7 +352,7 @@ __device__ __forceinline__ void store_row(const AppendParams& p, int32_t slot, c
 // 8190 tokens into bf16 with every norm and whole queries (321 MB): 90.5 us with
 // a warp per head and the rotation table read from the constant bank, 54.5 with
 // 4 heads a warp and CTAs of 8 warps, 52.1 with 2 heads, 50.5 with CTAs of 4 warps
-// (2: 50.6, 1: 75.8), 50.0 with the keys' CTAs among the queries': 95% of the copy
+// (2: 50.6, 1: 75.8), 49.7 with the keys' CTAs among the queries': 95% of the copy
 // rate.
 constexpr int kAppendWarps = 4;
 template <int kDtype, int kQ, int kHeads>
@@ -303,7 +386,10 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const __g
     unpack_bf16x8(a, x[0]);
     unpack_bf16x8(b, x[1]);
     norm_lat(p.norm, MLA_PART_KV_LAT, w, x);
-    store_row<kDtype>(p, slot, x, turned_pe(p, MLA_PART_KV_PE, w, r, u, lane), lane);
+    float2 y;
+    by_kind(p.norm.apply >> MLA_PART_KV_PE & 1, turn_kind(p),
+            [&](auto norm, auto turn) { y = turned_pe<norm.value, turn.value>(p.norm.eps, w, r, u); });
+    store_row<kDtype>(p, slot, x, y, lane);
     return;
   }
   if (kQ == 0) return;
@@ -329,18 +415,23 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const __g
   }
   load_weights_pe(p.norm, MLA_PART_Q_PE, lane, w);
   const Turn r = turn_of(p, t, lane);
+  by_kind(p.norm.apply >> MLA_PART_Q_PE & 1, turn_kind(p), [&](auto norm, auto turn) {
 #pragma unroll
-  for (int h = 0; h < kHeads; ++h) {
-    const float2 y = turned_pe(p, MLA_PART_Q_PE, w, r, u[h], lane);
-    uint8_t* row = out + h * (2 * kRow);
-    reinterpret_cast<uint32_t*>(row + 2 * kLat)[lane] = pack_bf16x2(y.x, y.y);
-    if (kQ == 2) {
+    for (int h = 0; h < kHeads; ++h) {
+      const float2 y = turned_pe<norm.value, turn.value>(p.norm.eps, w, r, u[h]);
+      reinterpret_cast<uint32_t*>(out + h * (2 * kRow) + 2 * kLat)[lane] = pack_bf16x2(y.x, y.y);
+    }
+  });
+  if (kQ == 2) {
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
       float x[2][8];
       unpack_bf16x8(v[h][0], x[0]);
       unpack_bf16x8(v[h][1], x[1]);
       norm_lat(p.norm, MLA_PART_Q_LAT, w, x);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) reinterpret_cast<uint4*>(row)[32 * i + lane] = pack_bf16x8(x[i]);
+      for (int i = 0; i < 2; ++i)
+        reinterpret_cast<uint4*>(out + h * (2 * kRow))[32 * i + lane] = pack_bf16x8(x[i]);
     }
   }
 }

@@ -244,6 +244,24 @@ def test_append_stores_as_the_quantisers_do(kv_dtype):
         assert torch.equal(pool.kv_scale.cpu()[0], bytes_)
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.011, 1 / 3, 0.99999994, 1.0000001, 5.7e-3, 448.0, 3.1e-7, 2.0 ** -61, 2.0 ** -59,
+                                   2.0 ** 59 * 1.1, 2.0 ** 61, 7e20, 1e-30, 3e38, 1.2e-38])
+def test_e4m3_of_every_bf16_value(scale):
+    """Every bf16 value (infinities, NaN and subnormals among them) is stored as
+    e4m3 of the correctly rounded quotient, whatever the scale."""
+    bits = torch.arange(65536, dtype=torch.int32)
+    x = torch.cat([bits, torch.zeros(114 * 576 - 65536, dtype=torch.int32)]).to(torch.int16).view(torch.bfloat16).view(114, 576)
+    s = torch.tensor([scale], dtype=torch.float32)
+    pool = new_pool("fp8", 114, scale=scale)
+    assert torch.equal(pool.kv_scale.cpu(), s)
+    pool.append(x.to(DEV)[:, :512], x.to(DEV)[:, 512:], torch.arange(114, dtype=torch.int32, device=DEV))
+    want = (x.float() / s).clamp(-448, 448).to(torch.float8_e4m3fn)
+    got = pool.kv.cpu()[0].view(torch.float8_e4m3fn)
+    nan = torch.isnan(want.float())
+    assert torch.equal(torch.isnan(got.float()), nan)
+    assert torch.equal(got.view(torch.uint8)[~nan], want.view(torch.uint8)[~nan])
+
+
 @pytest.mark.parametrize("kv_dtype", ["bf16", "fp8", "mxfp4"])
 def test_append_infinities_and_nan(kv_dtype):
     """bf16 keeps them; e4m3 saturates infinities and keeps NaN; an MXFP4 block
