@@ -31,10 +31,10 @@ constexpr unsigned kMaxGrid = 152 * 8;   // CTAs of 256 threads that carry out a
 // many table entries (8192 entries: 6.0 us against 8.3 in two launches) ...
 constexpr int64_t kClusterEntries = 32768;
 // ... and bytes of pages that may have to be copied: a fork of n bf16 sequences
-// of 64-row pages, with its free, takes 8.5 us against 9.9 at n = 16 (1.2 MB),
-// 10.3 against 9.6 at n = 32 and 32 against 12 at n = 256.  A resize copies a page
+// of 64-row pages, with its free, takes 7.4 us against 8.8 at n = 8 (0.6 MB),
+// 9.5 against 9.2 at n = 16 and 32 against 12 at n = 256.  A resize copies a page
 // only where a fork's sequence is cut inside a shared one, so it may risk more.
-constexpr int64_t kClusterForkBytes = 2 << 20, kClusterResizeBytes = 16 << 20;
+constexpr int64_t kClusterForkBytes = 1 << 20, kClusterResizeBytes = 16 << 20;
 // Table entries by a kernel of their own: 65,536 entries 11.1 us against 10.4 in
 // one with the rows, 262,144 entries 11.5 against 15.2.
 constexpr int64_t kApartEntries = 131072;
