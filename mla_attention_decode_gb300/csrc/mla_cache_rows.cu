@@ -128,11 +128,11 @@ __device__ __forceinline__ uint32_t e8m0_of(float amax, float& inv) {
 // ---------------------------------------------------------------- append
 // Bound by bytes at many tokens (a key row's 1152 in and 1152, 576 or 306 out, a
 // query head's 128 or 1152 each way), by a chain of three reads (slot or
-// position, row, store) at few: 2.1 us a call at 4 tokens into bf16, 2.4 into e4m3
-// or MXFP4, of which an empty launch is 1.2.  7147 tokens with their queries'
-// position columns (40 to 46 MB): 9.4, 9.0 and 8.8 us; the arithmetic is paired
-// (two fp32 operations an instruction) since instructions were 60% of the issue
-// slots there: 10.0, 10.4 and 9.8 us before.
+// position, row, store) at few: 2.1 us a call at 4 tokens into bf16 or e4m3, 2.3 into
+// MXFP4, of which an empty launch is 1.2.  7147 tokens with their queries'
+// position columns (40 to 46 MB): 9.4, 8.9 and 8.9 us into bf16, e4m3 and MXFP4;
+// the arithmetic is paired (two fp32 operations an instruction) since
+// instructions were 60% of the issue slots there: 10.0, 10.4 and 9.8 us before.
 // A warp holds a row or head as 16 latent columns a lane (8 lane + j and 256 +
 // 8 lane + j: each load is a warp-wide run of 512 bytes) and the position columns
 // 2 lane and 2 lane + 1.
@@ -268,10 +268,11 @@ __device__ __forceinline__ void by_kind(bool norm, int turn, F f) {
   }
 }
 
-// One key row into row `slot` of the cache, in its format.
+// One key row into row `slot` of the cache, in its format (sc: the scale of an
+// e4m3 cache).
 template <int kDtype>
-__device__ __forceinline__ void store_row(const AppendParams& p, int32_t slot, const float (&lat)[2][8], float2 pe,
-                                          int lane) {
+__device__ __forceinline__ void store_row(const AppendParams& p, int32_t slot, float sc, const float (&lat)[2][8],
+                                          float2 pe, int lane) {
   if (kDtype == MLA_KV_BF16) {
     uint8_t* dst = p.cache.kv + (int64_t)slot * (2 * kRow);
 #pragma unroll
@@ -286,7 +287,7 @@ __device__ __forceinline__ void store_row(const AppendParams& p, int32_t slot, c
     // within 2^+-60 and quotients below 1024 (past 448 all saturate); what is
     // smaller than 2^-10 becomes 0 either way.  Else the division itself.  (Dividing
     // each of a lane's 18 columns took 200 of 493 instructions a row.)
-    const float sc = *static_cast<const float*>(p.cache.scale), r = __frcp_rn(sc);
+    const float r = __frcp_rn(sc);
     float2 q[9], top = both(0.f);
 #pragma unroll
     for (int i = 0; i < 9; ++i) {
@@ -369,11 +370,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const __g
   if (role < 0) {
     const int t = group * kAppendWarps + warp;
     if (t >= p.a.num_tokens) return;
+    // everything is asked for before the slot is looked at
     const int32_t slot = p.a.slots[t];
-    if (slot < 0 || slot >= p.cache.rows) {
-      if (slot != -1 && lane == 0) set_error(p.error, MLA_ERR_DEVICE_INDEX);
-      return;
-    }
+    const float scale = kDtype == MLA_KV_FP8_E4M3 ? *static_cast<const float*>(p.cache.scale) : 1.f;
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.a.kv_lat) +
                                                       (int64_t)t * p.a.kv_lat_stride);
     const uint4 a = src[lane], b = src[32 + lane];
@@ -382,6 +381,10 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const __g
     load_weights_lat(p.norm, MLA_PART_KV_LAT, lane, w);
     load_weights_pe(p.norm, MLA_PART_KV_PE, lane, w);
     const Turn r = turn_of(p, t, lane);
+    if (slot < 0 || slot >= p.cache.rows) {
+      if (slot != -1 && lane == 0) set_error(p.error, MLA_ERR_DEVICE_INDEX);
+      return;
+    }
     float x[2][8];
     unpack_bf16x8(a, x[0]);
     unpack_bf16x8(b, x[1]);
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const __g
     float2 y;
     by_kind(p.norm.apply >> MLA_PART_KV_PE & 1, turn_kind(p),
             [&](auto norm, auto turn) { y = turned_pe<norm.value, turn.value>(p.norm.eps, w, r, u); });
-    store_row<kDtype>(p, slot, x, y, lane);
+    store_row<kDtype>(p, slot, scale, x, y, lane);
     return;
   }
   if (kQ == 0) return;
