@@ -248,7 +248,8 @@ class MLACachePool:
         if code == MLA_KV_FP8_E4M3:
             scale = torch.full((1,), float(kv_scale), dtype=torch.float32, device=device)
         elif code == MLA_KV_MXFP4:
-            scale = torch.full((num_layers, rows, 18), 127, dtype=torch.uint8, device=device)
+            # layers 16-byte aligned, as the decode takes them: whole runs of 8 rows
+            scale = torch.full((num_layers, -(-rows // 8) * 8, 18), 127, dtype=torch.uint8, device=device)[:, :rows]
         return cls(kv, code, page_size, kv_scale=scale, max_batch=max_batch)
 
     def table(self, batch: int, num_indices: int):

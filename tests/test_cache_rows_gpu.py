@@ -453,6 +453,17 @@ def test_layers_with_scales_and_strides_of_their_own():
     assert torch.all(raw[:, 48:] == 0), "rows of no layer"
 
 
+@pytest.mark.parametrize("kv_dtype", ["bf16", "fp8", "mxfp4"])
+def test_allocated_layers_fit_the_decode(kv_dtype):
+    """Every layer of an allocated pool meets the decode's alignments, whatever its rows."""
+    pool = cache.MLACachePool.allocate(kv_dtype, 13, 1, num_layers=3, device=DEV)
+    for layer in range(3):
+        assert pool.kv[layer].data_ptr() % 32 == 0
+        if kv_dtype == "mxfp4":
+            assert pool.kv_scale[layer].data_ptr() % 16 == 0
+    assert pool.num_pages == 13 and pool.num_layers == 3
+
+
 @pytest.mark.parametrize("how", ["stream", "handle"])
 def test_memory_made_on_the_calls_stream(how):
     """Without out= the result belongs to the stream that the call names, as a torch stream or a handle."""
