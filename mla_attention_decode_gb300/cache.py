@@ -10,7 +10,15 @@ library's CUDA kernels, nothing synchronises, and what only the device can see
 is reported by ``MLACachePool.poll_error``.
 
 A page table is a tuple ``(page_indptr, kv_indices, last_page_len)`` of int32
-CUDA tensors, the arrays that ``PagedMLADecoder`` takes.
+CUDA tensors, the arrays that ``PagedMLADecoder`` takes.  A decode step of one
+token per sequence, with two tables used in turn:
+
+    pool.resize(table, lengths, out=spare)                  # lengths: one more row each
+    slots, rows = pool.slots(spare, qo_indptr, batch, rows=positions)
+    for layer in ...:
+        pool.append(kv_a[:, :512], kv_a[:, 512:], slots, rope, positions, norm,
+                    q_pe=q_pe, q_out=q, layer=layer)        # q: latent columns there already
+        decoder(q, pool.kv[layer], *spare, qo_indptr, kv_scale=...)   # a PagedMLADecoder for the lengths
 """
 from __future__ import annotations
 
@@ -26,7 +34,7 @@ from . import binding
 from .binding import MLA_ERR_INVALID_ARG, MLA_KV_BF16, MLA_KV_FP8_E4M3, MLA_KV_MXFP4, MLA_OK, MLAError
 
 MLA_ERR_OUT_OF_PAGES = 8
-PAIRS, MAX_AXES = 32, 8
+PAIRS = 32
 ROW_WIDTH = {MLA_KV_BF16: 576, MLA_KV_FP8_E4M3: 576, MLA_KV_MXFP4: 288}
 _PARTS = ("kv_lat", "kv_pe", "q_lat", "q_pe")
 _PART_COLUMNS = (512, 64, 512, 64)

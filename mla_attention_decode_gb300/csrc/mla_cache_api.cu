@@ -15,8 +15,6 @@ constexpr int32_t kMaxTokens = 1 << 27;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-int64_t scale_row_bytes(const mla_cache* c) { return c->kv_dtype == MLA_KV_MXFP4 ? c->scale_stride : 0; }
-
 int check_cache(const mla_cache* c) {
   if (!c) return MLA_ERR_INVALID_ARG;
   if (c->kv_dtype < MLA_KV_BF16 || c->kv_dtype > MLA_KV_MXFP4) return MLA_ERR_UNSUPPORTED;
@@ -74,7 +72,7 @@ mla::PageBytes page_bytes(const mla_cache* c, int32_t rows_moved) {
     b.scale = static_cast<uint8_t*>(c->kv_scale);
     b.scale_layer = c->num_layers > 1 ? c->scale_layer_bytes : 0;
     b.scale_stride = c->scale_stride;
-    const int64_t len = scale_row_bytes(c) * rows_moved;
+    const int64_t len = (int64_t)c->scale_stride * rows_moved;
     while (len % b.scale_unit != 0 || b.scale_layer % b.scale_unit != 0) b.scale_unit /= 2;
   }
   return b;
@@ -88,7 +86,7 @@ int check_table(const mla_page_table* t) {
   return MLA_OK;
 }
 
-bool strides_fit(int64_t stride, int64_t mult) { return stride % mult == 0; }
+bool multiple(int64_t stride, int64_t of) { return stride % of == 0; }
 
 int done(cudaError_t e) {
   if (e == cudaSuccess) return MLA_OK;
@@ -176,20 +174,20 @@ int mla_cache_append(const mla_cache* cache, const mla_rope* rope, const mla_nor
   if (a.kv_lat) {
     if (!a.kv_pe || !a.slots || !aligned(a.slots, 4)) return MLA_ERR_INVALID_ARG;
     if (!aligned(a.kv_lat, 16) || !aligned(a.kv_pe, 4)) return MLA_ERR_INVALID_ARG;
-    if (!strides_fit(a.kv_lat_stride, 8) || !strides_fit(a.kv_pe_stride, 2)) return MLA_ERR_INVALID_ARG;
+    if (!multiple(a.kv_lat_stride, 8) || !multiple(a.kv_pe_stride, 2)) return MLA_ERR_INVALID_ARG;
   } else if (a.kv_pe) {
     return MLA_ERR_INVALID_ARG;
   }
   if (a.q_pe) {
     if (!a.q_out || !aligned(a.q_pe, 4) || !aligned(a.q_out, 16) || !aligned(a.q_lat, 16)) return MLA_ERR_INVALID_ARG;
-    if (!strides_fit(a.q_pe_token_stride, 2) || !strides_fit(a.q_pe_head_stride, 2)) return MLA_ERR_INVALID_ARG;
-    if (a.q_lat && (!strides_fit(a.q_lat_token_stride, 8) || !strides_fit(a.q_lat_head_stride, 8)))
+    if (!multiple(a.q_pe_token_stride, 2) || !multiple(a.q_pe_head_stride, 2)) return MLA_ERR_INVALID_ARG;
+    if (a.q_lat && (!multiple(a.q_lat_token_stride, 8) || !multiple(a.q_lat_head_stride, 8)))
       return MLA_ERR_INVALID_ARG;
   } else if (a.q_lat || a.q_out) {
     return MLA_ERR_INVALID_ARG;
   }
   if (rope && (!a.positions || !aligned(a.positions, 4))) return MLA_ERR_INVALID_ARG;
-  p.cache = mla::LayerRows(layer_rows(cache, args->layer));
+  p.cache = layer_rows(cache, args->layer);
   p.a = a;
   p.error = device_error;
   return done(mla::launch_append(p, cache->kv_dtype, static_cast<cudaStream_t>(stream)));
@@ -203,7 +201,7 @@ int mla_cache_gather(const mla_cache* cache, int32_t layer, const int32_t* slots
     return MLA_ERR_INVALID_ARG;
   if (num_rows == 0) return MLA_OK;
   if (!slots || !out || !aligned(slots, 4) || !aligned(out, 16)) return MLA_ERR_INVALID_ARG;
-  if (out_stride < mla::kRow || !strides_fit(out_stride, 8)) return MLA_ERR_INVALID_ARG;
+  if (out_stride < mla::kRow || !multiple(out_stride, 8)) return MLA_ERR_INVALID_ARG;
   mla::GatherParams p;
   p.cache = layer_rows(cache, layer);
   p.slots = slots;

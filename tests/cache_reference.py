@@ -46,11 +46,6 @@ def dequant(kv_dtype, kv, scale):
     return e2m1_values()[codes] * s.repeat_interleave(BLOCK, 1)
 
 
-def to_bf16(x):
-    """fp64 -> nearest bf16 (through fp32 only where that is exact or far from a tie)."""
-    return x.float().to(torch.bfloat16)
-
-
 # ------------------------------------------------------------------ pages
 class PoolModel:
     """The pages of a cache as lists: ``refs`` and, per page, a list of row tags."""

@@ -109,7 +109,7 @@ def test_copy_past_32_bit_offsets():
     assert torch.all(pool.kv[:, :64] == 0) and torch.all(pool.kv[:, 128:192] == 0)
 
 
-def check_state(pool, model, table, seqs, before, tags_to_bytes):
+def check_state(pool, model, table, seqs, tags_to_bytes):
     """The device's tables, counts and rows are the model's."""
     assert pool.refs.tolist() == model.refs
     got = seqs_of(table, pool.page_size)
@@ -199,7 +199,7 @@ def test_random_life_of_a_pool(kv_dtype, page, layers, pages, seed):
             table = (table[0], idx, table[2])
             seqs = [([place[g] for g in pgs], n) for pgs, n in seqs]
         assert pool.poll_error() == 0
-        check_state(pool, model, table, seqs, None, tags_to_bytes)
+        check_state(pool, model, table, seqs, tags_to_bytes)
 
 
 def test_truncating_into_a_shared_page_copies_it():
