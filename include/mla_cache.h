@@ -183,8 +183,8 @@ MLA_API int mla_cache_copy_pages(const mla_cache* cache, const int32_t* src, con
                                  int32_t* device_error, void* stream);
 
 /*
- * Page ownership.  page_refs: device int32 [num_pages], how many sequences hold
- * a page; 0 = free.  Fresh pages are always the free pages of lowest number, in
+ * Page ownership.  page_refs: device int32 [num_pages], 16-byte aligned, how many
+ * sequences hold a page; 0 = free.  Fresh pages are always the free pages of lowest number, in
  * order of sequence and place, so every result is the same from run to run.
  * Part-filled pages belong to one sequence: fork and resize copy a shared one
  * before it can be written.

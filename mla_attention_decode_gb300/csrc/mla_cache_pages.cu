@@ -862,7 +862,7 @@ __global__ void __launch_bounds__(256, kMoveCtas) mla_compact_apply_kernel(const
 constexpr int kLocalThreads = 256;
 struct CompactLocal {
   Scan<1, int32_t, kLocalThreads> scan;
-  int32_t kept, last;
+  int32_t last;
   int32_t pre[kLocalPages / 32];
   union {
     uint8_t bytes[kLocalPages / 8];  // a bit a page: in use
@@ -977,7 +977,8 @@ cudaError_t launch_copy_pages(const CopyParams& p, cudaStream_t s) {
 // kClusterEntries table entries, and at most so many bytes of part-filled pages
 // (a fork copies one per sequence; a resize seldom copies any).
 cudaError_t launch_table(const TableParams& p, cudaStream_t s) {
-  int64_t threads = copy_threads(p.c, p.to.batch), entries = p.to.num_indices;
+  // (a page of one row is never part-filled)
+  int64_t threads = p.c.page_size == 1 ? 0 : copy_threads(p.c, p.to.batch), entries = p.to.num_indices;
   const int64_t most = threads * 128;  // bytes: 8 units of 16 a thread
   if (!p.forks && entries < p.from.num_indices) entries = p.from.num_indices;
   if (p.to.batch <= kPlan && p.c.num_pages <= kLocalPages && entries <= kClusterEntries &&
@@ -985,7 +986,6 @@ cudaError_t launch_table(const TableParams& p, cudaStream_t s) {
     return launch_chained(mla_table_local_kernel, kCluster, kPlan, s, p, kCluster);
   cudaError_t e = plan_launch(mla_table_plan_kernel, p.refs, false, s, p);
   if (e != cudaSuccess) return e;
-  if (p.c.page_size == 1) threads = 0;  // no page is part-filled
   TableParams q = p;
   q.entries_apart = entries > kApartEntries || threads == 0;
   if (q.entries_apart) {
