@@ -166,8 +166,8 @@ typedef struct {
  *   rows[t * row_stride] its place in the sequence (a position for the rotation)
  * (rows may be NULL).  qo_indptr[0] must be 0.  Tokens from qo_indptr[batch] on
  * (a padded batch) get slot -1 and row 0.  A token before its sequence's first
- * row gets slot -1, and so does one whose table entry is out of range; both set
- * MLA_ERR_DEVICE_INDEX.
+ * row gets slot -1 (and that negative row), and so does one whose table entry is
+ * out of range; both set MLA_ERR_DEVICE_INDEX.
  */
 MLA_API int mla_cache_slots(const mla_cache* cache, const mla_page_table* table, const int32_t* qo_indptr,
                             int32_t num_tokens, int32_t* slots, int32_t* rows, int64_t row_stride,

@@ -521,3 +521,67 @@ def test_a_captured_decode_step():
     assert length.tolist() == lens and rows.tolist() == [n - 1 for n in lens]
     slots, _ = pool.slots(table, i32([0, lens[0], sum(lens)]), sum(lens))
     assert torch.equal(pool.gather(slots).cpu(), torch.cat([torch.cat(w) for w in want]))
+
+
+def test_two_graphs_share_a_pool():
+    """Calls captured into two graphs and replayed in turn, the pool's workspace theirs both."""
+    page = 8
+    pool = new_pool("fp8", 200, page)
+    t0 = pool.resize(pool.table(3, 0), i32([20, 0, 33]), pool.table(3, 30))
+    t1, t2, parents = pool.table(5, 60), pool.table(5, 60), i32([0, 2, 2, 1, 0])
+    longer = i32([29, 40, 33, 5, 20])
+    held = pool.refs.clone()
+
+    def one():
+        pool.fork(t0, parents, t1)
+
+    def two():
+        pool.resize(t1, longer, t2)
+
+    graphs = []
+    for call in (one, two):
+        call()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append(g)
+    want = None
+    for _ in range(3):
+        pool.refs.copy_(held)
+        for t in (t1, t2):
+            for x in t:
+                x.fill_(-3)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        got = (pool.refs.tolist(), seqs_of(t1, page), seqs_of(t2, page))
+        want = want or got
+        assert got == want and pool.poll_error() == 0
+    model = PoolModel(200, page)
+    seqs = model.resize([([], 0)] * 3, [20, 0, 33])
+    forks = model.fork(seqs, parents.tolist())
+    assert want[1] == forks
+    assert want[2] == model.resize(forks, longer.tolist()) and want[0] == model.refs
+
+
+def test_pools_on_streams_of_their_own():
+    """Two pools used at once from two streams, each as the model says."""
+    rng = np.random.RandomState(3)
+    pools = [new_pool("bf16", 300, 4), new_pool("mxfp4", 17000, 2)]
+    streams = [torch.cuda.Stream() for _ in pools]
+    models = [PoolModel(300, 4), PoolModel(17000, 2)]
+    tables = [p.table(4, 0) for p in pools]
+    seqs = [[([], 0)] * 4 for _ in pools]
+    for _ in range(12):
+        lengths = [[int(x) for x in rng.randint(0, 200, 4)] for _ in pools]
+        dev = [i32(x) for x in lengths]
+        outs = [p.table(4, 500) for p in pools]
+        torch.cuda.synchronize()
+        for p, s, t, n, o in zip(pools, streams, tables, dev, outs):
+            p.resize(t, n, o, stream=s)
+        torch.cuda.synchronize()
+        for i in range(2):
+            seqs[i] = models[i].resize(seqs[i], lengths[i])
+            assert seqs_of(outs[i], pools[i].page_size) == seqs[i] and pools[i].refs.tolist() == models[i].refs
+        tables = outs
+    assert all(p.poll_error() == 0 for p in pools)
