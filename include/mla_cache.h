@@ -51,6 +51,9 @@ typedef struct {
   int32_t num_layers;        /* >= 1 */
   int32_t scale_stride;      /* mxfp4: bytes between scale rows, >= 18; otherwise 0 */
   int32_t reserved;          /* 0 */
+  int32_t scale_width;       /* mxfp4: bytes of each scale row that are this cache's, 18..scale_stride (0: all
+                                of them); the others are neither read nor written; otherwise 0 */
+  int32_t reserved2;         /* 0 */
 } mla_cache;
 
 /*

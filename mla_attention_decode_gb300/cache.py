@@ -44,7 +44,7 @@ class mla_cache(ctypes.Structure):
     _fields_ = [("kv", ctypes.c_void_p), ("kv_scale", ctypes.c_void_p), ("kv_layer_bytes", ctypes.c_int64),
                 ("scale_layer_bytes", ctypes.c_int64), ("kv_dtype", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("num_pages", ctypes.c_int32), ("num_layers", ctypes.c_int32), ("scale_stride", ctypes.c_int32),
-                ("reserved", ctypes.c_int32)]
+                ("reserved", ctypes.c_int32), ("scale_width", ctypes.c_int32), ("reserved2", ctypes.c_int32)]
 
 
 class mla_rope(ctypes.Structure):
@@ -184,7 +184,8 @@ class MLACachePool:
     ``kv``: [rows, width] or [layers, rows, width] (rows = pages * page_size):
     bf16 [.., 576], e4m3 bytes [.., 576] or packed e2m1 [.., 288]; ``kv_scale``:
     fp32 [1] (or one per layer) for fp8, e8m0 bytes [(layers,) rows, >= 18] for
-    MXFP4.  ``refs``: int32, how many sequences hold each page (default: all
+    MXFP4 (columns of a wider tensor too, 16-byte aligned: the others are left
+    alone).  ``refs``: int32, how many sequences hold each page (default: all
     free).  A contiguous cache is one with pages of one row.
 
     Calls that share a pool are ordered on the GPU (one stream, or events).
@@ -227,7 +228,11 @@ class MLACachePool:
                 if (kv_scale.dtype != torch.uint8 or kv_scale.shape[:-1] != kv.shape[:-1] or kv_scale.shape[-1] < 18
                         or kv_scale.stride(-1) != 1):
                     raise ValueError("kv_scale is uint8 [.., rows, >= 18]")
-                c.scale_stride = kv_scale.stride(-2)
+                # the columns of a wider tensor: what lies between them is not the cache's.  (One row has no
+                # stride that means anything.)
+                c.scale_stride = kv_scale.stride(-2) if rows > 1 else kv_scale.shape[-1]
+                if kv_scale.shape[-1] < c.scale_stride:
+                    c.scale_width = kv_scale.shape[-1]
                 if layered and kv.shape[0] > 1:
                     c.scale_layer_bytes = kv_scale.stride(0)
             c.kv_scale = kv_scale.data_ptr()

@@ -841,7 +841,7 @@ const char* mla_status_string(int status) {
   }
 }
 
-const char* mla_decode_version(void) { return "0.3.0"; }
+const char* mla_decode_version(void) { return "0.4.0"; }
 
 int mla_decode_set_trace(uint64_t* buffer) {
 #if defined(MLA_TRACE) && MLA_TRACE

@@ -20,12 +20,15 @@ int check_cache(const mla_cache* c) {
   if (c->kv_dtype < MLA_KV_BF16 || c->kv_dtype > MLA_KV_MXFP4) return MLA_ERR_UNSUPPORTED;
   if (c->page_size < 1 || c->page_size > (1 << 20) || (c->page_size & (c->page_size - 1)) != 0)
     return MLA_ERR_UNSUPPORTED;
-  if (c->num_pages < 0 || c->num_layers < 1 || c->reserved != 0) return MLA_ERR_INVALID_ARG;
+  if (c->num_pages < 0 || c->num_layers < 1 || c->reserved != 0 || c->reserved2 != 0) return MLA_ERR_INVALID_ARG;
   const int64_t rows = (int64_t)c->num_pages * c->page_size;
   if (rows > INT32_MAX) return MLA_ERR_UNSUPPORTED;
   if ((rows > 0 && !c->kv) || !aligned(c->kv, 16)) return MLA_ERR_INVALID_ARG;
   if (c->num_layers > 1 &&
       (c->kv_layer_bytes % 16 != 0 || c->kv_layer_bytes < rows * mla::cache_row_bytes(c->kv_dtype)))
+    return MLA_ERR_INVALID_ARG;
+  if (c->scale_width != 0 && (c->kv_dtype != MLA_KV_MXFP4 || c->scale_width < MLA_MX_SCALES_PER_ROW ||
+                              c->scale_width > c->scale_stride))
     return MLA_ERR_INVALID_ARG;
   if (c->kv_dtype == MLA_KV_FP8_E4M3) {
     if (!c->kv_scale || !aligned(c->kv_scale, 4)) return MLA_ERR_INVALID_ARG;
@@ -69,11 +72,14 @@ mla::PageBytes page_bytes(const mla_cache* c, int32_t rows_moved) {
   b.num_layers = c->num_layers;
   b.scale_unit = 16;
   if (c->kv_dtype == MLA_KV_MXFP4) {
-    b.scale = static_cast<uint8_t*>(c->kv_scale);
+    const bool whole = c->scale_width == 0 || c->scale_width == c->scale_stride;
+    (whole ? b.scale : b.scale_cols) = static_cast<uint8_t*>(c->kv_scale);
     b.scale_layer = c->num_layers > 1 ? c->scale_layer_bytes : 0;
     b.scale_stride = c->scale_stride;
-    const int64_t len = (int64_t)c->scale_stride * rows_moved;
-    while (len % b.scale_unit != 0 || b.scale_layer % b.scale_unit != 0) b.scale_unit /= 2;
+    b.scale_width = whole ? c->scale_stride : c->scale_width;
+    // every address and length of the call: runs of whole rows, or single rows' columns
+    const int64_t step = (int64_t)c->scale_stride * (whole ? rows_moved : 1), len = whole ? step : c->scale_width;
+    while (step % b.scale_unit != 0 || len % b.scale_unit != 0 || b.scale_layer % b.scale_unit != 0) b.scale_unit /= 2;
   }
   return b;
 }

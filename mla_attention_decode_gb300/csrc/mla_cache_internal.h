@@ -55,9 +55,10 @@ struct SlotsParams {
 // of the call).
 struct PageBytes {
   uint8_t* kv;
-  uint8_t* scale;        // mxfp4 only, else null
+  uint8_t* scale;        // mxfp4 whose scale rows fill their stride, else null
+  uint8_t* scale_cols;   // mxfp4 whose scale rows are scale_width of scale_stride bytes, else null
   int64_t kv_layer, scale_layer;
-  int32_t row_bytes, scale_stride;
+  int32_t row_bytes, scale_stride, scale_width;
   int32_t page_size, page_shift, num_pages, num_layers;
   int32_t scale_unit;
 };

@@ -255,6 +255,48 @@ __global__ void __launch_bounds__(256, kMoveCtas) mla_copy_pages_kernel(const __
   });
 }
 
+// Scale rows that are some columns of a wider tensor: only those columns are the
+// cache's, so the rows do not move in runs with what lies between them.  A thread
+// a row: move(i) -> (source, destination, rows), i < n, in every layer.  This is a
+// launch of its own after the one that moves the keys' rows.
+template <class Move>
+__device__ __forceinline__ void move_scale_columns(const PageBytes& c, int64_t n, Move move) {
+  const int64_t step = (int64_t)gridDim.x * 256, per = (int64_t)c.page_size * c.num_layers;
+  for (int64_t task = (int64_t)blockIdx.x * 256 + threadIdx.x; task < n * per; task += step) {
+    const int64_t i = task / per, rest = task - i * per, l = rest >> c.page_shift, row = rest & (c.page_size - 1);
+    const int3 m = move(i);
+    if (m.x < 0 || row >= m.z) continue;
+    uint8_t* base = c.scale_cols + l * c.scale_layer;
+    const uint8_t* src = base + ((int64_t)m.x * c.page_size + row) * c.scale_stride;
+    uint8_t* dst = base + ((int64_t)m.y * c.page_size + row) * c.scale_stride;
+    for (int at = 0; at < c.scale_width; at += c.scale_unit)
+      store_unit(dst + at, load_unit(src + at, c.scale_unit), c.scale_unit);
+  }
+}
+__global__ void __launch_bounds__(256) mla_copy_scale_columns_kernel(const __grid_constant__ CopyParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  move_scale_columns(p.c, p.n, [&](int64_t i) {
+    const int src = p.src[i], dst = p.dst[i];
+    const bool ok = src >= 0 && src < p.c.num_pages && dst >= 0 && dst < p.c.num_pages && src != dst;
+    return make_int3(ok ? src : -1, dst, p.c.page_size);
+  });
+}
+__global__ void __launch_bounds__(256) mla_table_scale_columns_kernel(const __grid_constant__ TableParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  if (!p.ws.head[kHeadOk]) return;
+  move_scale_columns(p.c, p.ws.head[kHeadCopies], [&](int64_t i) {
+    return make_int3(p.ws.copy_src[i], p.ws.list[p.ws.copy_rank[i]], p.ws.copy_rows[i]);
+  });
+}
+__global__ void __launch_bounds__(256) mla_compact_scale_columns_kernel(const __grid_constant__ CompactParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  move_scale_columns(p.c, p.ws.head[kHeadMoves],
+                     [&](int64_t i) { return make_int3(p.ws.from[i], p.ws.list[i], p.c.page_size); });
+}
+
 // ---------------------------------------------------------------- prefix sums
 // Exclusive prefix sums of kN values over the CTA's kThreads threads, and the
 // totals.  Every thread of the CTA calls.
@@ -965,23 +1007,31 @@ unsigned grid_for(int64_t threads) {
 int64_t copy_threads(const PageBytes& c, int64_t pages) {
   return pages * c.num_layers * (kv_segs(c) + scale_segs(c)) * 32;
 }
+// The scale columns of up to `pages` pages, where they are apart.
+template <class Kernel, class Params>
+cudaError_t launch_scale_columns(Kernel kernel, int64_t pages, cudaStream_t s, const Params& p) {
+  if (!p.c.scale_cols) return cudaSuccess;
+  return launch_chained(kernel, grid_for(pages * p.c.num_layers * p.c.page_size), 256, s, p);
+}
 
 }  // namespace
 
 cudaError_t launch_copy_pages(const CopyParams& p, cudaStream_t s) {
   if (p.n == 0) return cudaSuccess;
-  return launch_chained(mla_copy_pages_kernel, grid_for(copy_threads(p.c, p.n)), 256, s, p);
+  const cudaError_t e = launch_chained(mla_copy_pages_kernel, grid_for(copy_threads(p.c, p.n)), 256, s, p);
+  return e != cudaSuccess ? e : launch_scale_columns(mla_copy_scale_columns_kernel, p.n, s, p);
 }
 
 // The cluster carries a call out by itself where that is little: up to
 // kClusterEntries table entries, and at most so many bytes of part-filled pages
-// (a fork copies one per sequence; a resize seldom copies any).
+// (a fork copies one per sequence; a resize seldom copies any).  Scale columns are
+// moved by what the deciding kernel leaves in the workspace.
 cudaError_t launch_table(const TableParams& p, cudaStream_t s) {
   // (a page of one row is never part-filled)
   int64_t threads = p.c.page_size == 1 ? 0 : copy_threads(p.c, p.to.batch), entries = p.to.num_indices;
   const int64_t most = threads * 128;  // bytes: 8 units of 16 a thread
   if (!p.forks && entries < p.from.num_indices) entries = p.from.num_indices;
-  if (p.to.batch <= kPlan && p.c.num_pages <= kLocalPages && entries <= kClusterEntries &&
+  if (!p.c.scale_cols && p.to.batch <= kPlan && p.c.num_pages <= kLocalPages && entries <= kClusterEntries &&
       most <= (p.forks ? kClusterForkBytes : kClusterResizeBytes))
     return launch_chained(mla_table_local_kernel, kCluster, kPlan, s, p, kCluster);
   cudaError_t e = plan_launch(mla_table_plan_kernel, p.refs, false, s, p);
@@ -991,11 +1041,13 @@ cudaError_t launch_table(const TableParams& p, cudaStream_t s) {
   if (q.entries_apart) {
     e = launch_chained(mla_table_entries_kernel, grid_for(entries), 256, s, q);
     if (e != cudaSuccess || threads == 0) return e;
-    return launch_chained(mla_table_apply_kernel, grid_for(threads), 256, s, q);
+    e = launch_chained(mla_table_apply_kernel, grid_for(threads), 256, s, q);
+    return e != cudaSuccess ? e : launch_scale_columns(mla_table_scale_columns_kernel, p.to.batch, s, q);
   }
   const unsigned by_rows = (grid_for(threads) + 2) / 3, by_entries = grid_for(entries);
   const unsigned quarter = by_rows > by_entries ? by_rows : by_entries;
-  return launch_chained(mla_table_apply_kernel, 4 * (quarter < kMaxGrid / 4 ? quarter : kMaxGrid / 4), 256, s, q);
+  e = launch_chained(mla_table_apply_kernel, 4 * (quarter < kMaxGrid / 4 ? quarter : kMaxGrid / 4), 256, s, q);
+  return e != cudaSuccess ? e : launch_scale_columns(mla_table_scale_columns_kernel, p.to.batch, s, q);
 }
 
 cudaError_t launch_free(int32_t* refs, int32_t num_pages, const int32_t* pages, int32_t n, int32_t* error,
@@ -1006,7 +1058,7 @@ cudaError_t launch_free(int32_t* refs, int32_t num_pages, const int32_t* pages, 
 }
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t s) {
-  if (p.c.num_pages <= kLocalPages) {
+  if (p.c.num_pages <= kLocalPages && !p.c.scale_cols) {
     int64_t threads = copy_threads(p.c, p.c.num_pages / 2);
     if (threads < p.num_indices) threads = p.num_indices;
     const unsigned grid = grid_for(threads);
@@ -1023,7 +1075,8 @@ cudaError_t launch_compact(const CompactParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     entries = 0;
   }
-  return launch_chained(mla_compact_apply_kernel, grid_for(threads < entries ? entries : threads), 256, s, q);
+  e = launch_chained(mla_compact_apply_kernel, grid_for(threads < entries ? entries : threads), 256, s, q);
+  return e != cudaSuccess ? e : launch_scale_columns(mla_compact_scale_columns_kernel, p.c.num_pages / 2, s, q);
 }
 
 }  // namespace mla

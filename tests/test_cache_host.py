@@ -209,3 +209,16 @@ def test_python_layer_refuses_host_tensors(lib):
     with pytest.raises(ValueError):
         cache.MLANorm(kv_lat=torch.ones(512))
     assert cache.MLANorm(kv_lat=True, q_pe=True).norm.apply == 0b1001
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(kv_dtype=2, scale_stride=34, scale_width=18), OK), (dict(kv_dtype=2, scale_stride=34, scale_width=34), OK),
+    (dict(kv_dtype=2, scale_stride=34, scale_width=17), INVALID),
+    (dict(kv_dtype=2, scale_stride=34, scale_width=35), INVALID),
+    (dict(kv_dtype=2, scale_stride=34, scale_width=-1), INVALID), (dict(kv_dtype=1, scale_width=18), INVALID),
+    (dict(kv_dtype=0, kv_scale=0, scale_width=18), INVALID), (dict(reserved2=1), INVALID)])
+def test_scale_width_refusals(lib, kw, status):
+    """Scale rows are 18 bytes or more of their stride; other formats have none."""
+    d = desc(**kw)
+    assert lib.mla_cache_copy_pages(ctypes.addressof(d), None, None, 0, None, None) == status
+    assert (lib.mla_cache_workspace_bytes(ctypes.addressof(d), 1) > 0) == (status == OK)

@@ -585,3 +585,101 @@ def test_pools_on_streams_of_their_own():
             assert seqs_of(outs[i], pools[i].page_size) == seqs[i] and pools[i].refs.tolist() == models[i].refs
         tables = outs
     assert all(p.poll_error() == 0 for p in pools)
+
+
+@pytest.mark.parametrize("first,width,wide", [(16, 18, 34), (32, 18, 64), (0, 18, 19), (0, 20, 24), (16, 32, 64)])
+@pytest.mark.parametrize("page,layers,pages", [(1, 1, 60), (8, 1, 60), (4, 3, 60), (2, 2, 16500), (1, 1, 33000)])
+def test_scales_in_columns_of_a_wider_tensor(first, width, wide, page, layers, pages):
+    """Only the view's columns are the cache's: every page operator leaves the
+    others, and what lies behind the last row, as they were, and does to the view
+    what it does to scale rows of their own."""
+    g = gen(wide + page)
+    rows = pages * page
+    kv = torch.randint(0, 256, (layers, rows, 288), generator=g, dtype=torch.uint8).to(DEV)
+    # rows behind the last one of a layer: a guard
+    store = torch.randint(0, 256, (layers, rows + 16, wide), generator=g, dtype=torch.uint8).to(DEV)
+    view = store[:, :rows, first:first + width]
+    kv1, own = kv.clone(), view.contiguous()
+    before = store.clone()
+    pools = [cache.MLACachePool(kv, "mxfp4", page, kv_scale=view), cache.MLACachePool(kv1, "mxfp4", page, kv_scale=own)]
+    rng = np.random.RandomState(width)
+
+    def same(what):
+        rest = store.clone()
+        rest[:, :rows, first:first + width] = before[:, :rows, first:first + width]
+        assert torch.equal(rest, before), f"{what}: bytes that are not the cache's"
+        assert torch.equal(view, own) and torch.equal(kv, kv1) and torch.equal(pools[0].refs, pools[1].refs), what
+        assert all(p.poll_error() == 0 for p in pools), what
+
+    perm = rng.permutation(pages)
+    src, dst = i32(perm[:9].tolist() + [pages - 1]), i32(perm[9:18].tolist() + [pages - 1])
+    for p in pools:
+        p.copy_pages(src, dst)
+    same("copy")
+    some = i32([0, pages - 1, 3]), i32([pages - 1, 1, 5])
+    for p in pools:
+        p.copy_pages(*some)
+    same("copy into the last page")
+    # pages at random places, the last one among them
+    lens = [5 * page + page // 2, 0, 3 * page, 6 * page + 1]
+    held = [int(x) for x in perm[:20]]
+    if pages - 1 not in held:
+        held[7] = pages - 1
+    seqs, at = [], 0
+    for n in lens:
+        k = -(-n // page)
+        seqs.append((held[at:at + k], n))
+        at += k
+    tables = []
+    for p in pools:
+        p.refs[torch.tensor(held[:at], device=DEV)] = 1
+        tables.append(table_of(seqs, page, device=DEV))
+    parents, cut = i32([0, 3, 3, 2, 0]), i32([2 * page + page // 2, 6 * page + 3, 1, 3 * page, 5 * page])
+    for k, p in enumerate(pools):
+        tables[k] = p.fork(tables[k], parents, p.table(5, 60))
+    same("fork")
+    for k, p in enumerate(pools):
+        tables[k] = p.resize(tables[k], cut, p.table(5, 60))
+    same("resize")
+    assert seqs_of(tables[0], page) == seqs_of(tables[1], page)
+    idx = [p.compact(t[1][:int(t[0][-1])].contiguous())[0] for p, t in zip(pools, tables)]
+    same("compact")
+    assert torch.equal(*idx)
+
+
+def test_two_pools_share_one_scale_tensor():
+    """Two caches whose scales lie side by side in one tensor do not see each other."""
+    g = gen(77)
+    scales = torch.randint(0, 256, (64, 64), generator=g, dtype=torch.uint8).to(DEV)
+    kv = [torch.randint(0, 256, (64, 288), generator=g, dtype=torch.uint8).to(DEV) for _ in range(2)]
+    a, b = (cache.MLACachePool(x, "mxfp4", 8, kv_scale=scales[:, at:at + 18]) for x, at in zip(kv, (0, 32)))
+    want = scales.clone()
+    want[8:16, :18], want[56:, 32:50] = scales[:8, :18], scales[16:24, 32:50]
+    a.copy_pages(i32([0]), i32([1]))
+    b.copy_pages(i32([2]), i32([7]))
+    assert a.poll_error() == 0 and b.poll_error() == 0
+    assert torch.equal(scales, want)
+
+
+@pytest.mark.parametrize("stride", [19, 24, 32])
+@pytest.mark.parametrize("page,pages", [(8, 90), (4, 16500)])
+def test_part_filled_pages_of_any_scale_stride(stride, page, pages):
+    """Forks copy, and cuts inside a shared page copy, scale rows of odd and wide strides."""
+    pool, model = new_pool("mxfp4", pages, page, 2, stride), PoolModel(pages, page)
+    lens = [3 * page + 3, page + 1, 2 * page]
+    t0 = pool.resize(pool.table(3, 0), i32(lens), pool.table(3, 20))
+    s0 = model.resize([([], 0)] * 3, lens)
+    before = bytes_of(pool)
+    t1 = pool.fork(t0, i32([0, 1, 0, 2]), pool.table(4, 30))
+    s1 = model.fork(s0, [0, 1, 0, 2])
+    cut = [2 * page + 1, page + 2, 3 * page + 2, page // 2]
+    t2 = pool.resize(t1, i32(cut), pool.table(4, 30))
+    s2 = model.resize(s1, cut)
+    assert pool.poll_error() == 0 and seqs_of(t1, page) == s1 and seqs_of(t2, page) == s2
+    want = before.clone()
+    for pages_of, source, n in ((s1[0][0], s0[0][0], 3), (s1[1][0], s0[1][0], 1), (s1[2][0], s0[0][0], 3)):
+        want[:, pages_of[-1], :n] = before[:, source[-1], :n]
+    assert s2[0][0][-1] != s1[0][0][2] and s2[3][0][-1] != s1[3][0][0]
+    want[:, s2[0][0][-1], :1] = want[:, s1[0][0][2], :1]
+    want[:, s2[3][0][-1], :page // 2] = want[:, s1[3][0][0], :page // 2]
+    assert torch.equal(bytes_of(pool), want)
