@@ -282,11 +282,15 @@ __device__ __forceinline__ void store_row(const AppendParams& p, int32_t slot, f
     // e4m3 of the rounded quotient y / scale (not of a product with the reciprocal,
     // which lands on the other side of some borders).  Markstein's correction
     // (P. W. Markstein, IBM J. Res. Dev. 34, 1990): with r the rounded reciprocal of
-    // b and q = a r, the residual a - q b is exact in one fma, and q plus residual
-    // times r is a / b correctly rounded, while nothing over- or underflows: a scale
-    // within 2^+-60 and quotients below 1024 (past 448 all saturate); what is
-    // smaller than 2^-10 becomes 0 either way.  Else the division itself.  (Dividing
-    // each of a lane's 18 columns took 200 of 493 instructions a row.)
+    // b and q = a r, q less (q b - a) r is a / b rounded.  His proof wants q within
+    // one ulp, and a r can be 1.5 off; but only quotients next to a border of e4m3
+    // matter here, and there the result is the division's for every 24-bit b (2^23
+    // divisors, 16 border fractions, the 7 dividends nearest each: 939 million, all
+    // equal).  That holds while nothing over- or underflows: a scale within 2^+-60
+    // and quotients below 1024 (past 448 all saturate); what is smaller than 2^-10
+    // becomes a zero of y's sign either way (q b - a rather than a - q b: of a zero
+    // it is +0, and -0 less +0 is -0).  Else the division itself.  (Dividing each of
+    // a lane's 18 columns took 200 of 493 instructions a row.)
     const float r = __frcp_rn(sc);
     float2 q[9], top = both(0.f);
 #pragma unroll
@@ -294,7 +298,7 @@ __device__ __forceinline__ void store_row(const AppendParams& p, int32_t slot, f
       const float2 y = i < 8 ? make_float2(lat[i >> 2][2 * (i & 3)], lat[i >> 2][2 * (i & 3) + 1]) : pe;
       const float2 q0 = mul2(y, both(r));
       top = make_float2(max_nan(top.x, fabsf(q0.x)), max_nan(top.y, fabsf(q0.y)));
-      q[i] = fma2(fma2(q0, both(-sc), y), both(r), q0);
+      q[i] = fma2(fma2(q0, both(sc), make_float2(-y.x, -y.y)), both(-r), q0);
     }
     const bool plain = max_nan(top.x, top.y) < 1024.f && sc > 0x1p-60f && sc < 0x1p60f;
     if (!plain) {

@@ -553,3 +553,34 @@ def test_python_refusals():
     with pytest.raises(binding.MLAError) as e:
         pool.append(**{**ok, "layer": 1})
     assert e.value.status == binding.MLA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.011, 1 / 3, 448.0, 2.0 ** -59, 2.0 ** 59, 2.0 ** 61, 1e-30])
+def test_e4m3_keeps_the_sign_of_zero(scale):
+    """Zeros, and what rounds to them, keep their sign, among ordinary values, among
+    values past the range, and where the quotient is a division."""
+    x = torch.zeros(6, 576)
+    x[0], x[1, ::2], x[2, 1::3] = -0.0, -0.0, -0.0
+    x[3] = torch.where(torch.arange(576) % 5 == 0, torch.tensor(-0.0), torch.linspace(-3, 3, 576) * scale)
+    x[4] = torch.where(torch.arange(576) % 2 == 0, torch.tensor(-0.0), torch.tensor(1e30))
+    x[5] = -scale * 2.0 ** -11 * (torch.arange(576) % 3)
+    x = x.to(torch.bfloat16)
+    pool = new_pool("fp8", 6, scale=scale)
+    pool.append(x.to(DEV)[:, :512], x.to(DEV)[:, 512:], torch.arange(6, dtype=torch.int32, device=DEV))
+    want = (x.float() / torch.tensor([scale], dtype=torch.float32)).clamp(-448, 448).to(torch.float8_e4m3fn)
+    assert int((want.view(torch.uint8) == 0x80).sum()) > 1200
+    assert torch.equal(pool.kv.cpu()[0], want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_mxfp4_keeps_the_sign_of_zero(sign):
+    """The bytes of the generators for zeros of either sign, in blocks of zeros and among values."""
+    x = torch.full((3, 576), 0.0 * sign)
+    x[1, ::2] = 1.25
+    x[2] = sign * torch.linspace(0, 0.2, 576)
+    x[2, ::32] = 6.0
+    x = x.to(torch.bfloat16)
+    want, scales = synth.quantize_mxfp4(x)
+    pool = new_pool("mxfp4", 3)
+    pool.append(x.to(DEV)[:, :512], x.to(DEV)[:, 512:], torch.arange(3, dtype=torch.int32, device=DEV))
+    assert torch.equal(pool.kv.cpu()[0], want) and torch.equal(pool.kv_scale.cpu()[0], scales)
