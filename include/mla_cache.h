@@ -194,11 +194,13 @@ MLA_API int mla_cache_copy_pages(const mla_cache* cache, const int32_t* src, con
  *
  * Both take a table `from` and write a table `to` (other buffers).  If the
  * call cannot be met (fewer free pages than it needs: MLA_ERR_OUT_OF_PAGES;
- * `to` has too little room, an inconsistent `from`, a bad parent or length:
- * MLA_ERR_DEVICE_INDEX), the error word is set, `to` is left with every
- * sequence empty, and neither the counts nor the cache change.  A page number
- * out of range within `from` becomes -1 in `to`, sets MLA_ERR_DEVICE_INDEX and
- * is not counted.
+ * `to` has too little room, page_indptr or last_page_len of `from`
+ * inconsistent, a bad parent or length: MLA_ERR_DEVICE_INDEX), the error word
+ * is set, `to` is left with every sequence empty, and neither the counts nor
+ * the cache change.  A page number within `from` that is out of range, or a
+ * page that is free as the call begins (its count 0: nobody holds it, and it
+ * may be handed out), becomes -1 in `to`, sets MLA_ERR_DEVICE_INDEX and is
+ * neither counted nor given back.
  *
  * The workspace is mla_cache_workspace_bytes(cache, batch of `to`) bytes,
  * 256-byte aligned, zeroed before its first use; calls that share it must be

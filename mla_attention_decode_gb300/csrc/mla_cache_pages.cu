@@ -341,6 +341,10 @@ struct Scan {
   }
 };
 
+// A page that a table may name: in range, and held (`used`: a bit a page).
+__device__ __forceinline__ bool is_held(const uint32_t* used, int num_pages, int32_t page) {
+  return page >= 0 && page < num_pages && (used[page >> 5] >> (page & 31) & 1);
+}
 // One hold on a page ends.  A page given back more often than it is held keeps
 // the count 0.
 __device__ __forceinline__ void release_page(int32_t* refs, int num_pages, int32_t page, int32_t* error) {
@@ -472,7 +476,7 @@ __device__ __forceinline__ SeqPlan plan_sequence(const TableParams& p, int n) {
   s.first = (int32_t)keep;
   if ((r0 & (P - 1)) != 0 && (p.forks || s.want != len)) {
     const int32_t page = p.from.kv_indices[s.a + keep - 1];
-    if (page >= 0 && page < p.c.num_pages && (p.forks || p.refs[page] > 1)) {
+    if (page >= 0 && page < p.c.num_pages && p.refs[page] > (p.forks ? 0 : 1)) {
       s.src = page;
       s.rows = (int32_t)(r0 & (P - 1));
       s.first -= 1;
@@ -545,7 +549,7 @@ __device__ __forceinline__ void apply_entries(const TableParams& p, int64_t at, 
       page = p.ws.list[p.ws.fresh[n] + j - first];
     } else {
       page = p.from.kv_indices[p.from.page_indptr[p.forks ? p.by[n] : n] + j];
-      if (page < 0 || page >= p.c.num_pages) {
+      if (!is_held(p.ws.mask, p.c.num_pages, page)) {
         page = -1;
         set_error(p.ws.err, MLA_ERR_DEVICE_INDEX);
       } else if (p.forks) {
@@ -559,7 +563,9 @@ __device__ __forceinline__ void apply_entries(const TableParams& p, int64_t at, 
     for (int64_t e = p.from.page_indptr[0] + at; e < end; e += step) {
       const int n = owner(p.from.page_indptr, B, (int)e);
       if ((int)e - p.from.page_indptr[n] < p.ws.first[n]) continue;
-      release_page(p.refs, p.c.num_pages, p.from.kv_indices[e], p.ws.err);
+      const int32_t page = p.from.kv_indices[e];
+      if (is_held(p.ws.mask, p.c.num_pages, page)) release_page(p.refs, p.c.num_pages, page, p.ws.err);
+      else set_error(p.ws.err, MLA_ERR_DEVICE_INDEX);
     }
   }
 }
@@ -671,7 +677,7 @@ struct TableLocal {
   uint16_t copy_src[kPlan], copy_rank[kPlan];
   int32_t flags;
   union {
-    uint8_t bytes[kLocalPages / 8];  // a bit a page: free
+    uint8_t bytes[kLocalPages / 8];  // a bit a page: in use
     uint32_t words[kLocalPages / 32];
   } mask;
   uint16_t list[kLocalPages];
@@ -701,12 +707,12 @@ __global__ void __launch_bounds__(kPlan, 1) mla_table_local_kernel(const __grid_
 #pragma unroll
   for (int i = 0; i < kPasses; ++i)
     put_nibble(s.mask.bytes, i * kPlan + tid,
-               (uint32_t)(c4[i].x <= 0) | (uint32_t)(c4[i].y <= 0) << 1 | (uint32_t)(c4[i].z <= 0) << 2 |
-                   (uint32_t)(c4[i].w <= 0) << 3);
+               (uint32_t)(c4[i].x > 0) | (uint32_t)(c4[i].y > 0) << 1 | (uint32_t)(c4[i].z > 0) << 2 |
+                   (uint32_t)(c4[i].w > 0) << 3);
   __syncthreads();
   if (!q.ok) atomicOr(&s.flags, 1);
   if (q.release) atomicOr(&s.flags, 2);
-  uint32_t m = s.mask.words[tid];
+  uint32_t m = ~s.mask.words[tid];  // the free pages
   int32_t v[4] = {q.ok ? (int32_t)q.cnt : 0, q.ok ? (int32_t)(q.cnt - q.first) : 0, q.ok && q.src >= 0, __popc(m)};
   int32_t sum[4];
   s.scan.run(v, sum);
@@ -750,7 +756,7 @@ __global__ void __launch_bounds__(kPlan, 1) mla_table_local_kernel(const __grid_
       page = s.list[s.fresh[n] + j - first];
     } else {
       page = p.from.kv_indices[s.from_at[n] + j];
-      if (page < 0 || page >= pages) {
+      if (!is_held(s.mask.words, pages, page)) {
         page = -1;
         set_error(p.ws.err, MLA_ERR_DEVICE_INDEX);
       } else if (p.forks) {
@@ -763,7 +769,10 @@ __global__ void __launch_bounds__(kPlan, 1) mla_table_local_kernel(const __grid_
   if (s.flags & 2)
     for (int e = s.from_at[0] + at; e < s.from_at[N]; e += step) {
       const int n = owner(s.from_at, N, e);
-      if (e - s.from_at[n] >= s.first[n]) release_page(p.refs, pages, p.from.kv_indices[e], p.ws.err);
+      if (e - s.from_at[n] < s.first[n]) continue;
+      const int32_t page = p.from.kv_indices[e];
+      if (is_held(s.mask.words, pages, page)) release_page(p.refs, pages, page, p.ws.err);
+      else set_error(p.ws.err, MLA_ERR_DEVICE_INDEX);
     }
   move_parts(p.c, copies, at, step,
              [&](int i) { return make_int3(s.copy_src[i], s.list[s.copy_rank[i]], s.copy_rows[i]); });

@@ -683,3 +683,53 @@ def test_part_filled_pages_of_any_scale_stride(stride, page, pages):
     want[:, s2[0][0][-1], :1] = want[:, s1[0][0][2], :1]
     want[:, s2[3][0][-1], :page // 2] = want[:, s1[3][0][0], :page // 2]
     assert torch.equal(bytes_of(pool), want)
+
+
+@pytest.mark.parametrize("pages", [12, 16500, 33000])
+def test_tables_that_name_free_pages(pages):
+    """A page that nobody holds is not shared, copied, kept or given back, whatever
+    the table says, and the fresh page that it may become is the new owner's alone."""
+    page, bad = 4, binding.MLA_ERR_DEVICE_INDEX
+    held = [0, 2, 3]  # page 1 is the first that a call hands out
+
+    def fresh_pool():
+        pool = new_pool("fp8", pages, page)
+        pool.refs[torch.tensor(held, device=DEV)] = 1
+        return pool, bytes_of(pool)
+
+    def refs(pool, want):
+        assert pool.refs[:6].tolist() == want and int(pool.refs[6:].abs().sum()) == 0
+
+    # grown: the free page within the table is dropped, the fresh one comes behind
+    pool, before = fresh_pool()
+    t = pool.resize((i32([0, 3]), i32([0, 1, 2]), i32([4])), i32([16]), pool.table(1, 9))
+    assert pool.poll_error() == bad
+    assert t[0].tolist() == [0, 4] and t[1][:4].tolist() == [0, -1, 2, 1] and t[2].tolist() == [4]
+    refs(pool, [1, 1, 1, 1, 0, 0])
+    # cut: it is not given back, and another sequence's fresh page stays that one's
+    pool, before = fresh_pool()
+    t = pool.resize((i32([0, 3, 4]), i32([0, 1, 2, 3]), i32([4, 4])), i32([0, 9]), pool.table(2, 9))
+    assert pool.poll_error() == bad
+    assert t[0].tolist() == [0, 0, 3] and t[1][:3].tolist() == [3, 1, 4]
+    refs(pool, [0, 1, 0, 1, 1, 0])
+    # forked as a full page
+    pool, before = fresh_pool()
+    t = pool.fork((i32([0, 3]), i32([0, 1, 2]), i32([4])), i32([0, 0]), pool.table(2, 9))
+    assert pool.poll_error() == bad
+    assert t[1][:6].tolist() == [0, -1, 2] * 2
+    refs(pool, [3, 0, 3, 1, 0, 0])
+    # forked as a part-filled last page, next to one whose copy goes into that page
+    pool, before = fresh_pool()
+    t = pool.fork((i32([0, 2, 4]), i32([0, 1, 2, 3]), i32([2, 3])), i32([0, 1]), pool.table(2, 9))
+    assert pool.poll_error() == bad
+    assert t[1][:4].tolist() == [0, -1, 2, 1] and t[2].tolist() == [2, 3]
+    refs(pool, [2, 1, 2, 1, 0, 0])
+    before[:, 1, :3] = before[:, 3, :3]
+    assert torch.equal(bytes_of(pool), before)
+    # cut inside it
+    pool, before = fresh_pool()
+    t = pool.resize((i32([0, 2]), i32([0, 1]), i32([4])), i32([6]), pool.table(1, 9))
+    assert pool.poll_error() == bad
+    assert t[1][:2].tolist() == [0, -1]
+    refs(pool, [1, 0, 1, 1, 0, 0])
+    assert torch.equal(bytes_of(pool), before) and pool.poll_error() == 0
