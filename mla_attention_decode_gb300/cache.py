@@ -300,6 +300,24 @@ class MLACachePool:
         return slots, rows
 
     # -------------------------------------------------------------- pages
+    @property
+    def refs(self):
+        """How many sequences hold each page, int32 [pages].  Assigning another tensor makes its counts the pool's."""
+        return self._refs
+
+    @refs.setter
+    def refs(self, refs):
+        self._refs, self._left = refs, None
+
+    def _counts(self):
+        """The counts, for a call that changes them."""
+        if self._left is not None:
+            if self._left == self._refs._version:
+                raise ValueError("compact(out=...) has left the pool's counts by the old page numbers: make the new counts "
+                                 "the pool's (pool.refs = refs), or keep the old table (pool.refs = pool.refs)")
+            self._left = None  # they have been written since
+        return self._refs
+
     def copy_pages(self, src, dst, stream=None):
         """Page ``dst[i]`` becomes a copy of page ``src[i]``, in every layer."""
         rc = _ext.copy_pages(self._core, src, dst, stream)
@@ -308,32 +326,40 @@ class MLACachePool:
 
     def fork(self, table, parents, out, stream=None):
         """Writes to ``out`` a batch whose sequence n is a fork of ``table``'s sequence ``parents[n]``."""
-        rc = _ext.fork(self._core, self.refs, table, parents, out, stream)
+        rc = _ext.fork(self._core, self._counts(), table, parents, out, stream)
         if rc:
             raise MLAError(rc, "mla_cache_fork")
         return out
 
     def resize(self, table, lengths, out, stream=None):
         """Writes to ``out`` the table whose sequence b has ``lengths[b]`` rows; ``table`` is void from then on."""
-        rc = _ext.resize(self._core, self.refs, table, lengths, out, stream)
+        rc = _ext.resize(self._core, self._counts(), table, lengths, out, stream)
         if rc:
             raise MLAError(rc, "mla_cache_resize")
         return out
 
     def free(self, pages, stream=None):
         """Ends one hold on each of ``pages``, e.g. the entries of a table that are in use (-1 is skipped)."""
-        rc = _ext.free(self._core, self.refs, pages, stream)
+        rc = _ext.free(self._core, self._counts(), pages, stream)
         if rc:
             raise MLAError(rc, "mla_cache_free")
 
     def compact(self, kv_indices, out=None, stream=None):
         """Moves the pages in use to the front and renumbers ``kv_indices`` (the entries of a table that are in use).
         ``out``: (kv_indices, refs, live [1]) to write; without it the pool's counts are rewritten in place and the
-        other two are new.  Returns the three."""
+        other two are new.  Returns the three.
+
+        Counts written to a tensor of ``out``'s own leave the pool's as they were, by the old numbers (which still
+        hold for the old table: the pages moved from keep their rows).  ``fork``, ``resize`` and ``free`` refuse from
+        then on until it is said which counts go on: ``pool.refs = refs`` with the new table (or the new counts copied
+        into ``pool.refs``), ``pool.refs = pool.refs`` with the old one.  (Inference tensors do not tell whether they
+        have been written: over such counts nothing is refused.)"""
         indices, refs, live = (None, None, None) if out is None else out
-        rc, indices, refs, live = _ext.compact(self._core, self.refs, kv_indices, indices, refs, live, stream)
+        rc, indices, refs, live = _ext.compact(self._core, self._refs, kv_indices, indices, refs, live, stream)
         if rc:
             raise MLAError(rc, "mla_cache_compact")
+        apart = refs.data_ptr() != self._refs.data_ptr() and not self._refs.is_inference()
+        self._left = self._refs._version if apart else None
         return indices, refs, live
 
     def poll_error(self, stream=None) -> int:

@@ -733,3 +733,65 @@ def test_tables_that_name_free_pages(pages):
     assert t[1][:2].tolist() == [0, -1]
     refs(pool, [1, 0, 1, 1, 0, 0])
     assert torch.equal(bytes_of(pool), before) and pool.poll_error() == 0
+
+
+@pytest.mark.parametrize("go_on", ["assign", "copy", "old", "in place"])
+def test_counts_that_compact_wrote_elsewhere(go_on):
+    """compact(out=...) leaves the pool's counts by the old numbers: calls that
+    change counts refuse until it is said which counts go on, and then a grown
+    sequence gets no page that holds live rows."""
+    page = 4
+    pool, model = new_pool("fp8", 12, page), PoolModel(12, page)
+    lens = [8, 6, 9]
+    t = pool.resize(pool.table(3, 0), i32(lens), pool.table(3, 12))
+    seqs = model.resize([([], 0)] * 3, lens)
+    t2 = pool.resize(t, i32([0, 6, 9]), pool.table(3, 12))  # pages 0 and 1 become holes
+    seqs = model.resize(seqs, [0, 6, 9])
+    entries = t2[1][:5].contiguous()
+    out = (torch.empty_like(entries), torch.full_like(pool.refs, -1), i32([0]))
+    old = pool.refs.clone()
+    before = bytes_of(pool)
+    got = pool.compact(entries, out=out)
+    assert all(a is b for a, b in zip(got, out)) and torch.equal(pool.refs, old)
+    pool.compact(entries, out=out)  # again, from the same counts: the same
+    moved = (t2[0], out[0], t2[2])
+    for call in (lambda: pool.resize(moved, i32([0, 9, 9]), pool.table(3, 12)),
+                 lambda: pool.fork(moved, i32([1]), pool.table(1, 12)), lambda: pool.free(out[0])):
+        with pytest.raises(ValueError, match="pool.refs"):
+            call()
+    assert torch.equal(pool.refs, old)
+    if go_on == "old":
+        pool.refs = pool.refs
+        table = t2
+    else:
+        if go_on == "assign":
+            pool.refs = out[1]
+        elif go_on == "copy":
+            pool.refs.copy_(out[1])
+        else:
+            moved = (t2[0], pool.compact(entries)[0], t2[2])
+        place, _ = model.compact()
+        seqs = [([place[g] for g in pages], n) for pages, n in seqs]
+        table = moved
+    grown = pool.resize(table, i32([5, 9, 9]), pool.table(3, 12))
+    want = model.resize(seqs, [5, 9, 9])
+    assert seqs_of(grown, page) == want and pool.refs.tolist() == model.refs
+    now = bytes_of(pool)
+    for (pages, n), (old_pages, m) in zip(want[1:], [([2, 3], 6), ([4, 5, 6], 9)]):
+        for r in range(m):
+            assert torch.equal(now[:, pages[r // page], r % page], before[:, old_pages[r // page], r % page])
+    pool.compact(grown[1][:int(grown[0][-1])].contiguous())  # in place: nothing is refused after it
+    pool.free(i32([0]))
+    assert pool.poll_error() == 0
+
+
+def test_compact_in_inference_mode():
+    """Counts that are inference tensors: the new ones go on by assignment."""
+    with torch.inference_mode():
+        pool = cache.MLACachePool.allocate("bf16", 8, 4, device=DEV)
+        t = pool.resize(pool.table(2, 0), i32([5, 7]), pool.table(2, 8))
+        t = pool.resize(t, i32([0, 7]), pool.table(2, 8))
+        idx, refs, live = pool.compact(t[1][:2].contiguous(), out=(i32([0, 0]), torch.empty_like(pool.refs), i32([0])))
+        pool.refs = refs
+        t = pool.resize((t[0], idx, t[2]), i32([3, 7]), pool.table(2, 8))
+        assert seqs_of(t, 4) == [([2], 3), ([0, 1], 7)] and int(live) == 2 and pool.poll_error() == 0
