@@ -230,8 +230,9 @@ MLA_API int mla_cache_resize(const mla_cache* cache, int32_t* page_refs, const m
 
 /*
  * mla_cache_free -- page_refs[pages[i]] -= 1, i < n: a sequence's hold on its
- * pages ends (pages: e.g. a range of kv_indices; a page may occur several
- * times).  -1 entries are skipped.  A page out of range, or one given back more
+ * pages ends (pages: e.g. the entries of a table that are in use; a page may
+ * occur several times; where only the device knows how many are in use, resize
+ * to lengths of 0 ends them).  -1 entries are skipped.  A page out of range, or one given back more
  * often than it is held (its count stays 0), sets MLA_ERR_DEVICE_INDEX.
  */
 MLA_API int mla_cache_free(const mla_cache* cache, int32_t* page_refs, const int32_t* pages, int32_t n,

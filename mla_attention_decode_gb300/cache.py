@@ -266,9 +266,9 @@ class MLACachePool:
         return cls(kv, code, page_size, kv_scale=scale, max_batch=max_batch)
 
     def table(self, batch: int, num_indices: int):
-        """Buffers of a page table of ``batch`` empty sequences, with room for ``num_indices`` entries."""
+        """Buffers of a page table of ``batch`` empty sequences, with room for ``num_indices`` entries (all -1)."""
         return (torch.zeros(batch + 1, dtype=torch.int32, device=self.device),
-                torch.zeros(num_indices, dtype=torch.int32, device=self.device),
+                torch.full((num_indices,), -1, dtype=torch.int32, device=self.device),
                 torch.zeros(batch, dtype=torch.int32, device=self.device))
 
     # -------------------------------------------------------------- rows
@@ -332,14 +332,17 @@ class MLACachePool:
         return out
 
     def resize(self, table, lengths, out, stream=None):
-        """Writes to ``out`` the table whose sequence b has ``lengths[b]`` rows; ``table`` is void from then on."""
+        """Writes to ``out`` the table whose sequence b has ``lengths[b]`` rows; ``table`` is void from then on.
+        Lengths of 0 end a batch, or some of its sequences: what they hold is given back, however long they are."""
         rc = _ext.resize(self._core, self._counts(), table, lengths, out, stream)
         if rc:
             raise MLAError(rc, "mla_cache_resize")
         return out
 
     def free(self, pages, stream=None):
-        """Ends one hold on each of ``pages``, e.g. the entries of a table that are in use (-1 is skipped)."""
+        """Ends one hold on each of ``pages`` (-1 is skipped): of a table, the entries that are in use, and only those.
+        What lies behind them in a buffer that was used before are pages too, and holds of others may end; where the
+        host does not know how many are in use, ``resize`` to lengths of 0 ends them."""
         rc = _ext.free(self._core, self._counts(), pages, stream)
         if rc:
             raise MLAError(rc, "mla_cache_free")

@@ -795,3 +795,18 @@ def test_compact_in_inference_mode():
         pool.refs = refs
         t = pool.resize((t[0], idx, t[2]), i32([3, 7]), pool.table(2, 8))
         assert seqs_of(t, 4) == [([2], 3), ([0, 1], 7)] and int(live) == 2 and pool.poll_error() == 0
+
+
+def test_ending_a_batch():
+    """A new table's buffer names no page, so that giving it back whole ends no
+    hold; lengths of 0 end a batch whose length only the device knows."""
+    page = 4
+    pool = new_pool("bf16", 20, page)
+    t = pool.resize(pool.table(2, 0), i32([9, 6]), pool.table(2, 16))
+    assert t[1].tolist() == [0, 1, 2, 3, 4] + [-1] * 11
+    forks = pool.fork(t, i32([0, 1]), pool.table(2, 16))
+    assert pool.refs[:7].tolist() == [2, 2, 1, 2, 1, 1, 1]
+    pool.free(forks[1])  # with its room to spare
+    assert pool.poll_error() == 0 and pool.refs[:7].tolist() == [1, 1, 1, 1, 1, 0, 0]
+    empty = pool.resize(t, i32([0, 0]), pool.table(2, 0))
+    assert pool.poll_error() == 0 and int(pool.refs.sum()) == 0 and empty[0].tolist() == [0, 0, 0]
