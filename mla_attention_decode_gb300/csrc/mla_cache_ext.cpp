@@ -121,6 +121,12 @@ int32_t count32(int64_t n, const char* what) {
   return static_cast<int32_t>(n);
 }
 
+// A layer's number; one that has no 32 bits is no layer of any cache.
+int32_t layer_of(PyObject* o) {
+  const long long v = whole(o);
+  return v < 0 || v > INT32_MAX ? -1 : static_cast<int32_t>(v);
+}
+
 // (page_indptr, kv_indices, last_page_len), a tuple or a list.
 mla_page_table table(const Core* c, PyObject* o, const char* what) {
   PyObject* seq = PySequence_Fast(o, "a page table is (page_indptr, kv_indices, last_page_len)");
@@ -207,7 +213,7 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const int64_t t = THPVariable_Unpack(first).size(0);
   mla_append_args args = {};
   args.num_tokens = count32(t, "the batch");
-  args.layer = static_cast<int32_t>(whole(a[10]));
+  args.layer = layer_of(a[10]);
   if (kv_lat != Py_None) {
     if (kv_pe == Py_None || slots == Py_None) refuse("keys come as kv_lat, kv_pe and slots");
     const at::Tensor& x = part(c, kv_lat, "kv_lat", t, false, MLA_V_DIM);
@@ -269,7 +275,7 @@ PyObject* py_gather(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const Core* c = core_of(a[0]);
   int64_t n = 0;
   const int32_t* slots = vec(c, a[1], "slots", -1, &n);
-  const int32_t rows = count32(n, "slots"), layer = static_cast<int32_t>(whole(a[3]));
+  const int32_t rows = count32(n, "slots"), layer = layer_of(a[3]);
   const Where w(c, a[4]);
   at::Tensor out = a[2] == Py_None ? fresh(c, w, {n, MLA_QK_DIM}, at::kBFloat16)
                                    : part(c, a[2], "out", n, false, MLA_QK_DIM);

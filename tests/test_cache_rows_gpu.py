@@ -584,3 +584,17 @@ def test_mxfp4_keeps_the_sign_of_zero(sign):
     pool = new_pool("mxfp4", 3)
     pool.append(x.to(DEV)[:, :512], x.to(DEV)[:, 512:], torch.arange(3, dtype=torch.int32, device=DEV))
     assert torch.equal(pool.kv.cpu()[0], want) and torch.equal(pool.kv_scale.cpu()[0], scales)
+
+
+@pytest.mark.parametrize("layer", [2, -1, 2 ** 31, 2 ** 32, 2 ** 32 + 1, -2 ** 32, 2 ** 62])
+def test_layers_out_of_range(layer):
+    """No number that is not a layer's is taken for one, whatever its low 32 bits."""
+    pool = new_pool("bf16", 8, layers=2)
+    before = pool.kv.clone()
+    x = torch.ones(2, 576, dtype=torch.bfloat16, device=DEV)
+    slots = torch.tensor([0, 5], dtype=torch.int32, device=DEV)
+    for call in (lambda: pool.append(x[:, :512], x[:, 512:], slots, layer=layer), lambda: pool.gather(slots, layer=layer)):
+        with pytest.raises(binding.MLAError) as e:
+            call()
+        assert e.value.status == binding.MLA_ERR_INVALID_ARG
+    assert torch.equal(pool.kv, before) and pool.poll_error() == 0
