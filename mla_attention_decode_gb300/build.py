@@ -26,6 +26,7 @@ BUILD_TRACE = os.path.join(PKG, "_build_trace")
 LIB_TRACE = os.path.join(PKG, "libmla_decode_trace.so")
 EXT_SRC = os.path.join(CSRC, "mla_cache_ext.cpp")
 EXT = os.path.join(PKG, "_mla_cache.so")
+EXT_TORCH = os.path.join(BUILD, "ext_torch_version")  # the torch that it was built for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               f"-I{INCLUDE}", f"-I{CSRC}"]
@@ -70,8 +71,7 @@ def _ext_stale() -> bool:
     deps = [EXT_SRC, os.path.join(INCLUDE, "mla_cache.h"), os.path.join(INCLUDE, "mla_decode.h")]
     if not os.path.exists(EXT) or any(os.path.getmtime(d) > os.path.getmtime(EXT) for d in deps):
         return True
-    stamp = os.path.join(BUILD, "ext_torch_version")
-    return not os.path.exists(stamp) or open(stamp).read() != torch.__version__
+    return not os.path.exists(EXT_TORCH) or open(EXT_TORCH).read() != str(torch.__version__)
 
 
 def build_ext() -> str:
@@ -82,7 +82,8 @@ def build_ext() -> str:
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     tmp = EXT + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DMLA_TORCH_VERSION="{torch.__version__}"', f"-I{INCLUDE}",
            f"-I{os.path.join(root, 'include')}", f"-I{os.path.join(root, 'include', 'torch', 'csrc', 'api', 'include')}",
            f"-I{os.path.join(cuda, 'include')}", f"-I{sysconfig.get_paths()['include']}", EXT_SRC, "-o", tmp,
            f"-L{os.path.join(root, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
@@ -90,8 +91,8 @@ def build_ext() -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {os.path.basename(EXT_SRC)}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, EXT)
-    with open(os.path.join(BUILD, "ext_torch_version"), "w") as f:
-        f.write(torch.__version__)
+    with open(EXT_TORCH, "w") as f:
+        f.write(str(torch.__version__))
     return EXT
 
 

@@ -72,10 +72,18 @@ class mla_page_table(ctypes.Structure):
 
 
 EXT_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_mla_cache.so")
+EXT_TORCH_PATH = os.path.join(os.path.dirname(EXT_PATH), "_build", "ext_torch_version")
 _ENTRY_POINTS = ("append", "gather", "slots", "copy_pages", "fork", "resize", "free", "compact")
 _lock = threading.Lock()
 _lib: ctypes.CDLL | None = None
 _ext = None
+
+
+def _load_extension():
+    loader = importlib.machinery.ExtensionFileLoader("_mla_cache", EXT_PATH)
+    ext = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_mla_cache", EXT_PATH, loader=loader))
+    loader.exec_module(ext)
+    return ext
 
 
 def load_library() -> ctypes.CDLL:
@@ -103,12 +111,13 @@ def load_library() -> ctypes.CDLL:
             lib.mla_cache_workspace_bytes.restype = sz
             if not os.path.exists(EXT_PATH):
                 raise RuntimeError(f"{EXT_PATH} is missing: build it with `python -m mla_attention_decode_gb300.build`")
-            loader = importlib.machinery.ExtensionFileLoader("_mla_cache", EXT_PATH)
-            ext = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_mla_cache", EXT_PATH, loader=loader))
-            loader.exec_module(ext)
-            if ext.torch_version != torch.__version__.split("+")[0]:
-                raise RuntimeError(f"{EXT_PATH} was built for torch {ext.torch_version}, this is {torch.__version__}: "
-                                   "build it again")
+            this = str(torch.__version__)
+            built_for = open(EXT_TORCH_PATH).read() if os.path.exists(EXT_TORCH_PATH) else this
+            if built_for == this:  # (else it may not even load)
+                ext = _load_extension()
+                built_for = ext.torch_version
+            if built_for != this:
+                raise RuntimeError(f"{EXT_PATH} was built for torch {built_for}, this is {this}: build it again")
             ext.bind(*(ctypes.cast(getattr(lib, "mla_cache_" + n), ctypes.c_void_p).value for n in _ENTRY_POINTS))
             _ext, _lib = ext, lib
     return _lib

@@ -23,7 +23,6 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
-#include <torch/version.h>
 
 #include "mla_cache.h"
 
@@ -453,6 +452,7 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mla_cache", nullptr, -1, methods,
 
 }  // namespace
 
+// MLA_TORCH_VERSION (the build's): the full version of the torch it was compiled against.
 PyMODINIT_FUNC PyInit__mla_cache(void) {
   s_address = PyUnicode_InternFromString("address");
   s_num_axes = PyUnicode_InternFromString("num_axes");
@@ -460,7 +460,7 @@ PyMODINIT_FUNC PyInit__mla_cache(void) {
   s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
   if (!s_address || !s_num_axes || !s_device_index || !s_cuda_stream) return nullptr;
   PyObject* m = PyModule_Create(&module);
-  if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0) {
+  if (m && PyModule_AddStringConstant(m, "torch_version", MLA_TORCH_VERSION) < 0) {
     Py_DECREF(m);
     return nullptr;
   }

@@ -222,3 +222,27 @@ def test_scale_width_refusals(lib, kw, status):
     d = desc(**kw)
     assert lib.mla_cache_copy_pages(ctypes.addressof(d), None, None, 0, None, None) == status
     assert (lib.mla_cache_workspace_bytes(ctypes.addressof(d), 1) > 0) == (status == OK)
+
+
+def test_extension_tells_the_full_torch_version(lib):
+    """Development builds of one release differ in what follows its three numbers."""
+    assert cache._ext.torch_version == torch.__version__ and open(build.EXT_TORCH).read() == torch.__version__
+    assert cache.EXT_TORCH_PATH == build.EXT_TORCH
+
+
+def test_extension_for_another_torch_is_refused(lib, tmp_path, monkeypatch):
+    """Before it is loaded where the build says so, by its own word otherwise."""
+    release = torch.__version__.split("+")[0]
+    monkeypatch.setattr(cache, "_lib", None)
+    said = tmp_path / "built_for"
+    said.write_text(release + ".dev20260101")
+    monkeypatch.setattr(cache, "EXT_TORCH_PATH", str(said))
+    monkeypatch.setattr(cache, "_load_extension", lambda: pytest.fail("loaded"))
+    with pytest.raises(RuntimeError, match="build it again"):
+        cache.load_library()
+    monkeypatch.setattr(cache, "EXT_TORCH_PATH", str(tmp_path / "none"))
+    other = type("Other", (), {"torch_version": release + "a0"})
+    monkeypatch.setattr(cache, "_load_extension", lambda: other)
+    with pytest.raises(RuntimeError, match="build it again"):
+        cache.load_library()
+    assert cache._lib is None
