@@ -810,3 +810,32 @@ def test_ending_a_batch():
     assert pool.poll_error() == 0 and pool.refs[:7].tolist() == [1, 1, 1, 1, 1, 0, 0]
     empty = pool.resize(t, i32([0, 0]), pool.table(2, 0))
     assert pool.poll_error() == 0 and int(pool.refs.sum()) == 0 and empty[0].tolist() == [0, 0, 0]
+
+
+@pytest.mark.parametrize("pages", [16384, 16385, 32769, 262143, 262145, 300007])
+def test_compaction_in_place_of_many_pages(pages):
+    """Counts and table rewritten in place while rows move, on both sides of the
+    sizes where other kernels take over, then fresh pages from the new counts."""
+    rng = np.random.RandomState(pages)
+    kv = torch.arange(pages, dtype=torch.int32, device=DEV).view(torch.uint8).view(pages, 4).repeat(1, 144)
+    pool = cache.MLACachePool(kv, "fp8", 1, kv_scale=torch.ones(1, device=DEV))
+    refs = (rng.rand(pages) < 0.4) * rng.randint(1, 4, pages)
+    pool.refs.copy_(torch.from_numpy(refs.astype(np.int32)))
+    alive = np.nonzero(refs)[0]
+    live = alive.size
+    holes, movers = np.nonzero(refs[:live] == 0)[0], alive[alive >= live]
+    place = np.arange(pages)
+    place[movers] = holes
+    table = rng.permutation(np.concatenate([alive, alive[::3], np.full(50, -1)])).astype(np.int32)
+    idx = torch.from_numpy(table).to(DEV)
+    kv0 = kv.clone()
+    got, counts, n = pool.compact(idx, out=(idx, pool.refs, i32([0])))
+    assert pool.poll_error() == 0 and int(n) == live
+    assert got.tolist() == np.where(table < 0, -1, place[table]).tolist()
+    new = np.zeros(pages, dtype=np.int64)
+    new[place[alive]] = refs[alive]
+    assert pool.refs.tolist() == new.tolist()
+    kv0[torch.from_numpy(holes).to(DEV)] = kv0[torch.from_numpy(movers).to(DEV)]
+    assert torch.equal(kv, kv0)
+    t = pool.resize(pool.table(1, 0), i32([100]), pool.table(1, 100))
+    assert pool.poll_error() == 0 and t[1].tolist() == list(range(live, live + 100))

@@ -598,3 +598,31 @@ def test_layers_out_of_range(layer):
             call()
         assert e.value.status == binding.MLA_ERR_INVALID_ARG
     assert torch.equal(pool.kv, before) and pool.poll_error() == 0
+
+
+@pytest.mark.parametrize("batch", [2047, 2048, 2049, 3000])
+def test_slots_of_many_sequences(batch):
+    """Batches on both sides of what is staged on chip, with empty sequences, sequences
+    without new tokens and a padded tail."""
+    g = gen(batch)
+    page = 4
+    lens = torch.randint(0, 12, (batch,), generator=g)
+    new = torch.minimum(torch.randint(0, 5, (batch,), generator=g), lens)
+    lens[0], new[0], lens[-1], new[-1] = 3, 0, 9, 9
+    lens[7], new[7] = 0, 0
+    counts = (lens + page - 1) // page
+    indptr = torch.cat([counts.new_zeros(1), counts.cumsum(0)])
+    qo = torch.cat([new.new_zeros(1), new.cumsum(0)])
+    total = int(indptr[-1])
+    perm = torch.randperm(total + 9, generator=g)[:total]
+    last = torch.where(counts > 0, lens - (counts - 1) * page, counts)
+    seq = torch.repeat_interleave(torch.arange(batch), new)
+    row = lens[seq] - new[seq] + torch.arange(seq.numel()) - qo[seq]
+    want = perm[indptr[seq] + row // page] * page + row % page
+    pool = new_pool("bf16", (total + 9) * page, page)
+    t = seq.numel() + 5
+    i32 = lambda v: v.to(torch.int32).to(DEV)  # noqa: E731
+    rows = torch.full((t,), -9, dtype=torch.int32, device=DEV)
+    slots, _ = pool.slots((i32(indptr), i32(perm), i32(last)), i32(qo), t, rows=rows)
+    assert pool.poll_error() == 0
+    assert slots.tolist() == want.tolist() + [-1] * 5 and rows.tolist() == row.tolist() + [0] * 5
