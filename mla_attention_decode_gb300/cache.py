@@ -318,14 +318,12 @@ class MLACachePool:
     def refs(self, refs):
         self._refs, self._left = refs, None
 
-    def _counts(self):
-        """The counts, for a call that changes them."""
-        if self._left is not None:
-            if self._left == self._refs._version:
-                raise ValueError("compact(out=...) has left the pool's counts by the old page numbers: make the new counts "
-                                 "the pool's (pool.refs = refs), or keep the old table (pool.refs = pool.refs)")
-            self._left = None  # they have been written since
-        return self._refs
+    def _settle(self):
+        """Before counts change that a compaction has left by the old numbers."""
+        if self._left == self._refs._version:
+            raise ValueError("compact(out=...) has left the pool's counts by the old page numbers: make the new counts "
+                             "the pool's (pool.refs = refs), or keep the old table (pool.refs = pool.refs)")
+        self._left = None  # they have been written since
 
     def copy_pages(self, src, dst, stream=None):
         """Page ``dst[i]`` becomes a copy of page ``src[i]``, in every layer."""
@@ -335,7 +333,9 @@ class MLACachePool:
 
     def fork(self, table, parents, out, stream=None):
         """Writes to ``out`` a batch whose sequence n is a fork of ``table``'s sequence ``parents[n]``."""
-        rc = _ext.fork(self._core, self._counts(), table, parents, out, stream)
+        if self._left is not None:
+            self._settle()
+        rc = _ext.fork(self._core, self._refs, table, parents, out, stream)
         if rc:
             raise MLAError(rc, "mla_cache_fork")
         return out
@@ -343,7 +343,9 @@ class MLACachePool:
     def resize(self, table, lengths, out, stream=None):
         """Writes to ``out`` the table whose sequence b has ``lengths[b]`` rows; ``table`` is void from then on.
         Lengths of 0 end a batch, or some of its sequences: what they hold is given back, however long they are."""
-        rc = _ext.resize(self._core, self._counts(), table, lengths, out, stream)
+        if self._left is not None:
+            self._settle()
+        rc = _ext.resize(self._core, self._refs, table, lengths, out, stream)
         if rc:
             raise MLAError(rc, "mla_cache_resize")
         return out
@@ -352,7 +354,9 @@ class MLACachePool:
         """Ends one hold on each of ``pages`` (-1 is skipped): of a table, the entries that are in use, and only those.
         What lies behind them in a buffer that was used before are pages too, and holds of others may end; where the
         host does not know how many are in use, ``resize`` to lengths of 0 ends them."""
-        rc = _ext.free(self._core, self._counts(), pages, stream)
+        if self._left is not None:
+            self._settle()
+        rc = _ext.free(self._core, self._refs, pages, stream)
         if rc:
             raise MLAError(rc, "mla_cache_free")
 
@@ -370,8 +374,9 @@ class MLACachePool:
         rc, indices, refs, live = _ext.compact(self._core, self._refs, kv_indices, indices, refs, live, stream)
         if rc:
             raise MLAError(rc, "mla_cache_compact")
-        apart = refs.data_ptr() != self._refs.data_ptr() and not self._refs.is_inference()
-        self._left = self._refs._version if apart else None
+        own = self._refs
+        apart = refs is not own and refs.data_ptr() != own.data_ptr() and not own.is_inference()
+        self._left = own._version if apart else None
         return indices, refs, live
 
     def poll_error(self, stream=None) -> int:
