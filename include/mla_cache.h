@@ -119,12 +119,17 @@ typedef struct {
  * mla_cache_append -- norms, rotates and stores the tokens' key rows, and norms
  * and rotates their query heads into the layout the decode reads.
  *
- * Everything is computed in fp32 (angles exactly, modulo one turn, at any int32
- * position) and rounded once: queries and bf16 rows to bf16; fp8 rows to
- * e4m3(y / kv_scale) (the quotient rounded to fp32 first), saturating at 448 (NaN stays NaN); mxfp4 rows to e2m1
+ * Everything is computed in fp32 and rounded once: queries and bf16 rows to
+ * bf16; fp8 rows to e4m3(y / kv_scale) (the quotient rounded to fp32 first),
+ * saturating at 448 (NaN stays NaN, a zero keeps its sign); mxfp4 rows to e2m1
  * under the smallest power of two 2^e with max|y| <= 6 * 2^e per block of 32
  * (scale byte e + 127; 127 for a block of zeros; a block with an infinity or a
  * NaN gets scale byte 255 = NaN and codes 0).
+ *
+ * Angles are taken modulo one turn by an integer product: at any int32 position
+ * off by at most 2^-23 radians (their conversion to fp32) and 2^-52 of
+ * |position * inv_freq| (the plan's fp64 quotient, 2^-21 at the far end for a
+ * frequency of 1).
  *
  * rope NULL: no rotation (positions is not read).  norm NULL: no norms.
  * q_lat / q_pe may be the very columns of q_out they go to (in place); no

@@ -141,11 +141,12 @@ int mla_rope_plan(const double* inv_freq, const int32_t* axis_of_pair, int32_t n
     const int32_t a = axis_of_pair ? axis_of_pair[i] : 0;
     if (a < 0 || a >= num_axes) return MLA_ERR_INVALID_ARG;
     r.axis[i] = static_cast<uint8_t>(a);
-    // the fraction of a turn in [0, 1), as a multiple of 2^-64 (2^64 itself is 0 turns)
-    double f = std::fmod(inv_freq[i] / 6.283185307179586476925286766559, 1.0);
-    if (f < 0) f += 1.0;
+    // the fraction of a turn as a multiple of 2^-64 (2^64 itself is 0 turns); a negative
+    // one as that many less than 2^64 (1 less the fraction would round it to 2^-54)
+    const double f = std::fmod(std::fabs(inv_freq[i]) / 6.283185307179586476925286766559, 1.0);
     const double u = std::nearbyint(std::ldexp(f, 64));
-    r.turn[i] = u >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(u);
+    const uint64_t turn = u >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(u);
+    r.turn[i] = inv_freq[i] < 0 ? 0 - turn : turn;
   }
   r.num_axes = num_axes;
   r.interleaved = interleaved;

@@ -198,7 +198,9 @@ struct Turn {
 };
 // The turn count pos * inv_freq / 2 pi matters modulo 1 only: with inv_freq / 2 pi
 // in units of 2^-64 turns the 64-bit product wraps to exactly that, at any
-// position, and its top 32 bits leave an angle error below 2 pi * 2^-33.
+// position.  Its top 32 bits leave 2^-33 turns, their conversion to fp32 up to
+// 2^-26 turns (2^-23.3 radians), sincospi 2 ulp; the plan's own rounding of
+// inv_freq / 2 pi (2^-52.4 of it) counts as often as the position says.
 // Lane i finds pair i's angle; paired halves (i, i + 32) then fetch the two pairs
 // that their columns belong to.
 __device__ __forceinline__ Turn turn_of(const AppendParams& p, int t, int lane) {

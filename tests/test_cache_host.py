@@ -246,3 +246,14 @@ def test_extension_for_another_torch_is_refused(lib, tmp_path, monkeypatch):
     with pytest.raises(RuntimeError, match="build it again"):
         cache.load_library()
     assert cache._lib is None
+
+
+@pytest.mark.parametrize("freq", [1.0, 0.3, 1e-4, 3.7e-9, 1e-13, 100.0, 2 * math.pi * 0.75])
+def test_rope_plan_of_negative_frequencies(lib, freq):
+    """A pair that turns the other way turns by exactly the opposite angle, and a
+    small frequency keeps its precision: the quotient's rounding (2^-52 of it) and
+    half a unit."""
+    there, back = cache.MLARope(inv_freq=[freq] * 32).rope, cache.MLARope(inv_freq=[-freq] * 32).rope
+    assert (there.turn[3] + back.turn[3]) % 2 ** 64 == 0
+    turns = (freq / (2 * math.pi)) % 1.0
+    assert abs(there.turn[3] - turns * 2.0 ** 64) <= 2.0 ** 64 * 2.0 ** -52 * max(turns, freq / 6) + 1
