@@ -1,12 +1,13 @@
 // mla_cache_pages.cu -- pages of the latent cache copied, forked, resized, freed
 // and compacted (include/mla_cache.h).
 //
-// A call that hands out or moves pages has two parts: a cluster of CTAs decides
-// (prefix sums over the sequences and over the pages' counts), then a grid, or
-// the same cluster where there is little to do, carries it out (table entries,
-// counts, rows).  Ranks come from prefix sums, never from the order in which
-// threads arrive, so results are the same from run to run; the only atomics add
-// to counts.
+// A call that hands out or moves pages has two parts: CTAs decide (prefix sums
+// over the sequences and over the pages' counts), then a grid carries it out
+// (table entries, counts, rows).  Over few pages every CTA decides for itself, in
+// shared memory, and carries out its share in the same launch.  Ranks come from
+// prefix sums, never from the order in which threads arrive, so results are the
+// same from run to run.  Atomics add to counts, gather flags, and tell which CTA
+// has been the last to read counts that are rewritten in place.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -35,7 +36,10 @@ constexpr int64_t kClusterEntries = 32768;
 // ... and bytes of pages that may have to be copied: a fork of n bf16 sequences
 // of 64-row pages, with its free, takes 7.4 us against 8.8 at n = 8 (0.6 MB),
 // 9.5 against 9.2 at n = 16 and 32 against 12 at n = 256.  A resize copies a page
-// only where a fork's sequence is cut inside a shared one, so it may risk more.
+// only where a fork's sequence is cut inside a shared one.  n such cuts take 8.1 us
+// against 8.5 at n = 16, 14.3 against 9.1 at n = 64 and 26.9 against 10.5 at n = 200;
+// cuts that copy nothing, as most do, take 4.8 against 7.3, 5.0 against 7.8 and 5.5
+// against 8.8.  The border serves those: at n = 64 one call in 3 may copy.
 constexpr int64_t kClusterForkBytes = 1 << 20, kClusterResizeBytes = 16 << 20;
 // Table entries by a kernel of their own: 65,536 entries 11.1 us against 10.4 in
 // one with the rows, 262,144 entries 11.5 against 15.2.
@@ -657,8 +661,9 @@ __global__ void __launch_bounds__(256, kPartCtas) mla_table_apply_kernel(const _
     apply_copies(p, (blockIdx.x - (entry_ctas > 0 ? quarter + 1 : 0)) * 256 + threadIdx.x,
                  (gridDim.x - entry_ctas) * 256);
 }
-// Long tables apart from the rows: moving rows takes 128 registers a thread, a
-// quarter of the threads that a chain of dependent reads per entry wants.
+// Long tables apart from the rows: moving rows takes 80 registers a thread and 3
+// CTAs an SM, under half of the threads that a chain of dependent reads per entry
+// wants (32 registers here, 8 CTAs an SM).
 __global__ void __launch_bounds__(256) mla_table_entries_kernel(const __grid_constant__ TableParams p) {
   pdl_wait_primary();
   pdl_launch_dependents();
