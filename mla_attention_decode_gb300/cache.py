@@ -195,7 +195,9 @@ class MLACachePool:
     fp32 [1] (or one per layer) for fp8, e8m0 bytes [(layers,) rows, >= 18] for
     MXFP4 (columns of a wider tensor too, 16-byte aligned: the others are left
     alone).  ``refs``: int32, how many sequences hold each page (default: all
-    free).  A contiguous cache is one with pages of one row.
+    free; a table made elsewhere has its pages counted here before ``fork`` or
+    ``resize`` take it: a page that nobody holds is no page of a sequence).  A
+    contiguous cache is one with pages of one row.
 
     Calls that share a pool are ordered on the GPU (one stream, or events).
     Methods enqueue on ``stream`` (default: torch's current one) of the pool's
