@@ -38,21 +38,25 @@ extern "C" {
  * A contiguous cache of R rows is num_pages = R pages of one row.
  */
 typedef struct {
-  void* kv;                  /* device, 16-byte aligned; rows of 1152 / 576 / 288 bytes */
+  void* kv;                  /* device, 16-byte aligned; rows of 1152 / 576 / 288 / (fp8_row) 576 bytes */
   void* kv_scale;            /* bf16: NULL; fp8: fp32 (per layer, or one for all); mxfp4: uint8
-                                e8m0 [rows, scale_stride] per layer, 16-byte aligned */
+                                e8m0 [rows, scale_stride] per layer, 16-byte aligned; fp8_row: fp32
+                                [rows] per layer, scale_stride bytes apart, 16-byte aligned */
   int64_t kv_layer_bytes;    /* bytes from a layer's rows to the next layer's: a multiple of 16, at
                                 least the rows of one layer (ignored with one layer) */
   int64_t scale_layer_bytes; /* the same for kv_scale: fp8 a multiple of 4 (0: one scale for all
-                                layers); mxfp4 at least one layer's scales */
+                                layers); mxfp4 at least one layer's scales; fp8_row the same and a
+                                multiple of 4 */
   int32_t kv_dtype;          /* mla_kv_dtype */
   int32_t page_size;         /* rows per page: a power of two */
   int32_t num_pages;         /* num_pages * page_size must fit in int32 */
   int32_t num_layers;        /* >= 1 */
-  int32_t scale_stride;      /* mxfp4: bytes between scale rows, >= 18; otherwise 0 */
+  int32_t scale_stride;      /* mxfp4: bytes between scale rows, >= 18; fp8_row: between the rows' scales,
+                                a multiple of 4, >= 4; otherwise 0 */
   int32_t reserved;          /* 0 */
   int32_t scale_width;       /* mxfp4: bytes of each scale row that are this cache's, 18..scale_stride (0: all
-                                of them); the others are neither read nor written; otherwise 0 */
+                                of them); the others are neither read nor written; fp8_row: 4 (0: all of
+                                them move with a row); otherwise 0 */
   int32_t reserved2;         /* 0 */
 } mla_cache;
 
@@ -124,7 +128,10 @@ typedef struct {
  * saturating at 448 (NaN stays NaN, a zero keeps its sign); mxfp4 rows to e2m1
  * under the smallest power of two 2^e with max|y| <= 6 * 2^e per block of 32
  * (scale byte e + 127; 127 for a block of zeros; a block with an infinity or a
- * NaN gets scale byte 255 = NaN and codes 0).
+ * NaN gets scale byte 255 = NaN and codes 0); fp8_row rows to e4m3(y / s) (the
+ * quotient rounded to fp32 first) with s = max(fp32(max|y| / 448), 2^-64) stored
+ * as the row's scale, a zero keeping its sign (a row with an infinity or a NaN
+ * gets scale NaN and codes 0).
  *
  * Angles are taken modulo one turn by an integer product: at any int32 position
  * off by at most 2^-23 radians (their conversion to fp32) and 2^-52 of
@@ -143,7 +150,7 @@ MLA_API int mla_cache_append(const mla_cache* cache, const mla_rope* rope, const
 
 /*
  * mla_cache_gather -- rows of one layer as bf16: out[t, :] = bf16(the value of
- * row slots[t]; fp8: the code times kv_scale in fp32).  out: device bf16 [num_rows, 576], rows out_stride elements
+ * row slots[t]; fp8 and fp8_row: the code times the scale in fp32).  out: device bf16 [num_rows, 576], rows out_stride elements
  * apart (a multiple of 8, >= 576), 16-byte aligned.  Rows of out with slot -1
  * are left as they were; so are those with a slot outside the cache, which
  * set MLA_ERR_DEVICE_INDEX.  Slots may repeat.

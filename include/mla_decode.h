@@ -23,6 +23,10 @@
  *   MLA_KV_MXFP4     packed e2m1 [rows, 288] (element 2i = low nibble of byte i)
  *                    with one e8m0 byte per 32 elements, [rows, scale_stride],
  *                    scale_stride >= 18 (only the first 18 bytes are read).
+ *   MLA_KV_FP8_ROW   e4m3fn bytes [rows, 576] with one fp32 scale per row, scale_stride
+ *                    bytes apart (a multiple of 4, >= 4): row t is code_t * scale_t.
+ *                    The scales are finite, >= 0 and at most 2^120.  (The pages have
+ *                    no counterpart; mla_cache_append writes it.)
  *
  * Calling sequence: mla_decode_plan() (or mla_decode_plan_multi /
  * mla_decode_plan_paged) on the host for a batch layout (it reads only the
@@ -63,7 +67,8 @@ extern "C" {
 typedef enum {
   MLA_KV_BF16 = 0,
   MLA_KV_FP8_E4M3 = 1,
-  MLA_KV_MXFP4 = 2
+  MLA_KV_MXFP4 = 2,
+  MLA_KV_FP8_ROW = 4 /* (3 names no format) */
 } mla_kv_dtype;
 
 typedef enum {
@@ -80,7 +85,7 @@ typedef enum {
 
 /*
  * The work decomposition of one batch layout (split-K over the KV sequence).
- * With R = tile_tokens (64 rows for bf16 KV, 128 for e4m3 and e2m1 KV),
+ * With R = tile_tokens (64 rows for bf16 KV, 128 for the 8- and 4-bit formats),
  * sequence b with L_b = kv_indptr[b+1] - kv_indptr[b] rows and
  * T_b = ceil(L_b / R) row tiles is cut into
  *   S_b = L_b == 0 ? 1 : min(max_splits, ceil(L_b / chunk_tokens), T_b)
@@ -126,7 +131,7 @@ typedef struct {
   int32_t num_pages;      /* paged: pages in the cache tensor; 0 otherwise */
   int32_t unit_cost;      /* schedule 1: U, empty tile positions between consecutive sequences */
   int32_t q_len;          /* query tokens per sequence (0 or 1: one; see mla_decode_plan_multi) */
-  int32_t tokens_fused;   /* 2: a two-token e4m3 plan whose split kernel reads each cache row once
+  int32_t tokens_fused;   /* 2: a two-token e4m3 (fp8, fp8_row) plan whose split kernel reads each cache row once
                              for both tokens (see mla_decode_plan_multi); 0 otherwise */
   int32_t mx_scores;      /* mxfp4 only, set by the caller after planning (the planners write 0):
                              0: both tensor-core products read an e4m3 copy of each tile made
@@ -177,8 +182,10 @@ MLA_API size_t mla_decode_workspace_bytes(const mla_plan* plan);
  *              16-byte aligned; 32-byte aligned for mxfp4 (the 4-bit tensor-map
  *              form the block-scaled kernel reads).
  *   kv_scale   device: NULL for bf16; fp32[1] for fp8 (dequant = e4m3 * kv_scale[0]);
- *              uint8 e8m0 [plan->total_kv, scale_stride] for mxfp4 (16-byte aligned).
- *   scale_stride  mxfp4: bytes between scale rows, >= 18; otherwise 0.
+ *              uint8 e8m0 [plan->total_kv, scale_stride] for mxfp4 (16-byte aligned);
+ *              fp32 [plan->total_kv], scale_stride bytes apart, for fp8_row (4-byte aligned).
+ *   scale_stride  mxfp4: bytes between scale rows, >= 18; fp8_row: bytes between the rows'
+ *              scales, a multiple of 4, >= 4; otherwise 0.
  *   kv_indptr  device int32 [batch+1], equal to the host copy the plan was made from.
  *   qo_indptr  device int32 [batch+1]; only qo_indptr[b] (the query row of b) is read.
  *   out        device, bf16 [batch, 16, 512] row-major (written).  8-byte aligned.
@@ -234,7 +241,7 @@ MLA_API int mla_decode_poll_error(void* workspace, void* stream);
  * [kv_indptr[b], kv_indptr[b+1] - (q_len - 1 - i)) (none when that is not
  * positive: out = 0, lse = -inf).
  *
- * Two forms.  With e4m3 KV and q_len = 2 the plan is fused (tokens_fused = 2):
+ * Two forms.  With e4m3 KV (fp8, fp8_row) and q_len = 2 the plan is fused (tokens_fused = 2):
  * the rule applies to the sequences' full row ranges, one work unit serves both
  * tokens, and the split kernel reads each cache row once, masking token 0's
  * last row; partial slot of token i of unit s of sequence b is
@@ -289,7 +296,8 @@ MLA_API int mla_decode_plan_paged(const int32_t* kv_page_indptr_host, const int3
  * from mla_decode_plan_paged.  Arguments as for mla_decode_fwd, except
  *   kv_pages          device, the cache: num_pages * page_size rows, 16-byte aligned
  *                     (mxfp4 with pages of 64 rows or more: 32-byte aligned).
- *   kv_scale          fp8: fp32[1]; mxfp4: uint8 e8m0 [num_pages * page_size, scale_stride].
+ *   kv_scale          fp8: fp32[1]; mxfp4: uint8 e8m0 [num_pages * page_size, scale_stride];
+ *                     fp8_row: fp32 [num_pages * page_size], scale_stride bytes apart.
  *   kv_page_indptr    device int32 [batch+1], equal to the host copy the plan was made from.
  *   kv_indices        device int32 [kv_page_indptr[batch]], each in [0, num_pages).
  *   kv_last_page_len  device int32 [batch].

@@ -17,8 +17,8 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmla_decode.so")
 
-MLA_KV_BF16, MLA_KV_FP8_E4M3, MLA_KV_MXFP4 = 0, 1, 2
-KV_DTYPE_CODES = {"bf16": MLA_KV_BF16, "fp8": MLA_KV_FP8_E4M3, "mxfp4": MLA_KV_MXFP4}
+MLA_KV_BF16, MLA_KV_FP8_E4M3, MLA_KV_MXFP4, MLA_KV_FP8_ROW = 0, 1, 2, 4
+KV_DTYPE_CODES = {"bf16": MLA_KV_BF16, "fp8": MLA_KV_FP8_E4M3, "mxfp4": MLA_KV_MXFP4, "fp8_row": MLA_KV_FP8_ROW}
 MLA_OK = 0
 MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED, MLA_ERR_WORKSPACE_TOO_SMALL, MLA_ERR_CUDA = 1, 2, 3, 4
 MLA_ERR_DEVICE_INDEX, MLA_ERR_DEVICE_TIMEOUT, MLA_ERR_NO_DEVICE = 5, 6, 7
@@ -231,15 +231,29 @@ def mla_decode_fwd_static(q, kv, kv_scale, kv_indptr, qo_indptr, out, lse, plan:
         raise MLAError(rc, "mla_decode_fwd_static")
 
 
+def _scale_stride(kv_dtype: int, kv_scale) -> int:
+    """Bytes between the rows' scales, where rows have scales of their own."""
+    if kv_scale is None:
+        return 0
+    if kv_dtype == MLA_KV_MXFP4:
+        return int(kv_scale.stride(0))
+    if kv_dtype == MLA_KV_FP8_ROW:
+        if kv_scale.dtype != torch.float32 or kv_scale.dim() != 1:
+            raise ValueError(f"kv_scale is fp32 [rows]: got {kv_scale.dtype} {tuple(kv_scale.shape)}")
+        return 4 * int(kv_scale.stride(0)) if kv_scale.numel() > 1 else 4  # (one scale has no stride)
+    return 0
+
+
 class MLADecoder:
     """Plan + workspace for one batch layout; call it with device tensors.
 
     The workspace is allocated once here (torch device memory) and zeroed; the
     library itself never allocates.  ``q_len > 1``: that many query tokens per
     sequence (rows ``qo_indptr[b] + i``, output rows ``b * q_len + i``); e4m3 KV
-    with ``q_len == 2`` gets the single-pass plan (``plan.tokens_fused == 2``).
+    ("fp8", "fp8_row") with ``q_len == 2`` gets the single-pass plan (``plan.tokens_fused == 2``).
     ``mx_block_scaled``: MXFP4 scores from block-scaled MMAs on the e2m1 tile
-    (``plan.mx_scores = 1``) instead of the e4m3 copy."""
+    (``plan.mx_scores = 1``) instead of the e4m3 copy.  ``kv_scale`` of a call: fp32
+    [1] ("fp8"), e8m0 bytes [rows, >= 18] ("mxfp4") or fp32 [rows] ("fp8_row")."""
 
     def __init__(self, kv_indptr_host, kv_dtype, device="cuda", num_sms: int = 0, num_splits: int = 0,
                  q_len: int = 1, mx_block_scaled: bool = False):
@@ -260,7 +274,7 @@ class MLADecoder:
             out = torch.empty(batch, 16, 512, dtype=torch.bfloat16, device=self.workspace.device)
         if lse is None:
             lse = torch.empty(batch, 16, dtype=torch.float32, device=self.workspace.device)
-        scale_stride = int(kv_scale.stride(0)) if (self.kv_dtype == MLA_KV_MXFP4 and kv_scale is not None) else 0
+        scale_stride = _scale_stride(self.kv_dtype, kv_scale)
         mla_decode_fwd(q, kv, kv_scale, kv_indptr, qo_indptr, out, lse, self.plan, self.workspace,
                        sm_scale=sm_scale, scale_stride=scale_stride, stream=stream)
         return out, lse
@@ -289,7 +303,7 @@ class PagedMLADecoder:
             out = torch.empty(batch, 16, 512, dtype=torch.bfloat16, device=self.workspace.device)
         if lse is None:
             lse = torch.empty(batch, 16, dtype=torch.float32, device=self.workspace.device)
-        scale_stride = int(kv_scale.stride(0)) if (self.kv_dtype == MLA_KV_MXFP4 and kv_scale is not None) else 0
+        scale_stride = _scale_stride(self.kv_dtype, kv_scale)
         mla_decode_fwd_paged(q, kv_pages, kv_scale, kv_page_indptr, kv_indices, kv_last_page_len, qo_indptr, out,
                              lse, self.plan, self.workspace, sm_scale=sm_scale, scale_stride=scale_stride,
                              stream=stream)

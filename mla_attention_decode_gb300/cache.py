@@ -31,11 +31,11 @@ import threading
 import torch
 
 from . import binding
-from .binding import MLA_ERR_INVALID_ARG, MLA_KV_BF16, MLA_KV_FP8_E4M3, MLA_KV_MXFP4, MLA_OK, MLAError
+from .binding import MLA_ERR_INVALID_ARG, MLA_KV_BF16, MLA_KV_FP8_E4M3, MLA_KV_FP8_ROW, MLA_KV_MXFP4, MLA_OK, MLAError
 
 MLA_ERR_OUT_OF_PAGES = 8
 PAIRS = 32
-ROW_WIDTH = {MLA_KV_BF16: 576, MLA_KV_FP8_E4M3: 576, MLA_KV_MXFP4: 288}
+ROW_WIDTH = {MLA_KV_BF16: 576, MLA_KV_FP8_E4M3: 576, MLA_KV_MXFP4: 288, MLA_KV_FP8_ROW: 576}
 _PARTS = ("kv_lat", "kv_pe", "q_lat", "q_pe")
 _PART_COLUMNS = (512, 64, 512, 64)
 
@@ -192,7 +192,8 @@ class MLACachePool:
 
     ``kv``: [rows, width] or [layers, rows, width] (rows = pages * page_size):
     bf16 [.., 576], e4m3 bytes [.., 576] or packed e2m1 [.., 288]; ``kv_scale``:
-    fp32 [1] (or one per layer) for fp8, e8m0 bytes [(layers,) rows, >= 18] for
+    fp32 [1] (or one per layer) for fp8, fp32 [(layers,) rows] for fp8_row (e4m3
+    bytes with a scale per row, which ``append`` finds), e8m0 bytes [(layers,) rows, >= 18] for
     MXFP4 (columns of a wider tensor too, 16-byte aligned: the others are left
     alone).  ``refs``: int32, how many sequences hold each page (default: all
     free; a table made elsewhere has its pages counted here before ``fork`` or
@@ -215,7 +216,7 @@ class MLACachePool:
         layered = kv.dim() == 3
         width, want = ROW_WIDTH[self.kv_dtype], (torch.bfloat16,)
         if self.kv_dtype != MLA_KV_BF16:
-            want = (torch.uint8, torch.float8_e4m3fn) if self.kv_dtype == MLA_KV_FP8_E4M3 else (torch.uint8,)
+            want = (torch.uint8,) if self.kv_dtype == MLA_KV_MXFP4 else (torch.uint8, torch.float8_e4m3fn)
         if kv.dtype not in want or kv.shape[-1] != width or kv.stride(-1) != 1 or kv.stride(-2) != width:
             raise ValueError(f"kv is {want[0]} [.., {width}] with consecutive rows: got {kv.dtype} {tuple(kv.shape)}")
         page_size, rows = int(page_size), kv.shape[-2]
@@ -235,6 +236,14 @@ class MLACachePool:
                 if kv_scale.dtype != torch.float32 or kv_scale.numel() not in (1, c.num_layers) or not kv_scale.is_contiguous():
                     raise ValueError("kv_scale is fp32, one or one per layer")
                 c.scale_layer_bytes = 4 if kv_scale.numel() > 1 else 0
+            elif self.kv_dtype == MLA_KV_FP8_ROW:
+                if kv_scale.dtype != torch.float32 or kv_scale.shape != kv.shape[:-1]:
+                    raise ValueError("kv_scale is fp32 [.., rows]")
+                c.scale_stride = 4 * kv_scale.stride(-1) if rows > 1 else 4
+                if c.scale_stride > 4:  # every so many columns of a wider tensor
+                    c.scale_width = 4
+                if layered and kv.shape[0] > 1:
+                    c.scale_layer_bytes = 4 * kv_scale.stride(0)
             else:
                 if (kv_scale.dtype != torch.uint8 or kv_scale.shape[:-1] != kv.shape[:-1] or kv_scale.shape[-1] < 18
                         or kv_scale.stride(-1) != 1):
@@ -271,6 +280,9 @@ class MLACachePool:
         scale = None
         if code == MLA_KV_FP8_E4M3:
             scale = torch.full((1,), float(kv_scale), dtype=torch.float32, device=device)
+        elif code == MLA_KV_FP8_ROW:
+            # layers 16-byte aligned: whole runs of 4 rows
+            scale = torch.ones(num_layers, -(-rows // 4) * 4, dtype=torch.float32, device=device)[:, :rows]
         elif code == MLA_KV_MXFP4:
             # layers 16-byte aligned, as the decode takes them: whole runs of 8 rows
             scale = torch.full((num_layers, -(-rows // 8) * 8, 18), 127, dtype=torch.uint8, device=device)[:, :rows]

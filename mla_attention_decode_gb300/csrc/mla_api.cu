@@ -20,6 +20,12 @@ using mla::kVDim;
 
 constexpr int32_t kNoCap = 1 << 30;
 
+bool known_dtype(int32_t kv_dtype) {
+  return kv_dtype == MLA_KV_BF16 || kv_dtype == MLA_KV_FP8_E4M3 || kv_dtype == MLA_KV_MXFP4 || kv_dtype == MLA_KV_FP8_ROW;
+}
+// Rows of e4m3 codes, with one scale for all or one each.
+bool is_e4m3(int32_t kv_dtype) { return kv_dtype == MLA_KV_FP8_E4M3 || kv_dtype == MLA_KV_FP8_ROW; }
+
 // KV rows per pipeline tile of each kernel: 64 (bf16, warp-level MMA) or 128
 // (e4m3 and e2m1, one tcgen05 M=128 block).  Splits end on tile boundaries.
 int tile_rows(int kv_dtype) { return kv_dtype == MLA_KV_BF16 ? 64 : 128; }
@@ -28,6 +34,7 @@ int rows_bytes(int kv_dtype) {
   switch (kv_dtype) {
     case MLA_KV_BF16: return 1152;
     case MLA_KV_FP8_E4M3: return 576;
+    case MLA_KV_FP8_ROW: return 576 + 4;
     default: return 288 + 18;
   }
 }
@@ -350,7 +357,7 @@ uint64_t* g_trace = nullptr;
 #endif
 int64_t late_tiles_for(int32_t kv_dtype, bool fused) {
   if (kv_dtype == MLA_KV_BF16) return 0;
-  return (kv_dtype == MLA_KV_FP8_E4M3 && !fused) ? MLA_LATE_TILES_E4M3 : MLA_LATE_TILES_OTHER;
+  return (is_e4m3(kv_dtype) && !fused) ? MLA_LATE_TILES_E4M3 : MLA_LATE_TILES_OTHER;
 }
 
 // prep_rows: output rows (the query-preparation grid); fused: the two-token e4m3 form
@@ -460,7 +467,7 @@ int mla_decode_plan(const int32_t* kv_indptr_host, int32_t batch, int32_t kv_dty
                     int32_t num_splits, mla_plan* plan) {
   if (!kv_indptr_host || !plan) return MLA_ERR_INVALID_ARG;
   if (batch < 0 || batch > MLA_MAX_BATCH) return MLA_ERR_INVALID_ARG;
-  if (kv_dtype < MLA_KV_BF16 || kv_dtype > MLA_KV_MXFP4) return MLA_ERR_UNSUPPORTED;
+  if (!known_dtype(kv_dtype)) return MLA_ERR_UNSUPPORTED;
   if (num_splits < 0) return MLA_ERR_INVALID_ARG;
   if (kv_indptr_host[0] < 0) return MLA_ERR_INVALID_ARG;
   std::vector<int64_t> lens(static_cast<size_t>(batch));
@@ -479,13 +486,13 @@ int mla_decode_plan_multi(const int32_t* kv_indptr_host, int32_t num_seqs, int32
   if (!kv_indptr_host || !plan) return MLA_ERR_INVALID_ARG;
   if (q_len < 1 || q_len > 16) return MLA_ERR_UNSUPPORTED;
   if (num_seqs < 0 || (int64_t)num_seqs * q_len > MLA_MAX_BATCH) return MLA_ERR_INVALID_ARG;
-  if (kv_dtype < MLA_KV_BF16 || kv_dtype > MLA_KV_MXFP4) return MLA_ERR_UNSUPPORTED;
+  if (!known_dtype(kv_dtype)) return MLA_ERR_UNSUPPORTED;
   if (num_splits < 0) return MLA_ERR_INVALID_ARG;
   if (kv_indptr_host[0] < 0) return MLA_ERR_INVALID_ARG;
   // e4m3, two tokens: one unit list over the sequences' rows serves both
   // tokens (the split kernel reads each row once); otherwise one entry per
   // token over the rows up to its own entry
-  const bool fused = q_len == 2 && kv_dtype == MLA_KV_FP8_E4M3;
+  const bool fused = q_len == 2 && is_e4m3(kv_dtype);
   std::vector<int64_t> lens(static_cast<size_t>(num_seqs) * (fused ? 1 : q_len));
   for (int32_t b = 0; b < num_seqs; ++b) {
     const int64_t L = (int64_t)kv_indptr_host[b + 1] - kv_indptr_host[b];
@@ -519,7 +526,7 @@ int mla_decode_plan_paged(const int32_t* kv_page_indptr_host, const int32_t* kv_
                           int32_t num_splits, mla_plan* plan) {
   if (!kv_page_indptr_host || !plan || (batch > 0 && !kv_last_page_len_host)) return MLA_ERR_INVALID_ARG;
   if (batch < 0 || batch > MLA_MAX_BATCH || num_pages < 0 || num_splits < 0) return MLA_ERR_INVALID_ARG;
-  if (kv_dtype < MLA_KV_BF16 || kv_dtype > MLA_KV_MXFP4) return MLA_ERR_UNSUPPORTED;
+  if (!known_dtype(kv_dtype)) return MLA_ERR_UNSUPPORTED;
   if (page_size < 1 || page_size > (1 << 20) || (page_size & (page_size - 1)) != 0) return MLA_ERR_UNSUPPORTED;
   if (kv_page_indptr_host[0] < 0) return MLA_ERR_INVALID_ARG;
   if ((int64_t)kv_page_indptr_host[batch] * page_size > INT32_MAX || (int64_t)num_pages * page_size > INT32_MAX)
@@ -582,7 +589,7 @@ int prepare(const void* q, const void* kv, const void* kv_scale, int32_t scale_s
     while ((1 << page_shift) < P) ++page_shift;
     cache_rows = plan->num_pages * P;
   }
-  if (plan->kv_dtype < MLA_KV_BF16 || plan->kv_dtype > MLA_KV_MXFP4) return MLA_ERR_UNSUPPORTED;
+  if (!known_dtype(plan->kv_dtype)) return MLA_ERR_UNSUPPORTED;
   if (plan->batch < 0 || plan->num_work < 0 || plan->grid < 0 || plan->chunk_tokens <= 0 || plan->max_splits <= 0)
     return MLA_ERR_INVALID_ARG;
   if (plan->batch == 0 || plan->num_work == 0) {
@@ -597,13 +604,16 @@ int prepare(const void* q, const void* kv, const void* kv_scale, int32_t scale_s
   if (plan->kv_dtype == MLA_KV_FP8_E4M3 && (!kv_scale || !aligned(kv_scale, 4))) return MLA_ERR_INVALID_ARG;
   if (plan->kv_dtype == MLA_KV_MXFP4 && (!kv_scale || !aligned(kv_scale, 16) || scale_stride < MLA_MX_SCALES_PER_ROW))
     return MLA_ERR_INVALID_ARG;
+  if (plan->kv_dtype == MLA_KV_FP8_ROW &&
+      (!kv_scale || !aligned(kv_scale, 4) || scale_stride < 4 || scale_stride % 4 != 0))
+    return MLA_ERR_INVALID_ARG;
   const mla::WsLayout w = mla::ws_layout(plan->batch, plan->num_work);
   if (workspace_bytes < w.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p->q = static_cast<const uint8_t*>(q);
   p->kv = static_cast<const uint8_t*>(kv);
   p->kv_scale = kv_scale;
-  p->scale_stride = plan->kv_dtype == MLA_KV_MXFP4 ? scale_stride : 0;
+  p->scale_stride = plan->kv_dtype == MLA_KV_MXFP4 || plan->kv_dtype == MLA_KV_FP8_ROW ? scale_stride : 0;
   p->kv_indptr = kv_indptr;
   p->qo_indptr = qo_indptr;
   p->kv_indices = paged ? paged->kv_indices : nullptr;
@@ -644,7 +654,7 @@ int prepare(const void* q, const void* kv, const void* kv_scale, int32_t scale_s
     if (r < -1 || r >= plan->total_kv) return MLA_ERR_INVALID_ARG;  // a row of the cache, or none
     p->first_row[c] = r;
   }
-  if (plan->tokens_fused != 0 && (plan->tokens_fused != 2 || plan->kv_dtype != MLA_KV_FP8_E4M3 ||
+  if (plan->tokens_fused != 0 && (plan->tokens_fused != 2 || !is_e4m3(plan->kv_dtype) ||
                                   plan->q_len != 2 || plan->num_work % 2 != 0))
     return MLA_ERR_INVALID_ARG;
   const int32_t entries = plan->batch / p->tok;  // sequences in the unit list
@@ -664,7 +674,7 @@ int prepare(const void* q, const void* kv, const void* kv_scale, int32_t scale_s
         C + (int64_t)p->late_ctas * plan->late_tiles > INT32_MAX)
       return MLA_ERR_INVALID_ARG;
   }
-  if (plan->kv_dtype == MLA_KV_FP8_E4M3) {
+  if (is_e4m3(plan->kv_dtype)) {
     if (!encode_kv_map_tc(&p->tmap_kv64, kv, cache_rows, 128)) return MLA_ERR_CUDA;
     if (paged && page_shift == 6) {
       // 64-row pages: a tile is two 64-row boxes
@@ -702,7 +712,7 @@ int prepare(const void* q, const void* kv, const void* kv_scale, int32_t scale_s
   return MLA_OK;
 }
 
-// The split stage: for e4m3 and MXFP4 KV the query preparation, then the split
+// The split stage: for 8- and 4-bit KV the query preparation, then the split
 // kernel (which overlaps its set-up with the preparation).
 int launch_split_stage(const mla::Stage1Params& p, int kv_dtype, cudaStream_t s) {
   cudaError_t e;
@@ -711,6 +721,10 @@ int launch_split_stage(const mla::Stage1Params& p, int kv_dtype, cudaStream_t s)
     case MLA_KV_FP8_E4M3:
       e = mla::launch_prep_q(p, false, s);
       if (e == cudaSuccess) e = mla::launch_stage1_fp8(p, s);
+      break;
+    case MLA_KV_FP8_ROW:
+      e = mla::launch_prep_q(p, true, s);  // no scale of the whole tensor
+      if (e == cudaSuccess) e = mla::launch_stage1_fp8_row(p, s);
       break;
     default:
       e = mla::launch_prep_q(p, true, s);
@@ -841,7 +855,7 @@ const char* mla_status_string(int status) {
   }
 }
 
-const char* mla_decode_version(void) { return "0.4.0"; }
+const char* mla_decode_version(void) { return "0.5.0"; }
 
 int mla_decode_set_trace(uint64_t* buffer) {
 #if defined(MLA_TRACE) && MLA_TRACE

@@ -17,7 +17,8 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 int check_cache(const mla_cache* c) {
   if (!c) return MLA_ERR_INVALID_ARG;
-  if (c->kv_dtype < MLA_KV_BF16 || c->kv_dtype > MLA_KV_MXFP4) return MLA_ERR_UNSUPPORTED;
+  if ((c->kv_dtype < MLA_KV_BF16 || c->kv_dtype > MLA_KV_MXFP4) && c->kv_dtype != MLA_KV_FP8_ROW)
+    return MLA_ERR_UNSUPPORTED;
   if (c->page_size < 1 || c->page_size > (1 << 20) || (c->page_size & (c->page_size - 1)) != 0)
     return MLA_ERR_UNSUPPORTED;
   if (c->num_pages < 0 || c->num_layers < 1 || c->reserved != 0 || c->reserved2 != 0) return MLA_ERR_INVALID_ARG;
@@ -27,8 +28,8 @@ int check_cache(const mla_cache* c) {
   if (c->num_layers > 1 &&
       (c->kv_layer_bytes % 16 != 0 || c->kv_layer_bytes < rows * mla::cache_row_bytes(c->kv_dtype)))
     return MLA_ERR_INVALID_ARG;
-  if (c->scale_width != 0 && (c->kv_dtype != MLA_KV_MXFP4 || c->scale_width < MLA_MX_SCALES_PER_ROW ||
-                              c->scale_width > c->scale_stride))
+  if (c->scale_width != 0 && (!mla::row_has_scale(c->kv_dtype) || c->scale_width > c->scale_stride ||
+                              (c->kv_dtype == MLA_KV_MXFP4 ? c->scale_width < MLA_MX_SCALES_PER_ROW : c->scale_width != 4)))
     return MLA_ERR_INVALID_ARG;
   if (c->kv_dtype == MLA_KV_FP8_E4M3) {
     if (!c->kv_scale || !aligned(c->kv_scale, 4)) return MLA_ERR_INVALID_ARG;
@@ -37,6 +38,11 @@ int check_cache(const mla_cache* c) {
     if ((rows > 0 && !c->kv_scale) || !aligned(c->kv_scale, 16) || c->scale_stride < MLA_MX_SCALES_PER_ROW)
       return MLA_ERR_INVALID_ARG;
     if (c->num_layers > 1 && c->scale_layer_bytes < rows * c->scale_stride) return MLA_ERR_INVALID_ARG;
+  } else if (c->kv_dtype == MLA_KV_FP8_ROW) {
+    if ((rows > 0 && !c->kv_scale) || !aligned(c->kv_scale, 16) || c->scale_stride < 4 || c->scale_stride % 4 != 0)
+      return MLA_ERR_INVALID_ARG;
+    if (c->num_layers > 1 && (c->scale_layer_bytes < rows * c->scale_stride || c->scale_layer_bytes % 4 != 0))
+      return MLA_ERR_INVALID_ARG;
   }
   return MLA_OK;
 }
@@ -48,7 +54,7 @@ mla::LayerRows layer_rows(const mla_cache* c, int32_t layer) {
   r.scale = c->kv_dtype == MLA_KV_BF16
                 ? nullptr
                 : static_cast<void*>(static_cast<uint8_t*>(c->kv_scale) + (layer ? layer * c->scale_layer_bytes : 0));
-  r.scale_stride = c->kv_dtype == MLA_KV_MXFP4 ? c->scale_stride : 0;
+  r.scale_stride = mla::row_has_scale(c->kv_dtype) ? c->scale_stride : 0;
   r.rows = c->num_pages * c->page_size;
   return r;
 }
@@ -71,7 +77,7 @@ mla::PageBytes page_bytes(const mla_cache* c, int32_t rows_moved) {
   b.num_pages = c->num_pages;
   b.num_layers = c->num_layers;
   b.scale_unit = 16;
-  if (c->kv_dtype == MLA_KV_MXFP4) {
+  if (mla::row_has_scale(c->kv_dtype)) {
     const bool whole = c->scale_width == 0 || c->scale_width == c->scale_stride;
     (whole ? b.scale : b.scale_cols) = static_cast<uint8_t*>(c->kv_scale);
     b.scale_layer = c->num_layers > 1 ? c->scale_layer_bytes : 0;

@@ -12,13 +12,15 @@ namespace mla {
 constexpr int kQueryHeads = MLA_NUM_HEADS, kLat = MLA_V_DIM, kPe = MLA_PE_DIM, kRow = MLA_QK_DIM, kPairs = MLA_PE_PAIRS;
 
 inline int cache_row_bytes(int kv_dtype) {
-  return kv_dtype == MLA_KV_BF16 ? kRow * 2 : (kv_dtype == MLA_KV_FP8_E4M3 ? kRow : kRow / 2);
+  return kv_dtype == MLA_KV_BF16 ? kRow * 2 : (kv_dtype == MLA_KV_MXFP4 ? kRow / 2 : kRow);
 }
+// Formats whose rows have scales of their own, which move with them.
+inline bool row_has_scale(int kv_dtype) { return kv_dtype == MLA_KV_MXFP4 || kv_dtype == MLA_KV_FP8_ROW; }
 
 // One layer of a cache as the row kernels see it.
 struct LayerRows {
   uint8_t* kv;
-  void* scale;           // fp8: fp32[1]; mxfp4: e8m0 [rows, scale_stride]
+  void* scale;           // fp8: fp32[1]; mxfp4: e8m0 [rows, scale_stride]; fp8_row: fp32 scale_stride bytes apart
   int32_t scale_stride;
   int32_t rows;          // num_pages * page_size
 };
@@ -55,8 +57,8 @@ struct SlotsParams {
 // of the call).
 struct PageBytes {
   uint8_t* kv;
-  uint8_t* scale;        // mxfp4 whose scale rows fill their stride, else null
-  uint8_t* scale_cols;   // mxfp4 whose scale rows are scale_width of scale_stride bytes, else null
+  uint8_t* scale;        // scale rows (mxfp4, fp8_row) that fill their stride, else null
+  uint8_t* scale_cols;   // scale rows of scale_width of scale_stride bytes, else null
   int64_t kv_layer, scale_layer;
   int32_t row_bytes, scale_stride, scale_width;
   int32_t page_size, page_shift, num_pages, num_layers;

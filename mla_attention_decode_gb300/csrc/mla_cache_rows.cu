@@ -271,7 +271,7 @@ __device__ __forceinline__ void by_kind(bool norm, int turn, F f) {
 }
 
 // One key row into row `slot` of the cache, in its format (sc: the scale of an
-// e4m3 cache).
+// e4m3 cache that has one for all).
 template <int kDtype>
 __device__ __forceinline__ void store_row(const AppendParams& p, int32_t slot, float sc, const float (&lat)[2][8],
                                           float2 pe, int lane) {
@@ -280,7 +280,31 @@ __device__ __forceinline__ void store_row(const AppendParams& p, int32_t slot, f
 #pragma unroll
     for (int h = 0; h < 2; ++h) reinterpret_cast<uint4*>(dst)[32 * h + lane] = pack_bf16x8(lat[h]);
     reinterpret_cast<uint32_t*>(dst + 2 * kLat)[lane] = pack_bf16x2(pe.x, pe.y);
-  } else if (kDtype == MLA_KV_FP8_E4M3) {
+  } else if (kDtype == MLA_KV_FP8_E4M3 || kDtype == MLA_KV_FP8_ROW) {
+    float top_y = 0.f;
+    if (kDtype == MLA_KV_FP8_ROW) {
+      // the row's scale: its largest magnitude over the lanes becomes 448, e4m3's
+      // largest value.  Not below 2^-64, so that the quotients and the decode's
+      // product of a score and a scale stay in range (a row of zeros has that scale).
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top_y = max_nan(top_y, fabsf(lat[h][j]));
+      top_y = max_nan(top_y, max_nan(fabsf(pe.x), fabsf(pe.y)));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top_y = max_nan(top_y, __shfl_xor_sync(kFull, top_y, o));
+      sc = fmaxf(__fdiv_rn(top_y, 448.f), 0x1p-64f);
+      const bool finite = top_y < INFINITY;
+      if (lane == 0)
+        *reinterpret_cast<float*>(static_cast<uint8_t*>(p.cache.scale) + (int64_t)slot * p.cache.scale_stride) =
+            finite ? sc : __int_as_float(0x7fc00000);
+      if (!finite) {  // an infinity or a NaN in the row: codes 0 under a scale that is NaN
+        uint8_t* dst = p.cache.kv + (int64_t)slot * kRow;
+        reinterpret_cast<uint2*>(dst)[lane] = reinterpret_cast<uint2*>(dst)[32 + lane] = make_uint2(0u, 0u);
+        reinterpret_cast<uint16_t*>(dst + kLat)[lane] = 0;
+        return;
+      }
+    }
     // e4m3 of the rounded quotient y / scale (not of a product with the reciprocal,
     // which lands on the other side of some borders).  Markstein's correction
     // (P. W. Markstein, IBM J. Res. Dev. 34, 1990): with r the rounded reciprocal of
@@ -474,17 +498,19 @@ __global__ void __launch_bounds__(kGatherThreads) mla_gather_kernel(const __grid
       slot[i] = -1;
     }
   }
-  uint4 raw[kGatherDeep];  // the row's 16, 8 or 4 bytes, and the block's scale byte
+  uint4 raw[kGatherDeep];  // the row's 16, 8 or 4 bytes, and the block's scale byte or the row's scale
 #pragma unroll
   for (int i = 0; i < kGatherDeep; ++i) {
     if (slot[i] < 0) continue;
     const int64_t s = slot[i];
     if (kDtype == MLA_KV_BF16) {
       raw[i] = __ldcs(reinterpret_cast<const uint4*>(p.cache.kv + s * (2 * kRow)) + c);
-    } else if (kDtype == MLA_KV_FP8_E4M3) {
+    } else if (kDtype == MLA_KV_FP8_E4M3 || kDtype == MLA_KV_FP8_ROW) {
       const uint2 r = __ldcs(reinterpret_cast<const uint2*>(p.cache.kv + s * kRow) + c);
       raw[i].x = r.x;
       raw[i].y = r.y;
+      if (kDtype == MLA_KV_FP8_ROW)
+        raw[i].z = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.cache.scale) + s * p.cache.scale_stride);
     } else {
       raw[i].x = __ldcs(reinterpret_cast<const uint32_t*>(p.cache.kv + s * (kRow / 2)) + c);
       raw[i].y = static_cast<const uint8_t*>(p.cache.scale)[s * p.cache.scale_stride + (c >> 2)];
@@ -494,14 +520,15 @@ __global__ void __launch_bounds__(kGatherThreads) mla_gather_kernel(const __grid
 #pragma unroll
   for (int i = 0; i < kGatherDeep; ++i) {
     if (slot[i] < 0) continue;
-    if (kDtype == MLA_KV_FP8_E4M3) {
+    if (kDtype == MLA_KV_FP8_E4M3 || kDtype == MLA_KV_FP8_ROW) {
+      const float sc = kDtype == MLA_KV_FP8_ROW ? __uint_as_float(raw[i].z) : tensor_scale;
       const uint32_t w[4] = {raw[i].x & 0xffffu, raw[i].x >> 16, raw[i].y & 0xffffu, raw[i].y >> 16};
       float x[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 f = __half22float2(e4m3x2_to_h2(w[j]));
-        x[2 * j] = f.x * tensor_scale;
-        x[2 * j + 1] = f.y * tensor_scale;
+        x[2 * j] = f.x * sc;
+        x[2 * j + 1] = f.y * sc;
       }
       raw[i] = pack_bf16x8(x);
     } else if (kDtype == MLA_KV_MXFP4) {
@@ -593,6 +620,7 @@ cudaError_t launch_append(const AppendParams& p, int kv_dtype, cudaStream_t s) {
   switch (kv_dtype) {
     case MLA_KV_BF16: return launch_append_to<MLA_KV_BF16>(p, s);
     case MLA_KV_FP8_E4M3: return launch_append_to<MLA_KV_FP8_E4M3>(p, s);
+    case MLA_KV_FP8_ROW: return launch_append_to<MLA_KV_FP8_ROW>(p, s);
     default: return launch_append_to<MLA_KV_MXFP4>(p, s);
   }
 }
@@ -604,6 +632,7 @@ cudaError_t launch_gather(const GatherParams& p, int kv_dtype, cudaStream_t s) {
   switch (kv_dtype) {
     case MLA_KV_BF16: return launch_chained(mla_gather_kernel<MLA_KV_BF16>, grid, kGatherThreads, s, p);
     case MLA_KV_FP8_E4M3: return launch_chained(mla_gather_kernel<MLA_KV_FP8_E4M3>, grid, kGatherThreads, s, p);
+    case MLA_KV_FP8_ROW: return launch_chained(mla_gather_kernel<MLA_KV_FP8_ROW>, grid, kGatherThreads, s, p);
     default: return launch_chained(mla_gather_kernel<MLA_KV_MXFP4>, grid, kGatherThreads, s, p);
   }
 }

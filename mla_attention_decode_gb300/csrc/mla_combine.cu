@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(128) mla_combine_kernel(const __grid_constant_
     float ws = 0.f;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      if (mpart[w] == -INFINITY) continue;  // no non-empty split in this warp
+      if (mpart[w] == -INFINITY && wpart[w] == 0.f) continue;  // no non-empty split in this warp
       const float c = __expf(mpart[w] - M);
       const float4 y = part[w][lane];
       t.x += c * y.x;
@@ -89,10 +89,10 @@ __global__ void __launch_bounds__(128) mla_combine_kernel(const __grid_constant_
       t.w += c * y.w;
       ws += c * wpart[w];
     }
-    const float inv = ws > 0.f ? 1.f / ws : 0.f;
+    const float inv = ws != 0.f ? 1.f / ws : 0.f;  // (a sum that is NaN stays it)
     uint16_t* out = p.out + ((size_t)b * kHeads + h) * kVDim + f;
     *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(t.x * inv, t.y * inv), pack_bf16x2(t.z * inv, t.w * inv));
-    if (quarter == 0 && lane == 0 && p.lse) p.lse[b * kHeads + h] = ws > 0.f ? M + logf(ws) : -INFINITY;
+    if (quarter == 0 && lane == 0 && p.lse) p.lse[b * kHeads + h] = ws != 0.f ? M + logf(ws) : -INFINITY;
   }
 }
 
@@ -144,11 +144,11 @@ __global__ void __launch_bounds__(128) mla_combine_few_kernel(const __grid_const
       wsum += w;
     }
   }
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const float inv = wsum != 0.f ? 1.f / wsum : 0.f;  // (a sum that is NaN stays it)
   uint16_t* out = p.out + ((size_t)b * kHeads + h) * kVDim + f;
   *reinterpret_cast<uint2*>(out) =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (threadIdx.x == 0 && p.lse) p.lse[b * kHeads + h] = wsum > 0.f ? m + logf(wsum) : -INFINITY;
+  if (threadIdx.x == 0 && p.lse) p.lse[b * kHeads + h] = wsum != 0.f ? m + logf(wsum) : -INFINITY;
 }
 
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream, bool pdl) {

@@ -56,7 +56,8 @@ struct Stage1Params {
                              // 64-row paged cache: 64-byte column blocks of 64 rows
   const uint8_t* q;          // bf16 [*, 16, 576]
   const uint8_t* kv;         // row bytes depend on the dtype
-  const void* kv_scale;      // fp32[1] (fp8) or e8m0 [rows, scale_stride] (mxfp4)
+  const void* kv_scale;      // fp32[1] (fp8), e8m0 [rows, scale_stride] (mxfp4) or fp32 scale_stride
+                             // bytes apart (fp8_row)
   int32_t scale_stride;
   const int32_t* kv_indptr;  // rows per sequence; for a paged cache, pages per sequence
   const int32_t* qo_indptr;
@@ -130,6 +131,8 @@ constexpr int32_t kErrDeviceTimeout = 6;
 cudaError_t launch_stage1_bf16(const Stage1Params& p, cudaStream_t s);
 cudaError_t launch_stage1_fp8(const Stage1Params& p, cudaStream_t s);
 cudaError_t launch_stage1_fp8_t2(const Stage1Params& p, cudaStream_t s);  // p.tok == 2
+// e4m3 rows with a scale each: every cache layout and number of tokens
+cudaError_t launch_stage1_fp8_row(const Stage1Params& p, cudaStream_t s);
 cudaError_t launch_stage1_mxfp4(const Stage1Params& p, cudaStream_t s);
 // paged caches with pages of fewer than 64 rows (e4m3 or MXFP4, one token)
 cudaError_t launch_stage1_small_pages(const Stage1Params& p, bool mx, cudaStream_t s);

@@ -8,7 +8,8 @@
 // per head (amax * 2^s_h <= 448).  This kernel writes, per sequence, the
 // 32 x 576 B image (rows h: hi, rows 16 + h: lo; K-major, 64-byte swizzle)
 // that the split kernel copies into shared memory unchanged, and the 16 score
-// factors sm_scale * log2(e) * kv_scale * 2^-s_h (kv_scale = 1 for MXFP4).
+// factors sm_scale * log2(e) * kv_scale * 2^-s_h (kv_scale = 1
+// where the rows have scales of their own).
 //
 // It runs ahead of the split kernel (programmatic dependent launch): it waits
 // for the previous kernel, then lets the split kernel start its set-up, which

@@ -54,6 +54,14 @@
 // prmt.  2^(G-127) goes into the row's score factor, and into P for P.V
 // relative to a running per-unit reference Gv (raised lazily like the softmax
 // reference, with O^T rescaled); the output is O^T 2^Gv / l.
+//
+// e4m3 KV with a scale per row: row t is code_t s_t, so the scores are
+// (q . code_t) s_t and the output sum_t P_t s_t code_t / l.  s_t joins the row's
+// score factor in fp32, and P as s_t 2^-Gv with Gv the running maximum of the
+// scales' exponents (as MXFP4's, each softmax thread fetching its row's scale
+// two tiles ahead).  P's reference is lowered by 4 (P <= 16 after a raise,
+// <= 256 before the next one), which puts the weights that vanish under e4m3's
+// smallest step at 2^-14 of the largest instead of 2^-10.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -72,12 +80,15 @@ constexpr int kPairBytes = 2 * kChunkBytes;  // two column blocks = features [12
 // contiguous cache and pages of 64 rows or more (kPathRows), pages of fewer
 // rows (kPathSmallPages), or MXFP4 scores from block-scaled MMAs on the e2m1
 // tile itself (kPathBlockScaled; otherwise MXFP4 is converted to e4m3 from a
-// staging ring for both MMAs).
-constexpr int kPathRows = 0, kPathSmallPages = 1, kPathBlockScaled = 2;
+// staging ring for both MMAs); the two with row scales are e4m3's.
+constexpr int kPathRows = 0, kPathSmallPages = 1, kPathBlockScaled = 2, kPathRowScales = 3, kPathRowScalesSmall = 4;
+__host__ __device__ constexpr bool small_pages(int path) { return path == kPathSmallPages || path == kPathRowScalesSmall; }
+__host__ __device__ constexpr bool row_scales(int path) { return path == kPathRowScales || path == kPathRowScalesSmall; }
 template <bool kMx, int kTok = 1, int kPath = kPathRows>
 struct Geo {
   static_assert(kTok == 1 || (kTok == 2 && !kMx), "two tokens per unit: e4m3 KV only");
   static_assert(kPath != kPathBlockScaled || (kMx && kTok == 1), "block-scaled scores: MXFP4, one token");
+  static_assert(!row_scales(kPath) || !kMx, "row scales: e4m3");
   static constexpr bool bs = kPath == kPathBlockScaled;
   static constexpr int pair_slots = kMx ? (bs ? 10 : 8) : (kTok == 1 ? 11 : 9);  // ring of column-block pairs (4 per tile)
   // e4m3, one token per unit: a separate epilogue group (warps 8-11) drains
@@ -150,7 +161,8 @@ struct Layout {
   static constexpr int grow = gred + 2 * 4 * 4;               // int8 [2][128] row exponent G - 127 (MXFP4)
   static constexpr int lut = grow + (kMx ? 2 * 128 : 0);      // u8 [32][8] e2m1 magnitude -> e4m3 per shift
   static constexpr int hand = lut + (kMx ? 256 : 0);          // float [2][32] l, m handed to the epilogue group
-  static constexpr int units = hand + (G::epi ? 256 : 0);
+  static constexpr int handg = hand + (G::epi ? 256 : 0);     // int [2] Gv handed over (row scales)
+  static constexpr int units = handg + (G::epi && row_scales(kPath) ? 8 : 0);
   static constexpr int bars = units + G::max_units * (int)sizeof(UnitDesc);
   // the epilogue group's four (e4m3, one token), then the two of block-scaled MXFP4
   static constexpr int nbars = G::bs ? 55 : (G::epi ? 53 : 49);
@@ -1010,7 +1022,7 @@ __host__ __device__ constexpr uint32_t hi_word(uint64_t d) { return (uint32_t)(d
 // scores at +32 i (two tokens: one N = 64 MMA per k step over both query images).
 template <bool kMx, int kTok, int kPath>
 __device__ void qk_issuer(const Stage1Params& p, const Ctx& x) {
-  constexpr bool kSmallPages = kPath == kPathSmallPages;
+  constexpr bool kSmallPages = small_pages(kPath);
   using L = Layout<kMx, kTok, kPath>;
   constexpr bool kBs = Geo<kMx, kTok, kPath>::bs;  // block-scaled e2m1 scores
   constexpr bool kR128 = (kSmallPages && !kMx) || kBs;    // pair slots of 128-byte rows
@@ -1094,7 +1106,7 @@ __device__ void qk_issuer(const Stage1Params& p, const Ctx& x) {
 // buffers and, on a unit's last tile, the unit's O^T.
 template <bool kMx, int kTok, int kPath>
 __device__ void pv_issuer(const Stage1Params& p, const Ctx& x) {
-  constexpr bool kSmallPages = kPath == kPathSmallPages;
+  constexpr bool kSmallPages = small_pages(kPath);
   using L = Layout<kMx, kTok, kPath>;
   constexpr bool kBs = Geo<kMx, kTok, kPath>::bs;  // block-scaled e2m1 scores, V converted in place
   constexpr bool kR128 = (kSmallPages && !kMx) || kBs;    // pair slots of 128-byte rows
@@ -1142,19 +1154,24 @@ __device__ void pv_issuer(const Stage1Params& p, const Ctx& x) {
   }
 }
 
+// 2^e for an integer e in [-126, 127] (exact).
+__device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
+
 // ------------------------------------------------------------------ unit output
 // A unit's output from O^T in TMEM: this thread's lane is feature row `row` of
 // each 128-feature block, the block's 32 columns at tl_o + blk fb (16 heads x
 // the query's two terms).  An unsplit sequence gets bf16 out and lse; a split
 // one an fp32 partial and lse in partial slot u.  l, m: the unit's softmax sum
 // and reference per head (log2 units); out_scale: the factor O^T carries.
-template <bool kTwo>
+// kNan: a sum that is NaN gives a NaN lse, so that a sequence split over several
+// units keeps it (else an lse of -inf, which the combine takes for an empty unit).
+template <bool kTwo, bool kNan>
 __device__ __forceinline__ void write_unit(const Stage1Params& p, uint32_t tl_o, uint32_t blk, int row, bool final_out,
                                            int ob, int u, const float (&l)[16], const float (&m)[16],
                                            float out_scale) {
   float inv[16];
 #pragma unroll
-  for (int h = 0; h < 16; ++h) inv[h] = l[h] > 0.f ? out_scale * __frcp_rn(l[h]) : 0.f;
+  for (int h = 0; h < 16; ++h) inv[h] = (kNan ? l[h] != 0.f : l[h] > 0.f) ? out_scale * __frcp_rn(l[h]) : 0.f;
   // kTwo: two blocks of 128 features per TMEM round trip (MXFP4: 0.1-0.5 us
   // off a bs32/kv8192 split stage in two A/B runs; the e4m3 kernel, which
   // needs four more registers for it, ran bs4/kv8192 1.4 us slower and keeps
@@ -1193,7 +1210,7 @@ __device__ __forceinline__ void write_unit(const Stage1Params& p, uint32_t tl_o,
       lh = row == h ? l[h] : lh;
       mh = row == h ? m[h] : mh;
     }
-    const float lse = lh > 0.f ? (mh + fast_log2(lh)) * kLn2 : -INFINITY;
+    const float lse = (kNan ? lh != 0.f : lh > 0.f) ? (mh + fast_log2(lh)) * kLn2 : -INFINITY;
     if (final_out) {
       if (p.lse) p.lse[ob * kHeads + row] = lse;
     } else {
@@ -1210,14 +1227,16 @@ __device__ __forceinline__ void write_unit(const Stage1Params& p, uint32_t tl_o,
 // after the second's: 32 KB of stores issued mid-stream delayed the copies of
 // the next tiles (a per-CTA trace at bs64/kv8192 showed the unit boundary
 // about 1.8 us longer with them), while at the end they follow the last P.V.
-template <bool kMx, int kTok>
+template <bool kMx, int kTok, int kPath>
 __device__ void epilogue_group(const Stage1Params& p, const Ctx& x, int ww, int lane) {
-  using L = Layout<kMx, kTok>;
+  using L = Layout<kMx, kTok, kPath>;
+  constexpr bool kRow = row_scales(kPath);
   using TM = Tmem<kTok>;
   const int row = 32 * ww + lane;
   const uint32_t tl = x.tmem + ((uint32_t)(32 * ww) << 16);
-  const float kv_scale = *static_cast<const float*>(p.kv_scale);
+  const float kv_scale = kRow ? 1.f : *static_cast<const float*>(p.kv_scale);
   const float* hand = reinterpret_cast<const float*>(x.smem + L::hand);
+  const int* handg = reinterpret_cast<const int*>(x.smem + L::handg);
   const bool defer = x.nunits == 2 && tiles_of(x.units[0]) > 0 && tiles_of(x.units[1]) >= 4;
   int ordinal = 0;
   for (int k = 0; k < x.nunits + (defer ? 1 : 0); ++k) {
@@ -1242,11 +1261,12 @@ __device__ void epilogue_group(const Stage1Params& p, const Ctx& x, int ww, int 
       l[h] = hand[32 * obuf + h];
       m[h] = hand[32 * obuf + 16 + h];
     }
+    const float out_scale = kRow ? exp2_int(handg[obuf]) : kv_scale;
     if (!late0) wait_phase(&x.bar[olast_bar(obuf)], use & 1, x.abort_flag, p.ws_err);
     if (row == 0 && k < 8 && !late0) trace_stamp(p, kTrUnitLastPV + k);
     tc::fence_after();
-    write_unit<false>(p, tl + TM::o + obuf * TM::obuf, TM::blk, row, (d.u & kFinalFlag) != 0, d.b, d.u & ~kFinalFlag, l, m,
-               kv_scale);
+    write_unit<false, kRow>(p, tl + TM::o + obuf * TM::obuf, TM::blk, row, (d.u & kFinalFlag) != 0, d.b, d.u & ~kFinalFlag, l, m,
+               out_scale);
     if (row == 0 && ku < 8) trace_stamp(p, kTrUnitDone + ku);
     tc::fence_before();
     __syncwarp();
@@ -1291,9 +1311,6 @@ __device__ __forceinline__ void group_reduce16(float (&v)[16], float* red, int w
   }
 }
 
-// 2^e for an integer e in [-126, 127] (exact).
-__device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
-
 // Softmax group ti (four warps; one group per query token of the unit):
 // thread `row` owns tile row `row` (its TMEM lane) for the token's 16 heads,
 // in TMEM columns [32 ti, +32) of the S^T buffers and O^T blocks.  With two
@@ -1301,16 +1318,29 @@ __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 12
 // entry), and token ti's partial slot is u + ti S_b.
 template <bool kMx, int kTok, int kPath>
 __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, int lane, int ti) {
-  constexpr bool kSmallPages = kPath == kPathSmallPages;
+  constexpr bool kSmallPages = small_pages(kPath);
   constexpr bool kR128 = kSmallPages && !kMx;  // e4m3 pair slots of 128-byte rows
   constexpr bool kBs = Geo<kMx, kTok, kPath>::bs;  // block-scaled e2m1 scores
   using L = Layout<kMx, kTok, kPath>;
   using TM = Tmem<kTok>;
-  constexpr int kGvNone = -1000;   // no MXFP4 reference yet
+  constexpr bool kRow = row_scales(kPath);    // a scale per row
+  constexpr bool kG = kMx || kRow;            // P carries the rows' scales relative to 2^Gv
+  constexpr float kLower = kRow ? 4.f : 0.f;  // P's reference lies this far below the maximum (log2)
+  constexpr int kGvNone = -1000;   // no such reference yet
   const int row = 32 * ww + lane;  // tile row == TMEM lane of this thread
   const uint32_t tl = x.tmem + ((uint32_t)(32 * ww) << 16) + 32 * ti;
   const uint32_t bar = kBarSoftmax + ti;  // the group's named barrier
-  const float kv_scale = kMx ? 1.f : *static_cast<const float*>(p.kv_scale);
+  const float kv_scale = kG ? 1.f : *static_cast<const float*>(p.kv_scale);
+  // row scales: this thread's row of the next tile and of the one after it (0 past
+  // a unit's end), fetched two tiles ahead
+  TileWalk ahead;
+  auto next_scale = [&]() -> float {
+    int t0, end;
+    if (!ahead.next(x, t0, end) || t0 + row >= end) return 0.f;
+    const int64_t at = (int64_t)cache_row(p, t0 + row) * p.scale_stride;
+    return __ldg(reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.kv_scale) + at));
+  };
+  float sc_next = kRow ? next_scale() : 0.f, sc_after = kRow ? next_scale() : 0.f;
   const int8_t* grow = reinterpret_cast<const int8_t*>(x.smem + L::grow);
   int* gred = reinterpret_cast<int*>(x.smem + L::gred);
   const float* rq = reinterpret_cast<const float*>(x.smem + L::rq) + 16 * ti;
@@ -1355,7 +1385,7 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
       m_ref[h] = -INFINITY;
       l_part[h] = 0.f;
     }
-    int gv = kGvNone;  // MXFP4: P.V reference exponent of the unit
+    int gv = kGvNone;  // P.V reference exponent of the unit
     const int obuf = kEpi ? (ordinal & 1) : 0;  // the unit's O^T buffer
     const uint32_t tl_o = tl + TM::o + obuf * TM::obuf;
     for (int t = 0; t < nt; ++t, ++it) {
@@ -1378,18 +1408,28 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
       __syncwarp();
       if (lane == 0) mbar_arrive(&x.bar[kSEmpty + sb]);
       if (kMx && !kBs) wait_phase(&x.bar[kConvFull + sb], (it >> 1) & 1, x.abort_flag, p.ws_err);
-      const int gsh = kBs ? gsh_bs : (kMx ? max(-126, (int)grow[sb * 128 + row]) : 0);
+      float row_sc = 0.f;
+      if constexpr (kRow) {
+        row_sc = sc_next;
+        sc_next = sc_after;
+        sc_after = next_scale();
+      }
+      // row scales: s in [2^(gsh - 1), 2^gsh), the exponent bounded so that 2^-gsh is finite
+      const int gsh = kBs ? gsh_bs
+                          : (kMx ? max(-126, (int)grow[sb * 128 + row])
+                                 : (kRow ? min(126, max(-100, (__float_as_int(row_sc) >> 23) - 126)) : 0));
       // the scores of block-scaled MMAs carry no row factor
-      const float row_fac = (kMx && !kBs) ? exp2_int(gsh) : 1.f;
+      const float row_fac = (kMx && !kBs) ? exp2_int(gsh) : (kRow ? row_sc : 1.f);
       float sv[16];
       uint32_t need = 0;  // heads with a score above m_ref + 8 in this row (bit 16: G above gv)
 #pragma unroll
       for (int h = 0; h < 16; ++h) {
         sv[h] = row < vis ? (__uint_as_float(acc[h]) + __uint_as_float(acc[16 + h])) * (r[h] * row_fac)
                           : -INFINITY;
-        need |= (sv[h] > m_ref[h] + kRescaleLog2 ? 1u : 0u) << h;
+        // (row scales: a NaN score raises too, so that it reaches the output)
+        need |= ((kRow ? !(sv[h] <= m_ref[h] + kRescaleLog2) : sv[h] > m_ref[h] + kRescaleLog2) ? 1u : 0u) << h;
       }
-      if (kMx && row < valid && gsh > gv) need |= 1u << 16;
+      if (kG && row < valid && gsh > gv) need |= 1u << 16;
       // heads whose reference rises: OR over the warp, then over the 4 warps
       need = __reduce_or_sync(0xffffffffu, need);
       {
@@ -1415,7 +1455,7 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
           for (int h = 0; h < 16; h += 4)
             *reinterpret_cast<int4*>(mx + ww * 16 + h) = make_int4(wmax[h], wmax[h + 1], wmax[h + 2], wmax[h + 3]);
         }
-        if (kMx && ((need >> 16) & 1u)) {
+        if (kG && ((need >> 16) & 1u)) {
           const int w = __reduce_max_sync(0xffffffffu, row < valid ? gsh : kGvNone);
           if (lane == 0) gred[red_par * 4 + ww] = w;
         }
@@ -1425,13 +1465,13 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
         for (int h = 0; h < 16; ++h) {
           fac[h] = 1.f;
           if ((need >> h) & 1u) {
-            const float mn = float_from_order_key(max(max(mx[h], mx[16 + h]), max(mx[32 + h], mx[48 + h])));
+            const float mn = float_from_order_key(max(max(mx[h], mx[16 + h]), max(mx[32 + h], mx[48 + h]))) - kLower;
             fac[h] = (m_ref[h] == -INFINITY) ? 0.f : fast_exp2(m_ref[h] - mn);
             m_ref[h] = mn;
             l_part[h] *= fac[h];
           }
         }
-        if (kMx && ((need >> 16) & 1u)) {
+        if (kG && ((need >> 16) & 1u)) {
           // raise the P.V reference: O^T so far is scaled down by 2^(gv_old - gv_new)
           const int* g4 = gred + red_par * 4;
           const int gnew = max(max(g4[0], g4[1]), max(g4[2], g4[3]));
@@ -1461,8 +1501,9 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
         }
       }
       // probabilities (<= 256), two e4m3 terms, MN-major B operand row = this row;
-      // MXFP4 weights for P.V carry the row's 2^(G-127) relative to 2^gv (<= 1)
-      const float pv_fac = kMx ? exp2_int(max(-126, gsh - gv)) : 1.f;
+      // MXFP4 weights for P.V carry the row's 2^(G-127) relative to 2^gv (<= 1),
+      // row scales the row's own s 2^-gv (< 1)
+      const float pv_fac = kMx ? exp2_int(max(-126, gsh - gv)) : (kRow ? row_sc * exp2_int(-gv) : 1.f);
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -1521,6 +1562,7 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
           hand[h] = l_part[h];
           hand[16 + h] = m_ref[h];
         }
+        if (kRow) reinterpret_cast<int*>(x.smem + L::handg)[obuf] = gv;
         mbar_arrive(&x.bar[kEpiReady + obuf]);
       }
       ++ordinal;
@@ -1531,8 +1573,8 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
       if (row == 0 && ti == 0 && k < 8) trace_stamp(p, kTrUnitLastPV + k);
       ++ordinal;
       tc::fence_after();
-      const float out_scale = kMx ? exp2_int(max(-126, min(127, gv))) : kv_scale;
-      write_unit<kMx>(p, tl_o, TM::blk, row, final_out, ob, u, l_part, m_ref, out_scale);
+      const float out_scale = kG ? exp2_int(max(-126, min(127, gv))) : kv_scale;
+      write_unit<kMx, kRow>(p, tl_o, TM::blk, row, final_out, ob, u, l_part, m_ref, out_scale);
       if (row == 0 && ti == 0 && k < 8) trace_stamp(p, kTrUnitDone + k);
       tc::fence_before();
       __syncwarp();
@@ -1542,14 +1584,15 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
   if (row == 0 && ti == 0) trace_value(p, kTrTiles, (uint64_t)it);
 }
 
-// kPath: the instance -- kPathSmallPages for paged caches with pages of fewer
+// kPath: the instance -- small_pages(kPath) for paged caches with pages of fewer
 // than 64 rows (one token per unit), whose producer warp fetches rows page by
-// page; kPathBlockScaled for MXFP4 scores from block-scaled MMAs.  Separate
+// page; kPathBlockScaled for MXFP4 scores from block-scaled MMAs; row_scales(kPath)
+// for e4m3 rows with a scale each.  Separate
 // instances, so that the others carry none of their code.
 template <bool kMx, int kTok, int kPath>
 __global__ void __launch_bounds__(Geo<kMx, kTok, kPath>::threads, 1)
     mla_split_tc_kernel(const __grid_constant__ Stage1Params p) {
-  constexpr bool kSmallPages = kPath == kPathSmallPages;
+  constexpr bool kSmallPages = small_pages(kPath);
   using L = Layout<kMx, kTok, kPath>;
   constexpr bool kBs = Geo<kMx, kTok, kPath>::bs;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -1696,7 +1739,7 @@ __global__ void __launch_bounds__(Geo<kMx, kTok, kPath>::threads, 1)
     else if constexpr (kMx)
       converter_mx<kSmallPages>(p, x, warp - 8, lane);
     else if constexpr (Geo<kMx, kTok, kPath>::epi)
-      epilogue_group<kMx, kTok>(p, x, warp & 3, lane);
+      epilogue_group<kMx, kTok, kPath>(p, x, warp & 3, lane);
   }
 
   if ((warp == 1 || warp == 2) && lane == 0) {
@@ -1722,7 +1765,7 @@ inline cudaError_t launch_split_tc(const Stage1Params& p, cudaStream_t stream) {
   static_assert(L::total <= 232448, "shared memory carve-up exceeds the 227 KB per-CTA limit");
   static_assert(L::qs % 1024 == 0 && L::pb % 1024 == 0 && L::rope % 1024 == 0, "swizzled operand alignment");
   static_assert(L::stage % 128 == 0 && L::sf % 16 == 0 && L::sfb % 16 == 0, "copy source / destination alignment");
-  static_assert(kPath != tcfp8::kPathSmallPages || kTok == 1, "paged caches take one token per sequence");
+  static_assert(!tcfp8::small_pages(kPath) || kTok == 1, "paged caches take one token per sequence");
   auto* kernel = tcfp8::mla_split_tc_kernel<kMx, kTok, kPath>;
   cudaError_t e = smem_opt_in<tcfp8::mla_split_tc_kernel<kMx, kTok, kPath>>(L::total);
   if (e != cudaSuccess) return e;
