@@ -33,18 +33,30 @@ namespace {
 constexpr int kSlotBytes = 128 * 128;  // 128 rows of 64 bf16 columns
 constexpr int kRing = 8;
 constexpr int kQChunks = 3, kVChunks = 2, kChunks = kQChunks + kVChunks;
-constexpr int kWarps = 10;             // 0-3, 4-7 softmax of tile 0 and 1; 8 copies; 9 MMAs
+constexpr int kSoftWarps = 16;         // 0-7, 8-15: softmax of tile 0 and 1
+constexpr int kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;  // MMAs of tile 0; the next warp: of tile 1
+constexpr int kWarps = kSoftWarps + 3;
 constexpr float kRaise = 8.f;
 
 struct Smem {
   static constexpr int q = 0;                                  // [2 tiles][3 chunks]
   static constexpr int ring = q + 2 * kQChunks * kSlotBytes;
   static constexpr int bars = ring + kRing * kSlotBytes;
-  static constexpr int nbars = 2 * kRing + 2 + 2 + 2 + 2 + 1;
-  static constexpr int misc = bars + 8 * nbars;                // tmem base, abort, document
+  static constexpr int nbars = 17;
+  static constexpr int meet = bars + 8 * (nbars + 1);          // float [2 tiles][2 halves][128 rows]
+  static constexpr int misc = meet + 2 * 2 * 128 * 4;          // tmem base, abort
   static constexpr int total = misc + 32;
 };
-enum { kFull = 0, kEmpty = kRing, kQ = 2 * kRing, kS = kQ + 2, kP = kS + 2, kO = kP + 2, kEnd = kO + 2 };
+// mbarriers.  Those of key tile j come in pairs, used by even and odd j in turn.
+enum {
+  kKFull = 0,  // [2] K tile j copied
+  kVFull = 2,  // [2] V tile j copied
+  kQ = 4,      // [2 tiles] queries copied
+  kS = 6,      // [2 tiles][2] scores written (their K tile read)
+  kO = 10,     // [2 tiles][2] products with V added to O (their V tile and weights read)
+  kP = 14,     // [2 tiles] weights written, O rescaled (8 warps)
+  kEnd = 16    // both MMA threads' last operation
+};
 
 // TMEM columns
 __device__ __forceinline__ uint32_t s_col(int g) { return 128u * g; }
@@ -58,19 +70,27 @@ constexpr uint32_t kIdescS = idesc_bf16(128, 128, 0), kIdescO = idesc_bf16(128, 
 constexpr uint64_t kTplK = tc::desc_template(16, 1024, 2);          // K-major, 128-byte swizzle
 constexpr uint64_t kTplV = tc::desc_template(kSlotBytes, 1024, 2);  // MN-major: 64-column atoms a slot apart
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// One lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -80,6 +100,36 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// 16 consecutive 32-bit TMEM columns of this thread's lane.
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
 // The CTA's share of the batch.
@@ -134,10 +184,32 @@ struct Ctx {
   volatile int* abort;
   uint32_t tmem;
   int32_t* err;
-  __device__ bool wait(int b, int use) const { return wait_phase(&bar[b], use & 1, abort, err); }
+  // Bounded: the clock is read every 1024 tries only (a wait is a step of the chain
+  // of scores, softmax and products that the kernel's time consists of).
+  __device__ __forceinline__ bool wait(int b, int use) const {
+    if (mbar_try_wait(&bar[b], use & 1)) return true;
+    uint64_t since = 0;
+    for (int tries = 1; !mbar_try_wait(&bar[b], use & 1); ++tries)
+      if (tries % 1024 == 0 && (since = look(since)) == kGaveUp) return false;
+    return true;
+  }
+  static constexpr uint64_t kGaveUp = ~0ull;
+  __device__ __noinline__ uint64_t look(uint64_t since) const;
   // by a whole warp, which goes on (or gives up) together
   __device__ bool wait_warp(int b, int use) const { return __all_sync(0xffffffffu, wait(b, use)); }
 };
+
+// Of a wait that began at `since` (0: its first look): when it began, or kGaveUp
+// after kWaitTimeoutNs, or if another thread of the CTA has given up.
+__device__ __noinline__ uint64_t Ctx::look(uint64_t since) const {
+  if (*abort) return kGaveUp;
+  const uint64_t now = global_timer_ns();
+  if (since == 0) return now;
+  if (now - since <= kWaitTimeoutNs) return since;
+  *abort = 1;
+  atomicCAS(err, 0, kErrDeviceTimeout);
+  return kGaveUp;
+}
 
 // ------------------------------------------------------------------ copies
 __device__ void copies(const PromptParams& p, const Ctx& x, const Work& w, int head, int n0, int n1) {
@@ -151,191 +223,181 @@ __device__ void copies(const PromptParams& p, const Ctx& x, const Work& w, int h
     tma_load_3d(dst + 2 * kSlotBytes, &p.q_pe, 0, head, w.q0 + 128 * g, &x.bar[kQ + g], once);
   }
   const int n = max(n0, n1);
-  int c = 0;
-  for (int j = 0; j < n && !*x.abort; ++j) {
+  int ks = 0, vs = 0;  // tiles asked for
+  // what K tile j and V tile j go over: a slot of K and both of V of tile j - 2, two
+  // slots of K of tile j - 1
+  auto read = [&](int bar, int j) {
+    return (j >= n0 || x.wait(bar + (j & 1), j >> 1)) && (j >= n1 || x.wait(bar + 2 + (j & 1), j >> 1));
+  };
+  for (int j = 0; j < n; ++j) {
     const int row = w.k0 + kPromptTile * j;
-    for (int i = 0; i < kChunks; ++i, ++c) {
-      const int sl = c % kRing, use = c / kRing;
-      if (use >= 1 && !x.wait(kEmpty + sl, use - 1)) break;
-      uint64_t* bar = &x.bar[kFull + sl];
-      uint8_t* dst = x.smem + Smem::ring + sl * kSlotBytes;
-      mbar_arrive_expect_tx(bar, kSlotBytes);
-      if (i < 2) tma_load_3d(dst, &p.k_nope, 64 * i, head, row, bar, keep);
-      else if (i == 2) tma_load_2d(dst, &p.k_pe, 0, row, bar, keep);
-      else tma_load_3d(dst, &p.v, 64 * (i - 3), head, row, bar, keep);
-    }
+    auto slot = [&](int c) { return x.smem + Smem::ring + (kChunks * j + c) % kRing * kSlotBytes; };
+    if (j >= 2 && !read(kO, j - 2)) break;
+    uint64_t* bar = &x.bar[kKFull + (j & 1)];
+    mbar_arrive_expect_tx(bar, kQChunks * kSlotBytes);
+    tma_load_3d(slot(0), &p.k_nope, 0, head, row, bar, keep);
+    tma_load_3d(slot(1), &p.k_nope, 64, head, row, bar, keep);
+    tma_load_2d(slot(2), &p.k_pe, 0, row, bar, keep);
+    ++ks;
+    if (j >= 1 && !read(kS, j - 1)) break;
+    bar = &x.bar[kVFull + (j & 1)];
+    mbar_arrive_expect_tx(bar, kVChunks * kSlotBytes);
+    tma_load_3d(slot(3), &p.v, 0, head, row, bar, keep);
+    tma_load_3d(slot(4), &p.v, 64, head, row, bar, keep);
+    ++vs;
   }
   if (*x.abort) {
     // a wait gave up somewhere: never leave with copies in flight (bounded)
     const uint64_t t0 = global_timer_ns();
-    for (int i = 0; i < kRing + 2; ++i) {
-      const int armed = i < kRing ? (c + kRing - 1 - i) / kRing : ((i - kRing ? n1 : n0) > 0 ? 1 : 0);
+    for (int i = 0; i < 6; ++i) {
+      const int armed = i < 4 ? ((i < 2 ? ks : vs) + 1 - (i & 1)) / 2 : ((i - 4 ? n1 : n0) > 0 ? 1 : 0);
       if (armed == 0) continue;
-      uint64_t* bar = i < kRing ? &x.bar[kFull + i] : &x.bar[kQ + i - kRing];
-      while (!mbar_try_wait(bar, (armed - 1) & 1) && global_timer_ns() - t0 < kWaitTimeoutNs) {
+      while (!mbar_try_wait(&x.bar[i], (armed - 1) & 1) && global_timer_ns() - t0 < kWaitTimeoutNs) {
       }
     }
   }
 }
 
 // ------------------------------------------------------------------ MMAs
-// One thread, in this order: S_0(0) S_1(0), then for every key tile j O_0(j)
-// S_0(j + 1) O_1(j) S_1(j + 1).  MMAs of one thread execute in the order of their
-// issue, so S_g(j + 1) may overwrite P_g(j), which O_g(j) read before it.
-__device__ void mmas(const Ctx& x, int n0, int n1) {
-  const int n = max(n0, n1);
-  const uint32_t ring = smem_u32(x.smem + Smem::ring), q = smem_u32(x.smem + Smem::q);
-  auto wait_chunks = [&](int j, int from, int to) {
-    for (int i = from; i < to; ++i) x.wait(kFull + (kChunks * j + i) % kRing, (kChunks * j + i) / kRing);
-  };
-  auto release = [&](int j, int from, int to) {
-    for (int i = from; i < to; ++i) tc::commit(&x.bar[kEmpty + (kChunks * j + i) % kRing]);
-  };
-  auto scores = [&](int g, int j) {
-    const uint64_t a0 = kTplK + ((q + g * kQChunks * kSlotBytes) >> 4);
+// One warp a query tile (its elected lane issues; the descriptors are the same in
+// every lane, so that they stay in uniform registers), in this order: S(0), then for every key tile j O(j),
+// S(j + 1).  MMAs of one thread execute in the order of their issue, so S(j + 1) may
+// overwrite the weights of tile j, which O(j) read before it.  (One thread for both
+// tiles: its waits, commits and issues take longer than the MMAs, and 1.5 times as
+// long a call.)  Descriptors are a constant high word and a low word to which
+// addresses / 16 are added.
+__device__ void mmas(const Ctx& x, int g, int n) {
+  const uint32_t ring = smem_u32(x.smem + Smem::ring) >> 4, q = (smem_u32(x.smem + Smem::q) + g * kQChunks * kSlotBytes) >> 4;
+  const uint32_t sc = x.tmem + s_col(g), oc = x.tmem + o_col(g);
+  constexpr uint32_t kSlot = kSlotBytes >> 4;
+  auto scores = [&](int j) {
+    const uint32_t a0 = (uint32_t)kTplK + q;
+    if (!elect()) return;
 #pragma unroll
     for (int c = 0; c < kQChunks; ++c) {
-      const uint64_t b0 = kTplK + ((ring + (kChunks * j + c) % kRing * kSlotBytes) >> 4);
+      const uint32_t b0 = (uint32_t)kTplK + ring + (kChunks * j + c) % kRing * kSlot;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        mma_ss(x.tmem + s_col(g), a0 + ((c * kSlotBytes + 32 * k) >> 4), b0 + 2 * k, kIdescS, c + k > 0);
+        mma_ss(sc, a0 + c * kSlot + 2 * k, b0 + 2 * k, (uint32_t)(kTplK >> 32), kIdescS, c + k > 0);
     }
-    tc::commit(&x.bar[kS + g]);
+    tc::commit(&x.bar[kS + 2 * g + (j & 1)]);
   };
-  auto values = [&](int g, int j) {
-    const int s0 = (kChunks * j + kQChunks) % kRing;
-    const uint64_t b0 = kTplV + ((ring + s0 * kSlotBytes) >> 4);
-    const uint32_t a0 = x.tmem + s_col(g), d = x.tmem + o_col(g);
+  auto values = [&](int j) {
+    const uint32_t s0 = (kChunks * j + kQChunks) % kRing;
+    const uint32_t b0 = (uint32_t)kTplV + ring + s0 * kSlot;
+    if (!elect()) return;
     if (s0 + 1 < kRing) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) mma_ts(d, a0 + 8 * k, b0 + 128 * k, kIdescO, (j > 0) | (k > 0));
+      for (int k = 0; k < 8; ++k) mma_ts(oc, sc + 8 * k, b0 + 128 * k, (uint32_t)(kTplV >> 32), kIdescO, (j > 0) | (k > 0));
     } else {  // the second 64 columns are in the ring's first slot
-      const uint64_t b1 = kTplV + (ring >> 4);
+      const uint32_t b1 = (uint32_t)kTplV + ring;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        mma_ts(d, a0 + 8 * k, b0 + 128 * k, kIdescOHalf, (j > 0) | (k > 0));
-        mma_ts(d + 64, a0 + 8 * k, b1 + 128 * k, kIdescOHalf, (j > 0) | (k > 0));
+        mma_ts(oc, sc + 8 * k, b0 + 128 * k, (uint32_t)(kTplV >> 32), kIdescOHalf, (j > 0) | (k > 0));
+        mma_ts(oc + 64, sc + 8 * k, b1 + 128 * k, (uint32_t)(kTplV >> 32), kIdescOHalf, (j > 0) | (k > 0));
       }
     }
-    tc::commit(&x.bar[kO + g]);
+    tc::commit(&x.bar[kO + 2 * g + (j & 1)]);
   };
-  if (n > 0) {
-    wait_chunks(0, 0, kQChunks);
-    for (int g = 0; g < 2; ++g) {
-      if ((g ? n1 : n0) == 0) continue;
-      x.wait(kQ + g, 0);
-      if (*x.abort) return;
-      tc::fence_after();
-      scores(g, 0);
-    }
-    release(0, 0, kQChunks);
-  }
+  if (n == 0) return;
+  if (!x.wait_warp(kQ + g, 0) || !x.wait_warp(kKFull, 0)) return;
+  tc::fence_after();
+  scores(0);
   for (int j = 0; j < n; ++j) {
-    wait_chunks(j, kQChunks, kChunks);
-    for (int g = 0; g < 2; ++g) {
-      const int ng = g ? n1 : n0;
-      if (j < ng) {
-        x.wait(kP + g, j);
-        if (*x.abort) return;
-        tc::fence_after();
-        values(g, j);
-      }
-      if (g == 1 || n1 <= j) release(j, kQChunks, kChunks);
-      if (j + 1 < ng) {
-        wait_chunks(j + 1, 0, kQChunks);
-        if (*x.abort) return;
-        scores(g, j + 1);
-      }
-      if (g == 1 || n1 <= j) {
-        if (j + 1 < n) release(j + 1, 0, kQChunks);
-        break;
-      }
+    if (!x.wait_warp(kVFull + (j & 1), j >> 1) || !x.wait_warp(kP + g, j)) return;
+    tc::fence_after();
+    values(j);
+    if (j + 1 < n) {
+      if (!x.wait_warp(kKFull + ((j + 1) & 1), (j + 1) >> 1)) return;
+      scores(j + 1);
     }
   }
 }
 
 // ------------------------------------------------------------------ softmax
+// Two warps a 32-row quarter of a tile: warp `half` has its columns [64 half, +64), so
+// that each SM sub-partition has four warps to choose from.  The two meet once a key
+// tile, to find the row's maximum.  No wait is left early: a warp that gives up
+// (abort) still comes to every meeting.
 __device__ void softmax(const PromptParams& p, const Ctx& x, const Work& w, int head, int g, int n) {
-  const int ww = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const int half = (threadIdx.x >> 7) & 1, ww = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const int row = 32 * ww + lane, i = 128 * g + row;  // of the tile, of the CTA
   const bool mine = i < w.rows;
   const int lim = mine ? seen(p, w, i) : 0;
   const uint32_t lanes = x.tmem + ((uint32_t)(32 * ww) << 16);
-  const uint32_t ts = lanes + s_col(g), to = lanes + o_col(g);
+  const uint32_t ts = lanes + s_col(g), to = lanes + o_col(g) + 64 * half;
+  float* const meet = reinterpret_cast<float*>(x.smem + Smem::meet) + 256 * g + row;  // + 128 per half
+  const uint32_t pair = 1 + 4 * g + ww;                                              // named barrier of the two
   float m = -INFINITY, l = 0.f;
   for (int j = 0; j < n; ++j) {
-    if (!x.wait_warp(kS + g, j)) break;
+    x.wait_warp(kS + 2 * g + (j & 1), j >> 1);
     tc::fence_after();
-    float s[128];
+    float s[64];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) tc::ld32(ts + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]));
+    for (int c = 0; c < 2; ++c) tc::ld32(ts + 64 * half + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c]));
     tc::wait_ld();
-    const int left = lim - kPromptTile * j;  // keys of this tile that the row sees
-    if (__any_sync(0xffffffffu, left < kPromptTile)) {
+    const int left = lim - kPromptTile * j - 64 * half;  // of these 64 keys, those that the row sees
+    if (__any_sync(0xffffffffu, left < 64)) {
 #pragma unroll
-      for (int k = 0; k < 128; ++k) s[k] = k < left ? s[k] : -INFINITY;
+      for (int k = 0; k < 64; ++k) s[k] = k < left ? s[k] : -INFINITY;
     }
-    float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
+    float t[4];
 #pragma unroll
-    for (int k = 4; k < 128; k += 4) {
-      t0 = fmaxf(t0, s[k]);
-      t1 = fmaxf(t1, s[k + 1]);
-      t2 = fmaxf(t2, s[k + 2]);
-      t3 = fmaxf(t3, s[k + 3]);
-    }
-    const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * p.scale_log2;
+    for (int k = 0; k < 4; ++k) t[k] = max3(s[k], s[4 + k], s[8 + k]);
+#pragma unroll
+    for (int k = 12; k < 60; k += 8)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) t[u] = max3(t[u], s[k + u], s[k + 4 + u]);
+    const float most = fmaxf(max3(t[0], s[60], s[61]), max3(max3(t[1], t[2], t[3]), s[62], s[63]));
+    meet[128 * half] = most;
+    named_bar_sync(pair, 64);  // both have their scores in registers, and each other's maximum
+    const float top = fmaxf(most, meet[128 * (half ^ 1)]) * p.scale_log2;
     const bool raise = top > m + kRaise;
     if (__any_sync(0xffffffffu, raise)) {
       const float f = !raise ? 1.f : (m == -INFINITY ? 0.f : fast_exp2(m - top));
       if (raise) m = top;
       l *= f;
       if (j > 0) {
-        if (!x.wait_warp(kO + g, j - 1)) break;
+        x.wait_warp(kO + 2 * g + ((j - 1) & 1), (j - 1) >> 1);
         tc::fence_after();
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
-          tc::ld32(to + 32 * c, o);
+          uint32_t o[16];
+          ld16(to + 16 * c, o);
           tc::wait_ld();
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-          tc::st32(to + 32 * c, o);
+          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+          st16(to + 16 * c, o);
         }
-        tc::wait_st();
       }
     }
     const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
     const float mm = m == -INFINITY ? 0.f : -m;
     const float2 m2 = make_float2(mm, mm);
-    float l0 = 0.f, l1 = 0.f;
+    float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t pk[32];
+      uint32_t pk[16];
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const float2 e = fma2(make_float2(s[64 * h + 2 * k], s[64 * h + 2 * k + 1]), c2, m2);
-        const float a = fast_exp2(e.x), b = fast_exp2(e.y);
-        l0 += a;
-        l1 += b;
-        pk[k] = pack_bf16x2(a, b);
+      for (int k = 0; k < 16; ++k) {
+        float2 e = fma2(make_float2(s[32 * h + 2 * k], s[32 * h + 2 * k + 1]), c2, m2);
+        e = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+        sum = add2(sum, e);
+        pk[k] = pack_bf16x2(e.x, e.y);
       }
-      tc::st32(ts + 32 * h, pk);
+      st16(ts + 32 * half + 16 * h, pk);
     }
-    l += l0 + l1;
+    l += sum.x + sum.y;
     const int valid = w.nk - kPromptTile * j;  // keys of the document in this tile
     if (valid < kPromptTile) {
       // rows past the document's last key hold other rows' data: zeros, so that a
-      // weight of 0 cannot meet a value that is not finite
-      const int c0 = kChunks * j + kQChunks;
-      x.wait(kFull + c0 % kRing, c0 / kRing);
-      x.wait(kFull + (c0 + 1) % kRing, (c0 + 1) / kRing);
+      // weight of 0 cannot meet a value that is not finite (each half: 64 columns)
+      const int c = kChunks * j + kQChunks + half;
+      x.wait_warp(kVFull + (j & 1), j >> 1);
       if (row >= valid) {
+        uint4* dst = reinterpret_cast<uint4*>(x.smem + Smem::ring + c % kRing * kSlotBytes + row * 128);
 #pragma unroll
-        for (int c = 0; c < kVChunks; ++c) {
-          uint4* dst = reinterpret_cast<uint4*>(x.smem + Smem::ring + (c0 + c) % kRing * kSlotBytes + row * 128);
-#pragma unroll
-          for (int u = 0; u < 8; ++u) dst[u] = make_uint4(0, 0, 0, 0);
-        }
+        for (int u = 0; u < 8; ++u) dst[u] = make_uint4(0, 0, 0, 0);
       }
       tc::fence_proxy_async();
     }
@@ -344,12 +406,18 @@ __device__ void softmax(const PromptParams& p, const Ctx& x, const Work& w, int 
     __syncwarp();
     if (lane == 0) mbar_arrive(&x.bar[kP + g]);
   }
-  if (n > 0 && !x.wait_warp(kO + g, n - 1)) return;
+  // the halves' sums (both have read the last maximum: its meeting is behind them
+  // only once each has come here)
+  named_bar_sync(pair, 64);
+  meet[128 * half] = l;
+  named_bar_sync(pair, 64);
+  l += meet[128 * (half ^ 1)];
+  if (n > 0 && !x.wait_warp(kO + 2 * g + ((n - 1) & 1), (n - 1) >> 1)) return;
   tc::fence_after();
   const float inv = l > 0.f ? __frcp_rn(l) : (l == 0.f ? 0.f : l);
-  uint4* out = reinterpret_cast<uint4*>(p.out + (int64_t)(w.q0 + i) * p.out_token_stride + (int64_t)head * p.out_head_stride);
+  uint4* out = reinterpret_cast<uint4*>(p.out + (int64_t)(w.q0 + i) * p.out_token_stride + (int64_t)head * p.out_head_stride + 64 * half);
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < 2; ++c) {
     uint32_t o[32];
     if (n > 0) {
       tc::ld32(to + 32 * c, o);
@@ -366,7 +434,8 @@ __device__ void softmax(const PromptParams& p, const Ctx& x, const Work& w, int 
     }
     __syncwarp();
   }
-  if (mine && p.lse) p.lse[(int64_t)(w.q0 + i) * p.heads + head] = l == 0.f ? -INFINITY : (m + fast_log2(l)) * kLn2;
+  if (mine && half == 0 && p.lse)
+    p.lse[(int64_t)(w.q0 + i) * p.heads + head] = l == 0.f ? -INFINITY : (m + fast_log2(l)) * kLn2;
 }
 
 __global__ void __launch_bounds__(32 * kWarps, 1) mla_prompt_kernel(const __grid_constant__ PromptParams p) {
@@ -379,7 +448,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) mla_prompt_kernel(const __grid
   x.abort = misc + 1;
   x.err = p.ws_err;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < Smem::nbars; ++i) mbar_init(&x.bar[i], i == kP || i == kP + 1 ? 4 : 1);
+    for (int i = 0; i < Smem::nbars; ++i) mbar_init(&x.bar[i], i == kP || i == kP + 1 ? 8 : (i == kEnd ? 2 : 1));
     misc[1] = 0;
     fence_mbar_init();
   }
@@ -400,7 +469,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) mla_prompt_kernel(const __grid
   }
   if (!any) return;  // (every warp finds the same)
   __syncwarp();
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tc::alloc(reinterpret_cast<uint32_t*>(misc), 512);
     tc::relinquish();
   }
@@ -409,14 +478,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) mla_prompt_kernel(const __grid
   tc::fence_after();
   x.tmem = *reinterpret_cast<uint32_t*>(misc);
   const int n0 = tiles_of(p, w, 0), n1 = tiles_of(p, w, 1);
-  if (warp < 8) {
-    softmax(p, x, w, head, warp >> 2, warp < 4 ? n0 : n1);
-  } else if (warp == 8) {
+  if (warp < kSoftWarps) {
+    softmax(p, x, w, head, warp >> 3, warp < 8 ? n0 : n1);
+  } else if (warp == kCopyWarp) {
     if (lane == 0) copies(p, x, w, head, n0, n1);
-  } else if (lane == 0) {
-    mmas(x, n0, n1);
-    // every MMA is complete before tensor memory is given back
-    tc::commit(&x.bar[kEnd]);
+  } else {
+    const int g = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);
+    x.tmem = __shfl_sync(0xffffffffu, x.tmem, 0);
+    mmas(x, g, __shfl_sync(0xffffffffu, g ? n1 : n0, 0));
+    // every MMA of both is complete before tensor memory is given back
+    __syncwarp();
+    if (elect()) tc::commit(&x.bar[kEnd]);
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait(&x.bar[kEnd], 0) && global_timer_ns() - t0 < kWaitTimeoutNs) {
     }
@@ -425,7 +497,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) mla_prompt_kernel(const __grid
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  if (warp == 9) tc::dealloc(x.tmem, 512);
+  if (warp == kMmaWarp) tc::dealloc(x.tmem, 512);
 }
 
 }  // namespace
