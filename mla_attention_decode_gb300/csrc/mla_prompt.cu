@@ -42,7 +42,7 @@ struct Smem {
   static constexpr int q = 0;                                  // [2 tiles][3 chunks]
   static constexpr int ring = q + 2 * kQChunks * kSlotBytes;
   static constexpr int bars = ring + kRing * kSlotBytes;
-  static constexpr int nbars = 17;
+  static constexpr int nbars = 21;
   static constexpr int meet = bars + 8 * (nbars + 1);          // float [2 tiles][2 halves][128 rows]
   static constexpr int misc = meet + 2 * 2 * 128 * 4;          // tmem base, abort
   static constexpr int total = misc + 32;
@@ -54,8 +54,9 @@ enum {
   kQ = 4,      // [2 tiles] queries copied
   kS = 6,      // [2 tiles][2] scores written (their K tile read)
   kO = 10,     // [2 tiles][2] products with V added to O (their V tile and weights read)
-  kP = 14,     // [2 tiles] weights written, O rescaled (8 warps)
-  kEnd = 16    // both MMA threads' last operation
+  kP = 14,     // [2 tiles][2] weights of the even, odd 32 keys written, O rescaled (8 warps)
+  kTurn = 18,  // [2 tiles] a tile's MMAs of one key tile issued
+  kEnd = 20    // both MMA threads' last operation
 };
 
 // TMEM columns
@@ -266,7 +267,7 @@ __device__ void copies(const PromptParams& p, const Ctx& x, const Work& w, int h
 // tiles: its waits, commits and issues take longer than the MMAs, and 1.5 times as
 // long a call.)  Descriptors are a constant high word and a low word to which
 // addresses / 16 are added.
-__device__ void mmas(const Ctx& x, int g, int n) {
+__device__ void mmas(const Ctx& x, int g, int n, int other) {
   const uint32_t ring = smem_u32(x.smem + Smem::ring) >> 4, q = (smem_u32(x.smem + Smem::q) + g * kQChunks * kSlotBytes) >> 4;
   const uint32_t sc = x.tmem + s_col(g), oc = x.tmem + o_col(g);
   constexpr uint32_t kSlot = kSlotBytes >> 4;
@@ -282,35 +283,47 @@ __device__ void mmas(const Ctx& x, int g, int n) {
     }
     tc::commit(&x.bar[kS + 2 * g + (j & 1)]);
   };
-  auto values = [&](int j) {
+  // 16-key steps of the weights: the first, second 32 keys of each 64
+  auto values = [&](int j, int part) {
     const uint32_t s0 = (kChunks * j + kQChunks) % kRing;
     const uint32_t b0 = (uint32_t)kTplV + ring + s0 * kSlot;
     if (!elect()) return;
     if (s0 + 1 < kRing) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) mma_ts(oc, sc + 8 * k, b0 + 128 * k, (uint32_t)(kTplV >> 32), kIdescO, (j > 0) | (k > 0));
+      for (int i = 0; i < 4; ++i) {
+        const int k = 4 * (i >> 1) + 2 * part + (i & 1);
+        mma_ts(oc, sc + 8 * k, b0 + 128 * k, (uint32_t)(kTplV >> 32), kIdescO, (j > 0) | (part + i > 0));
+      }
     } else {  // the second 64 columns are in the ring's first slot
       const uint32_t b1 = (uint32_t)kTplV + ring;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        mma_ts(oc, sc + 8 * k, b0 + 128 * k, (uint32_t)(kTplV >> 32), kIdescOHalf, (j > 0) | (k > 0));
-        mma_ts(oc + 64, sc + 8 * k, b1 + 128 * k, (uint32_t)(kTplV >> 32), kIdescOHalf, (j > 0) | (k > 0));
+      for (int i = 0; i < 4; ++i) {
+        const int k = 4 * (i >> 1) + 2 * part + (i & 1);
+        mma_ts(oc, sc + 8 * k, b0 + 128 * k, (uint32_t)(kTplV >> 32), kIdescOHalf, (j > 0) | (part + i > 0));
+        mma_ts(oc + 64, sc + 8 * k, b1 + 128 * k, (uint32_t)(kTplV >> 32), kIdescOHalf, (j > 0) | (part + i > 0));
       }
     }
-    tc::commit(&x.bar[kO + 2 * g + (j & 1)]);
+    if (part) tc::commit(&x.bar[kO + 2 * g + (j & 1)]);
   };
   if (n == 0) return;
   if (!x.wait_warp(kQ + g, 0) || !x.wait_warp(kKFull, 0)) return;
   tc::fence_after();
   scores(0);
   for (int j = 0; j < n; ++j) {
-    if (!x.wait_warp(kVFull + (j & 1), j >> 1) || !x.wait_warp(kP + g, j)) return;
+    if (!x.wait_warp(kVFull + (j & 1), j >> 1) || !x.wait_warp(kP + 2 * g, j)) return;
+    // the other tile's turn comes first: tile 0 follows tile 1's previous key tile
+    if (g == 0 ? (j > 0 && j - 1 < other) : j < other)
+      if (!x.wait_warp(kTurn + (g ^ 1), g == 0 ? j - 1 : j)) return;
     tc::fence_after();
-    values(j);
+    values(j, 0);
+    if (!x.wait_warp(kP + 2 * g + 1, j)) return;
+    tc::fence_after();
+    values(j, 1);
     if (j + 1 < n) {
       if (!x.wait_warp(kKFull + ((j + 1) & 1), (j + 1) >> 1)) return;
       scores(j + 1);
     }
+    if (elect()) mbar_arrive(&x.bar[kTurn + g]);
   }
 }
 
@@ -371,6 +384,19 @@ __device__ void softmax(const PromptParams& p, const Ctx& x, const Work& w, int 
         }
       }
     }
+    const int valid = w.nk - kPromptTile * j;  // keys of the document in this tile
+    if (valid < kPromptTile) {
+      // rows past the document's last key hold other rows' data: zeros, so that a
+      // weight of 0 cannot meet a value that is not finite (each half: 64 columns)
+      const int c = kChunks * j + kQChunks + half;
+      x.wait_warp(kVFull + (j & 1), j >> 1);
+      if (row >= valid) {
+        uint4* dst = reinterpret_cast<uint4*>(x.smem + Smem::ring + c % kRing * kSlotBytes + row * 128);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) dst[u] = make_uint4(0, 0, 0, 0);
+      }
+      tc::fence_proxy_async();
+    }
     const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
     const float mm = m == -INFINITY ? 0.f : -m;
     const float2 m2 = make_float2(mm, mm);
@@ -386,25 +412,12 @@ __device__ void softmax(const PromptParams& p, const Ctx& x, const Work& w, int 
         pk[k] = pack_bf16x2(e.x, e.y);
       }
       st16(ts + 32 * half + 16 * h, pk);
+      tc::wait_st();
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&x.bar[kP + 2 * g + h]);
     }
     l += sum.x + sum.y;
-    const int valid = w.nk - kPromptTile * j;  // keys of the document in this tile
-    if (valid < kPromptTile) {
-      // rows past the document's last key hold other rows' data: zeros, so that a
-      // weight of 0 cannot meet a value that is not finite (each half: 64 columns)
-      const int c = kChunks * j + kQChunks + half;
-      x.wait_warp(kVFull + (j & 1), j >> 1);
-      if (row >= valid) {
-        uint4* dst = reinterpret_cast<uint4*>(x.smem + Smem::ring + c % kRing * kSlotBytes + row * 128);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) dst[u] = make_uint4(0, 0, 0, 0);
-      }
-      tc::fence_proxy_async();
-    }
-    tc::wait_st();
-    tc::fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&x.bar[kP + g]);
   }
   // the halves' sums (both have read the last maximum: its meeting is behind them
   // only once each has come here)
@@ -448,7 +461,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) mla_prompt_kernel(const __grid
   x.abort = misc + 1;
   x.err = p.ws_err;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < Smem::nbars; ++i) mbar_init(&x.bar[i], i == kP || i == kP + 1 ? 8 : (i == kEnd ? 2 : 1));
+    for (int i = 0; i < Smem::nbars; ++i) mbar_init(&x.bar[i], i >= kP && i < kP + 4 ? 8 : (i == kEnd ? 2 : 1));
     misc[1] = 0;
     fence_mbar_init();
   }
@@ -485,7 +498,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) mla_prompt_kernel(const __grid
   } else {
     const int g = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);
     x.tmem = __shfl_sync(0xffffffffu, x.tmem, 0);
-    mmas(x, g, __shfl_sync(0xffffffffu, g ? n1 : n0, 0));
+    mmas(x, g, __shfl_sync(0xffffffffu, g ? n1 : n0, 0), __shfl_sync(0xffffffffu, g ? n0 : n1, 0));
     // every MMA of both is complete before tensor memory is given back
     __syncwarp();
     if (elect()) tc::commit(&x.bar[kEnd]);
