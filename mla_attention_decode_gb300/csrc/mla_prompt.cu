@@ -10,8 +10,8 @@
 //   O_g += P_g V_j        128 x 128, k = 128: 8 MMAs, P_g from tensor memory, V_j
 //                         MN-major from shared memory as TMA leaves it
 // The two tiles alternate: while the softmax warps of one turn S into P, the
-// tensor cores work for the other, so neither waits for long.  m is raised (and O,
-// l rescaled) only when a row's maximum exceeds it by 2^8.
+// tensor cores work for the other, so neither waits for long.  m is the row's maximum
+// over its first key tile, raised (and O, l rescaled) only far above it.
 //
 // What a row sees is always a run from the document's first key (causal order, or
 // a prefix, whichever is longer, or everything), so the mask is one length per row,
@@ -21,6 +21,8 @@
 // against 2 x 128 exponentials a row and tile.  Shared memory: 96 KB of queries, a
 // ring of 8 slots of 16 KB (64 columns x 128 keys: a K tile is three, a V tile two).
 // Tensor memory: S_0 S_1 O_0 O_1 of 128 columns each.
+#include <climits>
+
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -36,7 +38,9 @@ constexpr int kQChunks = 3, kVChunks = 2, kChunks = kQChunks + kVChunks;
 constexpr int kSoftWarps = 16;         // 0-7, 8-15: softmax of tile 0 and 1
 constexpr int kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;  // MMAs of tile 0; the next warp: of tile 1
 constexpr int kWarps = kSoftWarps + 3;
-constexpr float kRaise = 8.f;
+// m is raised when a row's maximum exceeds it by 2^24 (P and the sums keep their
+// relative precision in bf16 and fp32 whatever their size; O stays below 2^54 max|v|).
+constexpr float kRaise = 24.f;
 
 struct Smem {
   static constexpr int q = 0;                                  // [2 tiles][3 chunks]
@@ -116,6 +120,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+// Whether any of 64 threads (two warps, named barrier `id`) says so; all have come here.
+__device__ __forceinline__ bool any_of_pair(uint32_t id, bool says) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "bar.red.or.pred p, %1, 64, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)says)
+      : "memory");
+  return r != 0;
 }
 // 16 consecutive 32-bit TMEM columns of this thread's lane.
 __device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -329,14 +344,15 @@ __device__ void mmas(const Ctx& x, int g, int n, int other) {
 
 // ------------------------------------------------------------------ softmax
 // Two warps a 32-row quarter of a tile: warp `half` has its columns [64 half, +64), so
-// that each SM sub-partition has four warps to choose from.  The two meet once a key
-// tile, to find the row's maximum.  No wait is left early: a warp that gives up
+// that each SM sub-partition has four warps to choose from.  The two meet at a barrier
+// once a key tile, which tells whether any of them has to raise its maximum: only
+// then do they exchange maxima.  No wait is left early: a warp that gives up
 // (abort) still comes to every meeting.
 __device__ void softmax(const PromptParams& p, const Ctx& x, const Work& w, int head, int g, int n) {
   const int half = (threadIdx.x >> 7) & 1, ww = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const int row = 32 * ww + lane, i = 128 * g + row;  // of the tile, of the CTA
   const bool mine = i < w.rows;
-  const int lim = mine ? seen(p, w, i) : 0;
+  const int lim = mine ? seen(p, w, i) : INT_MAX;  // (what rows of no token hold is not written)
   const uint32_t lanes = x.tmem + ((uint32_t)(32 * ww) << 16);
   const uint32_t ts = lanes + s_col(g), to = lanes + o_col(g) + 64 * half;
   float* const meet = reinterpret_cast<float*>(x.smem + Smem::meet) + 256 * g + row;  // + 128 per half
@@ -362,11 +378,12 @@ __device__ void softmax(const PromptParams& p, const Ctx& x, const Work& w, int 
 #pragma unroll
       for (int u = 0; u < 4; ++u) t[u] = max3(t[u], s[k + u], s[k + 4 + u]);
     const float most = fmaxf(max3(t[0], s[60], s[61]), max3(max3(t[1], t[2], t[3]), s[62], s[63]));
-    meet[128 * half] = most;
-    named_bar_sync(pair, 64);  // both have their scores in registers, and each other's maximum
-    const float top = fmaxf(most, meet[128 * (half ^ 1)]) * p.scale_log2;
-    const bool raise = top > m + kRaise;
-    if (__any_sync(0xffffffffu, raise)) {
+    // from here on both have their scores in registers (the weights go over them)
+    if (any_of_pair(pair, most * p.scale_log2 > m + kRaise)) {
+      meet[128 * half] = most;
+      named_bar_sync(pair, 64);
+      const float top = fmaxf(most, meet[128 * (half ^ 1)]) * p.scale_log2;
+      const bool raise = top > m + kRaise;
       const float f = !raise ? 1.f : (m == -INFINITY ? 0.f : fast_exp2(m - top));
       if (raise) m = top;
       l *= f;
@@ -419,8 +436,7 @@ __device__ void softmax(const PromptParams& p, const Ctx& x, const Work& w, int 
     }
     l += sum.x + sum.y;
   }
-  // the halves' sums (both have read the last maximum: its meeting is behind them
-  // only once each has come here)
+  // the halves' sums (once both have read what they met for last)
   named_bar_sync(pair, 64);
   meet[128 * half] = l;
   named_bar_sync(pair, 64);
