@@ -36,8 +36,7 @@ constexpr int kSlotBytes = 128 * 128;  // 128 rows of 64 bf16 columns
 constexpr int kRing = 8;
 constexpr int kQChunks = 3, kVChunks = 2, kChunks = kQChunks + kVChunks;
 constexpr int kSoftWarps = 16;         // 0-7, 8-15: softmax of tile 0 and 1
-constexpr int kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;  // MMAs of tile 0; the next warp: of tile 1
-constexpr int kWarps = kSoftWarps + 3;
+constexpr int kCopyWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1, kWarps = kSoftWarps + 2;
 // m is raised when a row's maximum exceeds it by 2^24 (P and the sums keep their
 // relative precision in bf16 and fp32 whatever their size; O stays below 2^54 max|v|).
 constexpr float kRaise = 24.f;
@@ -46,7 +45,7 @@ struct Smem {
   static constexpr int q = 0;                                  // [2 tiles][3 chunks]
   static constexpr int ring = q + 2 * kQChunks * kSlotBytes;
   static constexpr int bars = ring + kRing * kSlotBytes;
-  static constexpr int nbars = 21;
+  static constexpr int nbars = 19;
   static constexpr int meet = bars + 8 * (nbars + 1);          // float [2 tiles][2 halves][128 rows]
   static constexpr int misc = meet + 2 * 2 * 128 * 4;          // tmem base, abort
   static constexpr int total = misc + 32;
@@ -59,8 +58,7 @@ enum {
   kS = 6,      // [2 tiles][2] scores written (their K tile read)
   kO = 10,     // [2 tiles][2] products with V added to O (their V tile and weights read)
   kP = 14,     // [2 tiles][2] weights of the even, odd 32 keys written, O rescaled (8 warps)
-  kTurn = 18,  // [2 tiles] a tile's MMAs of one key tile issued
-  kEnd = 20    // both MMA threads' last operation
+  kEnd = 18    // the last MMA
 };
 
 // TMEM columns
@@ -275,70 +273,75 @@ __device__ void copies(const PromptParams& p, const Ctx& x, const Work& w, int h
 }
 
 // ------------------------------------------------------------------ MMAs
-// One warp a query tile (its elected lane issues; the descriptors are the same in
-// every lane, so that they stay in uniform registers), in this order: S(0), then for every key tile j O(j),
-// S(j + 1).  MMAs of one thread execute in the order of their issue, so S(j + 1) may
-// overwrite the weights of tile j, which O(j) read before it.  (One thread for both
-// tiles: its waits, commits and issues take longer than the MMAs, and 1.5 times as
-// long a call.)  Descriptors are a constant high word and a low word to which
-// addresses / 16 are added.
-__device__ void mmas(const Ctx& x, int g, int n, int other) {
-  const uint32_t ring = smem_u32(x.smem + Smem::ring) >> 4, q = (smem_u32(x.smem + Smem::q) + g * kQChunks * kSlotBytes) >> 4;
-  const uint32_t sc = x.tmem + s_col(g), oc = x.tmem + o_col(g);
+// One warp, of which an elected lane issues (the descriptors are the same in every
+// lane, so that they stay in uniform registers), in this order: S_0(0) S_1(0), then for
+// every key tile j O_0(j) S_0(j + 1) O_1(j) S_1(j + 1).  MMAs of one thread execute in
+// the order of their issue, so S_g(j + 1) may overwrite the weights of tile j, which
+// O_g(j) read before it; and the query tiles stay half a period apart, one's softmax
+// under the other's MMAs.  Descriptors are a constant high word and a low word to
+// which addresses / 16 are added.
+__device__ void mmas(const Ctx& x, int n0, int n1) {
+  const uint32_t ring = smem_u32(x.smem + Smem::ring) >> 4, q = smem_u32(x.smem + Smem::q) >> 4;
   constexpr uint32_t kSlot = kSlotBytes >> 4;
-  auto scores = [&](int j) {
-    const uint32_t a0 = (uint32_t)kTplK + q;
-    if (!elect()) return;
+  auto scores = [&](int g, int j) {
+    const uint32_t a0 = (uint32_t)kTplK + q + g * kQChunks * kSlot;
 #pragma unroll
     for (int c = 0; c < kQChunks; ++c) {
       const uint32_t b0 = (uint32_t)kTplK + ring + (kChunks * j + c) % kRing * kSlot;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        mma_ss(sc, a0 + c * kSlot + 2 * k, b0 + 2 * k, (uint32_t)(kTplK >> 32), kIdescS, c + k > 0);
+        mma_ss(x.tmem + s_col(g), a0 + c * kSlot + 2 * k, b0 + 2 * k, (uint32_t)(kTplK >> 32), kIdescS, c + k > 0);
     }
     tc::commit(&x.bar[kS + 2 * g + (j & 1)]);
   };
   // 16-key steps of the weights: the first, second 32 keys of each 64
-  auto values = [&](int j, int part) {
+  auto values = [&](int g, int j, int part) {
     const uint32_t s0 = (kChunks * j + kQChunks) % kRing;
     const uint32_t b0 = (uint32_t)kTplV + ring + s0 * kSlot;
-    if (!elect()) return;
+    const uint32_t a0 = x.tmem + s_col(g), d = x.tmem + o_col(g);
     if (s0 + 1 < kRing) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int k = 4 * (i >> 1) + 2 * part + (i & 1);
-        mma_ts(oc, sc + 8 * k, b0 + 128 * k, (uint32_t)(kTplV >> 32), kIdescO, (j > 0) | (part + i > 0));
+        mma_ts(d, a0 + 8 * k, b0 + 128 * k, (uint32_t)(kTplV >> 32), kIdescO, (j > 0) | (part + i > 0));
       }
     } else {  // the second 64 columns are in the ring's first slot
       const uint32_t b1 = (uint32_t)kTplV + ring;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int k = 4 * (i >> 1) + 2 * part + (i & 1);
-        mma_ts(oc, sc + 8 * k, b0 + 128 * k, (uint32_t)(kTplV >> 32), kIdescOHalf, (j > 0) | (part + i > 0));
-        mma_ts(oc + 64, sc + 8 * k, b1 + 128 * k, (uint32_t)(kTplV >> 32), kIdescOHalf, (j > 0) | (part + i > 0));
+        mma_ts(d, a0 + 8 * k, b0 + 128 * k, (uint32_t)(kTplV >> 32), kIdescOHalf, (j > 0) | (part + i > 0));
+        mma_ts(d + 64, a0 + 8 * k, b1 + 128 * k, (uint32_t)(kTplV >> 32), kIdescOHalf, (j > 0) | (part + i > 0));
       }
     }
     if (part) tc::commit(&x.bar[kO + 2 * g + (j & 1)]);
   };
-  if (n == 0) return;
-  if (!x.wait_warp(kQ + g, 0) || !x.wait_warp(kKFull, 0)) return;
-  tc::fence_after();
-  scores(0);
+  const int n = max(n0, n1);
+  if (n == 0 || !x.wait_warp(kKFull, 0)) return;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    if ((g ? n1 : n0) == 0) continue;
+    if (!x.wait_warp(kQ + g, 0)) return;
+    tc::fence_after();
+    if (elect()) scores(g, 0);
+  }
   for (int j = 0; j < n; ++j) {
-    if (!x.wait_warp(kVFull + (j & 1), j >> 1) || !x.wait_warp(kP + 2 * g, j)) return;
-    // the other tile's turn comes first: tile 0 follows tile 1's previous key tile
-    if (g == 0 ? (j > 0 && j - 1 < other) : j < other)
-      if (!x.wait_warp(kTurn + (g ^ 1), g == 0 ? j - 1 : j)) return;
-    tc::fence_after();
-    values(j, 0);
-    if (!x.wait_warp(kP + 2 * g + 1, j)) return;
-    tc::fence_after();
-    values(j, 1);
-    if (j + 1 < n) {
-      if (!x.wait_warp(kKFull + ((j + 1) & 1), (j + 1) >> 1)) return;
-      scores(j + 1);
+    if (!x.wait_warp(kVFull + (j & 1), j >> 1)) return;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int ng = g ? n1 : n0;
+      if (j >= ng) continue;
+      if (!x.wait_warp(kP + 2 * g, j)) return;
+      tc::fence_after();
+      if (elect()) values(g, j, 0);
+      if (!x.wait_warp(kP + 2 * g + 1, j)) return;
+      tc::fence_after();
+      if (elect()) values(g, j, 1);
+      if (j + 1 < ng) {
+        if (!x.wait_warp(kKFull + ((j + 1) & 1), (j + 1) >> 1)) return;
+        if (elect()) scores(g, j + 1);
+      }
     }
-    if (elect()) mbar_arrive(&x.bar[kTurn + g]);
   }
 }
 
@@ -477,7 +480,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) mla_prompt_kernel(const __grid
   x.abort = misc + 1;
   x.err = p.ws_err;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < Smem::nbars; ++i) mbar_init(&x.bar[i], i >= kP && i < kP + 4 ? 8 : (i == kEnd ? 2 : 1));
+    for (int i = 0; i < Smem::nbars; ++i) mbar_init(&x.bar[i], i >= kP && i < kP + 4 ? 8 : 1);
     misc[1] = 0;
     fence_mbar_init();
   }
@@ -512,10 +515,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) mla_prompt_kernel(const __grid
   } else if (warp == kCopyWarp) {
     if (lane == 0) copies(p, x, w, head, n0, n1);
   } else {
-    const int g = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);
     x.tmem = __shfl_sync(0xffffffffu, x.tmem, 0);
-    mmas(x, g, __shfl_sync(0xffffffffu, g ? n1 : n0, 0), __shfl_sync(0xffffffffu, g ? n0 : n1, 0));
-    // every MMA of both is complete before tensor memory is given back
+    mmas(x, __shfl_sync(0xffffffffu, n0, 0), __shfl_sync(0xffffffffu, n1, 0));
+    // every MMA is complete before tensor memory is given back
     __syncwarp();
     if (elect()) tc::commit(&x.bar[kEnd]);
     const uint64_t t0 = global_timer_ns();
