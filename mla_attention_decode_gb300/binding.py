@@ -231,20 +231,25 @@ def mla_decode_fwd_static(q, kv, kv_scale, kv_indptr, qo_indptr, out, lse, plan:
         raise MLAError(rc, "mla_decode_fwd_static")
 
 
-def _scale_stride(kv_dtype: int, kv_scale) -> int:
-    """Bytes between the rows' scales, where rows have scales of their own."""
-    if kv_scale is None:
-        return 0
-    if kv_dtype == MLA_KV_MXFP4:
-        return int(kv_scale.stride(0))
-    if kv_dtype == MLA_KV_FP8_ROW:
-        if kv_scale.dtype != torch.float32 or kv_scale.dim() != 1:
-            raise ValueError(f"kv_scale is fp32 [rows]: got {kv_scale.dtype} {tuple(kv_scale.shape)}")
-        return 4 * int(kv_scale.stride(0)) if kv_scale.numel() > 1 else 4  # (one scale has no stride)
-    return 0
+class _Decoder:
+    """The compiled call of a decoder: what it needs of the plan and the workspace, made again when
+    either is another object (the plan's fields are read at each call)."""
+
+    _core = _of = _ext = None
+
+    def _decode(self, what, *args):
+        if self._core is None or self._of[0] is not self.plan or self._of[1] is not self.workspace:
+            from .cache import extension
+            self._ext, self._of, w = extension(), (self.plan, self.workspace), self.workspace
+            self._core = self._ext.decode_core(ctypes.addressof(self.plan), w.data_ptr(), w.numel() * w.element_size(),
+                                               w.device.index)
+        rc, out, lse = self._ext.decode(self._core, *args)
+        if rc:
+            raise MLAError(rc, what)
+        return out, lse
 
 
-class MLADecoder:
+class MLADecoder(_Decoder):
     """Plan + workspace for one batch layout; call it with device tensors.
 
     The workspace is allocated once here (torch device memory) and zeroed; the
@@ -269,21 +274,13 @@ class MLADecoder:
 
     def __call__(self, q, kv, kv_indptr, qo_indptr, kv_scale=None, out=None, lse=None,
                  sm_scale: float = SM_SCALE, stream=None):
-        batch = self.plan.batch
-        if out is None:
-            out = torch.empty(batch, 16, 512, dtype=torch.bfloat16, device=self.workspace.device)
-        if lse is None:
-            lse = torch.empty(batch, 16, dtype=torch.float32, device=self.workspace.device)
-        scale_stride = _scale_stride(self.kv_dtype, kv_scale)
-        mla_decode_fwd(q, kv, kv_scale, kv_indptr, qo_indptr, out, lse, self.plan, self.workspace,
-                       sm_scale=sm_scale, scale_stride=scale_stride, stream=stream)
-        return out, lse
+        return self._decode("mla_decode_fwd", q, kv, kv_scale, kv_indptr, None, None, qo_indptr, out, lse, sm_scale, stream)
 
     def poll_error(self, stream=None) -> int:
         return mla_decode_poll_error(self.workspace, stream)
 
 
-class PagedMLADecoder:
+class PagedMLADecoder(_Decoder):
     """Plan + workspace for one paged batch layout (see mla_decode_plan_paged)."""
 
     def __init__(self, kv_page_indptr_host, kv_last_page_len_host, page_size: int, num_pages: int, kv_dtype,
@@ -298,16 +295,8 @@ class PagedMLADecoder:
 
     def __call__(self, q, kv_pages, kv_page_indptr, kv_indices, kv_last_page_len, qo_indptr, kv_scale=None,
                  out=None, lse=None, sm_scale: float = SM_SCALE, stream=None):
-        batch = self.plan.batch
-        if out is None:
-            out = torch.empty(batch, 16, 512, dtype=torch.bfloat16, device=self.workspace.device)
-        if lse is None:
-            lse = torch.empty(batch, 16, dtype=torch.float32, device=self.workspace.device)
-        scale_stride = _scale_stride(self.kv_dtype, kv_scale)
-        mla_decode_fwd_paged(q, kv_pages, kv_scale, kv_page_indptr, kv_indices, kv_last_page_len, qo_indptr, out,
-                             lse, self.plan, self.workspace, sm_scale=sm_scale, scale_stride=scale_stride,
-                             stream=stream)
-        return out, lse
+        return self._decode("mla_decode_fwd_paged", q, kv_pages, kv_scale, kv_page_indptr, kv_indices, kv_last_page_len,
+                            qo_indptr, out, lse, sm_scale, stream)
 
     def poll_error(self, stream=None) -> int:
         return mla_decode_poll_error(self.workspace, stream)

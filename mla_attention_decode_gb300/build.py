@@ -1,5 +1,5 @@
 """Builds libmla_decode.so in-tree with nvcc for sm_103a (no cmake, no torch), and
-_mla_cache.so, the compiled argument marshalling of ``cache.py`` (g++, against
+_mla_cache.so, the compiled argument marshalling of the Python layer (g++, against
 the installed torch's headers).
 
 Each .cu translation unit is compiled in parallel, then linked into one shared
@@ -68,7 +68,7 @@ def _compile(src: str, verbose: bool, out_dir: str = BUILD, defines: tuple = ())
 def _ext_stale() -> bool:
     """Older than its sources, or built for another torch (a file beside it says which)."""
     import torch
-    deps = [EXT_SRC, os.path.join(INCLUDE, "mla_cache.h"), os.path.join(INCLUDE, "mla_decode.h")]
+    deps = [EXT_SRC, *glob.glob(os.path.join(INCLUDE, "*.h"))]
     if not os.path.exists(EXT) or any(os.path.getmtime(d) > os.path.getmtime(EXT) for d in deps):
         return True
     return not os.path.exists(EXT_TORCH) or open(EXT_TORCH).read() != str(torch.__version__)

@@ -119,8 +119,16 @@ def load_library() -> ctypes.CDLL:
             if built_for != this:
                 raise RuntimeError(f"{EXT_PATH} was built for torch {built_for}, this is {this}: build it again")
             ext.bind(*(ctypes.cast(getattr(lib, "mla_cache_" + n), ctypes.c_void_p).value for n in _ENTRY_POINTS))
+            ext.bind_attention(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in
+                                 ("mla_decode_fwd", "mla_decode_fwd_paged", "mla_prompt_fwd")))
             _ext, _lib = ext, lib
     return _lib
+
+
+def extension():
+    """The extension, loaded with the library."""
+    load_library()
+    return _ext
 
 
 class MLARope:

@@ -1,15 +1,17 @@
-// mla_cache_ext.cpp -- the Python side of mla_cache.h: checks of tensors and
-// packing of arguments, compiled.
+// mla_cache_ext.cpp -- the Python side of mla_cache.h, and of the calls of
+// mla_decode.h and mla_prompt.h that a step makes: checks of tensors and packing
+// of arguments, compiled.
 //
 // A decode step makes several of these calls, and each launch takes the host
 // about 1.5 us; checking and packing the arguments of one in Python took 6 to
 // 10 us on the Grace cores, several times the kernel's own time at small
-// batches.  Here it takes a few tenths.  The module knows nothing of CUDA
+// batches (a decode 15 to 20, a prompt call 40).  Here it takes a few tenths.  The module knows nothing of CUDA
 // kernels: it calls the entry points of libmla_decode.so by the addresses that
 // `bind` gives it, and returns their status.
 //
-// Every function takes a pool's core first (a capsule made by `core`) and the
-// stream last: None (torch's current stream of the pool's device), a handle, or
+// Every function takes a core first (a capsule: a pool's, made by `core`, a
+// decoder's by `decode_core`, a prompt's by `prompt_core`) and the
+// stream last: None (torch's current stream of the core's device), a handle, or
 // an object with a cuda_stream.  What a tensor must be and is not is a
 // ValueError; C++ exceptions become Python ones before they leave.
 #include <Python.h>
@@ -25,6 +27,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "mla_cache.h"
+#include "mla_prompt.h"
 
 namespace {
 
@@ -39,11 +42,31 @@ struct Entry {
   decltype(&mla_cache_compact) compact;
 } g_lib;
 
-struct Core {
+struct {
+  decltype(&mla_decode_fwd) decode;
+  decltype(&mla_decode_fwd_paged) decode_paged;
+  decltype(&mla_prompt_fwd) prompt;
+} g_attention;
+
+struct Device {
+  int device;
+};
+struct Core : Device {
   mla_cache cache;
   int32_t* workspace;  // its first word is the error word
   size_t workspace_bytes;
-  int device;
+};
+struct DecodeCore : Device {
+  const mla_plan* plan;  // the decoder's own, which keeps it
+  void* workspace;
+  size_t workspace_bytes;
+};
+struct PromptCore : Device {
+  void* workspace;
+  size_t workspace_bytes;
+  int64_t tokens, keys, batch;  // at most
+  int32_t heads, causal;
+  float sm_scale;
 };
 
 PyObject* s_address;
@@ -64,10 +87,28 @@ struct PyError {};
   throw PyError{};
 }
 
-Core* core_of(PyObject* o) {
-  auto* c = static_cast<Core*>(PyCapsule_GetPointer(o, "mla_cache_core"));
+template <class C>
+const char* name_of();
+template <>
+const char* name_of<Core>() { return "mla_cache_core"; }
+template <>
+const char* name_of<DecodeCore>() { return "mla_decode_core"; }
+template <>
+const char* name_of<PromptCore>() { return "mla_prompt_core"; }
+
+template <class C = Core>
+C* core_of(PyObject* o) {
+  auto* c = static_cast<C*>(PyCapsule_GetPointer(o, name_of<C>()));
   if (!c) throw PyError{};
   return c;
+}
+template <class C>
+void drop(PyObject* o) { delete static_cast<C*>(PyCapsule_GetPointer(o, name_of<C>())); }
+template <class C>
+PyObject* capsule(C* c) {
+  PyObject* o = PyCapsule_New(c, name_of<C>(), drop<C>);
+  if (!o) delete c;
+  return o;
 }
 
 long long whole(PyObject* o) {
@@ -85,17 +126,17 @@ long long attr(PyObject* o, PyObject* name) {
   return v;
 }
 
-// A CUDA tensor of the pool's device and the type.
-const at::Tensor& tensor(const Core* c, PyObject* o, const char* what, at::ScalarType type, const char* type_name) {
+// A CUDA tensor of the core's device and the type.
+const at::Tensor& tensor(const Device* c, PyObject* o, const char* what, at::ScalarType type, const char* type_name) {
   if (!THPVariable_Check(o)) refuse("%s is a tensor", what);
   const at::Tensor& t = THPVariable_Unpack(o);
-  if (!t.is_cuda() || t.get_device() != c->device) refuse("%s is on cuda:%d, the cache's device", what, c->device);
+  if (!t.is_cuda() || t.get_device() != c->device) refuse("%s is on cuda:%d, the call's device", what, c->device);
   if (t.scalar_type() != type) refuse("%s is %s", what, type_name);
   return t;
 }
 
 // A vector of consecutive int32; size < 0: of any length.
-int32_t* vec(const Core* c, PyObject* o, const char* what, int64_t size, int64_t* numel = nullptr) {
+int32_t* vec(const Device* c, PyObject* o, const char* what, int64_t size, int64_t* numel = nullptr) {
   const at::Tensor& t = tensor(c, o, what, at::kInt, "int32");
   if (t.dim() != 1 || (t.size(0) > 1 && t.stride(0) != 1)) refuse("%s is a contiguous vector", what);
   if (size >= 0 && t.size(0) != size)
@@ -147,13 +188,13 @@ mla_page_table table(const Core* c, PyObject* o, const char* what) {
   return t;
 }
 
-// The stream a call runs on, and the pool's device made current for as long.
+// The stream a call runs on, and the core's device made current for as long.
 struct Where {
   c10::cuda::OptionalCUDAGuard guard;
   c10::cuda::CUDAStream current;
   void* handle;
   bool given;
-  Where(const Core* c, PyObject* stream)
+  Where(const Device* c, PyObject* stream)
       : current(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(c->device))),
         given(stream != Py_None) {
     if (c10::cuda::current_device() != c->device) guard.set_index(static_cast<c10::DeviceIndex>(c->device));
@@ -168,7 +209,7 @@ struct Where {
 };
 
 // New memory that belongs to the stream of the call.
-at::Tensor fresh(const Core* c, const Where& w, at::IntArrayRef shape, at::ScalarType type) {
+at::Tensor fresh(const Device* c, const Where& w, at::IntArrayRef shape, at::ScalarType type) {
   const auto options = at::TensorOptions().dtype(type).device(at::kCUDA, static_cast<c10::DeviceIndex>(c->device));
   if (!w.given) return at::empty(shape, options);
   const c10::cuda::CUDAStreamGuard on(c10::cuda::getStreamFromExternal(
@@ -404,18 +445,184 @@ PyObject* py_compact(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   END
 }
 
-void drop_core(PyObject* o) { delete static_cast<Core*>(PyCapsule_GetPointer(o, "mla_cache_core")); }
-
 // core(address of an mla_cache, workspace address, its bytes, device index) -> capsule
 PyObject* py_core(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   ARGS(4)
   BEGIN
-  Core* c = new Core{*static_cast<const mla_cache*>(PyLong_AsVoidPtr(a[0])),
-                     static_cast<int32_t*>(PyLong_AsVoidPtr(a[1])), static_cast<size_t>(whole(a[2])),
-                     static_cast<int>(whole(a[3]))};
-  PyObject* o = PyCapsule_New(c, "mla_cache_core", drop_core);
-  if (!o) delete c;
-  return o;
+  const int device = static_cast<int>(whole(a[3]));
+  const size_t bytes = static_cast<size_t>(whole(a[2]));
+  return capsule(new Core{{device}, *static_cast<const mla_cache*>(PyLong_AsVoidPtr(a[0])),
+                          static_cast<int32_t*>(PyLong_AsVoidPtr(a[1])), bytes});
+  END
+}
+
+// decode_core(address of an mla_plan, workspace address, its bytes, device index) -> capsule
+PyObject* py_decode_core(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  ARGS(4)
+  BEGIN
+  const int device = static_cast<int>(whole(a[3]));
+  const size_t bytes = static_cast<size_t>(whole(a[2]));
+  return capsule(new DecodeCore{{device}, static_cast<const mla_plan*>(PyLong_AsVoidPtr(a[0])), PyLong_AsVoidPtr(a[1]), bytes});
+  END
+}
+
+// What a decode takes by address: device memory or pinned host memory, as the header says; None: null.
+const at::Tensor* given(PyObject* o, const char* what) {
+  if (o == Py_None) return nullptr;
+  if (!THPVariable_Check(o)) refuse("%s is a tensor", what);
+  return &THPVariable_Unpack(o);
+}
+template <class T = void>
+T* address(PyObject* o, const char* what) {
+  const at::Tensor* t = given(o, what);
+  return t ? static_cast<T*>(t->data_ptr()) : nullptr;
+}
+
+// decode(core, q, kv, kv_scale, indptr, kv_indices, last_page_len, qo_indptr, out, lse, sm_scale, stream)
+//   -> (status, out, lse); kv_indices and last_page_len None: a contiguous cache
+PyObject* py_decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  ARGS(12)
+  BEGIN
+  const DecodeCore* c = core_of<DecodeCore>(a[0]);
+  const mla_plan* plan = c->plan;
+  const void *q = address(a[1], "q"), *kv = address(a[2], "kv");
+  const at::Tensor* scale = given(a[3], "kv_scale");
+  int64_t stride = 0;
+  if (scale && plan->kv_dtype == MLA_KV_MXFP4) {
+    if (scale->dim() < 1) refuse("kv_scale is [rows, >= 18]");
+    stride = scale->stride(0);
+  } else if (scale && plan->kv_dtype == MLA_KV_FP8_ROW) {
+    if (scale->scalar_type() != at::kFloat || scale->dim() != 1) refuse("kv_scale is fp32 [rows]");
+    stride = scale->size(0) > 1 ? 4 * scale->stride(0) : 4;  // (one scale has no stride)
+  }
+  if (stride < 0 || stride > INT32_MAX) refuse("kv_scale's rows are too far apart");
+  const void* scales = scale ? scale->data_ptr() : nullptr;
+  const int32_t *indptr = address<int32_t>(a[4], "kv_indptr"), *indices = address<int32_t>(a[5], "kv_indices"),
+                *last = address<int32_t>(a[6], "kv_last_page_len"), *qo = address<int32_t>(a[7], "qo_indptr");
+  const double sm_scale = PyFloat_AsDouble(a[10]);
+  if (sm_scale == -1.0 && PyErr_Occurred()) throw PyError{};
+  const Where w(c, a[11]);
+  at::Tensor made_out, made_lse;
+  void* out;
+  float* lse;
+  if (a[8] == Py_None) {
+    made_out = fresh(c, w, {plan->batch, MLA_NUM_HEADS, MLA_V_DIM}, at::kBFloat16);
+    out = made_out.data_ptr();
+  } else {
+    out = address(a[8], "out");
+  }
+  if (a[9] == Py_None) {
+    made_lse = fresh(c, w, {plan->batch, MLA_NUM_HEADS}, at::kFloat);
+    lse = static_cast<float*>(made_lse.data_ptr());
+  } else {
+    lse = address<float>(a[9], "lse");
+  }
+  const int rc = without_gil([&] {
+    return plan->page_size ? g_attention.decode_paged(q, kv, scales, (int32_t)stride, indptr, indices, last, qo, out, lse,
+                                                      (float)sm_scale, plan, c->workspace, c->workspace_bytes, w.handle)
+                           : g_attention.decode(q, kv, scales, (int32_t)stride, indptr, qo, out, lse, (float)sm_scale, plan,
+                                                c->workspace, c->workspace_bytes, w.handle);
+  });
+  PyObject* o = a[8] == Py_None ? THPVariable_Wrap(std::move(made_out)) : Py_NewRef(a[8]);
+  PyObject* l = a[9] == Py_None ? THPVariable_Wrap(std::move(made_lse)) : Py_NewRef(a[9]);
+  return Py_BuildValue("(iNN)", rc, o, l);
+  END
+}
+
+// prompt_core(workspace address, its bytes, device index, tokens, keys, batch, heads, causal, sm_scale) -> capsule
+PyObject* py_prompt_core(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  ARGS(9)
+  BEGIN
+  const size_t bytes = static_cast<size_t>(whole(a[1]));
+  const int device = static_cast<int>(whole(a[2]));
+  const int64_t tokens = whole(a[3]), keys = whole(a[4]), batch = whole(a[5]);
+  const int32_t heads = static_cast<int32_t>(whole(a[6])), causal = static_cast<int32_t>(whole(a[7]));
+  const double sm_scale = PyFloat_AsDouble(a[8]);
+  if (sm_scale == -1.0 && PyErr_Occurred()) throw PyError{};
+  return capsule(new PromptCore{{device}, PyLong_AsVoidPtr(a[0]), bytes, tokens, keys, batch, heads, causal, (float)sm_scale});
+  END
+}
+
+// bf16 [rows, (heads,) columns], the last dimension consecutive; its strides.
+const at::Tensor& rows_of(const PromptCore* c, PyObject* o, const char* what, int64_t rows, bool heads, int64_t columns,
+                          int64_t& row_stride, int64_t* head_stride) {
+  const at::Tensor& t = tensor(c, o, what, at::kBFloat16, "bf16");
+  const int d = heads ? 3 : 2;
+  if (t.dim() != d || t.size(0) != rows || (heads && t.size(1) != c->heads) || t.size(d - 1) != columns)
+    refuse("%s is [%lld, %s%lld]", what, (long long)rows, heads ? "heads, " : "", (long long)columns);
+  if (t.stride(d - 1) != 1) refuse("%s: the last dimension is consecutive", what);
+  row_stride = t.stride(0);
+  if (heads) *head_stride = t.stride(1);
+  return t;
+}
+int64_t first_size(PyObject* o, const char* what) {
+  if (!THPVariable_Check(o) || THPVariable_Unpack(o).dim() < 1) refuse("%s is a tensor", what);
+  return THPVariable_Unpack(o).size(0);
+}
+
+// prompt(core, q_nope, q_pe, k_nope, k_pe, v, qo_indptr, kv_indptr, prefix, out, lse, stream) -> (status, out, lse)
+PyObject* py_prompt(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  ARGS(12)
+  BEGIN
+  const PromptCore* c = core_of<PromptCore>(a[0]);
+  const int64_t t = first_size(a[1], "q_nope"), s = first_size(a[3], "k_nope"), b = first_size(a[6], "qo_indptr") - 1;
+  if (t > c->tokens || s > c->keys || b < 0 || b > c->batch)
+    refuse("made for %lld tokens, %lld keys and %lld documents: got %lld, %lld, %lld", (long long)c->tokens, (long long)c->keys,
+           (long long)c->batch, (long long)t, (long long)s, (long long)b);
+  mla_prompt_args g = {};
+  g.q_nope = rows_of(c, a[1], "q_nope", t, true, MLA_PROMPT_NOPE, g.q_nope_token_stride, &g.q_nope_head_stride).data_ptr();
+  g.q_pe = rows_of(c, a[2], "q_pe", t, true, MLA_PROMPT_PE, g.q_pe_token_stride, &g.q_pe_head_stride).data_ptr();
+  g.k_nope = rows_of(c, a[3], "k_nope", s, true, MLA_PROMPT_NOPE, g.k_nope_token_stride, &g.k_nope_head_stride).data_ptr();
+  g.k_pe = rows_of(c, a[4], "k_pe", s, false, MLA_PROMPT_PE, g.k_pe_token_stride, nullptr).data_ptr();
+  g.v = rows_of(c, a[5], "v", s, true, MLA_PROMPT_V, g.v_token_stride, &g.v_head_stride).data_ptr();
+  g.qo_indptr = vec(c, a[6], "qo_indptr", b + 1);
+  g.kv_indptr = vec(c, a[7], "kv_indptr", b + 1);
+  g.prefix = a[8] == Py_None ? nullptr : vec(c, a[8], "prefix", b);
+  g.num_q = count32(t, "q_nope");
+  g.num_kv = count32(s, "k_nope");
+  g.batch = count32(b, "qo_indptr");
+  g.heads = c->heads;
+  g.causal = c->causal;
+  g.sm_scale = c->sm_scale;
+  const Where w(c, a[11]);
+  at::Tensor made_out, made_lse;
+  if (a[9] == Py_None) {
+    made_out = fresh(c, w, {t, c->heads, MLA_PROMPT_V}, at::kBFloat16);
+    g.out = made_out.data_ptr();
+    g.out_token_stride = (int64_t)c->heads * MLA_PROMPT_V;
+    g.out_head_stride = MLA_PROMPT_V;
+  } else {
+    g.out = rows_of(c, a[9], "out", t, true, MLA_PROMPT_V, g.out_token_stride, &g.out_head_stride).data_ptr();
+  }
+  if (a[10] == Py_None) {
+    made_lse = fresh(c, w, {t, c->heads}, at::kFloat);
+    g.lse = static_cast<float*>(made_lse.data_ptr());
+  } else {
+    const at::Tensor& l = tensor(c, a[10], "lse", at::kFloat, "fp32");
+    if (l.dim() != 2 || l.size(0) != t || l.size(1) != c->heads || !l.is_contiguous())
+      refuse("lse is [%lld, %d], contiguous", (long long)t, c->heads);
+    g.lse = static_cast<float*>(l.data_ptr());
+  }
+  const int rc = without_gil([&] { return g_attention.prompt(&g, c->workspace, c->workspace_bytes, w.handle); });
+  PyObject* o = a[9] == Py_None ? THPVariable_Wrap(std::move(made_out)) : Py_NewRef(a[9]);
+  PyObject* l = a[10] == Py_None ? THPVariable_Wrap(std::move(made_lse)) : Py_NewRef(a[10]);
+  return Py_BuildValue("(iNN)", rc, o, l);
+  END
+}
+
+// bind_attention(addresses of mla_decode_fwd, mla_decode_fwd_paged, mla_prompt_fwd)
+PyObject* py_bind_attention(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  ARGS(3)
+  BEGIN
+  void* at[3];
+  for (int i = 0; i < 3; ++i) {
+    at[i] = PyLong_AsVoidPtr(a[i]);
+    if (!at[i]) refuse("an entry point has no address");
+  }
+  g_attention.decode = reinterpret_cast<decltype(g_attention.decode)>(at[0]);
+  g_attention.decode_paged = reinterpret_cast<decltype(g_attention.decode_paged)>(at[1]);
+  g_attention.prompt = reinterpret_cast<decltype(g_attention.prompt)>(at[2]);
+  Py_RETURN_NONE;
   END
 }
 
@@ -447,6 +654,11 @@ PyMethodDef methods[] = {METHOD("append", py_append),
                          METHOD("compact", py_compact),
                          METHOD("core", py_core),
                          METHOD("bind", py_bind),
+                         METHOD("decode_core", py_decode_core),
+                         METHOD("decode", py_decode),
+                         METHOD("prompt_core", py_prompt_core),
+                         METHOD("prompt", py_prompt),
+                         METHOD("bind_attention", py_bind_attention),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mla_cache", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -2,8 +2,8 @@
 
 ``MLAPrompt`` is the workspace of one batch layout; a call takes the query
 projection's two parts, the up-projected keys and values, the position part of
-the rows, and the documents' bounds.  As in ``mla_attention_decode_gb300.binding``
-this marshals arguments only, nothing synchronises, and what only the device can
+the rows, and the documents' bounds.  As in ``mla_attention_decode_gb300.cache``
+this marshals arguments only (compiled), nothing synchronises, and what only the device can
 see is reported by ``poll_error``.
 
 The next chunk of a prompt whose context is cached:
@@ -22,7 +22,8 @@ import math
 import torch
 
 from . import binding
-from .binding import MLA_OK, MLAError
+from .binding import MLAError
+from .cache import extension
 
 NOPE, PE, V = 128, 64, 128
 _STRIDES = ("q_nope_token_stride", "q_nope_head_stride", "q_pe_token_stride", "q_pe_head_stride", "k_nope_token_stride",
@@ -66,12 +67,9 @@ class MLAPrompt:
             raise MLAError(binding.MLA_ERR_INVALID_ARG, "mla_prompt_workspace_bytes")
         self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=device)
         self.device = self.workspace.device
-
-    def _check(self, name, t, dtype, shape):
-        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != shape:
-            raise ValueError(f"{name} is {dtype} {shape} on {self.device}: got {t.dtype} {tuple(t.shape)} on {t.device}")
-        if t.dim() and t.numel() and t.stride(-1) != 1 and t.shape[-1] != 1:
-            raise ValueError(f"{name}: the last dimension is consecutive")
+        self._ext = extension()
+        self._core = self._ext.prompt_core(self.workspace.data_ptr(), nbytes, self.device.index, self.num_tokens, self.num_keys,
+                                           self.batch, self.heads, int(self.causal), self.sm_scale)
 
     def __call__(self, q_nope, q_pe, k_nope, k_pe, v, qo_indptr, kv_indptr, prefix=None, out=None, lse=None, stream=None):
         """Attention of the query tokens over their documents' keys: (out [T, heads, 128] bf16, lse [T, heads]).
@@ -80,38 +78,8 @@ class MLAPrompt:
         bf16, any strides that are multiples of 8.  ``qo_indptr``, ``kv_indptr`` int32 [documents + 1]; ``prefix``
         int32 [documents]: that many keys are seen by every token.  Rows of no document are left as they were
         in ``out`` and ``lse`` (unset without them)."""
-        t, s, b = q_nope.shape[0], k_nope.shape[0], qo_indptr.shape[0] - 1
-        h, bf, i32 = self.heads, torch.bfloat16, torch.int32
-        if t > self.num_tokens or s > self.num_keys or not 0 <= b <= self.batch:
-            raise ValueError(f"made for {self.num_tokens} tokens, {self.num_keys} keys and {self.batch} documents: got {t}, {s}, {b}")
-        for name, x, dtype, shape in (("q_nope", q_nope, bf, (t, h, NOPE)), ("q_pe", q_pe, bf, (t, h, PE)),
-                                      ("k_nope", k_nope, bf, (s, h, NOPE)), ("k_pe", k_pe, bf, (s, PE)),
-                                      ("v", v, bf, (s, h, V)), ("qo_indptr", qo_indptr, i32, (b + 1,)),
-                                      ("kv_indptr", kv_indptr, i32, (b + 1,))):
-            self._check(name, x, dtype, shape)
-        if prefix is not None:
-            self._check("prefix", prefix, i32, (b,))
-        if out is None:
-            out = torch.empty(t, h, V, dtype=bf, device=self.device)
-        else:
-            self._check("out", out, bf, (t, h, V))
-        if lse is None:
-            lse = torch.empty(t, h, dtype=torch.float32, device=self.device)
-        else:
-            self._check("lse", lse, torch.float32, (t, h))
-            if not lse.is_contiguous():
-                raise ValueError("lse is contiguous")
-        a = mla_prompt_args(q_nope.data_ptr(), q_pe.data_ptr(), k_nope.data_ptr(), k_pe.data_ptr(), v.data_ptr(),
-                            qo_indptr.data_ptr(), kv_indptr.data_ptr(), None if prefix is None else prefix.data_ptr(),
-                            out.data_ptr(), lse.data_ptr(), q_nope.stride(0), q_nope.stride(1), q_pe.stride(0), q_pe.stride(1),
-                            k_nope.stride(0), k_nope.stride(1), k_pe.stride(0), v.stride(0), v.stride(1), out.stride(0),
-                            out.stride(1), t, s, b, h, self.causal, self.sm_scale)
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        with torch.cuda.device(self.device):
-            rc = self._lib.mla_prompt_fwd(ctypes.addressof(a), self.workspace.data_ptr(), self.workspace.numel(), handle)
-        if rc != MLA_OK:
+        rc, out, lse = self._ext.prompt(self._core, q_nope, q_pe, k_nope, k_pe, v, qo_indptr, kv_indptr, prefix, out, lse, stream)
+        if rc:
             raise MLAError(rc, "mla_prompt_fwd")
         return out, lse
 
