@@ -60,8 +60,9 @@
 // score factor in fp32, and P as s_t 2^-Gv with Gv the running maximum of the
 // scales' exponents (as MXFP4's, each softmax thread fetching its row's scale
 // two tiles ahead).  P's reference is lowered by 4 (P <= 16 after a raise,
-// <= 256 before the next one), which puts the weights that vanish under e4m3's
-// smallest step at 2^-14 of the largest instead of 2^-10.
+// <= 256 before the next one) and its second term is carried 2^4 up in its own
+// columns of O^T: what e4m3's smallest step leaves out of a weight is 2^-18 of the
+// largest instead of 2^-10.
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -1163,15 +1164,17 @@ __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 12
 // the query's two terms).  An unsplit sequence gets bf16 out and lse; a split
 // one an fp32 partial and lse in partial slot u.  l, m: the unit's softmax sum
 // and reference per head (log2 units); out_scale: the factor O^T carries.
-// kNan: a sum that is NaN gives a NaN lse, so that a sequence split over several
-// units keeps it (else an lse of -inf, which the combine takes for an empty unit).
-template <bool kTwo, bool kNan>
+// kRow (row scales): the weights' second term is 2^4 up, and a sum that is NaN gives a
+// NaN lse, so that a sequence split over several units keeps it (else an lse of -inf,
+// which the combine takes for an empty unit).
+template <bool kTwo, bool kRow>
 __device__ __forceinline__ void write_unit(const Stage1Params& p, uint32_t tl_o, uint32_t blk, int row, bool final_out,
                                            int ob, int u, const float (&l)[16], const float (&m)[16],
                                            float out_scale) {
+  constexpr float kLo = kRow ? 0.0625f : 1.f;
   float inv[16];
 #pragma unroll
-  for (int h = 0; h < 16; ++h) inv[h] = (kNan ? l[h] != 0.f : l[h] > 0.f) ? out_scale * __frcp_rn(l[h]) : 0.f;
+  for (int h = 0; h < 16; ++h) inv[h] = (kRow ? l[h] != 0.f : l[h] > 0.f) ? out_scale * __frcp_rn(l[h]) : 0.f;
   // kTwo: two blocks of 128 features per TMEM round trip (MXFP4: 0.1-0.5 us
   // off a bs32/kv8192 split stage in two A/B runs; the e4m3 kernel, which
   // needs four more registers for it, ran bs4/kv8192 1.4 us slower and keeps
@@ -1190,14 +1193,14 @@ __device__ __forceinline__ void write_unit(const Stage1Params& p, uint32_t tl_o,
         uint16_t* op = p.out + (size_t)ob * kHeads * kVDim + f;
 #pragma unroll
         for (int h = 0; h < 16; ++h) {
-          const float v = (__uint_as_float(o[j][h]) + __uint_as_float(o[j][16 + h])) * inv[h];
+          const float v = (__uint_as_float(o[j][h]) + kLo * __uint_as_float(o[j][16 + h])) * inv[h];
           op[h * kVDim] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xffffu);
         }
       } else {
         float* op = p.ws_o + (size_t)u * kHeads * kVDim + f;
 #pragma unroll
         for (int h = 0; h < 16; ++h)
-          op[h * kVDim] = (__uint_as_float(o[j][h]) + __uint_as_float(o[j][16 + h])) * inv[h];
+          op[h * kVDim] = (__uint_as_float(o[j][h]) + kLo * __uint_as_float(o[j][16 + h])) * inv[h];
       }
     }
   }
@@ -1210,7 +1213,7 @@ __device__ __forceinline__ void write_unit(const Stage1Params& p, uint32_t tl_o,
       lh = row == h ? l[h] : lh;
       mh = row == h ? m[h] : mh;
     }
-    const float lse = (kNan ? lh != 0.f : lh > 0.f) ? (mh + fast_log2(lh)) * kLn2 : -INFINITY;
+    const float lse = (kRow ? lh != 0.f : lh > 0.f) ? (mh + fast_log2(lh)) * kLn2 : -INFINITY;
     if (final_out) {
       if (p.lse) p.lse[ob * kHeads + row] = lse;
     } else {
@@ -1515,7 +1518,10 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
           l_part[h] += pr;
           pv[e] = pr * pv_fac;
         }
-        two_term_e4m3(pv[0], pv[1], pv[2], pv[3], hi[g], lo[g]);
+        if constexpr (kRow)
+          two_term_e4m3_up(pv[0], pv[1], pv[2], pv[3], hi[g], lo[g]);
+        else
+          two_term_e4m3(pv[0], pv[1], pv[2], pv[3], hi[g], lo[g]);
       }
       uint8_t* pbuf = x.smem + L::pb + (sb * kTok + ti) * kPBytes + row * 32;
       const int xr = (row >> 2) & 1;  // 32 B swizzle: the 16-byte units of the row swap
