@@ -240,18 +240,36 @@ enum { kStill = 0, kPairs2 = 1, kHalves = 2 };
 __device__ __forceinline__ int turn_kind(const AppendParams& p) {
   return p.rope.num_axes == 0 ? kStill : (p.rope.interleaved ? kPairs2 : kHalves);
 }
-// The lane's two position columns (`u`: their bf16 pair) normed and rotated.
+// The squares of the lane's two position columns (`u`: their bf16 pair), summed.
+__device__ __forceinline__ float squares_pe(uint32_t u) {
+  const float2 x = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  return fmaf(x.x, x.x, x.y * x.y);
+}
+__device__ __forceinline__ float root_pe(float sum, float eps) { return rsqrtf(sum * (1.f / kPe) + eps); }
+// The lane's two position columns normed (by the factor q) and rotated.
 template <int kNorm, int kTurn>
-__device__ __forceinline__ float2 turned_pe(float eps, const Weights& w, const Turn& r, uint32_t u) {
+__device__ __forceinline__ float2 turned_pe(float q, const Weights& w, const Turn& r, uint32_t u) {
   float2 x = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-  if (kNorm) {
-    const float q = rsqrtf(warp_sum(fmaf(x.x, x.x, x.y * x.y)) * (1.f / kPe) + eps);
-    x = mul2(mul2(x, both(q)), make_float2(w.pe[0], w.pe[1]));
-  }
+  if (kNorm) x = mul2(mul2(x, both(q)), make_float2(w.pe[0], w.pe[1]));
   if (kTurn == kStill) return x;
   float2 y = make_float2(x.y, x.x);  // the partners of columns 2 lane, 2 lane + 1
   if (kTurn == kHalves) y = make_float2(__shfl_xor_sync(kFull, x.x, 16), __shfl_xor_sync(kFull, x.y, 16));
   return fma2(x, make_float2(r.c[0], r.c[1]), mul2(y, make_float2(r.s[0], r.s[1])));
+}
+// The sums over the warp of 16 values a lane, value h in lanes 2 h and 2 h + 1: each
+// step hands half of what is left to the lane across, so 16 shuffles instead of 80.
+// The additions are those of warp_sum, pair by pair.
+__device__ __forceinline__ float warp_sums16(float (&v)[16], int lane) {
+#pragma unroll
+  for (int n = 8; n > 0; n >>= 1) {  // values kept; the lane across: 2 n
+    const bool up = lane & (2 * n);
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(kFull, give, 2 * n);
+    }
+  }
+  return v[0] + __shfl_xor_sync(kFull, v[0], 1);
 }
 // f with the call's norm and turn as constants, so that a loop over heads has no
 // branch in it.
@@ -421,7 +439,10 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const __g
     norm_lat(p.norm, MLA_PART_KV_LAT, w, x);
     float2 y;
     by_kind(p.norm.apply >> MLA_PART_KV_PE & 1, turn_kind(p),
-            [&](auto norm, auto turn) { y = turned_pe<norm.value, turn.value>(p.norm.eps, w, r, u); });
+            [&](auto norm, auto turn) {
+              const float q = norm.value ? root_pe(warp_sum(squares_pe(u)), p.norm.eps) : 0.f;
+              y = turned_pe<norm.value, turn.value>(q, w, r, u);
+            });
     store_row<kDtype>(p, slot, scale, x, y, lane);
     return;
   }
@@ -449,9 +470,18 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_append_kernel(const __g
   load_weights_pe(p.norm, MLA_PART_Q_PE, lane, w);
   const Turn r = turn_of(p, t, lane);
   by_kind(p.norm.apply >> MLA_PART_Q_PE & 1, turn_kind(p), [&](auto norm, auto turn) {
+    float roots = 0.f;  // 16 heads: lane 2 h has head h's
+    if constexpr (norm.value && kHeads == 16) {
+      float ss[16];
+#pragma unroll
+      for (int h = 0; h < 16; ++h) ss[h] = squares_pe(u[h]);
+      roots = root_pe(warp_sums16(ss, lane), p.norm.eps);
+    }
 #pragma unroll
     for (int h = 0; h < kHeads; ++h) {
-      const float2 y = turned_pe<norm.value, turn.value>(p.norm.eps, w, r, u[h]);
+      float q = 0.f;
+      if constexpr (norm.value) q = kHeads == 16 ? __shfl_sync(kFull, roots, 2 * h) : root_pe(warp_sum(squares_pe(u[h])), p.norm.eps);
+      const float2 y = turned_pe<norm.value, turn.value>(q, w, r, u[h]);
       reinterpret_cast<uint32_t*>(out + h * (2 * kRow) + 2 * kLat)[lane] = pack_bf16x2(y.x, y.y);
     }
   });
