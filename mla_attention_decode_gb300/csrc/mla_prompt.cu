@@ -152,6 +152,7 @@ struct Work {
   int rows;         // query tokens of this CTA (1..256)
   int first;        // the first one's place in the document
   int nq, nk, prefix;
+  int skip;         // keys before this CTA's share of them (a multiple of 128)
 };
 // How many keys token i (of the CTA) sees.
 __device__ __forceinline__ int seen(const PromptParams& p, const Work& w, int i) {
@@ -189,7 +190,21 @@ __device__ __forceinline__ bool find_work(const PromptParams& p, int slot, int l
   w.k0 = k;
   w.rows = min(kPromptQ, w.nq - w.first);
   w.prefix = p.prefix ? __ldg(p.prefix + lo) : 0;
+  w.skip = 0;
   return true;
+}
+// The document of token t: its bounds fit and hold it.
+__device__ __forceinline__ bool owned(const PromptParams& p, int t, int lane) {
+  int lo = 0, hi = p.batch;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, i = lo + (lane + 1) * step;
+    const int n = __popc(__ballot_sync(0xffffffffu, i < hi && __ldg(p.qo_indptr + i) <= t));
+    lo += n * step;
+    hi = min(hi, lo + step);
+  }
+  const int q = __ldg(p.qo_indptr + lo), qe = __ldg(p.qo_indptr + lo + 1);
+  const int k = __ldg(p.kv_indptr + lo), ke = __ldg(p.kv_indptr + lo + 1);
+  return 0 <= q && q <= t && t < qe && qe <= p.num_q && 0 <= k && k <= ke && ke <= p.num_kv;
 }
 
 struct Ctx {
@@ -351,11 +366,11 @@ __device__ void mmas(const Ctx& x, int n0, int n1) {
 // once a key tile, which tells whether any of them has to raise its maximum: only
 // then do they exchange maxima.  No wait is left early: a warp that gives up
 // (abort) still comes to every meeting.
-__device__ void softmax(const PromptParams& p, const Ctx& x, const Work& w, int head, int g, int n) {
+__device__ void softmax(const PromptParams& p, const Ctx& x, const Work& w, int head, int split, int g, int n) {
   const int half = (threadIdx.x >> 7) & 1, ww = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const int row = 32 * ww + lane, i = 128 * g + row;  // of the tile, of the CTA
   const bool mine = i < w.rows;
-  const int lim = mine ? seen(p, w, i) : INT_MAX;  // (what rows of no token hold is not written)
+  const int lim = mine ? seen(p, w, i) - w.skip : INT_MAX;  // (what rows of no token hold is not written)
   const uint32_t lanes = x.tmem + ((uint32_t)(32 * ww) << 16);
   const uint32_t ts = lanes + s_col(g), to = lanes + o_col(g) + 64 * half;
   float* const meet = reinterpret_cast<float*>(x.smem + Smem::meet) + 256 * g + row;  // + 128 per half
@@ -404,7 +419,7 @@ __device__ void softmax(const PromptParams& p, const Ctx& x, const Work& w, int 
         }
       }
     }
-    const int valid = w.nk - kPromptTile * j;  // keys of the document in this tile
+    const int valid = w.nk - w.skip - kPromptTile * j;  // keys of the document in this tile
     if (valid < kPromptTile) {
       // rows past the document's last key hold other rows' data: zeros, so that a
       // weight of 0 cannot meet a value that is not finite (each half: 64 columns)
@@ -447,6 +462,30 @@ __device__ void softmax(const PromptParams& p, const Ctx& x, const Work& w, int 
   if (n > 0 && !x.wait_warp(kO + 2 * g + ((n - 1) & 1), (n - 1) >> 1)) return;
   tc::fence_after();
   const float inv = l > 0.f ? __frcp_rn(l) : (l == 0.f ? 0.f : l);
+  const float lse = l == 0.f ? -INFINITY : (m + fast_log2(l)) * kLn2;
+  if (p.splits > 1) {
+    const int64_t at = ((int64_t)split * p.num_q + w.q0 + i) * p.heads + head;
+    float4* part = reinterpret_cast<float4*>(p.part_o + at * MLA_PROMPT_V + 64 * half);
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t o[16];
+      if (n > 0) {
+        ld16(to + 16 * c, o);
+        tc::wait_ld();
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (inv != 0.f)
+          y = make_float4(__uint_as_float(o[4 * u]) * inv, __uint_as_float(o[4 * u + 1]) * inv,
+                          __uint_as_float(o[4 * u + 2]) * inv, __uint_as_float(o[4 * u + 3]) * inv);
+        if (mine) part[4 * c + u] = y;
+      }
+      __syncwarp();
+    }
+    if (mine && half == 0) p.part_lse[at] = lse;
+    return;
+  }
   uint4* out = reinterpret_cast<uint4*>(p.out + (int64_t)(w.q0 + i) * p.out_token_stride + (int64_t)head * p.out_head_stride + 64 * half);
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {
@@ -467,7 +506,7 @@ __device__ void softmax(const PromptParams& p, const Ctx& x, const Work& w, int 
     __syncwarp();
   }
   if (mine && half == 0 && p.lse)
-    p.lse[(int64_t)(w.q0 + i) * p.heads + head] = l == 0.f ? -INFINITY : (m + fast_log2(l)) * kLn2;
+    p.lse[(int64_t)(w.q0 + i) * p.heads + head] = lse;
 }
 
 __global__ void __launch_bounds__(32 * kWarps, 1) mla_prompt_kernel(const __grid_constant__ PromptParams p) {
@@ -487,7 +526,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) mla_prompt_kernel(const __grid
   pdl_wait_primary();
   pdl_launch_dependents();
   // the last tiles of a document see the most keys: they go first
-  const int head = (int)blockIdx.x % p.heads, slot = p.slots - 1 - (int)blockIdx.x / p.heads;
+  const int split = (int)blockIdx.x % p.splits, tile = (int)blockIdx.x / p.splits;
+  const int head = tile % p.heads, slot = p.slots - 1 - tile / p.heads;
   Work w;
   const bool any = find_work(p, slot, lane, w);
   if (blockIdx.x == 0) {
@@ -509,9 +549,16 @@ __global__ void __launch_bounds__(32 * kWarps, 1) mla_prompt_kernel(const __grid
   __syncthreads();
   tc::fence_after();
   x.tmem = *reinterpret_cast<uint32_t*>(misc);
-  const int n0 = tiles_of(p, w, 0), n1 = tiles_of(p, w, 1);
+  int n0 = tiles_of(p, w, 0), n1 = tiles_of(p, w, 1);
+  if (p.splits > 1) {
+    const int n = max(n0, n1), lo = n * split / p.splits, hi = n * (split + 1) / p.splits;
+    n0 = max(0, min(n0, hi) - lo);
+    n1 = max(0, min(n1, hi) - lo);
+    w.skip = kPromptTile * lo;
+    w.k0 += w.skip;
+  }
   if (warp < kSoftWarps) {
-    softmax(p, x, w, head, warp >> 3, warp < 8 ? n0 : n1);
+    softmax(p, x, w, head, split, warp >> 3, warp < 8 ? n0 : n1);
   } else if (warp == kCopyWarp) {
     if (lane == 0) copies(p, x, w, head, n0, n1);
   } else {
@@ -531,6 +578,49 @@ __global__ void __launch_bounds__(32 * kWarps, 1) mla_prompt_kernel(const __grid
   if (warp == kMmaWarp) tc::dealloc(x.tmem, 512);
 }
 
+// The partial results of a row joined: a warp a token and head, 4 columns a lane.
+constexpr int kJoinWarps = 4;
+__global__ void __launch_bounds__(32 * kJoinWarps) mla_prompt_join_kernel(const __grid_constant__ PromptParams p) {
+  pdl_wait_primary();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5), rows = (int64_t)p.num_q * p.heads;
+  if (row >= rows) return;
+  const int t = (int)(row / p.heads), head = (int)(row - (int64_t)t * p.heads);
+  const float mine = lane < p.splits ? p.part_lse[lane * rows + row] : -INFINITY;
+  float4 v[kPromptMaxSplits];
+#pragma unroll
+  for (int s = 0; s < kPromptMaxSplits; ++s)
+    if (s < p.splits) v[s] = reinterpret_cast<const float4*>(p.part_o + (s * rows + row) * MLA_PROMPT_V)[lane];
+  if (!owned(p, t, lane)) return;  // a row of no document stays as it is (what was read is no result)
+  float top = mine;
+  bool nan = mine != mine;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  nan = __any_sync(0xffffffffu, nan);
+  top = __shfl_sync(0xffffffffu, top, 0);
+  const float w = mine == -INFINITY ? 0.f : fast_exp2((mine - top) * kLog2e);
+  float sum = w;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  sum = __shfl_sync(0xffffffffu, sum, 0);
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int s = 0; s < kPromptMaxSplits; ++s) {
+    const float ws = __shfl_sync(0xffffffffu, w, s);
+    if (s < p.splits && ws != 0.f) {
+      y.x = fmaf(ws, v[s].x, y.x);
+      y.y = fmaf(ws, v[s].y, y.y);
+      y.z = fmaf(ws, v[s].z, y.z);
+      y.w = fmaf(ws, v[s].w, y.w);
+    }
+  }
+  const float inv = nan ? NAN : (sum > 0.f ? __frcp_rn(sum) : 0.f);
+  uint2* out = reinterpret_cast<uint2*>(p.out + (int64_t)t * p.out_token_stride + (int64_t)head * p.out_head_stride);
+  out[lane] = make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+  if (lane == 0 && p.lse) p.lse[row] = nan ? NAN : (sum > 0.f ? top + fast_log2(sum) * kLn2 : -INFINITY);
+}
+
 }  // namespace
 
 cudaError_t launch_prompt(const PromptParams& p, cudaStream_t stream) {
@@ -538,7 +628,7 @@ cudaError_t launch_prompt(const PromptParams& p, cudaStream_t stream) {
   cudaError_t e = smem_opt_in<mla_prompt_kernel>(Smem::total);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)p.slots * p.heads));
+  cfg.gridDim = dim3((unsigned)((int64_t)p.slots * p.heads * p.splits));
   cfg.blockDim = dim3(32 * kWarps);
   cfg.dynamicSmemBytes = Smem::total;
   cfg.stream = stream;
@@ -547,7 +637,13 @@ cudaError_t launch_prompt(const PromptParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mla_prompt_kernel, p);
+  e = cudaLaunchKernelEx(&cfg, mla_prompt_kernel, p);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  const int64_t rows = (int64_t)p.num_q * p.heads;
+  cfg.gridDim = dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps));
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, mla_prompt_join_kernel, p);
 }
 
 }  // namespace mla

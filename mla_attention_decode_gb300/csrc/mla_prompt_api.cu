@@ -26,6 +26,29 @@ int check_sizes(const mla_prompt_args* a) {
   return MLA_OK;
 }
 
+constexpr size_t kPartBytes = (MLA_PROMPT_V + 1) * sizeof(float);  // a row's partial result
+
+// How many CTAs share the keys of a tile.  Few rows leave SMs without a CTA, and a
+// tile's time is its key tiles one after the other: the keys are dealt to as many CTAs
+// as there are SMs, each with at least kSplitTiles key tiles of an average document.
+// 16 heads: 17 tokens after 8000 keys 99 -> 21 us, 200 each after 4000 in two documents
+// 69 -> 35; one token after 12,000 145 -> 26.  At least 2 tiles instead of 3: 100
+// tokens after 700 keys 13.9 us instead of 15.4, but a prompt of 500 tokens 19.9
+// instead of 15.0, which has more to join; at least 4: 16.9 and 15.0.
+constexpr int64_t kSplitTiles = 3;
+int32_t splits_of(const mla_prompt_args* a, int64_t slots, size_t workspace_bytes) {
+  // the tiles of documents of equal length (slots counts one more for most of them)
+  const int64_t each = (a->num_q + a->batch - 1) / a->batch, full = (each + mla::kPromptQ - 1) / mla::kPromptQ * a->batch;
+  const int64_t ctas = (full < slots ? full : slots) * a->heads, sms = mla::kPromptSplitCtas / 2;
+  const int64_t tiles = (int64_t)a->num_kv / a->batch / mla::kPromptTile + 1;
+  int64_t s = sms / ctas;
+  if (s > tiles / kSplitTiles) s = tiles / kSplitTiles;
+  if (s > mla::kPromptMaxSplits) s = mla::kPromptMaxSplits;
+  const int64_t room = (int64_t)((workspace_bytes - 256) / kPartBytes) / ((int64_t)a->num_q * a->heads);
+  if (s > room) s = room;  // (a workspace made for fewer rows)
+  return s < 1 ? 1 : static_cast<int32_t>(s);
+}
+
 // The 256-token tiles of the batch, at most (mla_prompt.cu says how they are counted).
 int64_t slots_of(const mla_prompt_args* a) { return a->num_q / mla::kPromptQ + (int64_t)a->batch; }
 
@@ -79,7 +102,10 @@ extern "C" {
 
 size_t mla_prompt_workspace_bytes(const mla_prompt_args* args) {
   if (check_sizes(args) != MLA_OK) return 0;
-  return 256;
+  // partial results of as many rows as any split has, of a call of at most these sizes
+  const int64_t rows = (int64_t)args->num_q * args->heads * mla::kPromptMaxSplits;
+  const int64_t most = (int64_t)mla::kPromptSplitCtas * mla::kPromptQ;
+  return 256 + (size_t)(rows < most ? rows : most) * kPartBytes;
 }
 
 int mla_prompt_fwd(const mla_prompt_args* args, void* workspace, size_t workspace_bytes, void* stream) {
@@ -111,6 +137,9 @@ int mla_prompt_fwd(const mla_prompt_args* args, void* workspace, size_t workspac
   }
   const int64_t slots = slots_of(args);
   if (slots * a.heads > INT32_MAX) return MLA_ERR_UNSUPPORTED;
+  p.splits = splits_of(args, slots, workspace_bytes);
+  p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 256);
+  p.part_lse = p.part_o + (int64_t)p.splits * a.num_q * a.heads * MLA_PROMPT_V;
   p.qo_indptr = a.qo_indptr;
   p.kv_indptr = a.kv_indptr;
   p.prefix = a.prefix;

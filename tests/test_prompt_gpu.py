@@ -9,6 +9,7 @@ Tolerances, per output of token i, head h and column c, with w_j the exact weigh
     moves by d = 2 (192 2^-24 max_j M_j + 2^-21 + 2^-22 max_j |s_j|) of itself, and so
     does the sum that it is divided by; sums of up to n weights: n 2^-24 of themselves
 and of the log of the sum half of that, 2^-23 of its size and 2^-21 for the logarithm."""
+import ctypes
 import math
 
 import pytest
@@ -334,3 +335,59 @@ def test_python_refusals():
                    ("v", torch.zeros(1, 2, 128, dtype=torch.bfloat16, device=DEV).expand(12, 2, 128))):
         with pytest.raises(binding.MLAError):
             p(**{**ok, k: bad})
+
+
+@pytest.mark.parametrize("n,context", [(1, 0), (1, 12000), (17, 5000), (130, 4000), (256, 1100), (300, 2500)])
+@pytest.mark.parametrize("heads", [1, 16])
+def test_few_tokens_after_a_long_context(n, context, heads):
+    """The keys dealt to several CTAs and their results joined."""
+    x = inputs(gen(n + heads), n, n + context, heads)
+    qo, kv = indptr([n]), indptr([n + context])
+    check(*run(x, qo, kv), reference(x, qo, kv))
+
+
+@pytest.mark.parametrize("mask", ["causal", "prefix", "full"])
+def test_uneven_documents_share_the_split(mask):
+    """Documents far shorter than the average that decides the split: shares without a key tile, documents without
+    keys; rows of no document stay."""
+    nq, nk = [3, 0, 5, 1, 40], [6003, 30, 5, 1, 3500]
+    x = inputs(gen(5), sum(nq) + 9, sum(nk) + 50, 2)
+    qo, kv = indptr(nq, 4), indptr(nk, 11)
+    prefix = [6000, 9, 2, 0, 10000] if mask == "prefix" else None
+    out, lse = torch.full((x["q_nope"].shape[0], 2, 128), 7.0, dtype=torch.bfloat16, device=DEV), torch.full((x["q_nope"].shape[0], 2), 7.0, device=DEV)
+    run(x, qo, kv, mask != "full", prefix, out=out, lse=lse)
+    check(out, lse, reference(x, qo, kv, mask != "full", prefix))
+    for t in (out, lse):
+        assert torch.all(t[:4] == 7.0) and torch.all(t[4 + sum(nq):] == 7.0)
+
+
+def test_split_and_unsplit_calls():
+    """An object made for more rows gives the bits of one made for these, and so does the C entry point; a NaN in
+    one share reaches its rows' results; bounds that do not fit."""
+    n, m = 20, 6000
+    x = inputs(gen(6), n, m, 2)
+    qo, kv = indptr([n]), indptr([m])
+    ref = reference(x, qo, kv)
+    args = dict(**x, qo_indptr=qo.to(DEV), kv_indptr=kv.to(DEV))
+    a, b = prompt.MLAPrompt(n, m, 1, heads=2), prompt.MLAPrompt(5 * n, 2 * m, 9, heads=2)
+    o1, l1 = a(**args)
+    o2, l2 = b(**args)
+    assert torch.equal(o1, o2) and torch.equal(l1, l2)
+    check(o1, l1, ref)
+    lib, o3, l3 = prompt.load_library(), torch.zeros_like(o1), torch.zeros_like(l1)
+    s = [x[k].stride(i) for k, d in (("q_nope", 2), ("q_pe", 2), ("k_nope", 2), ("k_pe", 1), ("v", 2)) for i in range(d)]
+    p = [x[k].data_ptr() for k in ("q_nope", "q_pe", "k_nope", "k_pe", "v")]
+    ws = torch.zeros(a.workspace.numel(), dtype=torch.uint8, device=DEV)
+    g = prompt.mla_prompt_args(*p, args["qo_indptr"].data_ptr(), args["kv_indptr"].data_ptr(), None, o3.data_ptr(), l3.data_ptr(),
+                               *s, 256, 128, n, m, 1, 2, 1, SM)
+    torch.cuda.synchronize()
+    need = int(lib.mla_prompt_workspace_bytes(ctypes.addressof(g)))
+    assert need == a.workspace.numel()
+    assert lib.mla_prompt_fwd(ctypes.addressof(g), ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(o3, o1) and torch.equal(l3, l1)
+    x["k_nope"][3000] = math.nan  # every token sees it
+    o, l = a(**args)
+    assert torch.all(torch.isnan(o)) and torch.all(torch.isnan(l))
+    o.fill_(7.0), l.fill_(7.0)
+    a(**{**args, "kv_indptr": torch.tensor([0, m + 1], dtype=torch.int32, device=DEV)}, out=o, lse=l)
+    assert a.poll_error() == binding.MLA_ERR_DEVICE_INDEX and torch.all(o == 7.0) and torch.all(l == 7.0)
