@@ -268,14 +268,15 @@ __device__ __noinline__ uint64_t Ctx::look(uint64_t since) const {
 // ------------------------------------------------------------------ copies
 __device__ void copies(const PromptParams& p, const Ctx& x, const Work& w, int head, int n0, int n1) {
   const uint64_t keep = policy_evict_last(), once = policy_evict_first();
-  for (int g = 0; g < 2; ++g) {
-    if ((g ? n1 : n0) == 0) continue;
+  auto queries = [&](int g) {
+    if ((g ? n1 : n0) == 0) return;
     mbar_arrive_expect_tx(&x.bar[kQ + g], kQChunks * kSlotBytes);
     uint8_t* dst = x.smem + Smem::q + g * kQChunks * kSlotBytes;
     tma_load_3d(dst, &p.q_nope, 0, head, w.q0 + 128 * g, &x.bar[kQ + g], once);
     tma_load_3d(dst + kSlotBytes, &p.q_nope, 64, head, w.q0 + 128 * g, &x.bar[kQ + g], once);
     tma_load_3d(dst + 2 * kSlotBytes, &p.q_pe, 0, head, w.q0 + 128 * g, &x.bar[kQ + g], once);
-  }
+  };
+  queries(0);
   const int n = max(n0, n1);
   int ks = 0, vs = 0;  // tiles asked for
   // what K tile j and V tile j go over: a slot of K and both of V of tile j - 2, two
@@ -293,6 +294,7 @@ __device__ void copies(const PromptParams& p, const Ctx& x, const Work& w, int h
     tma_load_3d(slot(1), &p.k_nope, 64, head, row, bar, keep);
     tma_load_2d(slot(2), &p.k_pe, 0, row, bar, keep);
     ++ks;
+    if (j == 0) queries(1);
     if (j >= 1 && !read(kS, j - 1)) break;
     bar = &x.bar[kVFull + (j & 1)];
     mbar_arrive_expect_tx(bar, kVChunks * kSlotBytes);
