@@ -89,12 +89,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
       "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// One lane of a converged warp, the same one each time.
-__device__ __forceinline__ bool elect() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
   asm("{\n\t.reg .b64 x, y, z, w;\n\t"
@@ -365,7 +359,7 @@ __device__ void mmas(const Ctx& x, int n0, int n1) {
     if ((g ? n1 : n0) == 0) continue;
     if (!x.wait_warp(kQ + g, 0)) return;
     tc::fence_after();
-    if (elect()) scores(g, 0);
+    if (tc::elect()) scores(g, 0);
   }
   for (int j = 0; j < n; ++j) {
     if (!x.wait_warp(kVFull + (j & 1), j >> 1)) return;
@@ -375,13 +369,13 @@ __device__ void mmas(const Ctx& x, int n0, int n1) {
       if (j >= ng) continue;
       if (!x.wait_warp(kP + 2 * g, j)) return;
       tc::fence_after();
-      if (elect()) values(g, j, 0);
+      if (tc::elect()) values(g, j, 0);
       if (!x.wait_warp(kP + 2 * g + 1, j)) return;
       tc::fence_after();
-      if (elect()) values(g, j, 1);
+      if (tc::elect()) values(g, j, 1);
       if (j + 1 < ng) {
         if (!x.wait_warp(kKFull + ((j + 1) & 1), (j + 1) >> 1)) return;
-        if (elect()) scores(g, j + 1);
+        if (tc::elect()) scores(g, j + 1);
       }
     }
   }
@@ -587,7 +581,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) mla_prompt_kernel(const __grid
     mmas(x, __shfl_sync(0xffffffffu, n0, 0), __shfl_sync(0xffffffffu, n1, 0));
     // every MMA is complete before tensor memory is given back
     __syncwarp();
-    if (elect()) tc::commit(&x.bar[kEnd]);
+    if (tc::elect()) tc::commit(&x.bar[kEnd]);
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait(&x.bar[kEnd], 0) && global_timer_ns() - t0 < kWaitTimeoutNs) {
     }

@@ -313,6 +313,15 @@ __device__ __forceinline__ void mma_mx_words(uint32_t d_tmem, uint32_t a_lo, uin
 __device__ __forceinline__ void cp_32x128b_warpx4(uint32_t taddr, uint64_t sdesc) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
+// One lane of a converged warp, the same one each time.  A warp that computes the
+// operands of tensor-core instructions together and issues them by this lane keeps
+// them in uniform registers, which is where the instructions take them from; from
+// code of a single lane each issue first moves them there, one after the other.
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 // Arrive once on `bar` when every tcgen05 operation issued so far by this thread is complete.
 __device__ __forceinline__ void commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(

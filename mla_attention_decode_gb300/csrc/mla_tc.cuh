@@ -214,6 +214,9 @@ struct Ctx {
                   // MXFP4: its two staging halves) issued before the unit scan (-1: none)
 };
 
+// Whether any lane of the warp sees that a wait has given up (the warp then stops together).
+__device__ __forceinline__ bool aborted(const Ctx& x) { return __any_sync(0xffffffffu, *x.abort_flag != 0); }
+
 __device__ __forceinline__ int tiles_of(const UnitDesc& d) { return (d.end - d.start + kTileRows - 1) / kTileRows; }
 
 // ------------------------------------------------------------------ producer
@@ -997,8 +1000,8 @@ __device__ void q_loader(const Stage1Params& p, const Ctx& x) {
 }
 
 // ------------------------------------------------------------------ MMA issuers
-// Two threads issue the tensor-core operations: warp 1 the QK of every tile,
-// warp 2 the P.V of every tile, each in tile order.  Operands are described by
+// Two warps issue the tensor-core operations (by an elected lane): warp 1 the QK of
+// every tile, warp 2 the P.V of every tile, each in tile order.  Operands are described by
 // descriptors built once per tile from templates and moved by constant
 // offsets (a few instructions per MMA).
 //
@@ -1022,7 +1025,7 @@ __host__ __device__ constexpr uint32_t hi_word(uint64_t d) { return (uint32_t)(d
 // QK of every tile: S^T(t) into TMEM columns [blk (t mod 2), +blk), token i's
 // scores at +32 i (two tokens: one N = 64 MMA per k step over both query images).
 template <bool kMx, int kTok, int kPath>
-__device__ void qk_issuer(const Stage1Params& p, const Ctx& x) {
+__device__ void qk_issuer(const Stage1Params& p, const Ctx& x, int lane) {
   constexpr bool kSmallPages = small_pages(kPath);
   using L = Layout<kMx, kTok, kPath>;
   constexpr bool kBs = Geo<kMx, kTok, kPath>::bs;  // block-scaled e2m1 scores
@@ -1033,8 +1036,8 @@ __device__ void qk_issuer(const Stage1Params& p, const Ctx& x) {
   const uint32_t pairs0 = smem_u32(x.smem + L::pairs), rope0 = smem_u32(x.smem + L::rope);
   const uint32_t bq = lo_word(kTplK64) + (smem_u32(x.smem + L::qs) >> 4);
   int it = 0;
-  for (int k = 0; k < x.nunits && !*x.abort_flag; ++k) {
-    const int nt = tiles_of(x.units[k]);
+  for (int k = 0; k < x.nunits && !aborted(x); ++k) {
+    const int nt = __shfl_sync(0xffffffffu, tiles_of(x.units[k]), 0);
     wait_phase(&x.bar[kQFull], k & 1, x.abort_flag, p.ws_err);
     for (int t = 0; t < nt; ++t, ++it) {
       const int s0 = (4 * it) % kPairSlots, use0 = (4 * it) / kPairSlots;
@@ -1054,8 +1057,8 @@ __device__ void qk_issuer(const Stage1Params& p, const Ctx& x) {
           wait_phase(&x.bar[kRopeFull + it % kRopeSlots], (it / kRopeSlots) & 1, x.abort_flag, p.ws_err);
       }
       if (it >= 2) wait_phase(&x.bar[kSEmpty + (it & 1)], ((it >> 1) - 1) & 1, x.abort_flag, p.ws_err);
-      if (*x.abort_flag) break;
-      if (it < 32) trace_stamp(p, kTrTileData + it);
+      if (aborted(x)) break;
+      if (it < 32 && lane == 0) trace_stamp(p, kTrTileData + it);
       tc::fence_after();
       uint32_t ap[4];
 #pragma unroll
@@ -1063,7 +1066,9 @@ __device__ void qk_issuer(const Stage1Params& p, const Ctx& x) {
         ap[f] = lo_word(kTplA) + ((pairs0 + (uint32_t)wrap_slot<kMx, kTok, kPath>(s0 + f) * kPairBytes) >> 4);
       const uint32_t ar = lo_word(kTplK64) + ((rope0 + (uint32_t)(it % kRopeSlots) * kChunkBytes) >> 4);
       const uint32_t d = x.tmem + TM::s + TM::blk * (it & 1);
-      if constexpr (kBs) {
+      if (!tc::elect()) {
+        // (the elected lane's)
+      } else if constexpr (kBs) {
         // scale factors into TMEM (executed before the MMAs that follow):
         // the B factors (all 2^0) once, the tile's A chunks per tile
         const uint32_t sfa = x.tmem + TM::sfa + 32 * (it & 1), sfb = x.tmem + TM::sfb;
@@ -1097,8 +1102,9 @@ __device__ void qk_issuer(const Stage1Params& p, const Ctx& x) {
         tc::commit(&x.bar[kSFull + (it & 1)]);
         tc::commit(&x.bar[kRopeEmpty + it % kRopeSlots]);
       }
+      __syncwarp();
     }
-    tc::commit(&x.bar[kQEmpty]);  // the query buffer may be refilled
+    if (tc::elect()) tc::commit(&x.bar[kQEmpty]);  // the query buffer may be refilled
   }
 }
 
@@ -1118,8 +1124,8 @@ __device__ void pv_issuer(const Stage1Params& p, const Ctx& x) {
   const uint32_t pairs0 = smem_u32(x.smem + L::pairs), pb0 = smem_u32(x.smem + L::pb);
   constexpr bool kEpi = Geo<kMx, kTok, kPath>::epi;
   int it = 0, ordinal = 0;
-  for (int k = 0; k < x.nunits && !*x.abort_flag; ++k) {
-    const int nt = tiles_of(x.units[k]);
+  for (int k = 0; k < x.nunits && !aborted(x); ++k) {
+    const int nt = __shfl_sync(0xffffffffu, tiles_of(x.units[k]), 0);
     if (nt == 0) continue;
     // the unit's O^T buffer, and how many units used it before
     const int obuf = kEpi ? (ordinal & 1) : 0, use = kEpi ? (ordinal >> 1) : ordinal;
@@ -1130,26 +1136,29 @@ __device__ void pv_issuer(const Stage1Params& p, const Ctx& x) {
       if (kBs) wait_phase(&x.bar[kConvFull + (it & 1)], (it >> 1) & 1, x.abort_flag, p.ws_err);
       // a unit's first P.V overwrites O^T: the epilogue of the buffer's previous unit must have read it
       if (t == 0 && use > 0) wait_phase(&x.bar[ofree_bar(obuf)], (use - 1) & 1, x.abort_flag, p.ws_err);
-      if (*x.abort_flag) break;
+      if (aborted(x)) break;
       tc::fence_after();
       constexpr uint64_t kTplPT = kTok == 1 ? kTplP : kTplP2;
       const uint32_t bp = lo_word(kTplPT) + ((pb0 + (uint32_t)(it & 1) * kTok * kPBytes) >> 4);
       const int s0 = (4 * it) % kPairSlots;
+      if (tc::elect()) {
 #pragma unroll
-      for (int fb = 0; fb < 4; ++fb) {
-        const int sl = wrap_slot<kMx, kTok, kPath>(s0 + fb);
+        for (int fb = 0; fb < 4; ++fb) {
+          const int sl = wrap_slot<kMx, kTok, kPath>(s0 + fb);
 
-        // V^T block: features [128 fb, 128 fb + 128) = the slot's two column blocks (LBO)
-        const uint32_t av = lo_word(kTplA) + ((pairs0 + (uint32_t)sl * kPairBytes) >> 4);
+          // V^T block: features [128 fb, 128 fb + 128) = the slot's two column blocks (LBO)
+          const uint32_t av = lo_word(kTplA) + ((pairs0 + (uint32_t)sl * kPairBytes) >> 4);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)  // rows [32 q, 32 q + 32): +kRows32 B of V^T, +1024 B of P^T (every token)
-          tc::mma_f8_words(od + TM::blk * fb, av + q * (kRows32 >> 4), hi_word(kTplA), bp + q * (1024 >> 4),
-                           hi_word(kTplPT), kTok == 1 ? kIdescPV : kIdescPV2, (t == 0 && q == 0) ? 0u : 1u);
-        tc::commit(&x.bar[kPairEmpty + sl]);
+          for (int q = 0; q < 4; ++q)  // rows [32 q, 32 q + 32): +kRows32 B of V^T, +1024 B of P^T (every token)
+            tc::mma_f8_words(od + TM::blk * fb, av + q * (kRows32 >> 4), hi_word(kTplA), bp + q * (1024 >> 4),
+                             hi_word(kTplPT), kTok == 1 ? kIdescPV : kIdescPV2, (t == 0 && q == 0) ? 0u : 1u);
+          tc::commit(&x.bar[kPairEmpty + sl]);
+        }
+        tc::commit(&x.bar[kODone]);
+        tc::commit(&x.bar[kPFree + (it & 1)]);
+        if (t == nt - 1) tc::commit(&x.bar[olast_bar(obuf)]);
       }
-      tc::commit(&x.bar[kODone]);
-      tc::commit(&x.bar[kPFree + (it & 1)]);
-      if (t == nt - 1) tc::commit(&x.bar[olast_bar(obuf)]);
+      __syncwarp();
     }
     ++ordinal;
   }
@@ -1729,10 +1738,14 @@ __global__ void __launch_bounds__(Geo<kMx, kTok, kPath>::threads, 1)
       else
         producer_e4m3<kTok>(p, x);
     }
-  } else if (warp == 1) {
-    if (lane == 0) qk_issuer<kMx, kTok, kPath>(p, x);
-  } else if (warp == 2) {
-    if (lane == 0) pv_issuer<kMx, kTok, kPath>(p, x);
+  } else if (warp == 1 || warp == 2) {
+    x.tmem = __shfl_sync(0xffffffffu, x.tmem, 0);
+    x.nunits = __shfl_sync(0xffffffffu, x.nunits, 0);
+    if (warp == 1)
+      qk_issuer<kMx, kTok, kPath>(p, x, lane);
+    else
+      pv_issuer<kMx, kTok, kPath>(p, x);
+    __syncwarp();
   } else if (warp == 3) {
     if (lane == 0) q_loader<kMx, kTok, kPath>(p, x);
   } else if (warp < 4 + 4 * (kMx ? 1 : kTok)) {
@@ -1748,9 +1761,9 @@ __global__ void __launch_bounds__(Geo<kMx, kTok, kPath>::threads, 1)
       epilogue_group<kMx, kTok, kPath>(p, x, warp & 3, lane);
   }
 
-  if ((warp == 1 || warp == 2) && lane == 0) {
+  if (warp == 1 || warp == 2) {
     // every tensor-core operation of this CTA is complete before TMEM is freed
-    tc::commit(&x.bar[kFinal]);
+    if (tc::elect()) tc::commit(&x.bar[kFinal]);
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait(&x.bar[kFinal], 0) && global_timer_ns() - t0 < kWaitTimeoutNs) {
     }
