@@ -60,7 +60,7 @@
 // score factor in fp32, and P as s_t 2^-Gv with Gv the running maximum of the
 // scales' exponents (as MXFP4's, each softmax thread fetching its row's scale
 // two tiles ahead).  P's reference is lowered by 4 (P <= 16 after a raise,
-// <= 256 before the next one) and its second term is carried 2^4 up in its own
+// <= 2^8.75 before the next one) and its second term is carried 2^4 up in its own
 // columns of O^T: what e4m3's smallest step leaves out of a weight is 2^-18 of the
 // largest instead of 2^-10.
 #pragma once
@@ -1337,7 +1337,8 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
   using TM = Tmem<kTok>;
   constexpr bool kRow = row_scales(kPath);    // a scale per row
   constexpr bool kG = kMx || kRow;            // P carries the rows' scales relative to 2^Gv
-  constexpr float kLower = kRow ? 4.f : 0.f;  // P's reference lies this far below the maximum (log2)
+  constexpr float kLower = kRow ? 4.f : 0.f;  // P's reference lies this far below the maximum (log2),
+  constexpr float kRise = kRow ? 8.75f : kRescaleLog2;  // and rises when a score exceeds it by that (2^8.75 < 448)
   constexpr int kGvNone = -1000;   // no such reference yet
   const int row = 32 * ww + lane;  // tile row == TMEM lane of this thread
   const uint32_t tl = x.tmem + ((uint32_t)(32 * ww) << 16) + 32 * ti;
@@ -1433,13 +1434,13 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
       // the scores of block-scaled MMAs carry no row factor
       const float row_fac = (kMx && !kBs) ? exp2_int(gsh) : (kRow ? row_sc : 1.f);
       float sv[16];
-      uint32_t need = 0;  // heads with a score above m_ref + 8 in this row (bit 16: G above gv)
+      uint32_t need = 0;  // heads with a score above m_ref + kRise in this row (bit 16: G above gv)
 #pragma unroll
       for (int h = 0; h < 16; ++h) {
         sv[h] = row < vis ? (__uint_as_float(acc[h]) + __uint_as_float(acc[16 + h])) * (r[h] * row_fac)
                           : -INFINITY;
         // (row scales: a NaN score raises too, so that it reaches the output)
-        need |= ((kRow ? !(sv[h] <= m_ref[h] + kRescaleLog2) : sv[h] > m_ref[h] + kRescaleLog2) ? 1u : 0u) << h;
+        need |= ((kRow ? !(sv[h] <= m_ref[h] + kRise) : sv[h] > m_ref[h] + kRise) ? 1u : 0u) << h;
       }
       if (kG && row < valid && gsh > gv) need |= 1u << 16;
       // heads whose reference rises: OR over the warp, then over the 4 warps

@@ -6,7 +6,7 @@ softmax weights and v_t = code_t s_t:
   * the output's rounding to bf16                               2^-8 |out|
   * a weight times its row's scale enters P.V as two e4m3 terms: each keeps 4 bits,
     so 2^-8 w_t |v_t|, or half of e4m3's smallest step, 2^-10, where that is more;
-    the reference of the weights lies at least 4 (log2) below the largest score of
+    the reference of the weights lies 4 (log2) below the largest score of
     the rows so far and scales are taken relative to a power of two S at most twice
     the largest scale, so that is 2^-14 w_max |code_t| S in the output
   * the query enters the scores as two e4m3 terms: exact for a bf16 query down to
