@@ -241,6 +241,8 @@ class _Decoder:
         if self._core is None or self._of[0] is not self.plan or self._of[1] is not self.workspace:
             from .cache import extension
             self._ext, self._of, w = extension(), (self.plan, self.workspace), self.workspace
+            if not w.is_cuda:
+                raise ValueError("the decoder's workspace is a CUDA tensor")
             self._core = self._ext.decode_core(ctypes.addressof(self.plan), w.data_ptr(), w.numel() * w.element_size(),
                                                w.device.index)
         rc, out, lse = self._ext.decode(self._core, *args)

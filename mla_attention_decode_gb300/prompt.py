@@ -67,6 +67,8 @@ class MLAPrompt:
             raise MLAError(binding.MLA_ERR_INVALID_ARG, "mla_prompt_workspace_bytes")
         self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=device)
         self.device = self.workspace.device
+        if not self.workspace.is_cuda:
+            raise ValueError("a prompt runs on a CUDA device")
         self._ext = extension()
         self._core = self._ext.prompt_core(self.workspace.data_ptr(), nbytes, self.device.index, self.num_tokens, self.num_keys,
                                            self.batch, self.heads, int(self.causal), self.sm_scale)

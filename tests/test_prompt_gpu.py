@@ -124,6 +124,21 @@ def test_documents(layout, mask, heads):
     check(out, lse, reference(x, qo, kv, mask != "full", prefix))
 
 
+@pytest.mark.parametrize("nq,nk", [(300, 100), (300, 172), (130, 1), (513, 129), (256, 128)])
+def test_more_tokens_than_keys(nq, nk):
+    """The first tokens see nothing: whole query tiles without a key tile."""
+    x = inputs(gen(nq), nq, nk, 2)
+    qo, kv = indptr([nq]), indptr([nk])
+    check(*run(x, qo, kv), reference(x, qo, kv))
+    check(*run(x, qo, kv, prefix=[nk // 2]), reference(x, qo, kv, prefix=[nk // 2]))
+
+
+def test_128_heads():
+    x = inputs(gen(128), 150, 200, 128)
+    qo, kv = indptr([100, 50]), indptr([120, 80])
+    check(*run(x, qo, kv), reference(x, qo, kv))
+
+
 @pytest.mark.parametrize("nk", [1, 63, 127, 128, 129, 384, 1025])
 def test_every_key_seen(nk):
     x = inputs(gen(nk), 300, nk, 2)
@@ -313,6 +328,11 @@ def test_a_prompt_in_chunks_over_the_cache():
     up = torch.einsum("hc,chd->hd", o[0].float(), wk[..., 128:].float())
     assert torch.all((l[0] - lse[-1]).abs() <= 0.02)
     assert torch.linalg.norm(up - out[-1].float()) <= 0.02 * torch.linalg.norm(up)
+
+
+def test_an_object_is_made_for_a_cuda_device():
+    with pytest.raises(ValueError):
+        prompt.MLAPrompt(1, 1, 1, device="cpu")
 
 
 def test_python_refusals():

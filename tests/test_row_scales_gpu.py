@@ -465,6 +465,23 @@ def test_a_conversation():
             check(outs[layer][0], outs[layer][1], reference(qs.cpu(), codes, s, spans))
 
 
+def test_a_decoder_whose_plan_or_workspace_is_replaced():
+    """A call goes by the objects that the decoder has then, not by those that it was made with."""
+    codes, s = random_cache(gen(7), 900)
+    q = torch.randn(2, 16, 576, generator=gen(7)).to(torch.bfloat16)
+    qo = torch.tensor([0, 1, 2], dtype=torch.int32)
+    dec = binding.MLADecoder([0, 300, 600], "fp8_row")
+    for ind in ([0, 300, 600], [0, 1, 900], [0, 0, 130]):
+        new = binding.MLADecoder(ind, "fp8_row")
+        dec.plan, dec.workspace = new.plan, new.workspace
+        del new
+        ind = torch.tensor(ind, dtype=torch.int32)
+        out, lse = dec(q.to(DEV), codes.to(DEV), ind.to(DEV), qo.to(DEV), kv_scale=s.to(DEV))
+        spans = [list(range(int(a), int(e))) for a, e in zip(ind[:-1], ind[1:])]
+        check(out, lse, reference(q, codes, s, spans))
+        assert dec.poll_error() == 0
+
+
 def test_another_stream():
     codes, s = random_cache(gen(6), 500)
     ind, qo = torch.tensor([0, 500], dtype=torch.int32), torch.tensor([0, 1], dtype=torch.int32)
