@@ -273,9 +273,9 @@ MLA_API int mla_decode_plan_multi(const int32_t* kv_indptr_host, int32_t num_seq
  *
  * page_size must be a power of two (1, 2, 4, ...; MLA_ERR_UNSUPPORTED
  * otherwise).  Pages of 64 rows or more hold whole tiles of the copies into
- * shared memory; smaller pages are gathered row by row (e4m3: four-row tensor
- * gathers, MXFP4: one bulk copy per row, bf16: one box per page), each row
- * through the page table.  The plan's splits and rule are those of
+ * shared memory; smaller pages are gathered (e4m3: one box per page of 8 rows or
+ * more, 16-byte copies of smaller ones; MXFP4: one bulk copy per page's rows; bf16:
+ * one box per page), each page through the page table.  The plan's splits and rule are those of
  * mla_decode_plan with start_b = kv_page_indptr[b] * page_size (a position in
  * the sequences' page-ordered row space) and L_b the token count above;
  * total_kv is kv_page_indptr[batch] * page_size.  Both that and

@@ -680,10 +680,9 @@ int prepare(const void* q, const void* kv, const void* kv_scale, int32_t scale_s
       // 64-row pages: a tile is two 64-row boxes
       if (!encode_kv_map_tc(&p->tmap_kv16, kv, cache_rows, 64)) return MLA_ERR_CUDA;
     } else if (paged && page_shift < 6) {
-      // smaller pages: a pair of column blocks (128 B) and the rope block (64 B)
-      // per box, one page high for pages of 8 to 32 rows, one row high (for
-      // four-row gathers) for pages of 1 to 4 rows
-      const uint32_t rows = page_shift >= 3 ? (1u << page_shift) : 1u;
+      // pages of 8 to 32 rows: a pair of column blocks (128 B) and the rope block
+      // (64 B) per box, one page high (smaller pages take no tensor map)
+      const uint32_t rows = 1u << page_shift;
       if (!encode_kv_map_pairs(&p->tmap_kv16, kv, cache_rows, rows) ||
           !encode_kv_map_tc(&p->tmap_kv64, kv, cache_rows, rows))
         return MLA_ERR_CUDA;

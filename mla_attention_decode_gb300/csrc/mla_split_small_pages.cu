@@ -1,8 +1,8 @@
 // mla_split_small_pages.cu -- the tcgen05 split kernel for paged caches whose
 // pages hold fewer than 64 rows (e4m3 and MXFP4, one token per sequence): a
-// tile's rows lie in several pages, so the producer warp fetches them with
-// per-page lookups (four-row TMA gathers for e4m3, one bulk copy per packed row
-// for MXFP4).  A separate instance, so that the contiguous-cache kernels carry
+// tile's rows lie in several pages, so the producer warps fetch them with
+// per-page lookups (e4m3: a TMA box a page, or 16-byte copies; one bulk copy per
+// packed row for MXFP4).  A separate instance, so that the contiguous-cache kernels carry
 // none of this code.
 #include "mla_tc.cuh"
 

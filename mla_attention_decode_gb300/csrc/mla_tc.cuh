@@ -101,6 +101,10 @@ struct Geo {
   static constexpr int threads = kMx ? 512 : 384;
   static constexpr int max_units = kMx ? kMaxUnitsPerCtaMx : kMaxUnitsPerCta;  // work units one CTA may own
 };
+// The QK issuer asks for the queries itself where the query loader's warp copies rows
+// (e4m3, small pages).
+template <bool kMx, int kPath>
+constexpr bool kQkLoads = !kMx && small_pages(kPath);
 constexpr int kRopeSlots = 2;                // ring of the rope column block (features 512..575)
 constexpr int kQsBytes = 9 * 32 * 64;        // two-term query: 32 rows x 576 B, K-major, 64 B swizzle
 constexpr int kPBytes = kTileRows * 32;      // two-term P^T: 128 rows x 32 B, MN-major, 32 B swizzle
@@ -163,7 +167,8 @@ struct Layout {
   static constexpr int lut = grow + (kMx ? 2 * 128 : 0);      // u8 [32][8] e2m1 magnitude -> e4m3 per shift
   static constexpr int hand = lut + (kMx ? 256 : 0);          // float [2][32] l, m handed to the epilogue group
   static constexpr int handg = hand + (G::epi ? 256 : 0);     // int [2] Gv handed over (row scales)
-  static constexpr int units = handg + (G::epi && row_scales(kPath) ? 8 : 0);
+  static constexpr int rows = handg + (G::epi && row_scales(kPath) ? 8 : 0);  // int [2][128] a tile's cache rows (small pages)
+  static constexpr int units = rows + (!kMx && small_pages(kPath) ? 1024 : 0);
   static constexpr int bars = units + G::max_units * (int)sizeof(UnitDesc);
   // the epilogue group's four (e4m3, one token), then the two of block-scaled MXFP4
   static constexpr int nbars = G::bs ? 55 : (G::epi ? 53 : 49);
@@ -352,41 +357,27 @@ __device__ void producer_e4m3(const Stage1Params& p, const Ctx& x) {
 }
 
 
-// Pages of fewer than 64 rows: a tile's rows lie in many pages, so the 32
-// lanes of warp 0 fetch them together, once lane 0 has waited for the tile's
-// slots and armed their barriers.  The pair slots hold 128-byte rows (both
-// column blocks of a pair side by side, 128-byte swizzle; the MMA descriptors
-// of this instance say so), so that one copy brings both blocks of a pair.
-// - Pages of 8 to 32 rows: lane l < 128 / P looks up page l of the tile and
-//   issues one box of 128 B x P rows per pair and one of 64 B x P rows for the
-//   rope block: 5 x 128 / P copies per tile.
-// - Pages of 1 to 4 rows: lane l looks up the cache rows of tile rows
-//   [4 l, 4 l + 4) and issues one four-row gather per pair (128 B wide) and
-//   one for the rope block (64 B wide), the maps' boxes one row high: 160
-//   copies per tile.
-// Rows past the unit's end repeat its last row, or page (the softmax masks
-// them and zeroes their V part).
+// Pages of 8 to 32 rows: a tile's rows lie in many pages, so the 32 lanes of warp 0
+// fetch them together, once lane 0 has waited for the tile's slots and armed their
+// barriers.  The pair slots hold 128-byte rows (both column blocks of a pair side by
+// side, 128-byte swizzle; the MMA descriptors of this instance say so), so that one copy
+// brings both blocks of a pair: lane l < 128 / P looks up page l of the tile and issues
+// one box of 128 B x P rows per pair and one of 64 B x P rows for the rope block, 5 x
+// 128 / P copies per tile.  Pages past the unit's end repeat its last one (the softmax
+// masks their rows and zeroes their V part).
 template <int kTok>
-__device__ void producer_e4m3_gather(const Stage1Params& p, const Ctx& x, int lane) {
+__device__ void producer_e4m3_boxes(const Stage1Params& p, const Ctx& x, int lane) {
   using L = Layout<false, kTok>;
   constexpr int kPairSlots = Geo<false, kTok>::pair_slots;
   const uint64_t pol = policy_evict_first();  // KV rows are read once
   int armed[kPairSlots + kRopeSlots];         // lane 0: fills issued per slot
   for (int i = 0; i < kPairSlots + kRopeSlots; ++i) armed[i] = 0;
-  const bool per_page = p.page_shift >= 3;
   const int page_mask = (1 << p.page_shift) - 1;
   TileWalk walk;
   int t0 = 0, end = 0;
   for (int it = 0; walk.next(x, t0, end); ++it) {
-    int cr[4];
-    if (per_page) {
-      // the first cache row of page `lane` of the tile (tiles start on page boundaries)
-      const int v = min(t0 + (lane << p.page_shift), end - 1);
-      cr[0] = cache_row(p, v) - (v & page_mask);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) cr[j] = cache_row(p, min(t0 + 4 * lane + j, end - 1));
-    }
+    // the first cache row of page `lane` of the tile (tiles start on page boundaries)
+    const int v = min(t0 + (lane << p.page_shift), end - 1), cr = cache_row(p, v) - (v & page_mask);
     int sl[4];
 #pragma unroll
     for (int f = 0; f < 4; ++f) sl[f] = pair_slot<false, kTok>(it, f);
@@ -410,25 +401,14 @@ __device__ void producer_e4m3_gather(const Stage1Params& p, const Ctx& x, int la
       }
     }
     if (__shfl_sync(0xffffffffu, lane == 0 ? *x.abort_flag : 0, 0)) break;
-    if (per_page) {
-      if (lane < (kTileRows >> p.page_shift)) {
-        // page `lane`: tile rows [lane P, lane P + P)
-        const int r_tile = lane << p.page_shift;
-#pragma unroll
-        for (int f = 0; f < 4; ++f)
-          tma_load_2d(x.smem + L::pairs + sl[f] * kPairBytes + r_tile * 128, &p.tmap_kv16, 128 * f, cr[0],
-                      &x.bar[kPairFull + sl[f]], pol);
-        tma_load_2d(x.smem + L::rope + rs * kChunkBytes + r_tile * 64, &p.tmap_kv64, 512, cr[0],
-                    &x.bar[kRopeFull + rs], pol);
-      }
-    } else {
-      // tile rows [4 lane, 4 lane + 4)
+    if (lane < (kTileRows >> p.page_shift)) {
+      // page `lane`: tile rows [lane P, lane P + P)
+      const int r_tile = lane << p.page_shift;
 #pragma unroll
       for (int f = 0; f < 4; ++f)
-        tma_gather4(x.smem + L::pairs + sl[f] * kPairBytes + 512 * lane, &p.tmap_kv16, 128 * f, cr[0], cr[1], cr[2],
-                    cr[3], &x.bar[kPairFull + sl[f]], pol);
-      tma_gather4(x.smem + L::rope + rs * kChunkBytes + 256 * lane, &p.tmap_kv64, 512, cr[0], cr[1], cr[2], cr[3],
-                  &x.bar[kRopeFull + rs], pol);
+        tma_load_2d(x.smem + L::pairs + sl[f] * kPairBytes + r_tile * 128, &p.tmap_kv16, 128 * f, cr,
+                    &x.bar[kPairFull + sl[f]], pol);
+      tma_load_2d(x.smem + L::rope + rs * kChunkBytes + r_tile * 64, &p.tmap_kv64, 512, cr, &x.bar[kRopeFull + rs], pol);
     }
     if (it == 0 && lane == 0) trace_stamp(p, kTrFirstLoad);
   }
@@ -442,6 +422,103 @@ __device__ void producer_e4m3_gather(const Stage1Params& p, const Ctx& x, int la
       }
     }
   }
+}
+
+// Pages of 1 to 4 rows by plain asynchronous copies: two warps share a tile's column
+// blocks (part 0: pairs 0, 1 and the rope block; part 1: pairs 2, 3).  Their
+// lanes copy 16 bytes each, four rows of 128 bytes at a time, through their own
+// page-table lookups, into 128-byte rows with the 128-byte swizzle.  A part's slots
+// are groups of copies in order; a group's barrier is arrived at once all lanes' copies
+// of it have landed, kBehind groups later, or when the warp would have to wait for a
+// slot.  Rows past the unit's end are not copied (the softmax masks them and zeroes
+// their V part).  64 x 8192 rows in pages of one row (e4m3, one scale): 188 us with 160
+// four-row tensor gathers a tile, 155 with one such warp, 114 with two; pages of 8
+// rows 108 us instead of 102 by boxes, which pages of 8 rows and more keep.
+template <int kTok, int kPath>
+__device__ void producer_e4m3_copies(const Stage1Params& p, const Ctx& x, int lane, int part) {
+  using L = Layout<false, kTok, kPath>;
+  constexpr int kBehind = 3;
+  const uint64_t pol = policy_evict_first();  // KV rows are read once
+  const uint32_t pairs0 = smem_u32(x.smem + L::pairs), rope0 = smem_u32(x.smem + L::rope);
+  int* const rows = reinterpret_cast<int*>(x.smem + L::rows) + 128 * part;
+  const int per = part ? 2 : 3;  // groups of a tile
+  int issued = 0, told = 0;      // groups
+  auto tell = [&]() {            // the next group's barrier
+    const int it = told / per, k = told - per * it;
+    ++told;
+    tc::fence_proxy_async();  // the tensor core reads them through the async proxy
+    __syncwarp();
+    if (lane == 0)
+      mbar_arrive(k < 2 ? &x.bar[kPairFull + pair_slot<false, kTok, kPath>(it, 2 * part + k)] : &x.bar[kRopeFull + it % kRopeSlots]);
+  };
+  auto tell_all = [&]() {
+    cp_async_wait<0>();
+    while (told < issued) tell();
+  };
+  // until the MMA that read a slot has completed; false: a wait has given up
+  auto free_slot = [&](uint64_t* bar, int use) -> bool {
+    if (use < 1) return true;
+    if (!__shfl_sync(0xffffffffu, mbar_test_wait(bar, (use - 1) & 1) ? 1 : 0, 0)) {
+      tell_all();
+      wait_phase(bar, (use - 1) & 1, x.abort_flag, p.ws_err);
+    }
+    return !aborted(x);
+  };
+  auto group_done = [&]() {
+    cp_async_commit();
+    if (++issued - told > kBehind) {
+      cp_async_wait<kBehind>();
+      tell();
+    }
+  };
+  TileWalk walk;
+  int t0 = 0, end = 0;
+  const int sub = lane >> 3, u = lane & 7;
+  for (int it = 0; walk.next(x, t0, end); ++it) {
+    // the tile's cache rows (-1: past the end), then each lane's 32 of them: rows 4 i + lane / 8
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int v = t0 + 32 * j + lane;
+      rows[32 * j + lane] = v < end ? cache_row(p, v) : -1;
+    }
+    __syncwarp();
+    const bool whole = t0 + kTileRows <= end;
+    const uint8_t* src[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) src[i] = p.kv + (int64_t)rows[4 * i + sub] * 576 + 256 * part + 16 * u;
+    bool ok = true;
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      const int sl = pair_slot<false, kTok, kPath>(it, 2 * part + f);
+      ok = ok && free_slot(&x.bar[kPairEmpty + sl], pair_use<false, kTok, kPath>(it, 2 * part + f));
+      if (!ok) continue;
+      const uint32_t dst = pairs0 + (uint32_t)sl * kPairBytes + sub * 128;
+      const uint32_t d0 = dst + (uint32_t)((u ^ sub) << 4), d1 = dst + (uint32_t)((u ^ (4 + sub)) << 4);
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) cp_async16((i & 1 ? d1 : d0) + 512 * i, src[i] + 128 * f, pol);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (t0 + 4 * i + sub < end) cp_async16((i & 1 ? d1 : d0) + 512 * i, src[i] + 128 * f, pol);
+      }
+      group_done();
+      if (it == 0 && f == 0 && part == 0 && lane == 0) trace_stamp(p, kTrFirstLoad);
+    }
+    if (!ok) break;
+    if (part) continue;
+    const int rs = it % kRopeSlots;
+    if (!free_slot(&x.bar[kRopeEmpty + rs], it / kRopeSlots)) break;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int r = 8 * i + (lane >> 2), c = rows[r];
+      if (c >= 0)
+        cp_async16(rope0 + (uint32_t)rs * kChunkBytes + sw64_off(r, 16 * (lane & 3)), p.kv + (int64_t)c * 576 + 512 + 16 * (lane & 3), pol);
+    }
+    group_done();
+  }
+  tell_all();
 }
 
 // ------------------------------------------------------- MXFP4 converters
@@ -955,6 +1032,25 @@ static __device__ void converter_mx_bs(const Stage1Params& p, const Ctx& x, int 
 }
 
 // ---------------------------------------------------------- query loader
+// The copies of unit k's query (and its score factors).
+template <bool kMx, int kTok, int kPath>
+__device__ __forceinline__ void load_query(const Stage1Params& p, const Ctx& x, int k, uint64_t pol) {
+  using L = Layout<kMx, kTok, kPath>;
+  mbar_arrive_expect_tx(&x.bar[kQFull], (uint32_t)(kTok * kQPrepBytes));
+#pragma unroll
+  for (int i = 0; i < kTok; ++i) {
+    const uint8_t* src = p.ws_q + ((size_t)x.units[k].b * kTok + i) * kQPrepBytes;
+    if constexpr (kTok == 1) {
+      bulk_g2s(x.smem + L::qs, src, (uint32_t)kQImageBytes, &x.bar[kQFull], pol);
+    } else {
+      // K block c of both tokens side by side (rows 32 i + r): the N = 64 B operand
+      for (int c = 0; c < 9; ++c)
+        bulk_g2s(x.smem + L::qs + c * 2048 * kTok + i * 2048, src + c * 2048, 2048u, &x.bar[kQFull], pol);
+    }
+    bulk_g2s(x.smem + L::rq + i * 16 * sizeof(float), src + kQImageBytes, 16 * sizeof(float), &x.bar[kQFull],
+             pol);
+  }
+}
 // One thread: the query of unit k, prepared by mla_prep_q_kernel as the exact
 // shared-memory image (two-term e4m3, 64-byte swizzle) plus its 16 score
 // factors, comes in by two bulk copies per token once the last QK of unit k-1
@@ -975,20 +1071,7 @@ __device__ void q_loader(const Stage1Params& p, const Ctx& x) {
       wait_phase(&x.bar[kRFree], (k - 1) & 1, x.abort_flag, p.ws_err);
       if (*x.abort_flag) break;
     }
-    mbar_arrive_expect_tx(&x.bar[kQFull], (uint32_t)(kTok * kQPrepBytes));
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      const uint8_t* src = p.ws_q + ((size_t)x.units[k].b * kTok + i) * kQPrepBytes;
-      if constexpr (kTok == 1) {
-        bulk_g2s(x.smem + L::qs, src, (uint32_t)kQImageBytes, &x.bar[kQFull], pol);
-      } else {
-        // K block c of both tokens side by side (rows 32 i + r): the N = 64 B operand
-        for (int c = 0; c < 9; ++c)
-          bulk_g2s(x.smem + L::qs + c * 2048 * kTok + i * 2048, src + c * 2048, 2048u, &x.bar[kQFull], pol);
-      }
-      bulk_g2s(x.smem + L::rq + i * 16 * sizeof(float), src + kQImageBytes, 16 * sizeof(float), &x.bar[kQFull],
-               pol);
-    }
+    load_query<kMx, kTok, kPath>(p, x, k, pol);
     ++uses;
   }
   if (*x.abort_flag && uses > 0) {
@@ -1035,9 +1118,23 @@ __device__ void qk_issuer(const Stage1Params& p, const Ctx& x, int lane) {
   constexpr int kPairSlots = Geo<kMx, kTok, kPath>::pair_slots;
   const uint32_t pairs0 = smem_u32(x.smem + L::pairs), rope0 = smem_u32(x.smem + L::rope);
   const uint32_t bq = lo_word(kTplK64) + (smem_u32(x.smem + L::qs) >> 4);
-  int it = 0;
+  int it = 0, asked = 0;  // tiles; queries asked for here
   for (int k = 0; k < x.nunits && !aborted(x); ++k) {
     const int nt = __shfl_sync(0xffffffffu, tiles_of(x.units[k]), 0);
+    if constexpr (kQkLoads<kMx, kPath>) {
+      // the query loader's warp copies rows here: this one asks for its queries itself
+      if (k == 0) {
+        pdl_wait_primary();
+        if (lane == 0) trace_stamp(p, kTrQueryReady);
+      } else {
+        wait_phase(&x.bar[kQEmpty], (k - 1) & 1, x.abort_flag, p.ws_err);
+        wait_phase(&x.bar[kRFree], (k - 1) & 1, x.abort_flag, p.ws_err);
+        if (aborted(x)) break;
+      }
+      if (lane == 0) load_query<kMx, kTok, kPath>(p, x, k, policy_evict_last());
+      __syncwarp();
+      asked = k + 1;
+    }
     wait_phase(&x.bar[kQFull], k & 1, x.abort_flag, p.ws_err);
     for (int t = 0; t < nt; ++t, ++it) {
       const int s0 = (4 * it) % kPairSlots, use0 = (4 * it) / kPairSlots;
@@ -1105,6 +1202,12 @@ __device__ void qk_issuer(const Stage1Params& p, const Ctx& x, int lane) {
       __syncwarp();
     }
     if (tc::elect()) tc::commit(&x.bar[kQEmpty]);  // the query buffer may be refilled
+  }
+  if (lane == 0 && *x.abort_flag && asked > 0) {
+    // never leave with a copy in flight (bounded)
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(&x.bar[kQFull], (asked - 1) & 1) && global_timer_ns() - t0 < kWaitTimeoutNs) {
+    }
   }
 }
 
@@ -1345,15 +1448,30 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
   const uint32_t bar = kBarSoftmax + ti;  // the group's named barrier
   const float kv_scale = kG ? 1.f : *static_cast<const float*>(p.kv_scale);
   // row scales: this thread's row of the next tile and of the one after it (0 past
-  // a unit's end), fetched two tiles ahead
+  // a unit's end), fetched two tiles ahead, its page a tile earlier still, so that
+  // neither load waits for the other here
   TileWalk ahead;
-  auto next_scale = [&]() -> float {
+  int pos = -1, page = 0;  // of the tile three ahead: the row's position, its page
+  auto next_page = [&]() {
     int t0, end;
-    if (!ahead.next(x, t0, end) || t0 + row >= end) return 0.f;
-    const int64_t at = (int64_t)cache_row(p, t0 + row) * p.scale_stride;
-    return __ldg(reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.kv_scale) + at));
+    pos = ahead.next(x, t0, end) && t0 + row < end ? t0 + row : -1;
+    if (p.paged && pos >= 0) page = __ldg(p.kv_indices + (pos >> p.page_shift));
   };
-  float sc_next = kRow ? next_scale() : 0.f, sc_after = kRow ? next_scale() : 0.f;
+  auto next_scale = [&]() -> float {
+    if (pos < 0) return 0.f;
+    int at = pos;
+    if (p.paged)  // (a page out of range: page 0, as the rows; the copies report it)
+      at = ((unsigned)page < (unsigned)p.num_pages ? page << p.page_shift : 0) | (pos & ((1 << p.page_shift) - 1));
+    return __ldg(reinterpret_cast<const float*>(static_cast<const uint8_t*>(p.kv_scale) + (int64_t)at * p.scale_stride));
+  };
+  float sc_next = 0.f, sc_after = 0.f;
+  if constexpr (kRow) {
+    next_page();
+    sc_next = next_scale();
+    next_page();
+    sc_after = next_scale();
+    next_page();
+  }
   const int8_t* grow = reinterpret_cast<const int8_t*>(x.smem + L::grow);
   int* gred = reinterpret_cast<int*>(x.smem + L::gred);
   const float* rq = reinterpret_cast<const float*>(x.smem + L::rq) + 16 * ti;
@@ -1426,6 +1544,7 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
         row_sc = sc_next;
         sc_next = sc_after;
         sc_after = next_scale();
+        next_page();
       }
       // row scales: s in [2^(gsh - 1), 2^gsh), the exponent bounded so that 2^-gsh is finite
       const int gsh = kBs ? gsh_bs
@@ -1730,7 +1849,11 @@ __global__ void __launch_bounds__(Geo<kMx, kTok, kPath>::threads, 1)
       if constexpr (kMx)
         producer_mx_rows(p, x, lane);
       else
-        producer_e4m3_gather<kTok>(p, x, lane);
+        // (the same for every CTA of a call)
+        if (p.page_shift < 3)
+          producer_e4m3_copies<kTok, kPath>(p, x, lane, 0);
+        else
+          producer_e4m3_boxes<kTok>(p, x, lane);
     } else if (lane == 0) {
       if constexpr (kBs)
         producer_mx_bs(p, x);
@@ -1748,7 +1871,10 @@ __global__ void __launch_bounds__(Geo<kMx, kTok, kPath>::threads, 1)
       pv_issuer<kMx, kTok, kPath>(p, x);
     __syncwarp();
   } else if (warp == 3) {
-    if (lane == 0) q_loader<kMx, kTok, kPath>(p, x);
+    if constexpr (kQkLoads<kMx, kPath>) {
+      if (p.page_shift < 3) producer_e4m3_copies<kTok, kPath>(p, x, lane, 1);
+    } else if (lane == 0)
+      q_loader<kMx, kTok, kPath>(p, x);
   } else if (warp < 4 + 4 * (kMx ? 1 : kTok)) {
     // softmax group (warp - 4) / 4: one per query token of the unit (one call
     // site, so that both groups run the same code)
