@@ -25,7 +25,9 @@
  *                    scale_stride >= 18 (only the first 18 bytes are read).
  *   MLA_KV_FP8_ROW   e4m3fn bytes [rows, 576] with one fp32 scale per row, scale_stride
  *                    bytes apart (a multiple of 4, >= 4): row t is code_t * scale_t.
- *                    The scales are finite, >= 0 and at most 2^120.  (The pages have
+ *                    The scales are finite, >= 0 and at most 2^120; a row of scale NaN (what
+ *                    mla_cache_append stores for values that are not finite, with codes 0)
+ *                    makes NaN of the outputs of the tokens that see it.  (The pages have
  *                    no counterpart; mla_cache_append writes it.)
  *
  * Calling sequence: mla_decode_plan() (or mla_decode_plan_multi /
@@ -241,10 +243,13 @@ MLA_API int mla_decode_poll_error(void* workspace, void* stream);
  * [kv_indptr[b], kv_indptr[b+1] - (q_len - 1 - i)) (none when that is not
  * positive: out = 0, lse = -inf).
  *
- * Two forms.  With e4m3 KV (fp8, fp8_row) and q_len = 2 the plan is fused (tokens_fused = 2):
- * the rule applies to the sequences' full row ranges, one work unit serves both
- * tokens, and the split kernel reads each cache row once, masking token 0's
- * last row; partial slot of token i of unit s of sequence b is
+ * Two forms.  With e4m3 KV (fp8 and q_len = 2; fp8_row and any q_len > 1) the plan is
+ * fused (tokens_fused = 2): the tokens of a sequence are taken in ceil(q_len / 2) pairs
+ * (2 i, 2 i + 1), of an odd number of tokens the first one alone; the rule applies
+ * to the pairs' row ranges in order (the rows that a pair's later token sees: for
+ * q_len = 2 the sequences' full rows), one work unit serves both tokens, and the split
+ * kernel reads each cache row once for them, masking the earlier token's
+ * last row (a code there that is NaN reaches both tokens, its scale only the later one); partial slot of token i of unit s of pair b is
  * 2 sum_{b' < b} S_b' + i S_b + s (num_work counts slots, 2 per unit).
  * Otherwise each token is decoded as a sequence of its own over its visible
  * rows, so the cache rows of a sequence are read once per token.
@@ -252,7 +257,7 @@ MLA_API int mla_decode_poll_error(void* workspace, void* stream);
  * mla_decode_plan_multi -- as mla_decode_plan for num_seqs sequences of
  * q_len (1..16) tokens each; the plan's batch is num_seqs * q_len (one output
  * row per token) and its rule applies to the tokens' row ranges in (b, i)
- * order (fused form: to the sequences' rows).  mla_decode_fwd with such a
+ * order (fused form: to the pairs').  mla_decode_fwd with such a
  * plan reads q rows qo_indptr[b] + i and writes out [num_seqs * q_len, 16, 512]
  * and lse [num_seqs * q_len, 16] in (b, i) order.  Returns the status codes of
  * mla_decode_plan.

@@ -256,8 +256,8 @@ class MLADecoder(_Decoder):
 
     The workspace is allocated once here (torch device memory) and zeroed; the
     library itself never allocates.  ``q_len > 1``: that many query tokens per
-    sequence (rows ``qo_indptr[b] + i``, output rows ``b * q_len + i``); e4m3 KV
-    ("fp8", "fp8_row") with ``q_len == 2`` gets the single-pass plan (``plan.tokens_fused == 2``).
+    sequence (rows ``qo_indptr[b] + i``, output rows ``b * q_len + i``); "fp8"
+    with ``q_len == 2`` and "fp8_row" read the cache once for two tokens (``plan.tokens_fused == 2``).
     ``mx_block_scaled``: MXFP4 scores from block-scaled MMAs on the e2m1 tile
     (``plan.mx_scores = 1``) instead of the e4m3 copy.  ``kv_scale`` of a call: fp32
     [1] ("fp8"), e8m0 bytes [rows, >= 18] ("mxfp4") or fp32 [rows] ("fp8_row")."""

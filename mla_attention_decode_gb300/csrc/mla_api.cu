@@ -489,16 +489,21 @@ int mla_decode_plan_multi(const int32_t* kv_indptr_host, int32_t num_seqs, int32
   if (!known_dtype(kv_dtype)) return MLA_ERR_UNSUPPORTED;
   if (num_splits < 0) return MLA_ERR_INVALID_ARG;
   if (kv_indptr_host[0] < 0) return MLA_ERR_INVALID_ARG;
-  // e4m3, two tokens: one unit list over the sequences' rows serves both
-  // tokens (the split kernel reads each row once); otherwise one entry per
-  // token over the rows up to its own entry
-  const bool fused = q_len == 2 && is_e4m3(kv_dtype);
-  std::vector<int64_t> lens(static_cast<size_t>(num_seqs) * (fused ? 1 : q_len));
+  // e4m3, two tokens (with row scales any number): one unit list entry for a
+  // pair of tokens, over the rows that the later one sees (the split kernel reads
+  // each row once for both); otherwise one entry per token over the rows up to
+  // its own entry
+  const bool fused = (q_len == 2 && kv_dtype == MLA_KV_FP8_E4M3) || (q_len >= 2 && kv_dtype == MLA_KV_FP8_ROW);
+  const int32_t pairs = (q_len + 1) / 2;
+  std::vector<int64_t> lens(static_cast<size_t>(num_seqs) * (fused ? pairs : q_len));
   for (int32_t b = 0; b < num_seqs; ++b) {
     const int64_t L = (int64_t)kv_indptr_host[b + 1] - kv_indptr_host[b];
     if (L < 0) return MLA_ERR_INVALID_ARG;
     if (fused) {
-      lens[static_cast<size_t>(b)] = L;
+      for (int32_t i = 0; i < pairs; ++i) {
+        const int64_t Li = L - 2 * (pairs - 1 - i);
+        lens[static_cast<size_t>(b) * pairs + i] = Li > 0 ? Li : 0;
+      }
       continue;
     }
     for (int32_t i = 0; i < q_len; ++i) {
@@ -512,7 +517,7 @@ int mla_decode_plan_multi(const int32_t* kv_indptr_host, int32_t num_seqs, int32
   if (rc != MLA_OK) return rc;
   if (fused) {
     if (2 * (int64_t)p.num_work > INT32_MAX) return MLA_ERR_UNSUPPORTED;
-    p.batch = 2 * num_seqs;
+    p.batch = q_len * num_seqs;
     p.num_work *= 2;  // partial slots: two per work unit
     p.tokens_fused = 2;
   }
@@ -654,10 +659,12 @@ int prepare(const void* q, const void* kv, const void* kv_scale, int32_t scale_s
     if (r < -1 || r >= plan->total_kv) return MLA_ERR_INVALID_ARG;  // a row of the cache, or none
     p->first_row[c] = r;
   }
-  if (plan->tokens_fused != 0 && (plan->tokens_fused != 2 || !is_e4m3(plan->kv_dtype) ||
-                                  plan->q_len != 2 || plan->num_work % 2 != 0))
+  if (plan->tokens_fused != 0 && (plan->tokens_fused != 2 || !is_e4m3(plan->kv_dtype) || plan->q_len < 2 ||
+                                  (plan->q_len > 2 && plan->kv_dtype != MLA_KV_FP8_ROW) || plan->num_work % 2 != 0))
     return MLA_ERR_INVALID_ARG;
-  const int32_t entries = plan->batch / p->tok;  // sequences in the unit list
+  // entries of the unit list: output rows, or pairs of tokens
+  const int32_t entries = p->tok == 2 ? plan->batch / p->q_len * ((p->q_len + 1) / 2) : plan->batch;
+  p->entries = entries;
   if (plan->schedule != 0 && (plan->schedule != 1 || plan->total_tiles < plan->grid)) return MLA_ERR_INVALID_ARG;
   // schedule 1's late CTAs (see late_ctas): every CTA keeps at least two positions
   p->late_tiles = plan->late_tiles;

@@ -146,16 +146,28 @@ __device__ __forceinline__ int query_row(const Stage1Params& p, int b) {
   return p.qo_indptr[b];
 }
 
+// With TOK = 2 tokens per unit, entry b of the unit list is a pair of tokens of one
+// sequence: pair i of the ceil(q_len / 2) of sequence s holds tokens 2 i - odd and
+// 2 i - odd + 1 (odd = q_len mod 2: an odd count's first pair has no first token).
+// Output row of token ti of entry b, -1 for a token that there is not.
+template <int TOK>
+__device__ __forceinline__ int entry_row(const Stage1Params& p, int b, int ti) {
+  if constexpr (TOK == 1) return b;
+  const int pairs = (p.q_len + 1) >> 1, s = b / pairs, tok = 2 * (b - s * pairs) - (p.q_len & 1) + ti;
+  return tok < 0 ? -1 : s * p.q_len + tok;
+}
+
 // Rows and query check of unit-list entry b: output row b (its own rows,
-// query row qo_indptr-derived), or with TOK = 2 tokens per unit sequence b,
-// whose full rows both tokens' units cover; qrow < 0 flags a bad query row.
+// query row qo_indptr-derived), or with TOK = 2 tokens per unit a pair of tokens,
+// over the rows that its last token sees; qrow < 0 flags a bad query row.
 template <int TOK>
 __device__ __forceinline__ bool entry_rows(const Stage1Params& p, int b, int& start, int& end, int& qrow) {
   if constexpr (TOK > 1) {
-    const int a = p.kv_indptr[b], z = p.kv_indptr[b + 1];
+    const int last = entry_row<TOK>(p, b, 1), s = last / p.q_len;
+    const int a = p.kv_indptr[s], z = p.kv_indptr[s + 1];
     start = a;
-    end = z;
-    qrow = query_row(p, TOK * b);  // the sequence's tokens are query rows qrow, qrow + 1, ...
+    end = max(a, z - (p.q_len - 1 - (last - s * p.q_len)));
+    qrow = query_row(p, s * p.q_len);  // the sequence's tokens are query rows qrow, qrow + 1, ...
     return a >= 0 && z >= a;
   } else {
     qrow = query_row(p, b);
@@ -256,7 +268,7 @@ template <int TILE, int MAX_UNITS, int TOK>
 __device__ __forceinline__ void scan_units_contiguous(const Stage1Params& p, UnitDesc* units, int* s_nunits,
                                                       int lane) {
   const long long T = p.total_tiles, G = p.grid, c = blockIdx.x, U = p.unit_cost;
-  const int nseq = p.batch / TOK;       // unit-list entries: sequences of a two-token plan
+  const int nseq = p.entries;           // unit-list entries: pairs of tokens of a two-token plan
   const int nunits = p.num_work / TOK;  // work units (num_work counts partial slots)
   const long long C = T + U * (nseq > 0 ? nseq - 1 : 0);
   const long long L = p.late_ctas, D = p.late_tiles, Cp = C + L * D;
@@ -308,8 +320,10 @@ __device__ __forceinline__ void scan_units_contiguous(const Stage1Params& p, Uni
       const bool fits = ub + sb <= nunits;
 #pragma unroll
       for (int i = 0; i < TOK; ++i) {
-        p.ws_seq[2 * (TOK * b + i)] = fits ? TOK * ub + i * sb : 0;
-        p.ws_seq[2 * (TOK * b + i) + 1] = fits ? sb : 0;
+        const int row = entry_row<TOK>(p, b, i);
+        if (TOK > 1 && row < 0) continue;
+        p.ws_seq[2 * row] = fits ? TOK * ub + i * sb : 0;
+        p.ws_seq[2 * row + 1] = fits ? sb : 0;
       }
     }
     // a unit past the plan's slots is not taken, and not counted (the list stays gap-free)
@@ -346,7 +360,7 @@ __device__ __forceinline__ void scan_units_contiguous(const Stage1Params& p, Uni
 }
 
 // TOK: output rows per unit-list entry (2: a two-token plan, whose entries are
-// sequences and whose units serve both tokens; compile-time, so that the
+// pairs of tokens and whose units serve both; compile-time, so that the
 // one-token scan carries none of it).
 template <int TILE, int MAX_UNITS = kMaxUnitsPerCta, int TOK = 1>
 __device__ __forceinline__ void scan_units(const Stage1Params& p, UnitDesc* units, int* s_nunits, int lane) {
@@ -354,7 +368,7 @@ __device__ __forceinline__ void scan_units(const Stage1Params& p, UnitDesc* unit
     scan_units_contiguous<TILE, MAX_UNITS, TOK>(p, units, s_nunits, lane);
     return;
   }
-  const int nseq = p.batch / TOK;       // unit-list entries: sequences of a two-token plan
+  const int nseq = p.entries;           // unit-list entries: pairs of tokens of a two-token plan
   const int nunits = p.num_work / TOK;  // work units (num_work counts partial slots)
   int prefix = 0, count = 0;
   bool bad = false;
@@ -382,8 +396,10 @@ __device__ __forceinline__ void scan_units(const Stage1Params& p, UnitDesc* unit
       const bool fits = pb + sb <= nunits;
 #pragma unroll
       for (int i = 0; i < TOK; ++i) {
-        p.ws_seq[2 * (TOK * b + i)] = fits ? TOK * pb + i * sb : 0;
-        p.ws_seq[2 * (TOK * b + i) + 1] = fits ? sb : 0;
+        const int row = entry_row<TOK>(p, b, i);
+        if (TOK > 1 && row < 0) continue;
+        p.ws_seq[2 * row] = fits ? TOK * pb + i * sb : 0;
+        p.ws_seq[2 * row + 1] = fits ? sb : 0;
       }
     }
     int n = 0, first = 0;

@@ -86,6 +86,7 @@ struct Stage1Params {
   int32_t q_len;        // query tokens per sequence; batch counts tokens
   int32_t tok;          // tokens one work unit serves (2: fused two-token e4m3 plan, else 1);
                         // num_work then counts partial slots, tok per unit
+  int32_t entries;      // of the unit list: output rows, or pairs of tokens of a fused plan
   int32_t mx_bs;        // MXFP4 (contiguous, pages >= 64 rows): 1 = scores by block-scaled MMAs
   int32_t late_ctas;    // schedule 1: the last late_ctas CTAs own late_tiles positions fewer
   int32_t late_tiles;

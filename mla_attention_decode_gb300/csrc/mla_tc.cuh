@@ -37,11 +37,14 @@
 // [32 (w mod 4), +32)).  Hand-offs are mbarriers (TMA transaction bytes,
 // tcgen05.commit, thread arrivals).
 //
-// Two query tokens per unit (kTok = 2, e4m3; several tokens per sequence,
+// Two query tokens per unit (kTok = 2, e4m3; pairs of several tokens per sequence,
 // the causal reading): each tile feeds two QKs and two P.V chains, one per
 // token, into their own TMEM columns, and warps 8-11 form a second softmax
 // group for token 1, so the cache rows are read once for both tokens.  Token
-// 0 does not see its sequence's last row (token 1's own entry).
+// 0 does not see the pair's last row (token 1's own entry).  An odd number of
+// tokens leaves its first one alone: that pair's token 0 repeats token 1's query
+// and writes nothing (five tokens over 32 x 4096 rows with scales 63.0 us in three
+// passes, against 71.4 a token at a time; eight in four passes 78.0 against 112.8).
 //
 // MXFP4 KV (kMx): rows arrive packed (288 B of e2m1 pairs, element 2i in the low
 // nibble of byte i) by 1-D bulk copies of 64-row halves into a staging ring,
@@ -162,8 +165,8 @@ struct Layout {
   static constexpr int pb = qs + kQsBytes * kTok;             // [2 tiles][kTok]
   static constexpr int rq = pb + 2 * kPBytes * kTok;          // float [kTok][16] score factor per head
   static constexpr int red = rq + 16 * 4 * kTok;              // float [2][4 warps][16 kTok]
-  static constexpr int gred = red + 2 * 4 * 16 * 4 * kTok;    // int [2][4] tile max of the row exponents
-  static constexpr int grow = gred + 2 * 4 * 4;               // int8 [2][128] row exponent G - 127 (MXFP4)
+  static constexpr int gred = red + 2 * 4 * 16 * 4 * kTok;    // int [kTok][2][4] tile max of the row exponents
+  static constexpr int grow = gred + 2 * 4 * 4 * kTok;        // int8 [2][128] row exponent G - 127 (MXFP4)
   static constexpr int lut = grow + (kMx ? 2 * 128 : 0);      // u8 [32][8] e2m1 magnitude -> e4m3 per shift
   static constexpr int hand = lut + (kMx ? 256 : 0);          // float [2][32] l, m handed to the epilogue group
   static constexpr int handg = hand + (G::epi ? 256 : 0);     // int [2] Gv handed over (row scales)
@@ -1039,7 +1042,9 @@ __device__ __forceinline__ void load_query(const Stage1Params& p, const Ctx& x, 
   mbar_arrive_expect_tx(&x.bar[kQFull], (uint32_t)(kTok * kQPrepBytes));
 #pragma unroll
   for (int i = 0; i < kTok; ++i) {
-    const uint8_t* src = p.ws_q + ((size_t)x.units[k].b * kTok + i) * kQPrepBytes;
+    int qr = entry_row<kTok>(p, x.units[k].b, i);
+    if (kTok > 1 && qr < 0) qr = entry_row<kTok>(p, x.units[k].b, 1);  // (no first token: the second one's again)
+    const uint8_t* src = p.ws_q + (size_t)qr * kQPrepBytes;
     if constexpr (kTok == 1) {
       bulk_g2s(x.smem + L::qs, src, (uint32_t)kQImageBytes, &x.bar[kQFull], pol);
     } else {
@@ -1055,7 +1060,7 @@ __device__ __forceinline__ void load_query(const Stage1Params& p, const Ctx& x, 
 // shared-memory image (two-term e4m3, 64-byte swizzle) plus its 16 score
 // factors, comes in by two bulk copies per token once the last QK of unit k-1
 // has completed and the softmax has taken unit k-1's factors (token i of a
-// two-token unit of sequence b: the prepared output row 2 b + i).  The
+// two-token unit: its prepared output row, entry_row).  The
 // prepared queries are the one input written by the preceding grid, so this
 // is the one thread that waits for it.
 template <bool kMx, int kTok, int kPath>
@@ -1429,7 +1434,7 @@ __device__ __forceinline__ void group_reduce16(float (&v)[16], float* red, int w
 // Softmax group ti (four warps; one group per query token of the unit):
 // thread `row` owns tile row `row` (its TMEM lane) for the token's 16 heads,
 // in TMEM columns [32 ti, +32) of the S^T buffers and O^T blocks.  With two
-// tokens, token 0 does not see the last row of its sequence (token 1's own
+// tokens, token 0 does not see the pair's last row (token 1's own
 // entry), and token ti's partial slot is u + ti S_b.
 template <bool kMx, int kTok, int kPath>
 __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, int lane, int ti) {
@@ -1473,7 +1478,7 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
     next_page();
   }
   const int8_t* grow = reinterpret_cast<const int8_t*>(x.smem + L::grow);
-  int* gred = reinterpret_cast<int*>(x.smem + L::gred);
+  int* gred = reinterpret_cast<int*>(x.smem + L::gred) + 8 * ti;  // (the groups raise at tiles of their own)
   const float* rq = reinterpret_cast<const float*>(x.smem + L::rq) + 16 * ti;
   float* redbuf = reinterpret_cast<float*>(x.smem + L::red) + 128 * ti;
   constexpr bool kEpi = Geo<kMx, kTok, kPath>::epi;
@@ -1489,12 +1494,14 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
     const bool final_out = (d.u & kFinalFlag) != 0;
     // output row and partial slot of this group's token; the rows it does not
     // see at the end of the sequence's last unit
-    const int ob = d.b * kTok + ti;
+    const int ob = entry_row<kTok>(p, d.b, ti);
+    const bool none = kTok > 1 && ob < 0;  // an odd count's first pair has no first token
     const int u = (d.u & ~kFinalFlag) + (kTok > 1 ? ti * (d.qrow & ~kLastUnitBit) : 0);
     const int hidden = (kTok > 1 && (d.qrow & kLastUnitBit) != 0) ? kTok - 1 - ti : 0;
     const int nt = tiles_of(d);
     if (nt == 0) {
       // empty sequence: out = 0, lse = -inf
+      if (none) continue;
       for (int i = row; i < kHeads * kVDim; i += 128) {
         if (final_out)
           p.out[(size_t)ob * kHeads * kVDim + i] = 0;
@@ -1541,7 +1548,7 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
       if (kMx && !kBs) wait_phase(&x.bar[kConvFull + sb], (it >> 1) & 1, x.abort_flag, p.ws_err);
       float row_sc = 0.f;
       if constexpr (kRow) {
-        row_sc = sc_next;
+        row_sc = kTok == 1 || row < vis ? sc_next : 0.f;  // (a hidden row's scale: nothing of it)
         sc_next = sc_after;
         sc_after = next_scale();
         next_page();
@@ -1709,7 +1716,7 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
       ++ordinal;
       tc::fence_after();
       const float out_scale = kG ? exp2_int(max(-126, min(127, gv))) : kv_scale;
-      write_unit<kMx, kRow>(p, tl_o, TM::blk, row, final_out, ob, u, l_part, m_ref, out_scale);
+      if (!none) write_unit<kMx, kRow>(p, tl_o, TM::blk, row, final_out, ob, u, l_part, m_ref, out_scale);
       if (row == 0 && ti == 0 && k < 8) trace_stamp(p, kTrUnitDone + k);
       tc::fence_before();
       __syncwarp();

@@ -271,20 +271,24 @@ def poisoned(codes, s, total):
 
 @pytest.mark.parametrize("lens,splits", [([1], 0), ([5, 0, 130, 1, 128, 257, 1000], 0), ([0, 0], 0), ([129, 3000, 64], 3),
                                          ([4097] * 3 + [17], 0), ([33] * 200, 0)])
-@pytest.mark.parametrize("q_len", [1, 2, 3])
+@pytest.mark.parametrize("q_len", [1, 2, 3, 4, 5, 8, 15, 16])
 def test_decode(lens, splits, q_len):
     g = gen(sum(lens) + q_len)
     ind = indptr_of(lens)
     codes, s = random_cache(g, max(1, sum(lens)))
     c, x = poisoned(codes, s, max(1, sum(lens)) + 130)
-    q = torch.randn(len(lens) * q_len + 1, 16, 576, generator=g).to(torch.bfloat16)
-    qo = (torch.arange(len(lens) + 1) * q_len).to(torch.int32)
+    # queries that no sequence has (behind the last; between two) are NaN
+    q = torch.randn(len(lens) * (q_len + 1) + 1, 16, 576, generator=g).to(torch.bfloat16)
+    qo = (torch.arange(len(lens) + 1) * (q_len + 1)).to(torch.int32)
+    owned = (torch.arange(len(lens)).view(-1, 1) * (q_len + 1) + torch.arange(q_len)).flatten()
+    q0, q = q[owned].clone(), torch.full_like(q, float("nan"))
+    q[owned] = q0
     dec = binding.MLADecoder(ind, "fp8_row", num_splits=splits, q_len=q_len)
-    assert dec.plan.tokens_fused == (2 if q_len == 2 else 0)
+    assert dec.plan.tokens_fused == (2 if q_len > 1 else 0) and dec.plan.batch == len(lens) * q_len
     out, lse = dec(q.to(DEV), c.to(DEV), ind.to(DEV), qo.to(DEV), kv_scale=x.to(DEV))
     assert dec.poll_error() == 0
     spans = [list(range(int(a), int(e))) for a, e in zip(ind[:-1], ind[1:])]
-    check(out, lse, reference(q, codes, s, spans, q_len))
+    check(out, lse, reference(q0, codes, s, spans, q_len))
 
 
 @pytest.mark.parametrize("page", [1, 2, 4, 8, 16, 32, 64, 128, 256])
@@ -339,6 +343,30 @@ def test_decode_scales_of_all_sizes(scale):
         out, lse = dec(q.to(DEV), codes.to(DEV), ind.to(DEV), qo.to(DEV), kv_scale=s.to(DEV))
         assert dec.poll_error() == 0
         check(out, lse, reference(q, codes, s, [list(range(n))]))
+
+
+@pytest.mark.parametrize("q_len", [2, 3, 4, 7])
+@pytest.mark.parametrize("scale", [float("nan"), 2.0 ** 120, 0.0])
+def test_scales_of_rows_that_a_token_does_not_see(q_len, scale):
+    """The last q_len - 1 rows hold any scale: the first token's output is the same, bit for bit,
+    and so is every token's that the rows behind it leave."""
+    g, lens = gen(17), [300, 129, 128, 2500, q_len]
+    ind = indptr_of(lens)
+    codes, s = random_cache(g, sum(lens))
+    q = torch.randn(len(lens) * q_len, 16, 576, generator=g).to(torch.bfloat16).to(DEV)
+    qo = (torch.arange(len(lens) + 1) * q_len).to(torch.int32).to(DEV)
+    dec = binding.MLADecoder(ind, "fp8_row", q_len=q_len)
+    full, full_lse = (x.clone() for x in dec(q, codes.to(DEV), ind.to(DEV), qo, kv_scale=s.to(DEV)))
+    for seen in range(1, q_len):  # tokens that keep every row they see
+        c, x = codes.clone(), s.clone()
+        for e in ind[1:].tolist():
+            c[e - (q_len - seen):e] = 0 if scale != scale else 120
+            x[e - (q_len - seen):e] = scale
+        out, lse = dec(q, c.to(DEV), ind.to(DEV), qo, kv_scale=x.to(DEV))
+        keep = torch.arange(len(lens) * q_len, device=DEV) % q_len < seen
+        assert torch.equal(out[keep], full[keep]) and torch.equal(lse[keep], full_lse[keep]), seen
+        if scale != scale:
+            assert torch.all(torch.isnan(out[~keep].float())) and torch.all(torch.isnan(lse[~keep]))
 
 
 @pytest.mark.parametrize("n,bad", [(1, 0), (300, 299), (300, 0), (900, 500)])

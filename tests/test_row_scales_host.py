@@ -54,7 +54,7 @@ def test_decode_refusals(lib, scale, stride, paged):
 
 
 @pytest.mark.parametrize("lens", [[5], [0, 300, 8192, 1], [2000] * 64])
-@pytest.mark.parametrize("q_len", [1, 2, 4])
+@pytest.mark.parametrize("q_len", [1, 2])
 def test_plans_are_those_of_one_scale_for_all(lens, q_len):
     """Tiles, ranges and fusion do not depend on where the scales are (the cost model's bytes a row
     differ by less than 1%, which these layouts do not notice)."""
@@ -65,6 +65,37 @@ def test_plans_are_those_of_one_scale_for_all(lens, q_len):
             binding.mla_decode_plan(ind, dt, num_sms=152) for dt in ("fp8", "fp8_row"))
     a.kv_dtype = ROW
     assert a.as_dict() == b.as_dict() and list(a.first_row) == list(b.first_row)
+
+
+@pytest.mark.parametrize("q_len", [2, 3, 4, 5, 15, 16])
+@pytest.mark.parametrize("splits", [0, 1, 17])
+def test_pairs_of_tokens_plan_as_entries(q_len, splits):
+    """The unit list is that of the rows which each pair's later token sees; two slots a unit."""
+    lens = [0, 1, 2, 5, 129, 300, 4000, 9000]
+    ind = [0]
+    for n in lens:
+        ind.append(ind[-1] + n)
+    plan = binding.mla_decode_plan_multi(ind, q_len, "fp8_row", num_sms=7, num_splits=splits)
+    assert (plan.tokens_fused, plan.q_len, plan.batch) == (2, q_len, len(lens) * q_len)
+    pairs = (q_len + 1) // 2
+    rows = [0]
+    for n in lens:
+        for i in range(pairs):  # the later token is q_len - 1 - 2 (pairs - 1 - i)
+            rows.append(rows[-1] + max(0, n - 2 * (pairs - 1 - i)))
+    ref = binding.mla_decode_plan(rows, "fp8_row", num_sms=7, num_splits=splits)
+    assert plan.schedule == ref.schedule and plan.total_tiles == ref.total_tiles
+    if plan.late_tiles == ref.late_tiles == 0:
+        assert plan.num_work == 2 * ref.num_work and plan.splits_max == ref.splits_max
+
+
+def test_fused_plans_are_checked(lib):
+    """What the planner does not make is refused: an odd number of slots, a fused plan of another format."""
+    def fwd(plan):
+        return lib.mla_decode_fwd(FAKE, FAKE, FAKE, 4, FAKE, FAKE, FAKE, None, 1 / 24, ctypes.byref(plan), FAKE + 8, 1 << 30, None)
+    for field, value in (("num_work", 3), ("q_len", 1), ("q_len", 17), ("tokens_fused", 3), ("kv_dtype", 1), ("kv_dtype", 2), ("batch", 7)):
+        plan = binding.mla_decode_plan_multi([0, 300, 700], 4, "fp8_row", num_sms=152)
+        setattr(plan, field, value)
+        assert fwd(plan) == INVALID, field
 
 
 def test_formats_that_do_not_exist_are_refused(lib):
