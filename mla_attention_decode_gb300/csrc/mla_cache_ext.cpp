@@ -492,7 +492,9 @@ PyObject* py_decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     if (scale->dim() < 1) refuse("kv_scale is [rows, >= 18]");
     stride = scale->stride(0);
   } else if (scale && plan->kv_dtype == MLA_KV_FP8_ROW) {
-    if (scale->scalar_type() != at::kFloat || scale->dim() != 1) refuse("kv_scale is fp32 [rows]");
+    const int64_t rows = plan->page_size ? (int64_t)plan->num_pages * plan->page_size : plan->total_kv;
+    if (scale->scalar_type() != at::kFloat || scale->dim() != 1 || scale->size(0) < rows)
+      refuse("kv_scale is fp32 [rows], rows >= %lld", (long long)rows);
     stride = scale->size(0) > 1 ? 4 * scale->stride(0) : 4;  // (one scale has no stride)
   }
   if (stride < 0 || stride > INT32_MAX) refuse("kv_scale's rows are too far apart");

@@ -535,7 +535,7 @@ def test_python_refusals():
             cache.MLACachePool(kv, "fp8_row", 16, kv_scale=bad)
     dec = binding.MLADecoder([0, 64], "fp8_row")
     q, ind = torch.zeros(1, 16, 576, dtype=torch.bfloat16, device=DEV), torch.tensor([0, 64], dtype=torch.int32, device=DEV)
-    for bad in (torch.ones(64, 1, device=DEV), torch.ones(64, dtype=torch.bfloat16, device=DEV)):
+    for bad in (torch.ones(64, 1, device=DEV), torch.ones(64, dtype=torch.bfloat16, device=DEV), torch.ones(63, device=DEV)):
         with pytest.raises(ValueError):
             dec(q, kv, ind, ind, kv_scale=bad)
     for bad in (None, torch.ones(1, device=DEV).expand(64)):
