@@ -305,12 +305,14 @@ int device_sm_count(int32_t* out) {
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // plan->first_row (mla_decode.h): the first row of the first non-empty unit of
-// each CTA, by the unit rules of the plan's schedule (contiguous single-token
-// plans; the others say -1).
-void fill_first_rows(mla_plan* plan, const int32_t* kv_indptr_host) {
+// each CTA, by the unit rules of the plan's schedule, for unit-list entries of lens[b] rows
+// that begin at row first(b) (contiguous plans of one token, or fp8_row's of pairs; the
+// others say -1).
+template <class First>
+void fill_first_rows(mla_plan* plan, const std::vector<int64_t>& lens, First first) {
   for (int c = 0; c < MLA_PLAN_FIRST_ROWS; ++c) plan->first_row[c] = -1;
-  if (!kv_indptr_host || plan->batch <= 0 || plan->grid <= 0) return;
-  const int64_t B = plan->batch, G = plan->grid, R = plan->tile_tokens;
+  if (lens.empty() || plan->grid <= 0) return;
+  const int64_t B = static_cast<int64_t>(lens.size()), G = plan->grid, R = plan->tile_tokens;
   auto set = [&](int64_t c, int64_t row) {
     if (c >= 0 && c < MLA_PLAN_FIRST_ROWS && plan->first_row[c] < 0) plan->first_row[c] = static_cast<int32_t>(row);
   };
@@ -320,24 +322,24 @@ void fill_first_rows(mla_plan* plan, const int32_t* kv_indptr_host) {
     const Partition part{C, G, L, D};
     int64_t P = 0;
     for (int64_t b = 0; b < B; ++b) {
-      const int64_t L = (int64_t)kv_indptr_host[b + 1] - kv_indptr_host[b];
+      const int64_t L = lens[static_cast<size_t>(b)];
       const int64_t w = L > 0 ? (L + R - 1) / R : 1;
       const int64_t X = P + U * b;
       if (L > 0)
         for (int64_t c = part.cta(X); c <= part.cta(X + w - 1); ++c) {
           const int64_t lo = part.lo(c);
-          set(c, kv_indptr_host[b] + R * ((lo > X ? lo : X) - X));
+          set(c, first(b) + R * ((lo > X ? lo : X) - X));
         }
       P += w;
     }
   } else {
     int64_t u = 0;
     for (int64_t b = 0; b < B; ++b) {
-      const int64_t L = (int64_t)kv_indptr_host[b + 1] - kv_indptr_host[b];
+      const int64_t L = lens[static_cast<size_t>(b)];
       const int32_t S = splits_for(L, plan->chunk_tokens, plan->max_splits, static_cast<int>(R));
       const int64_t t = (L + R - 1) / R;
       for (int32_t sp = 0; sp < S; ++sp, ++u)
-        if (L > 0) set(u % G, kv_indptr_host[b] + R * ((int64_t)sp * t / S));
+        if (L > 0) set(u % G, first(b) + R * ((int64_t)sp * t / S));
     }
   }
 }
@@ -477,7 +479,7 @@ int mla_decode_plan(const int32_t* kv_indptr_host, int32_t batch, int32_t kv_dty
     lens[static_cast<size_t>(b)] = L;
   }
   const int rc = plan_lengths(lens, kv_indptr_host[batch], kv_dtype, num_sms, num_splits, plan, batch);
-  if (rc == MLA_OK) fill_first_rows(plan, kv_indptr_host);
+  if (rc == MLA_OK) fill_first_rows(plan, lens, [&](int64_t b) { return (int64_t)kv_indptr_host[b]; });
   return rc;
 }
 
@@ -522,6 +524,8 @@ int mla_decode_plan_multi(const int32_t* kv_indptr_host, int32_t num_seqs, int32
     p.tokens_fused = 2;
   }
   p.q_len = q_len;
+  if (fused && kv_dtype == MLA_KV_FP8_ROW)
+    fill_first_rows(&p, lens, [&](int64_t b) { return (int64_t)kv_indptr_host[b / pairs]; });
   *plan = p;
   return MLA_OK;
 }
@@ -651,9 +655,9 @@ int prepare(const void* q, const void* kv, const void* kv_scale, int32_t scale_s
   // MXFP4 scores by block-scaled MMAs (pages of fewer than 64 rows take the copy)
   if (plan->mx_scores != 0 && (plan->mx_scores != 1 || plan->kv_dtype != MLA_KV_MXFP4)) return MLA_ERR_INVALID_ARG;
   p->mx_bs = (plan->mx_scores == 1 && !(paged && page_shift < 6)) ? 1 : 0;
-  // the first tile rows of a contiguous single-token plan (the e4m3 split
-  // kernel starts those copies before its unit scan)
-  const bool first_rows = !paged && p->q_len == 1 && p->tok == 1;
+  // the first tile rows of a contiguous plan of one token, or fp8_row's of pairs (the
+  // e4m3 split kernel starts those copies before its unit scan)
+  const bool first_rows = !paged && (p->tok == 2 ? plan->kv_dtype == MLA_KV_FP8_ROW : p->q_len == 1);
   for (int c = 0; c < MLA_PLAN_FIRST_ROWS; ++c) {
     const int32_t r = first_rows ? plan->first_row[c] : -1;
     if (r < -1 || r >= plan->total_kv) return MLA_ERR_INVALID_ARG;  // a row of the cache, or none
@@ -680,6 +684,12 @@ int prepare(const void* q, const void* kv, const void* kv_scale, int32_t scale_s
     if (C + (int64_t)p->late_ctas * plan->late_tiles < (int64_t)(plan->late_tiles + 2) * plan->grid ||
         C + (int64_t)p->late_ctas * plan->late_tiles > INT32_MAX)
       return MLA_ERR_INVALID_ARG;
+  }
+  if (plan->schedule == 1) {
+    const int64_t C = (int64_t)plan->total_tiles + (int64_t)plan->unit_cost * (entries > 0 ? entries - 1 : 0) +
+                      (int64_t)p->late_ctas * plan->late_tiles;
+    p->share = static_cast<int32_t>(C / plan->grid);
+    p->share_rest = static_cast<int32_t>(C % plan->grid);
   }
   if (is_e4m3(plan->kv_dtype)) {
     if (!encode_kv_map_tc(&p->tmap_kv64, kv, cache_rows, 128)) return MLA_ERR_CUDA;

@@ -248,11 +248,22 @@ __device__ __forceinline__ float4 bf16x4_to_f4(uint2 v) {
 // the combine kernel.  Sequence b is cut into S_b splits on TILE-row tile
 // boundaries.  Inconsistent index data raises MLA_ERR_DEVICE_INDEX and the
 // affected sequences are treated as empty.
+// floor(n / d), n >= 0, d > 0, for quotients far below 2^24 (numbers of CTAs or splits): a
+// float's estimate put right by products.  A 64-bit division is a call of a hundred
+// dependent instructions, and the unit list, which everything waits for, had seven
+// (a trace at 4 x 8192 rows: the list ready 1.8 us after a CTA's start instead of 4.2).
+__device__ __forceinline__ int small_quotient(long long n, long long d) {
+  int q = (int)__fdividef((float)n, (float)d);
+  while ((long long)q * d > n) --q;
+  while ((long long)(q + 1) * d <= n) ++q;
+  return q;
+}
+
 template <int TILE>
 __device__ __forceinline__ int splits_of(int len, int chunk, int cap) {
   if (len <= 0) return 1;
   const int tiles = (len + TILE - 1) / TILE;
-  int s = (int)(((long long)len + chunk - 1) / chunk);
+  int s = (int)(((unsigned)len + (unsigned)chunk - 1u) / (unsigned)chunk);  // (both below 2^31)
   s = min(s, cap);
   s = min(s, tiles);
   return max(s, 1);
@@ -272,10 +283,13 @@ __device__ __forceinline__ void scan_units_contiguous(const Stage1Params& p, Uni
   const int nunits = p.num_work / TOK;  // work units (num_work counts partial slots)
   const long long C = T + U * (nseq > 0 ? nseq - 1 : 0);
   const long long L = p.late_ctas, D = p.late_tiles, Cp = C + L * D;
-  auto bound = [&](long long k) { return k * Cp / G - D * (k > G - L ? k - (G - L) : 0); };
+  auto bound = [&](long long k) {  // floor(k C' / G) by the parts of C' / G
+    return k * p.share + small_quotient(k * p.share_rest, G) - D * (k > G - L ? k - (G - L) : 0);
+  };
   const long long lo = bound(c), hi = bound(c + 1), late0 = bound(G - L);
   auto cta_of = [&](long long x) {
-    return (D == 0 || x < late0) ? ((x + 1) * G - 1) / Cp : ((x - D * (G - L) + 1) * G - 1) / (Cp - D * G);
+    const bool late = D != 0 && x >= late0;
+    return small_quotient((late ? x - D * (G - L) + 1 : x + 1) * G - 1, late ? Cp - D * G : Cp);
   };
   long long tprefix = 0;  // tiles of the sequences before this chunk of 32
   int uprefix = 0, count = 0;
@@ -303,8 +317,8 @@ __device__ __forceinline__ void scan_units_contiguous(const Stage1Params& p, Uni
       if (P + w > T) {
         bad = true;  // the device kv_indptr holds more tiles than the plan
       } else {
-        cf = (int)cta_of(X);
-        sb = (int)(cta_of(X + w - 1) - cf + 1);
+        cf = cta_of(X);
+        sb = cta_of(X + w - 1) - cf + 1;
       }
     }
     int sincl = sb;
@@ -404,7 +418,7 @@ __device__ __forceinline__ void scan_units(const Stage1Params& p, UnitDesc* unit
     }
     int n = 0, first = 0;
     if (b < nseq) {
-      int off = (int)(((long long)blockIdx.x - pb) % p.grid);
+      int off = (int)blockIdx.x - (int)((unsigned)pb % (unsigned)p.grid);
       if (off < 0) off += p.grid;
       first = pb + off;
       if (first < pb + sb) n = (pb + sb - 1 - first) / p.grid + 1;
@@ -423,6 +437,9 @@ __device__ __forceinline__ void scan_units(const Stage1Params& p, UnitDesc* unit
     }
     const int pos = count + nincl - n;
     const int tiles = (end - start + TILE - 1) / TILE;
+    // the first tile of split s: floor(s tiles / sb), by the parts of tiles / sb
+    const int each = n > 0 ? (int)((unsigned)tiles / (unsigned)sb) : 0, rest = tiles - each * sb;
+    auto tile_of = [&](int s) { return s * each + small_quotient((long long)s * rest, sb); };
     for (int k = 0; k < n; ++k) {
       const int u = first + k * p.grid;
       const int s = u - pb;
@@ -432,8 +449,8 @@ __device__ __forceinline__ void scan_units(const Stage1Params& p, UnitDesc* unit
       }
       UnitDesc d;
       d.b = b;
-      d.start = start + TILE * (int)((long long)s * tiles / sb);
-      d.end = min(end, start + TILE * (int)((long long)(s + 1) * tiles / sb));
+      d.start = start + TILE * tile_of(s);
+      d.end = min(end, start + TILE * tile_of(s + 1));
       d.u = (TOK * pb + s) | (sb == 1 ? kFinalFlag : 0);
       d.qrow = TOK > 1 ? (sb | (s == sb - 1 ? kLastUnitBit : 0)) : qrow;
       units[pos + k] = d;

@@ -90,6 +90,7 @@ struct Stage1Params {
   int32_t mx_bs;        // MXFP4 (contiguous, pages >= 64 rows): 1 = scores by block-scaled MMAs
   int32_t late_ctas;    // schedule 1: the last late_ctas CTAs own late_tiles positions fewer
   int32_t late_tiles;
+  int32_t share, share_rest;  // schedule 1: C' = share grid + share_rest (C' as in scan_units_contiguous)
   uint64_t* trace;      // trace builds only: [grid][kTraceSlots] global-timer stamps (else null)
   int32_t first_row[MLA_PLAN_FIRST_ROWS];  // the plan's first tile row per CTA (-1: none; see mla_plan)
 };

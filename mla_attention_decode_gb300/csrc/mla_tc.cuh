@@ -94,7 +94,9 @@ struct Geo {
   static_assert(kPath != kPathBlockScaled || (kMx && kTok == 1), "block-scaled scores: MXFP4, one token");
   static_assert(!row_scales(kPath) || !kMx, "row scales: e4m3");
   static constexpr bool bs = kPath == kPathBlockScaled;
-  static constexpr int pair_slots = kMx ? (bs ? 10 : 8) : (kTok == 1 ? 11 : 9);  // ring of column-block pairs (4 per tile)
+  static constexpr int pair_slots = kMx ? (bs ? 10 : 8) : (kTok == 1 ? 11 : 10);  // ring of column-block pairs (4 per tile)
+  // P^T buffers: two tokens have one, the room of the other is a slot of the ring
+  static constexpr int p_bufs = kTok == 1 ? 2 : 1;
   // e4m3, one token per unit: a separate epilogue group (warps 8-11) drains
   // each unit's O^T from its own TMEM buffer, two buffers in turn, so that the
   // softmax warps and the next unit's P.V do not wait for the epilogue
@@ -162,8 +164,8 @@ struct Layout {
   static constexpr int sf = stage + (kMx ? (G::bs ? kRopeSlots * kRopeStageBytes : kStageSlots * kStageBytes) : 0);
   static constexpr int sfb = sf + (G::bs ? 2 * kSfTileBytes : 0);  // block-scaled: [2 tiles] A chunks, then B
   static constexpr int qs = round_up_1024(sfb + (G::bs ? 512 : 0));
-  static constexpr int pb = qs + kQsBytes * kTok;             // [2 tiles][kTok]
-  static constexpr int rq = pb + 2 * kPBytes * kTok;          // float [kTok][16] score factor per head
+  static constexpr int pb = qs + kQsBytes * kTok;             // [p_bufs tiles][kTok]
+  static constexpr int rq = pb + G::p_bufs * kPBytes * kTok;  // float [kTok][16] score factor per head
   static constexpr int red = rq + 16 * 4 * kTok;              // float [2][4 warps][16 kTok]
   static constexpr int gred = red + 2 * 4 * 16 * 4 * kTok;    // int [kTok][2][4] tile max of the row exponents
   static constexpr int grow = gred + 2 * 4 * 4 * kTok;        // int8 [2][128] row exponent G - 127 (MXFP4)
@@ -218,7 +220,7 @@ struct Ctx {
   uint64_t* bar;
   volatile int* abort_flag;
   uint32_t tmem;
-  int early_row;  // one token, contiguous cache: the first tile's row, its copy (e4m3: the tile; converted
+  int early_row;  // contiguous cache, where the plan says: the first tile's row, its copy (e4m3: the tile; converted
                   // MXFP4: its two staging halves) issued before the unit scan (-1: none)
 };
 
@@ -1247,7 +1249,7 @@ __device__ void pv_issuer(const Stage1Params& p, const Ctx& x) {
       if (aborted(x)) break;
       tc::fence_after();
       constexpr uint64_t kTplPT = kTok == 1 ? kTplP : kTplP2;
-      const uint32_t bp = lo_word(kTplPT) + ((pb0 + (uint32_t)(it & 1) * kTok * kPBytes) >> 4);
+      const uint32_t bp = lo_word(kTplPT) + ((pb0 + (uint32_t)(it % Geo<kMx, kTok, kPath>::p_bufs) * kTok * kPBytes) >> 4);
       const int s0 = (4 * it) % kPairSlots;
       if (tc::elect()) {
 #pragma unroll
@@ -1289,9 +1291,20 @@ __device__ __forceinline__ void write_unit(const Stage1Params& p, uint32_t tl_o,
                                            int ob, int u, const float (&l)[16], const float (&m)[16],
                                            float out_scale) {
   constexpr float kLo = kRow ? 0.0625f : 1.f;
+  // every thread holds all 16 heads' values: a lane inverts one (16 reciprocals a thread,
+  // one after the other, took 1.0 us)
+  const int mine = row & 15;
+  float lh = l[0], mh = m[0];
+#pragma unroll
+  for (int h = 1; h < 16; ++h) {
+    lh = mine == h ? l[h] : lh;
+    mh = mine == h ? m[h] : mh;
+  }
+  const bool any = kRow ? lh != 0.f : lh > 0.f;
+  const float ih = any ? out_scale * __frcp_rn(lh) : 0.f;
   float inv[16];
 #pragma unroll
-  for (int h = 0; h < 16; ++h) inv[h] = (kRow ? l[h] != 0.f : l[h] > 0.f) ? out_scale * __frcp_rn(l[h]) : 0.f;
+  for (int h = 0; h < 16; ++h) inv[h] = __shfl_sync(0xffffffffu, ih, h);
   // kTwo: two blocks of 128 features per TMEM round trip (MXFP4: 0.1-0.5 us
   // off a bs32/kv8192 split stage in two A/B runs; the e4m3 kernel, which
   // needs four more registers for it, ran bs4/kv8192 1.4 us slower and keeps
@@ -1321,16 +1334,9 @@ __device__ __forceinline__ void write_unit(const Stage1Params& p, uint32_t tl_o,
       }
     }
   }
-  // lse of head h is written by row h (every row holds all 16 values): pick
-  // this row's head with selects, no divergent branches
+  // lse of head h is written by row h
   if (row < kHeads) {
-    float lh = l[0], mh = m[0];
-#pragma unroll
-    for (int h = 1; h < 16; ++h) {
-      lh = row == h ? l[h] : lh;
-      mh = row == h ? m[h] : mh;
-    }
-    const float lse = (kRow ? lh != 0.f : lh > 0.f) ? (mh + fast_log2(lh)) * kLn2 : -INFINITY;
+    const float lse = any ? (mh + fast_log2(lh)) * kLn2 : -INFINITY;
     if (final_out) {
       if (p.lse) p.lse[ob * kHeads + row] = lse;
     } else {
@@ -1482,6 +1488,7 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
   const float* rq = reinterpret_cast<const float*>(x.smem + L::rq) + 16 * ti;
   float* redbuf = reinterpret_cast<float*>(x.smem + L::red) + 128 * ti;
   constexpr bool kEpi = Geo<kMx, kTok, kPath>::epi;
+  constexpr int kPBufs = Geo<kMx, kTok, kPath>::p_bufs;
   int it = 0, red_par = 0, ordinal = 0;
   for (int k = 0; k < x.nunits; ++k) {
     const UnitDesc d = x.units[k];
@@ -1580,7 +1587,8 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
       }
       // P buffer it mod 2 was read by P.V(it-2); waiting for it here also makes
       // the o_done wait below exact (the barrier is then one phase behind at most)
-      if (it >= 2) wait_phase(&x.bar[kPFree + sb], ((it >> 1) - 1) & 1, x.abort_flag, p.ws_err);
+      // (one P buffer: below, for P.V(it-1))
+      if (kPBufs == 2 && it >= 2) wait_phase(&x.bar[kPFree + sb], ((it >> 1) - 1) & 1, x.abort_flag, p.ws_err);
       if (need) {
         // tile max of the rising heads: redux over the warp (order-preserving
         // integer image of the float), then over the 4 warps through smem
@@ -1599,16 +1607,29 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
           if (lane == 0) gred[red_par * 4 + ww] = w;
         }
         named_bar_sync(bar, 128);
+        // (selects, so that the heads' chains overlap: with a branch a head this took 1.0 us)
+        int top[16];
+#pragma unroll
+        for (int h = 0; h < 16; h += 4) {
+          int4 a = *reinterpret_cast<const int4*>(mx + h);
+#pragma unroll
+          for (int w = 1; w < 4; ++w) {
+            const int4 b = *reinterpret_cast<const int4*>(mx + 16 * w + h);
+            a = make_int4(max(a.x, b.x), max(a.y, b.y), max(a.z, b.z), max(a.w, b.w));
+          }
+          top[h] = a.x;
+          top[h + 1] = a.y;
+          top[h + 2] = a.z;
+          top[h + 3] = a.w;
+        }
         float fac[16];
 #pragma unroll
         for (int h = 0; h < 16; ++h) {
-          fac[h] = 1.f;
-          if ((need >> h) & 1u) {
-            const float mn = float_from_order_key(max(max(mx[h], mx[16 + h]), max(mx[32 + h], mx[48 + h]))) - kLower;
-            fac[h] = (m_ref[h] == -INFINITY) ? 0.f : fast_exp2(m_ref[h] - mn);
-            m_ref[h] = mn;
-            l_part[h] *= fac[h];
-          }
+          const bool rises = (need >> h) & 1u;
+          const float mn = float_from_order_key(top[h]) - kLower, f = fast_exp2(m_ref[h] - mn);
+          fac[h] = !rises ? 1.f : (m_ref[h] == -INFINITY ? 0.f : f);
+          m_ref[h] = rises ? mn : m_ref[h];
+          l_part[h] *= fac[h];
         }
         if (kG && ((need >> 16) & 1u)) {
           // raise the P.V reference: O^T so far is scaled down by 2^(gv_old - gv_new)
@@ -1659,7 +1680,8 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
         else
           two_term_e4m3(pv[0], pv[1], pv[2], pv[3], hi[g], lo[g]);
       }
-      uint8_t* pbuf = x.smem + L::pb + (sb * kTok + ti) * kPBytes + row * 32;
+      if (kPBufs == 1 && it >= 1) wait_phase(&x.bar[kPFree + (sb ^ 1)], ((it - 1) >> 1) & 1, x.abort_flag, p.ws_err);
+      uint8_t* pbuf = x.smem + L::pb + (it % kPBufs * kTok + ti) * kPBytes + row * 32;
       const int xr = (row >> 2) & 1;  // 32 B swizzle: the 16-byte units of the row swap
       *reinterpret_cast<uint4*>(pbuf + 16 * xr) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       *reinterpret_cast<uint4*>(pbuf + 16 * (xr ^ 1)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -1770,7 +1792,7 @@ __global__ void __launch_bounds__(Geo<kMx, kTok, kPath>::threads, 1)
     *x.abort_flag = 0;
     fence_mbar_init();
     misc[3] = -1;
-    if constexpr (!kMx && kTok == 1 && !kSmallPages) {
+    if constexpr (!kMx && (kTok == 1 || row_scales(kPath)) && !kSmallPages) {
       // the first tile's copy starts now, before the unit scan: the plan names
       // its row (the producer checks it against the scan), into pair slots
       // 0..3 and rope slot 0, where the producer would put tile 0
@@ -1811,14 +1833,14 @@ __global__ void __launch_bounds__(Geo<kMx, kTok, kPath>::threads, 1)
       }
     }
   }
-  if (warp == 0) {
+  if (warp == 3) {
+    if (lane == 0 && !kMx) prefetch_tensormap(&p.tmap_kv64);
     // no grid-dependency wait here: this kernel is launched only once the
     // query-preparation grid has itself waited for all earlier work, so every
     // input but the prepared queries is complete (the query loader waits for those)
     scan_units<kTileRows, Geo<kMx, kTok, kPath>::max_units, kTok>(p, reinterpret_cast<UnitDesc*>(smem + L::units), s_nunits,
                                                      lane);
     if (lane == 0) trace_stamp(p, kTrScanDone);
-    if (lane == 0 && !kMx) prefetch_tensormap(&p.tmap_kv64);
   }
   if (kMx && threadIdx.x >= 128 && threadIdx.x < 384) {
     // e4m3 bytes of the e2m1 magnitudes {0, .5, 1, 1.5, 2, 3, 4, 6} times
