@@ -189,16 +189,34 @@ __device__ __forceinline__ int tiles_of(const PromptParams& p, const Work& w, in
 // over the batch is needed.  The document of a slot by a search of 32 probes a
 // step.  False: an empty slot.
 __device__ __forceinline__ bool find_work(const PromptParams& p, int slot, int lane, Work& w) {
-  auto base = [&](int b) { return (__ldg(p.qo_indptr + b) >> 8) + b; };
-  int lo = 0, hi = p.batch;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32, i = lo + (lane + 1) * step;
-    const int n = __popc(__ballot_sync(0xffffffffu, i < hi && base(i) <= slot));
-    lo += n * step;
-    hi = min(hi, lo + step);
+  int lo = 0, q, qe, k, ke, prefix;
+  auto load = [&](int b) {
+    q = __ldg(p.qo_indptr + b);
+    qe = __ldg(p.qo_indptr + b + 1);
+    k = __ldg(p.kv_indptr + b);
+    ke = __ldg(p.kv_indptr + b + 1);
+    prefix = p.prefix ? __ldg(p.prefix + b) : 0;
+  };
+  if (p.batch <= 32) {
+    // a document a lane: one round of loads
+    load(min(lane, p.batch - 1));
+    lo = max(0, __popc(__ballot_sync(0xffffffffu, lane < p.batch && (q >> 8) + lane <= slot)) - 1);
+    q = __shfl_sync(0xffffffffu, q, lo);
+    qe = __shfl_sync(0xffffffffu, qe, lo);
+    k = __shfl_sync(0xffffffffu, k, lo);
+    ke = __shfl_sync(0xffffffffu, ke, lo);
+    prefix = __shfl_sync(0xffffffffu, prefix, lo);
+  } else {
+    auto base = [&](int b) { return (__ldg(p.qo_indptr + b) >> 8) + b; };
+    int hi = p.batch;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, i = lo + (lane + 1) * step;
+      const int n = __popc(__ballot_sync(0xffffffffu, i < hi && base(i) <= slot));
+      lo += n * step;
+      hi = min(hi, lo + step);
+    }
+    load(lo);
   }
-  const int q = __ldg(p.qo_indptr + lo), qe = __ldg(p.qo_indptr + lo + 1);
-  const int k = __ldg(p.kv_indptr + lo), ke = __ldg(p.kv_indptr + lo + 1);
   if (q < 0 || qe < q || qe > p.num_q || k < 0 || ke < k || ke > p.num_kv) return false;  // (reported by another warp)
   const int t = slot - ((q >> 8) + lo);
   w.nq = qe - q;
@@ -208,7 +226,7 @@ __device__ __forceinline__ bool find_work(const PromptParams& p, int slot, int l
   w.q0 = q + w.first;
   w.k0 = k;
   w.rows = min(kPromptQ, w.nq - w.first);
-  w.prefix = p.prefix ? __ldg(p.prefix + lo) : 0;
+  w.prefix = prefix;
   w.skip = 0;
   return true;
 }
@@ -260,53 +278,80 @@ __device__ __noinline__ uint64_t Ctx::look(uint64_t since) const {
 }
 
 // ------------------------------------------------------------------ copies
-__device__ void copies(const PromptParams& p, const Ctx& x, const Work& w, int head, int n0, int n1) {
-  const uint64_t keep = policy_evict_last(), once = policy_evict_first();
-  auto queries = [&](int g) {
+// One lane.  begin() asks for all that needs no wait (it precedes the CTA's first
+// barrier), rest() for what is left.
+struct Copies {
+  const PromptParams& p;
+  const Ctx& x;
+  const Work& w;
+  int head, n0, n1;
+  int ks = 0, vs = 0;  // tiles asked for
+
+  __device__ void queries(int g) const {
     if ((g ? n1 : n0) == 0) return;
+    const uint64_t once = policy_evict_first();
     mbar_arrive_expect_tx(&x.bar[kQ + g], kQChunks * kSlotBytes);
     uint8_t* dst = x.smem + Smem::q + g * kQChunks * kSlotBytes;
     tma_load_3d(dst, &p.q_nope, 0, head, w.q0 + 128 * g, &x.bar[kQ + g], once);
     tma_load_3d(dst + kSlotBytes, &p.q_nope, 64, head, w.q0 + 128 * g, &x.bar[kQ + g], once);
     tma_load_3d(dst + 2 * kSlotBytes, &p.q_pe, 0, head, w.q0 + 128 * g, &x.bar[kQ + g], once);
-  };
-  queries(0);
-  const int n = max(n0, n1);
-  int ks = 0, vs = 0;  // tiles asked for
-  // what K tile j and V tile j go over: a slot of K and both of V of tile j - 2, two
-  // slots of K of tile j - 1
-  auto read = [&](int bar, int j) {
-    return (j >= n0 || x.wait(bar + (j & 1), j >> 1)) && (j >= n1 || x.wait(bar + 2 + (j & 1), j >> 1));
-  };
-  for (int j = 0; j < n; ++j) {
+  }
+  __device__ uint8_t* slot(int j, int c) const { return x.smem + Smem::ring + (kChunks * j + c) % kRing * kSlotBytes; }
+  __device__ void keys(int j) {
+    const uint64_t keep = policy_evict_last();
     const int row = w.k0 + kPromptTile * j;
-    auto slot = [&](int c) { return x.smem + Smem::ring + (kChunks * j + c) % kRing * kSlotBytes; };
-    if (j >= 2 && !read(kO, j - 2)) break;
     uint64_t* bar = &x.bar[kKFull + (j & 1)];
     mbar_arrive_expect_tx(bar, kQChunks * kSlotBytes);
-    tma_load_3d(slot(0), &p.k_nope, 0, head, row, bar, keep);
-    tma_load_3d(slot(1), &p.k_nope, 64, head, row, bar, keep);
-    tma_load_2d(slot(2), &p.k_pe, 0, row, bar, keep);
+    tma_load_3d(slot(j, 0), &p.k_nope, 0, head, row, bar, keep);
+    tma_load_3d(slot(j, 1), &p.k_nope, 64, head, row, bar, keep);
+    tma_load_2d(slot(j, 2), &p.k_pe, 0, row, bar, keep);
     ++ks;
-    if (j == 0) queries(1);
-    if (j >= 1 && !read(kS, j - 1)) break;
-    bar = &x.bar[kVFull + (j & 1)];
+  }
+  __device__ void values(int j) {
+    const uint64_t keep = policy_evict_last();
+    const int row = w.k0 + kPromptTile * j;
+    uint64_t* bar = &x.bar[kVFull + (j & 1)];
     mbar_arrive_expect_tx(bar, kVChunks * kSlotBytes);
-    tma_load_3d(slot(3), &p.v, 0, head, row, bar, keep);
-    tma_load_3d(slot(4), &p.v, 64, head, row, bar, keep);
+    tma_load_3d(slot(j, 3), &p.v, 0, head, row, bar, keep);
+    tma_load_3d(slot(j, 4), &p.v, 64, head, row, bar, keep);
     ++vs;
   }
-  if (*x.abort) {
-    // a wait gave up somewhere: never leave with copies in flight (bounded)
-    const uint64_t t0 = global_timer_ns();
-    for (int i = 0; i < 6; ++i) {
-      const int armed = i < 4 ? ((i < 2 ? ks : vs) + 1 - (i & 1)) / 2 : ((i - 4 ? n1 : n0) > 0 ? 1 : 0);
-      if (armed == 0) continue;
-      while (!mbar_try_wait(&x.bar[i], (armed - 1) & 1) && global_timer_ns() - t0 < kWaitTimeoutNs) {
+  __device__ void begin() {
+    const int n = max(n0, n1);
+    if (n == 0) return;
+    queries(0);
+    keys(0);
+    queries(1);
+    values(0);
+    if (n > 1) keys(1);
+  }
+  __device__ void rest() {
+    // what K tile j and V tile j go over: a slot of K and both of V of tile j - 2, two
+    // slots of K of tile j - 1
+    auto read = [&](int bar, int j) {
+      return (j >= n0 || x.wait(bar + (j & 1), j >> 1)) && (j >= n1 || x.wait(bar + 2 + (j & 1), j >> 1));
+    };
+    const int n = max(n0, n1);
+    for (int j = 1; j < n; ++j) {
+      if (j >= 2) {
+        if (!read(kO, j - 2)) break;
+        keys(j);
+      }
+      if (!read(kS, j - 1)) break;
+      values(j);
+    }
+    if (*x.abort) {
+      // a wait gave up somewhere: never leave with copies in flight (bounded)
+      const uint64_t t0 = global_timer_ns();
+      for (int i = 0; i < 6; ++i) {
+        const int armed = i < 4 ? ((i < 2 ? ks : vs) + 1 - (i & 1)) / 2 : ((i - 4 ? n1 : n0) > 0 ? 1 : 0);
+        if (armed == 0) continue;
+        while (!mbar_try_wait(&x.bar[i], (armed - 1) & 1) && global_timer_ns() - t0 < kWaitTimeoutNs) {
+        }
       }
     }
   }
-}
+};
 
 // ------------------------------------------------------------------ MMAs
 // One warp, of which an elected lane issues (the descriptors are the same in every
@@ -533,7 +578,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) mla_prompt_kernel(const __grid
   x.bar = reinterpret_cast<uint64_t*>(smem + Smem::bars);
   x.abort = misc + 1;
   x.err = p.ws_err;
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 32 * kCopyWarp) {
     for (int i = 0; i < Smem::nbars; ++i) mbar_init(&x.bar[i], i >= kP && i < kP + 4 ? 8 : 1);
     misc[1] = 0;
     fence_mbar_init();
@@ -556,14 +601,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) mla_prompt_kernel(const __grid
   }
   if (!any) return;  // (every warp finds the same)
   __syncwarp();
-  if (warp == kMmaWarp) {
-    tc::alloc(reinterpret_cast<uint32_t*>(misc), 512);
-    tc::relinquish();
-  }
-  tc::fence_before();
-  __syncthreads();
-  tc::fence_after();
-  x.tmem = *reinterpret_cast<uint32_t*>(misc);
   int n0 = tiles_of(p, w, 0), n1 = tiles_of(p, w, 1);
   if (p.splits > 1) {
     const int n = max(n0, n1), lo = n * split / p.splits, hi = n * (split + 1) / p.splits;
@@ -572,10 +609,22 @@ __global__ void __launch_bounds__(32 * kWarps, 1) mla_prompt_kernel(const __grid
     w.skip = kPromptTile * lo;
     w.k0 += w.skip;
   }
+  Copies copies{p, x, w, head, n0, n1};
+  if (warp == kMmaWarp) {
+    tc::alloc(reinterpret_cast<uint32_t*>(misc), 512);
+    tc::relinquish();
+  } else if (threadIdx.x == 32 * kCopyWarp) {
+    copies.begin();
+  }
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  x.tmem = *reinterpret_cast<uint32_t*>(misc);
   if (warp < kSoftWarps) {
     softmax(p, x, w, head, split, warp >> 3, warp < 8 ? n0 : n1);
   } else if (warp == kCopyWarp) {
-    if (lane == 0) copies(p, x, w, head, n0, n1);
+    if (lane == 0) copies.rest();
   } else {
     x.tmem = __shfl_sync(0xffffffffu, x.tmem, 0);
     mmas(x, __shfl_sync(0xffffffffu, n0, 0), __shfl_sync(0xffffffffu, n1, 0));
