@@ -30,9 +30,9 @@
 // Warp roles: 0 TMA producer (9 column boxes of 64 B x 128 rows per tile: the
 // 8 V blocks in pairs into a ring of 11 pair slots, each released by the
 // commit after its P.V block, the rope block into a ring of 2); 1 QK issuer and
-// TMEM owner; 2 P.V issuer (two issuing threads: one thread cannot issue these
-// small MMAs as fast as the tensor pipe retires them); 3 query loader (the
-// query image prepared by mla_prep_q_kernel, two bulk copies per unit); 4-7
+// TMEM owner; 2 P.V issuer (two warps, each issuing by an elected lane); 3 query loader (the
+// query image prepared by mla_prep_q_kernel, two bulk copies per unit; over pages of
+// 1 to 4 rows warps 0 and 3 copy rows and warp 1 loads the queries); 4-7
 // softmax, O^T rescale and the unit epilogue (warp w reads TMEM lanes
 // [32 (w mod 4), +32)).  Hand-offs are mbarriers (TMA transaction bytes,
 // tcgen05.commit, thread arrivals).
@@ -43,8 +43,8 @@
 // group for token 1, so the cache rows are read once for both tokens.  Token
 // 0 does not see the pair's last row (token 1's own entry).  An odd number of
 // tokens leaves its first one alone: that pair's token 0 repeats token 1's query
-// and writes nothing (five tokens over 32 x 4096 rows with scales 63.0 us in three
-// passes, against 71.4 a token at a time; eight in four passes 78.0 against 112.8).
+// and writes nothing (32 x 4096 rows with scales: eight tokens in four passes 71 us, five
+// in three 56; measured a step earlier, 78 and 63 against 113 and 71 a token at a time).
 //
 // MXFP4 KV (kMx): rows arrive packed (288 B of e2m1 pairs, element 2i in the low
 // nibble of byte i) by 1-D bulk copies of 64-row halves into a staging ring,
@@ -79,8 +79,8 @@ constexpr int kTileRows = 128;
 constexpr int kChunkBytes = kTileRows * 64;  // one 64-byte feature column block of a tile
 constexpr int kPairBytes = 2 * kChunkBytes;  // two column blocks = features [128 f, 128 f + 128)
 // kTok: query tokens one work unit serves (2: the fused two-token e4m3 form,
-// which holds a second query image and a second pair of P buffers in shared
-// memory at the cost of two ring slots).  kPath: which instance -- the
+// which holds a second query image in shared memory at the cost of a ring
+// slot).  kPath: which instance -- the
 // contiguous cache and pages of 64 rows or more (kPathRows), pages of fewer
 // rows (kPathSmallPages), or MXFP4 scores from block-scaled MMAs on the e2m1
 // tile itself (kPathBlockScaled; otherwise MXFP4 is converted to e4m3 from a
@@ -95,7 +95,8 @@ struct Geo {
   static_assert(!row_scales(kPath) || !kMx, "row scales: e4m3");
   static constexpr bool bs = kPath == kPathBlockScaled;
   static constexpr int pair_slots = kMx ? (bs ? 10 : 8) : (kTok == 1 ? 11 : 10);  // ring of column-block pairs (4 per tile)
-  // P^T buffers: two tokens have one, the room of the other is a slot of the ring
+  // P^T buffers: two tokens have one each, the room of the others is a slot of the ring
+  // (32 x 4096 rows 28.0 us; two each and 9 slots 28.8)
   static constexpr int p_bufs = kTok == 1 ? 2 : 1;
   // e4m3, one token per unit: a separate epilogue group (warps 8-11) drains
   // each unit's O^T from its own TMEM buffer, two buffers in turn, so that the
