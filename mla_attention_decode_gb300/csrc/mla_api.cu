@@ -136,20 +136,25 @@ struct BalancedPlan {
 // weight would leave CTAs without tiles).  Measured against weights one
 // higher and one lower: e4m3 bs64/kv8192 split stage 65.5 us against 66.6 (1)
 // and 66.1 (3); MXFP4 bs32/kv8192 51.6 us (1) against 53.6 (2) and 54.5 (3).
+// e4m3 rows with a scale each, whose plans came after a unit's first and last steps had
+// become cheaper, take 1, and 1 late tile (late_tiles_for), for a token a unit: 64 x 8192
+// rows 58.2 us against 59.2 with 2 and 2 (59.0 with 1 and 2, 59.5 with 2 and 1).  In pairs
+// of tokens 2 is better (32 x 4096 rows, four tokens 42.5 against 43.7).
 #ifndef MLA_UNIT_COST
 #define MLA_UNIT_COST 2
 #endif
 #ifndef MLA_UNIT_COST_MXFP4
 #define MLA_UNIT_COST_MXFP4 1
 #endif
-int32_t schedule_unit_cost(int kv_dtype) {
+int32_t schedule_unit_cost(int kv_dtype, bool fused) {
+  if (kv_dtype == MLA_KV_FP8_ROW && !fused) return 1;
   return kv_dtype == MLA_KV_MXFP4 ? MLA_UNIT_COST_MXFP4 : MLA_UNIT_COST;
 }
 
 // The busiest CTA's tiles plus kUnitCost per unit it owns, plus the combine
 // (same model as plan_cost).
 BalancedPlan plan_balanced(const std::vector<int64_t>& lens, int num_sms, int kv_dtype, int64_t prep_rows,
-                           int64_t late_tiles) {
+                           int64_t late_tiles, bool fused) {
   const double kUnitCost = 0.5, kCombineFixed = 2.0;
   const int tile = tile_rows(kv_dtype);
   BalancedPlan bp;
@@ -157,7 +162,7 @@ BalancedPlan plan_balanced(const std::vector<int64_t>& lens, int num_sms, int kv
   if (bp.T == 0) return bp;
   bp.G = bp.T < num_sms ? bp.T : num_sms;
   const int64_t B = static_cast<int64_t>(lens.size());
-  const int32_t U = schedule_unit_cost(kv_dtype);
+  const int32_t U = schedule_unit_cost(kv_dtype, fused);
   bp.unit_cost = bp.T >= (U + 2) * bp.G ? U : 0;
   bp.C = bp.T + bp.unit_cost * (B - 1);
   // the late CTAs' share, when every CTA keeps at least two positions
@@ -349,8 +354,8 @@ uint64_t* g_trace = nullptr;
 
 // The plan of a batch of sequences with lengths `lens` whose rows span
 // [0, total_kv) of the row space the kernels walk (see mla_decode.h).
-// Positions a late CTA gives up (see late_ctas): e4m3 one token per unit,
-// MXFP4 and the two-token e4m3 form; none for bf16 (no query preparation).
+// Positions a late CTA gives up (see late_ctas): e4m3 with one scale, one token
+// per unit; the others; none for bf16 (no query preparation).
 #ifndef MLA_LATE_TILES_E4M3
 #define MLA_LATE_TILES_E4M3 2
 #endif
@@ -359,7 +364,7 @@ uint64_t* g_trace = nullptr;
 #endif
 int64_t late_tiles_for(int32_t kv_dtype, bool fused) {
   if (kv_dtype == MLA_KV_BF16) return 0;
-  return (is_e4m3(kv_dtype) && !fused) ? MLA_LATE_TILES_E4M3 : MLA_LATE_TILES_OTHER;
+  return (kv_dtype == MLA_KV_FP8_E4M3 && !fused) ? MLA_LATE_TILES_E4M3 : MLA_LATE_TILES_OTHER;
 }
 
 // prep_rows: output rows (the query-preparation grid); fused: the two-token e4m3 form
@@ -411,7 +416,7 @@ int plan_lengths(const std::vector<int64_t>& lens, int32_t total_kv, int32_t kv_
     rr_cost = best;
     if (best >= 0.0) plan_cost(lens, chunk, cap, sms, kv_dtype, &work);
     // the contiguous schedule, when it is cheaper (or the only one that fits)
-    const BalancedPlan bp = plan_balanced(lens, sms, kv_dtype, prep_rows, late_tiles_for(kv_dtype, fused));
+    const BalancedPlan bp = plan_balanced(lens, sms, kv_dtype, prep_rows, late_tiles_for(kv_dtype, fused), fused);
     if (bp.cost >= 0.0 && bp.max_units <= mla::max_units_per_cta(kv_dtype) && bp.work <= INT32_MAX &&
         bp.C <= INT32_MAX && (rr_cost < 0.0 || bp.cost < rr_cost - 1e-9)) {
       mla_plan p;

@@ -83,7 +83,7 @@ def test_pairs_of_tokens_plan_as_entries(q_len, splits):
     for n in lens:
         for i in range(pairs):  # the later token is q_len - 1 - 2 (pairs - 1 - i)
             rows.append(rows[-1] + max(0, n - 2 * (pairs - 1 - i)))
-    ref = binding.mla_decode_plan(rows, "fp8_row", num_sms=7, num_splits=splits)
+    ref = binding.mla_decode_plan(rows, "fp8", num_sms=7, num_splits=splits)  # (a unit boundary of the same weight)
     assert plan.schedule == ref.schedule and plan.total_tiles == ref.total_tiles
     assert [c for c in range(256) if plan.first_row[c] >= 0] == [c for c in range(256) if ref.first_row[c] >= 0] or ref.late_tiles
     if plan.late_tiles == ref.late_tiles == 0:
@@ -117,3 +117,18 @@ def test_formats_that_do_not_exist_are_refused(lib):
     plan = binding.mla_decode_plan([0, 300], "fp8_row", num_sms=152)
     plan.mx_scores = 1  # of the 4-bit format only
     assert lib.mla_decode_fwd(FAKE, FAKE, FAKE, 4, FAKE, FAKE, FAKE, None, 1 / 24, ctypes.byref(plan), FAKE, 1 << 30, None) == INVALID
+
+
+@pytest.mark.parametrize("lens", [[8192] * 64, [5000 - 37 * i for i in range(100)], [2000] * 40])
+def test_ranges_of_tiles_weigh_a_unit_boundary_as_one_tile(lens):
+    """One token a sequence: balanced ranges with one empty position between sequences, the
+    late blocks one fewer; every tile is some block's."""
+    ind = [0]
+    for n in lens:
+        ind.append(ind[-1] + n)
+    plan = binding.mla_decode_plan(ind, "fp8_row", num_sms=152)
+    assert (plan.schedule, plan.unit_cost, plan.late_tiles) == (1, 1, 1)
+    assert plan.total_tiles == sum(-(-n // 128) for n in lens) and plan.grid == 152
+    assert plan.num_work >= len(lens) and min(plan.first_row[:152]) >= 0
+    pairs = binding.mla_decode_plan_multi(ind, 2, "fp8_row", num_sms=152)
+    assert pairs.schedule == 0 or (pairs.unit_cost, pairs.late_tiles) == (2, 1)
