@@ -221,7 +221,7 @@ struct Ctx {
   uint64_t* bar;
   volatile int* abort_flag;
   uint32_t tmem;
-  int early_row;  // contiguous cache, where the plan says: the first tile's row, its copy (e4m3: the tile; converted
+  int early_row;  // where the plan says: the first tile's cache row, its copy (e4m3: the tile; converted
                   // MXFP4: its two staging halves) issued before the unit scan (-1: none)
 };
 
@@ -311,7 +311,7 @@ __device__ void producer_e4m3(const Stage1Params& p, const Ctx& x) {
       early_pending = false;
       for (int f = 0; f < 4; ++f) ++armed[f];
       ++armed[kPairSlots];
-      if (!paged64 && nrows.r0 == x.early_row) {
+      if (nrows.r0 == x.early_row) {
         have = walk.next(x, nt0, nend);
         if (have) nrows = tile_rows(p, nt0, nend);
         continue;
@@ -1760,6 +1760,7 @@ __global__ void __launch_bounds__(Geo<kMx, kTok, kPath>::threads, 1)
   constexpr bool kSmallPages = small_pages(kPath);
   using L = Layout<kMx, kTok, kPath>;
   constexpr bool kBs = Geo<kMx, kTok, kPath>::bs;
+  constexpr bool kRow = row_scales(kPath);
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Ctx x;
@@ -1797,19 +1798,28 @@ __global__ void __launch_bounds__(Geo<kMx, kTok, kPath>::threads, 1)
       // the first tile's copy starts now, before the unit scan: the plan names
       // its row (the producer checks it against the scan), into pair slots
       // 0..3 and rope slot 0, where the producer would put tile 0
-      const int r0 = blockIdx.x < MLA_PLAN_FIRST_ROWS ? p.first_row[blockIdx.x] : -1;
-      if (r0 >= 0 && !p.paged) {
+      const int v0 = blockIdx.x < MLA_PLAN_FIRST_ROWS ? p.first_row[blockIdx.x] : -1;
+      if (v0 >= 0 && (kRow || !p.paged)) {
         const uint64_t pol = policy_evict_first();
+        // (pages of 64 rows: both halves, if there is a next page in the table at all;
+        // the softmax masks what is past the unit's end)
+        const TileRows r = kRow ? tile_rows(p, v0, p.total_kv) : TileRows{v0, -1};
+        const bool halves = kRow && p.paged && p.page_shift == 6;
+        const uint32_t bytes = halves && r.r1 < 0 ? kChunkBytes / 2 : kChunkBytes;
+        auto block = [&](uint8_t* dst, int col, uint64_t* bar) {
+          tma_load_2d(dst, halves ? &p.tmap_kv16 : &p.tmap_kv64, col, r.r0, bar, pol);
+          if (halves && r.r1 >= 0) tma_load_2d(dst + 64 * 64, &p.tmap_kv16, col, r.r1, bar, pol);
+        };
         for (int f = 0; f < 4; ++f) {
           uint8_t* dst = smem + L::pairs + f * kPairBytes;
-          mbar_arrive_expect_tx(&x.bar[kPairFull + f], 2 * kChunkBytes);
-          tma_load_2d(dst, &p.tmap_kv64, 128 * f, r0, &x.bar[kPairFull + f], pol);
-          tma_load_2d(dst + kChunkBytes, &p.tmap_kv64, 128 * f + 64, r0, &x.bar[kPairFull + f], pol);
+          mbar_arrive_expect_tx(&x.bar[kPairFull + f], 2 * bytes);
+          block(dst, 128 * f, &x.bar[kPairFull + f]);
+          block(dst + kChunkBytes, 128 * f + 64, &x.bar[kPairFull + f]);
         }
-        mbar_arrive_expect_tx(&x.bar[kRopeFull], kChunkBytes);
-        tma_load_2d(smem + L::rope, &p.tmap_kv64, 512, r0, &x.bar[kRopeFull], pol);
+        mbar_arrive_expect_tx(&x.bar[kRopeFull], bytes);
+        block(smem + L::rope, 512, &x.bar[kRopeFull]);
         trace_stamp(p, kTrFirstLoad);
-        misc[3] = r0;
+        misc[3] = r.r0;
       }
     }
     if constexpr (kMx && !kBs && kTok == 1 && !kSmallPages) {

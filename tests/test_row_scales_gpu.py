@@ -424,6 +424,29 @@ def test_decode_reports_a_bad_page():
     check(out, lse, reference(q, codes, s, [rows]))
 
 
+@pytest.mark.parametrize("page", [64, 128])
+def test_decode_reports_pages_that_are_not_the_plan(page):
+    """Sequences that begin elsewhere in the table than the plan says: the error word says so, or
+    (pages of 128 rows: the same tiles as the plan's) the result is that of the device's table; the
+    next call of the same decoder, with the plan's, is right."""
+    codes, s = random_cache(gen(3), 8 * page)
+    at, last = torch.tensor([0, 3, 7], dtype=torch.int32), torch.tensor([page, 5], dtype=torch.int32)
+    q = torch.randn(2, 16, 576, generator=gen(3)).to(torch.bfloat16)
+    dec = binding.PagedMLADecoder(at, last, page, 8, "fp8_row")
+    table = torch.tensor([6, 1, 4, 0, 3, 7, 2], dtype=torch.int32)
+    qo = torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV)
+    moved = torch.tensor([0, 4, 7], dtype=torch.int32)
+    for device_at in (moved, at):
+        out, lse = dec(q.to(DEV), codes.to(DEV), device_at.to(DEV), table.to(DEV), last.to(DEV), qo, kv_scale=s.to(DEV))
+        error = dec.poll_error()
+        assert error == (binding.MLA_ERR_DEVICE_INDEX if page == 64 and device_at is moved else 0)
+        if error == 0:
+            ends = [int(device_at[1]), 7]
+            spans = [[int(table[i]) * page + r for i in range(a, e) for r in range(n if i == e - 1 else page)]
+                     for a, e, n in zip([0, ends[0]], ends, last.tolist())]
+            check(out, lse, reference(q, codes, s, spans))
+
+
 def test_decode_static_and_stages_agree():
     """The entry point without a workspace, and the two stages apart, give the decode's bits."""
     lens = [700, 0, 64, 2000]

@@ -132,3 +132,25 @@ def test_ranges_of_tiles_weigh_a_unit_boundary_as_one_tile(lens):
     assert plan.num_work >= len(lens) and min(plan.first_row[:152]) >= 0
     pairs = binding.mla_decode_plan_multi(ind, 2, "fp8_row", num_sms=152)
     assert pairs.schedule == 0 or (pairs.unit_cost, pairs.late_tiles) == (2, 1)
+
+
+@pytest.mark.parametrize("page", [8, 64, 128])
+def test_paged_plans_say_where_blocks_begin(page):
+    """From pages of 64 rows on, the first row of each block's first tile, counted over the pages."""
+    lens = [5000 - 37 * i for i in range(100)] + [0, 1]
+    counts, at, ind = [-(-n // page) for n in lens], [0], [0]
+    for n, c in zip(lens, counts):
+        at.append(at[-1] + c)
+        ind.append(ind[-1] + n)
+    last = [n - (c - 1) * page if c else 0 for n, c in zip(lens, counts)]
+    plan = binding.mla_decode_plan_paged(at, last, page, at[-1], "fp8_row", num_sms=152)
+    if page < 64:
+        assert set(plan.first_row) == {-1}
+        return
+    flat = binding.mla_decode_plan(ind, "fp8_row", num_sms=152)
+    for got, want in zip(plan.first_row, flat.first_row):
+        if want < 0:
+            assert got == -1
+            continue
+        b = max(i for i in range(len(lens)) if ind[i] <= want and lens[i])
+        assert got == at[b] * page + want - ind[b]
