@@ -146,7 +146,7 @@ typedef struct {
   /* first_row[c] (c < MLA_PLAN_FIRST_ROWS): the row-space row of the first tile
    * CTA c of the split kernel reads, -1 when it reads none or the plan does not
    * say (paged plans and those of several tokens, of other formats than fp8_row;
-   * fp8_row's of pages of fewer than 64 rows).  The e4m3 split kernel starts that
+   * fp8_row's of pages of fewer than 8 rows).  The e4m3 split kernel starts that
    * tile's copy on entry, before its unit scan; the device kv_indptr must then
    * hold the values the plan was made from (as it must anyway). */
   int32_t first_row[MLA_PLAN_FIRST_ROWS];

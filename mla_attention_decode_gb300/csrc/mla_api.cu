@@ -312,7 +312,7 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 // plan->first_row (mla_decode.h): the first row of the first non-empty unit of
 // each CTA, by the unit rules of the plan's schedule, for unit-list entries of lens[b] rows
 // that begin at row first(b) (contiguous plans of one token; fp8_row's of pairs, and of
-// pages of 64 rows and more; the others say -1).
+// pages of 8 rows and more; the others say -1).
 template <class First>
 void fill_first_rows(mla_plan* plan, const std::vector<int64_t>& lens, First first) {
   for (int c = 0; c < MLA_PLAN_FIRST_ROWS; ++c) plan->first_row[c] = -1;
@@ -563,7 +563,7 @@ int mla_decode_plan_paged(const int32_t* kv_page_indptr_host, const int32_t* kv_
   if (rc != MLA_OK) return rc;
   p.page_size = page_size;
   p.num_pages = num_pages;
-  if (kv_dtype == MLA_KV_FP8_ROW && page_size >= 64)
+  if (kv_dtype == MLA_KV_FP8_ROW && page_size >= 8)
     fill_first_rows(&p, lens, [&](int64_t b) { return (int64_t)kv_page_indptr_host[b] * page_size; });
   *plan = p;
   return MLA_OK;
@@ -663,9 +663,9 @@ int prepare(const void* q, const void* kv, const void* kv_scale, int32_t scale_s
   if (plan->mx_scores != 0 && (plan->mx_scores != 1 || plan->kv_dtype != MLA_KV_MXFP4)) return MLA_ERR_INVALID_ARG;
   p->mx_bs = (plan->mx_scores == 1 && !(paged && page_shift < 6)) ? 1 : 0;
   // the first tile rows of a contiguous plan of one token, and of fp8_row's of pairs or of
-  // pages of 64 rows and more (the e4m3 split kernel starts those copies before its unit scan)
+  // pages of 8 rows and more (the e4m3 split kernel starts those copies before its unit scan)
   const bool row = plan->kv_dtype == MLA_KV_FP8_ROW;
-  const bool first_rows = paged ? row && page_shift >= 6 : (p->tok == 2 ? row : p->q_len == 1);
+  const bool first_rows = paged ? row && page_shift >= 3 : (p->tok == 2 ? row : p->q_len == 1);
   for (int c = 0; c < MLA_PLAN_FIRST_ROWS; ++c) {
     const int32_t r = first_rows ? plan->first_row[c] : -1;
     if (r < -1 || r >= plan->total_kv) return MLA_ERR_INVALID_ARG;  // a row of the cache, or none

@@ -377,10 +377,11 @@ __device__ void producer_e4m3_boxes(const Stage1Params& p, const Ctx& x, int lan
   constexpr int kPairSlots = Geo<false, kTok>::pair_slots;
   const uint64_t pol = policy_evict_first();  // KV rows are read once
   int armed[kPairSlots + kRopeSlots];         // lane 0: fills issued per slot
-  for (int i = 0; i < kPairSlots + kRopeSlots; ++i) armed[i] = 0;
+  for (int i = 0; i < kPairSlots + kRopeSlots; ++i) armed[i] = x.early_row >= 0 && (i < 4 || i == kPairSlots);
   const int page_mask = (1 << p.page_shift) - 1;
   TileWalk walk;
   int t0 = 0, end = 0;
+  bool early = x.early_row >= 0;  // the tile that the kernel's prologue copied (first_boxes)
   for (int it = 0; walk.next(x, t0, end); ++it) {
     // the first cache row of page `lane` of the tile (tiles start on page boundaries)
     const int v = min(t0 + (lane << p.page_shift), end - 1), cr = cache_row(p, v) - (v & page_mask);
@@ -388,6 +389,12 @@ __device__ void producer_e4m3_boxes(const Stage1Params& p, const Ctx& x, int lan
 #pragma unroll
     for (int f = 0; f < 4; ++f) sl[f] = pair_slot<false, kTok>(it, f);
     const int rs = it % kRopeSlots;
+    if (early) {
+      // slots 0..3 and rope slot 0, if the unit list begins where the plan says
+      if (__shfl_sync(0xffffffffu, cr, 0) != x.early_row) break;
+      early = false;
+      continue;
+    }
     if (lane == 0) {
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
@@ -418,6 +425,10 @@ __device__ void producer_e4m3_boxes(const Stage1Params& p, const Ctx& x, int lan
     }
     if (it == 0 && lane == 0) trace_stamp(p, kTrFirstLoad);
   }
+  if (early && lane == 0) {  // it does not: flagged, and the CTA stops
+    flag_error(p.ws_err, kErrDeviceIndex, kTagFirstTile, x.early_row);
+    *x.abort_flag = 1;
+  }
   if (lane == 0 && *x.abort_flag) {
     // a wait gave up somewhere: never leave with copies in flight (bounded wait per slot)
     for (int i = 0; i < kPairSlots + kRopeSlots; ++i) {
@@ -428,6 +439,29 @@ __device__ void producer_e4m3_boxes(const Stage1Params& p, const Ctx& x, int lan
       }
     }
   }
+}
+
+// The first tile of a CTA that the plan says begins at row-space row v0, before the unit
+// list is there (one warp; its lane 0 has made the barriers): returns the tile's first
+// cache row.  Pages past the sequence's end are the table's next ones, if any.  33 x 2500
+// rows in pages of 16: 23.0 us instead of 24.3.
+template <class L>
+__device__ __forceinline__ int first_boxes(const Stage1Params& p, uint8_t* smem, uint64_t* bar, int v0, int lane) {
+  const uint64_t pol = policy_evict_first();
+  const int r_tile = lane << p.page_shift;
+  const int v = min(v0 + r_tile, p.total_kv - 1), cr = cache_row(p, v) - (v & ((1 << p.page_shift) - 1));
+  if (lane == 0) {
+    for (int f = 0; f < 4; ++f) mbar_arrive_expect_tx(&bar[kPairFull + f], 2 * kChunkBytes);
+    mbar_arrive_expect_tx(&bar[kRopeFull], kChunkBytes);
+    trace_stamp(p, kTrFirstLoad);
+  }
+  __syncwarp();
+  if (r_tile < kTileRows) {
+    for (int f = 0; f < 4; ++f)
+      tma_load_2d(smem + L::pairs + f * kPairBytes + r_tile * 128, &p.tmap_kv16, 128 * f, cr, &bar[kPairFull + f], pol);
+    tma_load_2d(smem + L::rope + r_tile * 64, &p.tmap_kv64, 512, cr, &bar[kRopeFull], pol);
+  }
+  return __shfl_sync(0xffffffffu, cr, 0);
 }
 
 // Pages of 1 to 4 rows by plain asynchronous copies: two warps share a tile's column
@@ -1842,6 +1876,14 @@ __global__ void __launch_bounds__(Geo<kMx, kTok, kPath>::threads, 1)
         trace_stamp(p, kTrFirstLoad);
         misc[3] = r0;
       }
+    }
+  }
+  if constexpr (kRow && kSmallPages) {
+    const int v0 = blockIdx.x < MLA_PLAN_FIRST_ROWS ? p.first_row[blockIdx.x] : -1;
+    if (warp == 0 && v0 >= 0) {
+      __syncwarp();
+      const int first = first_boxes<L>(p, smem, x.bar, v0, lane);
+      if (lane == 0) misc[3] = first;
     }
   }
   if (warp == 3) {

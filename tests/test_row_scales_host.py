@@ -134,9 +134,9 @@ def test_ranges_of_tiles_weigh_a_unit_boundary_as_one_tile(lens):
     assert pairs.schedule == 0 or (pairs.unit_cost, pairs.late_tiles) == (2, 1)
 
 
-@pytest.mark.parametrize("page", [8, 64, 128])
+@pytest.mark.parametrize("page", [4, 8, 16, 64, 128])
 def test_paged_plans_say_where_blocks_begin(page):
-    """From pages of 64 rows on, the first row of each block's first tile, counted over the pages."""
+    """From pages of 8 rows on, the first row of each block's first tile, counted over the pages."""
     lens = [5000 - 37 * i for i in range(100)] + [0, 1]
     counts, at, ind = [-(-n // page) for n in lens], [0], [0]
     for n, c in zip(lens, counts):
@@ -144,7 +144,7 @@ def test_paged_plans_say_where_blocks_begin(page):
         ind.append(ind[-1] + n)
     last = [n - (c - 1) * page if c else 0 for n, c in zip(lens, counts)]
     plan = binding.mla_decode_plan_paged(at, last, page, at[-1], "fp8_row", num_sms=152)
-    if page < 64:
+    if page < 8:
         assert set(plan.first_row) == {-1}
         return
     flat = binding.mla_decode_plan(ind, "fp8_row", num_sms=152)
