@@ -291,6 +291,23 @@ def test_decode(lens, splits, q_len):
     check(out, lse, reference(q0, codes, s, spans, q_len))
 
 
+@pytest.mark.parametrize("q_len", [1, 2, 5])
+@pytest.mark.parametrize("sms", [0, 3])
+def test_decode_rows_that_begin_further_on(q_len, sms):
+    """The first sequence begins at a row of its own, with rows of nobody before it; few blocks
+    (many units each) and all of them."""
+    g, base, lens = gen(31), 777, [1500, 0, 129, 1, 4000, 640]
+    ind = indptr_of(lens) + base
+    codes, s = random_cache(g, base + sum(lens))
+    codes[:base], s[:base] = 127, float("nan")
+    q = torch.randn(len(lens) * q_len, 16, 576, generator=g).to(torch.bfloat16)
+    qo = (torch.arange(len(lens) + 1) * q_len).to(torch.int32)
+    dec = binding.MLADecoder(ind, "fp8_row", q_len=q_len, num_sms=sms)
+    out, lse = dec(q.to(DEV), codes.to(DEV), ind.to(DEV), qo.to(DEV), kv_scale=s.to(DEV))
+    assert dec.poll_error() == 0
+    check(out, lse, reference(q, codes, s, [list(range(int(a), int(e))) for a, e in zip(ind[:-1], ind[1:])], q_len))
+
+
 @pytest.mark.parametrize("page", [1, 2, 4, 8, 16, 32, 64, 128, 256])
 @pytest.mark.parametrize("lens", [[130, 0, 64, 5, 1000, 257, 128, 1], [3000, 1, 2047]])
 def test_decode_pages(page, lens):
@@ -445,6 +462,39 @@ def test_decode_reports_pages_that_are_not_the_plan(page):
             spans = [[int(table[i]) * page + r for i in range(a, e) for r in range(n if i == e - 1 else page)]
                      for a, e, n in zip([0, ends[0]], ends, last.tolist())]
             check(out, lse, reference(q, codes, s, spans))
+
+
+@pytest.mark.parametrize("page", [2, 16, 64])
+def test_replayed_decode_follows_the_table(page):
+    """A captured call, replayed after the page table, the rows and their scales have changed in
+    place just before it on the same stream."""
+    g, lens = gen(page), [700, 64, 1000]
+    counts = [-(-n // page) for n in lens]
+    at, pages = indptr_of(counts), sum(counts)
+    last = torch.tensor([n - (c - 1) * page for n, c in zip(lens, counts)], dtype=torch.int32)
+    q = torch.randn(3, 16, 576, generator=g).to(torch.bfloat16)
+    qo = torch.arange(4, dtype=torch.int32, device=DEV)
+    dec = binding.PagedMLADecoder(at, last, page, pages, "fp8_row")
+    codes, s = random_cache(g, pages * page)
+    kv, sc, table = codes.to(DEV), s.to(DEV), torch.zeros(pages, dtype=torch.int32, device=DEV)
+    args = (q.to(DEV), kv, at.to(DEV), table, last.to(DEV), qo)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        dec(*args, kv_scale=sc)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = dec(*args, kv_scale=sc)
+    for turn in range(3):
+        perm = torch.randperm(pages, generator=g).to(torch.int32)
+        codes, s = random_cache(g, pages * page)
+        new = perm.to(DEV), codes.to(DEV), s.to(DEV)
+        table.copy_(new[0]), kv.copy_(new[1]), sc.copy_(new[2])
+        graph.replay()
+        assert dec.poll_error() == 0
+        spans = [[int(perm[int(at[b]) + r // page]) * page + r % page for r in range(n)] for b, n in enumerate(lens)]
+        check(out, lse, reference(q, codes, s, spans))
 
 
 def test_decode_static_and_stages_agree():
