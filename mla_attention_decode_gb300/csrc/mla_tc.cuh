@@ -59,14 +59,19 @@
 // reference, with O^T rescaled); the output is O^T 2^Gv / l.
 //
 // e4m3 KV with a scale per row: row t is code_t s_t, so the scores are
-// (q . code_t) s_t and the output sum_t P_t s_t code_t / l.  s_t joins the row's
-// score factor in fp32, and P as s_t 2^-Gv with Gv the running maximum of the
-// scales' exponents (as MXFP4's, each softmax thread fetching its row's scale
-// two tiles ahead).  P's reference is lowered by 4 (P <= 16 after a raise,
-// <= 2^8.75 before the next one) and its second term is carried 2^4 up in its own
-// columns of O^T: what e4m3's smallest step leaves out of a weight is 2^-18 of the
-// largest instead of 2^-10.
+// (q . code_t) s_t and the output sum_t w_t s_t code_t / l.  s_t joins the row's
+// score factor in fp32 (each softmax thread fetches its row's scale two tiles ahead), and
+// what P.V takes are the products P = 2^(s - m) s_t c, with a power of two c per head that
+// follows the head's largest product: a scale counts by what its row weighs.  (Under the
+// largest scale of all rows, for every head alike, heads whose weight lay on rows with
+// scales 2^12 times smaller lost 40% of their output, with 2^16 all of it.)  The sum l of
+// the weights themselves needs no reference that close: m, a whole number, rises past
+// 2^24.  P's largest lies in [16, 32) after c has been set, is <= 2^8.75 before it is set
+// again, and P's second term is carried 2^4 up in its own columns of O^T: what e4m3's smallest
+// step leaves out of a product is 2^-18 of the largest instead of 2^-10.
 #pragma once
+#include <cfloat>
+
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -171,9 +176,10 @@ struct Layout {
   static constexpr int gred = red + 2 * 4 * 16 * 4 * kTok;    // int [kTok][2][4] tile max of the row exponents
   static constexpr int grow = gred + 2 * 4 * 4 * kTok;        // int8 [2][128] row exponent G - 127 (MXFP4)
   static constexpr int lut = grow + (kMx ? 2 * 128 : 0);      // u8 [32][8] e2m1 magnitude -> e4m3 per shift
-  static constexpr int hand = lut + (kMx ? 256 : 0);          // float [2][32] l, m handed to the epilogue group
-  static constexpr int handg = hand + (G::epi ? 256 : 0);     // int [2] Gv handed over (row scales)
-  static constexpr int rows = handg + (G::epi && row_scales(kPath) ? 8 : 0);  // int [2][128] a tile's cache rows (small pages)
+  // float [2][hand_floats] l, m (row scales: and c) handed to the epilogue group
+  static constexpr int hand_floats = row_scales(kPath) ? 48 : 32;
+  static constexpr int hand = lut + (kMx ? 256 : 0);
+  static constexpr int rows = hand + (G::epi ? 2 * 4 * hand_floats : 0);  // int [2][128] a tile's cache rows (small pages)
   static constexpr int units = rows + (!kMx && small_pages(kPath) ? 1024 : 0);
   static constexpr int bars = units + G::max_units * (int)sizeof(UnitDesc);
   // the epilogue group's four (e4m3, one token), then the two of block-scaled MXFP4
@@ -1311,6 +1317,16 @@ __device__ void pv_issuer(const Stage1Params& p, const Ctx& x) {
 
 // 2^e for an integer e in [-126, 127] (exact).
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
+// floor(log2 x) of a normal x > 0 (128: infinite or NaN; -127: 0 or subnormal).
+__device__ __forceinline__ int exponent_of(float x) { return (__float_as_int(x) >> 23) - 127; }
+
+// Row scales: products are formed as 2^(s - m) (s_t 2^-kScaleUp) c.  With scales of
+// [2^-64, 2^120] and 2^(s - m) <= 2^24 the first product is at most 2^117, and at least
+// 2^-92 in the row that m is from, so that what fp32 loses at its lower end is 2^-34 of it.
+constexpr int kScaleUp = 27;
+constexpr int kRiseSum = 24;       // m rises when a score exceeds it by that
+constexpr int kTopP = 4;           // P's largest after c has been set: [2^kTopP, 2^(kTopP + 1))
+constexpr int kNoC = 126;          // c's exponent before it has been set (any product is above it then)
 
 // ------------------------------------------------------------------ unit output
 // A unit's output from O^T in TMEM: this thread's lane is feature row `row` of
@@ -1318,25 +1334,27 @@ __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 12
 // the query's two terms).  An unsplit sequence gets bf16 out and lse; a split
 // one an fp32 partial and lse in partial slot u.  l, m: the unit's softmax sum
 // and reference per head (log2 units); out_scale: the factor O^T carries.
-// kRow (row scales): the weights' second term is 2^4 up, and a sum that is NaN gives a
-// NaN lse, so that a sequence split over several units keeps it (else an lse of -inf,
-// which the combine takes for an empty unit).
+// kRow (row scales): the factor is 1 / c[h] and 2^kScaleUp, the weights' second term is 2^4 up, and
+// a sum that is NaN gives a NaN lse, so that a sequence split over several units keeps it
+// (else an lse of -inf, which the combine takes for an empty unit).
 template <bool kTwo, bool kRow>
 __device__ __forceinline__ void write_unit(const Stage1Params& p, uint32_t tl_o, uint32_t blk, int row, bool final_out,
                                            int ob, int u, const float (&l)[16], const float (&m)[16],
-                                           float out_scale) {
+                                           const float (&c)[16], float out_scale) {
   constexpr float kLo = kRow ? 0.0625f : 1.f;
   // every thread holds all 16 heads' values: a lane inverts one (16 reciprocals a thread,
   // one after the other, took 1.0 us)
   const int mine = row & 15;
-  float lh = l[0], mh = m[0];
+  float lh = l[0], mh = m[0], ch = c[0];
 #pragma unroll
   for (int h = 1; h < 16; ++h) {
     lh = mine == h ? l[h] : lh;
     mh = mine == h ? m[h] : mh;
+    if (kRow) ch = mine == h ? c[h] : ch;
   }
   const bool any = kRow ? lh != 0.f : lh > 0.f;
-  const float ih = any ? out_scale * __frcp_rn(lh) : 0.f;
+  // (row scales: the exponents of 1 / c and 1 / l first, their product is in range)
+  const float ih = !any ? 0.f : (kRow ? exp2_int(-exponent_of(ch)) * __frcp_rn(lh) * exp2_int(kScaleUp) : out_scale * __frcp_rn(lh));
   float inv[16];
 #pragma unroll
   for (int h = 0; h < 16; ++h) inv[h] = __shfl_sync(0xffffffffu, ih, h);
@@ -1397,7 +1415,6 @@ __device__ void epilogue_group(const Stage1Params& p, const Ctx& x, int ww, int 
   const uint32_t tl = x.tmem + ((uint32_t)(32 * ww) << 16);
   const float kv_scale = kRow ? 1.f : *static_cast<const float*>(p.kv_scale);
   const float* hand = reinterpret_cast<const float*>(x.smem + L::hand);
-  const int* handg = reinterpret_cast<const int*>(x.smem + L::handg);
   const bool defer = x.nunits == 2 && tiles_of(x.units[0]) > 0 && tiles_of(x.units[1]) >= 4;
   int ordinal = 0;
   for (int k = 0; k < x.nunits + (defer ? 1 : 0); ++k) {
@@ -1416,18 +1433,18 @@ __device__ void epilogue_group(const Stage1Params& p, const Ctx& x, int ww, int 
     if (tiles_of(d) == 0) continue;
     const int obuf = ordinal & 1, use = ordinal >> 1;
     if (!late0) wait_phase(&x.bar[kEpiReady + obuf], use & 1, x.abort_flag, p.ws_err);
-    float l[16], m[16];
+    float l[16], m[16], c[16];
 #pragma unroll
     for (int h = 0; h < 16; ++h) {
-      l[h] = hand[32 * obuf + h];
-      m[h] = hand[32 * obuf + 16 + h];
+      l[h] = hand[L::hand_floats * obuf + h];
+      m[h] = hand[L::hand_floats * obuf + 16 + h];
+      c[h] = kRow ? hand[L::hand_floats * obuf + 32 + h] : 1.f;
     }
-    const float out_scale = kRow ? exp2_int(handg[obuf]) : kv_scale;
     if (!late0) wait_phase(&x.bar[olast_bar(obuf)], use & 1, x.abort_flag, p.ws_err);
     if (row == 0 && k < 8 && !late0) trace_stamp(p, kTrUnitLastPV + k);
     tc::fence_after();
-    write_unit<false, kRow>(p, tl + TM::o + obuf * TM::obuf, TM::blk, row, (d.u & kFinalFlag) != 0, d.b, d.u & ~kFinalFlag, l, m,
-               out_scale);
+    write_unit<false, kRow>(p, tl + TM::o + obuf * TM::obuf, TM::blk, row, (d.u & kFinalFlag) != 0, d.b, d.u & ~kFinalFlag, l, m, c,
+                            kv_scale);
     if (row == 0 && ku < 8) trace_stamp(p, kTrUnitDone + ku);
     tc::fence_before();
     __syncwarp();
@@ -1472,6 +1489,33 @@ __device__ __forceinline__ void group_reduce16(float (&v)[16], float* red, int w
   }
 }
 
+// Max over the tile's 128 rows for 16 heads: redux over the warp (order-preserving
+// integer image of the float), then over the 4 warps through `mx`.
+__device__ __forceinline__ void tile_max16(const float (&v)[16], int* mx, int ww, int lane, uint32_t bar, float (&top)[16]) {
+  int wmax[16];
+#pragma unroll
+  for (int h = 0; h < 16; ++h) wmax[h] = __reduce_max_sync(0xffffffffu, float_order_key(v[h]));
+  if (lane == 0) {
+#pragma unroll
+    for (int h = 0; h < 16; h += 4)
+      *reinterpret_cast<int4*>(mx + ww * 16 + h) = make_int4(wmax[h], wmax[h + 1], wmax[h + 2], wmax[h + 3]);
+  }
+  named_bar_sync(bar, 128);
+#pragma unroll
+  for (int h = 0; h < 16; h += 4) {
+    int4 a = *reinterpret_cast<const int4*>(mx + h);
+#pragma unroll
+    for (int w = 1; w < 4; ++w) {
+      const int4 b = *reinterpret_cast<const int4*>(mx + 16 * w + h);
+      a = make_int4(max(a.x, b.x), max(a.y, b.y), max(a.z, b.z), max(a.w, b.w));
+    }
+    top[h] = float_from_order_key(a.x);
+    top[h + 1] = float_from_order_key(a.y);
+    top[h + 2] = float_from_order_key(a.z);
+    top[h + 3] = float_from_order_key(a.w);
+  }
+}
+
 // Softmax group ti (four warps; one group per query token of the unit):
 // thread `row` owns tile row `row` (its TMEM lane) for the token's 16 heads,
 // in TMEM columns [32 ti, +32) of the S^T buffers and O^T blocks.  With two
@@ -1485,14 +1529,12 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
   using L = Layout<kMx, kTok, kPath>;
   using TM = Tmem<kTok>;
   constexpr bool kRow = row_scales(kPath);    // a scale per row
-  constexpr bool kG = kMx || kRow;            // P carries the rows' scales relative to 2^Gv
-  constexpr float kLower = kRow ? 4.f : 0.f;  // P's reference lies this far below the maximum (log2),
-  constexpr float kRise = kRow ? 8.75f : kRescaleLog2;  // and rises when a score exceeds it by that (2^8.75 < 448)
+  constexpr float kMostP = 430.f;             // row scales: c is set anew past that (e4m3's largest: 448)
   constexpr int kGvNone = -1000;   // no such reference yet
   const int row = 32 * ww + lane;  // tile row == TMEM lane of this thread
   const uint32_t tl = x.tmem + ((uint32_t)(32 * ww) << 16) + 32 * ti;
   const uint32_t bar = kBarSoftmax + ti;  // the group's named barrier
-  const float kv_scale = kG ? 1.f : *static_cast<const float*>(p.kv_scale);
+  const float kv_scale = kMx || kRow ? 1.f : *static_cast<const float*>(p.kv_scale);
   // row scales: this thread's row of the next tile and of the one after it (0 past
   // a unit's end), fetched two tiles ahead, its page a tile earlier still, so that
   // neither load waits for the other here
@@ -1559,13 +1601,14 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
       }
       continue;
     }
-    float m_ref[16], l_part[16];
+    float m_ref[16], l_part[16], c_ref[16];  // (c: row scales)
 #pragma unroll
     for (int h = 0; h < 16; ++h) {
       m_ref[h] = -INFINITY;
       l_part[h] = 0.f;
+      c_ref[h] = kRow ? exp2_int(kNoC) : 1.f;
     }
-    int gv = kGvNone;  // P.V reference exponent of the unit
+    int gv = kGvNone;  // MXFP4: P.V reference exponent of the unit
     const int obuf = kEpi ? (ordinal & 1) : 0;  // the unit's O^T buffer
     const uint32_t tl_o = tl + TM::o + obuf * TM::obuf;
     for (int t = 0; t < nt; ++t, ++it) {
@@ -1595,22 +1638,41 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
         sc_after = next_scale();
         next_page();
       }
-      // row scales: s in [2^(gsh - 1), 2^gsh), the exponent bounded so that 2^-gsh is finite
-      const int gsh = kBs ? gsh_bs
-                          : (kMx ? max(-126, (int)grow[sb * 128 + row])
-                                 : (kRow ? min(126, max(-100, (__float_as_int(row_sc) >> 23) - 126)) : 0));
+      const int gsh = kBs ? gsh_bs : (kMx ? max(-126, (int)grow[sb * 128 + row]) : 0);
       // the scores of block-scaled MMAs carry no row factor
       const float row_fac = (kMx && !kBs) ? exp2_int(gsh) : (kRow ? row_sc : 1.f);
       float sv[16];
-      uint32_t need = 0;  // heads with a score above m_ref + kRise in this row (bit 16: G above gv)
 #pragma unroll
-      for (int h = 0; h < 16; ++h) {
+      for (int h = 0; h < 16; ++h)
         sv[h] = row < vis ? (__uint_as_float(acc[h]) + __uint_as_float(acc[16 + h])) * (r[h] * row_fac)
                           : -INFINITY;
-        // (row scales: a NaN score raises too, so that it reaches the output)
-        need |= ((kRow ? !(sv[h] <= m_ref[h] + kRise) : sv[h] > m_ref[h] + kRise) ? 1u : 0u) << h;
+      // heads with a score above m_ref + kRescaleLog2 in this row (bit 16: G above gv); row
+      // scales: with a product above kMostP, or that is NaN, so that it reaches the output
+      // (bit 16: a score above m_ref + kRiseSum)
+      uint32_t need = 0;
+      float pr[16], pv[16];  // row scales: 2^(s - m), and that times the row's scale
+      const float up_sc = kRow ? row_sc * exp2_int(-kScaleUp) : 0.f;
+      if constexpr (kRow) {
+        if (t == 0) {
+          tile_max16(sv, reinterpret_cast<int*>(redbuf + red_par * 64), ww, lane, bar, m_ref);
+          red_par ^= 1;
+#pragma unroll
+          for (int h = 0; h < 16; ++h) m_ref[h] = m_ref[h] == -INFINITY ? -FLT_MAX : ceilf(m_ref[h]);
+        }
+        float most = 0.f;
+#pragma unroll
+        for (int h = 0; h < 16; ++h) {
+          pr[h] = fast_exp2(sv[h] - m_ref[h]);
+          most = fmaxf(most, pr[h]);
+          pv[h] = pr[h] * up_sc;
+          need |= (!(pv[h] * c_ref[h] <= kMostP) ? 1u : 0u) << h;
+        }
+        if (most > exp2_int(kRiseSum)) need |= 1u << 16;
+      } else {
+#pragma unroll
+        for (int h = 0; h < 16; ++h) need |= (sv[h] > m_ref[h] + kRescaleLog2 ? 1u : 0u) << h;
+        if (kMx && row < valid && gsh > gv) need |= 1u << 16;
       }
-      if (kG && row < valid && gsh > gv) need |= 1u << 16;
       // heads whose reference rises: OR over the warp, then over the 4 warps
       need = __reduce_or_sync(0xffffffffu, need);
       {
@@ -1625,55 +1687,60 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
       // (one P buffer: below, for P.V(it-1))
       if (kPBufs == 2 && it >= 2) wait_phase(&x.bar[kPFree + sb], ((it >> 1) - 1) & 1, x.abort_flag, p.ws_err);
       if (need) {
-        // tile max of the rising heads: redux over the warp (order-preserving
-        // integer image of the float), then over the 4 warps through smem
-        // (all 16 heads, without per-head branches: on a unit's first tile all rise)
-        int* mx = reinterpret_cast<int*>(redbuf + red_par * 64);
-        int wmax[16];
+        // tile max of the rising heads (all 16, without per-head branches: on a unit's
+        // first tile all rise; selects, so that the heads' chains overlap: with a branch a
+        // head this took 1.0 us)
+        float top[16], fac[16];
+        if constexpr (kRow) {
+          int by[16];  // how far m rises
 #pragma unroll
-        for (int h = 0; h < 16; ++h) wmax[h] = __reduce_max_sync(0xffffffffu, float_order_key(sv[h]));
-        if (lane == 0) {
+          for (int h = 0; h < 16; ++h) by[h] = 0;
+          if ((need >> 16) & 1u) {
+            tile_max16(sv, reinterpret_cast<int*>(redbuf + red_par * 64), ww, lane, bar, top);
+            red_par ^= 1;
 #pragma unroll
-          for (int h = 0; h < 16; h += 4)
-            *reinterpret_cast<int4*>(mx + ww * 16 + h) = make_int4(wmax[h], wmax[h + 1], wmax[h + 2], wmax[h + 3]);
-        }
-        if (kG && ((need >> 16) & 1u)) {
-          const int w = __reduce_max_sync(0xffffffffu, row < valid ? gsh : kGvNone);
-          if (lane == 0) gred[red_par * 4 + ww] = w;
-        }
-        named_bar_sync(bar, 128);
-        // (selects, so that the heads' chains overlap: with a branch a head this took 1.0 us)
-        int top[16];
-#pragma unroll
-        for (int h = 0; h < 16; h += 4) {
-          int4 a = *reinterpret_cast<const int4*>(mx + h);
-#pragma unroll
-          for (int w = 1; w < 4; ++w) {
-            const int4 b = *reinterpret_cast<const int4*>(mx + 16 * w + h);
-            a = make_int4(max(a.x, b.x), max(a.y, b.y), max(a.z, b.z), max(a.w, b.w));
+            for (int h = 0; h < 16; ++h) {
+              const float m = fmaxf(m_ref[h], ceilf(top[h]));
+              by[h] = (int)fminf(m - m_ref[h], 1000.f);
+              l_part[h] *= fast_exp2(m_ref[h] - m);
+              m_ref[h] = m;
+              pr[h] = fast_exp2(sv[h] - m);
+              pv[h] = pr[h] * up_sc;
+            }
           }
-          top[h] = a.x;
-          top[h + 1] = a.y;
-          top[h + 2] = a.z;
-          top[h + 3] = a.w;
-        }
-        float fac[16];
+          tile_max16(pv, reinterpret_cast<int*>(redbuf + red_par * 64), ww, lane, bar, top);
 #pragma unroll
-        for (int h = 0; h < 16; ++h) {
-          const bool rises = (need >> h) & 1u;
-          const float mn = float_from_order_key(top[h]) - kLower, f = fast_exp2(m_ref[h] - mn);
-          fac[h] = !rises ? 1.f : (m_ref[h] == -INFINITY ? 0.f : f);
-          m_ref[h] = rises ? mn : m_ref[h];
-          l_part[h] *= fac[h];
-        }
-        if (kG && ((need >> 16) & 1u)) {
-          // raise the P.V reference: O^T so far is scaled down by 2^(gv_old - gv_new)
-          const int* g4 = gred + red_par * 4;
-          const int gnew = max(max(g4[0], g4[1]), max(g4[2], g4[3]));
-          const float facg = gv == kGvNone ? 0.f : exp2_int(max(-126, gv - gnew));
-          gv = gnew;
+          for (int h = 0; h < 16; ++h) {
+            const int was = exponent_of(c_ref[h]), same = min(kNoC, was + by[h]);  // (same: O^T keeps its scale)
+            const bool sets = !(top[h] * exp2_int(same) <= kMostP);
+            const int now = sets ? min(same, max(-126, kTopP - exponent_of(top[h]))) : same;
+            const int d = now - was - by[h];
+            fac[h] = d < -126 ? 0.f : exp2_int(d);
+            c_ref[h] = exp2_int(now);
+          }
+        } else {
+          if (kMx && ((need >> 16) & 1u)) {
+            const int w = __reduce_max_sync(0xffffffffu, row < valid ? gsh : kGvNone);
+            if (lane == 0) gred[red_par * 4 + ww] = w;
+          }
+          tile_max16(sv, reinterpret_cast<int*>(redbuf + red_par * 64), ww, lane, bar, top);
 #pragma unroll
-          for (int h = 0; h < 16; ++h) fac[h] *= facg;
+          for (int h = 0; h < 16; ++h) {
+            const bool rises = (need >> h) & 1u;
+            const float f = fast_exp2(m_ref[h] - top[h]);
+            fac[h] = !rises ? 1.f : (m_ref[h] == -INFINITY ? 0.f : f);
+            m_ref[h] = rises ? top[h] : m_ref[h];
+            l_part[h] *= fac[h];
+          }
+          if (kMx && ((need >> 16) & 1u)) {
+            // raise the P.V reference: O^T so far is scaled down by 2^(gv_old - gv_new)
+            const int* g4 = gred + red_par * 4;
+            const int gnew = max(max(g4[0], g4[1]), max(g4[2], g4[3]));
+            const float facg = gv == kGvNone ? 0.f : exp2_int(max(-126, gv - gnew));
+            gv = gnew;
+#pragma unroll
+            for (int h = 0; h < 16; ++h) fac[h] *= facg;
+          }
         }
         red_par ^= 1;
         if (t > 0) {
@@ -1696,24 +1763,23 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
         }
       }
       // probabilities (<= 256), two e4m3 terms, MN-major B operand row = this row;
-      // MXFP4 weights for P.V carry the row's 2^(G-127) relative to 2^gv (<= 1),
-      // row scales the row's own s 2^-gv (< 1)
-      const float pv_fac = kMx ? exp2_int(max(-126, gsh - gv)) : (kRow ? row_sc * exp2_int(-gv) : 1.f);
+      // MXFP4 weights for P.V carry the row's 2^(G-127) relative to 2^gv (<= 1)
+      const float pv_fac = kMx ? exp2_int(max(-126, gsh - gv)) : 1.f;
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        float pv[4];
+        float w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int h = 4 * g + e;
-          const float pr = (m_ref[h] == -INFINITY) ? 0.f : fast_exp2(sv[h] - m_ref[h]);
-          l_part[h] += pr;
-          pv[e] = pr * pv_fac;
+          const float x = kRow ? pr[h] : (m_ref[h] == -INFINITY ? 0.f : fast_exp2(sv[h] - m_ref[h]));
+          l_part[h] += x;
+          w[e] = kRow ? pv[h] * c_ref[h] : x * pv_fac;
         }
         if constexpr (kRow)
-          two_term_e4m3_up(pv[0], pv[1], pv[2], pv[3], hi[g], lo[g]);
+          two_term_e4m3_up(w[0], w[1], w[2], w[3], hi[g], lo[g]);
         else
-          two_term_e4m3(pv[0], pv[1], pv[2], pv[3], hi[g], lo[g]);
+          two_term_e4m3(w[0], w[1], w[2], w[3], hi[g], lo[g]);
       }
       if (kPBufs == 1 && it >= 1) wait_phase(&x.bar[kPFree + (sb ^ 1)], ((it - 1) >> 1) & 1, x.abort_flag, p.ws_err);
       uint8_t* pbuf = x.smem + L::pb + (it % kPBufs * kTok + ti) * kPBytes + row * 32;
@@ -1755,13 +1821,13 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
       // epilogue of the slot's previous unit has run) and go on to the next unit
       if (row == 0) {
         if (ordinal >= 2) wait_phase(&x.bar[ofree_bar(obuf)], ((ordinal >> 1) - 1) & 1, x.abort_flag, p.ws_err);
-        float* hand = reinterpret_cast<float*>(x.smem + L::hand) + 32 * obuf;
+        float* hand = reinterpret_cast<float*>(x.smem + L::hand) + L::hand_floats * obuf;
 #pragma unroll
         for (int h = 0; h < 16; ++h) {
           hand[h] = l_part[h];
           hand[16 + h] = m_ref[h];
+          if (kRow) hand[32 + h] = c_ref[h];
         }
-        if (kRow) reinterpret_cast<int*>(x.smem + L::handg)[obuf] = gv;
         mbar_arrive(&x.bar[kEpiReady + obuf]);
       }
       ++ordinal;
@@ -1772,8 +1838,8 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
       if (row == 0 && ti == 0 && k < 8) trace_stamp(p, kTrUnitLastPV + k);
       ++ordinal;
       tc::fence_after();
-      const float out_scale = kG ? exp2_int(max(-126, min(127, gv))) : kv_scale;
-      if (!none) write_unit<kMx, kRow>(p, tl_o, TM::blk, row, final_out, ob, u, l_part, m_ref, out_scale);
+      const float out_scale = kMx ? exp2_int(max(-126, min(127, gv))) : kv_scale;
+      if (!none) write_unit<kMx, kRow>(p, tl_o, TM::blk, row, final_out, ob, u, l_part, m_ref, c_ref, out_scale);
       if (row == 0 && ti == 0 && k < 8) trace_stamp(p, kTrUnitDone + k);
       tc::fence_before();
       __syncwarp();
