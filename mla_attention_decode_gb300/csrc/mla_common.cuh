@@ -225,16 +225,16 @@ __device__ __forceinline__ void two_term_e4m3(float x0, float x1, float x2, floa
   lo = f32x2_to_e4m3x2(x0 - b01.x, x1 - b01.y) | (f32x2_to_e4m3x2(x2 - b23.x, x3 - b23.y) << 16);
 }
 
-// The same with the second term 2^4 up, e4m3(16 (x - hi)): hi is within half a step,
-// so that is at most 256 where hi is at most 448, and its own smallest step counts
-// 2^-4 as much.
+// The same with the second term 2^kUp up, e4m3(2^kUp (x - hi)): its smallest step counts 2^-kUp
+// as much.  x - hi is at most half a step of x.
+template <int kUp>
 __device__ __forceinline__ void two_term_e4m3_up(float x0, float x1, float x2, float x3, uint32_t& hi, uint32_t& lo) {
+  constexpr float up = (float)(1 << kUp);
   const uint32_t h01 = f32x2_to_e4m3x2(x0, x1), h23 = f32x2_to_e4m3x2(x2, x3);
   const float2 b01 = __half22float2(e4m3x2_to_h2(h01));
   const float2 b23 = __half22float2(e4m3x2_to_h2(h23));
   hi = h01 | (h23 << 16);
-  lo = f32x2_to_e4m3x2((x0 - b01.x) * 16.f, (x1 - b01.y) * 16.f) |
-       (f32x2_to_e4m3x2((x2 - b23.x) * 16.f, (x3 - b23.y) * 16.f) << 16);
+  lo = f32x2_to_e4m3x2((x0 - b01.x) * up, (x1 - b01.y) * up) | (f32x2_to_e4m3x2((x2 - b23.x) * up, (x3 - b23.y) * up) << 16);
 }
 
 __device__ __forceinline__ float4 bf16x4_to_f4(uint2 v) {

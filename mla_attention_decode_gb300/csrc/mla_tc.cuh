@@ -61,17 +61,16 @@
 // e4m3 KV with a scale per row: row t is code_t s_t, so the scores are
 // (q . code_t) s_t and the output sum_t w_t s_t code_t / l.  s_t joins the row's
 // score factor in fp32 (each softmax thread fetches its row's scale two tiles ahead), and
-// what P.V takes are the products P = 2^(s - m) s_t c, with a power of two c per head that
-// follows the head's largest product: a scale counts by what its row weighs.  (Under the
-// largest scale of all rows, for every head alike, heads whose weight lay on rows with
-// scales 2^12 times smaller lost 40% of their output, with 2^16 all of it.)  The sum l of
-// the weights themselves needs no reference that close: m, a whole number, rises past
-// 2^24.  P's largest lies in [16, 32) after c has been set, is <= 2^8.75 before it is set
-// again, and P's second term is carried 2^4 up in its own columns of O^T: what e4m3's smallest
-// step leaves out of a product is 2^-18 of the largest instead of 2^-10.
+// what P.V takes are the products p = 2^(s - m) s_t under a power of two per head and
+// block of 32 rows (one warp's), which the MMAs of kind::mxf8f6f4 take back as the scale
+// factor of that block of P^T: P = 2^-e p in [2^7, 2^8) for the block's largest, its second
+// term 2^5 up with a scale factor of its own.  So a product keeps 8 bits down to 2^-14 of the
+// largest of its 32 rows, and what is left out below is 2^-22 of that, whatever the scores
+// and scales of all other rows: under one reference for a unit, the rows of a long tail under
+// one large score were in l but not in the output (one row 12 nats above 32768: 15%
+// off), and the rows of small scales where a row of large scale had no weight.  m, a whole
+// number, rises (and O^T, l are rescaled) only when a score exceeds it by more than 10.
 #pragma once
-#include <cfloat>
-
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -148,6 +147,9 @@ struct Tmem {
   // lane quarters), the B scale factors (all 2^0) at sfb
   static constexpr uint32_t sfa = 256;
   static constexpr uint32_t sfb = 320;
+  // row scales: the scale factors of V^T (all 2^0) at psfa, of tile t's P^T at psfb + 4 (t mod 2)
+  static constexpr uint32_t psfa = 448;
+  static constexpr uint32_t psfb = 452;
 };
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kBarSoftmax = 1;  // named barrier of softmax group 0 (128 threads); group 1: 2
@@ -156,6 +158,10 @@ constexpr uint32_t kIdescPV = tc::idesc_e4m3(128, 32, 1, 1);
 // two tokens per unit: one MMA with N = 64 covers both tokens' columns
 constexpr uint32_t kIdescQK2 = tc::idesc_e4m3(128, 64, 0, 0);
 constexpr uint32_t kIdescPV2 = tc::idesc_e4m3(128, 64, 1, 1);
+// row scales: e4m3 A and B with a ue8m0 scale factor for each 32 rows, byte b_sf of P^T's
+__host__ __device__ constexpr uint32_t idesc_pv_scaled(int N, int b_sf) {
+  return ((uint32_t)b_sf << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
+}
 
 
 __host__ __device__ constexpr int round_up_1024(int v) { return (v + 1023) / 1024 * 1024; }
@@ -171,19 +177,19 @@ struct Layout {
   static constexpr int sfb = sf + (G::bs ? 2 * kSfTileBytes : 0);  // block-scaled: [2 tiles] A chunks, then B
   static constexpr int qs = round_up_1024(sfb + (G::bs ? 512 : 0));
   static constexpr int pb = qs + kQsBytes * kTok;             // [p_bufs tiles][kTok]
-  static constexpr int rq = pb + G::p_bufs * kPBytes * kTok;  // float [kTok][16] score factor per head
+  // row scales: [p_bufs] scale factors of P^T, byte q of word 4 c + i: column c of token i, rows [32 q, +32)
+  static constexpr int psf = pb + G::p_bufs * kPBytes * kTok;
+  static constexpr int rq = psf + (row_scales(kPath) ? G::p_bufs * 512 : 0);  // float [kTok][16] score factor per head
   static constexpr int red = rq + 16 * 4 * kTok;              // float [2][4 warps][16 kTok]
-  static constexpr int gred = red + 2 * 4 * 16 * 4 * kTok;    // int [kTok][2][4] tile max of the row exponents
-  static constexpr int grow = gred + 2 * 4 * 4 * kTok;        // int8 [2][128] row exponent G - 127 (MXFP4)
+  static constexpr int gred = red + 2 * 4 * 16 * 4 * kTok;    // int [2][4] tile max of the row exponents (MXFP4)
+  static constexpr int grow = gred + (kMx ? 2 * 4 * 4 : 0);   // int8 [2][128] row exponent G - 127 (MXFP4)
   static constexpr int lut = grow + (kMx ? 2 * 128 : 0);      // u8 [32][8] e2m1 magnitude -> e4m3 per shift
-  // float [2][hand_floats] l, m (row scales: and c) handed to the epilogue group
-  static constexpr int hand_floats = row_scales(kPath) ? 48 : 32;
-  static constexpr int hand = lut + (kMx ? 256 : 0);
-  static constexpr int rows = hand + (G::epi ? 2 * 4 * hand_floats : 0);  // int [2][128] a tile's cache rows (small pages)
+  static constexpr int hand = lut + (kMx ? 256 : 0);          // float [2][32] l, m handed to the epilogue group
+  static constexpr int rows = hand + (G::epi ? 256 : 0);      // int [2][128] a tile's cache rows (small pages)
   static constexpr int units = rows + (!kMx && small_pages(kPath) ? 1024 : 0);
   static constexpr int bars = units + G::max_units * (int)sizeof(UnitDesc);
-  // the epilogue group's four (e4m3, one token), then the two of block-scaled MXFP4
-  static constexpr int nbars = G::bs ? 55 : (G::epi ? 53 : 49);
+  // (none of MXFP4 with two tokens,) the epilogue group's four (e4m3, one token), then the two of block-scaled MXFP4
+  static constexpr int nbars = G::bs ? 55 : (G::epi ? 53 : (kMx ? 49 : 41));
   static constexpr int misc = bars + nbars * 8;  // tmem slot, abort flag, unit count
   static constexpr int total = misc + 16;
 };
@@ -1274,6 +1280,8 @@ __device__ void pv_issuer(const Stage1Params& p, const Ctx& x) {
   constexpr int kPairSlots = Geo<kMx, kTok, kPath>::pair_slots;
   const uint32_t pairs0 = smem_u32(x.smem + L::pairs), pb0 = smem_u32(x.smem + L::pb);
   constexpr bool kEpi = Geo<kMx, kTok, kPath>::epi;
+  constexpr bool kRow = row_scales(kPath);
+  constexpr int kPBufs = Geo<kMx, kTok, kPath>::p_bufs;
   int it = 0, ordinal = 0;
   for (int k = 0; k < x.nunits && !aborted(x); ++k) {
     const int nt = __shfl_sync(0xffffffffu, tiles_of(x.units[k]), 0);
@@ -1290,9 +1298,13 @@ __device__ void pv_issuer(const Stage1Params& p, const Ctx& x) {
       if (aborted(x)) break;
       tc::fence_after();
       constexpr uint64_t kTplPT = kTok == 1 ? kTplP : kTplP2;
-      const uint32_t bp = lo_word(kTplPT) + ((pb0 + (uint32_t)(it % Geo<kMx, kTok, kPath>::p_bufs) * kTok * kPBytes) >> 4);
+      const uint32_t bp = lo_word(kTplPT) + ((pb0 + (uint32_t)(it % kPBufs) * kTok * kPBytes) >> 4);
       const int s0 = (4 * it) % kPairSlots;
+      const uint32_t sfa = x.tmem + TM::psfa, sfb = x.tmem + TM::psfb + 4 * (it & 1);
       if (tc::elect()) {
+        // the tile's scale factors into TMEM (executed before the MMAs that follow)
+        if constexpr (kRow)
+          tc::cp_32x128b_warpx4(sfb, tc::smem_desc(smem_u32(x.smem + L::psf) + 512 * (it % kPBufs), 128, 128, 0));
 #pragma unroll
         for (int fb = 0; fb < 4; ++fb) {
           const int sl = wrap_slot<kMx, kTok, kPath>(s0 + fb);
@@ -1300,9 +1312,14 @@ __device__ void pv_issuer(const Stage1Params& p, const Ctx& x) {
           // V^T block: features [128 fb, 128 fb + 128) = the slot's two column blocks (LBO)
           const uint32_t av = lo_word(kTplA) + ((pairs0 + (uint32_t)sl * kPairBytes) >> 4);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)  // rows [32 q, 32 q + 32): +kRows32 B of V^T, +1024 B of P^T (every token)
-            tc::mma_f8_words(od + TM::blk * fb, av + q * (kRows32 >> 4), hi_word(kTplA), bp + q * (1024 >> 4),
-                             hi_word(kTplPT), kTok == 1 ? kIdescPV : kIdescPV2, (t == 0 && q == 0) ? 0u : 1u);
+          for (int q = 0; q < 4; ++q) {  // rows [32 q, 32 q + 32): +kRows32 B of V^T, +1024 B of P^T (every token)
+            if constexpr (kRow)
+              tc::mma_mx_words(od + TM::blk * fb, av + q * (kRows32 >> 4), hi_word(kTplA), bp + q * (1024 >> 4),
+                               hi_word(kTplPT), idesc_pv_scaled(32 * kTok, q), sfa, sfb, (t == 0 && q == 0) ? 0u : 1u);
+            else
+              tc::mma_f8_words(od + TM::blk * fb, av + q * (kRows32 >> 4), hi_word(kTplA), bp + q * (1024 >> 4),
+                               hi_word(kTplPT), kTok == 1 ? kIdescPV : kIdescPV2, (t == 0 && q == 0) ? 0u : 1u);
+          }
           tc::commit(&x.bar[kPairEmpty + sl]);
         }
         tc::commit(&x.bar[kODone]);
@@ -1317,16 +1334,15 @@ __device__ void pv_issuer(const Stage1Params& p, const Ctx& x) {
 
 // 2^e for an integer e in [-126, 127] (exact).
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
-// floor(log2 x) of a normal x > 0 (128: infinite or NaN; -127: 0 or subnormal).
-__device__ __forceinline__ int exponent_of(float x) { return (__float_as_int(x) >> 23) - 127; }
 
-// Row scales: products are formed as 2^(s - m) (s_t 2^-kScaleUp) c.  With scales of
-// [2^-64, 2^120] and 2^(s - m) <= 2^24 the first product is at most 2^117, and at least
-// 2^-92 in the row that m is from, so that what fp32 loses at its lower end is 2^-34 of it.
+// Row scales: products are formed as p = 2^(s - m) (s_t 2^-kScaleUp).  With scales of
+// [2^-64, 2^120] they are at most 2^(93 + 10), and at least 2^-91 in the row that m is from,
+// so that what fp32 and the scale factors lose at their lower ends (2^-126) is 2^-35
+// of it, and O^T, whose unit is 2^kScaleUp, stays finite where the output is.
 constexpr int kScaleUp = 27;
-constexpr int kRiseSum = 24;       // m rises when a score exceeds it by that
-constexpr int kTopP = 4;           // P's largest after c has been set: [2^kTopP, 2^(kTopP + 1))
-constexpr int kNoC = 126;          // c's exponent before it has been set (any product is above it then)
+constexpr float kRiseSum = 10.f;        // m rises when a score exceeds it by that
+constexpr int kTopP = 7, kLoUp = 5;     // P's largest in its block: [2^kTopP, 2^(kTopP + 1)); second term 2^kLoUp up
+constexpr int kLeastExp = kTopP - 126;  // of a block's largest, so that 2^(kTopP - e) is finite
 
 // ------------------------------------------------------------------ unit output
 // A unit's output from O^T in TMEM: this thread's lane is feature row `row` of
@@ -1334,27 +1350,23 @@ constexpr int kNoC = 126;          // c's exponent before it has been set (any p
 // the query's two terms).  An unsplit sequence gets bf16 out and lse; a split
 // one an fp32 partial and lse in partial slot u.  l, m: the unit's softmax sum
 // and reference per head (log2 units); out_scale: the factor O^T carries.
-// kRow (row scales): the factor is 1 / c[h] and 2^kScaleUp, the weights' second term is 2^4 up, and
-// a sum that is NaN gives a NaN lse, so that a sequence split over several units keeps it
-// (else an lse of -inf, which the combine takes for an empty unit).
+// kRow (row scales): a sum that is NaN gives a NaN lse, so that a sequence split over
+// several units keeps it (else an lse of -inf, which the combine takes for an empty unit).
 template <bool kTwo, bool kRow>
 __device__ __forceinline__ void write_unit(const Stage1Params& p, uint32_t tl_o, uint32_t blk, int row, bool final_out,
                                            int ob, int u, const float (&l)[16], const float (&m)[16],
-                                           const float (&c)[16], float out_scale) {
-  constexpr float kLo = kRow ? 0.0625f : 1.f;
+                                           float out_scale) {
   // every thread holds all 16 heads' values: a lane inverts one (16 reciprocals a thread,
   // one after the other, took 1.0 us)
   const int mine = row & 15;
-  float lh = l[0], mh = m[0], ch = c[0];
+  float lh = l[0], mh = m[0];
 #pragma unroll
   for (int h = 1; h < 16; ++h) {
     lh = mine == h ? l[h] : lh;
     mh = mine == h ? m[h] : mh;
-    if (kRow) ch = mine == h ? c[h] : ch;
   }
   const bool any = kRow ? lh != 0.f : lh > 0.f;
-  // (row scales: the exponents of 1 / c and 1 / l first, their product is in range)
-  const float ih = !any ? 0.f : (kRow ? exp2_int(-exponent_of(ch)) * __frcp_rn(lh) * exp2_int(kScaleUp) : out_scale * __frcp_rn(lh));
+  const float ih = any ? out_scale * __frcp_rn(lh) : 0.f;
   float inv[16];
 #pragma unroll
   for (int h = 0; h < 16; ++h) inv[h] = __shfl_sync(0xffffffffu, ih, h);
@@ -1376,14 +1388,14 @@ __device__ __forceinline__ void write_unit(const Stage1Params& p, uint32_t tl_o,
         uint16_t* op = p.out + (size_t)ob * kHeads * kVDim + f;
 #pragma unroll
         for (int h = 0; h < 16; ++h) {
-          const float v = (__uint_as_float(o[j][h]) + kLo * __uint_as_float(o[j][16 + h])) * inv[h];
+          const float v = (__uint_as_float(o[j][h]) + __uint_as_float(o[j][16 + h])) * inv[h];
           op[h * kVDim] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xffffu);
         }
       } else {
         float* op = p.ws_o + (size_t)u * kHeads * kVDim + f;
 #pragma unroll
         for (int h = 0; h < 16; ++h)
-          op[h * kVDim] = (__uint_as_float(o[j][h]) + kLo * __uint_as_float(o[j][16 + h])) * inv[h];
+          op[h * kVDim] = (__uint_as_float(o[j][h]) + __uint_as_float(o[j][16 + h])) * inv[h];
       }
     }
   }
@@ -1413,7 +1425,7 @@ __device__ void epilogue_group(const Stage1Params& p, const Ctx& x, int ww, int 
   using TM = Tmem<kTok>;
   const int row = 32 * ww + lane;
   const uint32_t tl = x.tmem + ((uint32_t)(32 * ww) << 16);
-  const float kv_scale = kRow ? 1.f : *static_cast<const float*>(p.kv_scale);
+  const float kv_scale = kRow ? exp2_int(kScaleUp) : *static_cast<const float*>(p.kv_scale);
   const float* hand = reinterpret_cast<const float*>(x.smem + L::hand);
   const bool defer = x.nunits == 2 && tiles_of(x.units[0]) > 0 && tiles_of(x.units[1]) >= 4;
   int ordinal = 0;
@@ -1433,17 +1445,16 @@ __device__ void epilogue_group(const Stage1Params& p, const Ctx& x, int ww, int 
     if (tiles_of(d) == 0) continue;
     const int obuf = ordinal & 1, use = ordinal >> 1;
     if (!late0) wait_phase(&x.bar[kEpiReady + obuf], use & 1, x.abort_flag, p.ws_err);
-    float l[16], m[16], c[16];
+    float l[16], m[16];
 #pragma unroll
     for (int h = 0; h < 16; ++h) {
-      l[h] = hand[L::hand_floats * obuf + h];
-      m[h] = hand[L::hand_floats * obuf + 16 + h];
-      c[h] = kRow ? hand[L::hand_floats * obuf + 32 + h] : 1.f;
+      l[h] = hand[32 * obuf + h];
+      m[h] = hand[32 * obuf + 16 + h];
     }
     if (!late0) wait_phase(&x.bar[olast_bar(obuf)], use & 1, x.abort_flag, p.ws_err);
     if (row == 0 && k < 8 && !late0) trace_stamp(p, kTrUnitLastPV + k);
     tc::fence_after();
-    write_unit<false, kRow>(p, tl + TM::o + obuf * TM::obuf, TM::blk, row, (d.u & kFinalFlag) != 0, d.b, d.u & ~kFinalFlag, l, m, c,
+    write_unit<false, kRow>(p, tl + TM::o + obuf * TM::obuf, TM::blk, row, (d.u & kFinalFlag) != 0, d.b, d.u & ~kFinalFlag, l, m,
                             kv_scale);
     if (row == 0 && ku < 8) trace_stamp(p, kTrUnitDone + ku);
     tc::fence_before();
@@ -1529,12 +1540,11 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
   using L = Layout<kMx, kTok, kPath>;
   using TM = Tmem<kTok>;
   constexpr bool kRow = row_scales(kPath);    // a scale per row
-  constexpr float kMostP = 430.f;             // row scales: c is set anew past that (e4m3's largest: 448)
   constexpr int kGvNone = -1000;   // no such reference yet
   const int row = 32 * ww + lane;  // tile row == TMEM lane of this thread
   const uint32_t tl = x.tmem + ((uint32_t)(32 * ww) << 16) + 32 * ti;
   const uint32_t bar = kBarSoftmax + ti;  // the group's named barrier
-  const float kv_scale = kMx || kRow ? 1.f : *static_cast<const float*>(p.kv_scale);
+  const float kv_scale = kMx ? 1.f : (kRow ? exp2_int(kScaleUp) : *static_cast<const float*>(p.kv_scale));
   // row scales: this thread's row of the next tile and of the one after it (0 past
   // a unit's end), fetched two tiles ahead, its page a tile earlier still, so that
   // neither load waits for the other here
@@ -1561,12 +1571,20 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
     next_page();
   }
   const int8_t* grow = reinterpret_cast<const int8_t*>(x.smem + L::grow);
-  int* gred = reinterpret_cast<int*>(x.smem + L::gred) + 8 * ti;  // (the groups raise at tiles of their own)
+  int* gred = reinterpret_cast<int*>(x.smem + L::gred);
   const float* rq = reinterpret_cast<const float*>(x.smem + L::rq) + 16 * ti;
   float* redbuf = reinterpret_cast<float*>(x.smem + L::red) + 128 * ti;
   constexpr bool kEpi = Geo<kMx, kTok, kPath>::epi;
   constexpr int kPBufs = Geo<kMx, kTok, kPath>::p_bufs;
   int it = 0, red_par = 0, ordinal = 0;
+  if (kRow && ti == 0) {
+    // V^T's scale factors, all 2^0 (the first kPFull hands them over)
+    uint32_t one[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) one[i] = 0x7f7f7f7fu;
+    tc::st32(x.tmem + ((uint32_t)(32 * ww) << 16) + TM::psfa, one);
+    tc::wait_st();
+  }
   for (int k = 0; k < x.nunits; ++k) {
     const UnitDesc d = x.units[k];
     wait_phase(&x.bar[kQFull], k & 1, x.abort_flag, p.ws_err);
@@ -1601,12 +1619,11 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
       }
       continue;
     }
-    float m_ref[16], l_part[16], c_ref[16];  // (c: row scales)
+    float m_ref[16], l_part[16];
 #pragma unroll
     for (int h = 0; h < 16; ++h) {
-      m_ref[h] = -INFINITY;
+      m_ref[h] = kRow ? 0.f : -INFINITY;
       l_part[h] = 0.f;
-      c_ref[h] = kRow ? exp2_int(kNoC) : 1.f;
     }
     int gv = kGvNone;  // MXFP4: P.V reference exponent of the unit
     const int obuf = kEpi ? (ordinal & 1) : 0;  // the unit's O^T buffer
@@ -1641,84 +1658,114 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
       const int gsh = kBs ? gsh_bs : (kMx ? max(-126, (int)grow[sb * 128 + row]) : 0);
       // the scores of block-scaled MMAs carry no row factor
       const float row_fac = (kMx && !kBs) ? exp2_int(gsh) : (kRow ? row_sc : 1.f);
+      // scores; row scales: less m_ref, which is the ceiling of such a rounded product (so no fused
+      // one: with scores of 2^60 the largest would be 2^38 off it)
       float sv[16];
 #pragma unroll
-      for (int h = 0; h < 16; ++h)
-        sv[h] = row < vis ? (__uint_as_float(acc[h]) + __uint_as_float(acc[16 + h])) * (r[h] * row_fac)
-                          : -INFINITY;
-      // heads with a score above m_ref + kRescaleLog2 in this row (bit 16: G above gv); row
-      // scales: with a product above kMostP, or that is NaN, so that it reaches the output
-      // (bit 16: a score above m_ref + kRiseSum)
-      uint32_t need = 0;
-      float pr[16], pv[16];  // row scales: 2^(s - m), and that times the row's scale
-      const float up_sc = kRow ? row_sc * exp2_int(-kScaleUp) : 0.f;
+      for (int h = 0; h < 16; ++h) {
+        const float a = __uint_as_float(acc[h]) + __uint_as_float(acc[16 + h]), fac = r[h] * row_fac;
+        sv[h] = row < vis ? (kRow ? __fsub_rn(__fmul_rn(a, fac), m_ref[h]) : a * fac) : -INFINITY;
+      }
+      // O^T in TMEM times fac, once the previous tile's P.V is complete
+      auto rescale = [&](const float (&fac)[16]) {
+        wait_phase(&x.bar[kODone], (it - 1) & 1, x.abort_flag, p.ws_err);
+        tc::fence_after();
+#pragma unroll 1
+        for (int fb = 0; fb < 4; ++fb) {
+          uint32_t o[32];
+          tc::ld32(tl_o + TM::blk * fb, o);
+          tc::wait_ld();
+#pragma unroll
+          for (int h = 0; h < 16; ++h) {
+            o[h] = __float_as_uint(__uint_as_float(o[h]) * fac[h]);
+            o[16 + h] = __float_as_uint(__uint_as_float(o[16 + h]) * fac[h]);
+          }
+          tc::st32(tl_o + TM::blk * fb, o);
+        }
+        tc::wait_st();
+      };
+      float pr[16], f[16];   // row scales: 2^(s - m), the block's powers of two
+      uint32_t factor = 0;   // and the scale factor of column `lane` of this warp's rows
+      const float up_sc = kRow ? fmaf(row_sc, exp2_int(-kScaleUp), 0.f) : 0.f;  // (-0 becomes 0)
       if constexpr (kRow) {
         if (t == 0) {
-          tile_max16(sv, reinterpret_cast<int*>(redbuf + red_par * 64), ww, lane, bar, m_ref);
+          // m is the tile's maximum (its place was 0)
+          float top[16];
+          tile_max16(sv, reinterpret_cast<int*>(redbuf + red_par * 64), ww, lane, bar, top);
           red_par ^= 1;
 #pragma unroll
-          for (int h = 0; h < 16; ++h) m_ref[h] = m_ref[h] == -INFINITY ? -FLT_MAX : ceilf(m_ref[h]);
+          for (int h = 0; h < 16; ++h) {
+            m_ref[h] = top[h] == -INFINITY ? 0.f : ceilf(top[h]);
+            sv[h] -= m_ref[h];
+          }
         }
-        float most = 0.f;
+        // (as below: what was read from this P buffer, and the o_done wait)
+        if (kPBufs == 2 && it >= 2) wait_phase(&x.bar[kPFree + sb], ((it >> 1) - 1) & 1, x.abort_flag, p.ws_err);
+        // once, as a rule; again after m has risen
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+          float most = sv[0];
+          uint32_t word[4];
 #pragma unroll
-        for (int h = 0; h < 16; ++h) {
-          pr[h] = fast_exp2(sv[h] - m_ref[h]);
-          most = fmaxf(most, pr[h]);
-          pv[h] = pr[h] * up_sc;
-          need |= (!(pv[h] * c_ref[h] <= kMostP) ? 1u : 0u) << h;
+          for (int h = 0; h < 16; ++h) {
+            most = fmaxf(most, sv[h]);
+            pr[h] = fast_exp2(sv[h]);
+            // the largest product of the block (not negative: its bits are in order; not finite: NaN)
+            const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(pr[h] * up_sc));
+            const bool nan = big >= 0x7f800000u;
+            const int e = nan ? 0 : max(kLeastExp, (int)(big >> 23) - 127);
+            f[h] = nan ? __int_as_float(0x7fffffff) : exp2_int(kTopP - e);
+            const uint32_t b = (uint32_t)max(0, 127 - kTopP + e);
+            word[h >> 2] = (h & 3) ? word[h >> 2] | (b << (8 * (h & 3))) : b;
+          }
+          const uint32_t lo = (lane & 4) ? word[1] : word[0], hi = (lane & 4) ? word[3] : word[2];
+          factor = (((lane & 8) ? hi : lo) >> (8 * (lane & 3))) & 0xffu;
+          if (t == 0 || pass == 1) break;  // (no score is above m)
+          // OR over the warp, then over the 4 warps
+          uint32_t* fl = reinterpret_cast<uint32_t*>(redbuf + red_par * 64);
+          const bool rises = __any_sync(0xffffffffu, most > kRiseSum);
+          if (lane == 0) fl[ww] = rises;
+          named_bar_sync(bar, 128);
+          const uint32_t any = fl[0] | fl[1] | fl[2] | fl[3];
+          red_par ^= 1;
+          if (!any) break;
+          float top[16];
+          tile_max16(sv, reinterpret_cast<int*>(redbuf + red_par * 64), ww, lane, bar, top);
+          red_par ^= 1;
+#pragma unroll
+          for (int h = 0; h < 16; ++h) {
+            const float by = fmaxf(0.f, ceilf(top[h]));
+            m_ref[h] += by;
+            sv[h] -= by;
+            top[h] = fast_exp2(-by);
+            l_part[h] *= top[h];
+          }
+          rescale(top);
         }
-        if (most > exp2_int(kRiseSum)) need |= 1u << 16;
       } else {
+        // heads with a score above m_ref + kRescaleLog2 in this row (bit 16: G above gv)
+        uint32_t need = 0;
 #pragma unroll
         for (int h = 0; h < 16; ++h) need |= (sv[h] > m_ref[h] + kRescaleLog2 ? 1u : 0u) << h;
         if (kMx && row < valid && gsh > gv) need |= 1u << 16;
-      }
-      // heads whose reference rises: OR over the warp, then over the 4 warps
-      need = __reduce_or_sync(0xffffffffu, need);
-      {
-        uint32_t* fl = reinterpret_cast<uint32_t*>(redbuf + red_par * 64);
-        if (lane == 0) fl[ww] = need;
-        named_bar_sync(bar, 128);
-        need = fl[0] | fl[1] | fl[2] | fl[3];
-        red_par ^= 1;
-      }
-      // P buffer it mod 2 was read by P.V(it-2); waiting for it here also makes
-      // the o_done wait below exact (the barrier is then one phase behind at most)
-      // (one P buffer: below, for P.V(it-1))
-      if (kPBufs == 2 && it >= 2) wait_phase(&x.bar[kPFree + sb], ((it >> 1) - 1) & 1, x.abort_flag, p.ws_err);
-      if (need) {
-        // tile max of the rising heads (all 16, without per-head branches: on a unit's
-        // first tile all rise; selects, so that the heads' chains overlap: with a branch a
-        // head this took 1.0 us)
-        float top[16], fac[16];
-        if constexpr (kRow) {
-          int by[16];  // how far m rises
-#pragma unroll
-          for (int h = 0; h < 16; ++h) by[h] = 0;
-          if ((need >> 16) & 1u) {
-            tile_max16(sv, reinterpret_cast<int*>(redbuf + red_par * 64), ww, lane, bar, top);
-            red_par ^= 1;
-#pragma unroll
-            for (int h = 0; h < 16; ++h) {
-              const float m = fmaxf(m_ref[h], ceilf(top[h]));
-              by[h] = (int)fminf(m - m_ref[h], 1000.f);
-              l_part[h] *= fast_exp2(m_ref[h] - m);
-              m_ref[h] = m;
-              pr[h] = fast_exp2(sv[h] - m);
-              pv[h] = pr[h] * up_sc;
-            }
-          }
-          tile_max16(pv, reinterpret_cast<int*>(redbuf + red_par * 64), ww, lane, bar, top);
-#pragma unroll
-          for (int h = 0; h < 16; ++h) {
-            const int was = exponent_of(c_ref[h]), same = min(kNoC, was + by[h]);  // (same: O^T keeps its scale)
-            const bool sets = !(top[h] * exp2_int(same) <= kMostP);
-            const int now = sets ? min(same, max(-126, kTopP - exponent_of(top[h]))) : same;
-            const int d = now - was - by[h];
-            fac[h] = d < -126 ? 0.f : exp2_int(d);
-            c_ref[h] = exp2_int(now);
-          }
-        } else {
+        // heads whose reference rises: OR over the warp, then over the 4 warps
+        need = __reduce_or_sync(0xffffffffu, need);
+        {
+          uint32_t* fl = reinterpret_cast<uint32_t*>(redbuf + red_par * 64);
+          if (lane == 0) fl[ww] = need;
+          named_bar_sync(bar, 128);
+          need = fl[0] | fl[1] | fl[2] | fl[3];
+          red_par ^= 1;
+        }
+        // P buffer it mod 2 was read by P.V(it-2); waiting for it here also makes
+        // the o_done wait below exact (the barrier is then one phase behind at most)
+        // (one P buffer: below, for P.V(it-1))
+        if (kPBufs == 2 && it >= 2) wait_phase(&x.bar[kPFree + sb], ((it >> 1) - 1) & 1, x.abort_flag, p.ws_err);
+        if (need) {
+          // tile max of the rising heads (all 16, without per-head branches: on a unit's
+          // first tile all rise; selects, so that the heads' chains overlap: with a branch a
+          // head this took 1.0 us)
+          float top[16], fac[16];
           if (kMx && ((need >> 16) & 1u)) {
             const int w = __reduce_max_sync(0xffffffffu, row < valid ? gsh : kGvNone);
             if (lane == 0) gred[red_par * 4 + ww] = w;
@@ -1727,8 +1774,8 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
 #pragma unroll
           for (int h = 0; h < 16; ++h) {
             const bool rises = (need >> h) & 1u;
-            const float f = fast_exp2(m_ref[h] - top[h]);
-            fac[h] = !rises ? 1.f : (m_ref[h] == -INFINITY ? 0.f : f);
+            const float fh = fast_exp2(m_ref[h] - top[h]);
+            fac[h] = !rises ? 1.f : (m_ref[h] == -INFINITY ? 0.f : fh);
             m_ref[h] = rises ? top[h] : m_ref[h];
             l_part[h] *= fac[h];
           }
@@ -1741,25 +1788,8 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
 #pragma unroll
             for (int h = 0; h < 16; ++h) fac[h] *= facg;
           }
-        }
-        red_par ^= 1;
-        if (t > 0) {
-          // rescale O^T in TMEM once the previous tile's P.V is complete
-          wait_phase(&x.bar[kODone], (it - 1) & 1, x.abort_flag, p.ws_err);
-          tc::fence_after();
-#pragma unroll 1
-          for (int fb = 0; fb < 4; ++fb) {
-            uint32_t o[32];
-            tc::ld32(tl_o + TM::blk * fb, o);
-            tc::wait_ld();
-#pragma unroll
-            for (int h = 0; h < 16; ++h) {
-              o[h] = __float_as_uint(__uint_as_float(o[h]) * fac[h]);
-              o[16 + h] = __float_as_uint(__uint_as_float(o[16 + h]) * fac[h]);
-            }
-            tc::st32(tl_o + TM::blk * fb, o);
-          }
-          tc::wait_st();
+          red_par ^= 1;
+          if (t > 0) rescale(fac);
         }
       }
       // probabilities (<= 256), two e4m3 terms, MN-major B operand row = this row;
@@ -1774,10 +1804,10 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
           const int h = 4 * g + e;
           const float x = kRow ? pr[h] : (m_ref[h] == -INFINITY ? 0.f : fast_exp2(sv[h] - m_ref[h]));
           l_part[h] += x;
-          w[e] = kRow ? pv[h] * c_ref[h] : x * pv_fac;
+          w[e] = kRow ? x * up_sc * f[h] : x * pv_fac;
         }
         if constexpr (kRow)
-          two_term_e4m3_up(w[0], w[1], w[2], w[3], hi[g], lo[g]);
+          two_term_e4m3_up<kLoUp>(w[0], w[1], w[2], w[3], hi[g], lo[g]);
         else
           two_term_e4m3(w[0], w[1], w[2], w[3], hi[g], lo[g]);
       }
@@ -1808,6 +1838,9 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
           }
         }
       }
+      if (kRow)  // the block's scale factors; the second terms' are 2^-kLoUp of them
+        x.smem[L::psf + 512 * (it % kPBufs) + 16 * lane + 4 * ti + ww] =
+            (uint8_t)(lane < 16 ? factor : (factor > kLoUp ? factor - kLoUp : 0u));
       tc::fence_proxy_async();
       tc::fence_before();
       __syncwarp();
@@ -1821,12 +1854,11 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
       // epilogue of the slot's previous unit has run) and go on to the next unit
       if (row == 0) {
         if (ordinal >= 2) wait_phase(&x.bar[ofree_bar(obuf)], ((ordinal >> 1) - 1) & 1, x.abort_flag, p.ws_err);
-        float* hand = reinterpret_cast<float*>(x.smem + L::hand) + L::hand_floats * obuf;
+        float* hand = reinterpret_cast<float*>(x.smem + L::hand) + 32 * obuf;
 #pragma unroll
         for (int h = 0; h < 16; ++h) {
           hand[h] = l_part[h];
           hand[16 + h] = m_ref[h];
-          if (kRow) hand[32 + h] = c_ref[h];
         }
         mbar_arrive(&x.bar[kEpiReady + obuf]);
       }
@@ -1839,7 +1871,7 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
       ++ordinal;
       tc::fence_after();
       const float out_scale = kMx ? exp2_int(max(-126, min(127, gv))) : kv_scale;
-      if (!none) write_unit<kMx, kRow>(p, tl_o, TM::blk, row, final_out, ob, u, l_part, m_ref, c_ref, out_scale);
+      if (!none) write_unit<kMx, kRow>(p, tl_o, TM::blk, row, final_out, ob, u, l_part, m_ref, out_scale);
       if (row == 0 && ti == 0 && k < 8) trace_stamp(p, kTrUnitDone + k);
       tc::fence_before();
       __syncwarp();

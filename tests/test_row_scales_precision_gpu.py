@@ -1,9 +1,11 @@
 """What the row-scaled decode keeps of weights and scales that lie far apart, against fp64.
 
 With w_t the exact softmax weights of a token and head, s_t the rows' scales, u_t = w_t s_t
-and U the largest u_t, the tolerance of an output sum_t u_t code_t is
+and U the largest u_t of a block of 32 rows, the tolerance of an output sum_t u_t code_t is
   * its rounding to bf16                                     2^-8 |out|
-  * a weight times its row's scale enters P.V in e4m3 terms  max(REL u_t, FLOOR U) |code_t|
+  * a weight times its row's scale enters P.V as two e4m3 terms that keep 4 bits each, under
+    a power of two that leaves the block's largest at 2^7 or more and the second term 2^5
+    up: half of the smallest step, 2^-10, is 2^-22 of U      max(2^-8 u_t, 2^-22 U) |code_t|
   * n rows take n / 32 accumulations in fp32, each off by at most 2^-23 of the sum of
     magnitudes; the exponentials and the sum of the weights  (n 2^-28 + 2^-16) u_t |code_t|
   * the query enters the scores as two e4m3 terms under a power of two (the largest that leaves
@@ -27,7 +29,7 @@ def built():
     assert torch.cuda.is_available()
 
 
-def reference(q, codes, scales, rows, rel, floor):
+def reference(q, codes, scales, rows):
     """One token's 16 heads over cache rows `rows`: out, lse and their tolerances."""
     code = codes[rows].view(torch.float8_e4m3fn).double()
     s = scales[rows].double()
@@ -42,12 +44,13 @@ def reference(q, codes, scales, rows, rel, floor):
     mean = (w * d).sum(-1, keepdim=True)
     u = w * s
     out = u @ code[:, :512]
-    t = torch.maximum(rel * u, floor * u.amax(-1, keepdim=True)) + u * (len(rows) * 2.0 ** -28 + 2.0 ** -16)
+    top = torch.nn.functional.pad(u, (0, -len(rows) % 32)).view(16, -1, 32).amax(-1).repeat_interleave(32, 1)[:, :len(rows)]
+    t = torch.maximum(2.0 ** -8 * u, 2.0 ** -22 * top) + u * (len(rows) * 2.0 ** -28 + 2.0 ** -16)
     t = t + 2 * torch.where(w > 0, u * (d + mean), 0.0)
     return out, l, 2.0 ** -8 * out.abs() + t @ code[:, :512].abs(), mean.squeeze(1) + 2.0 ** -22 * l.abs() + 2e-5
 
 
-def check(path, q, codes, s, lens, rel, floor):
+def check(path, q, codes, s, lens):
     """Each sequence one unit, over the layout that `path` names: ("rows", tokens) or ("pages", rows a page)."""
     kind, n = path
     q_len = n if kind == "rows" else 1
@@ -73,7 +76,7 @@ def check(path, q, codes, s, lens, rel, floor):
     out, lse = out.double().cpu(), lse.double().cpu()
     for b, x in enumerate(lens):
         for i in range(q_len):
-            ref, l, t, tl = reference(q[b * q_len + i], codes, s, torch.arange(start[b], start[b] + x - (q_len - 1 - i)), rel, floor)
+            ref, l, t, tl = reference(q[b * q_len + i], codes, s, torch.arange(start[b], start[b] + x - (q_len - 1 - i)))
             err, size = (out[b * q_len + i] - ref).abs(), ref.abs().amax(-1, keepdim=True)
             assert torch.all(err <= t), f"sequence {b}, token {i}: off by {float((err / size).max()):.2e} of the largest output"
             assert torch.all((lse[b * q_len + i] - l).abs() <= tl)
@@ -100,4 +103,26 @@ def test_rows_of_large_scale_without_weight(path, k):
     q = torch.zeros(3 * q_len, 16, 576)
     q[..., 512:575] = 3 * 2.0 ** k * torch.randn(3 * q_len, 16, 63, generator=g)
     q[:, ::2, 575], q[:, 1::2, 575] = 8 * 2.0 ** k, -8 * 2.0 ** k
-    check(path, q.to(torch.bfloat16), codes, s, lens, 2.0 ** -8, 2.0 ** -18)
+    check(path, q.to(torch.bfloat16), codes, s, lens)
+
+
+@pytest.mark.parametrize("path", PATHS, ids=lambda p: f"{p[0]}{p[1]}")
+@pytest.mark.parametrize("n,spread", [(8192, 0), (8192, 1), (32768, 0), (32768, 1)])
+@pytest.mark.parametrize("gap", [9, 11, 12, 13, 15])
+def test_one_row_far_above_a_long_tail(path, n, spread, gap):
+    """A row whose score lies `gap` nats above the others' (the first row, one among them, one near the
+    end): together they weigh as much as it does, or nearly, one by one next to nothing."""
+    g, q_len = torch.Generator("cpu").manual_seed(n + gap), path[1] if path[0] == "rows" else 1
+    lens = [n, 1000, n - 77]
+    total = sum(lens)
+    f = torch.exp(0.3 * torch.randn(total, 1, generator=g))  # the rows' sizes
+    y = torch.cat([f * (1 + 0.5 * torch.randn(total, 512, generator=g)), torch.randn(total, 64, generator=g)], 1)
+    y[:, 575] = 0
+    at = torch.tensor([0, n + 517, total - 20])
+    y[at, :512] -= 2 * f[at]
+    y[at, 575] = 0.375 * gap
+    codes, s = stored(y)
+    q = torch.zeros(3 * q_len, 16, 576)
+    q[..., 512:575] = spread * 24 / 63 ** 0.5 * torch.randn(3 * q_len, 16, 63, generator=g)
+    q[..., 575] = 64
+    check(path, q.to(torch.bfloat16), codes, s, lens)
