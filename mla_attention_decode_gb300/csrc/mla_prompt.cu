@@ -340,14 +340,13 @@ struct Copies {
       if (!read(kS, j - 1)) break;
       values(j);
     }
-    if (*x.abort) {
-      // a wait gave up somewhere: never leave with copies in flight (bounded)
-      const uint64_t t0 = global_timer_ns();
-      for (int i = 0; i < 6; ++i) {
-        const int armed = i < 4 ? ((i < 2 ? ks : vs) + 1 - (i & 1)) / 2 : ((i - 4 ? n1 : n0) > 0 ? 1 : 0);
-        if (armed == 0) continue;
-        while (!mbar_try_wait(&x.bar[i], (armed - 1) & 1) && global_timer_ns() - t0 < kWaitTimeoutNs) {
-        }
+    // Never leave with copies in flight, whatever gives up, now or later (bounded): the last
+    // use of each barrier.  As a rule the block's products wait for the same.
+    const uint64_t t0 = global_timer_ns();
+    for (int i = 0; i < 6; ++i) {
+      const int armed = i < 4 ? ((i < 2 ? ks : vs) + 1 - (i & 1)) / 2 : ((i - 4 ? n1 : n0) > 0 ? 1 : 0);
+      if (armed == 0) continue;
+      while (!mbar_try_wait(&x.bar[i], (armed - 1) & 1) && global_timer_ns() - t0 < kWaitTimeoutNs) {
       }
     }
   }
