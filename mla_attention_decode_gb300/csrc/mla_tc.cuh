@@ -190,8 +190,8 @@ struct Layout {
   static constexpr int bars = units + G::max_units * (int)sizeof(UnitDesc);
   // (none of MXFP4 with two tokens,) the epilogue group's four (e4m3, one token), then the two of block-scaled MXFP4
   static constexpr int nbars = G::bs ? 55 : (G::epi ? 53 : (kMx ? 49 : 41));
-  static constexpr int misc = bars + nbars * 8;  // tmem slot, abort flag, unit count
-  static constexpr int total = misc + 16;
+  static constexpr int misc = bars + nbars * 8;  // tmem slot, abort flag, unit count, first row, [3] asked
+  static constexpr int total = misc + 28;
 };
 
 // mbarrier slots
@@ -232,6 +232,7 @@ struct Ctx {
   int nunits;
   uint64_t* bar;
   volatile int* abort_flag;
+  int* asked;  // [3] what the copying lanes asked for: pairs or staged halves, rope blocks, queries (see land)
   uint32_t tmem;
   int early_row;  // where the plan says: the first tile's cache row, its copy (e4m3: the tile; converted
                   // MXFP4: its two staging halves) issued before the unit scan (-1: none)
@@ -239,6 +240,16 @@ struct Ctx {
 
 // Whether any lane of the warp sees that a wait has given up (the warp then stops together).
 __device__ __forceinline__ bool aborted(const Ctx& x) { return __any_sync(0xffffffffu, *x.abort_flag != 0); }
+
+// Where a wait has given up: until the last of the `n` uses of a ring of `slots` barriers is
+// complete, so that the CTA never ends with copies in flight (bounded).
+__device__ __forceinline__ void land(uint64_t* bar, int slots, int n) {
+  for (int i = 0; i < slots && i < n; ++i) {
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(&bar[i], ((n - 1 - i) / slots) & 1) && global_timer_ns() - t0 < kWaitTimeoutNs) {
+    }
+  }
+}
 
 __device__ __forceinline__ int tiles_of(const UnitDesc& d) { return (d.end - d.start + kTileRows - 1) / kTileRows; }
 
@@ -294,7 +305,6 @@ __device__ __forceinline__ TileRows tile_rows(const Stage1Params& p, int t0, int
 template <int kTok>
 __device__ void producer_e4m3(const Stage1Params& p, const Ctx& x) {
   using L = Layout<false, kTok>;
-  constexpr int kPairSlots = Geo<false, kTok>::pair_slots;
   const uint64_t pol = policy_evict_first();  // KV rows are read once
   const bool paged64 = p.paged && p.page_shift == 6;
   // one 64-byte column block of the tile (and the bytes it brings)
@@ -306,8 +316,7 @@ __device__ void producer_e4m3(const Stage1Params& p, const Ctx& x) {
       if (r.r1 >= 0) tma_load_2d(dst + 64 * 64, &p.tmap_kv16, col, r.r1, bar, pol);
     }
   };
-  int armed[kPairSlots + kRopeSlots];
-  for (int i = 0; i < kPairSlots + kRopeSlots; ++i) armed[i] = 0;
+  int pairs = 0, ropes = 0;  // asked for
   // the cache rows of the next tile are looked up one tile ahead (a paged
   // cache reads the page table; otherwise they are the tile's own rows)
   TileWalk walk;
@@ -321,8 +330,8 @@ __device__ void producer_e4m3(const Stage1Params& p, const Ctx& x) {
       // and rope slot 0; the scan must agree (it does unless the device
       // kv_indptr differs from the plan's), else flag it and stop
       early_pending = false;
-      for (int f = 0; f < 4; ++f) ++armed[f];
-      ++armed[kPairSlots];
+      pairs = 4;
+      ropes = 1;
       if (nrows.r0 == x.early_row) {
         have = walk.next(x, nt0, nend);
         if (have) nrows = tile_rows(p, nt0, nend);
@@ -344,7 +353,7 @@ __device__ void producer_e4m3(const Stage1Params& p, const Ctx& x) {
       mbar_arrive_expect_tx(&x.bar[kPairFull + sl], 2 * block_bytes);
       load_block(dst, 128 * f, rows, &x.bar[kPairFull + sl]);
       load_block(dst + kChunkBytes, 128 * f + 64, rows, &x.bar[kPairFull + sl]);
-      ++armed[sl];
+      ++pairs;
       if (it == 0 && f == 0) trace_stamp(p, kTrFirstLoad);
     }
     const int rs = it % kRopeSlots, ruse = it / kRopeSlots;
@@ -352,26 +361,18 @@ __device__ void producer_e4m3(const Stage1Params& p, const Ctx& x) {
     if (*x.abort_flag) break;
     mbar_arrive_expect_tx(&x.bar[kRopeFull + rs], block_bytes);
     load_block(x.smem + L::rope + rs * kChunkBytes, 512, rows, &x.bar[kRopeFull + rs]);
-    ++armed[kPairSlots + rs];
+    ++ropes;
   }
   if (early_pending) {
     // the plan named a tile that this CTA's scan does not have: flag it, and
     // let the copy land before leaving
     flag_error(p.ws_err, kErrDeviceIndex, kTagFirstTile, x.early_row);
     *x.abort_flag = 1;
-    for (int f = 0; f < 4; ++f) ++armed[f];
-    ++armed[kPairSlots];
+    pairs = 4;
+    ropes = 1;
   }
-  if (*x.abort_flag) {
-    // a wait gave up somewhere: never leave with copies in flight (bounded wait per slot)
-    for (int i = 0; i < kPairSlots + kRopeSlots; ++i) {
-      if (armed[i] == 0) continue;
-      uint64_t* bar = i < kPairSlots ? &x.bar[kPairFull + i] : &x.bar[kRopeFull + i - kPairSlots];
-      const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(bar, (armed[i] - 1) & 1) && global_timer_ns() - t0 < kWaitTimeoutNs) {
-      }
-    }
-  }
+  x.asked[0] = pairs;
+  x.asked[1] = ropes;
 }
 
 
@@ -386,10 +387,8 @@ __device__ void producer_e4m3(const Stage1Params& p, const Ctx& x) {
 template <int kTok>
 __device__ void producer_e4m3_boxes(const Stage1Params& p, const Ctx& x, int lane) {
   using L = Layout<false, kTok>;
-  constexpr int kPairSlots = Geo<false, kTok>::pair_slots;
   const uint64_t pol = policy_evict_first();  // KV rows are read once
-  int armed[kPairSlots + kRopeSlots];         // lane 0: fills issued per slot
-  for (int i = 0; i < kPairSlots + kRopeSlots; ++i) armed[i] = x.early_row >= 0 && (i < 4 || i == kPairSlots);
+  int tiles = x.early_row >= 0 ? 1 : 0;       // lane 0: asked for
   const int page_mask = (1 << p.page_shift) - 1;
   TileWalk walk;
   int t0 = 0, end = 0;
@@ -417,12 +416,9 @@ __device__ void producer_e4m3_boxes(const Stage1Params& p, const Ctx& x, int lan
       if (ruse >= 1) wait_phase(&x.bar[kRopeEmpty + rs], (ruse - 1) & 1, x.abort_flag, p.ws_err);
       if (!*x.abort_flag) {
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          mbar_arrive_expect_tx(&x.bar[kPairFull + sl[f]], 2 * kChunkBytes);
-          ++armed[sl[f]];
-        }
+        for (int f = 0; f < 4; ++f) mbar_arrive_expect_tx(&x.bar[kPairFull + sl[f]], 2 * kChunkBytes);
         mbar_arrive_expect_tx(&x.bar[kRopeFull + rs], kChunkBytes);
-        ++armed[kPairSlots + rs];
+        ++tiles;
       }
     }
     if (__shfl_sync(0xffffffffu, lane == 0 ? *x.abort_flag : 0, 0)) break;
@@ -441,15 +437,9 @@ __device__ void producer_e4m3_boxes(const Stage1Params& p, const Ctx& x, int lan
     flag_error(p.ws_err, kErrDeviceIndex, kTagFirstTile, x.early_row);
     *x.abort_flag = 1;
   }
-  if (lane == 0 && *x.abort_flag) {
-    // a wait gave up somewhere: never leave with copies in flight (bounded wait per slot)
-    for (int i = 0; i < kPairSlots + kRopeSlots; ++i) {
-      if (armed[i] == 0) continue;
-      uint64_t* bar = i < kPairSlots ? &x.bar[kPairFull + i] : &x.bar[kRopeFull + i - kPairSlots];
-      const uint64_t tw = global_timer_ns();
-      while (!mbar_try_wait(bar, (armed[i] - 1) & 1) && global_timer_ns() - tw < kWaitTimeoutNs) {
-      }
-    }
+  if (lane == 0) {
+    x.asked[0] = 4 * tiles;
+    x.asked[1] = tiles;
   }
 }
 
@@ -612,7 +602,6 @@ struct HalfCursor {
 // three ahead are prefetched into L2 for the converter warps.
 static __device__ void producer_mx_bs(const Stage1Params& p, const Ctx& x) {
   using L = Layout<true, 1, kPathBlockScaled>;
-  constexpr int kPairSlots = Geo<true, 1, kPathBlockScaled>::pair_slots;
   const uint64_t pol = policy_evict_first();  // KV rows are read once
   const bool paged64 = p.paged && p.page_shift == 6;
   const uint8_t* sc = static_cast<const uint8_t*>(p.kv_scale);
@@ -642,8 +631,7 @@ static __device__ void producer_mx_bs(const Stage1Params& p, const Ctx& x) {
     }
   };
   for (int i = 0; i < kScaleAhead; ++i) prefetch_next();
-  int armed[kPairSlots + kRopeSlots];
-  for (int i = 0; i < kPairSlots + kRopeSlots; ++i) armed[i] = 0;
+  int pairs = 0, ropes = 0;  // asked for
   // the rope block of tile t + 2 is requested before the pairs of tile t: its
   // staging slot was laid out by the converters' step 1 for tile t, which
   // needs nothing requested later than tile t - 2, while the pairs of tile t
@@ -663,7 +651,7 @@ static __device__ void producer_mx_bs(const Stage1Params& p, const Ctx& x) {
     mbar_arrive_expect_tx(&x.bar[kStageFull + rs], box_rows * 32);
     tma_load_2d(dst, &p.tmap_kv16, 256, rows.r0, &x.bar[kStageFull + rs], pol);
     if (paged64 && rows.r1 >= 0) tma_load_2d(dst + 64 * 32, &p.tmap_kv16, 256, rows.r1, &x.bar[kStageFull + rs], pol);
-    ++armed[kPairSlots + rs];
+    ++ropes;
   };
   request_rope();
   request_rope();
@@ -687,20 +675,12 @@ static __device__ void producer_mx_bs(const Stage1Params& p, const Ctx& x) {
       mbar_arrive_expect_tx(&x.bar[kPairFull + sl], box_rows * 64);
       tma_load_3d(dst, &p.tmap_kv64, 0, f, rows.r0, &x.bar[kPairFull + sl], pol);
       if (paged64 && rows.r1 >= 0) tma_load_3d(dst + 64 * 128, &p.tmap_kv64, 0, f, rows.r1, &x.bar[kPairFull + sl], pol);
-      ++armed[sl];
+      ++pairs;
       if (it == 0 && f == 0) trace_stamp(p, kTrFirstLoad);
     }
   }
-  if (*x.abort_flag) {
-    // a wait gave up somewhere: never leave with copies in flight (bounded wait per slot)
-    for (int i = 0; i < kPairSlots + kRopeSlots; ++i) {
-      if (armed[i] == 0) continue;
-      uint64_t* bar = i < kPairSlots ? &x.bar[kPairFull + i] : &x.bar[kStageFull + i - kPairSlots];
-      const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(bar, (armed[i] - 1) & 1) && global_timer_ns() - t0 < kWaitTimeoutNs) {
-      }
-    }
-  }
+  x.asked[0] = pairs;
+  x.asked[1] = ropes;
 }
 
 // Converted MXFP4, contiguous caches and pages of 64 rows or more: half tiles
@@ -717,7 +697,7 @@ static __device__ void producer_mx(const Stage1Params& p, const Ctx& x) {
   const uint64_t pol = policy_evict_first();  // KV rows are read once
   const uint8_t* sc = static_cast<const uint8_t*>(p.kv_scale);
   const size_t ss = (size_t)p.scale_stride;
-  int uses[kStageSlots] = {0, 0, 0};
+  int halves = 0;  // asked for
   // the scale bytes of the half kScalePrefetch ahead go to L2 (the converters
   // read them a half ahead; this keeps those reads L2 hits)
   constexpr int kScalePrefetch = 6;
@@ -759,10 +739,10 @@ static __device__ void producer_mx(const Stage1Params& p, const Ctx& x) {
       if (hh == 0 && (rows <= 0 || crow != x.early_row)) {
         flag_error(p.ws_err, kErrDeviceIndex, kTagFirstTile, x.early_row);
         *x.abort_flag = 1;
-        uses[0] = uses[1] = 1;
+        halves = 2;
         break;
       }
-      ++uses[sl];
+      ++halves;
       advance_prefetch();
       continue;
     }
@@ -776,25 +756,17 @@ static __device__ void producer_mx(const Stage1Params& p, const Ctx& x) {
     } else {
       mbar_arrive(&x.bar[kStageFull + sl]);
     }
-    ++uses[sl];
+    ++halves;
     advance_prefetch();
   }
-  if (early && uses[0] == 0) {
+  if (early && halves == 0) {
     // the plan named a tile that this CTA's scan does not have: flag it, and
     // let the two copies land before leaving
     flag_error(p.ws_err, kErrDeviceIndex, kTagFirstTile, x.early_row);
     *x.abort_flag = 1;
-    uses[0] = uses[1] = 1;
+    halves = 2;
   }
-  if (*x.abort_flag) {
-    // a wait gave up somewhere: never leave with copies in flight (bounded wait per slot)
-    for (int i = 0; i < kStageSlots; ++i) {
-      if (uses[i] == 0) continue;
-      const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(&x.bar[kStageFull + i], (uses[i] - 1) & 1) && global_timer_ns() - t0 < kWaitTimeoutNs) {
-      }
-    }
-  }
+  x.asked[0] = halves;
 }
 
 // Converted MXFP4, pages of fewer than 64 rows: half tiles as above.  A half's rows
@@ -806,7 +778,7 @@ static __device__ void producer_mx(const Stage1Params& p, const Ctx& x) {
 static __device__ void producer_mx_rows(const Stage1Params& p, const Ctx& x, int lane) {
   using L = Layout<true, 1, kPathSmallPages>;
   const uint64_t pol = policy_evict_first();  // KV rows are read once
-  int uses[kStageSlots] = {0, 0, 0};
+  int halves = 0;  // asked for (lane 0)
   HalfCursor cur;
   int r0 = 0, rows = 0;
   for (int hh = 0; cur.next(x, r0, rows); ++hh) {
@@ -822,7 +794,7 @@ static __device__ void producer_mx_rows(const Stage1Params& p, const Ctx& x, int
         } else {
           mbar_arrive(&x.bar[kStageFull + sl]);
         }
-        ++uses[sl];
+        ++halves;
       }
     }
     if (!__shfl_sync(0xffffffffu, armed_ok, 0)) break;
@@ -834,15 +806,7 @@ static __device__ void producer_mx_rows(const Stage1Params& p, const Ctx& x, int
                &x.bar[kStageFull + sl], pol);
     }
   }
-  if (lane == 0 && *x.abort_flag) {
-    // a wait gave up somewhere: never leave with copies in flight (bounded wait per slot)
-    for (int i = 0; i < kStageSlots; ++i) {
-      if (uses[i] == 0) continue;
-      const uint64_t t0 = global_timer_ns();
-      while (!mbar_try_wait(&x.bar[kStageFull + i], (uses[i] - 1) & 1) && global_timer_ns() - t0 < kWaitTimeoutNs) {
-      }
-    }
-  }
+  if (lane == 0) x.asked[0] = halves;
 }
 
 // The 18 scale bytes of a row as nine pairs (byte 2i in bits 0-7 of e[i], byte
@@ -1128,12 +1092,7 @@ __device__ void q_loader(const Stage1Params& p, const Ctx& x) {
     load_query<kMx, kTok, kPath>(p, x, k, pol);
     ++uses;
   }
-  if (*x.abort_flag && uses > 0) {
-    // never leave with a copy in flight (bounded)
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(&x.bar[kQFull], (uses - 1) & 1) && global_timer_ns() - t0 < kWaitTimeoutNs) {
-    }
-  }
+  x.asked[2] = uses;
 }
 
 // ------------------------------------------------------------------ MMA issuers
@@ -1257,12 +1216,7 @@ __device__ void qk_issuer(const Stage1Params& p, const Ctx& x, int lane) {
     }
     if (tc::elect()) tc::commit(&x.bar[kQEmpty]);  // the query buffer may be refilled
   }
-  if (lane == 0 && *x.abort_flag && asked > 0) {
-    // never leave with a copy in flight (bounded)
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(&x.bar[kQFull], (asked - 1) & 1) && global_timer_ns() - t0 < kWaitTimeoutNs) {
-    }
-  }
+  if (kQkLoads<kMx, kPath> && lane == 0) x.asked[2] = asked;
 }
 
 // P.V of every tile: O^T += V^T(t) . P^T(t) (token i: its own P buffer and O^T
@@ -1903,6 +1857,7 @@ __global__ void __launch_bounds__(Geo<kMx, kTok, kPath>::threads, 1)
   int* misc = reinterpret_cast<int*>(smem + L::misc);
   x.abort_flag = misc + 1;
   int* s_nunits = misc + 2;
+  x.asked = misc + 4;
   if (threadIdx.x == 0) {
     trace_stamp(p, kTrEntry);
     trace_smid(p);
@@ -1926,6 +1881,7 @@ __global__ void __launch_bounds__(Geo<kMx, kTok, kPath>::threads, 1)
     *x.abort_flag = 0;
     fence_mbar_init();
     misc[3] = -1;
+    for (int i = 0; i < 3; ++i) x.asked[i] = 0;
     if constexpr (!kMx && (kTok == 1 || row_scales(kPath)) && !kSmallPages) {
       // the first tile's copy starts now, before the unit scan: the plan names
       // its row (the producer checks it against the scan), into pair slots
@@ -2079,6 +2035,13 @@ __global__ void __launch_bounds__(Geo<kMx, kTok, kPath>::threads, 1)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
+  if (threadIdx.x == 0 && *x.abort_flag) {
+    // (by now whatever gives up has)
+    constexpr bool kStaged = kMx && !kBs;
+    land(&x.bar[kStaged ? kStageFull : kPairFull], kStaged ? kStageSlots : Geo<kMx, kTok, kPath>::pair_slots, x.asked[0]);
+    if (!kStaged) land(&x.bar[kBs ? kStageFull : kRopeFull], kRopeSlots, x.asked[1]);
+    land(&x.bar[kQFull], 1, x.asked[2]);
+  }
   if (threadIdx.x == 0) trace_stamp(p, kTrExit);
   if (warp == 1) tc::dealloc(x.tmem, Tmem<kTok>::cols);
 }
