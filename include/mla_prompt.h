@@ -21,6 +21,8 @@
  * num_kv) set MLA_ERR_DEVICE_INDEX in the workspace's first word, which
  * mla_decode_poll_error(workspace, stream) reads and clears; that document's rows
  * of out and lse are then not written, and nothing outside the tensors is read.
+ * The other documents are computed (of more than 32, some of their rows may stay as
+ * they were too), where no two of them claim the same rows.
  */
 #ifndef MLA_PROMPT_H
 #define MLA_PROMPT_H

@@ -184,64 +184,85 @@ __device__ __forceinline__ int tiles_of(const PromptParams& p, const Work& w, in
   return n <= 0 ? 0 : (seen(p, w, 128 * g + n - 1) + kPromptTile - 1) / kPromptTile;
 }
 
-// Document b's slots (tiles of 256 tokens) begin at qo_indptr[b] / 256 + b: that is
-// at least as many as it has tiles, whatever the lengths, so that no prefix sum
-// over the batch is needed.  The document of a slot by a search of 32 probes a
-// step.  False: an empty slot.
-__device__ __forceinline__ bool find_work(const PromptParams& p, int slot, int lane, Work& w) {
-  int lo = 0, q, qe, k, ke, prefix;
-  auto load = [&](int b) {
-    q = __ldg(p.qo_indptr + b);
-    qe = __ldg(p.qo_indptr + b + 1);
-    k = __ldg(p.kv_indptr + b);
-    ke = __ldg(p.kv_indptr + b + 1);
-    prefix = p.prefix ? __ldg(p.prefix + b) : 0;
-  };
-  if (p.batch <= 32) {
-    // a document a lane: one round of loads
-    load(min(lane, p.batch - 1));
-    lo = max(0, __popc(__ballot_sync(0xffffffffu, lane < p.batch && (q >> 8) + lane <= slot)) - 1);
-    q = __shfl_sync(0xffffffffu, q, lo);
-    qe = __shfl_sync(0xffffffffu, qe, lo);
-    k = __shfl_sync(0xffffffffu, k, lo);
-    ke = __shfl_sync(0xffffffffu, ke, lo);
-    prefix = __shfl_sync(0xffffffffu, prefix, lo);
-  } else {
-    auto base = [&](int b) { return (__ldg(p.qo_indptr + b) >> 8) + b; };
-    int hi = p.batch;
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32, i = lo + (lane + 1) * step;
-      const int n = __popc(__ballot_sync(0xffffffffu, i < hi && base(i) <= slot));
-      lo += n * step;
-      hi = min(hi, lo + step);
-    }
-    load(lo);
+// A document's bounds, and its slots: [at, at + tiles), a slot a tile of 256 tokens.
+struct Doc {
+  int q, qe, k, ke, prefix, at;
+  __device__ __forceinline__ int tiles(const PromptParams& p) const {  // 0: bounds that do not fit (another warp reports them)
+    return q >= 0 && qe > q && qe <= p.num_q && k >= 0 && ke >= k && ke <= p.num_kv ? ((qe - q - 1) >> 8) + 1 : 0;
   }
-  if (q < 0 || qe < q || qe > p.num_q || k < 0 || ke < k || ke > p.num_kv) return false;  // (reported by another warp)
-  const int t = slot - ((q >> 8) + lo);
-  w.nq = qe - q;
-  w.nk = ke - k;
-  if (t < 0 || t > (w.nq - 1) >> 8 || w.nq == 0) return false;
-  w.first = kPromptQ * t;
-  w.q0 = q + w.first;
-  w.k0 = k;
-  w.rows = min(kPromptQ, w.nq - w.first);
-  w.prefix = prefix;
-  w.skip = 0;
-  return true;
+};
+__device__ __forceinline__ Doc load_doc(const PromptParams& p, int b) {
+  Doc d;
+  d.q = __ldg(p.qo_indptr + b);
+  d.qe = __ldg(p.qo_indptr + b + 1);
+  d.k = __ldg(p.kv_indptr + b);
+  d.ke = __ldg(p.kv_indptr + b + 1);
+  d.prefix = p.prefix ? __ldg(p.prefix + b) : 0;
+  d.at = (d.q >> 8) + b;
+  return d;
 }
-// The document of token t: its bounds fit and hold it.
-__device__ __forceinline__ bool owned(const PromptParams& p, int t, int lane) {
-  int lo = 0, hi = p.batch;
+// The last document with key(b) <= x, key not decreasing, by 32 probes a step.
+template <class Key>
+__device__ __forceinline__ int last_at_most(int batch, int x, int lane, Key key) {
+  int lo = 0, hi = batch;
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32, i = lo + (lane + 1) * step;
-    const int n = __popc(__ballot_sync(0xffffffffu, i < hi && __ldg(p.qo_indptr + i) <= t));
+    const int n = __popc(__ballot_sync(0xffffffffu, i < hi && key(i) <= x));
     lo += n * step;
     hi = min(hi, lo + step);
   }
-  const int q = __ldg(p.qo_indptr + lo), qe = __ldg(p.qo_indptr + lo + 1);
-  const int k = __ldg(p.kv_indptr + lo), ke = __ldg(p.kv_indptr + lo + 1);
-  return 0 <= q && q <= t && t < qe && qe <= p.num_q && 0 <= k && k <= ke && ke <= p.num_kv;
+  return lo;
+}
+// The document of slot x, or of token x; false: of none.  Up to 32 documents are looked at in one
+// round of loads, one a lane, and their slots lie one after the other (a scan), so that
+// one whose bounds do not fit takes none and hides no other.  Of more, document b's slots begin at
+// qo_indptr[b] / 256 + b, which is as many as the documents before it have at least, and
+// a search takes the bounds as not decreasing.
+template <bool kToken>
+__device__ __forceinline__ bool find_doc(const PromptParams& p, int x, int lane, Doc& d) {
+  constexpr unsigned all = 0xffffffffu;
+  if (p.batch <= 32) {
+    const Doc mine = load_doc(p, min(lane, p.batch - 1));
+    const int n = lane < p.batch ? mine.tiles(p) : 0;
+    int end = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(all, end, o);
+      if (lane >= o) end += v;
+    }
+    const unsigned has = __ballot_sync(all, n > 0 && (kToken ? mine.q <= x && x < mine.qe : end - n <= x && x < end));
+    if (has == 0) return false;
+    const int b = __ffs(has) - 1;
+    d = {__shfl_sync(all, mine.q, b), __shfl_sync(all, mine.qe, b),     __shfl_sync(all, mine.k, b),
+         __shfl_sync(all, mine.ke, b), __shfl_sync(all, mine.prefix, b), __shfl_sync(all, end - n, b)};
+    return true;
+  }
+  auto at = [&](int b) { return kToken ? __ldg(p.qo_indptr + b) : (__ldg(p.qo_indptr + b) >> 8) + b; };
+  d = load_doc(p, last_at_most(p.batch, x, lane, at));
+  const int n = d.tiles(p);
+  return n > 0 && (kToken ? d.q <= x && x < d.qe : d.at <= x && x - d.at < n);
+}
+__device__ __forceinline__ bool find_work(const PromptParams& p, int slot, int lane, Work& w) {
+  Doc d;
+  if (!find_doc<false>(p, slot, lane, d)) return false;
+  w.nq = d.qe - d.q;
+  w.nk = d.ke - d.k;
+  w.first = kPromptQ * (slot - d.at);
+  w.q0 = d.q + w.first;
+  w.k0 = d.k;
+  w.rows = min(kPromptQ, w.nq - w.first);
+  w.prefix = d.prefix;
+  w.skip = 0;
+  return true;
+}
+// Whether token t has been attended: a document holds it, and its tile's slot is that
+// document's (with bounds that do not fit it may not be).
+__device__ __forceinline__ bool attended(const PromptParams& p, int t, int lane) {
+  Doc d, of;
+  if (!find_doc<true>(p, t, lane, d)) return false;
+  const int slot = d.at + ((t - d.q) >> 8);
+  if (p.batch <= 32) return slot < p.slots;
+  return find_doc<false>(p, slot, lane, of) && of.at == d.at && of.q == d.q;
 }
 
 struct Ctx {
@@ -655,7 +676,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) mla_prompt_join_kernel(const 
 #pragma unroll
   for (int s = 0; s < kPromptMaxSplits; ++s)
     if (s < p.splits) v[s] = reinterpret_cast<const float4*>(p.part_o + (s * rows + row) * MLA_PROMPT_V)[lane];
-  if (!owned(p, t, lane)) return;  // a row of no document stays as it is (what was read is no result)
+  if (!attended(p, t, lane)) return;  // a row of no document stays as it is (what was read is no result)
   float top = mine;
   bool nan = mine != mine;
 #pragma unroll
