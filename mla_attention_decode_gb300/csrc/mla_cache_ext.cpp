@@ -472,16 +472,32 @@ PyObject* py_decode_core(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   END
 }
 
-// What a decode takes by address: device memory or pinned host memory, as the header says; None: null.
+// What a decode takes by address (None: null), consecutive and of `least` elements or more: memory
+// of the core's device or, where the header allows it, pinned host memory.
 const at::Tensor* given(PyObject* o, const char* what) {
   if (o == Py_None) return nullptr;
   if (!THPVariable_Check(o)) refuse("%s is a tensor", what);
   return &THPVariable_Unpack(o);
 }
-template <class T = void>
-T* address(PyObject* o, const char* what) {
+void reachable(const Device* c, const at::Tensor& t, const char* what, bool host) {
+  if (t.is_cuda() ? t.get_device() != c->device : !host || t.numel() == 0 || !t.is_pinned())
+    refuse("%s is on cuda:%d, the call's device%s", what, c->device, host ? ", or in pinned host memory" : "");
+}
+void* plain(const Device* c, const at::Tensor* t, const char* what, const char* type_name, bool type_fits, int64_t least,
+            bool host) {
+  if (!t) return nullptr;
+  if (!type_fits) refuse("%s is %s", what, type_name);
+  if (!t->is_contiguous()) refuse("%s is contiguous", what);
+  if (t->numel() < least) refuse("%s has %lld elements, not %lld or more", what, (long long)t->numel(), (long long)least);
+  if (t->numel() > 0) reachable(c, *t, what, host);
+  return t->data_ptr();
+}
+void* plain(const Device* c, PyObject* o, const char* what, at::ScalarType type, const char* type_name, int64_t least, bool host) {
   const at::Tensor* t = given(o, what);
-  return t ? static_cast<T*>(t->data_ptr()) : nullptr;
+  return plain(c, t, what, type_name, t && t->scalar_type() == type, least, host);
+}
+const int32_t* indices(const Device* c, PyObject* o, const char* what, int64_t least) {
+  return static_cast<int32_t*>(plain(c, o, what, at::kInt, "int32", least, true));
 }
 
 // decode(core, q, kv, kv_scale, indptr, kv_indices, last_page_len, qo_indptr, out, lse, sm_scale, stream)
@@ -491,42 +507,50 @@ PyObject* py_decode(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   BEGIN
   const DecodeCore* c = core_of<DecodeCore>(a[0]);
   const mla_plan* plan = c->plan;
-  const void *q = address(a[1], "q"), *kv = address(a[2], "kv");
+  const int32_t type = plan->kv_dtype;
+  const int64_t rows = plan->page_size ? (int64_t)plan->num_pages * plan->page_size : plan->total_kv;
+  const int64_t sequences = plan->q_len > 1 ? plan->batch / plan->q_len : plan->batch;
+  const void* q = plain(c, a[1], "q", at::kBFloat16, "bf16", 0, type != MLA_KV_BF16);
+  const at::Tensor* cache = given(a[2], "kv");
+  const void* kv = plain(c, cache, "kv", type == MLA_KV_BF16 ? "bf16" : "of one byte an element",
+                         cache && (type == MLA_KV_BF16 ? cache->scalar_type() == at::kBFloat16 : cache->element_size() == 1),
+                         rows * (type == MLA_KV_MXFP4 ? MLA_QK_DIM / 2 : MLA_QK_DIM), false);
   const at::Tensor* scale = given(a[3], "kv_scale");
   int64_t stride = 0;
-  if (scale && plan->kv_dtype == MLA_KV_MXFP4) {
-    if (scale->dim() < 1) refuse("kv_scale is [rows, >= 18]");
-    stride = scale->stride(0);
-  } else if (scale && plan->kv_dtype == MLA_KV_FP8_ROW) {
-    const int64_t rows = plan->page_size ? (int64_t)plan->num_pages * plan->page_size : plan->total_kv;
+  if (scale && type == MLA_KV_MXFP4) {
+    if (scale->element_size() != 1 || scale->dim() != 2 || scale->size(0) < rows || scale->size(1) < MLA_MX_SCALES_PER_ROW ||
+        scale->stride(1) != 1)
+      refuse("kv_scale is e8m0 bytes [rows, >= 18], rows >= %lld", (long long)rows);
+    stride = scale->size(0) > 1 ? scale->stride(0) : scale->size(1);  // (one row has no stride)
+  } else if (scale && type == MLA_KV_FP8_ROW) {
     if (scale->scalar_type() != at::kFloat || scale->dim() != 1 || scale->size(0) < rows)
       refuse("kv_scale is fp32 [rows], rows >= %lld", (long long)rows);
     stride = scale->size(0) > 1 ? 4 * scale->stride(0) : 4;  // (one scale has no stride)
+  } else if (scale && type == MLA_KV_FP8_E4M3) {
+    if (scale->scalar_type() != at::kFloat || scale->numel() < 1) refuse("kv_scale is fp32 [1]");
   }
   if (stride < 0 || stride > INT32_MAX) refuse("kv_scale's rows are too far apart");
+  if (scale && type != MLA_KV_BF16 && scale->numel() > 0) reachable(c, *scale, "kv_scale", false);
   const void* scales = scale ? scale->data_ptr() : nullptr;
-  const int32_t *indptr = address<int32_t>(a[4], "kv_indptr"), *indices = address<int32_t>(a[5], "kv_indices"),
-                *last = address<int32_t>(a[6], "kv_last_page_len"), *qo = address<int32_t>(a[7], "qo_indptr");
+  const int32_t *indptr = indices(c, a[4], plan->page_size ? "kv_page_indptr" : "kv_indptr", sequences + 1),
+                *pages = indices(c, a[5], "kv_indices", plan->page_size ? plan->total_kv / plan->page_size : 0),
+                *last = indices(c, a[6], "kv_last_page_len", sequences), *qo = indices(c, a[7], "qo_indptr", sequences);
+  void* out = plain(c, a[8], "out", at::kBFloat16, "bf16", (int64_t)plan->batch * MLA_NUM_HEADS * MLA_V_DIM, true);
+  float* lse = static_cast<float*>(plain(c, a[9], "lse", at::kFloat, "fp32", (int64_t)plan->batch * MLA_NUM_HEADS, true));
   const double sm_scale = PyFloat_AsDouble(a[10]);
   if (sm_scale == -1.0 && PyErr_Occurred()) throw PyError{};
   const Where w(c, a[11]);
   at::Tensor made_out, made_lse;
-  void* out;
-  float* lse;
   if (a[8] == Py_None) {
     made_out = fresh(c, w, {plan->batch, MLA_NUM_HEADS, MLA_V_DIM}, at::kBFloat16);
     out = made_out.data_ptr();
-  } else {
-    out = address(a[8], "out");
   }
   if (a[9] == Py_None) {
     made_lse = fresh(c, w, {plan->batch, MLA_NUM_HEADS}, at::kFloat);
     lse = static_cast<float*>(made_lse.data_ptr());
-  } else {
-    lse = address<float>(a[9], "lse");
   }
   const int rc = without_gil([&] {
-    return plan->page_size ? g_attention.decode_paged(q, kv, scales, (int32_t)stride, indptr, indices, last, qo, out, lse,
+    return plan->page_size ? g_attention.decode_paged(q, kv, scales, (int32_t)stride, indptr, pages, last, qo, out, lse,
                                                       (float)sm_scale, plan, c->workspace, c->workspace_bytes, w.handle)
                            : g_attention.decode(q, kv, scales, (int32_t)stride, indptr, qo, out, lse, (float)sm_scale, plan,
                                                 c->workspace, c->workspace_bytes, w.handle);
