@@ -235,17 +235,18 @@ class _Decoder:
     """The compiled call of a decoder: what it needs of the plan and the workspace, made again when
     either is another object (the plan's fields are read at each call)."""
 
-    _core = _of = _ext = None
+    _made = None  # plan, workspace, extension, its core
 
     def _decode(self, what, *args):
-        if self._core is None or self._of[0] is not self.plan or self._of[1] is not self.workspace:
+        made = self._made  # (held for the call: another thread may replace the plan)
+        if made is None or made[0] is not self.plan or made[1] is not self.workspace:
             from .cache import extension
-            self._ext, self._of, w = extension(), (self.plan, self.workspace), self.workspace
+            ext, plan, w = extension(), self.plan, self.workspace
             if not w.is_cuda:
                 raise ValueError("the decoder's workspace is a CUDA tensor")
-            self._core = self._ext.decode_core(ctypes.addressof(self.plan), w.data_ptr(), w.numel() * w.element_size(),
-                                               w.device.index)
-        rc, out, lse = self._ext.decode(self._core, *args)
+            core = ext.decode_core(ctypes.addressof(plan), w.data_ptr(), w.numel() * w.element_size(), w.device.index)
+            made = self._made = (plan, w, ext, core)
+        rc, out, lse = made[2].decode(made[3], *args)
         if rc:
             raise MLAError(rc, what)
         return out, lse

@@ -1,0 +1,88 @@
+"""Decoder objects without a GPU: which plan and workspace a call goes by."""
+import ctypes
+
+import pytest
+import torch
+
+from mla_attention_decode_gb300 import binding, build, cache
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    build.build()
+
+
+class Extension:
+    """In place of the compiled one: its cores are those of the real one, its calls say which core they got."""
+
+    def __init__(self):
+        self.real, self.made, self.called = cache.extension(), [], []
+
+    def decode_core(self, plan, workspace, nbytes, device):
+        core = self.real.decode_core(plan, workspace, nbytes, 0)
+        self.made.append((plan, workspace, nbytes, core))
+        return core
+
+    def decode(self, core, *args):
+        self.called.append(core)
+        return 0, "out", "lse"
+
+
+class Workspace:
+    """A workspace that says it is in device memory."""
+    is_cuda, device = True, torch.device("cuda:0")
+
+    def __init__(self, n):
+        self.n = n
+
+    def data_ptr(self):
+        return 1 << 20
+
+    def numel(self):
+        return self.n
+
+    def element_size(self):
+        return 1
+
+
+def decoder(monkeypatch, paged=False):
+    ext = Extension()
+    monkeypatch.setattr(cache, "extension", lambda: ext)
+    dec = binding.PagedMLADecoder([0, 3], [5], 64, 4, "fp8", device="cpu", num_sms=152) if paged else \
+        binding.MLADecoder([0, 300, 700], "fp8_row", device="cpu", num_sms=152)
+    dec.workspace = Workspace(1 << 20)
+    return ext, dec
+
+
+def test_a_call_goes_by_the_plan_and_the_workspace_of_its_time(monkeypatch):
+    """Also when another thread replaces the plan between the two lines of a call that look at it."""
+    ext, dec = decoder(monkeypatch)
+    args = [None] * 4
+    dec(*args), dec(*args)
+    assert len(ext.made) == 1
+    first = dec.plan
+    dec.plan = binding.mla_decode_plan([0, 10], "fp8_row", num_sms=152)
+    dec(*args)
+    dec.workspace = Workspace(1 << 21)
+    dec(*args)
+    assert [m[0] for m in ext.made] == [ctypes.addressof(p) for p in (first, dec.plan, dec.plan)] and ext.made[2][2] == 1 << 21
+
+    class Decoder(type(dec)):
+        """Its plan is replaced by `raced` right after it has been read for the third time."""
+        raced = None
+
+        @property
+        def plan(self):
+            plan = self.__dict__["plan"]
+            if self.raced is not None:
+                self.__dict__["plan"], self.raced = self.raced, None
+            return plan
+
+    racer = Decoder.__new__(Decoder)
+    racer.__dict__.update({k: v for k, v in dec.__dict__.items() if k != "_made"})
+    racer.raced = binding.mla_decode_plan([0, 20], "fp8_row", num_sms=152)
+    held = racer.__dict__["plan"]
+    racer(*args)
+    racer(*args)  # the replaced plan's own core
+    made = [m[0] for m in ext.made[3:]]
+    assert made == [ctypes.addressof(held), ctypes.addressof(racer.plan)] and ext.called[-1] is ext.made[-1][3]
