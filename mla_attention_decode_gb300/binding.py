@@ -251,6 +251,10 @@ class _Decoder:
             raise MLAError(rc, what)
         return out, lse
 
+    def __getstate__(self):
+        """A copy makes its own."""
+        return {k: v for k, v in self.__dict__.items() if k != "_made"}
+
 
 class MLADecoder(_Decoder):
     """Plan + workspace for one batch layout; call it with device tensors.

@@ -1,5 +1,8 @@
-"""Decoder objects without a GPU: which plan and workspace a call goes by."""
+"""Decoder objects without a GPU: copies of one that has been called, and which plan and workspace a
+call goes by."""
+import copy
 import ctypes
+import pickle
 
 import pytest
 import torch
@@ -52,6 +55,19 @@ def decoder(monkeypatch, paged=False):
         binding.MLADecoder([0, 300, 700], "fp8_row", device="cpu", num_sms=152)
     dec.workspace = Workspace(1 << 20)
     return ext, dec
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy, lambda d: pickle.loads(pickle.dumps(d))], ids=["copy", "deepcopy", "pickle"])
+def test_a_decoder_that_was_called_can_be_copied(monkeypatch, paged, how):
+    ext, dec = decoder(monkeypatch, paged)
+    args = [None] * (6 if paged else 4)
+    assert dec(*args) == ("out", "lse")
+    other = how(dec)
+    assert other.plan.as_dict() == dec.plan.as_dict() and other.kv_dtype == dec.kv_dtype
+    other(*args), dec(*args)
+    assert len(ext.made) == 2 and ext.called == [ext.made[0][3], ext.made[1][3], ext.made[0][3]]
+    assert ext.made[1][0] == ctypes.addressof(other.plan)
 
 
 def test_a_call_goes_by_the_plan_and_the_workspace_of_its_time(monkeypatch):
