@@ -231,6 +231,29 @@ def mla_decode_fwd_static(q, kv, kv_scale, kv_indptr, qo_indptr, out, lse, plan:
         raise MLAError(rc, "mla_decode_fwd_static")
 
 
+def _decode_by_ctypes(plan, workspace, q, kv, kv_scale, indptr, indices, last, qo_indptr, out, lse, sm_scale, stream):
+    """A decoder's call where the extension is not there: the library suffices, the checks of tensors and
+    some microseconds are lost."""
+    stride = 0
+    if kv_scale is not None and plan.kv_dtype == MLA_KV_MXFP4:
+        stride = int(kv_scale.stride(0))
+    elif kv_scale is not None and plan.kv_dtype == MLA_KV_FP8_ROW:
+        rows = plan.num_pages * plan.page_size if plan.page_size else plan.total_kv
+        if kv_scale.dtype != torch.float32 or kv_scale.dim() != 1 or kv_scale.shape[0] < rows:
+            raise ValueError(f"kv_scale is fp32 [rows], rows >= {rows}")
+        stride = 4 * kv_scale.stride(0) if kv_scale.shape[0] > 1 else 4
+    if out is None:
+        out = torch.empty(plan.batch, 16, 512, dtype=torch.bfloat16, device=workspace.device)
+    if lse is None:
+        lse = torch.empty(plan.batch, 16, dtype=torch.float32, device=workspace.device)
+    more = dict(sm_scale=sm_scale, scale_stride=stride, stream=stream)
+    if plan.page_size:
+        mla_decode_fwd_paged(q, kv, kv_scale, indptr, indices, last, qo_indptr, out, lse, plan, workspace, **more)
+    else:
+        mla_decode_fwd(q, kv, kv_scale, indptr, qo_indptr, out, lse, plan, workspace, **more)
+    return out, lse
+
+
 class _Decoder:
     """The compiled call of a decoder: what it needs of the plan and the workspace, made again when
     either is another object (the plan's fields are read at each call)."""
@@ -240,8 +263,12 @@ class _Decoder:
     def _decode(self, what, *args):
         made = self._made  # (held for the call: another thread may replace the plan)
         if made is None or made[0] is not self.plan or made[1] is not self.workspace:
-            from .cache import extension
-            ext, plan, w = extension(), self.plan, self.workspace
+            from . import cache
+            plan, w = self.plan, self.workspace
+            try:
+                ext = cache.extension()
+            except (RuntimeError, ImportError):  # not built, or for another torch
+                return _decode_by_ctypes(plan, w, *args)
             if not w.is_cuda:
                 raise ValueError("the decoder's workspace is a CUDA tensor")
             core = ext.decode_core(ctypes.addressof(plan), w.data_ptr(), w.numel() * w.element_size(), w.device.index)

@@ -1,5 +1,5 @@
-"""Decoder objects without a GPU: copies of one that has been called, and which plan and workspace a
-call goes by."""
+"""Decoder objects without a GPU: copies of one that has been called, which plan and workspace a call goes
+by, and calls without the compiled extension."""
 import copy
 import ctypes
 import pickle
@@ -102,3 +102,32 @@ def test_a_call_goes_by_the_plan_and_the_workspace_of_its_time(monkeypatch):
     racer(*args)  # the replaced plan's own core
     made = [m[0] for m in ext.made[3:]]
     assert made == [ctypes.addressof(held), ctypes.addressof(racer.plan)] and ext.called[-1] is ext.made[-1][3]
+
+
+@pytest.mark.parametrize("error", [RuntimeError, ImportError])
+@pytest.mark.parametrize("kv_dtype,scale,stride", [("bf16", None, 0), ("fp8", torch.ones(1), 0), ("fp8_row", torch.ones(300), 4),
+                                                   ("fp8_row", torch.ones(300, 3)[:, 1], 12), ("mxfp4", torch.ones(300, 20), 20)])
+@pytest.mark.parametrize("paged", [False, True])
+def test_without_the_extension_a_decoder_calls_the_library(monkeypatch, error, kv_dtype, scale, stride, paged):
+    def missing():
+        raise error("not built")
+
+    calls = []
+    monkeypatch.setattr(cache, "extension", missing)
+    for name in ("mla_decode_fwd", "mla_decode_fwd_paged"):
+        monkeypatch.setattr(binding, name, lambda *a, _n=name, **kw: calls.append((_n, a, kw)))
+    if paged:
+        dec, table = binding.PagedMLADecoder([0, 3], [5], 64, 4, kv_dtype, device="cpu", num_sms=152), ("indptr", "indices", "last")
+    else:
+        dec, table = binding.MLADecoder([0, 256], kv_dtype, device="cpu", num_sms=152), ("indptr",)
+    out, lse = dec("q", "kv", *table, "qo", kv_scale=scale, sm_scale=0.5, stream=7)
+    assert out.shape == (1, 16, 512) and out.dtype == torch.bfloat16 and lse.shape == (1, 16) and lse.dtype == torch.float32
+    name, a, kw = calls[0]
+    assert name == ("mla_decode_fwd_paged" if paged else "mla_decode_fwd") and kw == dict(sm_scale=0.5, scale_stride=stride, stream=7)
+    assert a[:2] == ("q", "kv") and a[2] is scale and a[3:] == (*table, "qo", out, lse, dec.plan, dec.workspace)
+    mine = torch.zeros(1, 16, 512), torch.zeros(1, 16)
+    assert dec("q", "kv", *table, "qo", kv_scale=scale, out=mine[0], lse=mine[1]) == mine
+    if kv_dtype == "fp8_row":
+        for bad in (torch.ones(255), torch.ones(300).double(), torch.ones(300, 1)):
+            with pytest.raises(ValueError):
+                dec("q", "kv", *table, "qo", kv_scale=bad)
