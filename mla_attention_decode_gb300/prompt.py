@@ -61,6 +61,8 @@ class MLAPrompt:
         self.num_tokens, self.num_keys, self.batch, self.heads = int(num_tokens), int(num_keys), int(batch), int(heads)
         self.causal, self.sm_scale = bool(causal), float(sm_scale)
         self._lib = load_library()
+        if max(map(abs, (self.num_tokens, self.num_keys, self.batch, self.heads))) >= 1 << 31:  # (a ctypes field would wrap)
+            raise MLAError(binding.MLA_ERR_INVALID_ARG, "mla_prompt_workspace_bytes")
         a = mla_prompt_args(num_q=self.num_tokens, num_kv=self.num_keys, batch=self.batch, heads=self.heads)
         nbytes = int(self._lib.mla_prompt_workspace_bytes(ctypes.addressof(a)))
         if nbytes == 0:
