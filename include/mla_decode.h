@@ -27,12 +27,14 @@
  *                    bytes apart (a multiple of 4, >= 4): row t is code_t * scale_t.
  *                    The scales are finite, >= 0 and at most 2^120; a row of scale NaN (what
  *                    mla_cache_append stores for values that are not finite, with codes 0)
- *                    makes NaN of the outputs of the tokens that see it.  What a row adds to an
- *                    output, its weight times its scale times its code, is off by at most 2^-8
- *                    of itself or 2^-22 of the largest product of weight and scale among the 32
- *                    rows of its block, whatever scores and scales the other rows have (and by
- *                    2^-90 absolutely under scales below 2^-64).  (The pages have no
- *                    counterpart; mla_cache_append writes it.)
+ *                    makes NaN of the outputs of the tokens that see it.  (The pages have
+ *                    no counterpart; mla_cache_append writes it.)
+ *
+ * A row's weight enters an output with an error of at most 2^-8 of itself or, with fp8, 2^-22
+ * of the largest weight among the 32 rows of its block, whatever scores the other rows
+ * have; with fp8_row the same of the weights times the rows' scales (and 2^-90 under scales
+ * below 2^-64); with mxfp4 2^-10 of the largest weight times power of two of a row (its
+ * largest block scale) so far in its work unit.
  *
  * Calling sequence: mla_decode_plan() (or mla_decode_plan_multi /
  * mla_decode_plan_paged) on the host for a batch layout (it reads only the

@@ -20,12 +20,20 @@
 //           features x 4 k32 steps; V^T read MN-major from the same stage --
 //           V is the first 512 columns of K -- so each KV byte is read from HBM
 //           once per unit), O^T resident in TMEM across the unit's tiles
-// The running max is applied lazily: P = 2^(s - m_ref) with m_ref raised (and
-// O^T, l rescaled in place) only when some score of a head exceeds m_ref by more
-// than 8 (log2 units), which keeps P <= 256 inside e4m3 range.  Deciding that
-// takes one OR over the tile's rows; the tile max itself is reduced only for
-// the heads that rise (always on a unit's first tile).  Scores are in log2
-// units: s = (q . k) * sm_scale * log2(e) * kv_scale.
+// Scores are in log2 units: s = (q . k) * sm_scale * log2(e) * kv_scale.  The running
+// max is applied lazily: its place m, a whole number, is the first tile's maximum and
+// rises (and O^T, l are rescaled in place) only when some score of a head exceeds it by
+// more than 10 (MXFP4: 8).  Deciding that takes one OR over the tile's rows; the tile max itself is
+// reduced only then, and on a unit's first tile.
+//
+// e4m3 KV: what P.V takes are the weights p = 2^(s - m) under a power of two per head and
+// block of 32 rows (one warp's), which the MMAs of kind::mxf8f6f4 take back as the scale
+// factor of that block of P^T: P = 2^-e p in [2^7, 2^8) for the block's largest, its second
+// term 2^5 up with a scale factor of its own.  So a weight keeps 8 bits down to 2^-14 of the
+// largest of its 32 rows, and what is left out below is 2^-22 of that, whatever the scores
+// of all other rows: under one reference for a unit, what lay 2^-10 below the largest was in
+// l but not in the output, which adds up over a long tail (one row 8 nats above 8192
+// others: 93% off; 64 x 8192 rows took 56.6 us then, 57.6 now).
 //
 // Warp roles: 0 TMA producer (9 column boxes of 64 B x 128 rows per tile: the
 // 8 V blocks in pairs into a ring of 11 pair slots, each released by the
@@ -61,15 +69,9 @@
 // e4m3 KV with a scale per row: row t is code_t s_t, so the scores are
 // (q . code_t) s_t and the output sum_t w_t s_t code_t / l.  s_t joins the row's
 // score factor in fp32 (each softmax thread fetches its row's scale two tiles ahead), and
-// what P.V takes are the products p = 2^(s - m) s_t under a power of two per head and
-// block of 32 rows (one warp's), which the MMAs of kind::mxf8f6f4 take back as the scale
-// factor of that block of P^T: P = 2^-e p in [2^7, 2^8) for the block's largest, its second
-// term 2^5 up with a scale factor of its own.  So a product keeps 8 bits down to 2^-14 of the
-// largest of its 32 rows, and what is left out below is 2^-22 of that, whatever the scores
-// and scales of all other rows: under one reference for a unit, the rows of a long tail under
-// one large score were in l but not in the output (one row 12 nats above 32768: 15%
-// off), and the rows of small scales where a row of large scale had no weight.  m, a whole
-// number, rises (and O^T, l are rescaled) only when a score exceeds it by more than 10.
+// what P.V takes are products p = 2^(s - m) s_t: a scale counts by what its row weighs.  (Under
+// the largest scale of all rows, heads whose weight lay on rows with scales 2^12
+// times smaller lost 40% of their output.)
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -147,18 +149,17 @@ struct Tmem {
   // lane quarters), the B scale factors (all 2^0) at sfb
   static constexpr uint32_t sfa = 256;
   static constexpr uint32_t sfb = 320;
-  // row scales: the scale factors of V^T (all 2^0) at psfa, of tile t's P^T at psfb + 4 (t mod 2)
+  // e4m3: the scale factors of V^T (all 2^0) at psfa, of tile t's P^T at psfb + 4 (t mod 2)
   static constexpr uint32_t psfa = 448;
   static constexpr uint32_t psfb = 452;
 };
 constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kBarSoftmax = 1;  // named barrier of softmax group 0 (128 threads); group 1: 2
 constexpr uint32_t kIdescQK = tc::idesc_e4m3(128, 32, 0, 0);
-constexpr uint32_t kIdescPV = tc::idesc_e4m3(128, 32, 1, 1);
+constexpr uint32_t kIdescPV = tc::idesc_e4m3(128, 32, 1, 1);  // MXFP4
 // two tokens per unit: one MMA with N = 64 covers both tokens' columns
 constexpr uint32_t kIdescQK2 = tc::idesc_e4m3(128, 64, 0, 0);
-constexpr uint32_t kIdescPV2 = tc::idesc_e4m3(128, 64, 1, 1);
-// row scales: e4m3 A and B with a ue8m0 scale factor for each 32 rows, byte b_sf of P^T's
+// e4m3 KV: V^T and P^T with a ue8m0 scale factor for each 32 rows, byte b_sf of P^T's
 __host__ __device__ constexpr uint32_t idesc_pv_scaled(int N, int b_sf) {
   return ((uint32_t)b_sf << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
 }
@@ -177,9 +178,9 @@ struct Layout {
   static constexpr int sfb = sf + (G::bs ? 2 * kSfTileBytes : 0);  // block-scaled: [2 tiles] A chunks, then B
   static constexpr int qs = round_up_1024(sfb + (G::bs ? 512 : 0));
   static constexpr int pb = qs + kQsBytes * kTok;             // [p_bufs tiles][kTok]
-  // row scales: [p_bufs] scale factors of P^T, byte q of word 4 c + i: column c of token i, rows [32 q, +32)
+  // e4m3: [p_bufs] scale factors of P^T, byte q of word 4 c + i: column c of token i, rows [32 q, +32)
   static constexpr int psf = pb + G::p_bufs * kPBytes * kTok;
-  static constexpr int rq = psf + (row_scales(kPath) ? G::p_bufs * 512 : 0);  // float [kTok][16] score factor per head
+  static constexpr int rq = psf + (!kMx ? G::p_bufs * 512 : 0);  // float [kTok][16] score factor per head
   static constexpr int red = rq + 16 * 4 * kTok;              // float [2][4 warps][16 kTok]
   static constexpr int gred = red + 2 * 4 * 16 * 4 * kTok;    // int [2][4] tile max of the row exponents (MXFP4)
   static constexpr int grow = gred + (kMx ? 2 * 4 * 4 : 0);   // int8 [2][128] row exponent G - 127 (MXFP4)
@@ -1234,7 +1235,7 @@ __device__ void pv_issuer(const Stage1Params& p, const Ctx& x) {
   constexpr int kPairSlots = Geo<kMx, kTok, kPath>::pair_slots;
   const uint32_t pairs0 = smem_u32(x.smem + L::pairs), pb0 = smem_u32(x.smem + L::pb);
   constexpr bool kEpi = Geo<kMx, kTok, kPath>::epi;
-  constexpr bool kRow = row_scales(kPath);
+  constexpr bool kBlk = !kMx;  // scale factors for P^T
   constexpr int kPBufs = Geo<kMx, kTok, kPath>::p_bufs;
   int it = 0, ordinal = 0;
   for (int k = 0; k < x.nunits && !aborted(x); ++k) {
@@ -1257,7 +1258,7 @@ __device__ void pv_issuer(const Stage1Params& p, const Ctx& x) {
       const uint32_t sfa = x.tmem + TM::psfa, sfb = x.tmem + TM::psfb + 4 * (it & 1);
       if (tc::elect()) {
         // the tile's scale factors into TMEM (executed before the MMAs that follow)
-        if constexpr (kRow)
+        if constexpr (kBlk)
           tc::cp_32x128b_warpx4(sfb, tc::smem_desc(smem_u32(x.smem + L::psf) + 512 * (it % kPBufs), 128, 128, 0));
 #pragma unroll
         for (int fb = 0; fb < 4; ++fb) {
@@ -1267,12 +1268,12 @@ __device__ void pv_issuer(const Stage1Params& p, const Ctx& x) {
           const uint32_t av = lo_word(kTplA) + ((pairs0 + (uint32_t)sl * kPairBytes) >> 4);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {  // rows [32 q, 32 q + 32): +kRows32 B of V^T, +1024 B of P^T (every token)
-            if constexpr (kRow)
+            if constexpr (kBlk)
               tc::mma_mx_words(od + TM::blk * fb, av + q * (kRows32 >> 4), hi_word(kTplA), bp + q * (1024 >> 4),
                                hi_word(kTplPT), idesc_pv_scaled(32 * kTok, q), sfa, sfb, (t == 0 && q == 0) ? 0u : 1u);
             else
               tc::mma_f8_words(od + TM::blk * fb, av + q * (kRows32 >> 4), hi_word(kTplA), bp + q * (1024 >> 4),
-                               hi_word(kTplPT), kTok == 1 ? kIdescPV : kIdescPV2, (t == 0 && q == 0) ? 0u : 1u);
+                               hi_word(kTplPT), kIdescPV, (t == 0 && q == 0) ? 0u : 1u);
           }
           tc::commit(&x.bar[kPairEmpty + sl]);
         }
@@ -1289,14 +1290,14 @@ __device__ void pv_issuer(const Stage1Params& p, const Ctx& x) {
 // 2^e for an integer e in [-126, 127] (exact).
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
 
+constexpr float kRiseSum = 10.f;        // e4m3: m rises when a score exceeds it by that
+constexpr int kTopP = 7, kLoUp = 5;     // P's largest in its block: [2^kTopP, 2^(kTopP + 1)); second term 2^kLoUp up
+constexpr int kLeastExp = kTopP - 126;  // of a block's largest, so that 2^(kTopP - e) is finite
 // Row scales: products are formed as p = 2^(s - m) (s_t 2^-kScaleUp).  With scales of
 // [2^-64, 2^120] they are at most 2^(93 + 10), and at least 2^-91 in the row that m is from,
 // so that what fp32 and the scale factors lose at their lower ends (2^-126) is 2^-35
 // of it, and O^T, whose unit is 2^kScaleUp, stays finite where the output is.
 constexpr int kScaleUp = 27;
-constexpr float kRiseSum = 10.f;        // m rises when a score exceeds it by that
-constexpr int kTopP = 7, kLoUp = 5;     // P's largest in its block: [2^kTopP, 2^(kTopP + 1)); second term 2^kLoUp up
-constexpr int kLeastExp = kTopP - 126;  // of a block's largest, so that 2^(kTopP - e) is finite
 
 // ------------------------------------------------------------------ unit output
 // A unit's output from O^T in TMEM: this thread's lane is feature row `row` of
@@ -1454,6 +1455,18 @@ __device__ __forceinline__ void group_reduce16(float (&v)[16], float* red, int w
   }
 }
 
+// Whether any of a softmax group's 128 threads says so; all have come here.
+__device__ __forceinline__ bool any_of_group(uint32_t bar, bool says) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "bar.red.or.pred p, %1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(bar), "r"((uint32_t)says)
+      : "memory");
+  return r != 0;
+}
+
 // Max over the tile's 128 rows for 16 heads: redux over the warp (order-preserving
 // integer image of the float), then over the 4 warps through `mx`.
 __device__ __forceinline__ void tile_max16(const float (&v)[16], int* mx, int ww, int lane, uint32_t bar, float (&top)[16]) {
@@ -1494,6 +1507,7 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
   using L = Layout<kMx, kTok, kPath>;
   using TM = Tmem<kTok>;
   constexpr bool kRow = row_scales(kPath);    // a scale per row
+  constexpr bool kBlk = !kMx;                 // P under a power of two for each block of 32 rows
   constexpr int kGvNone = -1000;   // no such reference yet
   const int row = 32 * ww + lane;  // tile row == TMEM lane of this thread
   const uint32_t tl = x.tmem + ((uint32_t)(32 * ww) << 16) + 32 * ti;
@@ -1531,7 +1545,7 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
   constexpr bool kEpi = Geo<kMx, kTok, kPath>::epi;
   constexpr int kPBufs = Geo<kMx, kTok, kPath>::p_bufs;
   int it = 0, red_par = 0, ordinal = 0;
-  if (kRow && ti == 0) {
+  if (kBlk && ti == 0) {
     // V^T's scale factors, all 2^0 (the first kPFull hands them over)
     uint32_t one[32];
 #pragma unroll
@@ -1576,7 +1590,7 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
     float m_ref[16], l_part[16];
 #pragma unroll
     for (int h = 0; h < 16; ++h) {
-      m_ref[h] = kRow ? 0.f : -INFINITY;
+      m_ref[h] = kBlk ? 0.f : -INFINITY;
       l_part[h] = 0.f;
     }
     int gv = kGvNone;  // MXFP4: P.V reference exponent of the unit
@@ -1612,13 +1626,13 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
       const int gsh = kBs ? gsh_bs : (kMx ? max(-126, (int)grow[sb * 128 + row]) : 0);
       // the scores of block-scaled MMAs carry no row factor
       const float row_fac = (kMx && !kBs) ? exp2_int(gsh) : (kRow ? row_sc : 1.f);
-      // scores; row scales: less m_ref, which is the ceiling of such a rounded product (so no fused
+      // scores; e4m3: less m_ref, which is the ceiling of such a rounded product (so no fused
       // one: with scores of 2^60 the largest would be 2^38 off it)
       float sv[16];
 #pragma unroll
       for (int h = 0; h < 16; ++h) {
         const float a = __uint_as_float(acc[h]) + __uint_as_float(acc[16 + h]), fac = r[h] * row_fac;
-        sv[h] = row < vis ? (kRow ? __fsub_rn(__fmul_rn(a, fac), m_ref[h]) : a * fac) : -INFINITY;
+        sv[h] = row < vis ? (kBlk ? __fsub_rn(__fmul_rn(a, fac), m_ref[h]) : a * fac) : -INFINITY;
       }
       // O^T in TMEM times fac, once the previous tile's P.V is complete
       auto rescale = [&](const float (&fac)[16]) {
@@ -1638,10 +1652,10 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
         }
         tc::wait_st();
       };
-      float pr[16], f[16];   // row scales: 2^(s - m), the block's powers of two
+      float pr[16], f[16];   // e4m3: 2^(s - m), the block's powers of two
       uint32_t factor = 0;   // and the scale factor of column `lane` of this warp's rows
-      const float up_sc = kRow ? fmaf(row_sc, exp2_int(-kScaleUp), 0.f) : 0.f;  // (-0 becomes 0)
-      if constexpr (kRow) {
+      const float up_sc = kRow ? fmaf(row_sc, exp2_int(-kScaleUp), 0.f) : 1.f;  // (-0 becomes 0)
+      if constexpr (kBlk) {
         if (t == 0) {
           // m is the tile's maximum (its place was 0)
           float top[16];
@@ -1665,7 +1679,7 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
             most = fmaxf(most, sv[h]);
             pr[h] = fast_exp2(sv[h]);
             // the largest product of the block (not negative: its bits are in order; not finite: NaN)
-            const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(pr[h] * up_sc));
+            const uint32_t big = __reduce_max_sync(0xffffffffu, __float_as_uint(kRow ? pr[h] * up_sc : pr[h]));
             const bool nan = big >= 0x7f800000u;
             const int e = nan ? 0 : max(kLeastExp, (int)(big >> 23) - 127);
             f[h] = nan ? __int_as_float(0x7fffffff) : exp2_int(kTopP - e);
@@ -1675,14 +1689,7 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
           const uint32_t lo = (lane & 4) ? word[1] : word[0], hi = (lane & 4) ? word[3] : word[2];
           factor = (((lane & 8) ? hi : lo) >> (8 * (lane & 3))) & 0xffu;
           if (t == 0 || pass == 1) break;  // (no score is above m)
-          // OR over the warp, then over the 4 warps
-          uint32_t* fl = reinterpret_cast<uint32_t*>(redbuf + red_par * 64);
-          const bool rises = __any_sync(0xffffffffu, most > kRiseSum);
-          if (lane == 0) fl[ww] = rises;
-          named_bar_sync(bar, 128);
-          const uint32_t any = fl[0] | fl[1] | fl[2] | fl[3];
-          red_par ^= 1;
-          if (!any) break;
+          if (!any_of_group(bar, most > kRiseSum)) break;
           float top[16];
           tile_max16(sv, reinterpret_cast<int*>(redbuf + red_par * 64), ww, lane, bar, top);
           red_par ^= 1;
@@ -1756,11 +1763,11 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int h = 4 * g + e;
-          const float x = kRow ? pr[h] : (m_ref[h] == -INFINITY ? 0.f : fast_exp2(sv[h] - m_ref[h]));
+          const float x = kBlk ? pr[h] : (m_ref[h] == -INFINITY ? 0.f : fast_exp2(sv[h] - m_ref[h]));
           l_part[h] += x;
-          w[e] = kRow ? x * up_sc * f[h] : x * pv_fac;
+          w[e] = kRow ? x * up_sc * f[h] : (kBlk ? x * f[h] : x * pv_fac);
         }
-        if constexpr (kRow)
+        if constexpr (kBlk)
           two_term_e4m3_up<kLoUp>(w[0], w[1], w[2], w[3], hi[g], lo[g]);
         else
           two_term_e4m3(w[0], w[1], w[2], w[3], hi[g], lo[g]);
@@ -1792,7 +1799,7 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
           }
         }
       }
-      if (kRow)  // the block's scale factors; the second terms' are 2^-kLoUp of them
+      if (kBlk)  // the block's scale factors; the second terms' are 2^-kLoUp of them
         x.smem[L::psf + 512 * (it % kPBufs) + 16 * lane + 4 * ti + ww] =
             (uint8_t)(lane < 16 ? factor : (factor > kLoUp ? factor - kLoUp : 0u));
       tc::fence_proxy_async();
