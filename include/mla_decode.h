@@ -33,8 +33,9 @@
  * A row's weight enters an output with an error of at most 2^-8 of itself or, with fp8, 2^-22
  * of the largest weight among the 32 rows of its block, whatever scores the other rows
  * have; with fp8_row the same of the weights times the rows' scales (and 2^-90 under scales
- * below 2^-64); with mxfp4 2^-10 of the largest weight times power of two of a row (its
- * largest block scale) so far in its work unit.
+ * below 2^-64); with mxfp4 2^-18 of the largest weight in its work unit, times the largest block
+ * scale over its own row's (so a tail of 8192 rows in one unit, each of 2^-18 of the largest
+ * weight, may be off by all of its 3%).
  *
  * Calling sequence: mla_decode_plan() (or mla_decode_plan_multi /
  * mla_decode_plan_paged) on the host for a batch layout (it reads only the

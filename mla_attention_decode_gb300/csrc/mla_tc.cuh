@@ -23,7 +23,7 @@
 // Scores are in log2 units: s = (q . k) * sm_scale * log2(e) * kv_scale.  The running
 // max is applied lazily: its place m, a whole number, is the first tile's maximum and
 // rises (and O^T, l are rescaled in place) only when some score of a head exceeds it by
-// more than 10 (MXFP4: 8).  Deciding that takes one OR over the tile's rows; the tile max itself is
+// more than 10 (MXFP4: kRescaleLog2).  Deciding that takes one OR over the tile's rows; the tile max itself is
 // reduced only then, and on a unit's first tile.
 //
 // e4m3 KV: what P.V takes are the weights p = 2^(s - m) under a power of two per head and
@@ -153,7 +153,14 @@ struct Tmem {
   static constexpr uint32_t psfa = 448;
   static constexpr uint32_t psfb = 452;
 };
-constexpr float kRescaleLog2 = 8.f;
+// MXFP4: m_ref lies kLower below the largest score when it is set, and rises when one exceeds it
+// by kRescaleLog2 (P <= 430; e4m3's largest is 448); the weights' second term is 2^kLoUpMx up.
+// What e4m3's smallest step leaves out of a weight is 2^-18 of the largest that way, not
+// 2^-10, with which one row 8 nats above 8192 others left most of them out.  (A
+// power of two for each 32 rows, as for e4m3 KV, costs the softmax warps more here, beside
+// the converters: 32 x 8192 rows 41.4 -> 46.2 us.)
+constexpr float kRescaleLog2 = 8.75f, kLower = 4.f;
+constexpr int kLoUpMx = 4;
 constexpr uint32_t kBarSoftmax = 1;  // named barrier of softmax group 0 (128 threads); group 1: 2
 constexpr uint32_t kIdescQK = tc::idesc_e4m3(128, 32, 0, 0);
 constexpr uint32_t kIdescPV = tc::idesc_e4m3(128, 32, 1, 1);  // MXFP4
@@ -1307,10 +1314,11 @@ constexpr int kScaleUp = 27;
 // and reference per head (log2 units); out_scale: the factor O^T carries.
 // kRow (row scales): a sum that is NaN gives a NaN lse, so that a sequence split over
 // several units keeps it (else an lse of -inf, which the combine takes for an empty unit).
-template <bool kTwo, bool kRow>
+template <bool kMx, bool kRow>
 __device__ __forceinline__ void write_unit(const Stage1Params& p, uint32_t tl_o, uint32_t blk, int row, bool final_out,
                                            int ob, int u, const float (&l)[16], const float (&m)[16],
                                            float out_scale) {
+  constexpr float kLo = kMx ? 1.f / (1 << kLoUpMx) : 1.f;  // (e4m3 KV: in the scale factors)
   // every thread holds all 16 heads' values: a lane inverts one (16 reciprocals a thread,
   // one after the other, took 1.0 us)
   const int mine = row & 15;
@@ -1325,11 +1333,11 @@ __device__ __forceinline__ void write_unit(const Stage1Params& p, uint32_t tl_o,
   float inv[16];
 #pragma unroll
   for (int h = 0; h < 16; ++h) inv[h] = __shfl_sync(0xffffffffu, ih, h);
-  // kTwo: two blocks of 128 features per TMEM round trip (MXFP4: 0.1-0.5 us
+  // MXFP4: two blocks of 128 features per TMEM round trip (0.1-0.5 us
   // off a bs32/kv8192 split stage in two A/B runs; the e4m3 kernel, which
   // needs four more registers for it, ran bs4/kv8192 1.4 us slower and keeps
   // one block per round trip)
-  constexpr int kPer = kTwo ? 2 : 1;
+  constexpr int kPer = kMx ? 2 : 1;
 #pragma unroll 1
   for (int fp = 0; fp < 4; fp += kPer) {
     uint32_t o[kPer][32];
@@ -1343,14 +1351,14 @@ __device__ __forceinline__ void write_unit(const Stage1Params& p, uint32_t tl_o,
         uint16_t* op = p.out + (size_t)ob * kHeads * kVDim + f;
 #pragma unroll
         for (int h = 0; h < 16; ++h) {
-          const float v = (__uint_as_float(o[j][h]) + __uint_as_float(o[j][16 + h])) * inv[h];
+          const float v = (__uint_as_float(o[j][h]) + kLo * __uint_as_float(o[j][16 + h])) * inv[h];
           op[h * kVDim] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xffffu);
         }
       } else {
         float* op = p.ws_o + (size_t)u * kHeads * kVDim + f;
 #pragma unroll
         for (int h = 0; h < 16; ++h)
-          op[h * kVDim] = (__uint_as_float(o[j][h]) + __uint_as_float(o[j][16 + h])) * inv[h];
+          op[h * kVDim] = (__uint_as_float(o[j][h]) + kLo * __uint_as_float(o[j][16 + h])) * inv[h];
       }
     }
   }
@@ -1735,9 +1743,9 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
 #pragma unroll
           for (int h = 0; h < 16; ++h) {
             const bool rises = (need >> h) & 1u;
-            const float fh = fast_exp2(m_ref[h] - top[h]);
+            const float mn = top[h] - kLower, fh = fast_exp2(m_ref[h] - mn);
             fac[h] = !rises ? 1.f : (m_ref[h] == -INFINITY ? 0.f : fh);
-            m_ref[h] = rises ? top[h] : m_ref[h];
+            m_ref[h] = rises ? mn : m_ref[h];
             l_part[h] *= fac[h];
           }
           if (kMx && ((need >> 16) & 1u)) {
@@ -1767,10 +1775,7 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
           l_part[h] += x;
           w[e] = kRow ? x * up_sc * f[h] : (kBlk ? x * f[h] : x * pv_fac);
         }
-        if constexpr (kBlk)
-          two_term_e4m3_up<kLoUp>(w[0], w[1], w[2], w[3], hi[g], lo[g]);
-        else
-          two_term_e4m3(w[0], w[1], w[2], w[3], hi[g], lo[g]);
+        two_term_e4m3_up<kBlk ? kLoUp : kLoUpMx>(w[0], w[1], w[2], w[3], hi[g], lo[g]);
       }
       if (kPBufs == 1 && it >= 1) wait_phase(&x.bar[kPFree + (sb ^ 1)], ((it - 1) >> 1) & 1, x.abort_flag, p.ws_err);
       uint8_t* pbuf = x.smem + L::pb + (it % kPBufs * kTok + ti) * kPBytes + row * 32;
