@@ -23,8 +23,8 @@
 // Scores are in log2 units: s = (q . k) * sm_scale * log2(e) * kv_scale.  The running
 // max is applied lazily: its place m, a whole number, is the first tile's maximum and
 // rises (and O^T, l are rescaled in place) only when some score of a head exceeds it by
-// more than 10 (MXFP4: kRescaleLog2).  Deciding that takes one OR over the tile's rows; the tile max itself is
-// reduced only then, and on a unit's first tile.
+// more than 10 (MXFP4: 8.75, from 4 below the maximum).  Deciding that takes one OR over the tile's rows; the
+// tile max itself is reduced only then, and on a unit's first tile.
 //
 // e4m3 KV: what P.V takes are the weights p = 2^(s - m) under a power of two per head and
 // block of 32 rows (one warp's), which the MMAs of kind::mxf8f6f4 take back as the scale
@@ -33,7 +33,7 @@
 // largest of its 32 rows, and what is left out below is 2^-22 of that, whatever the scores
 // of all other rows: under one reference for a unit, what lay 2^-10 below the largest was in
 // l but not in the output, which adds up over a long tail (one row 8 nats above 8192
-// others: 93% off; 64 x 8192 rows took 56.6 us then, 57.6 now).
+// others: 93% off; 64 x 8192 rows took 56.6 us then, 57.5 now).
 //
 // Warp roles: 0 TMA producer (9 column boxes of 64 B x 128 rows per tile: the
 // 8 V blocks in pairs into a ring of 11 pair slots, each released by the
@@ -166,7 +166,7 @@ constexpr uint32_t kIdescQK = tc::idesc_e4m3(128, 32, 0, 0);
 constexpr uint32_t kIdescPV = tc::idesc_e4m3(128, 32, 1, 1);  // MXFP4
 // two tokens per unit: one MMA with N = 64 covers both tokens' columns
 constexpr uint32_t kIdescQK2 = tc::idesc_e4m3(128, 64, 0, 0);
-// e4m3 KV: V^T and P^T with a ue8m0 scale factor for each 32 rows, byte b_sf of P^T's
+// e4m3 KV: V^T and P^T (both MN-major) with a ue8m0 scale factor for each 32 rows, byte b_sf of P^T's
 __host__ __device__ constexpr uint32_t idesc_pv_scaled(int N, int b_sf) {
   return ((uint32_t)b_sf << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24);
 }
@@ -196,7 +196,7 @@ struct Layout {
   static constexpr int rows = hand + (G::epi ? 256 : 0);      // int [2][128] a tile's cache rows (small pages)
   static constexpr int units = rows + (!kMx && small_pages(kPath) ? 1024 : 0);
   static constexpr int bars = units + G::max_units * (int)sizeof(UnitDesc);
-  // (none of MXFP4 with two tokens,) the epilogue group's four (e4m3, one token), then the two of block-scaled MXFP4
+  // two tokens: up to kPFree; MXFP4's; the epilogue group's four (e4m3, one token); block-scaled MXFP4's two
   static constexpr int nbars = G::bs ? 55 : (G::epi ? 53 : (kMx ? 49 : 41));
   static constexpr int misc = bars + nbars * 8;  // tmem slot, abort flag, unit count, first row, [3] asked
   static constexpr int total = misc + 28;
