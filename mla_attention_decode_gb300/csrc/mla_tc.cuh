@@ -1675,7 +1675,9 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
             sv[h] -= m_ref[h];
           }
         }
-        // (as below: what was read from this P buffer, and the o_done wait)
+        // P buffer it mod 2 was read by P.V(it-2); waiting for it here also makes
+        // rescale's wait exact (the barrier is then one phase behind at most)
+        // (one P buffer: below, for P.V(it-1))
         if (kPBufs == 2 && it >= 2) wait_phase(&x.bar[kPFree + sb], ((it >> 1) - 1) & 1, x.abort_flag, p.ws_err);
         // once, as a rule; again after m has risen
 #pragma unroll 1
@@ -1716,7 +1718,7 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
         uint32_t need = 0;
 #pragma unroll
         for (int h = 0; h < 16; ++h) need |= (sv[h] > m_ref[h] + kRescaleLog2 ? 1u : 0u) << h;
-        if (kMx && row < valid && gsh > gv) need |= 1u << 16;
+        if (row < valid && gsh > gv) need |= 1u << 16;
         // heads whose reference rises: OR over the warp, then over the 4 warps
         need = __reduce_or_sync(0xffffffffu, need);
         {
@@ -1726,16 +1728,14 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
           need = fl[0] | fl[1] | fl[2] | fl[3];
           red_par ^= 1;
         }
-        // P buffer it mod 2 was read by P.V(it-2); waiting for it here also makes
-        // the o_done wait below exact (the barrier is then one phase behind at most)
-        // (one P buffer: below, for P.V(it-1))
-        if (kPBufs == 2 && it >= 2) wait_phase(&x.bar[kPFree + sb], ((it >> 1) - 1) & 1, x.abort_flag, p.ws_err);
+        // (as above)
+        if (it >= 2) wait_phase(&x.bar[kPFree + sb], ((it >> 1) - 1) & 1, x.abort_flag, p.ws_err);
         if (need) {
           // tile max of the rising heads (all 16, without per-head branches: on a unit's
           // first tile all rise; selects, so that the heads' chains overlap: with a branch a
           // head this took 1.0 us)
           float top[16], fac[16];
-          if (kMx && ((need >> 16) & 1u)) {
+          if ((need >> 16) & 1u) {
             const int w = __reduce_max_sync(0xffffffffu, row < valid ? gsh : kGvNone);
             if (lane == 0) gred[red_par * 4 + ww] = w;
           }
@@ -1748,7 +1748,7 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
             m_ref[h] = rises ? mn : m_ref[h];
             l_part[h] *= fac[h];
           }
-          if (kMx && ((need >> 16) & 1u)) {
+          if ((need >> 16) & 1u) {
             // raise the P.V reference: O^T so far is scaled down by 2^(gv_old - gv_new)
             const int* g4 = gred + red_par * 4;
             const int gnew = max(max(g4[0], g4[1]), max(g4[2], g4[3]));
@@ -1761,7 +1761,7 @@ __device__ void softmax_epilogue(const Stage1Params& p, const Ctx& x, int ww, in
           if (t > 0) rescale(fac);
         }
       }
-      // probabilities (<= 256), two e4m3 terms, MN-major B operand row = this row;
+      // weights (e4m3 KV: below 2^8; MXFP4: 430 at most), two e4m3 terms, MN-major B operand row = this row;
       // MXFP4 weights for P.V carry the row's 2^(G-127) relative to 2^gv (<= 1)
       const float pv_fac = kMx ? exp2_int(max(-126, gsh - gv)) : 1.f;
       uint32_t hi[4], lo[4];

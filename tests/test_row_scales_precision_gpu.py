@@ -126,3 +126,35 @@ def test_one_row_far_above_a_long_tail(path, n, spread, gap):
     q[..., 512:575] = spread * 24 / 63 ** 0.5 * torch.randn(3 * q_len, 16, 63, generator=g)
     q[..., 575] = 64
     check(path, q.to(torch.bfloat16), codes, s, lens)
+
+
+@pytest.mark.parametrize("q_len", [1, 2])
+def test_a_scale_of_minus_zero_is_zero(q_len):
+    g = torch.Generator("cpu").manual_seed(3)
+    codes, s = stored(torch.randn(700, 576, generator=g))
+    s[::7] = 0
+    q = torch.randn(2 * q_len, 16, 576, generator=g).to(torch.bfloat16).to(DEV)
+    ind, qo = indptr_of([300, 400]).to(DEV), (torch.arange(3) * q_len).to(torch.int32).to(DEV)
+    dec = binding.MLADecoder(ind.cpu(), "fp8_row", q_len=q_len)
+    want = [t.clone() for t in dec(q, codes.to(DEV), ind, qo, kv_scale=s.to(DEV))]
+    s[::7] = -0.0
+    got = dec(q, codes.to(DEV), ind, qo, kv_scale=s.to(DEV))
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.all(torch.isfinite(got[0]))
+
+
+@pytest.mark.parametrize("path", PATHS, ids=lambda p: f"{p[0]}{p[1]}")
+def test_scores_that_rise_far_from_tile_to_tile(path):
+    """Each sequence's scores rise by 12 nats over every 200 rows (the reference rises and what was summed is
+    rescaled, again and again), and then fall as far."""
+    g, q_len = torch.Generator("cpu").manual_seed(5), path[1] if path[0] == "rows" else 1
+    lens = [2600, 700, 1500]
+    total = sum(lens)
+    y = torch.cat([1 + 0.5 * torch.randn(total, 512, generator=g), torch.randn(total, 64, generator=g)], 1)
+    at = torch.cat([torch.arange(n).float() for n in lens])
+    half = torch.cat([torch.full((n,), n / 2) for n in lens])
+    y[:, 575] = 12 * (half - (at - half).abs()) / 200 * 24 / 512
+    codes, s = stored(y)
+    q = torch.zeros(3 * q_len, 16, 576)
+    q[..., 512:575] = torch.randn(3 * q_len, 16, 63, generator=g)
+    q[..., 575] = 512
+    check(path, q.to(torch.bfloat16), codes, s, lens)
